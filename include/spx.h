@@ -490,6 +490,140 @@ SPX_API int spx_noalloc_init(void);
  * counterpart in the paper. */
 SPX_API int spx_noalloc_status(int32_t *status, spx_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Latent attention over a paged cache, and the cache's append               */
+/* ------------------------------------------------------------------------ */
+/* Types of the operators below.  Sums, softmax statistics and norms are held
+ * in 32 bits whatever the type. */
+typedef enum { SPX_F16 = 0, SPX_BF16 = 1, SPX_F32 = 2 } spx_dtype;
+
+/* Attention whose keys and values of a token come from one latent vector c
+ * (width R) that all heads share, next to one rotated key part r (width P):
+ *   k[h] = (W_uk[h] c, r),  v[h] = W_uv[h] c.
+ * The cache keeps (c, r) per token, R + P values, in pages of page_size
+ * tokens; token p of request b is row p % page_size of page
+ * block_table[b][p / page_size].  The draft model's latent projections are the
+ * target's own tensors (only the routed experts are quantised) [P1 Key
+ * Contributions 2], so one cache serves both, and a rejected draft token is
+ * taken back by a smaller lens[b] [P2 What shipped: the target keeps the
+ * committed entries, the draft appends temporary ones].
+ * Positions at or after lens[b] are never used, whatever they hold. */
+typedef struct {
+    int dtype;                   /* SPX_F16 or SPX_BF16 */
+    void *cache;                 /* [num_pages][page_size][R + P], 16-byte aligned */
+    int num_pages, page_size;    /* page_size a multiple of 16 */
+    int R, P;                    /* R a multiple of 128, at most 512; P = 64 */
+    int64_t page_stride;         /* elements from page to page, and from token to token: */
+    int64_t token_stride;        /*   multiples of 8 (token_stride >= R + P) */
+    const int32_t *block_table;  /* [B][max_pages] */
+    int max_pages;
+    int B;                       /* requests */
+    const int32_t *lens;         /* [B] tokens in the cache (new ones included) */
+} spx_latent_cache;
+
+/* Write N new tokens to the cache, one launch.  Row n of kv ([N][R + P], rows
+ * kv_stride elements apart) is the output of the down-projection:
+ *   c = kv[n][0..R) * rsqrt(mean(kv[n][0..R)^2) + eps) * w_norm  (w_norm != NULL)
+ *   r = rotation of kv[n][R..R+P) by row pos[n] of cos/sin       (cos != NULL)
+ * each rounded once, to token pos[n] of request req[n].  The rotation turns the
+ * pair (a, b) into (a cos - b sin, b cos + a sin), pairs being elements (2i,
+ * 2i + 1) when interleaved, else (i, i + P/2); cos and sin are fp32
+ * [max_pos][P/2].  With q (NULL = none) the last P values of every head of the
+ * same token's queries [N][heads][q_width] are rotated too, the others copied,
+ * into q_out (which may be q).  A row is skipped when pos[n] is negative or
+ * beyond the cos/sin rows, and its cache part also when req[n] is outside [0,
+ * B) or its table entry is missing or names no page.  Two rows must not name
+ * the same token. */
+typedef struct {
+    const spx_latent_cache *cache;
+    int N;
+    const void *kv;              /* 16-byte aligned */
+    int64_t kv_stride;           /* a multiple of 8 */
+    const int32_t *req, *pos;    /* [N] */
+    const void *w_norm;          /* [R], or NULL: no norm; 16-byte aligned */
+    float eps;
+    const float *cos, *sin;      /* [max_pos][P/2], or both NULL: no rotation; 16-byte aligned */
+    int max_pos, interleaved;
+    const void *q;               /* 16-byte aligned */
+    void *q_out;
+    int64_t q_stride, q_out_stride; /* elements from token to token, multiples of 8 */
+    int heads, q_width;          /* q_width a multiple of 8, at least P */
+} spx_latent_append_args;
+SPX_API int spx_latent_append(const spx_latent_append_args *args, spx_stream_t stream);
+
+/* Attention of the requests' newest tokens over their cache.  Request b owns
+ * query rows q_start[b] .. q_start[b+1] - 1 (at most max_q of them, none
+ * allowed), which stand for its last tokens: row i of T sees the positions
+ *   p < lens[b] - T + i + 1 (causal), or p < lens[b].
+ *   score = scale * (q_nope . W_uk c_p + q_rope . r_p);
+ *   out   = W_uv sum_p softmax(score)_p c_p,  lse = log sum_p exp(score_p).
+ * A row that sees nothing gives out = 0 and lse = -inf.  A position that holds
+ * an infinity or a NaN reaches only the rows that see it.
+ * With w_uk and w_uv (both or neither): q is [N][heads][dn + P], out is
+ * [N][heads][dv].  Without (their products folded into the neighbouring
+ * projections): q is [N][heads][R + P], out is [N][heads][R].
+ * form: SPX_LATENT_ABSORBED multiplies q by W_uk and the result by W_uv and
+ * attends in latent space, so the cache is read once for all heads (draft and
+ * verify calls); SPX_LATENT_EXPANDED writes every head's keys and values to the
+ * workspace and attends per head with (R + P + R) / (dn + P + dv) times fewer
+ * operations per query-key pair (prompts; needs the weights with dn = dv =
+ * 128); SPX_LATENT_AUTO chooses by max_q.  max_q and max_len bound every
+ * request's rows and length (larger ones are cut to them).
+ * Roundings to the type: q W_uk, the softmax weights, and in the expanded form
+ * keys and values. */
+enum { SPX_LATENT_AUTO = 0, SPX_LATENT_ABSORBED = 1, SPX_LATENT_EXPANDED = 2 };
+typedef struct {
+    const spx_latent_cache *cache;
+    int N, heads;
+    const void *q;               /* 16-byte aligned; heads contiguous within a token */
+    int64_t q_stride, out_stride;/* elements from token to token, multiples of 8 */
+    const int32_t *q_start;      /* [B + 1], ascending from 0 on */
+    int max_q, max_len;
+    const void *w_uk;            /* [heads][dn][R], 16-byte aligned, or NULL */
+    const void *w_uv;            /* [heads][dv][R], 16-byte aligned, or NULL */
+    int dn, dv;                  /* 64 or 128 each (0 without weights) */
+    float scale;
+    int causal;
+    void *out;                   /* 16-byte aligned */
+    float *lse;                  /* [N][heads], or NULL */
+    int form;
+    void *ws;                    /* spx_latent_workspace_size() bytes, zeroed once by spx_workspace_init() */
+    size_t ws_bytes;
+    uint64_t wait_budget_ns;     /* bound of every device-side wait; 0 = 2 s */
+} spx_latent_args;
+SPX_API int spx_latent_attention(const spx_latent_args *args, spx_stream_t stream);
+/* Workspace of a call with B requests, N query rows (sum over the requests), at
+ * most max_q rows and max_len cached tokens each; 0 if unsupported.  A larger
+ * workspace serves smaller calls.  Its status word (spx_workspace_status) is
+ * SPX_ERR_TIMEOUT after a bounded wait that gave up. */
+SPX_API size_t spx_latent_workspace_size(int B, int N, int max_q, int max_len, int heads, int R, int P, int dn, int dv,
+                                         int form);
+
+/* ------------------------------------------------------------------------ */
+/* Log probabilities of given tokens                                         */
+/* ------------------------------------------------------------------------ */
+/* Per row x of logits ([N][V], rows stride elements apart, any alignment), one
+ * launch, one pass over memory: with log_z = log sum_v exp(x_v),
+ *   logp    = x[ids] - log_z         (NaN when ids is outside [0, V))
+ *   entropy = -sum_v p_v log p_v     (p_v = exp(x_v - log_z); 0 log 0 = 0)
+ *   top_ids, top_logp = the k largest logits in descending order, ties to the
+ *                       lower index, NaN above everything, and x - log_z.
+ * [P1 Main Findings: acceptance of drafted tokens; the verify pass scores each
+ * of them].  A row of -inf alone has no distribution: every log probability
+ * is -inf and the entropy 0.  Each output may be NULL (ids with logp; k = 0
+ * with top_ids and top_logp). */
+typedef struct {
+    int dtype;                   /* SPX_F16, SPX_BF16 or SPX_F32 */
+    const void *logits;
+    int64_t stride;              /* elements, >= V */
+    int N, V, k;                 /* 0 <= k <= 32, k <= V */
+    const int32_t *ids;          /* [N] */
+    float *logp, *entropy;       /* [N] */
+    int32_t *top_ids;            /* [N][k] */
+    float *top_logp;             /* [N][k] */
+} spx_logprobs_args;
+SPX_API int spx_token_logprobs(const spx_logprobs_args *args, spx_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,87 @@
+// spx_latent.cuh -- what the latent-attention launches share: element types,
+// the parameter block and the decoding of a request's rows and pages.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "spx_internal.cuh"
+
+namespace spx {
+
+// Element type by its spx_dtype: conversions to and from fp32, one rounding.
+template <int DT>
+struct Elem;
+template <>
+struct Elem<SPX_F16> {
+    using T = __half;
+    static __device__ __forceinline__ float up(T v) { return __half2float(v); }
+    static __device__ __forceinline__ T down(float v) { return __float2half_rn(v); }
+    static __device__ __forceinline__ float2 up2(uint32_t v) { return __half22float2(*reinterpret_cast<__half2 *>(&v)); }
+    static __device__ __forceinline__ uint32_t down2(float a, float b) {
+        __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+};
+template <>
+struct Elem<SPX_BF16> {
+    using T = __nv_bfloat16;
+    static __device__ __forceinline__ float up(T v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ T down(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ float2 up2(uint32_t v) {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t down2(float a, float b) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+};
+template <>
+struct Elem<SPX_F32> {
+    using T = float;
+    static __device__ __forceinline__ float up(T v) { return v; }
+    static __device__ __forceinline__ T down(float v) { return v; }
+};
+
+struct LatentParams {
+    // cache
+    const uint16_t *cache;
+    int64_t page_stride, token_stride;
+    int num_pages, page_size, R, P;
+    const int32_t *table;
+    int max_pages, B;
+    const int32_t *lens;
+    // call
+    int N, heads, max_q, max_len, dn, dv, causal;
+    int64_t q_stride, out_stride;
+    const int32_t *q_start;
+    const uint16_t *q, *w_uk, *w_uv;
+    uint16_t *out;
+    float *lse;
+    float scale, scale_log2;  // scale_log2 = scale * log2(e)
+    // workspace
+    WsHeader *hdr;
+    uint64_t budget;
+    uint16_t *q_lat;  // [N][heads][R + P]
+    float *o_lat;     // [N][heads][R]
+};
+
+// A request's query rows and cached length, cut to the call's bounds, so that
+// no content of q_start or lens leads out of a buffer.
+struct LatentReq {
+    int row0, T, len;
+};
+__device__ __forceinline__ LatentReq latent_req(const LatentParams &p, int b) {
+    LatentReq r;
+    const int s = __ldg(p.q_start + b), e = __ldg(p.q_start + b + 1);
+    r.row0 = min(max(s, 0), p.N);
+    r.T = min(min(max(e - r.row0, 0), p.max_q), p.N - r.row0);
+    const long long cap = (long long)p.max_pages * p.page_size;
+    r.len = (int)min((long long)min(max(__ldg(p.lens + b), 0), p.max_len), cap);
+    return r;
+}
+// Positions that token t of the request sees: [0, limit).
+__device__ __forceinline__ int latent_limit(const LatentParams &p, const LatentReq &r, int t) {
+    return p.causal ? max(r.len - r.T + t + 1, 0) : r.len;
+}
+
+}  // namespace spx

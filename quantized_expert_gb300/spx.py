@@ -66,6 +66,34 @@ class LayerArgs(C.Structure):
                 ("gguf", C.POINTER(GgufExperts)), ("verify_launch", C.c_int)]
 
 
+class LatentCacheC(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("cache", C.c_void_p), ("num_pages", C.c_int), ("page_size", C.c_int),
+                ("R", C.c_int), ("P", C.c_int), ("page_stride", C.c_int64), ("token_stride", C.c_int64),
+                ("block_table", C.c_void_p), ("max_pages", C.c_int), ("B", C.c_int), ("lens", C.c_void_p)]
+
+
+class LatentAppendArgs(C.Structure):
+    _fields_ = [("cache", C.POINTER(LatentCacheC)), ("N", C.c_int), ("kv", C.c_void_p), ("kv_stride", C.c_int64),
+                ("req", C.c_void_p), ("pos", C.c_void_p), ("w_norm", C.c_void_p), ("eps", C.c_float),
+                ("cos", C.c_void_p), ("sin", C.c_void_p), ("max_pos", C.c_int), ("interleaved", C.c_int),
+                ("q", C.c_void_p), ("q_out", C.c_void_p), ("q_stride", C.c_int64), ("q_out_stride", C.c_int64),
+                ("heads", C.c_int), ("q_width", C.c_int)]
+
+
+class LatentArgs(C.Structure):
+    _fields_ = [("cache", C.POINTER(LatentCacheC)), ("N", C.c_int), ("heads", C.c_int), ("q", C.c_void_p),
+                ("q_stride", C.c_int64), ("out_stride", C.c_int64), ("q_start", C.c_void_p), ("max_q", C.c_int),
+                ("max_len", C.c_int), ("w_uk", C.c_void_p), ("w_uv", C.c_void_p), ("dn", C.c_int), ("dv", C.c_int),
+                ("scale", C.c_float), ("causal", C.c_int), ("out", C.c_void_p), ("lse", C.c_void_p),
+                ("form", C.c_int), ("ws", C.c_void_p), ("ws_bytes", C.c_size_t), ("wait_budget_ns", C.c_uint64)]
+
+
+class LogprobsArgs(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("logits", C.c_void_p), ("stride", C.c_int64), ("N", C.c_int), ("V", C.c_int),
+                ("k", C.c_int), ("ids", C.c_void_p), ("logp", C.c_void_p), ("entropy", C.c_void_p),
+                ("top_ids", C.c_void_p), ("top_logp", C.c_void_p)]
+
+
 _SIGS = {
     "spx_status_string": (C.c_char_p, [C.c_int]),
     "spx_version": (C.c_int, []),
@@ -110,6 +138,10 @@ _SIGS = {
     "spx_prefetch_issue": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p,
                                      C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_void_p]),
     "spx_noalloc_status": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "spx_latent_append": (C.c_int, [C.POINTER(LatentAppendArgs), C.c_void_p]),
+    "spx_latent_attention": (C.c_int, [C.POINTER(LatentArgs), C.c_void_p]),
+    "spx_latent_workspace_size": (C.c_size_t, [C.c_int] * 10),
+    "spx_token_logprobs": (C.c_int, [C.POINTER(LogprobsArgs), C.c_void_p]),
 }
 
 
@@ -521,3 +553,181 @@ def spx_prefetch_issue(actions, host_experts, dev_experts, expert_bytes: int, re
     _chk(load().spx_prefetch_issue(acts.ctypes.data, int(acts.shape[0]), hp, dp, int(expert_bytes), _p(ready),
                                    _p(resident), C.c_void_p(prefetch_host_flags().data_ptr()), L, E,
                                    _stream(stream)), "spx_prefetch_issue")
+
+
+# ------------------------------------- latent attention, log probabilities --
+SPX_F16, SPX_BF16, SPX_F32 = 0, 1, 2
+SPX_LATENT_AUTO, SPX_LATENT_ABSORBED, SPX_LATENT_EXPANDED = 0, 1, 2
+_DTYPES = {torch.float16: SPX_F16, torch.bfloat16: SPX_BF16, torch.float32: SPX_F32}
+
+
+def _dt(t) -> int:
+    if t.dtype not in _DTYPES:
+        raise SpxError(SPX_ERR_UNSUPPORTED, f"element type {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _same(t, ref, what: str):
+    if t is not None and t.dtype != ref.dtype:
+        raise ValueError(f"{what}: {t.dtype}, expected {ref.dtype}")
+
+
+def _i32(t, what: str, shape=None):
+    if t.dtype != torch.int32 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what}: int32 {tuple(shape) if shape is not None else ''} expected, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    return _p(t)
+
+
+def _rows(t, what: str):
+    """Pointer and token stride of a device tensor whose rows (all but its
+    first dimension) are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("libspx takes device tensors")
+    n = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != n:
+            raise ValueError(f"{what}: contiguous rows expected")
+        n *= size
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else n
+
+
+@dataclass
+class LatentCache:
+    """Paged latent cache: buf [pages][page_size][R + P] (page and token strides
+    free, values of a token contiguous), block_table int32 [B][max_pages], lens
+    int32 [B].  See include/spx.h."""
+    buf: torch.Tensor
+    block_table: torch.Tensor
+    lens: torch.Tensor
+    R: int = 512
+    P: int = 64
+
+    def cstruct(self) -> LatentCacheC:
+        b = self.buf
+        if not b.is_cuda or b.dim() != 3 or b.shape[2] != self.R + self.P or b.stride(2) != 1:
+            raise ValueError(f"cache: device tensor [pages][page_size][{self.R + self.P}] expected")
+        B = self.lens.numel()
+        if self.block_table.dim() != 2 or self.block_table.shape[0] != B:
+            raise ValueError("block_table: [B][max_pages] expected")
+        return LatentCacheC(_dt(b), b.data_ptr(), b.shape[0], b.shape[1], self.R, self.P, b.stride(0), b.stride(1),
+                            _i32(self.block_table, "block_table"), self.block_table.shape[1], B,
+                            _i32(self.lens, "lens", (B,)))
+
+
+def latent_append_args(cache: LatentCache, kv, req, pos, w_norm=None, eps=1e-6, cos=None, sin=None, interleaved=True,
+                       q=None, q_out=None):
+    """Build (and keep alive) the argument block of spx_latent_append: kv [N][R + P],
+    req and pos int32 [N], w_norm [R], cos and sin float32 [max_pos][P/2],
+    q and q_out [N][heads][width]."""
+    cs = cache.cstruct()
+    a = LatentAppendArgs()
+    N = kv.shape[0]
+    for t, what in ((kv, "kv"), (w_norm, "w_norm"), (q, "q"), (q_out, "q_out")):
+        _same(t, cache.buf, what)
+    if kv.dim() != 2 or kv.shape[1] != cache.R + cache.P or (w_norm is not None and w_norm.numel() != cache.R):
+        raise ValueError("kv: [N][R + P] and w_norm: [R] expected")
+    a.cache, a.N = C.pointer(cs), N
+    a.kv, a.kv_stride = _rows(kv, "kv")
+    a.req, a.pos, a.w_norm, a.eps = _i32(req, "req", (N,)), _i32(pos, "pos", (N,)), _p(w_norm), float(eps)
+    if cos is not None:
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.shape != sin.shape or \
+                cos.dim() != 2 or cos.shape[1] != cache.P // 2:
+            raise ValueError("cos, sin: float32 [max_pos][P/2] expected")
+        a.cos, a.sin, a.max_pos = _p(cos), _p(sin), cos.shape[0]
+    a.interleaved = int(bool(interleaved))
+    if q is not None:
+        if q_out is None:
+            q_out = q
+        if q.dim() != 3 or q.shape[0] != N or q_out.shape != q.shape:
+            raise ValueError("q, q_out: [N][heads][width] expected")
+        a.q, a.q_stride = _rows(q, "q")
+        a.q_out, a.q_out_stride = _rows(q_out, "q_out")
+        a.heads, a.q_width = q.shape[1], q.shape[2]
+    return a, [cs, cache, kv, req, pos, w_norm, cos, sin, q, q_out]
+
+
+def spx_latent_append(args: LatentAppendArgs, stream=None):
+    _chk(load().spx_latent_append(C.byref(args), _stream(stream)), "spx_latent_append")
+
+
+def spx_latent_workspace_size(B, N, max_q, max_len, heads, R=512, P=64, dn=0, dv=0, form=SPX_LATENT_AUTO) -> int:
+    return load().spx_latent_workspace_size(B, N, max_q, max_len, heads, R, P, dn, dv, form)
+
+
+def new_latent_workspace(q, cache: LatentCache, max_q: int, max_len: int, w_uk=None, w_uv=None,
+                         form=SPX_LATENT_AUTO, stream=None) -> torch.Tensor:
+    """Allocate (through torch) and initialise a workspace for latent_args()."""
+    n = spx_latent_workspace_size(cache.lens.numel(), q.shape[0], max_q, max_len, q.shape[1], cache.R, cache.P,
+                                  w_uk.shape[1] if w_uk is not None else 0, w_uv.shape[1] if w_uv is not None else 0,
+                                  form)
+    if n == 0:
+        raise SpxError(SPX_ERR_UNSUPPORTED, "spx_latent_workspace_size")
+    ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    _chk(load().spx_workspace_init(_p(ws), min(n, 256), _stream(stream)), "spx_workspace_init")
+    return ws
+
+
+def latent_args(q, cache: LatentCache, q_start, max_q: int, max_len: int, scale: float, out, ws, w_uk=None, w_uv=None,
+                causal=True, lse=None, form=SPX_LATENT_AUTO, wait_budget_ns=0):
+    """Build (and keep alive) the argument block of spx_latent_attention: q
+    [N][heads][dn + P] with w_uk [heads][dn][R] and w_uv [heads][dv][R], out
+    [N][heads][dv]; without them q [N][heads][R + P] and out [N][heads][R];
+    lse float32 [N][heads]."""
+    cs = cache.cstruct()
+    a = LatentArgs()
+    for t, what in ((q, "q"), (out, "out"), (w_uk, "w_uk"), (w_uv, "w_uv")):
+        _same(t, cache.buf, what)
+    if (w_uk is None) != (w_uv is None):
+        raise ValueError("w_uk and w_uv: both or neither")
+    N, heads = q.shape[:2]
+    dn, dv = (w_uk.shape[1], w_uv.shape[1]) if w_uk is not None else (0, 0)
+    if tuple(q.shape) != (N, heads, (dn or cache.R) + cache.P) or tuple(out.shape) != (N, heads, dv or cache.R):
+        raise ValueError("q: [N][heads][dn + P] and out: [N][heads][dv] expected (R for dn and dv without weights)")
+    for t, d, what in ((w_uk, dn, "w_uk"), (w_uv, dv, "w_uv")):
+        if t is not None and tuple(t.shape) != (heads, d, cache.R):
+            raise ValueError(f"{what}: [heads][{d}][R] expected")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (N, heads)):
+        raise ValueError("lse: float32 [N][heads] expected")
+    a.cache, a.N, a.heads = C.pointer(cs), N, heads
+    a.q, a.q_stride = _rows(q, "q")
+    a.out, a.out_stride = _rows(out, "out")
+    a.q_start, a.max_q, a.max_len = _i32(q_start, "q_start", (cs.B + 1,)), int(max_q), int(max_len)
+    a.w_uk, a.w_uv, a.dn, a.dv = _p(w_uk), _p(w_uv), dn, dv
+    a.scale, a.causal, a.lse, a.form = float(scale), int(bool(causal)), _p(lse), int(form)
+    a.ws, a.ws_bytes, a.wait_budget_ns = _p(ws), ws.numel() if ws is not None else 0, int(wait_budget_ns)
+    return a, [cs, cache, q, q_start, out, w_uk, w_uv, lse, ws]
+
+
+def spx_latent_attention(args: LatentArgs, stream=None):
+    """Attention of the requests' newest tokens over the paged latent cache
+    (draft and verify calls, prompts).  See include/spx.h."""
+    _chk(load().spx_latent_attention(C.byref(args), _stream(stream)), "spx_latent_attention")
+
+
+def logprobs_args(logits, ids=None, logp=None, entropy=None, top_ids=None, top_logp=None):
+    """Build (and keep alive) the argument block of spx_token_logprobs: logits
+    [N][V] (rows contiguous), ids int32 [N], logp and entropy float32 [N],
+    top_ids int32 and top_logp float32 [N][k]."""
+    if logits.dim() != 2:
+        raise ValueError("logits: [N][V] expected")
+    N, V = logits.shape
+    a = LogprobsArgs()
+    a.dtype, a.N, a.V = _dt(logits), N, V
+    a.logits, a.stride = _rows(logits, "logits")
+    if ids is not None:
+        a.ids = _i32(ids, "ids", (N,))
+    k = top_ids.shape[1] if top_ids is not None else 0
+    for t, shape, what in ((logp, (N,), "logp"), (entropy, (N,), "entropy"), (top_logp, (N, k), "top_logp")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape):
+            raise ValueError(f"{what}: float32 {shape} expected")
+    if top_ids is not None:
+        a.top_ids = _i32(top_ids, "top_ids", (N, k))
+    a.k, a.logp, a.entropy, a.top_logp = k, _p(logp), _p(entropy), _p(top_logp)
+    return a, [logits, ids, logp, entropy, top_ids, top_logp]
+
+
+def spx_token_logprobs(args: LogprobsArgs, stream=None):
+    """Log probabilities of given tokens, entropy and most likely alternatives
+    of rows of logits.  See include/spx.h."""
+    _chk(load().spx_token_logprobs(C.byref(args), _stream(stream)), "spx_token_logprobs")
