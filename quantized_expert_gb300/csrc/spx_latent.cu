@@ -3,155 +3,1053 @@
 // With k[h] = (W_uk[h] c, r) and v[h] = W_uv[h] c the products with the
 // up-projections move out of the sum over the cache:
 //   q_nope . (W_uk c) = (q_nope W_uk) . c,   sum_p w_p W_uv c_p = W_uv sum_p w_p c_p,
-// so the cached (c, r) is read once for all heads.  Three launches: queries to
-// latent space, attention there, results through W_uv.
-#include "spx_latent.cuh"
-
+// so the cached (c, r) is read once for all heads.  Launches:
+//
+//   query launch      q_lat = (q_nope W_uk, q_rope), rounded to the type;
+//   attention launch  softmax(scale q_lat . (c, r)) c in latent space, the
+//                     cache cut into equal shares over the SMs, partial sums
+//                     (with their maximum and weight) where a cut falls;
+//   result launch     partial sums joined, times W_uv (or, with folded
+//                     weights, a launch that only joins).
+//
+// Every launch is a programmatic dependent of the one before it.
 #include <math.h>
+#include <string.h>
+
+#include "spx_latent.cuh"
+#include "spx_tcgen05.cuh"
 
 namespace spx {
 
 namespace {
 
-constexpr int kRows = 4;  // (token, head) rows of one block
-
+// --------------------------------------------------- small tensor products --
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
 template <int DT>
-__global__ void __launch_bounds__(128) latent_q_kernel(LatentParams p) {
-    using E = Elem<DT>;
-    using T = typename E::T;
-    const size_t row = blockIdx.x;
-    const int h = (int)(row % p.heads);
-    const T *q = reinterpret_cast<const T *>(p.q) + (row / p.heads) * p.q_stride + (size_t)h * (p.dn + p.P);
-    T *dst = reinterpret_cast<T *>(p.q_lat) + row * (p.R + p.P);
-    const T *w = reinterpret_cast<const T *>(p.w_uk) + (size_t)h * p.dn * p.R;
-    for (int r = threadIdx.x; r < p.R; r += blockDim.x) {
-        float s = 0.f;
-        for (int d = 0; d < p.dn; ++d) s = fmaf(E::up(q[d]), E::up(w[(size_t)d * p.R + r]), s);
-        dst[r] = E::down(s);
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (DT == SPX_F16) {
+        mma_16816(d, a, b0, b1);
+    } else {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
-    for (int i = threadIdx.x; i < p.P; i += blockDim.x) dst[p.R + i] = q[p.dn + i];
 }
 
-// One block: kRows rows of one request, a warp per cached token, online
-// softmax per warp, the warps' sums joined at the end.
-template <int DT>
-__global__ void __launch_bounds__(256) latent_rows_kernel(LatentParams p) {
-    using E = Elem<DT>;
-    using T = typename E::T;
-    const LatentReq rq = latent_req(p, blockIdx.y);
-    const int nrows = rq.T * p.heads, r0 = blockIdx.x * kRows;
-    if (r0 >= nrows) return;
-    __shared__ float qs[kRows][576];
-    __shared__ float ml[8][kRows][2];
-    __shared__ float os[8][512];
-    const int D = p.R + p.P, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const T *ql = p.w_uk ? reinterpret_cast<const T *>(p.q_lat) : reinterpret_cast<const T *>(p.q);
-    int lim[kRows], most = 0;
-    for (int i = 0; i < kRows; ++i) {
-        const int r = min(r0 + i, nrows - 1), t = r / p.heads, h = r - t * p.heads;
-        lim[i] = latent_limit(p, rq, t);
-        most = max(most, lim[i]);
-        const size_t n = rq.row0 + t;
-        const T *src = p.w_uk ? ql + (n * p.heads + h) * D : ql + n * p.q_stride + (size_t)h * D;
-        for (int d = threadIdx.x; d < D; d += blockDim.x) qs[i][d] = E::up(src[d]) * p.scale_log2;
+// ------------------------------------------------------------ query launch --
+// Block (s, h, g): 16 * MT tokens' queries of head h times columns 64 s .. + 63
+// of W_uk[h]; block s = 0 also copies the rotated part.  A block reads its
+// slice of the weights once for all its tokens; the whole of W_uk is 2 MB for
+// 16 heads, so the launch is bound by latency up to some hundred tokens.
+template <int DT, int MT>
+__global__ void __launch_bounds__(128) latent_q_kernel(const __grid_constant__ LatentParams p) {
+    extern __shared__ __align__(128) uint8_t lq_smem[];
+    const int ldq = p.dn + 8;
+    uint16_t *qs = reinterpret_cast<uint16_t *>(lq_smem);  // [16 MT][dn + 8]
+    uint16_t *ws = qs + 16 * MT * ldq;                     // [dn][72]
+    const int s = blockIdx.x, h = blockIdx.y, n0 = blockIdx.z * 16 * MT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = min(16 * MT, p.N - n0);
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint16_t *wsrc = p.w_uk + (size_t)h * p.dn * p.R + 64 * s;
+    for (int i = threadIdx.x; i < p.dn * 8; i += 128)
+        cp_async16(ws + (i >> 3) * 72 + 8 * (i & 7), wsrc + (size_t)(i >> 3) * p.R + 8 * (i & 7));
+    const int qv = p.dn / 8;
+    for (int i = threadIdx.x; i < 16 * MT * qv; i += 128) {
+        const int r = i / qv, c = i - r * qv;
+        if (r < rows)
+            cp_async16(qs + r * ldq + 8 * c, p.q + (n0 + r) * p.q_stride + (size_t)h * (p.dn + p.P) + 8 * c);
+        else
+            *reinterpret_cast<uint4 *>(qs + r * ldq + 8 * c) = make_uint4(0, 0, 0, 0);
     }
+    cp_async_wait_all();
     __syncthreads();
-    float m[kRows], l[kRows], o[kRows][16];
-    for (int i = 0; i < kRows; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        for (int d = 0; d < 16; ++d) o[i][d] = 0.f;
-    }
-    for (int j = warp; j < most; j += 8) {
-        const int pg = __ldg(p.table + (size_t)blockIdx.y * p.max_pages + j / p.page_size);
-        float kv[18];
-        const bool ok = pg >= 0 && pg < p.num_pages;
-        const T *src = reinterpret_cast<const T *>(p.cache) + (int64_t)(ok ? pg : 0) * p.page_stride +
-                       (int64_t)(j % p.page_size) * p.token_stride;
+    float acc[MT][2][4] = {};
+    for (int k = 0; k < p.dn; k += 16) {
+        uint32_t b[4];
+        ldsm4t(b, ws + (k + (lane & 15)) * 72 + 16 * warp + 8 * (lane >> 4));
 #pragma unroll
-        for (int d = 0; d < 18; ++d) kv[d] = (ok && 32 * d + lane < D) ? E::up(src[32 * d + lane]) : 0.f;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (j >= lim[i]) continue;
-            float s = 0.f;
-#pragma unroll
-            for (int d = 0; d < 18; ++d)
-                if (32 * d + lane < D) s = fmaf(qs[i][32 * d + lane], kv[d], s);
-#pragma unroll
-            for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            const float mn = fmaxf(m[i], s), ref = mn == -INFINITY ? 0.f : mn;
-            const float c = exp2f(m[i] - ref), w = exp2f(s - ref);
-            l[i] = l[i] * c + w;
-#pragma unroll
-            for (int d = 0; d < 16; ++d) o[i][d] = o[i][d] * c + w * kv[d];
-            m[i] = mn;
+        for (int m = 0; m < MT; ++m) {
+            uint32_t a[4];
+            ldsm4(a, qs + (16 * m + (lane & 15)) * ldq + k + 8 * (lane >> 4));
+            mma16816<DT>(acc[m][0], a, b[0], b[1]);
+            mma16816<DT>(acc[m][1], a, b[2], b[3]);
         }
     }
-    for (int i = 0; i < kRows; ++i) {
-        if (lane == 0) {
-            ml[warp][i][0] = m[i];
-            ml[warp][i][1] = l[i];
+    const int D = p.R + p.P;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 16 * m + (lane >> 2) + 8 * (j & 1);
+            if (r < rows)
+                *reinterpret_cast<uint32_t *>(p.q_lat + ((size_t)(n0 + r) * p.heads + h) * D + 64 * s + 16 * warp +
+                                              8 * (j >> 1) + 2 * (lane & 3)) =
+                    Elem<DT>::down2(acc[m][j >> 1][2 * (j & 1)], acc[m][j >> 1][2 * (j & 1) + 1]);
         }
+    if (s == 0)
+        for (int i = threadIdx.x; i < rows * (p.P / 8); i += 128) {
+            const int r = i / (p.P / 8), c = i - r * (p.P / 8);
+            *reinterpret_cast<uint4 *>(p.q_lat + ((size_t)(n0 + r) * p.heads + h) * D + p.R + 8 * c) =
+                *reinterpret_cast<const uint4 *>(p.q + (n0 + r) * p.q_stride + (size_t)h * (p.dn + p.P) + p.dn + 8 * c);
+        }
+}
+
+// Folded queries whose tokens are not contiguous, packed for the attention launch.
+__global__ void __launch_bounds__(128) latent_pack_kernel(const __grid_constant__ LatentParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int per = p.heads * (p.R + p.P) / 8;
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.q + blockIdx.x * p.q_stride);
+    uint4 *dst = reinterpret_cast<uint4 *>(p.q_lat) + (size_t)blockIdx.x * per;
+    for (int i = threadIdx.x; i < per; i += 128) dst[i] = src[i];
+}
+
+// -------------------------------------------------------- attention launch --
+// A unit is a request's rows NR g .. NR g + NR - 1 in (token, head) order; its
+// cache, in tiles of 64 tokens, is one stretch of the call's tiles, which are
+// dealt out in equal contiguous shares, one per block.
+//
+// The products are transposed, so that few rows leave no tensor-core lane
+// idle and one copy of a tile in shared memory serves both:
+//   S^T [64 tokens x rows] = C [64 x (R + P)] . Q^T        (A = the tile, k-major)
+//   O^T [R x rows]        += V^T [R x 64 tokens] . P^T     (A = the tile, m-major)
+// with Q and P as the B operands (N = rows) and O^T in tensor memory (R / 128
+// accumulators of 128 lanes).  S^T has M = 64 (16 lanes of each quarter).
+//
+// Softmax runs in base 2 with one reference per row; the sums are rescaled
+// only when a maximum rises by more than 2^kSlack over it, which fp32 sums and
+// fp16 weights of at most 2^(kSlack + kShift) bear.  kShift moves the weights
+// away from the subnormals of fp16.
+constexpr int kTile = 64;
+constexpr float kSlack = 8.f, kShift = 5.f;
+constexpr int kAttnThreads = 192;  // copies, products, 4 softmax warps
+constexpr int kPairBytes = kTile * 256;  // 64 tokens x 128 latent values, as two 64-value halves
+constexpr int kRopeBytes = kTile * 128;
+constexpr int kPBytes = kTile * 128;
+
+// Ring depths by rows per unit, as shared memory allows.  Tiles are handled in
+// pairs (both S, then both O), so at least two tiles (8 pairs) stay resident.
+template <int NR>
+struct AttnGeo {
+    static constexpr int kPairs = NR <= 32 ? 10 : 8;
+    static constexpr int kRopes = NR <= 16 ? 3 : 2;
+    static constexpr int kQBytes = 9 * NR * 128;
+    static constexpr int kMisc = 3072;
+    static constexpr int kSmem = kQBytes + kPBytes + kPairs * kPairBytes + kRopes * kRopeBytes + kMisc;
+    static constexpr uint32_t kTmem = NR <= 16 ? 128 : NR <= 32 ? 256 : 512;  // >= 6 NR, a power of two
+    static_assert(kSmem <= kSmemLimit, "shared memory of one block");
+};
+
+struct AttnMisc {
+    uint64_t pfull[12], pempty[12], rfull[4], rempty[4];  // copies landed / slot free
+    uint64_t qfull, qempty;       // the unit's queries landed / read for the last time
+    uint64_t sfull[2];            // S^T of a tile is in tensor memory
+    uint64_t wfull;               // a tile's weights are in shared memory (4 warps)
+    uint64_t odone;               // O^T has taken a tile
+    uint64_t ofree;               // O^T of the unit has been read out (4 warps)
+    uint64_t fin;                 // products drained (abort path)
+    uint32_t tmem;
+    int abort;
+    int b, g, off, flat, left, share;  // tiles of a share, and where this block's begins
+    int pad[2];
+    int lim[64];                  // positions that each row sees
+    float fac[64];
+    float red[2][4][64];
+};
+static_assert(sizeof(AttnMisc) <= 3072, "the misc area holds it");
+
+struct AttnMaps {
+    CUtensorMap cache;  // [pages][page_size][R + P], boxes of 64 values x gcd(page_size, 64) tokens
+    CUtensorMap q;      // [N * heads][R + P], boxes of 64 values x NR rows
+};
+
+template <int NR>
+__device__ __forceinline__ int unit_tiles(const LatentParams &p, const LatentReq &r, int g) {
+    const int rows = r.T * p.heads;
+    if (g * NR >= rows) return 0;
+    const int last = (min((g + 1) * NR, rows) - 1) / p.heads;
+    return (latent_limit(p, r, last) + kTile - 1) / kTile;
+}
+
+// A block's walk over its share, unit by unit; the same in every role.
+template <int NR>
+struct Walk {
+    int b, g, nt;        // unit, its tiles
+    int tile, end;       // tiles of the unit in this share
+    int flat, left;      // index of `tile` among the call's tiles; tiles left from `tile` on
+    bool first;          // the share begins inside or with this unit
+    LatentReq rq;
+    __device__ __forceinline__ void begin(const LatentParams &p, const AttnMisc &m) {
+        b = m.b;
+        g = m.g;
+        flat = m.flat;
+        left = m.left;
+        first = true;
+        if (left <= 0) return;
+        rq = latent_req(p, b);
+        nt = unit_tiles<NR>(p, rq, g);
+        tile = m.off;
+        end = min(nt, tile + left);
     }
-    for (int i = 0; i < kRows; ++i) {
-        __syncthreads();
-        for (int d = 0; d < 16; ++d) os[warp][32 * d + lane] = o[i][d];
-        __syncthreads();
-        if (r0 + i >= nrows) continue;
-        float mx = -INFINITY, L = 0.f;
-        for (int w = 0; w < 8; ++w) mx = fmaxf(mx, ml[w][i][0]);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        for (int w = 0; w < 8; ++w) L += ml[w][i][1] * exp2f(ml[w][i][0] - ref);
-        const int r = r0 + i, t = r / p.heads, h = r - t * p.heads;
-        const size_t row = (size_t)(rq.row0 + t) * p.heads + h;
-        const bool none = lim[i] <= 0;
-        for (int d = threadIdx.x; d < p.R; d += blockDim.x) {
-            float a = 0.f;
-            for (int w = 0; w < 8; ++w) a += ml[w][i][1] == 0.f ? 0.f : os[w][d] * exp2f(ml[w][i][0] - ref);
-            a = none ? 0.f : a / L;
-            if (p.w_uv)
-                p.o_lat[row * p.R + d] = a;
-            else
-                reinterpret_cast<T *>(p.out)[(rq.row0 + t) * p.out_stride + (size_t)h * p.R + d] = E::down(a);
+    __device__ __forceinline__ void next(const LatentParams &p) {
+        left -= end - tile;
+        flat += end - tile;
+        first = false;
+        if (left <= 0) return;
+        ++g;
+        while (true) {
+            nt = unit_tiles<NR>(p, rq, g);
+            if (nt > 0) break;
+            if ((g + 1) * NR < rq.T * p.heads) {
+                ++g;
+                continue;
+            }
+            if (++b >= p.B) {  // does not happen while tiles are left
+                left = 0;
+                return;
+            }
+            rq = latent_req(p, b);
+            g = 0;
         }
-        if (p.lse && threadIdx.x == 0) p.lse[row] = none ? -INFINITY : (mx + log2f(L)) * 0.693147180559945f;
+        tile = 0;
+        end = min(nt, left);
+    }
+};
+
+// One warp: all tiles of the call, this block's share, and where it begins.
+template <int NR>
+__device__ __forceinline__ void find_share(const LatentParams &p, AttnMisc &m, int lane) {
+    int total = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        const int share = pass ? max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1) : 0;
+        const int from = share * (int)blockIdx.x;
+        if (pass) {
+            const int left = min(share, total - from);
+            if (lane == 0) {
+                m.left = left;
+                m.flat = from;
+                m.share = share;
+            }
+            if (left <= 0) return;
+        }
+        int before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int n = 0;
+            LatentReq r{0, 0, 0};
+            if (b0 + lane < p.B) {
+                r = latent_req(p, b0 + lane);
+                for (int g = 0; g * NR < r.T * p.heads; ++g) n += unit_tiles<NR>(p, r, g);
+            }
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const int sum = __shfl_sync(0xffffffffu, incl, 31);
+            if (pass) {
+                const int lo = before + incl - n;
+                const bool mine = n > 0 && from >= lo && from < lo + n;
+                if (mine) {
+                    int off = from - lo, g = 0;
+                    while (off >= unit_tiles<NR>(p, r, g)) off -= unit_tiles<NR>(p, r, g++);
+                    m.b = b0 + lane;
+                    m.g = g;
+                    m.off = off;
+                }
+                if (__any_sync(0xffffffffu, mine)) return;
+            }
+            before += sum;
+        }
+        total = before;
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(128) latent_out_kernel(LatentParams p) {
-    using E = Elem<DT>;
-    using T = typename E::T;
-    const size_t row = blockIdx.x;
-    const int h = (int)(row % p.heads);
-    const float *o = p.o_lat + row * p.R;
-    for (int v = threadIdx.x; v < p.dv; v += blockDim.x) {
-        const T *w = reinterpret_cast<const T *>(p.w_uv) + ((size_t)h * p.dv + v) * p.R;
-        float s = 0.f;
-        for (int r = 0; r < p.R; ++r) s = fmaf(o[r], E::up(w[r]), s);
-        reinterpret_cast<T *>(p.out)[(row / p.heads) * p.out_stride + (size_t)h * p.dv + v] = E::down(s);
+template <int DT, int NR>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    latent_attn_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ AttnMaps maps) {
+    using G = AttnGeo<NR>;
+    constexpr int PR = G::kPairs, RR = G::kRopes;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *qs = smem, *ps = qs + G::kQBytes, *pairs = ps + kPBytes, *ropes = pairs + PR * kPairBytes;
+    AttnMisc &m = *reinterpret_cast<AttnMisc *>(ropes + RR * kRopeBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int np = p.R / 128;  // pairs of a tile
+
+    if (!p.chained) griddep_wait();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < PR; ++i) {
+            mbar_init(&m.pfull[i], 1);
+            mbar_init(&m.pempty[i], 1);
+        }
+        for (int i = 0; i < RR; ++i) {
+            mbar_init(&m.rfull[i], 1);
+            mbar_init(&m.rempty[i], 1);
+        }
+        mbar_init(&m.qfull, 1);
+        mbar_init(&m.qempty, 1);
+        mbar_init(&m.sfull[0], 1);
+        mbar_init(&m.sfull[1], 1);
+        mbar_init(&m.wfull, 4);
+        mbar_init(&m.odone, 1);
+        mbar_init(&m.ofree, 4);
+        mbar_init(&m.fin, 1);
+        m.abort = 0;
+        fence_mbar_init();
+        prefetch_tmap(&maps.cache);
+        prefetch_tmap(&maps.q);
+    }
+    if (warp == 0) find_share<NR>(p, m, lane);
+    if (warp == 1) {
+        tmem_alloc(&m.tmem, G::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();
+    const uint32_t tmem = m.tmem;
+    const uint32_t s_col = (uint32_t)(np * NR);  // S^T buffers after the R / 128 parts of O^T
+    const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_LATENT};
+    Walk<NR> w;
+
+    if (warp == 0 && lane == 0) {
+        // ---- copies: a tile is np pairs and a rotated part, in boxes that do not cross a page
+        const uint64_t pol = p.groups > 1 ? policy_evict_normal() : policy_evict_first();
+        const uint64_t pol_q = policy_evict_last();
+        const int bt = p.box_tokens, nb = kTile / bt;
+        uint32_t it = 0, rt = 0, seg = 0;
+        bool ok = true, waited = !p.chained;
+        for (w.begin(p, m); ok && w.left > 0; w.next(p), ++seg) {
+            const int32_t *tab = p.table + (size_t)w.b * p.max_pages;
+            for (int i = w.tile; ok && i < w.end; ++i) {
+                int page[4], at[4];
+                for (int j = 0; j < nb; ++j) {
+                    const int pos = kTile * i + bt * j, pi = pos / p.page_size;
+                    at[j] = pos - pi * p.page_size;
+                    // positions past the length come as zeros (a page out of range)
+                    int pg = pos < w.rq.len ? __ldg(tab + pi) : p.num_pages;
+                    page[j] = pg < 0 || pg >= p.num_pages ? p.num_pages : pg;
+                }
+                for (int c = 0; ok && c < np; ++c, ++it) {
+                    const int s = (int)(it % PR);
+                    ok = ctl_wait(&m.pempty[s], ((it / PR) & 1) ^ 1, ctl);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&m.pfull[s], kPairBytes);
+                    for (int hf = 0; hf < 2; ++hf)
+                        for (int j = 0; j < nb; ++j)
+                            tma_load_3d(pairs + s * kPairBytes + hf * (kPairBytes / 2) + j * bt * 128, &maps.cache,
+                                        128 * c + 64 * hf, at[j], page[j], &m.pfull[s], pol);
+                }
+                if (!ok) break;
+                const int s = (int)(rt % RR);
+                ok = ctl_wait(&m.rempty[s], ((rt / RR) & 1) ^ 1, ctl);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&m.rfull[s], kRopeBytes);
+                for (int j = 0; j < nb; ++j)
+                    tma_load_3d(ropes + s * kRopeBytes + j * bt * 128, &maps.cache, p.R, at[j], page[j], &m.rfull[s],
+                                pol);
+                ++rt;
+                if (i == w.tile) {
+                    // the unit's queries, behind its first tile (which needs no earlier launch of the call)
+                    if (!waited) {
+                        griddep_wait();
+                        waited = true;
+                    }
+                    ok = ctl_wait(&m.qempty, (seg & 1) ^ 1, ctl);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&m.qfull, (uint32_t)(2 * np + 1) * NR * 128);
+                    const int row = w.rq.row0 * p.heads + NR * w.g;
+                    for (int c = 0; c < 2 * np + 1; ++c)
+                        tma_load_2d(qs + c * NR * 128, &maps.q, 64 * c, row, &m.qfull, pol_q);
+                }
+            }
+        }
+        if (!waited) griddep_wait();
+        if (!ok) {  // copies in flight land before the block ends
+            for (uint32_t j = it > PR ? it - PR : 0; j < it; ++j) ctl_drain(&m.pfull[j % PR], (j / PR) & 1, 100000000ull);
+            for (uint32_t j = rt > RR ? rt - RR : 0; j < rt; ++j) ctl_drain(&m.rfull[j % RR], (j / RR) & 1, 100000000ull);
+            for (uint32_t j = 0; j <= seg && j < 2; ++j) ctl_drain(&m.qfull, (seg - j) & 1, 1000000ull);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ---- products
+        const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
+        const uint32_t qa = smem_u32(qs), pa = smem_u32(ps), kva = smem_u32(pairs), ra = smem_u32(ropes);
+        uint32_t it = 0, tc = 0, seg = 0;
+        bool ok = true;
+        for (w.begin(p, m); ok && w.left > 0; w.next(p), ++seg) {
+            const int n16 = (min(NR, w.rq.T * p.heads - NR * w.g) + 15) & ~15;
+            const uint32_t idS = idesc_f16_f32(64, n16) | fmt;
+            const uint32_t idO = idesc_f16_f32(128, n16) | fmt | kIdescAMn | kIdescBMn;
+            const int nt = w.end - w.tile;
+            if (!(ok = ctl_wait(&m.qfull, seg & 1, ctl))) break;
+            tc_fence_after();
+            for (int i = 0; ok && i < nt; i += 2) {
+                const int two = min(2, nt - i);
+                for (int d = 0; ok && d < two; ++d) {
+                    const uint32_t t = tc + d, sd = tmem + s_col + (t & 1) * NR;
+                    for (int c = 0; c < np; ++c) {
+                        const uint32_t k = it + d * np + c, s = k % PR;
+                        if (!(ok = ctl_wait(&m.pfull[s], (k / PR) & 1, ctl))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            umma_f16(sd, sw128_desc(kva + s * kPairBytes + (j >> 2) * (kPairBytes / 2) + 32 * (j & 3)),
+                                     sw128_desc(qa + (2 * c + (j >> 2)) * NR * 128 + 32 * (j & 3)), idS, (c | j) != 0);
+                    }
+                    if (!ok) break;
+                    const uint32_t s = t % RR;
+                    if (!(ok = ctl_wait(&m.rfull[s], (t / RR) & 1, ctl))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        umma_f16(sd, sw128_desc(ra + s * kRopeBytes + 32 * j),
+                                 sw128_desc(qa + 2 * np * NR * 128 + 32 * j), idS, 1);
+                    umma_commit(&m.rempty[s]);
+                    umma_commit(&m.sfull[t & 1]);
+                    if (i + d == nt - 1) umma_commit(&m.qempty);
+                }
+                for (int d = 0; ok && d < two; ++d) {
+                    if (i + d == 0 && !(ok = ctl_wait(&m.ofree, (seg & 1) ^ 1, ctl))) break;
+                    if (!(ok = ctl_wait(&m.wfull, (tc + d) & 1, ctl))) break;
+                    tc_fence_after();
+                    for (int c = 0; c < np; ++c) {
+                        const uint32_t s = (it + d * np + c) % PR;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            umma_f16(tmem + c * NR, sw128_desc_mn(kva + s * kPairBytes + 2048 * j, kPairBytes / 2),
+                                     sw128_desc_mn(pa + 2048 * j, 0), idO, (i + d) != 0 || j != 0);
+                        umma_commit(&m.pempty[s]);
+                    }
+                    umma_commit(&m.odone);
+                }
+                it += two * np;
+                tc += two;
+            }
+        }
+        if (m.abort) {
+            umma_commit(&m.fin);
+            ctl_drain(&m.fin, 0, 100000000ull);
+        }
+    } else if (warp >= 2) {
+        // ---- softmax, rescaling, results
+        const int q = warp & 3, tid = 32 * q + lane;  // tensor-memory quarter; index among the 128
+        const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16);
+        constexpr int NB = NR / 8;
+        const int cl = 2 * (lane & 3);  // this lane's columns: 8x + cl, 8x + cl + 1
+        const int tok = 16 * q + (lane >> 2);  // its tokens: tok, tok + 8
+        uint32_t tc = 0;
+        bool ok = true;
+        // (after a wait that gave up the loop runs on, as every warp has to meet the barriers)
+        for (w.begin(p, m); w.left > 0; w.next(p)) {
+            const int rows = min(NR, w.rq.T * p.heads - NR * w.g), n16 = (rows + 15) & ~15;
+            const int row0 = NR * w.g;
+            bar_sync(1, 128);  // the last unit's limits and sums are read
+            if (tid < NR) m.lim[tid] = tid < rows ? latent_limit(p, w.rq, (row0 + tid) / p.heads) : 0;
+            bar_sync(1, 128);
+            const int lim_lo = m.lim[0], lim_hi = m.lim[rows - 1];
+            float mr[2 * NB], l[2 * NB];
+#pragma unroll
+            for (int c = 0; c < 2 * NB; ++c) {
+                mr[c] = -INFINITY;
+                l[c] = 0.f;
+            }
+            for (int i = w.tile; i < w.end; ++i, ++tc) {
+                ok &= ctl_wait(&m.sfull[tc & 1], (tc >> 1) & 1, ctl);
+                tc_fence_after();
+                uint32_t r[4 * NB];
+#pragma unroll
+                for (int x = 0; x < NB; x += 2)
+                    tmem_ld_16x256b_x2(quarter + s_col + (tc & 1) * NR + 8 * x, r + 4 * x);
+                tmem_wait_ld();
+                const int p0 = kTile * i;
+                const bool masked = p0 + kTile > lim_lo;
+                float mx[2 * NB];
+#pragma unroll
+                for (int x = 0; x < NB; ++x) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = __uint_as_float(r[4 * x + e]) * p.scale_log2;
+                        if (masked && p0 + tok + 8 * (e >> 1) >= m.lim[8 * x + cl + (e & 1)]) v = -INFINITY;
+                        if (8 * x >= n16) v = -INFINITY;
+                        r[4 * x + e] = __float_as_uint(v);
+                    }
+                    mx[2 * x] = fmaxf(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 2]));
+                    mx[2 * x + 1] = fmaxf(__uint_as_float(r[4 * x + 1]), __uint_as_float(r[4 * x + 3]));
+                }
+#pragma unroll
+                for (int c = 0; c < 2 * NB; ++c)
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
+                float(*red)[64] = m.red[tc & 1];
+                if (lane < 4)
+#pragma unroll
+                    for (int x = 0; x < NB; ++x)
+                        *reinterpret_cast<float2 *>(&red[q][8 * x + cl]) = make_float2(mx[2 * x], mx[2 * x + 1]);
+                bar_sync(1, 128);
+                bool rise = false;
+#pragma unroll
+                for (int x = 0; x < NB; ++x) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 v = *reinterpret_cast<const float2 *>(&red[k][8 * x + cl]);
+                        mx[2 * x] = fmaxf(mx[2 * x], v.x);
+                        mx[2 * x + 1] = fmaxf(mx[2 * x + 1], v.y);
+                    }
+                    rise |= mx[2 * x] > mr[2 * x] + kSlack || mx[2 * x + 1] > mr[2 * x + 1] + kSlack;
+                }
+                if (__any_sync(0xffffffffu, rise)) {  // the same in all four warps
+#pragma unroll
+                    for (int c = 0; c < 2 * NB; ++c) {
+                        const float mn = fmaxf(mr[c], mx[c]);
+                        const float f = mn == mr[c] ? 1.f : ex2(mr[c] - mn);
+                        mr[c] = mn;
+                        l[c] *= f;
+                        if (q == 0 && lane < 4) m.fac[8 * (c >> 1) + cl + (c & 1)] = f;
+                    }
+                    if (i > w.tile) {
+                        bar_sync(1, 128);
+                        ok &= ctl_wait(&m.odone, (tc - 1) & 1, ctl);
+                        tc_fence_after();
+                        for (int c = 0; c < np; ++c)
+#pragma unroll
+                            for (int x = 0; x < NR; x += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(quarter + c * NR + x, o);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * m.fac[x + k]);
+                                tmem_st16(quarter + c * NR + x, o);
+                            }
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < NB; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float ref = mr[2 * x + (e & 1)];
+                        const float v = ex2(__uint_as_float(r[4 * x + e]) - (ref == -INFINITY ? 0.f : ref - kShift));
+                        l[2 * x + (e & 1)] += v;
+                        r[4 * x + e] = __float_as_uint(v);
+                    }
+                // the weights' buffer is free once the tile before has been taken
+                if (i > w.tile) ok &= ctl_wait(&m.odone, (tc - 1) & 1, ctl);
+#pragma unroll
+                for (int x = 0; x < NB; ++x)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int t = tok + 8 * k;
+                        *reinterpret_cast<uint32_t *>(ps + t * 128 + 16 * (x ^ (t & 7)) + 2 * cl) =
+                            Elem<DT>::down2(__uint_as_float(r[4 * x + 2 * k]), __uint_as_float(r[4 * x + 2 * k + 1]));
+                    }
+                if (masked) {
+                    // What some row may not see has weight 0 there, and 0 times an infinity or a NaN would
+                    // still reach it: rows of the tile that nobody sees become 0, and in those that only
+                    // some see every value that is not finite (whoever sees it got a NaN from S already).
+                    const uint32_t k0 = tc * np;
+                    for (int c = 0; c < np; ++c) {
+                        uint8_t *base = pairs + ((k0 + c) % PR) * kPairBytes;
+                        const int t0 = max(lim_lo - p0, 0);
+                        for (int e = tid; e < (kTile - t0) * 16; e += 128) {
+                            const int t = t0 + (e >> 4), k = e & 15;
+                            uint4 *at = reinterpret_cast<uint4 *>(base + (k >> 3) * (kPairBytes / 2) + t * 128 +
+                                                                  16 * (k & 7));
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (p0 + t < lim_hi) {
+                                v = *at;
+                                uint32_t *h = &v.x;
+                                constexpr uint32_t kExp = DT == SPX_F16 ? 0x7C00u : 0x7F80u;
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    if ((h[y] & kExp) == kExp) h[y] &= 0xFFFF0000u;
+                                    if (((h[y] >> 16) & kExp) == kExp) h[y] &= 0x0000FFFFu;
+                                }
+                            }
+                            *at = v;
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.wfull);
+            }
+            // ---- results of the unit, or of its part in this share
+            ok &= ctl_wait(&m.odone, (tc - 1) & 1, ctl);
+            tc_fence_after();
+            const bool whole = w.tile == 0 && w.end == w.nt;
+            const int slot = 2 * (int)blockIdx.x + (w.first ? 0 : 1);
+            if (tid == 0 && w.tile == 0)
+                p.units[(size_t)w.b * p.groups + w.g] =
+                    make_int4((int)blockIdx.x, (w.flat + w.nt - 1) / m.share, slot, whole);
+            float(*red)[64] = m.red[tc & 1];
+            long long *at = reinterpret_cast<long long *>(m.red[(tc & 1) ^ 1]);
+#pragma unroll
+            for (int c = 0; c < 2 * NB; ++c) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
+                if (lane < 4) {
+                    const int col = 8 * (c >> 1) + cl + (c & 1);
+                    red[q][col] = l[c];
+                    if (q == 0) m.fac[col] = mr[c];
+                }
+            }
+            bar_sync(1, 128);
+            if (tid < rows) {
+                const float L = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid], M = m.fac[tid];
+                const long long row = (long long)w.rq.row0 * p.heads + row0 + tid;
+                if (whole) {
+                    m.fac[tid] = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
+                    if (p.lse) p.lse[row] = (M + log2f(L) - kShift) * 0.6931471805599453f;
+                    at[tid] = p.w_uv ? row * p.R : row / p.heads * p.out_stride + row % p.heads * p.R;
+                } else {
+                    m.fac[tid] = 1.f;
+                    p.ml[(size_t)slot * NR + tid] = make_float2(M, L);
+                    at[tid] = ((long long)slot * NR + tid) * p.R;
+                }
+            }
+            bar_sync(1, 128);
+            float *dst = whole ? p.o_lat : p.part;
+            const bool direct = whole && !p.w_uv;
+            for (int c = 0; c < np; ++c) {
+                const int d = 128 * c + tid;
+#pragma unroll
+                for (int x = 0; x < NR; x += 16) {
+                    if (x >= rows) continue;
+                    uint32_t o[16];
+                    tmem_ld16(quarter + c * NR + x, o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (x + k < rows) {
+                            const float v = __uint_as_float(o[k]) * m.fac[x + k];
+                            if (direct)
+                                reinterpret_cast<typename Elem<DT>::T *>(p.out)[at[x + k] + d] = Elem<DT>::down(v);
+                            else
+                                dst[at[x + k] + d] = v;
+                        }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.ofree);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, G::kTmem);
     }
 }
 
+// ----------------------------------------------------------- result launch --
+// What became of a row of the call: its unit's shares, or nothing.
+struct RowSum {
+    int first, last, slot, col;  // blocks of the unit's shares, first slot, row within the unit
+    bool whole, none, owned;
+};
+// Warp-wide: the request of query row n, then the unit of (n, head h).
+__device__ __forceinline__ RowSum find_row(const LatentParams &p, int n, int h, int lane) {
+    RowSum r{0, -1, 0, 0, false, true, false};
+    int b = -1;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        bool in = false;
+        if (b0 + lane < p.B) {
+            const LatentReq rq = latent_req(p, b0 + lane);
+            in = n >= rq.row0 && n < rq.row0 + rq.T;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, in);
+        if (hit) {
+            b = b0 + __ffs(hit) - 1;
+            break;
+        }
+    }
+    if (b < 0) return r;
+    r.owned = true;
+    const LatentReq rq = latent_req(p, b);
+    const int row = (n - rq.row0) * p.heads + h, g = row / p.nr;
+    r.col = row - g * p.nr;
+    const int last = (min((g + 1) * p.nr, rq.T * p.heads) - 1) / p.heads;
+    if (latent_limit(p, rq, last) <= 0) return r;  // a unit without tiles
+    const int4 u = __ldcg(p.units + (size_t)b * p.groups + g);
+    r.first = u.x;
+    r.last = u.y;
+    r.slot = u.z;
+    r.whole = u.w != 0;
+    r.none = false;
+    return r;
+}
+__device__ __forceinline__ int slot_of(const RowSum &r, int c) { return c == r.first ? r.slot : 2 * c; }
+// Warp-wide: reference and total weight of a row's partial sums.
+__device__ __forceinline__ float2 join_weights(const LatentParams &p, const RowSum &r, int lane) {
+    float M = -INFINITY, L = 0.f;
+    for (int c = r.first + lane; c <= r.last; c += 32) {
+        const float2 v = __ldcg(p.ml + (size_t)slot_of(r, c) * p.nr + r.col);
+        const float mn = fmaxf(M, v.x);
+        L = (M == -INFINITY ? L : L * ex2(M - mn)) + (v.x == -INFINITY ? v.y : v.y * ex2(v.x - mn));
+        M = mn;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+        const float mn = fmaxf(M, m2);
+        L = (M == -INFINITY ? L : L * ex2(M - mn)) + (m2 == -INFINITY ? l2 : l2 * ex2(m2 - mn));
+        M = mn;
+    }
+    return make_float2(M, L);
+}
+// Factor of one share's sums.
+__device__ __forceinline__ float share_factor(const LatentParams &p, const RowSum &r, int c, float2 j) {
+    const float m = __ldcg(p.ml + (size_t)slot_of(r, c) * p.nr + r.col).x;
+    return m == -INFINITY ? 0.f : ex2(m - j.x) / j.y;
+}
+__device__ __forceinline__ float joined_lse(float2 j) { return (j.x + log2f(j.y) - kShift) * 0.6931471805599453f; }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ float2 cluster_ld2(const void *p, uint32_t rank) {
+    uint32_t a;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// Cluster of R / 64 blocks per (head h, 16 MT tokens): block s joins the
+// partial sums of latent columns 64 s .. + 63, multiplies them by that slice of
+// W_uv[h] and the cluster adds the slices up.  The joined sums enter the
+// product as two values of the type (v and what its rounding left), which
+// costs nothing here and saves a rounding.
+template <int DT, int MT>
+__global__ void __launch_bounds__(256) latent_out_kernel(const __grid_constant__ LatentParams p) {
+    extern __shared__ __align__(128) uint8_t lo_smem[];
+    uint16_t *wv = reinterpret_cast<uint16_t *>(lo_smem);          // [dv][72]
+    uint16_t *hi = wv + p.dv * 72, *lo = hi + 16 * MT * 72;        // [16 MT][72] each
+    float *part = reinterpret_cast<float *>(lo + 16 * MT * 72);    // [16 MT][dv]
+    __shared__ float2 spread[8][32];
+    const int s = blockIdx.x, h = blockIdx.y, n0 = blockIdx.z * 16 * MT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = min(16 * MT, p.N - n0);
+    const uint16_t *wsrc = p.w_uv + (size_t)h * p.dv * p.R + 64 * s;
+    for (int i = threadIdx.x; i < p.dv * 8; i += 256)
+        cp_async16(wv + (i >> 3) * 72 + 8 * (i & 7), wsrc + (size_t)(i >> 3) * p.R + 8 * (i & 7));
+    for (int i = rows * 9 + threadIdx.x; i < 16 * MT * 9; i += 256)  // rows past the last token
+        reinterpret_cast<uint4 *>(hi)[i] = reinterpret_cast<uint4 *>(lo)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int wp = rows >= 8 ? 1 : rows >= 4 ? 2 : rows >= 2 ? 4 : 8;  // warps that share a row's partial sums
+    const int sub = warp % wp, half = lane >> 4, d4 = 4 * (lane & 15);
+    for (int r0 = 0; r0 < rows; r0 += 8 / wp) {
+        const int r = r0 + warp / wp;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+            const RowSum u = find_row(p, n0 + r, h, lane);
+            const size_t row = (size_t)(n0 + r) * p.heads + h;
+            if (!u.none && u.whole) {
+                if (sub == 0 && half == 0) a = __ldcg(reinterpret_cast<const float4 *>(p.o_lat + row * p.R + 64 * s + d4));
+            } else if (!u.none) {
+                const float2 j = join_weights(p, u, lane);
+#pragma unroll 4
+                for (int c = u.first + 2 * sub + half; c <= u.last; c += 2 * wp) {
+                    const float f = share_factor(p, u, c, j);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                        p.part + ((size_t)slot_of(u, c) * p.nr + u.col) * p.R + 64 * s + d4));
+                    a.x = fmaf(f, v.x, a.x);
+                    a.y = fmaf(f, v.y, a.y);
+                    a.z = fmaf(f, v.z, a.z);
+                    a.w = fmaf(f, v.w, a.w);
+                }
+                if (s == 0 && sub == 0 && lane == 0 && p.lse) p.lse[row] = joined_lse(j);
+            } else if (u.owned && s == 0 && sub == 0 && lane == 0 && p.lse) {
+                p.lse[row] = -INFINITY;
+            }
+        }
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
+        a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
+        a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
+        if (wp > 1) {
+            if (half == 0) {
+                spread[warp][2 * lane] = make_float2(a.x, a.y);
+                spread[warp][2 * lane + 1] = make_float2(a.z, a.w);
+            }
+            __syncthreads();
+            if (sub == 0 && half == 0)
+                for (int k = 1; k < wp; ++k) {
+                    const float2 y = spread[warp + k][2 * lane], z = spread[warp + k][2 * lane + 1];
+                    a.x += y.x;
+                    a.y += y.y;
+                    a.z += z.x;
+                    a.w += z.y;
+                }
+            __syncthreads();
+        }
+        if (sub == 0 && half == 0) {
+            const uint2 v = make_uint2(Elem<DT>::down2(a.x, a.y), Elem<DT>::down2(a.z, a.w));
+            const float2 y = Elem<DT>::up2(v.x), z = Elem<DT>::up2(v.y);
+            *reinterpret_cast<uint2 *>(hi + r * 72 + d4) = v;
+            *reinterpret_cast<uint2 *>(lo + r * 72 + d4) =
+                make_uint2(Elem<DT>::down2(a.x - y.x, a.y - y.y), Elem<DT>::down2(a.z - z.x, a.w - z.y));
+        }
+    }
+    cp_async_wait_all();
+    __syncthreads();
+    for (int v0 = 16 * warp; v0 < p.dv; v0 += 128) {
+        float acc[MT][2][4] = {};
+#pragma unroll
+        for (int k = 0; k < 64; k += 16) {
+            uint32_t b[4];
+            ldsm4(b, wv + (v0 + (lane & 7) + 8 * (lane >> 4)) * 72 + k + 8 * ((lane >> 3) & 1));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                uint32_t a[4];
+                ldsm4(a, hi + (16 * m + (lane & 15)) * 72 + k + 8 * (lane >> 4));
+                mma16816<DT>(acc[m][0], a, b[0], b[1]);
+                mma16816<DT>(acc[m][1], a, b[2], b[3]);
+                ldsm4(a, lo + (16 * m + (lane & 15)) * 72 + k + 8 * (lane >> 4));
+                mma16816<DT>(acc[m][0], a, b[0], b[1]);
+                mma16816<DT>(acc[m][1], a, b[2], b[3]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float2 *>(part + (16 * m + (lane >> 2) + 8 * (j & 1)) * p.dv + v0 + 8 * (j >> 1) +
+                                            2 * (lane & 3)) =
+                    make_float2(acc[m][j >> 1][2 * (j & 1)], acc[m][j >> 1][2 * (j & 1) + 1]);
+    }
+    cluster_arrive();
+    cluster_wait();
+    const int ns = p.R / 64, pairs = rows * p.dv / 2;
+    const uint32_t rank = cluster_rank();
+    for (int i = (int)rank * 256 + threadIdx.x; i < pairs; i += ns * 256) {
+        float2 a = make_float2(0.f, 0.f);
+        for (int k = 0; k < ns; ++k) {
+            const float2 v = cluster_ld2(part + 2 * i, (uint32_t)k);
+            a.x += v.x;
+            a.y += v.y;
+        }
+        const int r = 2 * i / p.dv, v = 2 * i - r * p.dv;
+        *reinterpret_cast<uint32_t *>(p.out + (n0 + r) * p.out_stride + (size_t)h * p.dv + v) =
+            Elem<DT>::down2(a.x, a.y);
+    }
+    cluster_arrive();
+    cluster_wait();
+}
+
+// Folded weights: one block per row joins its partial sums, 4 columns a thread
+// and four threads a column; rows of whole units are there already.
 template <int DT>
-int launch(const LatentParams &p, cudaStream_t s) {
-    int st = SPX_OK;
-    if (p.w_uk) {
-        latent_q_kernel<DT><<<p.N * p.heads, 128, 0, s>>>(p);
-        if ((st = record_launch(cudaGetLastError()))) return st;
+__global__ void __launch_bounds__(512) latent_join_kernel(const __grid_constant__ LatentParams p) {
+    __shared__ float4 spread[3][128];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int row = blockIdx.x, n = row / p.heads, h = row - n * p.heads, lane = threadIdx.x & 31;
+    const int sub = threadIdx.x >> 7, d4 = 4 * (threadIdx.x & 127);
+    const RowSum u = find_row(p, n, h, lane);
+    if (u.whole || !u.owned) return;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float lse = -INFINITY;
+    if (!u.none) {
+        const float2 j = join_weights(p, u, lane);
+        if (d4 < p.R)
+#pragma unroll 4
+            for (int c = u.first + sub; c <= u.last; c += 4) {
+                const float f = share_factor(p, u, c, j);
+                const float4 v = __ldcg(
+                    reinterpret_cast<const float4 *>(p.part + ((size_t)slot_of(u, c) * p.nr + u.col) * p.R + d4));
+                a.x = fmaf(f, v.x, a.x);
+                a.y = fmaf(f, v.y, a.y);
+                a.z = fmaf(f, v.z, a.z);
+                a.w = fmaf(f, v.w, a.w);
+            }
+        lse = joined_lse(j);
     }
-    const long long gx = ((long long)p.max_q * p.heads + kRows - 1) / kRows;
-    latent_rows_kernel<DT><<<dim3((unsigned)gx, p.B), 256, 0, s>>>(p);
-    if ((st = record_launch(cudaGetLastError()))) return st;
-    if (p.w_uv) {
-        latent_out_kernel<DT><<<p.N * p.heads, 128, 0, s>>>(p);
-        st = record_launch(cudaGetLastError());
+    if (sub) spread[sub - 1][threadIdx.x & 127] = a;
+    __syncthreads();
+    if (sub || d4 >= p.R) return;
+    for (int k = 0; k < 3; ++k) {
+        const float4 v = spread[k][threadIdx.x];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
     }
-    return st;
+    *reinterpret_cast<uint2 *>(p.out + n * p.out_stride + (size_t)h * p.R + d4) =
+        make_uint2(Elem<DT>::down2(a.x, a.y), Elem<DT>::down2(a.z, a.w));
+    if (threadIdx.x == 0 && p.lse) p.lse[row] = lse;
+}
+
+// -------------------------------------------------------------------- host --
+cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr, int cluster) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    c.attrs = attr;
+    c.numAttrs = cluster > 1 ? 2 : 1;
+    return c;
+}
+
+template <auto kernel>
+int set_smem(size_t bytes) {
+    static thread_local int done_dev = -1;  // one per kernel
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return record_launch(e);
+    if (done_dev == dev) return SPX_OK;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return record_launch(e);
+    done_dev = dev;
+    return SPX_OK;
+}
+
+bool map3(CUtensorMap *m, int dt, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
+          uint32_t box1) {
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {d0, d1, d2};
+    const cuuint64_t strides[2] = {s1, s2};
+    const cuuint32_t box[3] = {64, box1, 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, dt == SPX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+bool map2(CUtensorMap *m, int dt, const void *base, uint64_t d0, uint64_t d1, uint64_t s1, uint32_t box1) {
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {d0, d1};
+    const cuuint64_t strides[1] = {s1};
+    const cuuint32_t box[2] = {64, box1};
+    const cuuint32_t es[2] = {1, 1};
+    return fn(m, dt == SPX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+constexpr int kMaxBlocks = 160;  // blocks of the attention launch: one per SM, at most this many
+
+template <int DT, int NR>
+int launch_attn(const LatentParams &p, const AttnMaps &maps, int blocks, cudaStream_t s) {
+    int st = set_smem<latent_attn_kernel<DT, NR>>(AttnGeo<NR>::kSmem);
+    if (st) return st;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t c = config(dim3(blocks), kAttnThreads, AttnGeo<NR>::kSmem, s, attr, 1);
+    return record_launch(cudaLaunchKernelEx(&c, latent_attn_kernel<DT, NR>, p, maps));
+}
+
+// Tokens per block of the products with the up-projections: 64 once there are
+// enough of them to fill the SMs (16 heads x 8 slices of blocks per group).
+int token_tiles(int N) { return N > 64 ? 4 : 1; }
+
+template <int DT>
+int launch_q(const LatentParams &p, cudaStream_t s) {
+    cudaLaunchAttribute attr[2];
+    if (!p.w_uk) {
+        cudaLaunchConfig_t c = config(dim3(p.N), 128, 0, s, attr, 1);
+        return record_launch(cudaLaunchKernelEx(&c, latent_pack_kernel, p));
+    }
+    const int mt = token_tiles(p.N);
+    const size_t smem = (size_t)(16 * mt * (p.dn + 8) + p.dn * 72) * 2;
+    cudaLaunchConfig_t c = config(dim3(p.R / 64, p.heads, (p.N + 16 * mt - 1) / (16 * mt)), 128, smem, s, attr, 1);
+    return record_launch(mt == 1 ? cudaLaunchKernelEx(&c, latent_q_kernel<DT, 1>, p)
+                                 : cudaLaunchKernelEx(&c, latent_q_kernel<DT, 4>, p));
+}
+
+template <int DT, int MT>
+int launch_out_mt(const LatentParams &p, cudaStream_t s) {
+    const size_t smem = (size_t)(p.dv * 72 + 2 * 16 * MT * 72) * 2 + (size_t)16 * MT * p.dv * 4;
+    const int st = set_smem<latent_out_kernel<DT, MT>>((size_t)(128 * 72 + 2 * 16 * MT * 72) * 2 + (size_t)16 * MT * 512);
+    if (st) return st;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t c =
+        config(dim3(p.R / 64, p.heads, (p.N + 16 * MT - 1) / (16 * MT)), 256, smem, s, attr, p.R / 64);
+    return record_launch(cudaLaunchKernelEx(&c, latent_out_kernel<DT, MT>, p));
+}
+
+template <int DT>
+int launch_absorbed(LatentParams &p, int dtype, bool packed, cudaStream_t s) {
+    int st;
+    p.chained = p.w_uk || !packed;
+    const void *q = p.chained ? p.q_lat : p.q;
+    const int D = p.R + p.P;
+    AttnMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    const uint64_t page_b = (uint64_t)p.page_stride * 2, tok_b = (uint64_t)p.token_stride * 2;
+    if (!map3(&maps.cache, dtype, p.cache, D, p.page_size, p.num_pages, tok_b,
+              p.num_pages > 1 ? page_b : (page_b > tok_b ? page_b : tok_b), p.box_tokens) ||
+        !map2(&maps.q, dtype, q, D, (uint64_t)p.N * p.heads, (uint64_t)D * 2, p.nr))
+        return SPX_ERR_UNSUPPORTED;
+    const int sms = device_sm_count();
+    if (sms < 1) return SPX_ERR_CUDA;
+    const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
+    if (p.chained && (st = launch_q<DT>(p, s))) return st;
+    st = p.nr == 16 ? launch_attn<DT, 16>(p, maps, blocks, s)
+         : p.nr == 32 ? launch_attn<DT, 32>(p, maps, blocks, s)
+                      : launch_attn<DT, 64>(p, maps, blocks, s);
+    if (st) return st;
+    if (p.w_uv) return token_tiles(p.N) == 1 ? launch_out_mt<DT, 1>(p, s) : launch_out_mt<DT, 4>(p, s);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t c = config(dim3(p.N * p.heads), 512, 0, s, attr, 1);
+    return record_launch(cudaLaunchKernelEx(&c, latent_join_kernel<DT>, p));
+}
+
+// Rows per unit: the call's largest request in one unit where 16 or 32 rows
+// hold it (least padding), else 64, the most that shared memory leaves room for.
+int rows_per_unit(int max_q, int heads) {
+    const long long rows = (long long)max_q * heads;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 constexpr size_t kHdr = 256;
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+// The workspace of the absorbed form.
+struct AbsorbedLayout {
+    size_t units, ml, part, q_lat, o_lat, bytes;
+};
+AbsorbedLayout absorbed_layout(int B, int N, int max_q, int heads, int R, int P, bool weights) {
+    const int nr = rows_per_unit(max_q, heads);
+    const size_t groups = ((size_t)max_q * heads + nr - 1) / nr;
+    AbsorbedLayout l;
+    l.units = kHdr;
+    l.ml = l.units + up256((size_t)B * groups * 16);
+    l.part = l.ml + up256((size_t)2 * kMaxBlocks * 64 * 8);
+    l.q_lat = l.part + up256((size_t)2 * kMaxBlocks * nr * R * 4);
+    l.o_lat = l.q_lat + up256((size_t)N * heads * (R + P) * 2);
+    l.bytes = l.o_lat + (weights ? up256((size_t)N * heads * R * 4) : 0);
+    return l;
+}
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
@@ -179,9 +1077,7 @@ extern "C" size_t spx_latent_workspace_size(int B, int N, int max_q, int max_len
     if (R < 128 || R > 512 || R % 128 || P != 64 || heads > 1024 || B > 65535) return 0;
     if ((dn != 0) != (dv != 0) || (dn && dn != 64 && dn != 128) || (dv && dv != 64 && dv != 128)) return 0;
     if (form == SPX_LATENT_EXPANDED) return 0;
-    size_t n = kHdr;
-    if (dn) n += up256((size_t)N * heads * (R + P) * 2) + up256((size_t)N * heads * R * 4);
-    return n;
+    return absorbed_layout(B, N, max_q, heads, R, P, dn != 0).bytes;
 }
 
 extern "C" int spx_latent_attention(const spx_latent_args *a, spx_stream_t stream) {
@@ -216,7 +1112,7 @@ extern "C" int spx_latent_attention(const spx_latent_args *a, spx_stream_t strea
     p.lens = c.lens;
     p.N = a->N;
     p.heads = a->heads;
-    p.max_q = a->max_q < a->N ? a->max_q : a->N;
+    p.max_q = a->max_q;
     p.max_len = a->max_len;
     p.dn = a->dn;
     p.dv = a->dv;
@@ -233,8 +1129,18 @@ extern "C" int spx_latent_attention(const spx_latent_args *a, spx_stream_t strea
     p.scale_log2 = a->scale * 1.4426950408889634f;
     uint8_t *ws = static_cast<uint8_t *>(a->ws);
     p.hdr = reinterpret_cast<WsHeader *>(ws);
-    p.q_lat = reinterpret_cast<uint16_t *>(ws + kHdr);
-    p.o_lat = reinterpret_cast<float *>(ws + kHdr + up256((size_t)a->N * a->heads * (c.R + c.P) * 2));
+    p.budget = a->wait_budget_ns ? a->wait_budget_ns : 2000000000ull;
+    const AbsorbedLayout l = absorbed_layout(c.B, a->N, a->max_q, a->heads, c.R, c.P, p.w_uk != nullptr);
+    p.nr = rows_per_unit(a->max_q, a->heads);
+    p.groups = (int)(((long long)a->max_q * a->heads + p.nr - 1) / p.nr);
+    p.box_tokens = c.page_size % 64 == 0 ? 64 : c.page_size % 32 == 0 ? 32 : 16;
+    p.units = reinterpret_cast<int4 *>(ws + l.units);
+    p.ml = reinterpret_cast<float2 *>(ws + l.ml);
+    p.part = reinterpret_cast<float *>(ws + l.part);
+    p.q_lat = reinterpret_cast<uint16_t *>(ws + l.q_lat);
+    p.o_lat = reinterpret_cast<float *>(ws + l.o_lat);
+    const bool packed = a->q_stride == qw || a->N == 1;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return c.dtype == SPX_F16 ? launch<SPX_F16>(p, s) : launch<SPX_BF16>(p, s);
+    return c.dtype == SPX_F16 ? launch_absorbed<SPX_F16>(p, c.dtype, packed, s)
+                              : launch_absorbed<SPX_BF16>(p, c.dtype, packed, s);
 }

@@ -62,7 +62,13 @@ struct LatentParams {
     WsHeader *hdr;
     uint64_t budget;
     uint16_t *q_lat;  // [N][heads][R + P]
-    float *o_lat;     // [N][heads][R]
+    float *o_lat;     // [N][heads][R]: rows of units that one share holds whole
+    int4 *units;      // [B][groups]: first and last block of its shares, first slot, whole
+    float2 *ml;       // [slots][nr]: reference and weight of a partial sum
+    float *part;      // [slots][nr][R]: partial sums; block c has slots 2c (its first unit) and 2c + 1 (its last)
+    // geometry of the attention launch
+    int nr, groups, box_tokens;
+    int chained;      // a launch of this call precedes the attention launch
 };
 
 // A request's query rows and cached length, cut to the call's bounds, so that
