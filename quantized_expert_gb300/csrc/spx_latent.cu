@@ -326,44 +326,49 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_LATENT};
     Walk<NR> w;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ---- copies: a tile is np pairs and a rotated part, in boxes that do not cross a page
         const uint64_t pol = p.groups > 1 ? policy_evict_normal() : policy_evict_first();
-        const uint64_t pol_q = policy_evict_last();
         const int bt = p.box_tokens, nb = kTile / bt;
         uint32_t it = 0, rt = 0, seg = 0;
         bool ok = true, waited = !p.chained;
         for (w.begin(p, m); ok && w.left > 0; w.next(p), ++seg) {
             const int32_t *tab = p.table + (size_t)w.b * p.max_pages;
-            for (int i = w.tile; ok && i < w.end; ++i) {
-                int page[4], at[4];
-                for (int j = 0; j < nb; ++j) {
-                    const int pos = kTile * i + bt * j, pi = pos / p.page_size;
-                    at[j] = pos - pi * p.page_size;
+            int box = 32, my_page = 0, my_at = 0;  // this lane's box of the 32 looked up together
+            for (int i = w.tile; ok && i < w.end; ++i, box += nb) {
+                if (box >= 32) {
+                    const int pos = kTile * i + bt * lane, pi = pos / p.page_size;
+                    my_at = pos - pi * p.page_size;
                     // positions past the length come as zeros (a page out of range)
-                    int pg = pos < w.rq.len ? __ldg(tab + pi) : p.num_pages;
-                    page[j] = pg < 0 || pg >= p.num_pages ? p.num_pages : pg;
+                    my_page = pos < w.rq.len ? __ldg(tab + pi) : p.num_pages;
+                    if (my_page < 0 || my_page >= p.num_pages) my_page = p.num_pages;
+                    box = 0;
                 }
-                for (int c = 0; ok && c < np; ++c, ++it) {
-                    const int s = (int)(it % PR);
-                    ok = ctl_wait(&m.pempty[s], ((it / PR) & 1) ^ 1, ctl);
+#pragma unroll 1
+                for (int c = 0; c <= np; ++c) {  // c == np: the rotated part
+                    const bool rope = c == np;
+                    const uint32_t k = rope ? rt : it, s = rope ? rt % RR : it % PR;
+                    uint64_t *full = rope ? &m.rfull[s] : &m.pfull[s];
+                    ok = ctl_wait(rope ? &m.rempty[s] : &m.pempty[s], ((k / (rope ? RR : PR)) & 1) ^ 1, ctl);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(&m.pfull[s], kPairBytes);
-                    for (int hf = 0; hf < 2; ++hf)
-                        for (int j = 0; j < nb; ++j)
-                            tma_load_3d(pairs + s * kPairBytes + hf * (kPairBytes / 2) + j * bt * 128, &maps.cache,
-                                        128 * c + 64 * hf, at[j], page[j], &m.pfull[s], pol);
+                    uint8_t *dst = rope ? ropes + s * kRopeBytes : pairs + s * kPairBytes;
+                    const bool lead = elect_one();
+                    if (lead) mbar_arrive_expect_tx(full, rope ? kRopeBytes : kPairBytes);
+#pragma unroll 1
+                    for (int j = 0; j < nb; ++j) {
+                        const int at = __shfl_sync(0xffffffffu, my_at, box + j);
+                        const int page = __shfl_sync(0xffffffffu, my_page, box + j);
+                        if (lead) {
+                            tma_load_3d(dst + j * bt * 128, &maps.cache, 128 * c, at, page, full, pol);
+                            if (!rope)
+                                tma_load_3d(dst + kPairBytes / 2 + j * bt * 128, &maps.cache, 128 * c + 64, at, page,
+                                            full, pol);
+                        }
+                    }
+                    if (rope) ++rt;
+                    else ++it;
                 }
-                if (!ok) break;
-                const int s = (int)(rt % RR);
-                ok = ctl_wait(&m.rempty[s], ((rt / RR) & 1) ^ 1, ctl);
-                if (!ok) break;
-                mbar_arrive_expect_tx(&m.rfull[s], kRopeBytes);
-                for (int j = 0; j < nb; ++j)
-                    tma_load_3d(ropes + s * kRopeBytes + j * bt * 128, &maps.cache, p.R, at[j], page[j], &m.rfull[s],
-                                pol);
-                ++rt;
-                if (i == w.tile) {
+                if (ok && i == w.tile) {
                     // the unit's queries, behind its first tile (which needs no earlier launch of the call)
                     if (!waited) {
                         griddep_wait();
@@ -371,10 +376,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     ok = ctl_wait(&m.qempty, (seg & 1) ^ 1, ctl);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(&m.qfull, (uint32_t)(2 * np + 1) * NR * 128);
-                    const int row = w.rq.row0 * p.heads + NR * w.g;
-                    for (int c = 0; c < 2 * np + 1; ++c)
-                        tma_load_2d(qs + c * NR * 128, &maps.q, 64 * c, row, &m.qfull, pol_q);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&m.qfull, (uint32_t)(2 * np + 1) * NR * 128);
+                        const int row = w.rq.row0 * p.heads + NR * w.g;
+                        for (int c = 0; c < 2 * np + 1; ++c)
+                            tma_load_2d(qs + c * NR * 128, &maps.q, 64 * c, row, &m.qfull, pol);
+                    }
                 }
             }
         }
@@ -382,12 +389,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (!ok) {  // copies in flight land before the block ends
             for (uint32_t j = it > PR ? it - PR : 0; j < it; ++j) ctl_drain(&m.pfull[j % PR], (j / PR) & 1, 100000000ull);
             for (uint32_t j = rt > RR ? rt - RR : 0; j < rt; ++j) ctl_drain(&m.rfull[j % RR], (j / RR) & 1, 100000000ull);
-            for (uint32_t j = 0; j <= seg && j < 2; ++j) ctl_drain(&m.qfull, (seg - j) & 1, 1000000ull);
+            for (uint32_t j = 0; j < 2 && j <= seg; ++j) ctl_drain(&m.qfull, (seg - j) & 1, 1000000ull);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ---- products
         const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
-        const uint32_t qa = smem_u32(qs), pa = smem_u32(ps), kva = smem_u32(pairs), ra = smem_u32(ropes);
+        const uint64_t qd = sw128_desc(smem_u32(qs)), kd = sw128_desc(smem_u32(pairs)), rd = sw128_desc(smem_u32(ropes));
+        const uint64_t vd = sw128_desc_mn(smem_u32(pairs), kPairBytes / 2), pd = sw128_desc_mn(smem_u32(ps), 0);
         uint32_t it = 0, tc = 0, seg = 0;
         bool ok = true;
         for (w.begin(p, m); ok && w.left > 0; w.next(p), ++seg) {
@@ -396,52 +404,63 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const uint32_t idO = idesc_f16_f32(128, n16) | fmt | kIdescAMn | kIdescBMn;
             const int nt = w.end - w.tile;
             if (!(ok = ctl_wait(&m.qfull, seg & 1, ctl))) break;
-            tc_fence_after();
             for (int i = 0; ok && i < nt; i += 2) {
                 const int two = min(2, nt - i);
+#pragma unroll 1
                 for (int d = 0; ok && d < two; ++d) {
                     const uint32_t t = tc + d, sd = tmem + s_col + (t & 1) * NR;
+#pragma unroll 1
                     for (int c = 0; c < np; ++c) {
                         const uint32_t k = it + d * np + c, s = k % PR;
                         if (!(ok = ctl_wait(&m.pfull[s], (k / PR) & 1, ctl))) break;
                         tc_fence_after();
+                        if (elect_one()) {
+                            // descriptors count in 16 bytes: 32 bytes a k-step, half a pair, a chunk of Q
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            umma_f16(sd, sw128_desc(kva + s * kPairBytes + (j >> 2) * (kPairBytes / 2) + 32 * (j & 3)),
-                                     sw128_desc(qa + (2 * c + (j >> 2)) * NR * 128 + 32 * (j & 3)), idS, (c | j) != 0);
+                            for (int j = 0; j < 8; ++j)
+                                umma_f16(sd, kd + s * (kPairBytes / 16) + (j >> 2) * (kPairBytes / 32) + 2 * (j & 3),
+                                         qd + (2 * c + (j >> 2)) * (NR * 8) + 2 * (j & 3), idS, (c | j) != 0);
+                        }
                     }
                     if (!ok) break;
                     const uint32_t s = t % RR;
                     if (!(ok = ctl_wait(&m.rfull[s], (t / RR) & 1, ctl))) break;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        umma_f16(sd, sw128_desc(ra + s * kRopeBytes + 32 * j),
-                                 sw128_desc(qa + 2 * np * NR * 128 + 32 * j), idS, 1);
-                    umma_commit(&m.rempty[s]);
-                    umma_commit(&m.sfull[t & 1]);
-                    if (i + d == nt - 1) umma_commit(&m.qempty);
+                        for (int j = 0; j < 4; ++j)
+                            umma_f16(sd, rd + s * (kRopeBytes / 16) + 2 * j, qd + 2 * np * (NR * 8) + 2 * j, idS, 1);
+                        umma_commit(&m.rempty[s]);
+                        umma_commit(&m.sfull[t & 1]);
+                        if (i + d == nt - 1) umma_commit(&m.qempty);
+                    }
+                    __syncwarp();
                 }
+#pragma unroll 1
                 for (int d = 0; ok && d < two; ++d) {
                     if (i + d == 0 && !(ok = ctl_wait(&m.ofree, (seg & 1) ^ 1, ctl))) break;
                     if (!(ok = ctl_wait(&m.wfull, (tc + d) & 1, ctl))) break;
                     tc_fence_after();
-                    for (int c = 0; c < np; ++c) {
-                        const uint32_t s = (it + d * np + c) % PR;
+                    if (elect_one()) {
+#pragma unroll 1
+                        for (int c = 0; c < np; ++c) {
+                            const uint32_t s = (it + d * np + c) % PR;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            umma_f16(tmem + c * NR, sw128_desc_mn(kva + s * kPairBytes + 2048 * j, kPairBytes / 2),
-                                     sw128_desc_mn(pa + 2048 * j, 0), idO, (i + d) != 0 || j != 0);
-                        umma_commit(&m.pempty[s]);
+                            for (int j = 0; j < 4; ++j)
+                                umma_f16(tmem + c * NR, vd + s * (kPairBytes / 16) + 128 * j, pd + 128 * j, idO,
+                                         (i + d) != 0 || j != 0);
+                            umma_commit(&m.pempty[s]);
+                        }
+                        umma_commit(&m.odone);
                     }
-                    umma_commit(&m.odone);
+                    __syncwarp();
                 }
                 it += two * np;
                 tc += two;
             }
         }
         if (m.abort) {
-            umma_commit(&m.fin);
+            if (elect_one()) umma_commit(&m.fin);
             ctl_drain(&m.fin, 0, 100000000ull);
         }
     } else if (warp >= 2) {
@@ -482,10 +501,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 for (int x = 0; x < NB; ++x) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float v = __uint_as_float(r[4 * x + e]) * p.scale_log2;
-                        if (masked && p0 + tok + 8 * (e >> 1) >= m.lim[8 * x + cl + (e & 1)]) v = -INFINITY;
-                        if (8 * x >= n16) v = -INFINITY;
-                        r[4 * x + e] = __float_as_uint(v);
+                        const float v = __uint_as_float(r[4 * x + e]) * p.scale_log2;
+                        r[4 * x + e] = __float_as_uint(8 * x < n16 ? v : -INFINITY);
+                    }
+                    if (masked) {
+                        const int2 lim = *reinterpret_cast<const int2 *>(&m.lim[8 * x + cl]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (p0 + tok + 8 * (e >> 1) >= (e & 1 ? lim.y : lim.x)) r[4 * x + e] = 0xFF800000u;
                     }
                     mx[2 * x] = fmaxf(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 2]));
                     mx[2 * x + 1] = fmaxf(__uint_as_float(r[4 * x + 1]), __uint_as_float(r[4 * x + 3]));
@@ -524,9 +547,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         bar_sync(1, 128);
                         ok &= ctl_wait(&m.odone, (tc - 1) & 1, ctl);
                         tc_fence_after();
+#pragma unroll 1
                         for (int c = 0; c < np; ++c)
-#pragma unroll
-                            for (int x = 0; x < NR; x += 16) {
+#pragma unroll 1
+                            for (int x = 0; x < n16; x += 16) {
                                 uint32_t o[16];
                                 tmem_ld16(quarter + c * NR + x, o);
 #pragma unroll
@@ -626,11 +650,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             bar_sync(1, 128);
             float *dst = whole ? p.o_lat : p.part;
             const bool direct = whole && !p.w_uv;
+#pragma unroll 1
             for (int c = 0; c < np; ++c) {
                 const int d = 128 * c + tid;
-#pragma unroll
-                for (int x = 0; x < NR; x += 16) {
-                    if (x >= rows) continue;
+#pragma unroll 1
+                for (int x = 0; x < n16; x += 16) {
                     uint32_t o[16];
                     tmem_ld16(quarter + c * NR + x, o);
 #pragma unroll

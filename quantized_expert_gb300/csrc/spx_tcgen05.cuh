@@ -124,6 +124,19 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// One lane of a converged warp, the same every time.  Products issued under it
+// (rather than under lane == 0) keep their descriptors in uniform registers:
+// 128 x 16 x 16 products then take 39 cycles each instead of 47, 64 x 16 x 16
+// ones 23 instead of 47 (measured; shared memory feeds 128 bytes a cycle).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
