@@ -135,8 +135,8 @@ __global__ void __launch_bounds__(128) latent_pack_kernel(const __grid_constant_
 // away from the subnormals of fp16.
 constexpr int kTile = 64;
 constexpr float kSlack = 8.f, kShift = 5.f;
-constexpr int kAttnThreads = 192;  // copies, products, 4 softmax warps
 constexpr int kPairBytes = kTile * 256;  // 64 tokens x 128 latent values, as two 64-value halves
+constexpr int kMaxBlocks = 160;  // blocks of the attention launch: one per SM, at most this many
 constexpr int kRopeBytes = kTile * 128;
 constexpr int kPBytes = kTile * 128;
 
@@ -146,6 +146,10 @@ template <int NR>
 struct AttnGeo {
     static constexpr int kPairs = NR <= 32 ? 10 : 8;
     static constexpr int kRopes = NR <= 16 ? 3 : 2;
+    // Softmax warps: four (one per quarter of tensor memory) for each share of
+    // the rows: one warp a scheduler cannot keep up with the products on 64 rows.
+    static constexpr int kShares = NR <= 16 ? 1 : 2;
+    static constexpr int kThreads = 64 + 128 * kShares;
     static constexpr int kQBytes = 9 * NR * 128;
     static constexpr int kMisc = 3072;
     static constexpr int kSmem = kQBytes + kPBytes + kPairs * kPairBytes + kRopes * kRopeBytes + kMisc;
@@ -157,9 +161,9 @@ struct AttnMisc {
     uint64_t pfull[12], pempty[12], rfull[4], rempty[4];  // copies landed / slot free
     uint64_t qfull, qempty;       // the unit's queries landed / read for the last time
     uint64_t sfull[2];            // S^T of a tile is in tensor memory
-    uint64_t wfull;               // a tile's weights are in shared memory (4 warps)
+    uint64_t wfull;               // a tile's weights are in shared memory (all softmax warps)
     uint64_t odone;               // O^T has taken a tile
-    uint64_t ofree;               // O^T of the unit has been read out (4 warps)
+    uint64_t ofree;               // O^T of the unit has been read out (all softmax warps)
     uint64_t fin;                 // products drained (abort path)
     uint32_t tmem;
     int abort;
@@ -232,54 +236,56 @@ struct Walk {
 // One warp: all tiles of the call, this block's share, and where it begins.
 template <int NR>
 __device__ __forceinline__ void find_share(const LatentParams &p, AttnMisc &m, int lane) {
-    int total = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        const int share = pass ? max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1) : 0;
-        const int from = share * (int)blockIdx.x;
-        if (pass) {
-            const int left = min(share, total - from);
-            if (lane == 0) {
-                m.left = left;
-                m.flat = from;
-                m.share = share;
-            }
-            if (left <= 0) return;
-        }
+    LatentReq r{0, 0, 0};
+    int n = 0, total = 0, share = 0, from = 0;
+    bool found = false;
+#pragma unroll 1
+    for (int pass = 0; pass < 2 && !found; ++pass) {
         int before = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int n = 0;
-            LatentReq r{0, 0, 0};
-            if (b0 + lane < p.B) {
-                r = latent_req(p, b0 + lane);
-                for (int g = 0; g * NR < r.T * p.heads; ++g) n += unit_tiles<NR>(p, r, g);
+#pragma unroll 1
+        for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
+            if (pass == 0 || p.B > 32) {
+                n = 0;
+                if (b0 + lane < p.B) {
+                    r = latent_req(p, b0 + lane);
+                    for (int g = 0; g * NR < r.T * p.heads; ++g) n += unit_tiles<NR>(p, r, g);
+                }
             }
             int incl = n;
-#pragma unroll
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
-            const int sum = __shfl_sync(0xffffffffu, incl, 31);
             if (pass) {
-                const int lo = before + incl - n;
-                const bool mine = n > 0 && from >= lo && from < lo + n;
+                int off = from - (before + incl - n);
+                const bool mine = off >= 0 && off < n;
                 if (mine) {
-                    int off = from - lo, g = 0;
-                    while (off >= unit_tiles<NR>(p, r, g)) off -= unit_tiles<NR>(p, r, g++);
+                    int g = 0;
+                    for (int u; off >= (u = unit_tiles<NR>(p, r, g)); ++g) off -= u;
                     m.b = b0 + lane;
                     m.g = g;
                     m.off = off;
                 }
-                if (__any_sync(0xffffffffu, mine)) return;
+                found = __any_sync(0xffffffffu, mine);
             }
-            before += sum;
+            before += __shfl_sync(0xffffffffu, incl, 31);
         }
+        if (pass) break;
         total = before;
+        share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
+        from = share * (int)blockIdx.x;
+        if (lane == 0) {
+            m.left = min(share, total - from);
+            m.flat = from;
+            m.share = share;
+        }
+        found = from >= total;
     }
 }
 
 template <int DT, int NR>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
     latent_attn_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ AttnMaps maps) {
     using G = AttnGeo<NR>;
     constexpr int PR = G::kPairs, RR = G::kRopes;
@@ -303,9 +309,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(&m.qempty, 1);
         mbar_init(&m.sfull[0], 1);
         mbar_init(&m.sfull[1], 1);
-        mbar_init(&m.wfull, 4);
+        mbar_init(&m.wfull, 4 * G::kShares);
         mbar_init(&m.odone, 1);
-        mbar_init(&m.ofree, 4);
+        mbar_init(&m.ofree, 4 * G::kShares);
         mbar_init(&m.fin, 1);
         m.abort = 0;
         fence_mbar_init();
@@ -404,33 +410,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const uint32_t idO = idesc_f16_f32(128, n16) | fmt | kIdescAMn | kIdescBMn;
             const int nt = w.end - w.tile;
             if (!(ok = ctl_wait(&m.qfull, seg & 1, ctl))) break;
+#pragma unroll 1
             for (int i = 0; ok && i < nt; i += 2) {
                 const int two = min(2, nt - i);
+                // All of a tile's waits come before its products, which then issue without a gap
+                // (waits between them left 20 to 30 cycles a product).
 #pragma unroll 1
-                for (int d = 0; ok && d < two; ++d) {
-                    const uint32_t t = tc + d, sd = tmem + s_col + (t & 1) * NR;
-#pragma unroll 1
-                    for (int c = 0; c < np; ++c) {
-                        const uint32_t k = it + d * np + c, s = k % PR;
-                        if (!(ok = ctl_wait(&m.pfull[s], (k / PR) & 1, ctl))) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            // descriptors count in 16 bytes: 32 bytes a k-step, half a pair, a chunk of Q
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                umma_f16(sd, kd + s * (kPairBytes / 16) + (j >> 2) * (kPairBytes / 32) + 2 * (j & 3),
-                                         qd + (2 * c + (j >> 2)) * (NR * 8) + 2 * (j & 3), idS, (c | j) != 0);
-                        }
+                for (int d = 0; d < two; ++d) {
+                    const uint32_t t = tc + d, sd = tmem + s_col + (t & 1) * NR, rs = t % RR, s0 = (it + d * np) % PR;
+                    for (int c = 0; ok && c < np; ++c) {
+                        const uint32_t k = it + d * np + c;
+                        ok = ctl_wait(&m.pfull[k % PR], (k / PR) & 1, ctl);
                     }
+                    ok = ok && ctl_wait(&m.rfull[rs], (t / RR) & 1, ctl);
                     if (!ok) break;
-                    const uint32_t s = t % RR;
-                    if (!(ok = ctl_wait(&m.rfull[s], (t / RR) & 1, ctl))) break;
                     tc_fence_after();
                     if (elect_one()) {
+                        // descriptors count in 16 bytes: 32 bytes a k-step, half a pair, a chunk of Q
+                        uint64_t a = kd + s0 * (kPairBytes / 16), q = qd;
+                        uint32_t s = s0;
+#pragma unroll 1
+                        for (int c = 0; c < np; ++c) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            umma_f16(sd, rd + s * (kRopeBytes / 16) + 2 * j, qd + 2 * np * (NR * 8) + 2 * j, idS, 1);
-                        umma_commit(&m.rempty[s]);
+                            for (int j = 0; j < 8; ++j)
+                                umma_f16(sd, a + (j >> 2) * (kPairBytes / 32) + 2 * (j & 3),
+                                         q + (j >> 2) * (NR * 8) + 2 * (j & 3), idS, (c | j) != 0);
+                            q += 2 * NR * 8;
+                            a += kPairBytes / 16;
+                            if (++s == PR) {
+                                s = 0;
+                                a = kd;
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) umma_f16(sd, rd + rs * (kRopeBytes / 16) + 2 * j, q + 2 * j, idS, 1);
+                        umma_commit(&m.rempty[rs]);
                         umma_commit(&m.sfull[t & 1]);
                         if (i + d == nt - 1) umma_commit(&m.qempty);
                     }
@@ -442,14 +456,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (!(ok = ctl_wait(&m.wfull, (tc + d) & 1, ctl))) break;
                     tc_fence_after();
                     if (elect_one()) {
+                        uint32_t s = (it + d * np) % PR;
 #pragma unroll 1
                         for (int c = 0; c < np; ++c) {
-                            const uint32_t s = (it + d * np + c) % PR;
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 umma_f16(tmem + c * NR, vd + s * (kPairBytes / 16) + 128 * j, pd + 128 * j, idO,
                                          (i + d) != 0 || j != 0);
                             umma_commit(&m.pempty[s]);
+                            s = s + 1 == PR ? 0 : s + 1;
                         }
                         umma_commit(&m.odone);
                     }
@@ -465,20 +480,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
     } else if (warp >= 2) {
         // ---- softmax, rescaling, results
-        const int q = warp & 3, tid = 32 * q + lane;  // tensor-memory quarter; index among the 128
+        constexpr int SH = G::kShares, NC = NR / SH, NB = NC / 8;  // rows of a share, in blocks of 8
+        const int q = warp & 3;                                    // tensor-memory quarter
+        const int sh = (warp - 2) >> 2, c0 = NC * sh;              // this warp's share of the rows: c0 ..
+        const int tid = 32 * q + lane, all = 128 * sh + tid;       // index within the share's warps, among all
         const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16);
-        constexpr int NB = NR / 8;
-        const int cl = 2 * (lane & 3);  // this lane's columns: 8x + cl, 8x + cl + 1
+        const int cl = c0 + 2 * (lane & 3);    // this lane's rows: 8x + cl, 8x + cl + 1
         const int tok = 16 * q + (lane >> 2);  // its tokens: tok, tok + 8
         uint32_t tc = 0;
-        bool ok = true;
         // (after a wait that gave up the loop runs on, as every warp has to meet the barriers)
         for (w.begin(p, m); w.left > 0; w.next(p)) {
             const int rows = min(NR, w.rq.T * p.heads - NR * w.g), n16 = (rows + 15) & ~15;
             const int row0 = NR * w.g;
-            bar_sync(1, 128);  // the last unit's limits and sums are read
-            if (tid < NR) m.lim[tid] = tid < rows ? latent_limit(p, w.rq, (row0 + tid) / p.heads) : 0;
-            bar_sync(1, 128);
+            bar_sync(3, 128 * SH);  // the last unit's limits and sums are read
+            if (all < NR) m.lim[all] = all < rows ? latent_limit(p, w.rq, (row0 + all) / p.heads) : 0;
+            bar_sync(3, 128 * SH);
             const int lim_lo = m.lim[0], lim_hi = m.lim[rows - 1];
             float mr[2 * NB], l[2 * NB];
 #pragma unroll
@@ -486,13 +502,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 mr[c] = -INFINITY;
                 l[c] = 0.f;
             }
+#pragma unroll 1
             for (int i = w.tile; i < w.end; ++i, ++tc) {
-                ok &= ctl_wait(&m.sfull[tc & 1], (tc >> 1) & 1, ctl);
+                ctl_wait(&m.sfull[tc & 1], (tc >> 1) & 1, ctl);
                 tc_fence_after();
                 uint32_t r[4 * NB];
 #pragma unroll
                 for (int x = 0; x < NB; x += 2)
-                    tmem_ld_16x256b_x2(quarter + s_col + (tc & 1) * NR + 8 * x, r + 4 * x);
+                    tmem_ld_16x256b_x2(quarter + s_col + (tc & 1) * NR + c0 + 8 * x, r + 4 * x);
                 tmem_wait_ld();
                 const int p0 = kTile * i;
                 const bool masked = p0 + kTile > lim_lo;
@@ -500,11 +517,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                 for (int x = 0; x < NB; ++x) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float v = __uint_as_float(r[4 * x + e]) * p.scale_log2;
-                        r[4 * x + e] = __float_as_uint(8 * x < n16 ? v : -INFINITY);
-                    }
-                    if (masked) {
+                    for (int e = 0; e < 4; ++e) r[4 * x + e] = __float_as_uint(__uint_as_float(r[4 * x + e]) * p.scale_log2);
+                    if (masked || c0 + NC > n16) {
                         const int2 lim = *reinterpret_cast<const int2 *>(&m.lim[8 * x + cl]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -514,15 +528,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     mx[2 * x + 1] = fmaxf(__uint_as_float(r[4 * x + 1]), __uint_as_float(r[4 * x + 3]));
                 }
 #pragma unroll
-                for (int c = 0; c < 2 * NB; ++c)
+                for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
+                    for (int c = 0; c < 2 * NB; ++c) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
                 float(*red)[64] = m.red[tc & 1];
                 if (lane < 4)
 #pragma unroll
                     for (int x = 0; x < NB; ++x)
                         *reinterpret_cast<float2 *>(&red[q][8 * x + cl]) = make_float2(mx[2 * x], mx[2 * x + 1]);
-                bar_sync(1, 128);
+                bar_sync(1 + sh, 128);
                 bool rise = false;
 #pragma unroll
                 for (int x = 0; x < NB; ++x) {
@@ -534,7 +548,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     rise |= mx[2 * x] > mr[2 * x] + kSlack || mx[2 * x + 1] > mr[2 * x + 1] + kSlack;
                 }
-                if (__any_sync(0xffffffffu, rise)) {  // the same in all four warps
+                if (__any_sync(0xffffffffu, rise)) {  // the same in the share's four warps
 #pragma unroll
                     for (int c = 0; c < 2 * NB; ++c) {
                         const float mn = fmaxf(mr[c], mx[c]);
@@ -544,13 +558,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (q == 0 && lane < 4) m.fac[8 * (c >> 1) + cl + (c & 1)] = f;
                     }
                     if (i > w.tile) {
-                        bar_sync(1, 128);
-                        ok &= ctl_wait(&m.odone, (tc - 1) & 1, ctl);
+                        bar_sync(1 + sh, 128);
+                        ctl_wait(&m.odone, (tc - 1) & 1, ctl);
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < np; ++c)
 #pragma unroll 1
-                            for (int x = 0; x < n16; x += 16) {
+                            for (int x = c0; x < min(c0 + NC, n16); x += 16) {
                                 uint32_t o[16];
                                 tmem_ld16(quarter + c * NR + x, o);
 #pragma unroll
@@ -565,20 +579,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                 for (int x = 0; x < NB; ++x)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float ref = mr[2 * x + (e & 1)];
-                        const float v = ex2(__uint_as_float(r[4 * x + e]) - (ref == -INFINITY ? 0.f : ref - kShift));
-                        l[2 * x + (e & 1)] += v;
-                        r[4 * x + e] = __float_as_uint(v);
+                    for (int f = 0; f < 2; ++f) {
+                        const float ref = mr[2 * x + f] == -INFINITY ? 0.f : mr[2 * x + f] - kShift;
+                        const float v = ex2(__uint_as_float(r[4 * x + f]) - ref);
+                        const float y = ex2(__uint_as_float(r[4 * x + 2 + f]) - ref);
+                        l[2 * x + f] += v + y;
+                        r[4 * x + f] = __float_as_uint(v);
+                        r[4 * x + 2 + f] = __float_as_uint(y);
                     }
                 // the weights' buffer is free once the tile before has been taken
-                if (i > w.tile) ok &= ctl_wait(&m.odone, (tc - 1) & 1, ctl);
+                if (i > w.tile) ctl_wait(&m.odone, (tc - 1) & 1, ctl);
 #pragma unroll
                 for (int x = 0; x < NB; ++x)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int t = tok + 8 * k;
-                        *reinterpret_cast<uint32_t *>(ps + t * 128 + 16 * (x ^ (t & 7)) + 2 * cl) =
+                        *reinterpret_cast<uint32_t *>(ps + t * 128 + 16 * ((x + c0 / 8) ^ (t & 7)) + 4 * (lane & 3)) =
                             Elem<DT>::down2(__uint_as_float(r[4 * x + 2 * k]), __uint_as_float(r[4 * x + 2 * k + 1]));
                     }
                 if (masked) {
@@ -586,10 +602,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     // still reach it: rows of the tile that nobody sees become 0, and in those that only
                     // some see every value that is not finite (whoever sees it got a NaN from S already).
                     const uint32_t k0 = tc * np;
+                    const int t0 = max(lim_lo - p0, 0);
+#pragma unroll 1
                     for (int c = 0; c < np; ++c) {
                         uint8_t *base = pairs + ((k0 + c) % PR) * kPairBytes;
-                        const int t0 = max(lim_lo - p0, 0);
-                        for (int e = tid; e < (kTile - t0) * 16; e += 128) {
+#pragma unroll 1
+                        for (int e = all; e < (kTile - t0) * 16; e += 128 * SH) {
                             const int t = t0 + (e >> 4), k = e & 15;
                             uint4 *at = reinterpret_cast<uint4 *>(base + (k >> 3) * (kPairBytes / 2) + t * 128 +
                                                                   16 * (k & 7));
@@ -614,58 +632,66 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0) mbar_arrive(&m.wfull);
             }
             // ---- results of the unit, or of its part in this share
-            ok &= ctl_wait(&m.odone, (tc - 1) & 1, ctl);
+            ctl_wait(&m.odone, (tc - 1) & 1, ctl);
             tc_fence_after();
             const bool whole = w.tile == 0 && w.end == w.nt;
             const int slot = 2 * (int)blockIdx.x + (w.first ? 0 : 1);
-            if (tid == 0 && w.tile == 0)
+            if (all == 0 && w.tile == 0)
                 p.units[(size_t)w.b * p.groups + w.g] =
                     make_int4((int)blockIdx.x, (w.flat + w.nt - 1) / m.share, slot, whole);
             float(*red)[64] = m.red[tc & 1];
             long long *at = reinterpret_cast<long long *>(m.red[(tc & 1) ^ 1]);
 #pragma unroll
-            for (int c = 0; c < 2 * NB; ++c) {
+            for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
-                if (lane < 4) {
+                for (int c = 0; c < 2 * NB; ++c) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
+            if (lane < 4)
+#pragma unroll
+                for (int c = 0; c < 2 * NB; ++c) {
                     const int col = 8 * (c >> 1) + cl + (c & 1);
                     red[q][col] = l[c];
                     if (q == 0) m.fac[col] = mr[c];
                 }
-            }
-            bar_sync(1, 128);
-            if (tid < rows) {
-                const float L = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid], M = m.fac[tid];
-                const long long row = (long long)w.rq.row0 * p.heads + row0 + tid;
-                if (whole) {
-                    m.fac[tid] = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
-                    if (p.lse) p.lse[row] = (M + log2f(L) - kShift) * 0.6931471805599453f;
-                    at[tid] = p.w_uv ? row * p.R : row / p.heads * p.out_stride + row % p.heads * p.R;
-                } else {
-                    m.fac[tid] = 1.f;
-                    p.ml[(size_t)slot * NR + tid] = make_float2(M, L);
-                    at[tid] = ((long long)slot * NR + tid) * p.R;
-                }
-            }
-            bar_sync(1, 128);
-            float *dst = whole ? p.o_lat : p.part;
+            bar_sync(3, 128 * SH);
             const bool direct = whole && !p.w_uv;
+            const long long first_row = (long long)w.rq.row0 * p.heads + row0;
+            if (all < rows) {
+                const float L = red[0][all] + red[1][all] + red[2][all] + red[3][all], M = m.fac[all];
+                const long long row = first_row + all;
+                if (whole) {
+                    m.fac[all] = M == -INFINITY && L == 0.f ? 0.f : 1.f / L;
+                    if (p.lse) p.lse[row] = (M + log2f(L) - kShift) * 0.6931471805599453f;
+                } else {
+                    m.fac[all] = 1.f;
+                    p.ml[(size_t)slot * NR + all] = make_float2(M, L);
+                }
+                if (direct) at[all] = row / p.heads * p.out_stride + row % p.heads * p.R;
+            }
+            bar_sync(3, 128 * SH);
+            float *dst = whole ? p.o_lat + first_row * p.R : p.part + (size_t)slot * NR * p.R;
 #pragma unroll 1
-            for (int c = 0; c < np; ++c) {
-                const int d = 128 * c + tid;
+            for (int x = c0; x < min(c0 + NC, n16); x += 16) {
+                float f[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) f[k] = m.fac[x + k];
+                const int left = rows - x;  // rows of these 16
 #pragma unroll 1
-                for (int x = 0; x < n16; x += 16) {
+                for (int c = 0; c < np; ++c) {
+                    const int d = 128 * c + tid;
                     uint32_t o[16];
                     tmem_ld16(quarter + c * NR + x, o);
+                    if (direct) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        if (x + k < rows) {
-                            const float v = __uint_as_float(o[k]) * m.fac[x + k];
-                            if (direct)
-                                reinterpret_cast<typename Elem<DT>::T *>(p.out)[at[x + k] + d] = Elem<DT>::down(v);
-                            else
-                                dst[at[x + k] + d] = v;
-                        }
+                        for (int k = 0; k < 16; ++k)
+                            if (k < left)
+                                reinterpret_cast<typename Elem<DT>::T *>(p.out)[at[x + k] + d] =
+                                    Elem<DT>::down(__uint_as_float(o[k]) * f[k]);
+                    } else {
+                        float *to = dst + (size_t)x * p.R + d;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k, to += p.R)
+                            if (k < left) __stcg(to, __uint_as_float(o[k]) * f[k]);
+                    }
                 }
             }
             tc_fence_before();
@@ -719,28 +745,57 @@ __device__ __forceinline__ RowSum find_row(const LatentParams &p, int n, int h, 
     return r;
 }
 __device__ __forceinline__ int slot_of(const RowSum &r, int c) { return c == r.first ? r.slot : 2 * c; }
-// Warp-wide: reference and total weight of a row's partial sums.
-__device__ __forceinline__ float2 join_weights(const LatentParams &p, const RowSum &r, int lane) {
+// Warp-wide: total weight and reference of a row's partial sums; f[q] becomes
+// the factor of the share r.first + 32 q + lane.  Every load is issued before
+// the first is used: with 150 shares a chain of loads cost 10 us.
+constexpr int kShareChunks = kMaxBlocks / 32;
+__device__ __forceinline__ float2 join_weights(const LatentParams &p, const RowSum &r, int lane, float (&f)[kShareChunks]) {
+    float2 v[kShareChunks];
     float M = -INFINITY, L = 0.f;
-    for (int c = r.first + lane; c <= r.last; c += 32) {
-        const float2 v = __ldcg(p.ml + (size_t)slot_of(r, c) * p.nr + r.col);
-        const float mn = fmaxf(M, v.x);
-        L = (M == -INFINITY ? L : L * ex2(M - mn)) + (v.x == -INFINITY ? v.y : v.y * ex2(v.x - mn));
-        M = mn;
+#pragma unroll
+    for (int q = 0; q < kShareChunks; ++q) {
+        const int c = r.first + 32 * q + lane;
+        v[q] = make_float2(-INFINITY, 0.f);
+        if (c <= r.last) v[q] = __ldcg(p.ml + (size_t)slot_of(r, c) * p.nr + r.col);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
-        const float mn = fmaxf(M, m2);
-        L = (M == -INFINITY ? L : L * ex2(M - mn)) + (m2 == -INFINITY ? l2 : l2 * ex2(m2 - mn));
-        M = mn;
+    for (int q = 0; q < kShareChunks; ++q) M = fmaxf(M, v[q].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+    for (int q = 0; q < kShareChunks; ++q) {
+        f[q] = v[q].x == -INFINITY ? 0.f : ex2(v[q].x - M);
+        L += v[q].x == -INFINITY ? v[q].y : v[q].y * f[q];
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int q = 0; q < kShareChunks; ++q) f[q] *= inv;
     return make_float2(M, L);
 }
-// Factor of one share's sums.
-__device__ __forceinline__ float share_factor(const LatentParams &p, const RowSum &r, int c, float2 j) {
-    const float m = __ldcg(p.ml + (size_t)slot_of(r, c) * p.nr + r.col).x;
-    return m == -INFINITY ? 0.f : ex2(m - j.x) / j.y;
+// Warp-wide: columns d4 .. d4 + 3 of the row's joined sum over the shares
+// first + k0, + step and so on (step at most 32).
+__device__ __forceinline__ float4 join_sums(const LatentParams &p, const RowSum &r, const float (&f)[kShareChunks],
+                                            int k0, int step, int d4) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < kShareChunks; ++q) {
+        const int n = r.last - r.first + 1 - 32 * q;
+#pragma unroll 4
+        for (int k = 0; k < min(n, 32); k += step) {
+            const float g = __shfl_sync(0xffffffffu, f[q], (k + k0) & 31);
+            if (k + k0 < min(n, 32)) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                    p.part + ((size_t)slot_of(r, r.first + 32 * q + k + k0) * p.nr + r.col) * p.R + d4));
+                a.x = fmaf(g, v.x, a.x);
+                a.y = fmaf(g, v.y, a.y);
+                a.z = fmaf(g, v.z, a.z);
+                a.w = fmaf(g, v.w, a.w);
+            }
+        }
+    }
+    return a;
 }
 __device__ __forceinline__ float joined_lse(float2 j) { return (j.x + log2f(j.y) - kShift) * 0.6931471805599453f; }
 
@@ -765,48 +820,45 @@ __device__ __forceinline__ float2 cluster_ld2(const void *p, uint32_t rank) {
 // product as two values of the type (v and what its rounding left), which
 // costs nothing here and saves a rounding.
 template <int DT, int MT>
-__global__ void __launch_bounds__(256) latent_out_kernel(const __grid_constant__ LatentParams p) {
+__global__ void __launch_bounds__(512) latent_out_kernel(const __grid_constant__ LatentParams p) {
     extern __shared__ __align__(128) uint8_t lo_smem[];
     uint16_t *wv = reinterpret_cast<uint16_t *>(lo_smem);          // [dv][72]
     uint16_t *hi = wv + p.dv * 72, *lo = hi + 16 * MT * 72;        // [16 MT][72] each
     float *part = reinterpret_cast<float *>(lo + 16 * MT * 72);    // [16 MT][dv]
-    __shared__ float2 spread[8][32];
+    __shared__ float4 spread[16][16];
     const int s = blockIdx.x, h = blockIdx.y, n0 = blockIdx.z * 16 * MT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = min(16 * MT, p.N - n0);
-    const uint16_t *wsrc = p.w_uv + (size_t)h * p.dv * p.R + 64 * s;
-    for (int i = threadIdx.x; i < p.dv * 8; i += 256)
-        cp_async16(wv + (i >> 3) * 72 + 8 * (i & 7), wsrc + (size_t)(i >> 3) * p.R + 8 * (i & 7));
-    for (int i = rows * 9 + threadIdx.x; i < 16 * MT * 9; i += 256)  // rows past the last token
-        reinterpret_cast<uint4 *>(hi)[i] = reinterpret_cast<uint4 *>(lo)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
-    const int wp = rows >= 8 ? 1 : rows >= 4 ? 2 : rows >= 2 ? 4 : 8;  // warps that share a row's partial sums
+    const uint16_t *wsrc = p.w_uv + (size_t)h * p.dv * p.R + 64 * s;
+    for (int i = threadIdx.x; i < p.dv * 8; i += 512)
+        cp_async16(wv + (i >> 3) * 72 + 8 * (i & 7), wsrc + (size_t)(i >> 3) * p.R + 8 * (i & 7));
+    if (rows < 16 * MT) {  // rows past the last token
+        for (int i = rows * 9 + threadIdx.x; i < 16 * MT * 9; i += 512)
+            reinterpret_cast<uint4 *>(hi)[i] = reinterpret_cast<uint4 *>(lo)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
+    const int wp = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;  // warps that share a row
     const int sub = warp % wp, half = lane >> 4, d4 = 4 * (lane & 15);
-    for (int r0 = 0; r0 < rows; r0 += 8 / wp) {
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 16 / wp) {
         const int r = r0 + warp / wp;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < rows) {
             const RowSum u = find_row(p, n0 + r, h, lane);
             const size_t row = (size_t)(n0 + r) * p.heads + h;
-            if (!u.none && u.whole) {
+            if (u.whole) {
                 if (sub == 0 && half == 0) a = __ldcg(reinterpret_cast<const float4 *>(p.o_lat + row * p.R + 64 * s + d4));
-            } else if (!u.none) {
-                const float2 j = join_weights(p, u, lane);
-#pragma unroll 4
-                for (int c = u.first + 2 * sub + half; c <= u.last; c += 2 * wp) {
-                    const float f = share_factor(p, u, c, j);
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                        p.part + ((size_t)slot_of(u, c) * p.nr + u.col) * p.R + 64 * s + d4));
-                    a.x = fmaf(f, v.x, a.x);
-                    a.y = fmaf(f, v.y, a.y);
-                    a.z = fmaf(f, v.z, a.z);
-                    a.w = fmaf(f, v.w, a.w);
+            } else {
+                float lse = -INFINITY;
+                if (!u.none) {
+                    float f[kShareChunks];
+                    const float2 j = join_weights(p, u, lane, f);
+                    a = join_sums(p, u, f, 2 * sub + half, 2 * wp, 64 * s + d4);
+                    lse = joined_lse(j);
                 }
-                if (s == 0 && sub == 0 && lane == 0 && p.lse) p.lse[row] = joined_lse(j);
-            } else if (u.owned && s == 0 && sub == 0 && lane == 0 && p.lse) {
-                p.lse[row] = -INFINITY;
+                if (u.owned && s == 0 && sub == 0 && lane == 0 && p.lse) p.lse[row] = lse;
             }
         }
         a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
@@ -814,22 +866,19 @@ __global__ void __launch_bounds__(256) latent_out_kernel(const __grid_constant__
         a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
         a.w += __shfl_xor_sync(0xffffffffu, a.w, 16);
         if (wp > 1) {
-            if (half == 0) {
-                spread[warp][2 * lane] = make_float2(a.x, a.y);
-                spread[warp][2 * lane + 1] = make_float2(a.z, a.w);
-            }
+            if (half == 0) spread[warp][lane] = a;
             __syncthreads();
             if (sub == 0 && half == 0)
                 for (int k = 1; k < wp; ++k) {
-                    const float2 y = spread[warp + k][2 * lane], z = spread[warp + k][2 * lane + 1];
-                    a.x += y.x;
-                    a.y += y.y;
-                    a.z += z.x;
-                    a.w += z.y;
+                    const float4 v = spread[warp + k][lane];
+                    a.x += v.x;
+                    a.y += v.y;
+                    a.z += v.z;
+                    a.w += v.w;
                 }
             __syncthreads();
         }
-        if (sub == 0 && half == 0) {
+        if (sub == 0 && half == 0 && r < rows) {
             const uint2 v = make_uint2(Elem<DT>::down2(a.x, a.y), Elem<DT>::down2(a.z, a.w));
             const float2 y = Elem<DT>::up2(v.x), z = Elem<DT>::up2(v.y);
             *reinterpret_cast<uint2 *>(hi + r * 72 + d4) = v;
@@ -839,28 +888,30 @@ __global__ void __launch_bounds__(256) latent_out_kernel(const __grid_constant__
     }
     cp_async_wait_all();
     __syncthreads();
-    for (int v0 = 16 * warp; v0 < p.dv; v0 += 128) {
-        float acc[MT][2][4] = {};
+    const int v0 = 16 * (warp & 7), m0 = MT / 2 * (warp >> 3);  // with 4 m-tiles, half of them a warp
+    if (v0 < p.dv && (MT > 1 || warp < 8)) {
+        constexpr int MW = MT > 1 ? MT / 2 : 1;
+        float acc[MW][2][4] = {};
 #pragma unroll
         for (int k = 0; k < 64; k += 16) {
             uint32_t b[4];
             ldsm4(b, wv + (v0 + (lane & 7) + 8 * (lane >> 4)) * 72 + k + 8 * ((lane >> 3) & 1));
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
+            for (int m = 0; m < MW; ++m) {
                 uint32_t a[4];
-                ldsm4(a, hi + (16 * m + (lane & 15)) * 72 + k + 8 * (lane >> 4));
+                ldsm4(a, hi + (16 * (m0 + m) + (lane & 15)) * 72 + k + 8 * (lane >> 4));
                 mma16816<DT>(acc[m][0], a, b[0], b[1]);
                 mma16816<DT>(acc[m][1], a, b[2], b[3]);
-                ldsm4(a, lo + (16 * m + (lane & 15)) * 72 + k + 8 * (lane >> 4));
+                ldsm4(a, lo + (16 * (m0 + m) + (lane & 15)) * 72 + k + 8 * (lane >> 4));
                 mma16816<DT>(acc[m][0], a, b[0], b[1]);
                 mma16816<DT>(acc[m][1], a, b[2], b[3]);
             }
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MW; ++m)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<float2 *>(part + (16 * m + (lane >> 2) + 8 * (j & 1)) * p.dv + v0 + 8 * (j >> 1) +
+                *reinterpret_cast<float2 *>(part + (16 * (m0 + m) + (lane >> 2) + 8 * (j & 1)) * p.dv + v0 + 8 * (j >> 1) +
                                             2 * (lane & 3)) =
                     make_float2(acc[m][j >> 1][2 * (j & 1)], acc[m][j >> 1][2 * (j & 1) + 1]);
     }
@@ -868,7 +919,7 @@ __global__ void __launch_bounds__(256) latent_out_kernel(const __grid_constant__
     cluster_wait();
     const int ns = p.R / 64, pairs = rows * p.dv / 2;
     const uint32_t rank = cluster_rank();
-    for (int i = (int)rank * 256 + threadIdx.x; i < pairs; i += ns * 256) {
+    for (int i = (int)rank * 512 + threadIdx.x; i < pairs; i += ns * 512) {
         float2 a = make_float2(0.f, 0.f);
         for (int k = 0; k < ns; ++k) {
             const float2 v = cluster_ld2(part + 2 * i, (uint32_t)k);
@@ -897,18 +948,9 @@ __global__ void __launch_bounds__(512) latent_join_kernel(const __grid_constant_
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float lse = -INFINITY;
     if (!u.none) {
-        const float2 j = join_weights(p, u, lane);
-        if (d4 < p.R)
-#pragma unroll 4
-            for (int c = u.first + sub; c <= u.last; c += 4) {
-                const float f = share_factor(p, u, c, j);
-                const float4 v = __ldcg(
-                    reinterpret_cast<const float4 *>(p.part + ((size_t)slot_of(u, c) * p.nr + u.col) * p.R + d4));
-                a.x = fmaf(f, v.x, a.x);
-                a.y = fmaf(f, v.y, a.y);
-                a.z = fmaf(f, v.z, a.z);
-                a.w = fmaf(f, v.w, a.w);
-            }
+        float f[kShareChunks];
+        const float2 j = join_weights(p, u, lane, f);
+        if (d4 < p.R) a = join_sums(p, u, f, sub, 4, d4);
         lse = joined_lse(j);
     }
     if (sub) spread[sub - 1][threadIdx.x & 127] = a;
@@ -982,14 +1024,12 @@ bool map2(CUtensorMap *m, int dt, const void *base, uint64_t d0, uint64_t d1, ui
            CUDA_SUCCESS;
 }
 
-constexpr int kMaxBlocks = 160;  // blocks of the attention launch: one per SM, at most this many
-
 template <int DT, int NR>
 int launch_attn(const LatentParams &p, const AttnMaps &maps, int blocks, cudaStream_t s) {
     int st = set_smem<latent_attn_kernel<DT, NR>>(AttnGeo<NR>::kSmem);
     if (st) return st;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t c = config(dim3(blocks), kAttnThreads, AttnGeo<NR>::kSmem, s, attr, 1);
+    cudaLaunchConfig_t c = config(dim3(blocks), AttnGeo<NR>::kThreads, AttnGeo<NR>::kSmem, s, attr, 1);
     return record_launch(cudaLaunchKernelEx(&c, latent_attn_kernel<DT, NR>, p, maps));
 }
 
@@ -1018,7 +1058,7 @@ int launch_out_mt(const LatentParams &p, cudaStream_t s) {
     if (st) return st;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t c =
-        config(dim3(p.R / 64, p.heads, (p.N + 16 * MT - 1) / (16 * MT)), 256, smem, s, attr, p.R / 64);
+        config(dim3(p.R / 64, p.heads, (p.N + 16 * MT - 1) / (16 * MT)), 512, smem, s, attr, p.R / 64);
     return record_launch(cudaLaunchKernelEx(&c, latent_out_kernel<DT, MT>, p));
 }
 
