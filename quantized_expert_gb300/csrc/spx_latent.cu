@@ -138,27 +138,29 @@ constexpr float kSlack = 8.f, kShift = 5.f;
 constexpr int kPairBytes = kTile * 256;  // 64 tokens x 128 latent values, as two 64-value halves
 constexpr int kMaxBlocks = 160;  // blocks of the attention launch: one per SM, at most this many
 constexpr int kRopeBytes = kTile * 128;
-constexpr int kPBytes = kTile * 128;
 
-// Ring depths by rows per unit, as shared memory allows.  Tiles are handled in
-// pairs (both S, then both O), so at least two tiles (8 pairs) stay resident.
+// Ring depths by rows per unit, as shared memory allows: 2.75, 2.5 and 2 tiles.
+// A tile's rotated part is not needed once its S^T is there, so its slot then
+// takes the tile's softmax weights, P^T [64 tokens x 64 rows].
 template <int NR>
 struct AttnGeo {
-    static constexpr int kPairs = NR <= 32 ? 10 : 8;
-    static constexpr int kRopes = NR <= 16 ? 3 : 2;
+    static constexpr int kPairs = NR <= 16 ? 11 : NR <= 32 ? 10 : 8;
+    static constexpr int kRopes = 3;
     // Softmax warps: four (one per quarter of tensor memory) for each share of
     // the rows: one warp a scheduler cannot keep up with the products on 64 rows.
     static constexpr int kShares = NR <= 16 ? 1 : 2;
     static constexpr int kThreads = 64 + 128 * kShares;
     static constexpr int kQBytes = 9 * NR * 128;
     static constexpr int kMisc = 3072;
-    static constexpr int kSmem = kQBytes + kPBytes + kPairs * kPairBytes + kRopes * kRopeBytes + kMisc;
+    static constexpr int kSmem = kQBytes + kPairs * kPairBytes + kRopes * kRopeBytes + kMisc;
     static constexpr uint32_t kTmem = NR <= 16 ? 128 : NR <= 32 ? 256 : 512;  // >= 6 NR, a power of two
     static_assert(kSmem <= kSmemLimit, "shared memory of one block");
+    static_assert(kPairs < 12 && kRopes == 3, "at most 3 tiles begun: 4 landing barriers never lap");
 };
 
 struct AttnMisc {
-    uint64_t pfull[12], pempty[12], rfull[4], rempty[4];  // copies landed / slot free
+    uint64_t full[4];             // a tile's copies have landed
+    uint64_t pempty[12], rempty[4];  // slots free: pairs, rotated parts
     uint64_t qfull, qempty;       // the unit's queries landed / read for the last time
     uint64_t sfull[2];            // S^T of a tile is in tensor memory
     uint64_t wfull;               // a tile's weights are in shared memory (all softmax warps)
@@ -175,6 +177,25 @@ struct AttnMisc {
 };
 static_assert(sizeof(AttnMisc) <= 3072, "the misc area holds it");
 
+// A place in a ring of N slots and the parity of its use.
+template <int N>
+struct Slot {
+    uint32_t i = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
+    __device__ __forceinline__ void advance(int n) {  // n <= N
+        i += n;
+        if (i >= N) {
+            i -= N;
+            phase ^= 1;
+        }
+    }
+};
+
 struct AttnMaps {
     CUtensorMap cache;  // [pages][page_size][R + P], boxes of 64 values x gcd(page_size, 64) tokens
     CUtensorMap q;      // [N * heads][R + P], boxes of 64 values x NR rows
@@ -184,7 +205,7 @@ template <int NR>
 __device__ __forceinline__ int unit_tiles(const LatentParams &p, const LatentReq &r, int g) {
     const int rows = r.T * p.heads;
     if (g * NR >= rows) return 0;
-    const int last = (min((g + 1) * NR, rows) - 1) / p.heads;
+    const int last = p.by_heads(min((g + 1) * NR, rows) - 1);
     return (latent_limit(p, r, last) + kTile - 1) / kTile;
 }
 
@@ -290,38 +311,28 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
     using G = AttnGeo<NR>;
     constexpr int PR = G::kPairs, RR = G::kRopes;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *qs = smem, *ps = qs + G::kQBytes, *pairs = ps + kPBytes, *ropes = pairs + PR * kPairBytes;
+    uint8_t *qs = smem, *pairs = qs + G::kQBytes, *ropes = pairs + PR * kPairBytes;
     AttnMisc &m = *reinterpret_cast<AttnMisc *>(ropes + RR * kRopeBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int np = p.R / 128;  // pairs of a tile
 
     if (!p.chained) griddep_wait();
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < PR; ++i) {
-            mbar_init(&m.pfull[i], 1);
-            mbar_init(&m.pempty[i], 1);
-        }
-        for (int i = 0; i < RR; ++i) {
-            mbar_init(&m.rfull[i], 1);
-            mbar_init(&m.rempty[i], 1);
-        }
-        mbar_init(&m.qfull, 1);
-        mbar_init(&m.qempty, 1);
-        mbar_init(&m.sfull[0], 1);
-        mbar_init(&m.sfull[1], 1);
-        mbar_init(&m.wfull, 4 * G::kShares);
-        mbar_init(&m.odone, 1);
-        mbar_init(&m.ofree, 4 * G::kShares);
-        mbar_init(&m.fin, 1);
-        m.abort = 0;
-        fence_mbar_init();
-        prefetch_tmap(&maps.cache);
-        prefetch_tmap(&maps.q);
-    }
-    if (warp == 0) find_share<NR>(p, m, lane);
-    if (warp == 1) {
+    if (warp == 0) {
+        find_share<NR>(p, m, lane);
+    } else if (warp == 1) {
         tmem_alloc(&m.tmem, G::kTmem);
         tmem_relinquish();
+    } else if (warp == 2) {
+        // a barrier a lane; the words from full to fin are all barriers
+        uint64_t *bars = m.full;
+        constexpr int kBars = 4 + 12 + 4 + 2 + 2 + 4;
+        if (lane < kBars) mbar_init(&bars[lane], &bars[lane] == &m.wfull || &bars[lane] == &m.ofree ? 4 * G::kShares : 1);
+        if (lane == 0) m.abort = 0;
+        fence_mbar_init();
+        if (lane == 0) {
+            prefetch_tmap(&maps.cache);
+            prefetch_tmap(&maps.q);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -336,142 +347,146 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
         // ---- copies: a tile is np pairs and a rotated part, in boxes that do not cross a page
         const uint64_t pol = p.groups > 1 ? policy_evict_normal() : policy_evict_first();
         const int bt = p.box_tokens, nb = kTile / bt;
-        uint32_t it = 0, rt = 0, seg = 0;
+        const uint32_t tile_bytes = (uint32_t)(np * kPairBytes + kRopeBytes);
+        uint32_t tc = 0, seg = 0;
+        Slot<PR> ps;
+        Slot<RR> rs;
         bool ok = true, waited = !p.chained;
         for (w.begin(p, m); ok && w.left > 0; w.next(p), ++seg) {
             const int32_t *tab = p.table + (size_t)w.b * p.max_pages;
             int box = 32, my_page = 0, my_at = 0;  // this lane's box of the 32 looked up together
-            for (int i = w.tile; ok && i < w.end; ++i, box += nb) {
+#pragma unroll 1
+            for (int i = w.tile; i < w.end; ++i, ++tc, box += nb) {
                 if (box >= 32) {
-                    const int pos = kTile * i + bt * lane, pi = pos / p.page_size;
+                    const int pos = kTile * i + bt * lane, pi = p.by_page(pos);
                     my_at = pos - pi * p.page_size;
                     // positions past the length come as zeros (a page out of range)
                     my_page = pos < w.rq.len ? __ldg(tab + pi) : p.num_pages;
                     if (my_page < 0 || my_page >= p.num_pages) my_page = p.num_pages;
                     box = 0;
                 }
+                uint64_t *full = &m.full[tc & 3];
+                if (!(ok = ctl_wait(&m.rempty[rs.i], rs.phase ^ 1, ctl))) break;
+                if (elect_one()) mbar_arrive_expect_tx(full, tile_bytes);
 #pragma unroll 1
                 for (int c = 0; c <= np; ++c) {  // c == np: the rotated part
-                    const bool rope = c == np;
-                    const uint32_t k = rope ? rt : it, s = rope ? rt % RR : it % PR;
-                    uint64_t *full = rope ? &m.rfull[s] : &m.pfull[s];
-                    ok = ctl_wait(rope ? &m.rempty[s] : &m.pempty[s], ((k / (rope ? RR : PR)) & 1) ^ 1, ctl);
-                    if (!ok) break;
-                    uint8_t *dst = rope ? ropes + s * kRopeBytes : pairs + s * kPairBytes;
+                    if (c < np && !(ok = ctl_wait(&m.pempty[ps.i], ps.phase ^ 1, ctl))) break;
+                    uint8_t *dst = c < np ? pairs + ps.i * kPairBytes : ropes + rs.i * kRopeBytes;
                     const bool lead = elect_one();
-                    if (lead) mbar_arrive_expect_tx(full, rope ? kRopeBytes : kPairBytes);
 #pragma unroll 1
                     for (int j = 0; j < nb; ++j) {
                         const int at = __shfl_sync(0xffffffffu, my_at, box + j);
                         const int page = __shfl_sync(0xffffffffu, my_page, box + j);
                         if (lead) {
                             tma_load_3d(dst + j * bt * 128, &maps.cache, 128 * c, at, page, full, pol);
-                            if (!rope)
+                            if (c < np)
                                 tma_load_3d(dst + kPairBytes / 2 + j * bt * 128, &maps.cache, 128 * c + 64, at, page,
                                             full, pol);
                         }
                     }
-                    if (rope) ++rt;
-                    else ++it;
+                    if (c < np) ps.next();
                 }
-                if (ok && i == w.tile) {
-                    // the unit's queries, behind its first tile (which needs no earlier launch of the call)
+                if (!ok) break;
+                rs.next();
+                if (i == min(w.tile + 1, w.end - 1)) {
+                    // the unit's queries, behind its first two tiles (which need no earlier launch of the call
+                    // and find room without the queries' products)
                     if (!waited) {
                         griddep_wait();
                         waited = true;
                     }
-                    ok = ctl_wait(&m.qempty, (seg & 1) ^ 1, ctl);
-                    if (!ok) break;
+                    if (!(ok = ctl_wait(&m.qempty, (seg & 1) ^ 1, ctl))) break;
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&m.qfull, (uint32_t)(2 * np + 1) * NR * 128);
                         const int row = w.rq.row0 * p.heads + NR * w.g;
                         for (int c = 0; c < 2 * np + 1; ++c)
                             tma_load_2d(qs + c * NR * 128, &maps.q, 64 * c, row, &m.qfull, pol);
                     }
+                    __syncwarp();
                 }
             }
         }
         if (!waited) griddep_wait();
-        if (!ok) {  // copies in flight land before the block ends
-            for (uint32_t j = it > PR ? it - PR : 0; j < it; ++j) ctl_drain(&m.pfull[j % PR], (j / PR) & 1, 100000000ull);
-            for (uint32_t j = rt > RR ? rt - RR : 0; j < rt; ++j) ctl_drain(&m.rfull[j % RR], (j / RR) & 1, 100000000ull);
-            for (uint32_t j = 0; j < 2 && j <= seg; ++j) ctl_drain(&m.qfull, (seg - j) & 1, 1000000ull);
-        }
+        if (!ok) ctl_settle(100000000ull);  // copies in flight land before the block ends
     } else if (warp == 1) {
-        // ---- products
+        // ---- products: whichever is ready, the oldest tile's O first; S at most two tiles ahead of O
         const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
         const uint64_t qd = sw128_desc(smem_u32(qs)), kd = sw128_desc(smem_u32(pairs)), rd = sw128_desc(smem_u32(ropes));
-        const uint64_t vd = sw128_desc_mn(smem_u32(pairs), kPairBytes / 2), pd = sw128_desc_mn(smem_u32(ps), 0);
-        uint32_t it = 0, tc = 0, seg = 0;
+        const uint64_t vd = sw128_desc_mn(smem_u32(pairs), kPairBytes / 2), pd = sw128_desc_mn(smem_u32(ropes), 0);
+        uint32_t ts = 0, to = 0, seg = 0;  // next tile for S and for O
+        Slot<PR> sp, op;                   // their first pairs
+        Slot<RR> sr, orp;                  // and rotated parts / weights
         bool ok = true;
         for (w.begin(p, m); ok && w.left > 0; w.next(p), ++seg) {
             const int n16 = (min(NR, w.rq.T * p.heads - NR * w.g) + 15) & ~15;
             const uint32_t idS = idesc_f16_f32(64, n16) | fmt;
             const uint32_t idO = idesc_f16_f32(128, n16) | fmt | kIdescAMn | kIdescBMn;
-            const int nt = w.end - w.tile;
+            const uint32_t t0 = ts, t1 = ts + (uint32_t)(w.end - w.tile);
             if (!(ok = ctl_wait(&m.qfull, seg & 1, ctl))) break;
+            uint64_t since = 0;
 #pragma unroll 1
-            for (int i = 0; ok && i < nt; i += 2) {
-                const int two = min(2, nt - i);
-                // All of a tile's waits come before its products, which then issue without a gap
-                // (waits between them left 20 to 30 cycles a product).
-#pragma unroll 1
-                for (int d = 0; d < two; ++d) {
-                    const uint32_t t = tc + d, sd = tmem + s_col + (t & 1) * NR, rs = t % RR, s0 = (it + d * np) % PR;
-                    for (int c = 0; ok && c < np; ++c) {
-                        const uint32_t k = it + d * np + c;
-                        ok = ctl_wait(&m.pfull[k % PR], (k / PR) & 1, ctl);
-                    }
-                    ok = ok && ctl_wait(&m.rfull[rs], (t / RR) & 1, ctl);
-                    if (!ok) break;
+            while (to < t1) {
+                if (to < ts && mbar_try_wait(&m.wfull, to & 1) &&
+                    (to != t0 || mbar_try_wait(&m.ofree, (seg & 1) ^ 1))) {
                     tc_fence_after();
                     if (elect_one()) {
-                        // descriptors count in 16 bytes: 32 bytes a k-step, half a pair, a chunk of Q
-                        uint64_t a = kd + s0 * (kPairBytes / 16), q = qd;
-                        uint32_t s = s0;
+                        Slot<PR> k = op;
 #pragma unroll 1
                         for (int c = 0; c < np; ++c) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                umma_f16(tmem + c * NR, vd + k.i * (kPairBytes / 16) + 128 * j,
+                                         pd + orp.i * (kRopeBytes / 16) + 128 * j, idO, to != t0 || j != 0);
+                            umma_commit(&m.pempty[k.i]);
+                            k.next();
+                        }
+                        umma_commit(&m.rempty[orp.i]);
+                        umma_commit(&m.odone);
+                    }
+                    __syncwarp();
+                    op.advance(np);
+                    orp.next();
+                    ++to;
+                    since = 0;
+                } else if (ts < t1 && ts - to < 2 && mbar_try_wait(&m.full[ts & 3], (ts >> 2) & 1)) {
+                    tc_fence_after();
+                    const uint32_t sd = tmem + s_col + (ts & 1) * NR;
+                    if (elect_one()) {
+                        // descriptors count in 16 bytes: 32 bytes a k-step, half a pair, a chunk of Q
+                        Slot<PR> k = sp;
+                        uint64_t q = qd;
+#pragma unroll 1
+                        for (int c = 0; c < np; ++c) {
+                            const uint64_t a = kd + k.i * (kPairBytes / 16);
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 umma_f16(sd, a + (j >> 2) * (kPairBytes / 32) + 2 * (j & 3),
                                          q + (j >> 2) * (NR * 8) + 2 * (j & 3), idS, (c | j) != 0);
                             q += 2 * NR * 8;
-                            a += kPairBytes / 16;
-                            if (++s == PR) {
-                                s = 0;
-                                a = kd;
-                            }
+                            k.next();
                         }
+                        const uint64_t a = rd + sr.i * (kRopeBytes / 16);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) umma_f16(sd, rd + rs * (kRopeBytes / 16) + 2 * j, q + 2 * j, idS, 1);
-                        umma_commit(&m.rempty[rs]);
-                        umma_commit(&m.sfull[t & 1]);
-                        if (i + d == nt - 1) umma_commit(&m.qempty);
+                        for (int j = 0; j < 4; ++j) umma_f16(sd, a + 2 * j, q + 2 * j, idS, 1);
+                        umma_commit(&m.sfull[ts & 1]);
+                        if (ts + 1 == t1) umma_commit(&m.qempty);
                     }
                     __syncwarp();
+                    sp.advance(np);
+                    sr.next();
+                    ++ts;
+                    since = 0;
+                } else if (*ctl.abort) {
+                    ok = false;
+                    break;
+                } else if (!since) {
+                    since = global_timer_ns();
+                } else if (global_timer_ns() - since > ctl.budget) {
+                    record_timeout(ctl.status, ctl.site);
+                    *ctl.abort = 1;
+                    ok = false;
+                    break;
                 }
-#pragma unroll 1
-                for (int d = 0; ok && d < two; ++d) {
-                    if (i + d == 0 && !(ok = ctl_wait(&m.ofree, (seg & 1) ^ 1, ctl))) break;
-                    if (!(ok = ctl_wait(&m.wfull, (tc + d) & 1, ctl))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        uint32_t s = (it + d * np) % PR;
-#pragma unroll 1
-                        for (int c = 0; c < np; ++c) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                umma_f16(tmem + c * NR, vd + s * (kPairBytes / 16) + 128 * j, pd + 128 * j, idO,
-                                         (i + d) != 0 || j != 0);
-                            umma_commit(&m.pempty[s]);
-                            s = s + 1 == PR ? 0 : s + 1;
-                        }
-                        umma_commit(&m.odone);
-                    }
-                    __syncwarp();
-                }
-                it += two * np;
-                tc += two;
             }
         }
         if (m.abort) {
@@ -488,12 +503,14 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
         const int cl = c0 + 2 * (lane & 3);    // this lane's rows: 8x + cl, 8x + cl + 1
         const int tok = 16 * q + (lane >> 2);  // its tokens: tok, tok + 8
         uint32_t tc = 0;
+        Slot<RR> rs;
+        Slot<PR> ps;
         // (after a wait that gave up the loop runs on, as every warp has to meet the barriers)
         for (w.begin(p, m); w.left > 0; w.next(p)) {
             const int rows = min(NR, w.rq.T * p.heads - NR * w.g), n16 = (rows + 15) & ~15;
             const int row0 = NR * w.g;
             bar_sync(3, 128 * SH);  // the last unit's limits and sums are read
-            if (all < NR) m.lim[all] = all < rows ? latent_limit(p, w.rq, (row0 + all) / p.heads) : 0;
+            if (all < NR) m.lim[all] = all < rows ? latent_limit(p, w.rq, p.by_heads(row0 + all)) : 0;
             bar_sync(3, 128 * SH);
             const int lim_lo = m.lim[0], lim_hi = m.lim[rows - 1];
             float mr[2 * NB], l[2 * NB];
@@ -503,7 +520,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                 l[c] = 0.f;
             }
 #pragma unroll 1
-            for (int i = w.tile; i < w.end; ++i, ++tc) {
+            for (int i = w.tile; i < w.end; ++i, ++tc, rs.next(), ps.advance(np)) {
                 ctl_wait(&m.sfull[tc & 1], (tc >> 1) & 1, ctl);
                 tc_fence_after();
                 uint32_t r[4 * NB];
@@ -587,25 +604,24 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                         r[4 * x + f] = __float_as_uint(v);
                         r[4 * x + 2 + f] = __float_as_uint(y);
                     }
-                // the weights' buffer is free once the tile before has been taken
-                if (i > w.tile) ctl_wait(&m.odone, (tc - 1) & 1, ctl);
+                uint8_t *wt = ropes + rs.i * kRopeBytes;
 #pragma unroll
                 for (int x = 0; x < NB; ++x)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int t = tok + 8 * k;
-                        *reinterpret_cast<uint32_t *>(ps + t * 128 + 16 * ((x + c0 / 8) ^ (t & 7)) + 4 * (lane & 3)) =
+                        *reinterpret_cast<uint32_t *>(wt + t * 128 + 16 * ((x + c0 / 8) ^ (t & 7)) + 4 * (lane & 3)) =
                             Elem<DT>::down2(__uint_as_float(r[4 * x + 2 * k]), __uint_as_float(r[4 * x + 2 * k + 1]));
                     }
                 if (masked) {
                     // What some row may not see has weight 0 there, and 0 times an infinity or a NaN would
                     // still reach it: rows of the tile that nobody sees become 0, and in those that only
                     // some see every value that is not finite (whoever sees it got a NaN from S already).
-                    const uint32_t k0 = tc * np;
                     const int t0 = max(lim_lo - p0, 0);
+                    Slot<PR> k0 = ps;
 #pragma unroll 1
-                    for (int c = 0; c < np; ++c) {
-                        uint8_t *base = pairs + ((k0 + c) % PR) * kPairBytes;
+                    for (int c = 0; c < np; ++c, k0.next()) {
+                        uint8_t *base = pairs + k0.i * kPairBytes;
 #pragma unroll 1
                         for (int e = all; e < (kTile - t0) * 16; e += 128 * SH) {
                             const int t = t0 + (e >> 4), k = e & 15;
@@ -734,7 +750,7 @@ __device__ __forceinline__ RowSum find_row(const LatentParams &p, int n, int h, 
     const LatentReq rq = latent_req(p, b);
     const int row = (n - rq.row0) * p.heads + h, g = row / p.nr;
     r.col = row - g * p.nr;
-    const int last = (min((g + 1) * p.nr, rq.T * p.heads) - 1) / p.heads;
+    const int last = p.by_heads(min((g + 1) * p.nr, rq.T * p.heads) - 1);
     if (latent_limit(p, rq, last) <= 0) return r;  // a unit without tiles
     const int4 u = __ldcg(p.units + (size_t)b * p.groups + g);
     r.first = u.x;
@@ -1177,7 +1193,10 @@ extern "C" int spx_latent_attention(const spx_latent_args *a, spx_stream_t strea
     p.N = a->N;
     p.heads = a->heads;
     p.max_q = a->max_q;
-    p.max_len = a->max_len;
+    const long long cap = (long long)c.max_pages * c.page_size;
+    p.max_len = a->max_len < cap ? a->max_len : (int)cap;
+    p.by_heads.set(a->heads);
+    p.by_page.set(c.page_size);
     p.dn = a->dn;
     p.dv = a->dv;
     p.causal = a->causal != 0;

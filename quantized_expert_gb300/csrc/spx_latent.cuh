@@ -42,6 +42,20 @@ struct Elem<SPX_F32> {
     static __device__ __forceinline__ T down(float v) { return v; }
 };
 
+// Quotients by a divisor known to the host: q = (hi(x m) + x) >> s, exact for
+// 0 <= x < 2^31 (m = floor(2^32 (2^s - d) / d) + 1, 2^s the least power >= d).
+struct FastDiv {
+    uint32_t m, s;
+    int d;
+    void set(int div) {
+        d = div;
+        s = 0;
+        while ((1ull << s) < (uint64_t)div) ++s;
+        m = (uint32_t)((((1ull << s) - (uint64_t)div) << 32) / (uint64_t)div + 1);
+    }
+    __device__ __forceinline__ int operator()(int x) const { return (int)((__umulhi((uint32_t)x, m) + (uint32_t)x) >> s); }
+};
+
 struct LatentParams {
     // cache
     const uint16_t *cache;
@@ -51,7 +65,8 @@ struct LatentParams {
     int max_pages, B;
     const int32_t *lens;
     // call
-    int N, heads, max_q, max_len, dn, dv, causal;
+    int N, heads, max_q, max_len, dn, dv, causal;  // max_len: within the block table too
+    FastDiv by_heads, by_page;
     int64_t q_stride, out_stride;
     const int32_t *q_start;
     const uint16_t *q, *w_uk, *w_uv;
@@ -81,8 +96,7 @@ __device__ __forceinline__ LatentReq latent_req(const LatentParams &p, int b) {
     const int s = __ldg(p.q_start + b), e = __ldg(p.q_start + b + 1);
     r.row0 = min(max(s, 0), p.N);
     r.T = min(min(max(e - r.row0, 0), p.max_q), p.N - r.row0);
-    const long long cap = (long long)p.max_pages * p.page_size;
-    r.len = (int)min((long long)min(max(__ldg(p.lens + b), 0), p.max_len), cap);
+    r.len = min(max(__ldg(p.lens + b), 0), p.max_len);
     return r;
 }
 // Positions that token t of the request sees: [0, limit).

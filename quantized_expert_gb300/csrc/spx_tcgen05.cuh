@@ -175,6 +175,14 @@ __device__ __forceinline__ void ctl_drain(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
+// After an abort, where what is in flight cannot be waited for one by one:
+// copies were issued by then and land within microseconds.
+__device__ __forceinline__ void ctl_settle(uint64_t ns) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < ns) {
+    }
+}
+
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *tm) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
 }
