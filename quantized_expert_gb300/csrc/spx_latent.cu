@@ -138,6 +138,9 @@ constexpr float kSlack = 8.f, kShift = 5.f;
 constexpr int kPairBytes = kTile * 256;  // 64 tokens x 128 latent values, as two 64-value halves
 constexpr int kMaxBlocks = 160;  // blocks of the attention launch: one per SM, at most this many
 constexpr int kRopeBytes = kTile * 128;
+// Copies are issued by one warp per pair of a tile: a warp takes 250 to 300
+// cycles for each, and one warp's nine of a tile were slower than the products.
+constexpr int kCopyWarps = 4;
 
 // Ring depths by rows per unit, as shared memory allows: 2.75, 2.5 and 2 tiles.
 // A tile's rotated part is not needed once its S^T is there, so its slot then
@@ -149,7 +152,7 @@ struct AttnGeo {
     // Softmax warps: four (one per quarter of tensor memory) for each share of
     // the rows: one warp a scheduler cannot keep up with the products on 64 rows.
     static constexpr int kShares = NR <= 16 ? 1 : 2;
-    static constexpr int kThreads = 64 + 128 * kShares;
+    static constexpr int kThreads = 32 * (kCopyWarps + 1) + 128 * kShares;
     static constexpr int kQBytes = 9 * NR * 128;
     static constexpr int kMisc = 3072;
     static constexpr int kSmem = kQBytes + kPairs * kPairBytes + kRopes * kRopeBytes + kMisc;
@@ -159,11 +162,11 @@ struct AttnGeo {
 };
 
 struct AttnMisc {
-    uint64_t full[4];             // a tile's copies have landed
+    uint64_t full[4];             // a tile's copies have landed (one arrival per copying warp)
     uint64_t pempty[12], rempty[4];  // slots free: pairs, rotated parts
     uint64_t qfull, qempty;       // the unit's queries landed / read for the last time
     uint64_t sfull[2];            // S^T of a tile is in tensor memory
-    uint64_t wfull;               // a tile's weights are in shared memory (all softmax warps)
+    uint64_t wfull[2];            // a tile's weights are in shared memory (all softmax warps)
     uint64_t odone;               // O^T has taken a tile
     uint64_t ofree;               // O^T of the unit has been read out (all softmax warps)
     uint64_t fin;                 // products drained (abort path)
@@ -196,9 +199,11 @@ struct Slot {
     }
 };
 
+// Tensor maps in pieces of 64 values (one swizzled row of 128 bytes).
 struct AttnMaps {
-    CUtensorMap cache;  // [pages][page_size][R + P], boxes of 64 values x gcd(page_size, 64) tokens
-    CUtensorMap q;      // [N * heads][R + P], boxes of 64 values x NR rows
+    CUtensorMap pair;  // cache as [page][piece][token][64]: boxes of 2 pieces x 64 tokens, or 1 x gcd(page_size, 64)
+    CUtensorMap rope;  // the same, boxes of 1 piece
+    CUtensorMap q;     // queries as [piece][row][64], a box is all of a unit's
 };
 
 template <int NR>
@@ -319,18 +324,23 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
     if (!p.chained) griddep_wait();
     if (warp == 0) {
         find_share<NR>(p, m, lane);
-    } else if (warp == 1) {
+    } else if (warp == kCopyWarps) {
         tmem_alloc(&m.tmem, G::kTmem);
         tmem_relinquish();
-    } else if (warp == 2) {
+    } else if (warp == kCopyWarps + 1) {
         // a barrier a lane; the words from full to fin are all barriers
         uint64_t *bars = m.full;
-        constexpr int kBars = 4 + 12 + 4 + 2 + 2 + 4;
-        if (lane < kBars) mbar_init(&bars[lane], &bars[lane] == &m.wfull || &bars[lane] == &m.ofree ? 4 * G::kShares : 1);
+        constexpr int kBars = 4 + 12 + 4 + 2 + 2 + 2 + 3;
+        if (lane < kBars)
+            mbar_init(&bars[lane], lane < 4 ? np
+                                    : &bars[lane] == m.wfull || &bars[lane] == m.wfull + 1 || &bars[lane] == &m.ofree
+                                        ? 4 * G::kShares
+                                        : 1);
         if (lane == 0) m.abort = 0;
         fence_mbar_init();
         if (lane == 0) {
-            prefetch_tmap(&maps.cache);
+            prefetch_tmap(&maps.pair);
+            prefetch_tmap(&maps.rope);
             prefetch_tmap(&maps.q);
         }
     }
@@ -343,16 +353,16 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
     const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_LATENT};
     Walk<NR> w;
 
-    if (warp == 0) {
-        // ---- copies: a tile is np pairs and a rotated part, in boxes that do not cross a page
+    if (warp < kCopyWarps) {
+        // ---- copies: warp c takes pair c of every tile, warp 0 the rotated part and the queries too
         const uint64_t pol = p.groups > 1 ? policy_evict_normal() : policy_evict_first();
-        const int bt = p.box_tokens, nb = kTile / bt;
-        const uint32_t tile_bytes = (uint32_t)(np * kPairBytes + kRopeBytes);
+        const int bt = p.box_tokens, nb = kTile / bt;  // boxes do not cross a page
         uint32_t tc = 0, seg = 0;
         Slot<PR> ps;
         Slot<RR> rs;
+        ps.i = warp;
         bool ok = true, waited = !p.chained;
-        for (w.begin(p, m); ok && w.left > 0; w.next(p), ++seg) {
+        for (w.begin(p, m); ok && warp < np && w.left > 0; w.next(p), ++seg) {
             const int32_t *tab = p.table + (size_t)w.b * p.max_pages;
             int box = 32, my_page = 0, my_at = 0;  // this lane's box of the 32 looked up together
 #pragma unroll 1
@@ -366,29 +376,28 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     box = 0;
                 }
                 uint64_t *full = &m.full[tc & 3];
-                if (!(ok = ctl_wait(&m.rempty[rs.i], rs.phase ^ 1, ctl))) break;
-                if (elect_one()) mbar_arrive_expect_tx(full, tile_bytes);
+                // a tile is begun once its rotated slot is free, so that a landing barrier never laps
+                if (!(ok = ctl_wait(&m.rempty[rs.i], rs.phase ^ 1, ctl) && ctl_wait(&m.pempty[ps.i], ps.phase ^ 1, ctl)))
+                    break;
+                uint8_t *dst = pairs + ps.i * kPairBytes, *rope = ropes + rs.i * kRopeBytes;
+                const bool lead = elect_one();
+                if (lead) mbar_arrive_expect_tx(full, kPairBytes + (warp == 0 ? kRopeBytes : 0));
 #pragma unroll 1
-                for (int c = 0; c <= np; ++c) {  // c == np: the rotated part
-                    if (c < np && !(ok = ctl_wait(&m.pempty[ps.i], ps.phase ^ 1, ctl))) break;
-                    uint8_t *dst = c < np ? pairs + ps.i * kPairBytes : ropes + rs.i * kRopeBytes;
-                    const bool lead = elect_one();
-#pragma unroll 1
-                    for (int j = 0; j < nb; ++j) {
-                        const int at = __shfl_sync(0xffffffffu, my_at, box + j);
-                        const int page = __shfl_sync(0xffffffffu, my_page, box + j);
-                        if (lead) {
-                            tma_load_3d(dst + j * bt * 128, &maps.cache, 128 * c, at, page, full, pol);
-                            if (c < np)
-                                tma_load_3d(dst + kPairBytes / 2 + j * bt * 128, &maps.cache, 128 * c + 64, at, page,
-                                            full, pol);
-                        }
+                for (int j = 0; j < nb; ++j) {
+                    const int at = __shfl_sync(0xffffffffu, my_at, box + j);
+                    const int page = __shfl_sync(0xffffffffu, my_page, box + j);
+                    if (lead) {
+                        tma_load_4d(dst + j * bt * 128, &maps.pair, 0, at, 2 * warp, page, full, pol);
+                        if (nb > 1)
+                            tma_load_4d(dst + kPairBytes / 2 + j * bt * 128, &maps.pair, 0, at, 2 * warp + 1, page, full,
+                                        pol);
+                        if (warp == 0) tma_load_4d(rope + j * bt * 128, &maps.rope, 0, at, 2 * np, page, full, pol);
                     }
-                    if (c < np) ps.next();
                 }
-                if (!ok) break;
+                __syncwarp();
+                ps.advance(np);
                 rs.next();
-                if (i == min(w.tile + 1, w.end - 1)) {
+                if (warp == 0 && i == min(w.tile + 1, w.end - 1)) {
                     // the unit's queries, behind its first two tiles (which need no earlier launch of the call
                     // and find room without the queries' products)
                     if (!waited) {
@@ -398,9 +407,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     if (!(ok = ctl_wait(&m.qempty, (seg & 1) ^ 1, ctl))) break;
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&m.qfull, (uint32_t)(2 * np + 1) * NR * 128);
-                        const int row = w.rq.row0 * p.heads + NR * w.g;
-                        for (int c = 0; c < 2 * np + 1; ++c)
-                            tma_load_2d(qs + c * NR * 128, &maps.q, 64 * c, row, &m.qfull, pol);
+                        tma_load_3d(qs, &maps.q, 0, w.rq.row0 * p.heads + NR * w.g, 0, &m.qfull, pol);
                     }
                     __syncwarp();
                 }
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
         }
         if (!waited) griddep_wait();
         if (!ok) ctl_settle(100000000ull);  // copies in flight land before the block ends
-    } else if (warp == 1) {
+    } else if (warp == kCopyWarps) {
         // ---- products: whichever is ready, the oldest tile's O first; S at most two tiles ahead of O
         const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
         const uint64_t qd = sw128_desc(smem_u32(qs)), kd = sw128_desc(smem_u32(pairs)), rd = sw128_desc(smem_u32(ropes));
@@ -426,8 +433,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
             uint64_t since = 0;
 #pragma unroll 1
             while (to < t1) {
-                if (to < ts && mbar_try_wait(&m.wfull, to & 1) &&
-                    (to != t0 || mbar_try_wait(&m.ofree, (seg & 1) ^ 1))) {
+                if (to < ts && mbar_test(&m.wfull[to & 1], (to >> 1) & 1) && (to != t0 || mbar_test(&m.ofree, (seg & 1) ^ 1))) {
                     tc_fence_after();
                     if (elect_one()) {
                         Slot<PR> k = op;
@@ -448,7 +454,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     orp.next();
                     ++to;
                     since = 0;
-                } else if (ts < t1 && ts - to < 2 && mbar_try_wait(&m.full[ts & 3], (ts >> 2) & 1)) {
+                } else if (ts < t1 && ts - to < 2 && mbar_test(&m.full[ts & 3], (ts >> 2) & 1)) {
                     tc_fence_after();
                     const uint32_t sd = tmem + s_col + (ts & 1) * NR;
                     if (elect_one()) {
@@ -493,11 +499,11 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
             if (elect_one()) umma_commit(&m.fin);
             ctl_drain(&m.fin, 0, 100000000ull);
         }
-    } else if (warp >= 2) {
+    } else {
         // ---- softmax, rescaling, results
         constexpr int SH = G::kShares, NC = NR / SH, NB = NC / 8;  // rows of a share, in blocks of 8
         const int q = warp & 3;                                    // tensor-memory quarter
-        const int sh = (warp - 2) >> 2, c0 = NC * sh;              // this warp's share of the rows: c0 ..
+        const int sh = (warp - kCopyWarps - 1) >> 2, c0 = NC * sh;              // this warp's share of the rows: c0 ..
         const int tid = 32 * q + lane, all = 128 * sh + tid;       // index within the share's warps, among all
         const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16);
         const int cl = c0 + 2 * (lane & 3);    // this lane's rows: 8x + cl, 8x + cl + 1
@@ -576,6 +582,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     }
                     if (i > w.tile) {
                         bar_sync(1 + sh, 128);
+                        // (O of the tile before that is done: S of this tile came behind it)
                         ctl_wait(&m.odone, (tc - 1) & 1, ctl);
                         tc_fence_after();
 #pragma unroll 1
@@ -645,9 +652,11 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&m.wfull);
+                if (lane == 0) mbar_arrive(&m.wfull[tc & 1]);
             }
             // ---- results of the unit, or of its part in this share
+            // (phase by phase: S of the last tile does not wait for O of the one before)
+            if (w.end - w.tile > 1) ctl_wait(&m.odone, (tc - 2) & 1, ctl);
             ctl_wait(&m.odone, (tc - 1) & 1, ctl);
             tc_fence_after();
             const bool whole = w.tile == 0 && w.end == w.nt;
@@ -717,7 +726,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == kCopyWarps) {
         tc_fence_after();
         tmem_dealloc(tmem, G::kTmem);
     }
@@ -1014,30 +1023,34 @@ int set_smem(size_t bytes) {
     return SPX_OK;
 }
 
-bool map3(CUtensorMap *m, int dt, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
-          uint32_t box1) {
+// A tensor map of `rank` dimensions of two-byte values, innermost 64 of them
+// (one swizzled row); strides in bytes of dimensions 1 on.
+bool map_rows64(CUtensorMap *m, int dt, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                const uint32_t *box) {
     const EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[3] = {d0, d1, d2};
-    const cuuint64_t strides[2] = {s1, s2};
-    const cuuint32_t box[3] = {64, box1, 1};
-    const cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, dt == SPX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-              const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], es[4];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1;
+        if (i) st[i - 1] = strides[i - 1];
+    }
+    return fn(m, dt == SPX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+              const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool map2(CUtensorMap *m, int dt, const void *base, uint64_t d0, uint64_t d1, uint64_t s1, uint32_t box1) {
-    const EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {d0, d1};
-    const cuuint64_t strides[1] = {s1};
-    const cuuint32_t box[2] = {64, box1};
-    const cuuint32_t es[2] = {1, 1};
-    return fn(m, dt == SPX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-              const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
+bool attn_maps(const LatentParams &p, int dt, const void *q, AttnMaps *maps) {
+    const uint64_t tok = (uint64_t)p.token_stride * 2, pieces = (uint64_t)(p.R + p.P) / 64;
+    const uint64_t dims[4] = {64, (uint64_t)p.page_size, pieces, (uint64_t)p.num_pages};
+    const uint64_t strides[3] = {tok, 128, p.num_pages > 1 ? (uint64_t)p.page_stride * 2 : tok * p.page_size};
+    const uint32_t pair[4] = {64, (uint32_t)p.box_tokens, p.box_tokens == kTile ? 2u : 1u, 1};
+    const uint32_t rope[4] = {64, (uint32_t)p.box_tokens, 1, 1};
+    const uint64_t qd[3] = {64, (uint64_t)p.N * p.heads, pieces}, qs[2] = {(uint64_t)(p.R + p.P) * 2, 128};
+    const uint32_t qb[3] = {64, (uint32_t)p.nr, (uint32_t)pieces};
+    return map_rows64(&maps->pair, dt, p.cache, 4, dims, strides, pair) &&
+           map_rows64(&maps->rope, dt, p.cache, 4, dims, strides, rope) && map_rows64(&maps->q, dt, q, 3, qd, qs, qb);
 }
 
 template <int DT, int NR>
@@ -1083,14 +1096,9 @@ int launch_absorbed(LatentParams &p, int dtype, bool packed, cudaStream_t s) {
     int st;
     p.chained = p.w_uk || !packed;
     const void *q = p.chained ? p.q_lat : p.q;
-    const int D = p.R + p.P;
     AttnMaps maps;
     memset(&maps, 0, sizeof(maps));
-    const uint64_t page_b = (uint64_t)p.page_stride * 2, tok_b = (uint64_t)p.token_stride * 2;
-    if (!map3(&maps.cache, dtype, p.cache, D, p.page_size, p.num_pages, tok_b,
-              p.num_pages > 1 ? page_b : (page_b > tok_b ? page_b : tok_b), p.box_tokens) ||
-        !map2(&maps.q, dtype, q, D, (uint64_t)p.N * p.heads, (uint64_t)D * 2, p.nr))
-        return SPX_ERR_UNSUPPORTED;
+    if (!attn_maps(p, dtype, q, &maps)) return SPX_ERR_UNSUPPORTED;
     const int sms = device_sm_count();
     if (sms < 1) return SPX_ERR_CUDA;
     const int blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
