@@ -733,97 +733,152 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
 }
 
 // ----------------------------------------------------------- result launch --
-// What became of a row of the call: its unit's shares, or nothing.
-struct RowSum {
-    int first, last, slot, col;  // blocks of the unit's shares, first slot, row within the unit
-    bool whole, none, owned;
+// What became of a row of the call: its unit's shares, or nothing.  A warp
+// looks up RW rows together and issues each kind of load for all of them, and
+// for all shares, before it uses the first: the launch is a chain of four
+// dependent reads (requests, units, weights, sums), which one after another
+// for four rows and 150 shares cost over 10 us.
+template <int RW>
+struct RowSums {
+    int first[RW], n[RW], slot[RW], col[RW];  // first block, shares, first slot, row within the unit
+    bool whole[RW], owned[RW];
+    float f[RW][kMaxBlocks / 32];             // factor of the share first + 32 q + lane
+    float lse[RW];
+    __device__ __forceinline__ int slot_of(int i, int k) const { return k == 0 ? slot[i] : 2 * (first[i] + k); }
 };
-// Warp-wide: the request of query row n, then the unit of (n, head h).
-__device__ __forceinline__ RowSum find_row(const LatentParams &p, int n, int h, int lane) {
-    RowSum r{0, -1, 0, 0, false, true, false};
-    int b = -1;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        bool in = false;
-        if (b0 + lane < p.B) {
-            const LatentReq rq = latent_req(p, b0 + lane);
-            in = n >= rq.row0 && n < rq.row0 + rq.T;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, in);
-        if (hit) {
-            b = b0 + __ffs(hit) - 1;
-            break;
-        }
-    }
-    if (b < 0) return r;
-    r.owned = true;
-    const LatentReq rq = latent_req(p, b);
-    const int row = (n - rq.row0) * p.heads + h, g = row / p.nr;
-    r.col = row - g * p.nr;
-    const int last = p.by_heads(min((g + 1) * p.nr, rq.T * p.heads) - 1);
-    if (latent_limit(p, rq, last) <= 0) return r;  // a unit without tiles
-    const int4 u = __ldcg(p.units + (size_t)b * p.groups + g);
-    r.first = u.x;
-    r.last = u.y;
-    r.slot = u.z;
-    r.whole = u.w != 0;
-    r.none = false;
-    return r;
-}
-__device__ __forceinline__ int slot_of(const RowSum &r, int c) { return c == r.first ? r.slot : 2 * c; }
-// Warp-wide: total weight and reference of a row's partial sums; f[q] becomes
-// the factor of the share r.first + 32 q + lane.  Every load is issued before
-// the first is used: with 150 shares a chain of loads cost 10 us.
 constexpr int kShareChunks = kMaxBlocks / 32;
-__device__ __forceinline__ float2 join_weights(const LatentParams &p, const RowSum &r, int lane, float (&f)[kShareChunks]) {
-    float2 v[kShareChunks];
-    float M = -INFINITY, L = 0.f;
+
+// Warp-wide: rows (n[i], head h); n[i] < 0 = none.
+template <int RW>
+__device__ __forceinline__ void find_rows(const LatentParams &p, const int (&n)[RW], int h, int lane, RowSums<RW> &r) {
+    int unit[RW];
 #pragma unroll
-    for (int q = 0; q < kShareChunks; ++q) {
-        const int c = r.first + 32 * q + lane;
-        v[q] = make_float2(-INFINITY, 0.f);
-        if (c <= r.last) v[q] = __ldcg(p.ml + (size_t)slot_of(r, c) * p.nr + r.col);
+    for (int i = 0; i < RW; ++i) {
+        unit[i] = -1;
+        r.owned[i] = r.whole[i] = false;
+        r.first[i] = r.n[i] = r.slot[i] = r.col[i] = 0;
     }
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        LatentReq rq{0, 0, 0};
+        if (b0 + lane < p.B) rq = latent_req(p, b0 + lane);
 #pragma unroll
-    for (int q = 0; q < kShareChunks; ++q) M = fmaxf(M, v[q].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-#pragma unroll
-    for (int q = 0; q < kShareChunks; ++q) {
-        f[q] = v[q].x == -INFINITY ? 0.f : ex2(v[q].x - M);
-        L += v[q].x == -INFINITY ? v[q].y : v[q].y * f[q];
+        for (int i = 0; i < RW; ++i) {
+            const uint32_t hit = __ballot_sync(0xffffffffu, n[i] >= rq.row0 && n[i] < rq.row0 + rq.T);
+            if (!hit || r.owned[i]) continue;
+            const int src = __ffs(hit) - 1;
+            const LatentReq o{__shfl_sync(0xffffffffu, rq.row0, src), __shfl_sync(0xffffffffu, rq.T, src),
+                              __shfl_sync(0xffffffffu, rq.len, src)};
+            r.owned[i] = true;
+            const int row = (n[i] - o.row0) * p.heads + h, g = row >> p.nr_log2;
+            r.col[i] = row & (p.nr - 1);
+            const int last = p.by_heads(min((g + 1) << p.nr_log2, o.T * p.heads) - 1);
+            if (latent_limit(p, o, last) > 0) unit[i] = (b0 + src) * p.groups + g;  // else a unit without tiles
+        }
     }
+    int4 u[RW];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    for (int i = 0; i < RW; ++i) u[i] = unit[i] >= 0 ? __ldcg(p.units + unit[i]) : make_int4(0, -1, 0, 0);
 #pragma unroll
-    for (int q = 0; q < kShareChunks; ++q) f[q] *= inv;
-    return make_float2(M, L);
+    for (int i = 0; i < RW; ++i) {
+        r.first[i] = u[i].x;
+        r.whole[i] = u[i].w != 0;
+        r.n[i] = r.whole[i] ? 0 : u[i].y - u[i].x + 1;
+        r.slot[i] = u[i].z;
+    }
+    float2 v[RW][kShareChunks];
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int q = 0; q < kShareChunks; ++q) {
+            const int k = 32 * q + lane;
+            v[i][q] = make_float2(-INFINITY, 0.f);
+            if (k < r.n[i]) v[i][q] = __ldcg(p.ml + (size_t)r.slot_of(i, k) * p.nr + r.col[i]);
+        }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int q = 0; q < kShareChunks; ++q) M = fmaxf(M, v[i][q].x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+        for (int q = 0; q < kShareChunks; ++q) {
+            r.f[i][q] = v[i][q].x == -INFINITY ? 0.f : ex2(v[i][q].x - M);
+            L += v[i][q].x == -INFINITY ? v[i][q].y : v[i][q].y * r.f[i][q];
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int q = 0; q < kShareChunks; ++q) r.f[i][q] *= inv;
+        r.lse[i] = (M + log2f(L) - kShift) * 0.6931471805599453f;
+    }
 }
-// Warp-wide: columns d4 .. d4 + 3 of the row's joined sum over the shares
-// first + k0, + step and so on (step at most 32).
-__device__ __forceinline__ float4 join_sums(const LatentParams &p, const RowSum &r, const float (&f)[kShareChunks],
-                                            int k0, int step, int d4) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+// The same for one row, handed by the warp that looked it up to the others of
+// its block (each of them asking for itself made every block's 16 warps queue
+// for the same few lines of L2: 10 us with 150 shares).
+struct RowCard {
+    int first, n, slot, col, whole, owned;
+    float f[kMaxBlocks];
+    __device__ __forceinline__ void put(const RowSums<1> &r, int lane) {
+        if (lane == 0) {
+            first = r.first[0];
+            n = r.n[0];
+            slot = r.slot[0];
+            col = r.col[0];
+            whole = r.whole[0];
+            owned = r.owned[0];
+        }
+        for (int q = 0; q < kShareChunks; ++q) f[32 * q + lane] = r.f[0][q];
+    }
+    __device__ __forceinline__ void get(RowSums<1> &r, int lane) const {
+        r.first[0] = first;
+        r.n[0] = n;
+        r.slot[0] = slot;
+        r.col[0] = col;
+        r.whole[0] = whole;
+        r.owned[0] = owned;
+#pragma unroll
+        for (int q = 0; q < kShareChunks; ++q) r.f[0][q] = f[32 * q + lane];
+    }
+};
+// Warp-wide: columns d4 .. d4 + 3 of the rows' joined sums over the shares k0,
+// k0 + step and so on (step at most 32).
+template <int RW>
+__device__ __forceinline__ void join_sums(const LatentParams &p, const RowSums<RW> &r, int k0, int step, int d4,
+                                          float4 (&a)[RW]) {
+    int most = 0;
+#pragma unroll
+    for (int i = 0; i < RW; ++i) most = max(most, r.n[i]);
 #pragma unroll
     for (int q = 0; q < kShareChunks; ++q) {
-        const int n = r.last - r.first + 1 - 32 * q;
-#pragma unroll 4
-        for (int k = 0; k < min(n, 32); k += step) {
-            const float g = __shfl_sync(0xffffffffu, f[q], (k + k0) & 31);
-            if (k + k0 < min(n, 32)) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                    p.part + ((size_t)slot_of(r, r.first + 32 * q + k + k0) * p.nr + r.col) * p.R + d4));
-                a.x = fmaf(g, v.x, a.x);
-                a.y = fmaf(g, v.y, a.y);
-                a.z = fmaf(g, v.z, a.z);
-                a.w = fmaf(g, v.w, a.w);
+        if (32 * q >= most) break;
+#pragma unroll(RW == 1 ? 8 : 2)
+        for (int k = 0; k < min(most - 32 * q, 32); k += step) {
+            float4 v[RW];
+            float g[RW];
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const int c = 32 * q + k + k0;
+                const bool in = k + k0 < 32 && c < r.n[i];
+                g[i] = __shfl_sync(0xffffffffu, r.f[i][q], (k + k0) & 31);
+                if (!in) g[i] = 0.f;
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (in)
+                    v[i] = __ldcg(reinterpret_cast<const float4 *>(
+                        p.part + ((size_t)r.slot_of(i, c) * p.nr + r.col[i]) * p.R + d4));
+            }
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                a[i].x = fmaf(g[i], v[i].x, a[i].x);
+                a[i].y = fmaf(g[i], v[i].y, a[i].y);
+                a[i].z = fmaf(g[i], v[i].z, a[i].z);
+                a[i].w = fmaf(g[i], v[i].w, a[i].w);
             }
         }
     }
-    return a;
 }
-__device__ __forceinline__ float joined_lse(float2 j) { return (j.x + log2f(j.y) - kShift) * 0.6931471805599453f; }
-
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -831,11 +886,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// Another block's shared memory (between two cluster barriers, so that the
+// loads need no order among themselves).
 __device__ __forceinline__ float2 cluster_ld2(const void *p, uint32_t rank) {
     uint32_t a;
     float2 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
     return v;
 }
 
@@ -845,7 +902,7 @@ __device__ __forceinline__ float2 cluster_ld2(const void *p, uint32_t rank) {
 // product as two values of the type (v and what its rounding left), which
 // costs nothing here and saves a rounding.
 template <int DT, int MT>
-__global__ void __launch_bounds__(512) latent_out_kernel(const __grid_constant__ LatentParams p) {
+__global__ void __launch_bounds__(512, 1) latent_out_kernel(const __grid_constant__ LatentParams p) {
     extern __shared__ __align__(128) uint8_t lo_smem[];
     uint16_t *wv = reinterpret_cast<uint16_t *>(lo_smem);          // [dv][72]
     uint16_t *hi = wv + p.dv * 72, *lo = hi + 16 * MT * 72;        // [16 MT][72] each
@@ -864,28 +921,42 @@ __global__ void __launch_bounds__(512) latent_out_kernel(const __grid_constant__
             reinterpret_cast<uint4 *>(hi)[i] = reinterpret_cast<uint4 *>(lo)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
     }
-    const int wp = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;  // warps that share a row
+    // 16 warps: MT rows each, or with few rows several warps (and always both halves) for one
+    const int wp = MT > 1 || rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;
     const int sub = warp % wp, half = lane >> 4, d4 = 4 * (lane & 15);
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 16 / wp) {
-        const int r = r0 + warp / wp;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) {
-            const RowSum u = find_row(p, n0 + r, h, lane);
-            const size_t row = (size_t)(n0 + r) * p.heads + h;
-            if (u.whole) {
-                if (sub == 0 && half == 0) a = __ldcg(reinterpret_cast<const float4 *>(p.o_lat + row * p.R + 64 * s + d4));
-            } else {
-                float lse = -INFINITY;
-                if (!u.none) {
-                    float f[kShareChunks];
-                    const float2 j = join_weights(p, u, lane, f);
-                    a = join_sums(p, u, f, 2 * sub + half, 2 * wp, 64 * s + d4);
-                    lse = joined_lse(j);
-                }
-                if (u.owned && s == 0 && sub == 0 && lane == 0 && p.lse) p.lse[row] = lse;
-            }
+    int n[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) n[i] = warp / wp + 16 * i < rows ? n0 + warp / wp + 16 * i : -1;
+    RowSums<MT> rs;
+    if (MT == 1) {
+        __shared__ RowCard cards[16];
+        if (warp < rows) {
+            const int one[1] = {n0 + warp};
+            RowSums<1> r;
+            find_rows<1>(p, one, h, lane, r);
+            cards[warp].put(r, lane);
+            if (r.owned[0] && !r.whole[0] && s == 0 && lane == 0 && p.lse)
+                p.lse[(size_t)one[0] * p.heads + h] = r.lse[0];
         }
+        __syncthreads();
+        cards[min(warp / wp, rows - 1)].get(reinterpret_cast<RowSums<1> &>(rs), lane);
+        if (n[0] < 0) rs.n[0] = rs.whole[0] = 0;
+    } else {
+        find_rows<MT>(p, n, h, lane, rs);
+    }
+    float4 sum[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const size_t row = (size_t)n[i] * p.heads + h;
+        if (rs.whole[i] && sub == 0 && half == 0)
+            sum[i] = __ldcg(reinterpret_cast<const float4 *>(p.o_lat + row * p.R + 64 * s + d4));
+        if (MT > 1 && rs.owned[i] && !rs.whole[i] && s == 0 && lane == 0 && p.lse) p.lse[row] = rs.lse[i];
+    }
+    join_sums<MT>(p, rs, 2 * sub + half, 2 * wp, 64 * s + d4, sum);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        float4 a = sum[i];
         a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
         a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
         a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
@@ -901,9 +972,9 @@ __global__ void __launch_bounds__(512) latent_out_kernel(const __grid_constant__
                     a.z += v.z;
                     a.w += v.w;
                 }
-            __syncthreads();
         }
-        if (sub == 0 && half == 0 && r < rows) {
+        if (sub == 0 && half == 0 && n[i] >= 0) {
+            const int r = n[i] - n0;
             const uint2 v = make_uint2(Elem<DT>::down2(a.x, a.y), Elem<DT>::down2(a.z, a.w));
             const float2 y = Elem<DT>::up2(v.x), z = Elem<DT>::up2(v.y);
             *reinterpret_cast<uint2 *>(hi + r * 72 + d4) = v;
@@ -942,17 +1013,19 @@ __global__ void __launch_bounds__(512) latent_out_kernel(const __grid_constant__
     }
     cluster_arrive();
     cluster_wait();
-    const int ns = p.R / 64, pairs = rows * p.dv / 2;
-    const uint32_t rank = cluster_rank();
-    for (int i = (int)rank * 512 + threadIdx.x; i < pairs; i += ns * 512) {
-        float2 a = make_float2(0.f, 0.f);
-        for (int k = 0; k < ns; ++k) {
-            const float2 v = cluster_ld2(part + 2 * i, (uint32_t)k);
-            a.x += v.x;
-            a.y += v.y;
+    const int ns = p.R / 64, dv_log2 = p.dv == 128 ? 7 : 6, pairs = rows << (dv_log2 - 1);
+    for (int i = (int)cluster_rank() * 512 + threadIdx.x; i < pairs; i += ns * 512) {
+        float2 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < ns ? cluster_ld2(part + 2 * i, (uint32_t)k) : make_float2(0.f, 0.f);
+        float2 a = v[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+            a.x += v[k].x;
+            a.y += v[k].y;
         }
-        const int r = 2 * i / p.dv, v = 2 * i - r * p.dv;
-        *reinterpret_cast<uint32_t *>(p.out + (n0 + r) * p.out_stride + (size_t)h * p.dv + v) =
+        const int r = 2 * i >> dv_log2, d = 2 * i & (p.dv - 1);
+        *reinterpret_cast<uint32_t *>(p.out + (n0 + r) * p.out_stride + (size_t)h * p.dv + d) =
             Elem<DT>::down2(a.x, a.y);
     }
     cluster_arrive();
@@ -962,35 +1035,36 @@ __global__ void __launch_bounds__(512) latent_out_kernel(const __grid_constant__
 // Folded weights: one block per row joins its partial sums, 4 columns a thread
 // and four threads a column; rows of whole units are there already.
 template <int DT>
-__global__ void __launch_bounds__(512) latent_join_kernel(const __grid_constant__ LatentParams p) {
+__global__ void __launch_bounds__(512, 2) latent_join_kernel(const __grid_constant__ LatentParams p) {
     __shared__ float4 spread[3][128];
+    __shared__ RowCard card;
     griddep_wait();
     griddep_launch_dependents();
-    const int row = blockIdx.x, n = row / p.heads, h = row - n * p.heads, lane = threadIdx.x & 31;
+    const int row = blockIdx.x, n[1] = {p.by_heads(row)}, h = row - n[0] * p.heads, lane = threadIdx.x & 31;
     const int sub = threadIdx.x >> 7, d4 = 4 * (threadIdx.x & 127);
-    const RowSum u = find_row(p, n, h, lane);
-    if (u.whole || !u.owned) return;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float lse = -INFINITY;
-    if (!u.none) {
-        float f[kShareChunks];
-        const float2 j = join_weights(p, u, lane, f);
-        if (d4 < p.R) a = join_sums(p, u, f, sub, 4, d4);
-        lse = joined_lse(j);
+    RowSums<1> rs;
+    if (threadIdx.x < 32) {
+        find_rows<1>(p, n, h, lane, rs);
+        card.put(rs, lane);
     }
-    if (sub) spread[sub - 1][threadIdx.x & 127] = a;
+    __syncthreads();
+    if (card.whole || !card.owned) return;
+    card.get(rs, lane);
+    float4 a[1] = {make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (d4 < p.R) join_sums<1>(p, rs, sub, 4, d4, a);
+    if (sub) spread[sub - 1][threadIdx.x & 127] = a[0];
     __syncthreads();
     if (sub || d4 >= p.R) return;
     for (int k = 0; k < 3; ++k) {
         const float4 v = spread[k][threadIdx.x];
-        a.x += v.x;
-        a.y += v.y;
-        a.z += v.z;
-        a.w += v.w;
+        a[0].x += v.x;
+        a[0].y += v.y;
+        a[0].z += v.z;
+        a[0].w += v.w;
     }
-    *reinterpret_cast<uint2 *>(p.out + n * p.out_stride + (size_t)h * p.R + d4) =
-        make_uint2(Elem<DT>::down2(a.x, a.y), Elem<DT>::down2(a.z, a.w));
-    if (threadIdx.x == 0 && p.lse) p.lse[row] = lse;
+    *reinterpret_cast<uint2 *>(p.out + n[0] * p.out_stride + (size_t)h * p.R + d4) =
+        make_uint2(Elem<DT>::down2(a[0].x, a[0].y), Elem<DT>::down2(a[0].z, a[0].w));
+    if (threadIdx.x == 0 && p.lse) p.lse[row] = rs.lse[0];
 }
 
 // -------------------------------------------------------------------- host --
@@ -1223,6 +1297,7 @@ extern "C" int spx_latent_attention(const spx_latent_args *a, spx_stream_t strea
     p.budget = a->wait_budget_ns ? a->wait_budget_ns : 2000000000ull;
     const AbsorbedLayout l = absorbed_layout(c.B, a->N, a->max_q, a->heads, c.R, c.P, p.w_uk != nullptr);
     p.nr = rows_per_unit(a->max_q, a->heads);
+    p.nr_log2 = p.nr == 16 ? 4 : p.nr == 32 ? 5 : 6;
     p.groups = (int)(((long long)a->max_q * a->heads + p.nr - 1) / p.nr);
     p.box_tokens = c.page_size % 64 == 0 ? 64 : c.page_size % 32 == 0 ? 32 : 16;
     p.units = reinterpret_cast<int4 *>(ws + l.units);

@@ -82,7 +82,7 @@ struct LatentParams {
     float2 *ml;       // [slots][nr]: reference and weight of a partial sum
     float *part;      // [slots][nr][R]: partial sums; block c has slots 2c (its first unit) and 2c + 1 (its last)
     // geometry of the attention launch
-    int nr, groups, box_tokens;
+    int nr, nr_log2, groups, box_tokens;
     int chained;      // a launch of this call precedes the attention launch
 };
 
