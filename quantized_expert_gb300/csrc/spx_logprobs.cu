@@ -1,5 +1,17 @@
 // spx_logprobs.cu -- log probabilities of given tokens, entropy and the most
-// likely alternatives of rows of logits.
+// likely alternatives of rows of logits, in one pass over memory.
+//
+// With a reference m and t_v = (x_v - m) log2(e) a row needs z = sum 2^t_v and
+// d = sum t_v 2^t_v:  log_z = m + ln z,  entropy = ln z - ln(2) d / z.  Every
+// thread keeps a reference of its own (its running maximum), its z and d, and
+// the threads' triples are joined at the end, as are those of the blocks that
+// share a row (a cluster).
+//
+// Alternatives: each thread also remembers where its maximum lies.  The k-th
+// largest of the threads' maxima is a bound that k elements reach, and only
+// the k threads whose own maximum reaches it can hold an alternative; their
+// elements alone are read again (from L2), and the few that reach the bound
+// are ranked by counting.
 #include "spx_latent.cuh"
 
 #include <math.h>
@@ -18,85 +30,372 @@ struct LogprobParams {
 };
 
 // Order of the alternatives as one 64-bit key: the value first (larger is
-// larger, -0 = +0, NaN above all), then the lower index.
+// larger, -0 = +0, NaN above all), then the lower index.  0 is below every key.
 __device__ __forceinline__ uint32_t order32(float x) {
     if (x != x) return 0xFFFFFFFFu;
     const uint32_t u = __float_as_uint(x + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ uint64_t order64(float x, int v) {
-    return ((uint64_t)order32(x) << 32) | (uint32_t)~v;
+__device__ __forceinline__ uint64_t order64(float x, int v) { return ((uint64_t)order32(x) << 32) | (uint32_t)~v; }
+
+constexpr int kThreadsLp = 512, kWarpsLp = kThreadsLp / 32;
+constexpr int kMaxCluster = 8, kMaxTop = 32;
+constexpr int kCandidates = 2048;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// One block per row: one pass for the statistics, one per alternative.
+// Reference, sum, and sum weighted by the exponent (in base 2).
+struct Stat {
+    float m, z, d;
+};
+__device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
+    Stat r;
+    r.m = fmaxf(a.m, b.m);
+    r.z = r.d = 0.f;
+    if (a.z != 0.f) {  // (a NaN is not 0)
+        const float t = (a.m - r.m) * kLog2e, f = ex2f(t);
+        r.z += a.z * f;
+        r.d += (a.d + t * a.z) * f;
+    }
+    if (b.z != 0.f) {
+        const float t = (b.m - r.m) * kLog2e, f = ex2f(t);
+        r.z += b.z * f;
+        r.d += (b.d + t * b.z) * f;
+    }
+    return r;
+}
+
+// 16 bytes of a row: EPC elements from index v0 on, those outside [0, V) as -inf.
 template <int DT>
-__global__ void __launch_bounds__(1024) logprobs_kernel(LogprobParams p) {
-    using E = Elem<DT>;
-    const typename E::T *x = static_cast<const typename E::T *>(p.logits) + (int64_t)blockIdx.x * p.stride;
-    __shared__ float sm[32], sz[32], sd[32];
-    __shared__ uint64_t sk[32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float m = -INFINITY;
-    bool nan = false;
-    for (int v = threadIdx.x; v < p.V; v += 1024) {
-        const float f = E::up(x[v]);
-        nan |= f != f;
-        m = fmaxf(m, f);
+struct Chunk {
+    using T = typename Elem<DT>::T;
+    static constexpr int kN = 16 / (int)sizeof(T);
+    static __device__ __forceinline__ uint4 load(const T *x, int v0, int V) {
+        if (v0 >= 0 && v0 + kN <= V) return __ldg(reinterpret_cast<const uint4 *>(x + v0));
+        uint4 r;
+        T *e = reinterpret_cast<T *>(&r);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) e[i] = v0 + i >= 0 && v0 + i < V ? x[v0 + i] : Elem<DT>::down(-INFINITY);
+        return r;
     }
-    nan = __syncthreads_or(nan);
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) sm[warp] = m;
-    __syncthreads();
-    for (int w = 0; w < 32; ++w) m = fmaxf(m, sm[w]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float z = 0.f, d = 0.f;
-    for (int v = threadIdx.x; v < p.V; v += 1024) {
-        const float t = E::up(x[v]) - ref, e = expf(t);
-        z += e;
-        d += e > 0.f ? e * t : 0.f;
-    }
-    for (int o = 16; o; o >>= 1) {
-        z += __shfl_xor_sync(0xffffffffu, z, o);
-        d += __shfl_xor_sync(0xffffffffu, d, o);
-    }
-    if (lane == 0) {
-        sz[warp] = z;
-        sd[warp] = d;
-    }
-    __syncthreads();
-    z = d = 0.f;
-    for (int w = 0; w < 32; ++w) {
-        z += sz[w];
-        d += sd[w];
-    }
-    const bool none = m == -INFINITY && !nan;
-    const float log_z = nan ? NAN : none ? 0.f : m == INFINITY ? m : m + logf(z);
-    if (threadIdx.x == 0) {
-        if (p.logp) {
-            const int id = p.ids[blockIdx.x];
-            p.logp[blockIdx.x] = id >= 0 && id < p.V ? E::up(x[id]) - log_z : NAN;
+    static __device__ __forceinline__ void unpack(const uint4 &r, float (&f)[kN]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (kN == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else {
+                const float2 p = Elem<DT == SPX_F32 ? SPX_F16 : DT>::up2(w[i]);
+                f[kN == 4 ? i : 2 * i] = p.x;
+                f[kN == 4 ? i : 2 * i + 1] = p.y;
+            }
         }
-        if (p.entropy) p.entropy[blockIdx.x] = nan ? NAN : none ? 0.f : logf(z) - d / z;
     }
+};
+
+struct LogprobSmem {
+    uint64_t key[kThreadsLp];        // the threads' maxima, sorted within each warp
+    uint64_t cand[kCandidates];
+    uint64_t top[kMaxCluster][kMaxTop];  // block 0: every block's alternatives
+    Stat part[kMaxCluster];              // block 0: every block's sums
+    Stat warp[kWarpsLp];
+    uint64_t tau;
+    int n_cand, n_slices, slices[kThreadsLp];
+    int slow;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a)
+        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void cluster_st(uint32_t a, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_st(uint32_t a, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+// The k largest keys of a row, one pass over it for each: rows with an
+// infinity or a NaN, and more candidates than the buffer holds.
+template <int DT>
+__device__ void top_by_passes(const typename Elem<DT>::T *x, int lo, int hi, int k, uint64_t *top, uint64_t *scratch) {
     uint64_t last = ~0ull;
-    for (int j = 0; j < p.k; ++j) {
+    for (int j = 0; j < k; ++j) {
         uint64_t best = 0;
-        for (int v = threadIdx.x; v < p.V; v += 1024) {
-            const uint64_t key = order64(E::up(x[v]), v);
+        for (int v = lo + threadIdx.x; v < hi; v += kThreadsLp) {
+            const uint64_t key = order64(Elem<DT>::up(x[v]), v);
             if (key < last && key > best) best = key;
         }
         for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
         __syncthreads();
-        if (lane == 0) sk[warp] = best;
+        if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = best;
         __syncthreads();
-        for (int w = 0; w < 32; ++w) best = max(best, sk[w]);
+        for (int w = 0; w < kWarpsLp; ++w) best = max(best, scratch[w]);
         last = best;
-        if (threadIdx.x == 0) {
-            const int v = (int)~(uint32_t)best;
-            p.top_ids[(size_t)blockIdx.x * p.k + j] = v;
-            p.top_logp[(size_t)blockIdx.x * p.k + j] = E::up(x[v]) - log_z;
+        if (threadIdx.x == 0) top[j] = best;
+    }
+    __syncthreads();
+}
+
+// One cluster per row, its blocks taking equal stretches of it.
+template <int DT>
+__global__ void __launch_bounds__(kThreadsLp, 3) logprobs_kernel(const __grid_constant__ LogprobParams p) {
+    using E = Elem<DT>;
+    using T = typename E::T;
+    using C = Chunk<DT>;
+    constexpr int N = C::kN;
+    __shared__ LogprobSmem s;
+    const int nb = gridDim.x, row = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const T *x = static_cast<const T *>(p.logits) + (int64_t)row * p.stride;
+    // chunk c holds the elements N c - shift on, so that its 16 bytes are aligned
+    const int shift = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    const int chunks = (p.V + shift + N - 1) / N, share = (chunks + nb - 1) / nb;
+    const int c0 = (int)rank * share, c1 = min(chunks, c0 + share);
+
+    Stat a{-INFINITY, 0.f, 0.f};
+    int at = c0 + tid;    // chunk of the first maximum
+    bool bad = false;
+    constexpr int kAhead = 4;  // loads in flight per thread
+#pragma unroll 1
+    for (int first = c0 + tid; first < c1; first += kAhead * kThreadsLp) {
+        uint4 raw[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (first + u * kThreadsLp < c1) raw[u] = C::load(x, N * (first + u * kThreadsLp) - shift, p.V);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int c = first + u * kThreadsLp;
+            if (c >= c1) break;
+            float f[N];
+            C::unpack(raw[u], f);
+            float mx = f[0];
+#pragma unroll
+            for (int i = 1; i < N; ++i) mx = fmaxf(mx, f[i]);
+            if (mx > a.m) {
+                if (a.z != 0.f) {
+                    const float t = (a.m - mx) * kLog2e, g = ex2f(t);
+                    a.d = (a.d + t * a.z) * g;
+                    a.z *= g;
+                }
+                a.m = mx;
+                at = c;
+            }
+            if (a.m > -INFINITY) {
+                // A difference first: logits near the type's largest would overflow in base 2.  The weight
+                // of -inf is 0, and so is its term of d (0 times a clamped exponent); a NaN stays in z.
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float t = (f[i] - a.m) * kLog2e, e = ex2f(t);
+                    a.z += e;
+                    a.d = fmaf(e, fmaxf(t, -200.f), a.d);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) bad |= f[i] != f[i];
+            }
         }
     }
+    bad |= a.m == INFINITY || a.z != a.z;
+    const float own_m = a.m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        Stat b;
+        b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+        b.z = __shfl_xor_sync(0xffffffffu, a.z, o);
+        b.d = __shfl_xor_sync(0xffffffffu, a.d, o);
+        a = join(a, b);
+    }
+    if (lane == 0) s.warp[warp] = a;
+    if (tid == 0) s.n_cand = s.n_slices = 0;
+    const bool block_bad = __syncthreads_or(bad);
+
+    if (p.k > 0 && !block_bad) {
+        // Lower and upper end of the keys that this thread's maximum may have.
+        const bool any = c0 + tid < c1;
+        const uint64_t hi_key = any ? order64(own_m, max(N * at - shift, 0)) : 0;
+        uint64_t key = any ? order64(own_m, N * at - shift + N - 1) : 0;
+        // sort the warp's 32, largest first
+#pragma unroll
+        for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+            for (int o = size >> 1; o; o >>= 1) {
+                const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+                const bool down = (lane & size) == 0 || size == 32, first = (lane & o) == 0;
+                key = (first == down) ? max(key, other) : min(key, other);
+            }
+        s.key[tid] = key;
+        __syncthreads();
+        // rank among all: position here plus, in every other warp's list, how many are larger
+        // (equal keys, of threads without elements, by the warp's number)
+        int rank_of = lane;
+#pragma unroll 4
+        for (int w = 0; w < kWarpsLp; ++w) {
+            if (w == warp) continue;
+            int lo = 0;
+#pragma unroll
+            for (int step = 16; step; step >>= 1) {
+                const uint64_t v = s.key[32 * w + lo + step - 1];
+                if (v > key || (v == key && w < warp)) lo += step;
+            }
+            const uint64_t v = s.key[32 * w + min(lo, 31)];
+            if (lo < 32 && (v > key || (v == key && w < warp))) ++lo;
+            rank_of += lo;
+        }
+        if (rank_of == p.k - 1) s.tau = key;
+        __syncthreads();
+        const uint64_t tau = s.tau;
+        if (any && hi_key >= tau) s.slices[atomicAdd(&s.n_slices, 1)] = tid;
+        __syncthreads();
+        // a warp per such thread reads its chunks again
+        for (int i = warp; i < s.n_slices; i += kWarpsLp) {
+            const int t = s.slices[i];
+            for (int c = c0 + t + lane * kThreadsLp; c < c1; c += 32 * kThreadsLp) {
+                float f[N];
+                C::unpack(C::load(x, N * c - shift, p.V), f);
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const int v = N * c - shift + e;
+                    if (v < 0 || v >= p.V) continue;
+                    const uint64_t kk = order64(f[e], v);
+                    if (kk >= tau) {
+                        const int n = atomicAdd(&s.n_cand, 1);
+                        if (n < kCandidates) s.cand[n] = kk;
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (s.n_cand > kCandidates) {
+            top_by_passes<DT>(x, max(N * c0 - shift, 0), min(N * c1 - shift, p.V), p.k, s.cand, s.key);
+            if (tid == 0) s.n_cand = p.k;
+            __syncthreads();
+        }
+        // the block's alternatives, to block 0
+        const int n = s.n_cand;
+        for (int i = tid; i < n; i += kThreadsLp) {
+            const uint64_t kk = s.cand[i];
+            int r = 0;
+            for (int j = 0; j < n && r < p.k; ++j) r += s.cand[j] > kk;
+            // (a pass over too short a stretch leaves zeros)
+            if (r < p.k && kk) cluster_st(cluster_addr(&s.top[rank][r], 0), kk);
+        }
+        for (int i = n + tid; i < p.k; i += kThreadsLp) cluster_st(cluster_addr(&s.top[rank][i], 0), (uint64_t)0);
+    }
+    if (warp == 0) {
+        a = lane < kWarpsLp ? s.warp[lane] : Stat{-INFINITY, 0.f, 0.f};
+#pragma unroll
+        for (int o = kWarpsLp / 2; o; o >>= 1) {
+            Stat b;
+            b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+            b.z = __shfl_xor_sync(0xffffffffu, a.z, o);
+            b.d = __shfl_xor_sync(0xffffffffu, a.d, o);
+            a = join(a, b);
+        }
+        if (lane == 0) {
+            const uint32_t to = cluster_addr(&s.part[rank], 0);
+            cluster_st(to, a.m);
+            cluster_st(to + 4, block_bad ? NAN : a.z);
+            cluster_st(to + 8, a.d);
+        }
+    }
+    cluster_sync();
+    if (rank != 0) return;
+
+    // ---- block 0: the row
+    a = s.part[0];
+    bool slow = a.z != a.z, nan = false;  // (block_bad)
+    for (int b = 1; b < nb; ++b) {
+        slow |= s.part[b].z != s.part[b].z;
+        a = join(a, s.part[b]);
+    }
+    if (slow) {  // an infinity or a NaN somewhere
+        bool n = false;
+        for (int v = tid; v < p.V; v += kThreadsLp) {
+            const float f = E::up(x[v]);
+            n |= f != f;
+        }
+        nan = __syncthreads_or(n);
+    }
+    const bool none = !slow && a.m == -INFINITY;
+    const float log_z = slow ? (nan ? NAN : INFINITY) : none ? 0.f : a.m + logf(a.z);
+    if (tid == 0) {
+        if (p.logp) {
+            const int id = p.ids[row];
+            p.logp[row] = id >= 0 && id < p.V ? E::up(x[id]) - log_z : NAN;
+        }
+        if (p.entropy) p.entropy[row] = slow ? NAN : none ? 0.f : fmaxf(logf(a.z) - kLn2 * a.d / a.z, 0.f);
+    }
+    if (p.k > 0) {
+        if (slow) top_by_passes<DT>(x, 0, p.V, p.k, s.cand, s.key);
+        const int n = slow ? p.k : nb * p.k;
+        for (int i = tid; i < n; i += kThreadsLp) {
+            const uint64_t kk = slow ? s.cand[i] : s.top[i / p.k][i % p.k];
+            if (!kk) continue;
+            int r = i;
+            if (!slow && nb > 1) {
+                r = 0;
+                for (int b = 0; b < nb; ++b)
+                    for (int j = 0; j < p.k && s.top[b][j] > kk; ++j) ++r;
+            }
+            if (r < p.k) {
+                const int v = (int)~(uint32_t)kk;
+                p.top_ids[(size_t)row * p.k + r] = v;
+                p.top_logp[(size_t)row * p.k + r] = E::up(x[v]) - log_z;
+            }
+        }
+    }
+}
+
+// Blocks per row: enough of them to give every SM work, at most a portable
+// cluster, and none with less than two chunks a thread.
+int blocks_per_row(int N, int64_t bytes) {
+    int nb = 1;
+    while (nb < kMaxCluster && (int64_t)N * nb < 4 * 152 && bytes / (2 * nb) >= 2 * 16 * kThreadsLp) nb *= 2;
+    return nb;
+}
+
+template <int DT>
+int launch(const LogprobParams &p, cudaStream_t s) {
+    const int nb = blocks_per_row(p.N, (int64_t)p.V * (int64_t)sizeof(typename Elem<DT>::T));
+    LogprobParams q = p;
+    for (int r0 = 0; r0 < p.N; r0 += 65535) {  // the grid's second dimension
+        q.logits = static_cast<const typename Elem<DT>::T *>(p.logits) + (int64_t)r0 * p.stride;
+        q.N = p.N - r0 < 65535 ? p.N - r0 : 65535;
+        q.ids = p.ids ? p.ids + r0 : nullptr;
+        q.logp = p.logp ? p.logp + r0 : nullptr;
+        q.entropy = p.entropy ? p.entropy + r0 : nullptr;
+        q.top_ids = p.top_ids ? p.top_ids + (size_t)r0 * p.k : nullptr;
+        q.top_logp = p.top_logp ? p.top_logp + (size_t)r0 * p.k : nullptr;
+        cudaLaunchConfig_t c = {};
+        c.gridDim = dim3(nb, q.N);
+        c.blockDim = dim3(kThreadsLp);
+        c.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = nb;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        c.attrs = attr;
+        c.numAttrs = 1;
+        const int st = record_launch(cudaLaunchKernelEx(&c, logprobs_kernel<DT>, q));
+        if (st) return st;
+    }
+    return SPX_OK;
 }
 
 }  // namespace
@@ -108,7 +407,7 @@ using namespace spx;
 extern "C" int spx_token_logprobs(const spx_logprobs_args *a, spx_stream_t stream) {
     if (!a || a->N < 0 || a->V < 1 || a->k < 0 || a->k > a->V) return SPX_ERR_INVALID_ARG;
     if (a->dtype != SPX_F16 && a->dtype != SPX_BF16 && a->dtype != SPX_F32) return SPX_ERR_UNSUPPORTED;
-    if (a->k > 32) return SPX_ERR_UNSUPPORTED;
+    if (a->k > kMaxTop || a->V > 1 << 30) return SPX_ERR_UNSUPPORTED;
     if (a->N == 0) return SPX_OK;
     if (!a->logits || a->stride < a->V || !a->ids != !a->logp || (a->k > 0) != (a->top_ids != nullptr) ||
         (a->k > 0) != (a->top_logp != nullptr))
@@ -117,11 +416,6 @@ extern "C" int spx_token_logprobs(const spx_logprobs_args *a, spx_stream_t strea
     if (reinterpret_cast<uintptr_t>(a->logits) % es) return SPX_ERR_INVALID_ARG;
     LogprobParams p{a->logits, a->stride, a->N, a->V, a->k, a->ids, a->logp, a->entropy, a->top_logp, a->top_ids};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (a->dtype == SPX_F16)
-        logprobs_kernel<SPX_F16><<<a->N, 1024, 0, s>>>(p);
-    else if (a->dtype == SPX_BF16)
-        logprobs_kernel<SPX_BF16><<<a->N, 1024, 0, s>>>(p);
-    else
-        logprobs_kernel<SPX_F32><<<a->N, 1024, 0, s>>>(p);
-    return record_launch(cudaGetLastError());
+    return a->dtype == SPX_F16 ? launch<SPX_F16>(p, s) : a->dtype == SPX_BF16 ? launch<SPX_BF16>(p, s)
+                                                                                : launch<SPX_F32>(p, s);
 }
