@@ -7,11 +7,11 @@
 // the threads' triples are joined at the end, as are those of the blocks that
 // share a row (a cluster).
 //
-// Alternatives: each thread also remembers where its maximum lies.  The k-th
-// largest of the threads' maxima is a bound that k elements reach, and only
-// the k threads whose own maximum reaches it can hold an alternative; their
-// elements alone are read again (from L2), and the few that reach the bound
-// are ranked by counting.
+// Alternatives: each thread also remembers where its maximum lies.  A bound
+// that between k and 2k of the threads' maxima reach (found by bisection) is
+// one that at least k elements reach, and only those threads can hold an
+// alternative; their elements alone are read again (from L2), and the few that
+// reach the bound are ranked by counting.
 #include "spx_latent.cuh"
 
 #include <math.h>
@@ -38,7 +38,7 @@ __device__ __forceinline__ uint32_t order32(float x) {
 }
 __device__ __forceinline__ uint64_t order64(float x, int v) { return ((uint64_t)order32(x) << 32) | (uint32_t)~v; }
 
-constexpr int kThreadsLp = 512, kWarpsLp = kThreadsLp / 32;
+constexpr int kThreadsLp = 256, kWarpsLp = kThreadsLp / 32;
 constexpr int kMaxCluster = 8, kMaxTop = 32;
 constexpr int kCandidates = 2048;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -70,7 +70,34 @@ __device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
     return r;
 }
 
-// 16 bytes of a row: EPC elements from index v0 on, those outside [0, V) as -inf.
+// Two fp32 values in one 64-bit register and the instructions that take them.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// 16 bytes of a row: kN elements from index v0 on, those outside [0, V) as -inf.
 template <int DT>
 struct Chunk {
     using T = typename Elem<DT>::T;
@@ -98,13 +125,54 @@ struct Chunk {
     }
 };
 
+// One thread's running sums over the elements of its chunks (two of each kind).
+template <int DT>
+struct Running {
+    float m = -INFINITY;
+    uint64_t minus_m = 0, z = 0, d = 0;
+    int at;  // chunk of the first maximum
+    bool bad = false;
+    __device__ __forceinline__ void take(const uint4 &raw, int c) {
+        using C = Chunk<DT>;
+        float f[C::kN];
+        C::unpack(raw, f);
+        float mx = f[0];
+#pragma unroll
+        for (int i = 1; i < C::kN; ++i) mx = fmaxf(mx, f[i]);
+        if (mx > m) {
+            if (m > -INFINITY) {
+                const float t = (m - mx) * kLog2e, g = ex2f(t);
+                d = mul2(fma2(pack2(t, t), z, d), pack2(g, g));
+                z = mul2(z, pack2(g, g));
+            }
+            m = mx;
+            minus_m = pack2(-mx, -mx);
+            at = c;
+        }
+        if (m > -INFINITY) {
+            // A difference first: logits near the type's largest would overflow in base 2.  The weight
+            // of -inf is 0, and so is its term of d (0 times a clamped exponent); a NaN stays in z.
+#pragma unroll
+            for (int i = 0; i < C::kN; i += 2) {
+                const float2 t = unpack2(mul2(add2(pack2(f[i], f[i + 1]), minus_m), pack2(kLog2e, kLog2e)));
+                const uint64_t e = pack2(ex2f(t.x), ex2f(t.y));
+                z = add2(z, e);
+                d = fma2(e, pack2(fmaxf(t.x, -200.f), fmaxf(t.y, -200.f)), d);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < C::kN; ++i) bad |= f[i] != f[i];
+        }
+    }
+};
+
 struct LogprobSmem {
-    uint64_t key[kThreadsLp];        // the threads' maxima, sorted within each warp
+    uint64_t key[kWarpsLp];              // scratch
     uint64_t cand[kCandidates];
     uint64_t top[kMaxCluster][kMaxTop];  // block 0: every block's alternatives
     Stat part[kMaxCluster];              // block 0: every block's sums
     Stat warp[kWarpsLp];
-    uint64_t tau;
+    uint32_t lo[kWarpsLp], hi[kWarpsLp];
     int n_cand, n_slices, slices[kThreadsLp];
     int slow;
 };
@@ -128,6 +196,11 @@ __device__ __forceinline__ void cluster_st(uint32_t a, float v) {
 }
 __device__ __forceinline__ void cluster_st(uint32_t a, uint64_t v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+// The value of a key's upper half.
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return o == 0xFFFFFFFFu ? NAN : __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
 
 // The k largest keys of a row, one pass over it for each: rows with an
@@ -154,7 +227,7 @@ __device__ void top_by_passes(const typename Elem<DT>::T *x, int lo, int hi, int
 
 // One cluster per row, its blocks taking equal stretches of it.
 template <int DT>
-__global__ void __launch_bounds__(kThreadsLp, 3) logprobs_kernel(const __grid_constant__ LogprobParams p) {
+__global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_constant__ LogprobParams p) {
     using E = Elem<DT>;
     using T = typename E::T;
     using C = Chunk<DT>;
@@ -168,50 +241,44 @@ __global__ void __launch_bounds__(kThreadsLp, 3) logprobs_kernel(const __grid_co
     const int chunks = (p.V + shift + N - 1) / N, share = (chunks + nb - 1) / nb;
     const int c0 = (int)rank * share, c1 = min(chunks, c0 + share);
 
-    Stat a{-INFINITY, 0.f, 0.f};
-    int at = c0 + tid;    // chunk of the first maximum
-    bool bad = false;
+    float given = NAN;  // the given token's logit
+    if (rank == 0 && tid == 0 && p.logp) {
+        const int id = p.ids[row];
+        if (id >= 0 && id < p.V) given = E::up(x[id]);
+    }
+    Running<DT> run;
+    run.at = c0 + tid;
     constexpr int kAhead = 4;  // loads in flight per thread
+    const int whole = min(c1, (p.V + shift) / N);  // chunks that do not reach past the row
+    int c = c0 + tid;
 #pragma unroll 1
-    for (int first = c0 + tid; first < c1; first += kAhead * kThreadsLp) {
+    for (; c + (kAhead - 1) * kThreadsLp < whole; c += kAhead * kThreadsLp) {
+        uint4 raw[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int v0 = N * (c + u * kThreadsLp) - shift;
+            raw[u] = u == 0 && v0 < 0 ? C::load(x, v0, p.V) : __ldg(reinterpret_cast<const uint4 *>(x + v0));
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) run.take(raw[u], c + u * kThreadsLp);
+    }
+#pragma unroll 1
+    for (; c < c1; c += kAhead * kThreadsLp) {
         uint4 raw[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            if (first + u * kThreadsLp < c1) raw[u] = C::load(x, N * (first + u * kThreadsLp) - shift, p.V);
+            if (c + u * kThreadsLp < c1) raw[u] = C::load(x, N * (c + u * kThreadsLp) - shift, p.V);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int c = first + u * kThreadsLp;
-            if (c >= c1) break;
-            float f[N];
-            C::unpack(raw[u], f);
-            float mx = f[0];
-#pragma unroll
-            for (int i = 1; i < N; ++i) mx = fmaxf(mx, f[i]);
-            if (mx > a.m) {
-                if (a.z != 0.f) {
-                    const float t = (a.m - mx) * kLog2e, g = ex2f(t);
-                    a.d = (a.d + t * a.z) * g;
-                    a.z *= g;
-                }
-                a.m = mx;
-                at = c;
-            }
-            if (a.m > -INFINITY) {
-                // A difference first: logits near the type's largest would overflow in base 2.  The weight
-                // of -inf is 0, and so is its term of d (0 times a clamped exponent); a NaN stays in z.
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float t = (f[i] - a.m) * kLog2e, e = ex2f(t);
-                    a.z += e;
-                    a.d = fmaf(e, fmaxf(t, -200.f), a.d);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) bad |= f[i] != f[i];
-            }
-        }
+        for (int u = 0; u < kAhead; ++u)
+            if (c + u * kThreadsLp < c1) run.take(raw[u], c + u * kThreadsLp);
     }
-    bad |= a.m == INFINITY || a.z != a.z;
+    Stat a;
+    {
+        const float2 z = unpack2(run.z), d = unpack2(run.d);
+        a = Stat{run.m, z.x + z.y, d.x + d.y};
+    }
+    const int at = run.at;
+    const bool bad = run.bad || a.m == INFINITY || a.z != a.z;
     const float own_m = a.m;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -222,61 +289,55 @@ __global__ void __launch_bounds__(kThreadsLp, 3) logprobs_kernel(const __grid_co
         a = join(a, b);
     }
     if (lane == 0) s.warp[warp] = a;
+    const bool any = c0 + tid < c1;
+    const uint32_t val = any ? order32(own_m) : 0;
+    {
+        const uint32_t lo = __reduce_min_sync(0xffffffffu, val), hi = __reduce_max_sync(0xffffffffu, val);
+        if (lane == 0) {
+            s.lo[warp] = lo;
+            s.hi[warp] = hi;
+        }
+    }
     if (tid == 0) s.n_cand = s.n_slices = 0;
     const bool block_bad = __syncthreads_or(bad);
 
     if (p.k > 0 && !block_bad) {
-        // Lower and upper end of the keys that this thread's maximum may have.
-        const bool any = c0 + tid < c1;
-        const uint64_t hi_key = any ? order64(own_m, max(N * at - shift, 0)) : 0;
-        uint64_t key = any ? order64(own_m, N * at - shift + N - 1) : 0;
-        // sort the warp's 32, largest first
-#pragma unroll
-        for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-            for (int o = size >> 1; o; o >>= 1) {
-                const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
-                const bool down = (lane & size) == 0 || size == 32, first = (lane & o) == 0;
-                key = (first == down) ? max(key, other) : min(key, other);
+        // Upper and lower end of the keys that this thread's maximum may have.
+        const uint64_t hi_key = any ? (uint64_t)val << 32 | (uint32_t)~max(N * at - shift, 0) : 0;
+        const uint64_t key = any ? (uint64_t)val << 32 | (uint32_t)~(N * at - shift + N - 1) : 0;
+        uint32_t lo32 = s.lo[lane & (kWarpsLp - 1)], hi32 = s.hi[lane & (kWarpsLp - 1)];
+        lo32 = __reduce_min_sync(0xffffffffu, lo32);
+        hi32 = __reduce_max_sync(0xffffffffu, hi32);
+        // at least k keys reach lo (all of them at first), fewer reach hi
+        uint64_t tau = (uint64_t)lo32 << 32, hi = ((uint64_t)hi32 << 32) + 0xffffffffull;
+        int reach = kThreadsLp;
+        while (reach > 2 * p.k && hi - tau > 1) {
+            const uint64_t mid = tau + (hi - tau) / 2;
+            const int n = __syncthreads_count(key >= mid);
+            if (n >= p.k) {
+                tau = mid;
+                reach = n;
+            } else {
+                hi = mid;
             }
-        s.key[tid] = key;
-        __syncthreads();
-        // rank among all: position here plus, in every other warp's list, how many are larger
-        // (equal keys, of threads without elements, by the warp's number)
-        int rank_of = lane;
-#pragma unroll 4
-        for (int w = 0; w < kWarpsLp; ++w) {
-            if (w == warp) continue;
-            int lo = 0;
-#pragma unroll
-            for (int step = 16; step; step >>= 1) {
-                const uint64_t v = s.key[32 * w + lo + step - 1];
-                if (v > key || (v == key && w < warp)) lo += step;
-            }
-            const uint64_t v = s.key[32 * w + min(lo, 31)];
-            if (lo < 32 && (v > key || (v == key && w < warp))) ++lo;
-            rank_of += lo;
         }
-        if (rank_of == p.k - 1) s.tau = key;
-        __syncthreads();
-        const uint64_t tau = s.tau;
         if (any && hi_key >= tau) s.slices[atomicAdd(&s.n_slices, 1)] = tid;
         __syncthreads();
-        // a warp per such thread reads its chunks again
-        for (int i = warp; i < s.n_slices; i += kWarpsLp) {
-            const int t = s.slices[i];
-            for (int c = c0 + t + lane * kThreadsLp; c < c1; c += 32 * kThreadsLp) {
-                float f[N];
-                C::unpack(C::load(x, N * c - shift, p.V), f);
+        // their chunks, dealt out over the block
+        const int per = (c1 - c0 + kThreadsLp - 1) / kThreadsLp, items = s.n_slices * per;
+#pragma unroll 1
+        for (int i = tid; i < items; i += kThreadsLp) {
+            const int slice = i / per, c = c0 + s.slices[slice] + (i - slice * per) * kThreadsLp;
+            if (c >= c1) continue;
+            float f[N];
+            C::unpack(C::load(x, N * c - shift, p.V), f);
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const int v = N * c - shift + e;
-                    if (v < 0 || v >= p.V) continue;
-                    const uint64_t kk = order64(f[e], v);
-                    if (kk >= tau) {
-                        const int n = atomicAdd(&s.n_cand, 1);
-                        if (n < kCandidates) s.cand[n] = kk;
-                    }
+            for (int e = 0; e < N; ++e) {
+                const int v = N * c - shift + e;
+                const uint64_t kk = order64(f[e], v);
+                if (kk >= tau && v >= 0 && v < p.V) {
+                    const int n = atomicAdd(&s.n_cand, 1);
+                    if (n < kCandidates) s.cand[n] = kk;
                 }
             }
         }
@@ -291,7 +352,8 @@ __global__ void __launch_bounds__(kThreadsLp, 3) logprobs_kernel(const __grid_co
         for (int i = tid; i < n; i += kThreadsLp) {
             const uint64_t kk = s.cand[i];
             int r = 0;
-            for (int j = 0; j < n && r < p.k; ++j) r += s.cand[j] > kk;
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) r += s.cand[j] > kk;
             // (a pass over too short a stretch leaves zeros)
             if (r < p.k && kk) cluster_st(cluster_addr(&s.top[rank][r], 0), kk);
         }
@@ -335,10 +397,7 @@ __global__ void __launch_bounds__(kThreadsLp, 3) logprobs_kernel(const __grid_co
     const bool none = !slow && a.m == -INFINITY;
     const float log_z = slow ? (nan ? NAN : INFINITY) : none ? 0.f : a.m + logf(a.z);
     if (tid == 0) {
-        if (p.logp) {
-            const int id = p.ids[row];
-            p.logp[row] = id >= 0 && id < p.V ? E::up(x[id]) - log_z : NAN;
-        }
+        if (p.logp) p.logp[row] = given - log_z;
         if (p.entropy) p.entropy[row] = slow ? NAN : none ? 0.f : fmaxf(logf(a.z) - kLn2 * a.d / a.z, 0.f);
     }
     if (p.k > 0) {
@@ -351,12 +410,13 @@ __global__ void __launch_bounds__(kThreadsLp, 3) logprobs_kernel(const __grid_co
             if (!slow && nb > 1) {
                 r = 0;
                 for (int b = 0; b < nb; ++b)
-                    for (int j = 0; j < p.k && s.top[b][j] > kk; ++j) ++r;
+#pragma unroll 8
+                    for (int j = 0; j < p.k; ++j) r += s.top[b][j] > kk;
             }
             if (r < p.k) {
                 const int v = (int)~(uint32_t)kk;
                 p.top_ids[(size_t)row * p.k + r] = v;
-                p.top_logp[(size_t)row * p.k + r] = E::up(x[v]) - log_z;
+                p.top_logp[(size_t)row * p.k + r] = value_of((uint32_t)(kk >> 32)) - log_z;
             }
         }
     }
@@ -391,7 +451,7 @@ int launch(const LogprobParams &p, cudaStream_t s) {
         attr[0].val.clusterDim.x = nb;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         c.attrs = attr;
-        c.numAttrs = 1;
+        c.numAttrs = nb > 1;
         const int st = record_launch(cudaLaunchKernelEx(&c, logprobs_kernel<DT>, q));
         if (st) return st;
     }
