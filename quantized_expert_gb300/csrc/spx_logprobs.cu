@@ -422,11 +422,15 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
     }
 }
 
-// Blocks per row: enough of them to give every SM work, at most a portable
-// cluster, and none with less than two chunks a thread.
+// Blocks per row: doubled while there are fewer than 256 of them (1.7 an SM),
+// to a portable cluster at most, and while each keeps 16 KB of the row; a block
+// costs some 5 us of its own.  Measured with 102400 logits a row, blocks 1, 2,
+// 4, 8 (us): 17 rows fp32 20.3, 13.1, 9.2, 8.3; 64 rows bf16 17.8, 12.0, 10.9,
+// 13.8; 152 rows 17.9, 14.4, 17.1, 23.8; 608 rows 38.3, 43.0, 52.6, 74.4; 17
+// rows of 32000 8.6, 8.2, 7.8, 9.0.
 int blocks_per_row(int N, int64_t bytes) {
     int nb = 1;
-    while (nb < kMaxCluster && (int64_t)N * nb < 4 * 152 && bytes / (2 * nb) >= 2 * 16 * kThreadsLp) nb *= 2;
+    while (nb < kMaxCluster && (int64_t)N * nb < 256 && bytes / (2 * nb) >= 16000) nb *= 2;
     return nb;
 }
 
