@@ -1068,53 +1068,6 @@ __global__ void __launch_bounds__(512, 2) latent_join_kernel(const __grid_consta
 }
 
 // -------------------------------------------------------------------- host --
-cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr, int cluster) {
-    cudaLaunchConfig_t c = {};
-    c.gridDim = grid;
-    c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    c.attrs = attr;
-    c.numAttrs = cluster > 1 ? 2 : 1;
-    return c;
-}
-
-template <auto kernel>
-int set_smem(size_t bytes) {
-    static thread_local int done_dev = -1;  // one per kernel
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return record_launch(e);
-    if (done_dev == dev) return SPX_OK;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return record_launch(e);
-    done_dev = dev;
-    return SPX_OK;
-}
-
-// A tensor map of `rank` dimensions of two-byte values, innermost 64 of them
-// (one swizzled row); strides in bytes of dimensions 1 on.
-bool map_rows64(CUtensorMap *m, int dt, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-                const uint32_t *box) {
-    const EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t d[4], st[3];
-    cuuint32_t b[4], es[4];
-    for (int i = 0; i < rank; ++i) {
-        d[i] = dims[i];
-        b[i] = box[i];
-        es[i] = 1;
-        if (i) st[i - 1] = strides[i - 1];
-    }
-    return fn(m, dt == SPX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
-              const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 bool attn_maps(const LatentParams &p, int dt, const void *q, AttnMaps *maps) {
     const uint64_t tok = (uint64_t)p.token_stride * 2, pieces = (uint64_t)(p.R + p.P) / 64;
     const uint64_t dims[4] = {64, (uint64_t)p.page_size, pieces, (uint64_t)p.num_pages};
@@ -1132,7 +1085,7 @@ int launch_attn(const LatentParams &p, const AttnMaps &maps, int blocks, cudaStr
     int st = set_smem<latent_attn_kernel<DT, NR>>(AttnGeo<NR>::kSmem);
     if (st) return st;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t c = config(dim3(blocks), AttnGeo<NR>::kThreads, AttnGeo<NR>::kSmem, s, attr, 1);
+    cudaLaunchConfig_t c = latent_config(dim3(blocks), AttnGeo<NR>::kThreads, AttnGeo<NR>::kSmem, s, attr, 1);
     return record_launch(cudaLaunchKernelEx(&c, latent_attn_kernel<DT, NR>, p, maps));
 }
 
@@ -1144,12 +1097,12 @@ template <int DT>
 int launch_q(const LatentParams &p, cudaStream_t s) {
     cudaLaunchAttribute attr[2];
     if (!p.w_uk) {
-        cudaLaunchConfig_t c = config(dim3(p.N), 128, 0, s, attr, 1);
+        cudaLaunchConfig_t c = latent_config(dim3(p.N), 128, 0, s, attr, 1);
         return record_launch(cudaLaunchKernelEx(&c, latent_pack_kernel, p));
     }
     const int mt = token_tiles(p.N);
     const size_t smem = (size_t)(16 * mt * (p.dn + 8) + p.dn * 72) * 2;
-    cudaLaunchConfig_t c = config(dim3(p.R / 64, p.heads, (p.N + 16 * mt - 1) / (16 * mt)), 128, smem, s, attr, 1);
+    cudaLaunchConfig_t c = latent_config(dim3(p.R / 64, p.heads, (p.N + 16 * mt - 1) / (16 * mt)), 128, smem, s, attr, 1);
     return record_launch(mt == 1 ? cudaLaunchKernelEx(&c, latent_q_kernel<DT, 1>, p)
                                  : cudaLaunchKernelEx(&c, latent_q_kernel<DT, 4>, p));
 }
@@ -1161,7 +1114,7 @@ int launch_out_mt(const LatentParams &p, cudaStream_t s) {
     if (st) return st;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t c =
-        config(dim3(p.R / 64, p.heads, (p.N + 16 * MT - 1) / (16 * MT)), 512, smem, s, attr, p.R / 64);
+        latent_config(dim3(p.R / 64, p.heads, (p.N + 16 * MT - 1) / (16 * MT)), 512, smem, s, attr, p.R / 64);
     return record_launch(cudaLaunchKernelEx(&c, latent_out_kernel<DT, MT>, p));
 }
 
@@ -1183,7 +1136,7 @@ int launch_absorbed(LatentParams &p, int dtype, bool packed, cudaStream_t s) {
     if (st) return st;
     if (p.w_uv) return token_tiles(p.N) == 1 ? launch_out_mt<DT, 1>(p, s) : launch_out_mt<DT, 4>(p, s);
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t c = config(dim3(p.N * p.heads), 512, 0, s, attr, 1);
+    cudaLaunchConfig_t c = latent_config(dim3(p.N * p.heads), 512, 0, s, attr, 1);
     return record_launch(cudaLaunchKernelEx(&c, latent_join_kernel<DT>, p));
 }
 
@@ -1194,6 +1147,7 @@ int rows_per_unit(int max_q, int heads) {
     return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
+constexpr int kExpandFrom = 200;
 constexpr size_t kHdr = 256;
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // The workspace of the absorbed form.
@@ -1212,6 +1166,27 @@ AbsorbedLayout absorbed_layout(int B, int N, int max_q, int heads, int R, int P,
     l.bytes = l.o_lat + (weights ? up256((size_t)N * heads * R * 4) : 0);
     return l;
 }
+// The workspace of the expanded form.
+struct ExpandedLayout {
+    size_t k, v, rope, bytes;
+    int rows;
+};
+ExpandedLayout expanded_layout(int B, int max_len, int heads) {
+    ExpandedLayout l;
+    l.rows = max_len <= 128 ? 128 : (int)(((long long)max_len + 127) / 128 * 128);
+    const size_t one = (size_t)heads * B * l.rows * 256;
+    l.k = kHdr;
+    l.v = l.k + one;
+    l.rope = l.v + one;
+    l.bytes = l.rope + (size_t)B * l.rows * 128;
+    return l;
+}
+// The form that a call takes.
+int latent_form(int form, int max_q, int dn, int dv) {
+    if (form != SPX_LATENT_AUTO) return form;
+    return dn == 128 && dv == 128 && max_q >= kExpandFrom ? SPX_LATENT_EXPANDED : SPX_LATENT_ABSORBED;
+}
+
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
@@ -1237,8 +1212,11 @@ extern "C" size_t spx_latent_workspace_size(int B, int N, int max_q, int max_len
                                             int dv, int form) {
     if (B < 1 || N < 0 || max_q < 0 || max_len < 0 || heads < 1 || form < 0 || form > 2) return 0;
     if (R < 128 || R > 512 || R % 128 || P != 64 || heads > 1024 || B > 65535) return 0;
+    // (token, head) rows and cached rows are counted in 31 bits
+    if ((long long)N * heads > 1 << 30 || (long long)max_q * heads > 1 << 30 || (long long)B * max_len > 1 << 30) return 0;
     if ((dn != 0) != (dv != 0) || (dn && dn != 64 && dn != 128) || (dv && dv != 64 && dv != 128)) return 0;
-    if (form == SPX_LATENT_EXPANDED) return 0;
+    const int used = latent_form(form, max_q, dn, dv);
+    if (used == SPX_LATENT_EXPANDED) return dn == 128 && dv == 128 ? expanded_layout(B, max_len, heads).bytes : 0;
     return absorbed_layout(B, N, max_q, heads, R, P, dn != 0).bytes;
 }
 
@@ -1295,18 +1273,26 @@ extern "C" int spx_latent_attention(const spx_latent_args *a, spx_stream_t strea
     uint8_t *ws = static_cast<uint8_t *>(a->ws);
     p.hdr = reinterpret_cast<WsHeader *>(ws);
     p.budget = a->wait_budget_ns ? a->wait_budget_ns : 2000000000ull;
+    p.box_tokens = c.page_size % 64 == 0 ? 64 : c.page_size % 32 == 0 ? 32 : 16;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (latent_form(a->form, a->max_q, a->dn, a->dv) == SPX_LATENT_EXPANDED) {
+        const ExpandedLayout l = expanded_layout(c.B, a->max_len, a->heads);
+        p.k_x = reinterpret_cast<uint16_t *>(ws + l.k);
+        p.v_x = reinterpret_cast<uint16_t *>(ws + l.v);
+        p.rope_x = reinterpret_cast<uint16_t *>(ws + l.rope);
+        p.kv_rows = l.rows;
+        return launch_expanded(p, c.dtype, s);
+    }
     const AbsorbedLayout l = absorbed_layout(c.B, a->N, a->max_q, a->heads, c.R, c.P, p.w_uk != nullptr);
     p.nr = rows_per_unit(a->max_q, a->heads);
     p.nr_log2 = p.nr == 16 ? 4 : p.nr == 32 ? 5 : 6;
     p.groups = (int)(((long long)a->max_q * a->heads + p.nr - 1) / p.nr);
-    p.box_tokens = c.page_size % 64 == 0 ? 64 : c.page_size % 32 == 0 ? 32 : 16;
     p.units = reinterpret_cast<int4 *>(ws + l.units);
     p.ml = reinterpret_cast<float2 *>(ws + l.ml);
     p.part = reinterpret_cast<float *>(ws + l.part);
     p.q_lat = reinterpret_cast<uint16_t *>(ws + l.q_lat);
     p.o_lat = reinterpret_cast<float *>(ws + l.o_lat);
     const bool packed = a->q_stride == qw || a->N == 1;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return c.dtype == SPX_F16 ? launch_absorbed<SPX_F16>(p, c.dtype, packed, s)
                               : launch_absorbed<SPX_BF16>(p, c.dtype, packed, s);
 }

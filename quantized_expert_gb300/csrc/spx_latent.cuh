@@ -84,6 +84,9 @@ struct LatentParams {
     // geometry of the attention launch
     int nr, nr_log2, groups, box_tokens;
     int chained;      // a launch of this call precedes the attention launch
+    // expanded form: keys, values [heads][B][kv_rows][128], rotated parts [B][kv_rows][64]
+    uint16_t *k_x, *v_x, *rope_x;
+    int kv_rows, head_group;  // rows of a request (whole tiles); heads per block of the expand launch
 };
 
 // A request's query rows and cached length, cut to the call's bounds, so that
@@ -103,5 +106,41 @@ __device__ __forceinline__ LatentReq latent_req(const LatentParams &p, int b) {
 __device__ __forceinline__ int latent_limit(const LatentParams &p, const LatentReq &r, int t) {
     return p.causal ? max(r.len - r.T + t + 1, 0) : r.len;
 }
+
+// -------------------------------------------------------------------- host --
+inline cudaLaunchConfig_t latent_config(dim3 grid, int threads, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr,
+                                        int cluster) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    c.attrs = attr;
+    c.numAttrs = cluster > 1 ? 2 : 1;
+    return c;
+}
+
+// The most dynamic shared memory that a kernel's launches ask for, set once per
+// device and thread.
+template <auto kernel>
+int set_smem(size_t bytes) {
+    static thread_local int done_dev = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return record_launch(e);
+    if (done_dev == dev) return SPX_OK;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return record_launch(e);
+    done_dev = dev;
+    return SPX_OK;
+}
+
+// spx_latent_prompt.cu: the expanded form's launches.
+int launch_expanded(LatentParams &p, int dt, cudaStream_t s);
 
 }  // namespace spx

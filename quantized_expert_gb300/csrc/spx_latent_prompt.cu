@@ -1,0 +1,574 @@
+// spx_latent_prompt.cu -- attention over the paged latent cache, expanded form.
+//
+// A prompt has so many query rows that every head's keys and values are worth
+// writing out: a query-key pair then costs dn + P + dv = 320 products instead
+// of R + P + R = 1088.  Two launches:
+//
+//   expand launch     k[h] = W_uk[h] c, v[h] = W_uv[h] c for every cached token
+//                     of the call's requests, rounded to the type, and the
+//                     rotated parts side by side;
+//   attention launch  softmax(scale (q_nope . k + q_rope . r)) v per head, a
+//                     running maximum and sum per row.
+//
+// The second is a programmatic dependent of the first.
+#include <math.h>
+#include <string.h>
+
+#include "spx_latent.cuh"
+#include "spx_tcgen05.cuh"
+
+namespace spx {
+
+namespace {
+
+constexpr int kPTile = 128;                 // tokens of a tile: rows of one product
+constexpr int kPiece = kPTile * 128;        // 128 rows x 64 values, 16 KB
+
+struct PromptMaps {
+    CUtensorMap cache;       // [page][piece][token][64], boxes of 1 piece x box_tokens
+    CUtensorMap w_uk, w_uv;  // [piece][head * 128 + row][64], boxes of 1 piece x 128 rows
+    CUtensorMap q;           // [head][piece][token][64], boxes of 3 pieces x 128 tokens
+    CUtensorMap k, v;        // [head][piece][row][64]: k in boxes of 1 piece x 128 rows, v of 2 x 64
+    CUtensorMap rope;        // [row][64], boxes of 128 rows
+};
+
+// ----------------------------------------------------------- expand launch --
+// Block (token tile, group of heads, request): the tile's latent vectors stay
+// in shared memory (A, R / 64 pieces of 128 tokens) while the heads' weights
+// stream past in stages of 64 latent columns, W_uk[h] and W_uv[h] as the 256
+// rows of B: D[128 tokens x 256] = keys and values of one head, in one of two
+// accumulators.  Bound by the tensor cores (256 columns a product) and by L2,
+// which reads the weights once per token tile.
+constexpr int kExStages = 3;
+constexpr int kExStage = 2 * kPiece;
+constexpr int kExThreads = 256;  // copies of W, products, 2 warps' copies of A, 4 epilogue warps
+struct ExMisc {
+    uint64_t afull, wfull[kExStages], wempty[kExStages], dfull[2], dempty[2], fin;
+    uint32_t tmem;
+    int abort;
+};
+constexpr size_t kExSmem = 8 * (size_t)kPiece + kExStages * (size_t)kExStage + 1024;
+static_assert(kExSmem <= (size_t)kSmemLimit && sizeof(ExMisc) <= 1024, "shared memory of one block");
+
+// 32 lanes x 32 consecutive columns of tensor memory (no wait).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kExThreads, 1)
+    latent_expand_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ PromptMaps maps) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *as = smem, *ws = as + 8 * kPiece;
+    ExMisc &m = *reinterpret_cast<ExMisc *>(ws + kExStages * kExStage);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.z, t0 = kPTile * blockIdx.x, h0 = p.head_group * blockIdx.y;
+    const int nh = min(p.head_group, p.heads - h0), nc = p.R / 64;
+    griddep_wait();
+    griddep_launch_dependents();
+    const LatentReq rq = latent_req(p, b);
+    if (t0 >= rq.len || rq.T == 0) return;
+    if (threadIdx.x == 0) {
+        mbar_init(&m.afull, 2);
+        for (int s = 0; s < kExStages; ++s) {
+            mbar_init(&m.wfull[s], 1);
+            mbar_init(&m.wempty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&m.dfull[s], 1);
+            mbar_init(&m.dempty[s], 4);
+        }
+        mbar_init(&m.fin, 1);
+        m.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&m.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m.tmem;
+    const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_LATENT};
+
+    if (warp == 2 || warp == 3) {
+        // ---- the latent vectors of 64 tokens
+        const uint64_t pol = policy_evict_normal();
+        const int bt = p.box_tokens, nb = 64 / bt, half = warp - 2;
+        const int pos = t0 + 64 * half + bt * (lane & 3), pi = p.by_page(pos), my_at = pos - pi * p.page_size;
+        int my_page = pos < rq.len ? __ldg(p.table + (size_t)b * p.max_pages + pi) : p.num_pages;
+        if (my_page < 0 || my_page >= p.num_pages) my_page = p.num_pages;
+        if (elect_one()) mbar_arrive_expect_tx(&m.afull, (uint32_t)nc * (kPiece / 2));
+        for (int j = 0; j < nb; ++j) {
+            const int at = __shfl_sync(0xffffffffu, my_at, j), page = __shfl_sync(0xffffffffu, my_page, j);
+            if (elect_one())
+                for (int c = 0; c < nc; ++c)
+                    tma_load_4d(as + c * kPiece + half * (kPiece / 2) + j * bt * 128, &maps.cache, 0, at, c, page,
+                                &m.afull, pol);
+            __syncwarp();
+        }
+        // ---- their rotated parts (once for all heads), 8 values a lane
+        if (h0 == 0)
+            for (int i = lane; i < 64 * 8; i += 32) {
+                const int t = t0 + 64 * half + (i >> 3), pg_i = p.by_page(t);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (t < rq.len) {
+                    const int pg = __ldg(p.table + (size_t)b * p.max_pages + pg_i);
+                    if (pg >= 0 && pg < p.num_pages)
+                        v = *reinterpret_cast<const uint4 *>(p.cache + (int64_t)pg * p.page_stride +
+                                                             (int64_t)(t - pg_i * p.page_size) * p.token_stride + p.R +
+                                                             8 * (i & 7));
+                }
+                *reinterpret_cast<uint4 *>(p.rope_x + ((size_t)b * p.kv_rows + t) * 64 + 8 * (i & 7)) = v;
+            }
+    } else if (warp == 0) {
+        // ---- the weights
+        const uint64_t pol = policy_evict_last();
+        uint32_t it = 0;
+        bool ok = true;
+        for (int h = h0; ok && h < h0 + nh; ++h)
+            for (int c = 0; c < nc; ++c, ++it) {
+                const uint32_t s = it % kExStages;
+                if (!(ok = ctl_wait(&m.wempty[s], ((it / kExStages) & 1) ^ 1, ctl))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&m.wfull[s], kExStage);
+                    tma_load_3d(ws + s * kExStage, &maps.w_uk, 0, 128 * h, c, &m.wfull[s], pol);
+                    tma_load_3d(ws + s * kExStage + kPiece, &maps.w_uv, 0, 128 * h, c, &m.wfull[s], pol);
+                }
+                __syncwarp();
+            }
+        if (!ok) ctl_settle(100000000ull);
+    } else if (warp == 1) {
+        // ---- products
+        const uint32_t id = idesc_f16_f32(128, 256) | (DT == SPX_BF16 ? kIdescBf16 : 0u);
+        const uint64_t ad = sw128_desc(smem_u32(as)), wd = sw128_desc(smem_u32(ws));
+        uint32_t it = 0;
+        bool ok = ctl_wait(&m.afull, 0, ctl);
+        for (int i = 0; ok && i < nh; ++i) {
+            const uint32_t d = tmem + (i & 1) * 256;
+            if (!(ok = ctl_wait(&m.dempty[i & 1], ((i >> 1) & 1) ^ 1, ctl))) break;
+            for (int c = 0; c < nc; ++c, ++it) {
+                const uint32_t s = it % kExStages;
+                if (!(ok = ctl_wait(&m.wfull[s], (it / kExStages) & 1, ctl))) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        umma_f16(d, ad + c * (kPiece / 16) + 2 * j, wd + s * (kExStage / 16) + 2 * j, id, (c | j) != 0);
+                    umma_commit(&m.wempty[s]);
+                    if (c == nc - 1) umma_commit(&m.dfull[i & 1]);
+                }
+                __syncwarp();
+            }
+        }
+        if (m.abort) {
+            if (elect_one()) umma_commit(&m.fin);
+            ctl_drain(&m.fin, 0, 100000000ull);
+        }
+    } else {
+        // ---- epilogue: a token a lane, its keys, then its values
+        const int q = warp & 3, t = t0 + 32 * q + lane;
+        const bool live = t < rq.len;
+        for (int i = 0; i < nh; ++i) {
+            ctl_wait(&m.dfull[i & 1], (i >> 1) & 1, ctl);
+            tc_fence_after();
+            const size_t row = (size_t)(h0 + i) * p.B * p.kv_rows + (size_t)b * p.kv_rows + t;
+#pragma unroll 1
+            for (int x = 0; x < 256; x += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (i & 1) * 256 + x, r);
+                tmem_wait_ld();
+                // Past the length: zeros.  A value that is not finite: 0, as its weight 0 elsewhere times it would
+                // not be 0; its key carries it to the rows that see it.
+                uint32_t o[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float u = __uint_as_float(r[2 * k]), v = __uint_as_float(r[2 * k + 1]);
+                    if (!live || (x >= 128 && !(fabsf(u) < INFINITY))) u = 0.f;
+                    if (!live || (x >= 128 && !(fabsf(v) < INFINITY))) v = 0.f;
+                    o[k] = Elem<DT>::down2(u, v);
+                }
+                uint4 *dst = reinterpret_cast<uint4 *>((x < 128 ? p.k_x : p.v_x) + row * 128 + (x & 127));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.dempty[i & 1]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// -------------------------------------------------------- attention launch --
+// Block (two adjacent tiles of 128 query rows of a request, head).  Per tile X
+// and key tile j:  S_X = Q_X K_j^T (128 x 128, 192 deep), softmax in registers
+// (a row a thread), P_X back into S_X's tensor memory as the A operand of
+// O_X += P_X V_j.  The two tiles share every key and value tile and take
+// turns: while one's softmax runs, the other's products do (order PV_0, S_0,
+// PV_1, S_1, so that S_X(j + 1) stands right behind PV_X(j)).  Tensor memory:
+// S_0, S_1, O_0, O_1, 128 columns each.  Shared memory: Q 96 KB, keys in a
+// ring of 5 pieces (128 tokens x 64), values in one of 3 halves (64 tokens x
+// 128).
+//
+// Per key tile 2 (768 + 512) cycles of products against 2 x 16384 exponentials;
+// the keys and values of a tile, 80 KB, come once per 256 rows (32 bytes a
+// cycle and SM).
+constexpr int kFaThreads = 384;  // copies, products, two idle; 4 softmax warps per tile
+constexpr int kKRing = 5, kVRing = 3;
+struct FaMisc {
+    uint64_t qfull[2], kfull[kKRing], kempty[kKRing], vfull[kVRing], vempty[kVRing];
+    uint64_t sfull[2], pfull[2], odone[2], fin;
+    uint32_t tmem;
+    int abort;
+};
+constexpr size_t kFaSmem = 6 * (size_t)kPiece + kKRing * (size_t)kPiece + kVRing * (size_t)kPiece + 1024;
+static_assert(kFaSmem <= (size_t)kSmemLimit && sizeof(FaMisc) <= 1024, "shared memory of one block");
+constexpr float kFaSlack = 8.f, kFaShift = 5.f;  // as in the absorbed form
+
+// D (tensor memory) (+)= A (tensor memory) . B (shared, descriptor)
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+template <int N>
+struct Ring {
+    uint32_t i = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kFaThreads, 1)
+    latent_prompt_kernel(const __grid_constant__ LatentParams p, const __grid_constant__ PromptMaps maps) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *qs = smem, *ks = qs + 6 * kPiece, *vs = ks + kKRing * kPiece;
+    FaMisc &m = *reinterpret_cast<FaMisc *>(vs + kVRing * kPiece);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the longest rows first, as their blocks take longest
+    const int b = blockIdx.y, h = blockIdx.x % p.heads, qt = (int)(gridDim.x / p.heads) - 1 - (int)(blockIdx.x / p.heads);
+    const LatentReq rq = latent_req(p, b);
+    const int r0 = 2 * kPTile * qt;
+    if (r0 >= rq.T) {
+        griddep_wait();
+        return;
+    }
+    // key tiles of each query tile (0: no rows, or none that sees anything)
+    int n[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int last = min(r0 + kPTile * (x + 1), rq.T) - 1;
+        n[x] = last < r0 + kPTile * x ? 0 : (latent_limit(p, rq, last) + kPTile - 1) / kPTile;
+    }
+    const int most = max(n[0], n[1]);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kKRing; ++i) {
+            mbar_init(&m.kfull[i], 1);
+            mbar_init(&m.kempty[i], 1);
+        }
+        for (int i = 0; i < kVRing; ++i) {
+            mbar_init(&m.vfull[i], 1);
+            mbar_init(&m.vempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&m.qfull[i], 1);
+            mbar_init(&m.sfull[i], 1);
+            mbar_init(&m.pfull[i], 4);
+            mbar_init(&m.odone[i], 1);
+        }
+        mbar_init(&m.fin, 1);
+        m.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&m.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m.tmem;
+    const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_LATENT};
+
+    if (warp == 0) {
+        // ---- copies
+        const uint64_t pol = policy_evict_normal();
+        for (int x = 0; x < 2; ++x)
+            if (n[x] && elect_one()) {
+                mbar_arrive_expect_tx(&m.qfull[x], 3 * kPiece);
+                tma_load_4d(qs + 3 * x * kPiece, &maps.q, 0, rq.row0 + r0 + kPTile * x, 0, h, &m.qfull[x], pol);
+            }
+        __syncwarp();
+        griddep_wait();
+        Ring<kKRing> kr;
+        Ring<kVRing> vr;
+        bool ok = true;
+        for (int j = 0; ok && j < most; ++j) {
+            const int row = b * p.kv_rows + kPTile * j;
+            for (int c = 0; c < 3; ++c, kr.next()) {
+                if (!(ok = ctl_wait(&m.kempty[kr.i], kr.phase ^ 1, ctl))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&m.kfull[kr.i], kPiece);
+                    if (c < 2)
+                        tma_load_4d(ks + kr.i * kPiece, &maps.k, 0, row, c, h, &m.kfull[kr.i], pol);
+                    else
+                        tma_load_2d(ks + kr.i * kPiece, &maps.rope, 0, row, &m.kfull[kr.i], pol);
+                }
+                __syncwarp();
+            }
+            for (int c = 0; ok && c < 2; ++c, vr.next()) {
+                if (!(ok = ctl_wait(&m.vempty[vr.i], vr.phase ^ 1, ctl))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&m.vfull[vr.i], kPiece);
+                    tma_load_4d(vs + vr.i * kPiece, &maps.v, 0, row + 64 * c, 0, h, &m.vfull[vr.i], pol);
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) ctl_settle(100000000ull);
+    } else if (warp == 1) {
+        // ---- products
+        const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
+        const uint32_t id_s = idesc_f16_f32(128, 128) | fmt, id_o = idesc_f16_f32(128, 128) | fmt | kIdescBMn;
+        const uint64_t qd = sw128_desc(smem_u32(qs)), kd = sw128_desc(smem_u32(ks));
+        const uint64_t vd = sw128_desc_mn(smem_u32(vs), kPiece / 2);
+        Ring<kKRing> kr;
+        Ring<kVRing> vr;
+        bool ok = true;
+        // S_x(j); `done`: its keys are not needed again
+        auto product_s = [&](int x, int j, bool done) {
+            if (j == 0) ok = ok && ctl_wait(&m.qfull[x], 0, ctl);
+            Ring<kKRing> k = kr;
+            for (int c = 0; ok && c < 3; ++c, k.next()) ok = ctl_wait(&m.kfull[k.i], k.phase, ctl);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+                k = kr;
+#pragma unroll 1
+                for (int c = 0; c < 3; ++c, k.next()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        umma_f16(tmem + 128 * x, qd + (3 * x + c) * (kPiece / 16) + 2 * i, kd + k.i * (kPiece / 16) + 2 * i,
+                                 id_s, (c | i) != 0);
+                    if (done) umma_commit(&m.kempty[k.i]);
+                }
+                umma_commit(&m.sfull[x]);
+            }
+            __syncwarp();
+            if (done)
+                for (int c = 0; c < 3; ++c) kr.next();
+        };
+        auto product_o = [&](int x, int j, bool done) {
+            Ring<kVRing> v = vr;
+            for (int c = 0; ok && c < 2; ++c, v.next()) ok = ctl_wait(&m.vfull[v.i], v.phase, ctl);
+            ok = ok && ctl_wait(&m.pfull[x], j & 1, ctl);
+            if (!ok) return;
+            tc_fence_after();
+            if (elect_one()) {
+                v = vr;
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c, v.next()) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        umma_f16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 32 * c + 8 * i,
+                                    vd + v.i * (kPiece / 16) + 128 * i, id_o, (j | c | i) != 0);
+                    if (done) umma_commit(&m.vempty[v.i]);
+                }
+                if (j == n[x] - 1) umma_commit(&m.odone[x]);
+            }
+            __syncwarp();
+            if (done)
+                for (int c = 0; c < 2; ++c) vr.next();
+        };
+        if (n[0]) product_s(0, 0, !n[1]);
+        if (n[1]) product_s(1, 0, true);
+        for (int j = 0; ok && j < most; ++j) {
+            if (j < n[0]) product_o(0, j, j >= n[1]);
+            if (j + 1 < n[0]) product_s(0, j + 1, j + 1 >= n[1]);
+            if (j < n[1]) product_o(1, j, true);
+            if (j + 1 < n[1]) product_s(1, j + 1, true);
+        }
+        if (m.abort) {
+            if (elect_one()) umma_commit(&m.fin);
+            ctl_drain(&m.fin, 0, 100000000ull);
+        }
+    } else if (warp >= 4) {
+        // ---- softmax and results: a row a thread
+        const int x = (warp - 4) >> 2, q = warp & 3, t = r0 + kPTile * x + 32 * q + lane;
+        const uint32_t quarter = (uint32_t)(32 * q) << 16;
+        const uint32_t st = tmem + quarter + 128 * x, ot = tmem + quarter + 256 + 128 * x;
+        const bool live = t < rq.T;
+        const int lim = live ? latent_limit(p, rq, t) : 0;
+        const int lim_lo = latent_limit(p, rq, r0 + kPTile * x + 32 * q);  // the warp's first row sees least
+        float mr = -INFINITY, l = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < n[x]; ++j) {
+            ctl_wait(&m.sfull[x], j & 1, ctl);
+            tc_fence_after();
+            const int p0 = kPTile * j;
+            const bool masked = p0 + kPTile > lim_lo || !live;
+            const int left = lim - p0;  // columns of this tile that the row sees
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(st + c, r);
+                tmem_wait_ld();
+                if (__any_sync(0xffffffffu, masked)) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (c + k < left) mx = fmaxf(mx, __uint_as_float(r[k]) * p.scale_log2);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r[k]) * p.scale_log2);
+                }
+            }
+            const bool rise = mx > mr + kFaSlack;
+            if (__any_sync(0xffffffffu, rise)) {
+                const float mn = rise ? mx : mr, f = mn == mr ? 1.f : ex2(mr - mn);
+                mr = mn;
+                l *= f;
+                if (j > 0) {
+                    // (O_x(j - 1) is done: S_x(j) came behind it)
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(ot + c, o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st16(ot + c, o);
+                    }
+                }
+            }
+            const float ref = mr == -INFINITY ? 0.f : mr - kFaShift;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(st + c, r);
+                tmem_wait_ld();
+                const bool cut = __any_sync(0xffffffffu, masked);
+                uint32_t o[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    float u = ex2(fmaf(__uint_as_float(r[k]), p.scale_log2, -ref));
+                    float v = ex2(fmaf(__uint_as_float(r[k + 1]), p.scale_log2, -ref));
+                    if (cut) {
+                        if (c + k >= left) u = 0.f;
+                        if (c + k + 1 >= left) v = 0.f;
+                    }
+                    l += u + v;
+                    o[k / 2] = Elem<DT>::down2(u, v);
+                }
+                tmem_st16(st + c / 2, o);  // over columns read before
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.pfull[x]);
+        }
+        if (live) {
+            if (p.lse)
+                p.lse[(size_t)(rq.row0 + t) * p.heads + h] = n[x] ? (mr + log2f(l) - kFaShift) * 0.6931471805599453f : -INFINITY;
+        }
+        if (n[x]) ctl_wait(&m.odone[x], 0, ctl);
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        typename Elem<DT>::T *out = reinterpret_cast<typename Elem<DT>::T *>(p.out) +
+                                    (int64_t)(rq.row0 + (live ? t : r0)) * p.out_stride + (size_t)h * 128;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 16) {
+            uint32_t o[16];
+            if (n[x]) {
+                tmem_ld16(ot + c, o);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = 0u;
+            }
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                w[k] = Elem<DT>::down2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+            if (live) {
+                uint4 *d = reinterpret_cast<uint4 *>(out + c);
+                d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// -------------------------------------------------------------------- host --
+bool prompt_maps(const LatentParams &p, int dt, PromptMaps *m) {
+    memset(m, 0, sizeof(*m));
+    const uint64_t tok = (uint64_t)p.token_stride * 2, rows = (uint64_t)p.B * p.kv_rows;
+    const uint64_t cd[4] = {64, (uint64_t)p.page_size, (uint64_t)(p.R + p.P) / 64, (uint64_t)p.num_pages};
+    const uint64_t cs[3] = {tok, 128, p.num_pages > 1 ? (uint64_t)p.page_stride * 2 : tok * p.page_size};
+    const uint32_t cb[4] = {64, (uint32_t)p.box_tokens, 1, 1};
+    const uint64_t wd[3] = {64, (uint64_t)p.heads * 128, (uint64_t)p.R / 64}, wst[2] = {(uint64_t)p.R * 2, 128};
+    const uint32_t wb[3] = {64, 128, 1};
+    const uint64_t qd[4] = {64, (uint64_t)p.N, 3, (uint64_t)p.heads}, qst[3] = {(uint64_t)p.q_stride * 2, 128, 192 * 2};
+    const uint32_t qb[4] = {64, 128, 3, 1};
+    const uint64_t kd[4] = {64, rows, 2, (uint64_t)p.heads}, kst[3] = {256, 128, rows * 256};
+    const uint32_t kb[4] = {64, 128, 1, 1}, vb[4] = {64, 64, 2, 1};
+    const uint64_t rd[2] = {64, rows}, rst[1] = {128};
+    const uint32_t rb[2] = {64, 128};
+    return map_rows64(&m->cache, dt, p.cache, 4, cd, cs, cb) && map_rows64(&m->w_uk, dt, p.w_uk, 3, wd, wst, wb) &&
+           map_rows64(&m->w_uv, dt, p.w_uv, 3, wd, wst, wb) && map_rows64(&m->q, dt, p.q, 4, qd, qst, qb) &&
+           map_rows64(&m->k, dt, p.k_x, 4, kd, kst, kb) && map_rows64(&m->v, dt, p.v_x, 4, kd, kst, vb) &&
+           map_rows64(&m->rope, dt, p.rope_x, 2, rd, rst, rb);
+}
+
+template <int DT>
+int launch_expanded_dt(const LatentParams &p, int dt, cudaStream_t s) {
+    PromptMaps maps;
+    if (!prompt_maps(p, dt, &maps)) return SPX_ERR_UNSUPPORTED;
+    int st = set_smem<latent_expand_kernel<DT>>(kExSmem);
+    if (!st) st = set_smem<latent_prompt_kernel<DT>>(kFaSmem);
+    if (st) return st;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t c = latent_config(
+        dim3(p.kv_rows / kPTile, (p.heads + p.head_group - 1) / p.head_group, p.B), kExThreads, kExSmem, s, attr, 1);
+    if ((st = record_launch(cudaLaunchKernelEx(&c, latent_expand_kernel<DT>, p, maps)))) return st;
+    const int pairs = (p.max_q + 2 * kPTile - 1) / (2 * kPTile);
+    c = latent_config(dim3(pairs * p.heads, p.B), kFaThreads, kFaSmem, s, attr, 1);
+    return record_launch(cudaLaunchKernelEx(&c, latent_prompt_kernel<DT>, p, maps));
+}
+
+}  // namespace
+
+int launch_expanded(LatentParams &p, int dt, cudaStream_t s) {
+    p.head_group = 4;
+    return dt == SPX_F16 ? launch_expanded_dt<SPX_F16>(p, dt, s) : launch_expanded_dt<SPX_BF16>(p, dt, s);
+}
+
+}  // namespace spx

@@ -224,4 +224,22 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
+// A tensor map of `rank` dimensions of two-byte values, innermost 64 of them
+// (one swizzled row); strides in bytes of dimensions 1 on.
+inline bool map_rows64(CUtensorMap *m, int dt, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                const uint32_t *box) {
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], es[4];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1;
+        if (i) st[i - 1] = strides[i - 1];
+    }
+    return fn(m, dt == SPX_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+              const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace spx

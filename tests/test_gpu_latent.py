@@ -165,10 +165,54 @@ def test_widths(R, dn, dv, folded):
     check(s, call(s), reference(s))
 
 
+@pytest.mark.parametrize("form", [1, 2])
+def test_large_prompt_scores(form):
+    s = make([900], [300], 4, F16, 64)
+    s["q"] *= 40
+    out, lse = call(s, form=form)
+    ref, rl = reference(s)
+    # scores of deviation 40 carry 40 times the error: 4 u grows to 160 u
+    assert (out.double() - ref).norm() <= 160 * U[F16] * ref.norm()
+    assert torch.isfinite(out).all()
+
+
 @pytest.mark.parametrize("lens,news", [([517, 65], [17, 1]), ([0, 3], [2, 5])])
 def test_not_causal(lens, news):
     s = make(lens, news, 16, F16, 64)
     check(s, call(s, causal=False), reference(s, causal=False))
+
+
+@pytest.mark.parametrize("lens,news,heads,page", [c for c in CASES if c[2] <= 64])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_expanded_form_matches_definition(lens, news, heads, page, dtype):
+    s = make(lens, news, heads, dtype, page, seed=len(lens) + heads)
+    check(s, call(s, form=2), reference(s))
+
+
+@pytest.mark.parametrize("lens,news,heads,page,R", [
+    ([256], [256], 4, 64, 512), ([257], [257], 3, 48, 512), ([1000], [700], 5, 16, 512), ([900, 333], [300, 333], 4, 32, 256),
+    ([512, 0, 130], [384, 0, 129], 6, 128, 128), ([40], [300], 4, 64, 512), ([1500, 700], [1, 513], 4, 64, 384),
+    ([4096], [4096], 2, 64, 512)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts(lens, news, heads, page, R, causal):
+    """Prompts take the expanded form by themselves; tiles of 128 rows and keys
+    that end early, rows that see nothing, requests of other lengths."""
+    s = make(lens, news, heads, BF16 if heads % 2 else F16, page, R=R, seed=sum(lens))
+    auto = call(s, causal=causal)
+    check(s, auto, reference(s, causal))
+    assert torch.equal(call(s, form=2, causal=causal)[0], auto[0])
+
+
+def test_forms_agree_on_masked_values():
+    """What a later token holds does not reach the rows before it."""
+    for bad in (math.nan, math.inf):
+        s = make([700], [300], 4, F16, 64)
+        clean, _ = call(s, form=2)
+        s["cache"].buf[s["cache"].block_table[0, 650 // 64].long(), 650 % 64] = bad
+        out, _ = call(s, form=2)
+        assert torch.equal(out[:250], clean[:250])
+        if math.isnan(bad):
+            assert torch.isnan(out[250:]).all()
 
 
 def test_long_context_and_batch():
