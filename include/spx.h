@@ -582,7 +582,7 @@ typedef struct {
     const void *w_uk;            /* [heads][dn][R], 16-byte aligned, or NULL */
     const void *w_uv;            /* [heads][dv][R], 16-byte aligned, or NULL */
     int dn, dv;                  /* 64 or 128 each (0 without weights) */
-    float scale;
+    float scale;                 /* finite and above 0 */
     int causal;
     void *out;                   /* 16-byte aligned */
     float *lse;                  /* [N][heads], or NULL */

@@ -232,7 +232,7 @@ constexpr int kFaThreads = 384;  // copies, products, two idle; 4 softmax warps 
 constexpr int kKRing = 5, kVRing = 3;
 struct FaMisc {
     uint64_t qfull[2], kfull[kKRing], kempty[kKRing], vfull[kVRing], vempty[kVRing];
-    uint64_t sfull[2], pfull[2], odone[2], fin;
+    uint64_t sfull[2], pfull[2][2], odone[2], fin;  // pfull: by halves of the keys
     uint32_t tmem;
     int abort;
 };
@@ -259,6 +259,10 @@ struct Ring {
             i = 0;
             phase ^= 1;
         }
+    }
+    __device__ __forceinline__ void back2() {
+        if (i < 2) phase ^= 1;
+        i = i < 2 ? i + N - 2 : i - 2;
     }
 };
 
@@ -297,7 +301,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m.qfull[i], 1);
             mbar_init(&m.sfull[i], 1);
-            mbar_init(&m.pfull[i], 4);
+            mbar_init(&m.pfull[i][0], 4);
+            mbar_init(&m.pfull[i][1], 4);
             mbar_init(&m.odone[i], 1);
         }
         mbar_init(&m.fin, 1);
@@ -383,26 +388,23 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 for (int c = 0; c < 3; ++c) kr.next();
         };
         auto product_o = [&](int x, int j, bool done) {
-            Ring<kVRing> v = vr;
-            for (int c = 0; ok && c < 2; ++c, v.next()) ok = ctl_wait(&m.vfull[v.i], v.phase, ctl);
-            ok = ok && ctl_wait(&m.pfull[x], j & 1, ctl);
-            if (!ok) return;
-            tc_fence_after();
-            if (elect_one()) {
-                v = vr;
 #pragma unroll 1
-                for (int c = 0; c < 2; ++c, v.next()) {
+            for (int c = 0; ok && c < 2; ++c) {
+                ok = ctl_wait(&m.vfull[vr.i], vr.phase, ctl) && ctl_wait(&m.pfull[x][c], j & 1, ctl);
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         umma_f16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 32 * c + 8 * i,
-                                    vd + v.i * (kPiece / 16) + 128 * i, id_o, (j | c | i) != 0);
-                    if (done) umma_commit(&m.vempty[v.i]);
+                                    vd + vr.i * (kPiece / 16) + 128 * i, id_o, (j | c | i) != 0);
+                    if (done) umma_commit(&m.vempty[vr.i]);
+                    if (c && j == n[x] - 1) umma_commit(&m.odone[x]);
                 }
-                if (j == n[x] - 1) umma_commit(&m.odone[x]);
+                __syncwarp();
+                vr.next();
             }
-            __syncwarp();
-            if (done)
-                for (int c = 0; c < 2; ++c) vr.next();
+            if (!done) vr.back2();
         };
         if (n[0]) product_s(0, 0, !n[1]);
         if (n[1]) product_s(1, 0, true);
@@ -432,24 +434,27 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             const int p0 = kPTile * j;
             const bool masked = p0 + kPTile > lim_lo || !live;
             const int left = lim - p0;  // columns of this tile that the row sees
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                uint32_t r[32];
-                tmem_ld32(st + c, r);
-                tmem_wait_ld();
-                if (__any_sync(0xffffffffu, masked)) {
+            uint32_t r[128];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (c + k < left) mx = fmaxf(mx, __uint_as_float(r[k]) * p.scale_log2);
-                } else {
+            for (int c = 0; c < 4; ++c) tmem_ld32(st + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * c));
+            tmem_wait_ld();
+            if (__any_sync(0xffffffffu, masked))
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r[k]) * p.scale_log2);
-                }
-            }
-            const bool rise = mx > mr + kFaSlack;
+                for (int k = 0; k < 128; ++k)
+                    if (k >= left) r[k] = 0xFF800000u;
+            float mx[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(r[k]);
+#pragma unroll
+            for (int k = 8; k < 128; ++k) mx[k & 7] = fmaxf(mx[k & 7], __uint_as_float(r[k]));
+#pragma unroll
+            for (int o = 4; o; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < o; ++k) mx[k] = fmaxf(mx[k], mx[k + o]);
+            const float top = mx[0] * p.scale_log2;  // (scale > 0)
+            const bool rise = top > mr + kFaSlack;
             if (__any_sync(0xffffffffu, rise)) {
-                const float mn = rise ? mx : mr, f = mn == mr ? 1.f : ex2(mr - mn);
+                const float mn = rise ? top : mr, f = mn == mr ? 1.f : ex2(mr - mn);
                 mr = mn;
                 l *= f;
                 if (j > 0) {
@@ -464,31 +469,30 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     }
                 }
             }
-            const float ref = mr == -INFINITY ? 0.f : mr - kFaShift;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                uint32_t r[32];
-                tmem_ld32(st + c, r);
-                tmem_wait_ld();
-                const bool cut = __any_sync(0xffffffffu, masked);
+            const float ref = mr == -INFINITY ? 0.f : kFaShift - mr;
+            const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), ref2 = pack2(ref, ref);
+            uint64_t l2[2] = {0, 0};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
                 uint32_t o[16];
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    float u = ex2(fmaf(__uint_as_float(r[k]), p.scale_log2, -ref));
-                    float v = ex2(fmaf(__uint_as_float(r[k + 1]), p.scale_log2, -ref));
-                    if (cut) {
-                        if (c + k >= left) u = 0.f;
-                        if (c + k + 1 >= left) v = 0.f;
-                    }
-                    l += u + v;
-                    o[k / 2] = Elem<DT>::down2(u, v);
+                for (int k = 0; k < 16; ++k) {
+                    const float2 t = unpack2(fma2(pack2(__uint_as_float(r[32 * c + 2 * k]), __uint_as_float(r[32 * c + 2 * k + 1])),
+                                                  sc2, ref2));
+                    const float u = ex2(t.x), v = ex2(t.y);
+                    l2[k & 1] = add2(l2[k & 1], pack2(u, v));
+                    o[k] = Elem<DT>::down2(u, v);
                 }
-                tmem_st16(st + c / 2, o);  // over columns read before
+                tmem_st16(st + 16 * c, o);  // over S, which is in registers
+                if (c & 1) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&m.pfull[x][c >> 1]);
+                }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&m.pfull[x]);
+            const float2 la = unpack2(add2(l2[0], l2[1]));
+            l += la.x + la.y;
         }
         if (live) {
             if (p.lse)

@@ -79,7 +79,8 @@ def attention(c, **kw):
     (dict(q=None), INV), (dict(q_start=None), INV), (dict(out=None), INV), (dict(N=-1), INV), (dict(heads=0), INV),
     (dict(max_q=-1), INV), (dict(max_len=-1), INV), (dict(w_uk=None), INV), (dict(w_uv=None), INV),
     (dict(w_uk=None, w_uv=None), INV), (dict(dn=96), UNS), (dict(dv=256, out_stride=16 * 256), UNS),
-    (dict(form=3), INV), (dict(form=-1), INV), (dict(q=FAKE + 2), INV), (dict(out=FAKE + 8), INV),
+    (dict(form=3), INV), (dict(form=-1), INV), (dict(scale=0.0), INV), (dict(scale=-1.0), INV),
+    (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV), (dict(q=FAKE + 2), INV), (dict(out=FAKE + 8), INV),
     (dict(w_uk=FAKE + 8), INV), (dict(q_stride=16 * 192 - 8), INV), (dict(out_stride=16 * 128 - 8), INV),
     (dict(q_stride=16 * 192 + 4), INV), (dict(out_stride=16 * 128 + 1), INV), (dict(ws=None), WSP),
     (dict(ws_bytes=100), WSP), (dict(ws=FAKE + 8), WSP), (dict(heads=2000, q_stride=1 << 30, out_stride=1 << 30), UNS)])
