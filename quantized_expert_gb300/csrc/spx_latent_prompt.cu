@@ -219,8 +219,12 @@ __global__ void __launch_bounds__(kExThreads, 1)
 // and key tile j:  S_X = Q_X K_j^T (128 x 128, 192 deep), softmax in registers
 // (a row a thread), P_X back into S_X's tensor memory as the A operand of
 // O_X += P_X V_j.  The two tiles share every key and value tile and take
-// turns: while one's softmax runs, the other's products do (order PV_0, S_0,
-// PV_1, S_1, so that S_X(j + 1) stands right behind PV_X(j)).  Tensor memory:
+// turns: while one's softmax runs, the other's products do.  Each has a warp of
+// its own to issue them (O_X(j), then S_X(j + 1)): the waits for barriers that
+// are long complete cost 150 cycles each, and with one issuing warp for both
+// they left the tensor cores idle half the time.  The two pass a turn to each
+// other, for otherwise they fall into step, both softmaxes at once and then
+// both products (3900 cycles per key tile instead of 2900).  Tensor memory:
 // S_0, S_1, O_0, O_1, 128 columns each.  Shared memory: Q 96 KB, keys in a
 // ring of 5 pieces (128 tokens x 64), values in one of 3 halves (64 tokens x
 // 128).
@@ -228,11 +232,13 @@ __global__ void __launch_bounds__(kExThreads, 1)
 // Per key tile 2 (768 + 512) cycles of products against 2 x 16384 exponentials;
 // the keys and values of a tile, 80 KB, come once per 256 rows (32 bytes a
 // cycle and SM).
-constexpr int kFaThreads = 384;  // copies, products, two idle; 4 softmax warps per tile
+constexpr int kFaThreads = 384;  // copies, two issuers of products, one idle; 4 softmax warps per tile
 constexpr int kKRing = 5, kVRing = 3;
 struct FaMisc {
-    uint64_t qfull[2], kfull[kKRing], kempty[kKRing], vfull[kVRing], vempty[kVRing];
-    uint64_t sfull[2], pfull[2][2], odone[2], fin;  // pfull: by halves of the keys
+    uint64_t qfull[2], kfull[2], rfull[2], vfull[2];  // by tiles, of which two are under way; rfull: the rotated part
+    uint64_t kempty[kKRing], vempty[kVRing];     // both issuers are done with a piece
+    uint64_t sfull[2], pfull[2], odone[2], fin[2];
+    uint64_t turn[2];                            // the other issuer has handed in its products
     uint32_t tmem;
     int abort;
 };
@@ -260,10 +266,6 @@ struct Ring {
             phase ^= 1;
         }
     }
-    __device__ __forceinline__ void back2() {
-        if (i < 2) phase ^= 1;
-        i = i < 2 ? i + N - 2 : i - 2;
-    }
 };
 
 template <int DT>
@@ -290,22 +292,21 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     }
     const int most = max(n[0], n[1]);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kKRing; ++i) {
-            mbar_init(&m.kfull[i], 1);
-            mbar_init(&m.kempty[i], 1);
-        }
-        for (int i = 0; i < kVRing; ++i) {
-            mbar_init(&m.vfull[i], 1);
-            mbar_init(&m.vempty[i], 1);
-        }
+        for (int i = 0; i < kKRing; ++i) mbar_init(&m.kempty[i], 2);
+        for (int i = 0; i < kVRing; ++i) mbar_init(&m.vempty[i], 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m.qfull[i], 1);
+            mbar_init(&m.kfull[i], 1);
+            mbar_init(&m.rfull[i], 1);
+            mbar_init(&m.vfull[i], 1);
             mbar_init(&m.sfull[i], 1);
-            mbar_init(&m.pfull[i][0], 4);
-            mbar_init(&m.pfull[i][1], 4);
+            mbar_init(&m.pfull[i], 4);
             mbar_init(&m.odone[i], 1);
         }
-        mbar_init(&m.fin, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&m.fin[i], 1);
+            mbar_init(&m.turn[i], 1);
+        }
         m.abort = 0;
         fence_mbar_init();
     }
@@ -334,89 +335,110 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         bool ok = true;
         for (int j = 0; ok && j < most; ++j) {
             const int row = b * p.kv_rows + kPTile * j;
+            uint64_t *kf = &m.kfull[j & 1], *rf = &m.rfull[j & 1], *vf = &m.vfull[j & 1];
             for (int c = 0; c < 3; ++c, kr.next()) {
                 if (!(ok = ctl_wait(&m.kempty[kr.i], kr.phase ^ 1, ctl))) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&m.kfull[kr.i], kPiece);
-                    if (c < 2)
-                        tma_load_4d(ks + kr.i * kPiece, &maps.k, 0, row, c, h, &m.kfull[kr.i], pol);
-                    else
-                        tma_load_2d(ks + kr.i * kPiece, &maps.rope, 0, row, &m.kfull[kr.i], pol);
+                    if (c == 0) mbar_arrive_expect_tx(kf, 2 * kPiece);
+                    if (c < 2) {
+                        tma_load_4d(ks + kr.i * kPiece, &maps.k, 0, row, c, h, kf, pol);
+                    } else {
+                        mbar_arrive_expect_tx(rf, kPiece);
+                        tma_load_2d(ks + kr.i * kPiece, &maps.rope, 0, row, rf, pol);
+                    }
                 }
                 __syncwarp();
             }
             for (int c = 0; ok && c < 2; ++c, vr.next()) {
                 if (!(ok = ctl_wait(&m.vempty[vr.i], vr.phase ^ 1, ctl))) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&m.vfull[vr.i], kPiece);
-                    tma_load_4d(vs + vr.i * kPiece, &maps.v, 0, row + 64 * c, 0, h, &m.vfull[vr.i], pol);
+                    if (c == 0) mbar_arrive_expect_tx(vf, 2 * kPiece);
+                    tma_load_4d(vs + vr.i * kPiece, &maps.v, 0, row + 64 * c, 0, h, vf, pol);
                 }
                 __syncwarp();
             }
         }
         if (!ok) ctl_settle(100000000ull);
-    } else if (warp == 1) {
-        // ---- products
+    } else if (warp < 3) {
+        // ---- products of one query tile
+        const int x = warp - 1;
         const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
         const uint32_t id_s = idesc_f16_f32(128, 128) | fmt, id_o = idesc_f16_f32(128, 128) | fmt | kIdescBMn;
-        const uint64_t qd = sw128_desc(smem_u32(qs)), kd = sw128_desc(smem_u32(ks));
+        const uint64_t qd = sw128_desc(smem_u32(qs) + 3 * x * kPiece), kd = sw128_desc(smem_u32(ks));
         const uint64_t vd = sw128_desc_mn(smem_u32(vs), kPiece / 2);
+        const uint32_t st = tmem + 128 * x, ot = tmem + 256 + 128 * x;
+        const int nx = n[x];
         Ring<kKRing> kr;
         Ring<kVRing> vr;
-        bool ok = true;
-        // S_x(j); `done`: its keys are not needed again
-        auto product_s = [&](int x, int j, bool done) {
-            if (j == 0) ok = ok && ctl_wait(&m.qfull[x], 0, ctl);
-            Ring<kKRing> k = kr;
-            for (int c = 0; ok && c < 3; ++c, k.next()) ok = ctl_wait(&m.kfull[k.i], k.phase, ctl);
-            if (!ok) return;
+        bool ok = !nx || ctl_wait(&m.qfull[x], 0, ctl);
+        // O_x(j - 1), then S_x(j), in one stretch behind everything that they wait for; past the tile's last
+        // key both only pass the pieces on.  The rotated part of the keys, whose slot comes free last, has a
+        // wait of its own behind the rest.
+#pragma unroll 1
+        for (int j = 0; ok && j <= most; ++j) {
+            const bool has_o = j > 0 && j <= nx, has_s = j < nx;
+            ok = (j == most || ctl_wait(&m.kfull[j & 1], (j >> 1) & 1, ctl)) &&
+                 (j == 0 || ctl_wait(&m.vfull[(j - 1) & 1], ((j - 1) >> 1) & 1, ctl)) &&
+                 (!has_o || ctl_wait(&m.pfull[x], (j - 1) & 1, ctl)) &&
+                 // tile 1 goes behind tile 0's products of the same j, tile 0 behind tile 1's of the last
+                 (x ? ctl_wait(&m.turn[1], j & 1, ctl) : j == 0 || ctl_wait(&m.turn[0], (j - 1) & 1, ctl));
+            if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                k = kr;
+                Ring<kVRing> v = vr;
+                if (j > 0)
 #pragma unroll 1
-                for (int c = 0; c < 3; ++c, k.next()) {
+                    for (int c = 0; c < 2; ++c, v.next()) {
+                        if (has_o) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        umma_f16(tmem + 128 * x, qd + (3 * x + c) * (kPiece / 16) + 2 * i, kd + k.i * (kPiece / 16) + 2 * i,
-                                 id_s, (c | i) != 0);
-                    if (done) umma_commit(&m.kempty[k.i]);
-                }
-                umma_commit(&m.sfull[x]);
+                            for (int i = 0; i < 4; ++i)
+                                umma_f16_ta(ot, st + 32 * c + 8 * i, vd + v.i * (kPiece / 16) + 128 * i, id_o,
+                                            (j != 1) | c | i);
+                            umma_commit(&m.vempty[v.i]);
+                        } else {
+                            mbar_arrive(&m.vempty[v.i]);
+                        }
+                    }
+                if (has_o && j == nx) umma_commit(&m.odone[x]);
+                Ring<kKRing> k = kr;
+                if (j < most)
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c, k.next()) {
+                        if (has_s) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                umma_f16(st, qd + c * (kPiece / 16) + 2 * i, kd + k.i * (kPiece / 16) + 2 * i, id_s, c | i);
+                            umma_commit(&m.kempty[k.i]);
+                        } else {
+                            mbar_arrive(&m.kempty[k.i]);
+                        }
+                    }
+                mbar_arrive(&m.turn[x ^ 1]);  // before the last piece, to hide the other's waking
             }
             __syncwarp();
-            if (done)
-                for (int c = 0; c < 3; ++c) kr.next();
-        };
-        auto product_o = [&](int x, int j, bool done) {
-#pragma unroll 1
-            for (int c = 0; ok && c < 2; ++c) {
-                ok = ctl_wait(&m.vfull[vr.i], vr.phase, ctl) && ctl_wait(&m.pfull[x][c], j & 1, ctl);
-                if (!ok) return;
-                tc_fence_after();
-                if (elect_one()) {
+            if (j > 0)
+                for (int c = 0; c < 2; ++c) vr.next();
+            if (j == most) break;
+            for (int c = 0; c < 2; ++c) kr.next();
+            if (!(ok = ctl_wait(&m.rfull[j & 1], (j >> 1) & 1, ctl))) break;
+            tc_fence_after();
+            if (elect_one()) {
+                if (has_s) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        umma_f16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 32 * c + 8 * i,
-                                    vd + vr.i * (kPiece / 16) + 128 * i, id_o, (j | c | i) != 0);
-                    if (done) umma_commit(&m.vempty[vr.i]);
-                    if (c && j == n[x] - 1) umma_commit(&m.odone[x]);
+                        umma_f16(st, qd + 2 * (kPiece / 16) + 2 * i, kd + kr.i * (kPiece / 16) + 2 * i, id_s, 1);
+                    umma_commit(&m.kempty[kr.i]);
+                    umma_commit(&m.sfull[x]);
+                } else {
+                    mbar_arrive(&m.kempty[kr.i]);
                 }
-                __syncwarp();
-                vr.next();
             }
-            if (!done) vr.back2();
-        };
-        if (n[0]) product_s(0, 0, !n[1]);
-        if (n[1]) product_s(1, 0, true);
-        for (int j = 0; ok && j < most; ++j) {
-            if (j < n[0]) product_o(0, j, j >= n[1]);
-            if (j + 1 < n[0]) product_s(0, j + 1, j + 1 >= n[1]);
-            if (j < n[1]) product_o(1, j, true);
-            if (j + 1 < n[1]) product_s(1, j + 1, true);
+            __syncwarp();
+            kr.next();
         }
         if (m.abort) {
-            if (elect_one()) umma_commit(&m.fin);
-            ctl_drain(&m.fin, 0, 100000000ull);
+            if (elect_one()) umma_commit(&m.fin[x]);
+            ctl_drain(&m.fin[x], 0, 100000000ull);
         }
     } else if (warp >= 4) {
         // ---- softmax and results: a row a thread
@@ -484,13 +506,11 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     o[k] = Elem<DT>::down2(u, v);
                 }
                 tmem_st16(st + 16 * c, o);  // over S, which is in registers
-                if (c & 1) {
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&m.pfull[x][c >> 1]);
-                }
             }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.pfull[x]);
             const float2 la = unpack2(add2(l2[0], l2[1]));
             l += la.x + la.y;
         }
