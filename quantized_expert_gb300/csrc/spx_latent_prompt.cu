@@ -232,12 +232,12 @@ __global__ void __launch_bounds__(kExThreads, 1)
 // Per key tile 2 (768 + 512) cycles of products against 2 x 16384 exponentials;
 // the keys and values of a tile, 80 KB, come once per 256 rows (32 bytes a
 // cycle and SM).
-constexpr int kFaThreads = 384;  // copies, two issuers of products, one idle; 4 softmax warps per tile
+constexpr int kFaThreads = 384;  // copies of Q and K, two issuers of products, copies of V; 4 softmax warps per tile
 constexpr int kKRing = 5, kVRing = 3;
 struct FaMisc {
     uint64_t qfull[2], kfull[2], rfull[2], vfull[2];  // by tiles, of which two are under way; rfull: the rotated part
     uint64_t kempty[kKRing], vempty[kVRing];     // both issuers are done with a piece
-    uint64_t sfull[2], pfull[2], odone[2], fin[2];
+    uint64_t sfull[2], pfull[2][2], odone[2], fin[2];  // pfull: by halves of the keys
     uint64_t turn[2];                            // the other issuer has handed in its products
     uint32_t tmem;
     int abort;
@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             mbar_init(&m.rfull[i], 1);
             mbar_init(&m.vfull[i], 1);
             mbar_init(&m.sfull[i], 1);
-            mbar_init(&m.pfull[i], 4);
+            mbar_init(&m.pfull[i][0], 4);
+            mbar_init(&m.pfull[i][1], 4);
             mbar_init(&m.odone[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_LATENT};
 
     if (warp == 0) {
-        // ---- copies
+        // ---- copies of Q and K
         const uint64_t pol = policy_evict_normal();
         for (int x = 0; x < 2; ++x)
             if (n[x] && elect_one()) {
@@ -331,33 +332,38 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         __syncwarp();
         griddep_wait();
         Ring<kKRing> kr;
-        Ring<kVRing> vr;
         bool ok = true;
-        for (int j = 0; ok && j < most; ++j) {
-            const int row = b * p.kv_rows + kPTile * j;
-            uint64_t *kf = &m.kfull[j & 1], *rf = &m.rfull[j & 1], *vf = &m.vfull[j & 1];
+        for (int j = 0; ok && j < most; ++j)
             for (int c = 0; c < 3; ++c, kr.next()) {
                 if (!(ok = ctl_wait(&m.kempty[kr.i], kr.phase ^ 1, ctl))) break;
                 if (elect_one()) {
-                    if (c == 0) mbar_arrive_expect_tx(kf, 2 * kPiece);
-                    if (c < 2) {
-                        tma_load_4d(ks + kr.i * kPiece, &maps.k, 0, row, c, h, kf, pol);
-                    } else {
-                        mbar_arrive_expect_tx(rf, kPiece);
-                        tma_load_2d(ks + kr.i * kPiece, &maps.rope, 0, row, rf, pol);
-                    }
+                    const int row = b * p.kv_rows + kPTile * j;
+                    uint64_t *full = c < 2 ? &m.kfull[j & 1] : &m.rfull[j & 1];
+                    if (c != 1) mbar_arrive_expect_tx(full, c ? kPiece : 2 * kPiece);
+                    if (c < 2)
+                        tma_load_4d(ks + kr.i * kPiece, &maps.k, 0, row, c, h, full, pol);
+                    else
+                        tma_load_2d(ks + kr.i * kPiece, &maps.rope, 0, row, full, pol);
                 }
                 __syncwarp();
             }
-            for (int c = 0; ok && c < 2; ++c, vr.next()) {
+        if (!ok) ctl_settle(100000000ull);
+    } else if (warp == 3) {
+        // ---- copies of V: apart from those of K, which would wait behind them for room
+        const uint64_t pol = policy_evict_normal();
+        griddep_wait();
+        Ring<kVRing> vr;
+        bool ok = true;
+        for (int j = 0; ok && j < most; ++j)
+            for (int c = 0; c < 2; ++c, vr.next()) {
                 if (!(ok = ctl_wait(&m.vempty[vr.i], vr.phase ^ 1, ctl))) break;
                 if (elect_one()) {
-                    if (c == 0) mbar_arrive_expect_tx(vf, 2 * kPiece);
-                    tma_load_4d(vs + vr.i * kPiece, &maps.v, 0, row + 64 * c, 0, h, vf, pol);
+                    if (c == 0) mbar_arrive_expect_tx(&m.vfull[j & 1], 2 * kPiece);
+                    tma_load_4d(vs + vr.i * kPiece, &maps.v, 0, b * p.kv_rows + kPTile * j + 64 * c, 0, h, &m.vfull[j & 1],
+                                pol);
                 }
                 __syncwarp();
             }
-        }
         if (!ok) ctl_settle(100000000ull);
     } else if (warp < 3) {
         // ---- products of one query tile
@@ -379,27 +385,37 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             const bool has_o = j > 0 && j <= nx, has_s = j < nx;
             ok = (j == most || ctl_wait(&m.kfull[j & 1], (j >> 1) & 1, ctl)) &&
                  (j == 0 || ctl_wait(&m.vfull[(j - 1) & 1], ((j - 1) >> 1) & 1, ctl)) &&
-                 (!has_o || ctl_wait(&m.pfull[x], (j - 1) & 1, ctl)) &&
                  // tile 1 goes behind tile 0's products of the same j, tile 0 behind tile 1's of the last
-                 (x ? ctl_wait(&m.turn[1], j & 1, ctl) : j == 0 || ctl_wait(&m.turn[0], (j - 1) & 1, ctl));
+                 (x ? ctl_wait(&m.turn[1], j & 1, ctl) : j == 0 || ctl_wait(&m.turn[0], (j - 1) & 1, ctl)) &&
+                 (!has_o || ctl_wait(&m.pfull[x][0], (j - 1) & 1, ctl));
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
-                Ring<kVRing> v = vr;
-                if (j > 0)
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c, v.next()) {
-                        if (has_o) {
+            if (j > 0) {  // the first half while the softmax is at the second
+                if (elect_one()) {
+                    if (has_o) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                umma_f16_ta(ot, st + 32 * c + 8 * i, vd + v.i * (kPiece / 16) + 128 * i, id_o,
-                                            (j != 1) | c | i);
-                            umma_commit(&m.vempty[v.i]);
-                        } else {
-                            mbar_arrive(&m.vempty[v.i]);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            umma_f16_ta(ot, st + 8 * i, vd + vr.i * (kPiece / 16) + 128 * i, id_o, (j != 1) | i);
+                        umma_commit(&m.vempty[vr.i]);
+                    } else {
+                        mbar_arrive(&m.vempty[vr.i]);
                     }
-                if (has_o && j == nx) umma_commit(&m.odone[x]);
+                }
+                __syncwarp();
+                vr.next();
+                if (has_o && !(ok = ctl_wait(&m.pfull[x][1], (j - 1) & 1, ctl))) break;
+                tc_fence_after();
+            }
+            if (elect_one()) {
+                if (has_o) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        umma_f16_ta(ot, st + 32 + 8 * i, vd + vr.i * (kPiece / 16) + 128 * i, id_o, 1);
+                    umma_commit(&m.vempty[vr.i]);
+                    if (j == nx) umma_commit(&m.odone[x]);
+                } else if (j > 0) {
+                    mbar_arrive(&m.vempty[vr.i]);
+                }
                 Ring<kKRing> k = kr;
                 if (j < most)
 #pragma unroll 1
@@ -416,8 +432,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 mbar_arrive(&m.turn[x ^ 1]);  // before the last piece, to hide the other's waking
             }
             __syncwarp();
-            if (j > 0)
-                for (int c = 0; c < 2; ++c) vr.next();
+            if (j > 0) vr.next();
             if (j == most) break;
             for (int c = 0; c < 2; ++c) kr.next();
             if (!(ok = ctl_wait(&m.rfull[j & 1], (j >> 1) & 1, ctl))) break;
@@ -506,11 +521,13 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     o[k] = Elem<DT>::down2(u, v);
                 }
                 tmem_st16(st + 16 * c, o);  // over S, which is in registers
+                if (c & 1) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&m.pfull[x][c >> 1]);
+                }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&m.pfull[x]);
             const float2 la = unpack2(add2(l2[0], l2[1]));
             l += la.x + la.y;
         }
