@@ -879,13 +879,6 @@ __device__ __forceinline__ void join_sums(const LatentParams &p, const RowSums<R
         }
     }
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 // Another block's shared memory (between two cluster barriers, so that the
 // loads need no order among themselves).
 __device__ __forceinline__ float2 cluster_ld2(const void *p, uint32_t rank) {

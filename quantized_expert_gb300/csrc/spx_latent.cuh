@@ -134,6 +134,14 @@ __device__ __forceinline__ int latent_limit(const LatentParams &p, const LatentR
     return p.causal ? max(r.len - r.T + t + 1, 0) : r.len;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // -------------------------------------------------------------------- host --
 inline cudaLaunchConfig_t latent_config(dim3 grid, int threads, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr,
                                         int cluster) {

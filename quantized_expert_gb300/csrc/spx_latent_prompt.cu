@@ -28,20 +28,35 @@ struct PromptMaps {
     CUtensorMap cache;       // [page][piece][token][64], boxes of 1 piece x box_tokens
     CUtensorMap w_uk, w_uv;  // [piece][head * 128 + row][64], boxes of 1 piece x 128 rows
     CUtensorMap q;           // [head][piece][token][64], boxes of 3 pieces x 128 tokens
-    CUtensorMap k, v;        // [head][piece][row][64]: k in boxes of 1 piece x 128 rows, v of 2 x 64
-    CUtensorMap rope;        // [row][64], boxes of 128 rows
 };
+
+// Keys and values are written as the attention launch reads them, in core
+// matrices (units of 8 values, 16 bytes, of consecutive tokens side by side):
+// per head, request and tile of 128 tokens 32 KB each, keys [unit 16][token
+// 128][8], values [half 2][unit 16][token 64][8]; the rotated parts [unit
+// 8][token 128][8] per request and tile.  A warp of tokens then stores 512
+// bytes in a row (rows of 256 bytes a token cost four times the store
+// transactions and held up the products), and a piece is one plain copy.
+__device__ __forceinline__ size_t key_unit(int tile, int t, int unit) {
+    return (size_t)tile * (2 * kPiece / 2) + (size_t)unit * (kPTile * 8) + (size_t)(t & (kPTile - 1)) * 8;
+}
+__device__ __forceinline__ size_t value_unit(int tile, int t, int unit) {
+    return (size_t)tile * (2 * kPiece / 2) + (size_t)(t >> 6 & 1) * (kPiece / 2) + (size_t)unit * (64 * 8) +
+           (size_t)(t & 63) * 8;
+}
 
 // ----------------------------------------------------------- expand launch --
 // Block (token tile, group of heads, request): the tile's latent vectors stay
 // in shared memory (A, R / 64 pieces of 128 tokens) while the heads' weights
 // stream past in stages of 64 latent columns, W_uk[h] and W_uv[h] as the 256
 // rows of B: D[128 tokens x 256] = keys and values of one head, in one of two
-// accumulators.  Bound by the tensor cores (256 columns a product) and by L2,
-// which reads the weights once per token tile.
+// accumulators.  A product of 256 columns takes 512 cycles a stage, in which an
+// SM would have to fetch 32 KB from L2, 64 bytes a cycle and more than it gets:
+// two blocks of neighbouring token tiles form a cluster, each fetches one of
+// the two matrices and the copy goes to both.
 constexpr int kExStages = 3;
 constexpr int kExStage = 2 * kPiece;
-constexpr int kExThreads = 256;  // copies of W, products, 2 warps' copies of A, 4 epilogue warps
+constexpr int kExThreads = 384;  // copies of W, products, 2 warps' copies of A, 8 epilogue warps
 struct ExMisc {
     uint64_t afull, wfull[kExStages], wempty[kExStages], dfull[2], dempty[2], fin;
     uint32_t tmem;
@@ -75,16 +90,17 @@ __global__ void __launch_bounds__(kExThreads, 1)
     griddep_wait();
     griddep_launch_dependents();
     const LatentReq rq = latent_req(p, b);
-    if (t0 >= rq.len || rq.T == 0) return;
+    const uint32_t rank = cluster_rank();
+    if (t0 - kPTile * (int)rank >= rq.len || rq.T == 0) return;  // both blocks of the cluster alike
     if (threadIdx.x == 0) {
         mbar_init(&m.afull, 2);
         for (int s = 0; s < kExStages; ++s) {
             mbar_init(&m.wfull[s], 1);
-            mbar_init(&m.wempty[s], 1);
+            mbar_init(&m.wempty[s], 2);  // both blocks have used it
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&m.dfull[s], 1);
-            mbar_init(&m.dempty[s], 4);
+            mbar_init(&m.dempty[s], 8);
         }
         mbar_init(&m.fin, 1);
         m.abort = 0;
@@ -96,6 +112,8 @@ __global__ void __launch_bounds__(kExThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    cluster_arrive();  // the other block's barriers exist
+    cluster_wait();
     tc_fence_after();
     const uint32_t tmem = m.tmem;
     const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_LATENT};
@@ -116,19 +134,19 @@ __global__ void __launch_bounds__(kExThreads, 1)
                                 &m.afull, pol);
             __syncwarp();
         }
-        // ---- their rotated parts (once for all heads), 8 values a lane
-        if (h0 == 0)
-            for (int i = lane; i < 64 * 8; i += 32) {
-                const int t = t0 + 64 * half + (i >> 3), pg_i = p.by_page(t);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (t < rq.len) {
-                    const int pg = __ldg(p.table + (size_t)b * p.max_pages + pg_i);
-                    if (pg >= 0 && pg < p.num_pages)
-                        v = *reinterpret_cast<const uint4 *>(p.cache + (int64_t)pg * p.page_stride +
-                                                             (int64_t)(t - pg_i * p.page_size) * p.token_stride + p.R +
-                                                             8 * (i & 7));
-                }
-                *reinterpret_cast<uint4 *>(p.rope_x + ((size_t)b * p.kv_rows + t) * 64 + 8 * (i & 7)) = v;
+        // ---- their rotated parts (once for all heads), a token a lane
+        if (h0 == 0 && t0 < rq.len)
+            for (int t = t0 + 64 * half + lane; t < t0 + 64 * half + 64; t += 32) {
+                const int pg_i = p.by_page(t), pg = t < rq.len ? __ldg(p.table + (size_t)b * p.max_pages + pg_i) : -1;
+                const bool ok = pg >= 0 && pg < p.num_pages;
+                const uint16_t *src = p.cache + (int64_t)(ok ? pg : 0) * p.page_stride +
+                                      (int64_t)(t - pg_i * p.page_size) * p.token_stride + p.R;
+                uint16_t *dst = p.rope_x + ((size_t)b * (p.kv_rows / kPTile) + blockIdx.x) * (kPiece / 2) +
+                                (size_t)(t & (kPTile - 1)) * 8;
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    *reinterpret_cast<uint4 *>(dst + u * (kPTile * 8)) =
+                        ok ? *reinterpret_cast<const uint4 *>(src + 8 * u) : make_uint4(0, 0, 0, 0);
             }
     } else if (warp == 0) {
         // ---- the weights
@@ -141,8 +159,8 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 if (!(ok = ctl_wait(&m.wempty[s], ((it / kExStages) & 1) ^ 1, ctl))) break;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&m.wfull[s], kExStage);
-                    tma_load_3d(ws + s * kExStage, &maps.w_uk, 0, 128 * h, c, &m.wfull[s], pol);
-                    tma_load_3d(ws + s * kExStage + kPiece, &maps.w_uv, 0, 128 * h, c, &m.wfull[s], pol);
+                    tma_load_3d_multicast(ws + s * kExStage + rank * kPiece, rank ? &maps.w_uv : &maps.w_uk, 0, 128 * h, c,
+                                          &m.wfull[s], 3, pol);
                 }
                 __syncwarp();
             }
@@ -164,7 +182,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         umma_f16(d, ad + c * (kPiece / 16) + 2 * j, wd + s * (kExStage / 16) + 2 * j, id, (c | j) != 0);
-                    umma_commit(&m.wempty[s]);
+                    umma_commit_multicast(&m.wempty[s], 3);
                     if (c == nc - 1) umma_commit(&m.dfull[i & 1]);
                 }
                 __syncwarp();
@@ -175,31 +193,40 @@ __global__ void __launch_bounds__(kExThreads, 1)
             ctl_drain(&m.fin, 0, 100000000ull);
         }
     } else {
-        // ---- epilogue: a token a lane, its keys, then its values
+        // ---- epilogue: a token a lane, its keys (warps 4-7) or its values
         const int q = warp & 3, t = t0 + 32 * q + lane;
-        const bool live = t < rq.len;
+        const bool live = t < rq.len, values = warp >= 8;
         for (int i = 0; i < nh; ++i) {
             ctl_wait(&m.dfull[i & 1], (i >> 1) & 1, ctl);
             tc_fence_after();
-            const size_t row = (size_t)(h0 + i) * p.B * p.kv_rows + (size_t)b * p.kv_rows + t;
+            const size_t of_head = ((size_t)(h0 + i) * p.B + b) * p.kv_rows * 128;
+            uint16_t *dst = values ? p.v_x + of_head + value_unit(blockIdx.x, t, 0) : p.k_x + of_head + key_unit(blockIdx.x, t, 0);
+            const int step = values ? 64 * 8 : kPTile * 8;  // from unit to unit
 #pragma unroll 1
-            for (int x = 0; x < 256; x += 32) {
+            for (int x = 0; x < 128 && t0 < rq.len; x += 32) {
                 uint32_t r[32];
-                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (i & 1) * 256 + x, r);
+                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (i & 1) * 256 + (values ? 128 : 0) + x, r);
                 tmem_wait_ld();
-                // Past the length: zeros.  A value that is not finite: 0, as its weight 0 elsewhere times it would
-                // not be 0; its key carries it to the rows that see it.
+                // A value that is not finite becomes 0, as its weight 0 elsewhere times it would not be 0; its
+                // key carries it to the rows that see it.  (0 times the 32, summed, is a NaN if one is not.)
+                uint64_t test = 0;
+                if (values)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+                        test = fma2(pack2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), 0ull, test);
+                const float2 bad = unpack2(test);
+                if (bad.x + bad.y != 0.f)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(fabsf(__uint_as_float(r[k])) < INFINITY)) r[k] = 0u;
                 uint32_t o[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    float u = __uint_as_float(r[2 * k]), v = __uint_as_float(r[2 * k + 1]);
-                    if (!live || (x >= 128 && !(fabsf(u) < INFINITY))) u = 0.f;
-                    if (!live || (x >= 128 && !(fabsf(v) < INFINITY))) v = 0.f;
-                    o[k] = Elem<DT>::down2(u, v);
-                }
-                uint4 *dst = reinterpret_cast<uint4 *>((x < 128 ? p.k_x : p.v_x) + row * 128 + (x & 127));
+                for (int k = 0; k < 16; ++k)  // past the length: zeros
+                    o[k] = live ? Elem<DT>::down2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])) : 0u;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                for (int k = 0; k < 4; ++k)
+                    *reinterpret_cast<uint4 *>(dst + (x / 8 + k) * step) =
+                        make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             }
             tc_fence_before();
             __syncwarp();
@@ -212,6 +239,8 @@ __global__ void __launch_bounds__(kExThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    cluster_arrive();  // the other block copies into this one's shared memory until its end
+    cluster_wait();
 }
 
 // -------------------------------------------------------- attention launch --
@@ -337,13 +366,11 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             for (int c = 0; c < 3; ++c, kr.next()) {
                 if (!(ok = ctl_wait(&m.kempty[kr.i], kr.phase ^ 1, ctl))) break;
                 if (elect_one()) {
-                    const int row = b * p.kv_rows + kPTile * j;
                     uint64_t *full = c < 2 ? &m.kfull[j & 1] : &m.rfull[j & 1];
                     if (c != 1) mbar_arrive_expect_tx(full, c ? kPiece : 2 * kPiece);
-                    if (c < 2)
-                        tma_load_4d(ks + kr.i * kPiece, &maps.k, 0, row, c, h, full, pol);
-                    else
-                        tma_load_2d(ks + kr.i * kPiece, &maps.rope, 0, row, full, pol);
+                    const uint16_t *src = c < 2 ? p.k_x + ((size_t)h * p.B + b) * p.kv_rows * 128 + key_unit(j, 0, 8 * c)
+                                                : p.rope_x + ((size_t)b * (p.kv_rows / kPTile) + j) * (kPiece / 2);
+                    bulk_g2s(ks + kr.i * kPiece, src, kPiece, full, pol);
                 }
                 __syncwarp();
             }
@@ -359,8 +386,9 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 if (!(ok = ctl_wait(&m.vempty[vr.i], vr.phase ^ 1, ctl))) break;
                 if (elect_one()) {
                     if (c == 0) mbar_arrive_expect_tx(&m.vfull[j & 1], 2 * kPiece);
-                    tma_load_4d(vs + vr.i * kPiece, &maps.v, 0, b * p.kv_rows + kPTile * j + 64 * c, 0, h, &m.vfull[j & 1],
-                                pol);
+                    bulk_g2s(vs + vr.i * kPiece,
+                             p.v_x + ((size_t)h * p.B + b) * p.kv_rows * 128 + value_unit(j, 64 * c, 0), kPiece,
+                             &m.vfull[j & 1], pol);
                 }
                 __syncwarp();
             }
@@ -370,8 +398,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         const int x = warp - 1;
         const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
         const uint32_t id_s = idesc_f16_f32(128, 128) | fmt, id_o = idesc_f16_f32(128, 128) | fmt | kIdescBMn;
-        const uint64_t qd = sw128_desc(smem_u32(qs) + 3 * x * kPiece), kd = sw128_desc(smem_u32(ks));
-        const uint64_t vd = sw128_desc_mn(smem_u32(vs), kPiece / 2);
+        const uint64_t qd = sw128_desc(smem_u32(qs) + 3 * x * kPiece), kd = plain_desc(smem_u32(ks), kPTile * 16, 128);
+        const uint64_t vd = plain_desc(smem_u32(vs), 128, 64 * 16);  // a k-step: two units of K, 16 tokens of V
         const uint32_t st = tmem + 128 * x, ot = tmem + 256 + 128 * x;
         const int nx = n[x];
         Ring<kKRing> kr;
@@ -395,7 +423,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                     if (has_o) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            umma_f16_ta(ot, st + 8 * i, vd + vr.i * (kPiece / 16) + 128 * i, id_o, (j != 1) | i);
+                            umma_f16_ta(ot, st + 8 * i, vd + vr.i * (kPiece / 16) + 16 * i, id_o, (j != 1) | i);
                         umma_commit(&m.vempty[vr.i]);
                     } else {
                         mbar_arrive(&m.vempty[vr.i]);
@@ -410,7 +438,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 if (has_o) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        umma_f16_ta(ot, st + 32 + 8 * i, vd + vr.i * (kPiece / 16) + 128 * i, id_o, 1);
+                        umma_f16_ta(ot, st + 32 + 8 * i, vd + vr.i * (kPiece / 16) + 16 * i, id_o, 1);
                     umma_commit(&m.vempty[vr.i]);
                     if (j == nx) umma_commit(&m.odone[x]);
                 } else if (j > 0) {
@@ -423,7 +451,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                         if (has_s) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                umma_f16(st, qd + c * (kPiece / 16) + 2 * i, kd + k.i * (kPiece / 16) + 2 * i, id_s, c | i);
+                                umma_f16(st, qd + c * (kPiece / 16) + 2 * i, kd + k.i * (kPiece / 16) + 2 * kPTile * i, id_s, c | i);
                             umma_commit(&m.kempty[k.i]);
                         } else {
                             mbar_arrive(&m.kempty[k.i]);
@@ -441,7 +469,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 if (has_s) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        umma_f16(st, qd + 2 * (kPiece / 16) + 2 * i, kd + kr.i * (kPiece / 16) + 2 * i, id_s, 1);
+                        umma_f16(st, qd + 2 * (kPiece / 16) + 2 * i, kd + kr.i * (kPiece / 16) + 2 * kPTile * i, id_s, 1);
                     umma_commit(&m.kempty[kr.i]);
                     umma_commit(&m.sfull[x]);
                 } else {
@@ -571,7 +599,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
 // -------------------------------------------------------------------- host --
 bool prompt_maps(const LatentParams &p, int dt, PromptMaps *m) {
     memset(m, 0, sizeof(*m));
-    const uint64_t tok = (uint64_t)p.token_stride * 2, rows = (uint64_t)p.B * p.kv_rows;
+    const uint64_t tok = (uint64_t)p.token_stride * 2;
     const uint64_t cd[4] = {64, (uint64_t)p.page_size, (uint64_t)(p.R + p.P) / 64, (uint64_t)p.num_pages};
     const uint64_t cs[3] = {tok, 128, p.num_pages > 1 ? (uint64_t)p.page_stride * 2 : tok * p.page_size};
     const uint32_t cb[4] = {64, (uint32_t)p.box_tokens, 1, 1};
@@ -579,14 +607,8 @@ bool prompt_maps(const LatentParams &p, int dt, PromptMaps *m) {
     const uint32_t wb[3] = {64, 128, 1};
     const uint64_t qd[4] = {64, (uint64_t)p.N, 3, (uint64_t)p.heads}, qst[3] = {(uint64_t)p.q_stride * 2, 128, 192 * 2};
     const uint32_t qb[4] = {64, 128, 3, 1};
-    const uint64_t kd[4] = {64, rows, 2, (uint64_t)p.heads}, kst[3] = {256, 128, rows * 256};
-    const uint32_t kb[4] = {64, 128, 1, 1}, vb[4] = {64, 64, 2, 1};
-    const uint64_t rd[2] = {64, rows}, rst[1] = {128};
-    const uint32_t rb[2] = {64, 128};
     return map_rows64(&m->cache, dt, p.cache, 4, cd, cs, cb) && map_rows64(&m->w_uk, dt, p.w_uk, 3, wd, wst, wb) &&
-           map_rows64(&m->w_uv, dt, p.w_uv, 3, wd, wst, wb) && map_rows64(&m->q, dt, p.q, 4, qd, qst, qb) &&
-           map_rows64(&m->k, dt, p.k_x, 4, kd, kst, kb) && map_rows64(&m->v, dt, p.v_x, 4, kd, kst, vb) &&
-           map_rows64(&m->rope, dt, p.rope_x, 2, rd, rst, rb);
+           map_rows64(&m->w_uv, dt, p.w_uv, 3, wd, wst, wb) && map_rows64(&m->q, dt, p.q, 4, qd, qst, qb);
 }
 
 template <int DT>
@@ -598,7 +620,8 @@ int launch_expanded_dt(const LatentParams &p, int dt, cudaStream_t s) {
     if (st) return st;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t c = latent_config(
-        dim3(p.kv_rows / kPTile, (p.heads + p.head_group - 1) / p.head_group, p.B), kExThreads, kExSmem, s, attr, 1);
+        dim3((p.kv_rows / kPTile + 1) / 2 * 2, (p.heads + p.head_group - 1) / p.head_group, p.B), kExThreads, kExSmem, s,
+        attr, 2);
     if ((st = record_launch(cudaLaunchKernelEx(&c, latent_expand_kernel<DT>, p, maps)))) return st;
     const int pairs = (p.max_q + 2 * kPTile - 1) / (2 * kPTile);
     c = latent_config(dim3(pairs * p.heads, p.B), kFaThreads, kFaSmem, s, attr, 1);
@@ -608,7 +631,18 @@ int launch_expanded_dt(const LatentParams &p, int dt, cudaStream_t s) {
 }  // namespace
 
 int launch_expanded(LatentParams &p, int dt, cudaStream_t s) {
-    p.head_group = 4;
+    // Heads per block of the expand launch: whole rounds over the SMs, a block's own cost taken as that of a head
+    // (its latent vectors are two heads' bytes of weights, fetched beside the first head's).
+    const long long tiles = (long long)p.B * ((p.kv_rows / kPTile + 1) / 2 * 2), sms = device_sm_count();
+    if (sms < 1) return SPX_ERR_CUDA;
+    long long best = 0;
+    for (int g = 1; g <= 8 && g <= p.heads; ++g) {
+        const long long blocks = tiles * ((p.heads + g - 1) / g), cost = (blocks + sms - 1) / sms * (g + 1);
+        if (!best || cost < best) {
+            best = cost;
+            p.head_group = g;
+        }
+    }
     return dt == SPX_F16 ? launch_expanded_dt<SPX_F16>(p, dt, s) : launch_expanded_dt<SPX_BF16>(p, dt, s);
 }
 

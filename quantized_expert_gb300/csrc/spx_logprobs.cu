@@ -150,14 +150,6 @@ struct LogprobSmem {
     int slow;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
     uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a)
@@ -349,7 +341,8 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
             cluster_st(to + 8, a.d);
         }
     }
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
     if (rank != 0) return;
 
     // ---- block 0: the row

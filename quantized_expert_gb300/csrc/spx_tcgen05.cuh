@@ -61,6 +61,23 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
+// The same arrival on the barrier at this address in every block of `mask`.
+__device__ __forceinline__ void umma_commit_multicast(uint64_t *bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(mask)
+        : "memory");
+}
+// A copy to the same place in every block of `mask`, counted on each block's barrier at this address.
+__device__ __forceinline__ void tma_load_3d_multicast(void *dst, const CUtensorMap *tm, int x, int y, int z,
+                                                      uint64_t *bar, uint16_t mask, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6, %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "h"(mask), "l"(policy)
+        : "memory");
+}
 // 32 lanes (this warp's quarter) x 16 consecutive 32-bit columns
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -100,6 +117,14 @@ __device__ __forceinline__ uint32_t idesc_f16_f32(int M, int N) {
 __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lead) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// A matrix in plain core matrices (8 rows of 16 bytes, contiguous; no swizzle).
+// K-major: `lead` bytes to the next 8 values of k, `stride` to the next 8 rows.
+// MN-major (a row of 16 bytes is 8 values of M or N for one k): `lead` to the
+// next 8 of k, `stride` to the next 8 of M or N.
+__device__ __forceinline__ uint64_t plain_desc(uint32_t saddr, uint32_t lead, uint32_t stride) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+           ((uint64_t)1 << 46);
 }
 // Further fields of the instruction descriptor: both operands bf16 (bits 7-9,
 // 10-12 = 1), A or B stored MN-major (bits 15, 16).
