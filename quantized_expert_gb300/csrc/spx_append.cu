@@ -25,27 +25,35 @@ struct AppendParams {
     float eps;
     const float *cos, *sin;
     int max_pos, interleaved, heads, q_width;
+    int kv_blocks, copy_blocks;
+    int64_t copies;              // units of all queries to copy (none in place)
+    FastDiv by_units, by_heads;  // units to copy per head, heads
 };
 
-// Rotation of the pairs held in 8 consecutive values x[i0 .. i0 + 8) of a
-// P-wide part; `o` are the values at the partner half when not interleaved.
-__device__ __forceinline__ void rotate8(float (&x)[8], const float (&o)[8], int i0, int P, bool inter, const float *cs,
-                                        const float *sn) {
-    if (inter) {
+// Rotation of 16 values of a 64-wide part, its units of 8 values u and u + 4
+// (u < 4), in place: both hold whole pairs in either order of the pairs.
+__device__ __forceinline__ void rotate16(float (&x)[8], float (&y)[8], int u, bool interleaved, const float *cs,
+                                         const float *sn) {
+    const int i0 = interleaved ? 4 * u : 8 * u, i1 = interleaved ? 16 + 4 * u : 8 * u + 4;
+    const float4 c0 = __ldg(reinterpret_cast<const float4 *>(cs + i0)), c1 = __ldg(reinterpret_cast<const float4 *>(cs + i1));
+    const float4 s0 = __ldg(reinterpret_cast<const float4 *>(sn + i0)), s1 = __ldg(reinterpret_cast<const float4 *>(sn + i1));
+    const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    if (interleaved) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float c = __ldg(cs + i0 / 2 + j), s = __ldg(sn + i0 / 2 + j);
-            const float a = x[2 * j], b = x[2 * j + 1];
-            x[2 * j] = a * c - b * s;
-            x[2 * j + 1] = b * c + a * s;
+            const float a = x[2 * j], b = x[2 * j + 1], d = y[2 * j], e = y[2 * j + 1];
+            x[2 * j] = a * c[j] - b * s[j];
+            x[2 * j + 1] = b * c[j] + a * s[j];
+            y[2 * j] = d * c[4 + j] - e * s[4 + j];
+            y[2 * j + 1] = e * c[4 + j] + d * s[4 + j];
         }
     } else {
-        const bool second = i0 >= P / 2;
-        const int k = second ? i0 - P / 2 : i0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float c = __ldg(cs + k + j), s = __ldg(sn + k + j);
-            x[j] = second ? x[j] * c + o[j] * s : x[j] * c - o[j] * s;
+            const float a = x[j], b = y[j];
+            x[j] = a * c[j] - b * s[j];
+            y[j] = b * c[j] + a * s[j];
         }
     }
 }
@@ -67,28 +75,26 @@ __device__ __forceinline__ void store8(uint16_t *p, const float (&x)[8]) {
                                                Elem<DT>::down2(x[4], x[5]), Elem<DT>::down2(x[6], x[7]));
 }
 
-// One warp per task: task n < N is the cache row of token n (lane l holds the
-// values 8l and, for R > 256, 256 + 8l on; lanes 0-7 then take the rotated
-// part); the others are one head of a token's queries each.
+// Blocks below kv_blocks: a warp per cache row (lane l holds the values 8l on
+// and, for R > 256, 256 + 8l on; lanes 0-3 also the rotated part).  Then the
+// queries in units of 8 values: blocks that copy, four units a thread, and
+// blocks that rotate, two units (u and u + 4 of a head's rotated part).  A warp
+// per head moved 384 bytes at a time and was bound by its instructions (8192
+// tokens 67 us); copies and rotations in one warp took turns (31 us).
+constexpr int kUnitsPerThread = 4;
 template <int DT>
-__global__ void __launch_bounds__(256) latent_append_kernel(AppendParams p) {
-    const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constant__ AppendParams p) {
     const int lane = threadIdx.x & 31;
-    const long long ntask = p.N + (p.q ? (long long)p.N * p.heads : 0);
-    if (task >= ntask) return;
-    const int n = (int)(task < p.N ? task : (task - p.N) / p.heads);
-    const int pos = __ldg(p.pos + n);
-    if (pos < 0 || (p.cos && pos >= p.max_pos)) return;
-    const float *cs = p.cos ? p.cos + (size_t)pos * (p.P / 2) : nullptr;
-    const float *sn = p.cos ? p.sin + (size_t)pos * (p.P / 2) : nullptr;
-    if (task < p.N) {
-        const int b = __ldg(p.req + n), pi = pos / p.page_size;
-        if (b < 0 || b >= p.B || pi >= p.max_pages) return;
+    if ((int)blockIdx.x < p.kv_blocks) {
+        const int n = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+        if (n >= p.N) return;
+        const int pos = __ldg(p.pos + n), b = __ldg(p.req + n), pi = pos / p.page_size;
+        if (pos < 0 || (p.cos && pos >= p.max_pos) || b < 0 || b >= p.B || pi >= p.max_pages) return;
         const int pg = __ldg(p.table + (size_t)b * p.max_pages + pi);
         if (pg < 0 || pg >= p.num_pages) return;
         const uint16_t *src = p.kv + (int64_t)n * p.kv_stride;
         uint16_t *dst = p.cache + (int64_t)pg * p.page_stride + (int64_t)(pos - pi * p.page_size) * p.token_stride;
-        float x[2][8], rot[8], oth[8], ss = 0.f;
+        float x[2][8], r0[8], r1[8], ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int c0 = 256 * i + 8 * lane;
@@ -98,9 +104,9 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendParams p) {
                 for (int j = 0; j < 8; ++j) ss = fmaf(x[i][j], x[i][j], ss);
             }
         }
-        if (lane < p.P / 8) {
-            load8<DT>(rot, src + p.R + 8 * lane);
-            load8<DT>(oth, src + p.R + (8 * lane + p.P / 2) % p.P);
+        if (lane < 4) {
+            load8<DT>(r0, src + p.R + 8 * lane);
+            load8<DT>(r1, src + p.R + 32 + 8 * lane);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -118,28 +124,48 @@ __global__ void __launch_bounds__(256) latent_append_kernel(AppendParams p) {
                 store8<DT>(dst + c0, x[i]);
             }
         }
-        if (lane < p.P / 8) {
-            if (cs) rotate8(rot, oth, 8 * lane, p.P, p.interleaved, cs, sn);
-            store8<DT>(dst + p.R + 8 * lane, rot);
+        if (lane < 4) {
+            if (p.cos) rotate16(r0, r1, lane, p.interleaved, p.cos + (size_t)pos * 32, p.sin + (size_t)pos * 32);
+            store8<DT>(dst + p.R + 8 * lane, r0);
+            store8<DT>(dst + p.R + 32 + 8 * lane, r1);
         }
         return;
     }
-    const int h = (int)((task - p.N) % p.heads);
-    const uint16_t *src = p.q + (int64_t)n * p.q_stride + (int64_t)h * p.q_width;
-    uint16_t *dst = p.q_out + (int64_t)n * p.q_out_stride + (int64_t)h * p.q_width;
-    const int r0 = p.q_width - p.P;
-    if (src != dst)
-        for (int c0 = 8 * lane; c0 < r0; c0 += 256) *reinterpret_cast<uint4 *>(dst + c0) = *reinterpret_cast<const uint4 *>(src + c0);
-    float x[8], oth[8];
-    if (lane < p.P / 8) {
-        load8<DT>(x, src + r0 + 8 * lane);
-        load8<DT>(oth, src + r0 + (8 * lane + p.P / 2) % p.P);
+    if (blockIdx.x < (unsigned)(p.kv_blocks + p.copy_blocks)) {  // copies: q_width / 8 - 8 units a head
+        const int64_t first = (int64_t)(blockIdx.x - p.kv_blocks) * (256 * kUnitsPerThread) + threadIdx.x;
+        uint4 v[kUnitsPerThread];
+        uint4 *dst[kUnitsPerThread];
+#pragma unroll
+        for (int k = 0; k < kUnitsPerThread; ++k) {
+            const int64_t i = first + 256 * k;
+            dst[k] = nullptr;
+            if (i >= p.copies) continue;
+            const int head = p.by_units((int)i), n = p.by_heads(head), h = head - n * p.heads;  // of all heads; token
+            const int at = 8 * ((int)i - head * p.by_units.d), pos = __ldg(p.pos + n);
+            if (pos < 0 || (p.cos && pos >= p.max_pos)) continue;
+            dst[k] = reinterpret_cast<uint4 *>(p.q_out + (int64_t)n * p.q_out_stride + (int64_t)h * p.q_width + at);
+            v[k] = *reinterpret_cast<const uint4 *>(p.q + (int64_t)n * p.q_stride + (int64_t)h * p.q_width + at);
+        }
+#pragma unroll
+        for (int k = 0; k < kUnitsPerThread; ++k)
+            if (dst[k]) *dst[k] = v[k];
+        return;
     }
-    __syncwarp();  // in place: every lane's loads before any lane's store
-    if (lane < p.P / 8) {
-        if (cs) rotate8(x, oth, 8 * lane, p.P, p.interleaved, cs, sn);
-        store8<DT>(dst + r0 + 8 * lane, x);
-    }
+    // rotations: 4 a head
+    const int64_t i = (int64_t)(blockIdx.x - p.kv_blocks - p.copy_blocks) * 256 + threadIdx.x;
+    const int head = (int)(i >> 2), u = (int)i & 3, n = p.by_heads(head), h = head - n * p.heads;
+    if (n >= p.N) return;
+    const int pos = __ldg(p.pos + n);
+    if (pos < 0 || (p.cos && pos >= p.max_pos)) return;
+    const int at = p.q_width - 64 + 8 * u;
+    const uint16_t *src = p.q + (int64_t)n * p.q_stride + (int64_t)h * p.q_width + at;
+    uint16_t *dst = p.q_out + (int64_t)n * p.q_out_stride + (int64_t)h * p.q_width + at;
+    float x[8], y[8];
+    load8<DT>(x, src);
+    load8<DT>(y, src + 32);
+    if (p.cos) rotate16(x, y, u, p.interleaved, p.cos + (size_t)pos * 32, p.sin + (size_t)pos * 32);
+    store8<DT>(dst, x);
+    store8<DT>(dst + 32, y);
 }
 
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -168,8 +194,13 @@ extern "C" int spx_latent_append(const spx_latent_append_args *a, spx_stream_t s
             return SPX_ERR_INVALID_ARG;
         if (a->q == a->q_out && a->q_stride != a->q_out_stride) return SPX_ERR_INVALID_ARG;
     }
-    const long long tasks = (long long)a->N * (a->q ? 1 + a->heads : 1), blocks = (tasks + 7) / 8;
-    if (blocks > 0x7fffffffll) return SPX_ERR_UNSUPPORTED;
+    // in place only the rotated parts move
+    const int per_head = a->q && a->q != a->q_out ? (a->q_width - c.P) / 8 : 0;
+    const long long heads = a->q ? (long long)a->N * a->heads : 0, copies = heads * per_head;
+    if (copies > 0x7ffffffell || heads > 0x1fffffffll) return SPX_ERR_UNSUPPORTED;
+    const long long kv_blocks = ((long long)a->N + 7) / 8;
+    const long long copy_blocks = (copies + 256 * kUnitsPerThread - 1) / (256 * kUnitsPerThread);
+    const long long blocks = kv_blocks + copy_blocks + (4 * heads + 255) / 256;
     AppendParams p{};
     p.cache = static_cast<uint16_t *>(c.cache);
     p.page_stride = c.page_stride;
@@ -198,6 +229,11 @@ extern "C" int spx_latent_append(const spx_latent_append_args *a, spx_stream_t s
     p.interleaved = a->interleaved;
     p.heads = a->heads;
     p.q_width = a->q_width;
+    p.kv_blocks = (int)kv_blocks;
+    p.copy_blocks = (int)copy_blocks;
+    p.copies = copies;
+    p.by_units.set(per_head ? per_head : 1);
+    p.by_heads.set(a->q ? a->heads : 1);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (c.dtype == SPX_F16)
         latent_append_kernel<SPX_F16><<<(unsigned)blocks, 256, 0, s>>>(p);
