@@ -362,7 +362,19 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
         Slot<RR> rs;
         ps.i = warp;
         bool ok = true, waited = !p.chained;
+        auto queries = [&]() {  // the unit's, once the last unit's have been read
+            if (!(ok = ctl_wait(&m.qempty, (seg & 1) ^ 1, ctl))) return;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&m.qfull, (uint32_t)(2 * np + 1) * NR * 128);
+                tma_load_3d(qs, &maps.q, 0, w.rq.row0 * p.heads + NR * w.g, 0, &m.qfull, pol);
+            }
+            __syncwarp();
+        };
         for (w.begin(p, m); ok && warp < np && w.left > 0; w.next(p), ++seg) {
+            // Queries that no launch of this call writes come first in the block; the others, and those of
+            // later units, behind the unit's first two tiles, which find room without the queries' products.
+            const bool ahead = !p.chained && seg == 0;
+            if (warp == 0 && ahead) queries();
             const int32_t *tab = p.table + (size_t)w.b * p.max_pages;
             int box = 32, my_page = 0, my_at = 0;  // this lane's box of the 32 looked up together
 #pragma unroll 1
@@ -397,19 +409,13 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                 __syncwarp();
                 ps.advance(np);
                 rs.next();
-                if (warp == 0 && i == min(w.tile + 1, w.end - 1)) {
-                    // the unit's queries, behind its first two tiles (which need no earlier launch of the call
-                    // and find room without the queries' products)
+                if (warp == 0 && !ahead && i == min(w.tile + 1, w.end - 1)) {
                     if (!waited) {
                         griddep_wait();
                         waited = true;
                     }
-                    if (!(ok = ctl_wait(&m.qempty, (seg & 1) ^ 1, ctl))) break;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&m.qfull, (uint32_t)(2 * np + 1) * NR * 128);
-                        tma_load_3d(qs, &maps.q, 0, w.rq.row0 * p.heads + NR * w.g, 0, &m.qfull, pol);
-                    }
-                    __syncwarp();
+                    queries();
+                    if (!ok) break;
                 }
             }
         }
@@ -433,6 +439,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
             uint64_t since = 0;
 #pragma unroll 1
             while (to < t1) {
+                const bool room = ts < t1 && ts - to < 2;
                 if (to < ts && mbar_test(&m.wfull[to & 1], (to >> 1) & 1) && (to != t0 || mbar_test(&m.ofree, (seg & 1) ^ 1))) {
                     tc_fence_after();
                     if (elect_one()) {
@@ -454,7 +461,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     orp.next();
                     ++to;
                     since = 0;
-                } else if (ts < t1 && ts - to < 2 && mbar_test(&m.full[ts & 3], (ts >> 2) & 1)) {
+                } else if (room && mbar_test(&m.full[ts & 3], (ts >> 2) & 1)) {
                     tc_fence_after();
                     const uint32_t sd = tmem + s_col + (ts & 1) * NR;
                     if (elect_one()) {
@@ -515,16 +522,19 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
         for (w.begin(p, m); w.left > 0; w.next(p)) {
             const int rows = min(NR, w.rq.T * p.heads - NR * w.g), n16 = (rows + 15) & ~15;
             const int row0 = NR * w.g;
-            bar_sync(3, 128 * SH);  // the last unit's limits and sums are read
+            bar_sync(7, 128 * SH);  // the last unit's limits and sums are read
             if (all < NR) m.lim[all] = all < rows ? latent_limit(p, w.rq, p.by_heads(row0 + all)) : 0;
-            bar_sync(3, 128 * SH);
+            bar_sync(7, 128 * SH);
             const int lim_lo = m.lim[0], lim_hi = m.lim[rows - 1];
-            float mr[2 * NB], l[2 * NB];
+            // References less kShift, and sums of weights, of this lane's rows (in pairs).  A row that has seen
+            // nothing has a reference below every score.
+            constexpr float kNone = -3e38f;
+            float ref[2 * NB];
+            uint64_t l2[NB];
 #pragma unroll
-            for (int c = 0; c < 2 * NB; ++c) {
-                mr[c] = -INFINITY;
-                l[c] = 0.f;
-            }
+            for (int c = 0; c < 2 * NB; ++c) ref[c] = kNone;
+#pragma unroll
+            for (int x = 0; x < NB; ++x) l2[x] = 0;
 #pragma unroll 1
             for (int i = w.tile; i < w.end; ++i, ++tc, rs.next(), ps.advance(np)) {
                 ctl_wait(&m.sfull[tc & 1], (tc >> 1) & 1, ctl);
@@ -536,49 +546,81 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                 tmem_wait_ld();
                 const int p0 = kTile * i;
                 const bool masked = p0 + kTile > lim_lo;
-                float mx[2 * NB];
+                // exponents of the weights by the present references
+                uint64_t w2[2 * NB];
+                const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+                auto exponents = [&]() {
 #pragma unroll
-                for (int x = 0; x < NB; ++x) {
+                    for (int x = 0; x < NB; ++x) {
+                        const uint64_t minus = pack2(-ref[2 * x], -ref[2 * x + 1]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) r[4 * x + e] = __float_as_uint(__uint_as_float(r[4 * x + e]) * p.scale_log2);
-                    if (masked || c0 + NC > n16) {
-                        const int2 lim = *reinterpret_cast<const int2 *>(&m.lim[8 * x + cl]);
+                        for (int k = 0; k < 2; ++k)
+                            w2[2 * x + k] = fma2(pack2(__uint_as_float(r[4 * x + 2 * k]), __uint_as_float(r[4 * x + 2 * k + 1])),
+                                                 scale2, minus);
+                        if (masked || c0 + NC > n16) {
+                            const int2 lim = *reinterpret_cast<const int2 *>(&m.lim[8 * x + cl]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (p0 + tok + 8 * (e >> 1) >= (e & 1 ? lim.y : lim.x)) r[4 * x + e] = 0xFF800000u;
+                            for (int k = 0; k < 2; ++k) {
+                                float2 v = unpack2(w2[2 * x + k]);
+                                if (p0 + tok + 8 * k >= lim.x) v.x = -INFINITY;
+                                if (p0 + tok + 8 * k >= lim.y) v.y = -INFINITY;
+                                w2[2 * x + k] = pack2(v.x, v.y);
+                            }
+                        }
                     }
-                    mx[2 * x] = fmaxf(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 2]));
-                    mx[2 * x + 1] = fmaxf(__uint_as_float(r[4 * x + 1]), __uint_as_float(r[4 * x + 3]));
+                };
+                exponents();
+                float most = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < 2 * NB; ++x) {
+                    const float2 v = unpack2(w2[x]);
+                    most = fmaxf(most, fmaxf(v.x, v.y));
                 }
+                // A barrier that carries one bit: the products keep shared memory busy, and an exchange of the
+                // maxima through it took longer than all the rest.  Only a rise beyond the slack needs one.
+                if (bar_any(1 + sh, 128, most > kSlack + kShift)) {
+                    float(*red)[64] = m.red[tc & 1];
+                    float mx[2 * NB];
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-                    for (int c = 0; c < 2 * NB; ++c) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
-                float(*red)[64] = m.red[tc & 1];
-                if (lane < 4)
-#pragma unroll
-                    for (int x = 0; x < NB; ++x)
-                        *reinterpret_cast<float2 *>(&red[q][8 * x + cl]) = make_float2(mx[2 * x], mx[2 * x + 1]);
-                bar_sync(1 + sh, 128);
-                bool rise = false;
-#pragma unroll
-                for (int x = 0; x < NB; ++x) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 v = *reinterpret_cast<const float2 *>(&red[k][8 * x + cl]);
-                        mx[2 * x] = fmaxf(mx[2 * x], v.x);
-                        mx[2 * x + 1] = fmaxf(mx[2 * x + 1], v.y);
+                    for (int x = 0; x < NB; ++x) {
+                        const float2 u = unpack2(w2[2 * x]), v = unpack2(w2[2 * x + 1]);
+                        // the larger of the two scores that the row sees
+                        const float a0 = u.x == -INFINITY ? -INFINITY : __uint_as_float(r[4 * x]) * p.scale_log2;
+                        const float a1 = u.y == -INFINITY ? -INFINITY : __uint_as_float(r[4 * x + 1]) * p.scale_log2;
+                        const float b0 = v.x == -INFINITY ? -INFINITY : __uint_as_float(r[4 * x + 2]) * p.scale_log2;
+                        const float b1 = v.y == -INFINITY ? -INFINITY : __uint_as_float(r[4 * x + 3]) * p.scale_log2;
+                        mx[2 * x] = fmaxf(a0, b0);
+                        mx[2 * x + 1] = fmaxf(a1, b1);
                     }
-                    rise |= mx[2 * x] > mr[2 * x] + kSlack || mx[2 * x + 1] > mr[2 * x + 1] + kSlack;
-                }
-                if (__any_sync(0xffffffffu, rise)) {  // the same in the share's four warps
 #pragma unroll
-                    for (int c = 0; c < 2 * NB; ++c) {
-                        const float mn = fmaxf(mr[c], mx[c]);
-                        const float f = mn == mr[c] ? 1.f : ex2(mr[c] - mn);
-                        mr[c] = mn;
-                        l[c] *= f;
-                        if (q == 0 && lane < 4) m.fac[8 * (c >> 1) + cl + (c & 1)] = f;
+                    for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                        for (int c = 0; c < 2 * NB; ++c) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
+                    if (lane < 4)
+#pragma unroll
+                        for (int x = 0; x < NB; ++x)
+                            *reinterpret_cast<float2 *>(&red[q][8 * x + cl]) = make_float2(mx[2 * x], mx[2 * x + 1]);
+                    bar_sync(1 + sh, 128);
+#pragma unroll
+                    for (int x = 0; x < NB; ++x) {
+                        float f[2];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 v = *reinterpret_cast<const float2 *>(&red[k][8 * x + cl]);
+                            mx[2 * x] = fmaxf(mx[2 * x], v.x);
+                            mx[2 * x + 1] = fmaxf(mx[2 * x + 1], v.y);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float now = mx[2 * x + k] - kShift;
+                            f[k] = 1.f;
+                            if (now > ref[2 * x + k] + kSlack) {
+                                f[k] = ex2(ref[2 * x + k] - now);
+                                ref[2 * x + k] = now;
+                            }
+                        }
+                        l2[x] = mul2(l2[x], pack2(f[0], f[1]));
+                        if (q == 0 && lane < 4) *reinterpret_cast<float2 *>(&m.fac[8 * x + cl]) = make_float2(f[0], f[1]);
                     }
                     if (i > w.tile) {
                         bar_sync(1 + sh, 128);
@@ -599,26 +641,23 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                         tmem_wait_st();
                         tc_fence_before();
                     }
+                    exponents();
                 }
 #pragma unroll
-                for (int x = 0; x < NB; ++x)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const float ref = mr[2 * x + f] == -INFINITY ? 0.f : mr[2 * x + f] - kShift;
-                        const float v = ex2(__uint_as_float(r[4 * x + f]) - ref);
-                        const float y = ex2(__uint_as_float(r[4 * x + 2 + f]) - ref);
-                        l[2 * x + f] += v + y;
-                        r[4 * x + f] = __float_as_uint(v);
-                        r[4 * x + 2 + f] = __float_as_uint(y);
-                    }
+                for (int x = 0; x < 2 * NB; ++x) {
+                    const float2 v = unpack2(w2[x]);
+                    w2[x] = pack2(ex2(v.x), ex2(v.y));
+                    l2[x >> 1] = add2(l2[x >> 1], w2[x]);
+                }
                 uint8_t *wt = ropes + rs.i * kRopeBytes;
 #pragma unroll
                 for (int x = 0; x < NB; ++x)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int t = tok + 8 * k;
+                        const float2 v = unpack2(w2[2 * x + k]);
                         *reinterpret_cast<uint32_t *>(wt + t * 128 + 16 * ((x + c0 / 8) ^ (t & 7)) + 4 * (lane & 3)) =
-                            Elem<DT>::down2(__uint_as_float(r[4 * x + 2 * k]), __uint_as_float(r[4 * x + 2 * k + 1]));
+                            Elem<DT>::down2(v.x, v.y);
                     }
                 if (masked) {
                     // What some row may not see has weight 0 there, and 0 times an infinity or a NaN would
@@ -666,6 +705,13 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     make_int4((int)blockIdx.x, (w.flat + w.nt - 1) / m.share, slot, whole);
             float(*red)[64] = m.red[tc & 1];
             long long *at = reinterpret_cast<long long *>(m.red[(tc & 1) ^ 1]);
+            float l[2 * NB];
+#pragma unroll
+            for (int x = 0; x < NB; ++x) {
+                const float2 v = unpack2(l2[x]);
+                l[2 * x] = v.x;
+                l[2 * x + 1] = v.y;
+            }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
@@ -675,9 +721,9 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                 for (int c = 0; c < 2 * NB; ++c) {
                     const int col = 8 * (c >> 1) + cl + (c & 1);
                     red[q][col] = l[c];
-                    if (q == 0) m.fac[col] = mr[c];
+                    if (q == 0) m.fac[col] = ref[c] == kNone ? -INFINITY : ref[c] + kShift;
                 }
-            bar_sync(3, 128 * SH);
+            bar_sync(7, 128 * SH);
             const bool direct = whole && !p.w_uv;
             const long long first_row = (long long)w.rq.row0 * p.heads + row0;
             if (all < rows) {
@@ -692,7 +738,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                 }
                 if (direct) at[all] = row / p.heads * p.out_stride + row % p.heads * p.R;
             }
-            bar_sync(3, 128 * SH);
+            bar_sync(7, 128 * SH);
             float *dst = whole ? p.o_lat + first_row * p.R : p.part + (size_t)slot * NR * p.R;
 #pragma unroll 1
             for (int x = c0; x < min(c0 + NC, n16); x += 16) {
@@ -854,7 +900,7 @@ __device__ __forceinline__ void join_sums(const LatentParams &p, const RowSums<R
 #pragma unroll
     for (int q = 0; q < kShareChunks; ++q) {
         if (32 * q >= most) break;
-#pragma unroll(RW == 1 ? 8 : 2)
+#pragma unroll 2
         for (int k = 0; k < min(most - 32 * q, 32); k += step) {
             float4 v[RW];
             float g[RW];

@@ -157,6 +157,19 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// The same with every thread told whether any of them brought a true `pred`.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool pred) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(threads), "r"((uint32_t)pred)
+        : "memory");
+    return any != 0;
+}
 // One lane of a converged warp, the same every time.  Products issued under it
 // (rather than under lane == 0) keep their descriptors in uniform registers:
 // 128 x 16 x 16 products then take 39 cycles each instead of 47, 64 x 16 x 16
