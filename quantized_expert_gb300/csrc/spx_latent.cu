@@ -1072,15 +1072,17 @@ __global__ void __launch_bounds__(512, 1) latent_out_kernel(const __grid_constan
 }
 
 // Folded weights: one block per row joins its partial sums, 4 columns a thread
-// and four threads a column; rows of whole units are there already.
-template <int DT>
-__global__ void __launch_bounds__(512, 2) latent_join_kernel(const __grid_constant__ LatentParams p) {
-    __shared__ float4 spread[3][128];
+// and SUB threads a column; rows of whole units are there already.  SUB = 4
+// shortens the sums of few rows, 1 leaves room for more blocks (4096 rows of 3
+// shares: 25 us with 4).
+template <int DT, int SUB>
+__global__ void __launch_bounds__(128 * SUB) latent_join_kernel(const __grid_constant__ LatentParams p) {
+    __shared__ float4 spread[SUB][128];
     __shared__ RowCard card;
     griddep_wait();
     griddep_launch_dependents();
     const int row = blockIdx.x, n[1] = {p.by_heads(row)}, h = row - n[0] * p.heads, lane = threadIdx.x & 31;
-    const int sub = threadIdx.x >> 7, d4 = 4 * (threadIdx.x & 127);
+    const int sub = threadIdx.x >> 7, col = threadIdx.x & 127, d4 = 4 * col;
     RowSums<1> rs;
     if (threadIdx.x < 32) {
         find_rows<1>(p, n, h, lane, rs);
@@ -1090,19 +1092,22 @@ __global__ void __launch_bounds__(512, 2) latent_join_kernel(const __grid_consta
     if (card.whole || !card.owned) return;
     card.get(rs, lane);
     float4 a[1] = {make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (d4 < p.R) join_sums<1>(p, rs, sub, 4, d4, a);
-    if (sub) spread[sub - 1][threadIdx.x & 127] = a[0];
-    __syncthreads();
-    if (sub || d4 >= p.R) return;
-    for (int k = 0; k < 3; ++k) {
-        const float4 v = spread[k][threadIdx.x];
-        a[0].x += v.x;
-        a[0].y += v.y;
-        a[0].z += v.z;
-        a[0].w += v.w;
+    if (d4 < p.R) join_sums<1>(p, rs, sub, SUB, d4, a);
+    if (SUB > 1) {
+        spread[sub][col] = a[0];
+        __syncthreads();
+        if (sub) return;
+        for (int k = 1; k < SUB; ++k) {
+            const float4 v = spread[k][col];
+            a[0].x += v.x;
+            a[0].y += v.y;
+            a[0].z += v.z;
+            a[0].w += v.w;
+        }
     }
-    *reinterpret_cast<uint2 *>(p.out + n[0] * p.out_stride + (size_t)h * p.R + d4) =
-        make_uint2(Elem<DT>::down2(a[0].x, a[0].y), Elem<DT>::down2(a[0].z, a[0].w));
+    if (d4 < p.R)
+        *reinterpret_cast<uint2 *>(p.out + n[0] * p.out_stride + (size_t)h * p.R + d4) =
+            make_uint2(Elem<DT>::down2(a[0].x, a[0].y), Elem<DT>::down2(a[0].z, a[0].w));
     if (threadIdx.x == 0 && p.lse) p.lse[row] = rs.lse[0];
 }
 
@@ -1175,8 +1180,10 @@ int launch_absorbed(LatentParams &p, int dtype, bool packed, cudaStream_t s) {
     if (st) return st;
     if (p.w_uv) return token_tiles(p.N) == 1 ? launch_out_mt<DT, 1>(p, s) : launch_out_mt<DT, 4>(p, s);
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t c = latent_config(dim3(p.N * p.heads), 512, 0, s, attr, 1);
-    return record_launch(cudaLaunchKernelEx(&c, latent_join_kernel<DT>, p));
+    const int sub = p.N * p.heads <= 4 * sms ? 4 : 1;
+    cudaLaunchConfig_t c = latent_config(dim3(p.N * p.heads), 128 * sub, 0, s, attr, 1);
+    return record_launch(sub == 4 ? cudaLaunchKernelEx(&c, latent_join_kernel<DT, 4>, p)
+                                  : cudaLaunchKernelEx(&c, latent_join_kernel<DT, 1>, p));
 }
 
 // Rows per unit: the call's largest request in one unit where 16 or 32 rows
