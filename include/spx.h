@@ -567,7 +567,7 @@ SPX_API int spx_latent_append(const spx_latent_append_args *args, spx_stream_t s
  * verify calls); SPX_LATENT_EXPANDED writes every head's keys and values to the
  * workspace and attends per head with (R + P + R) / (dn + P + dv) times fewer
  * operations per query-key pair (prompts; needs the weights with dn = dv =
- * 128); SPX_LATENT_AUTO chooses by max_q.  max_q and max_len bound every
+ * 128); SPX_LATENT_AUTO chooses by B, max_q, max_len and heads.  max_q and max_len bound every
  * request's rows and length (larger ones are cut to them).
  * Roundings to the type: q W_uk, the softmax weights, and in the expanded form
  * keys and values. */
@@ -593,8 +593,9 @@ typedef struct {
 } spx_latent_args;
 SPX_API int spx_latent_attention(const spx_latent_args *args, spx_stream_t stream);
 /* Workspace of a call with B requests, N query rows (sum over the requests), at
- * most max_q rows and max_len cached tokens each; 0 if unsupported.  A larger
- * workspace serves smaller calls.  Its status word (spx_workspace_status) is
+ * most max_q rows and max_len cached tokens each, in the form that such a call
+ * takes; 0 if unsupported.  Any larger workspace serves too (a program takes the
+ * largest over its calls).  Its status word (spx_workspace_status) is
  * SPX_ERR_TIMEOUT after a bounded wait that gave up. */
 SPX_API size_t spx_latent_workspace_size(int B, int N, int max_q, int max_len, int heads, int R, int P, int dn, int dv,
                                          int form);

@@ -935,67 +935,59 @@ __device__ __forceinline__ float2 cluster_ld2(const void *p, uint32_t rank) {
     return v;
 }
 
-// Cluster of R / 64 blocks per (head h, 16 MT tokens): block s joins the
-// partial sums of latent columns 64 s .. + 63, multiplies them by that slice of
-// W_uv[h] and the cluster adds the slices up.  The joined sums enter the
-// product as two values of the type (v and what its rounding left), which
-// costs nothing here and saves a rounding.
-template <int DT, int MT>
-__global__ void __launch_bounds__(512, 1) latent_out_kernel(const __grid_constant__ LatentParams p) {
+// Cluster of R / 64 blocks per (head h, 16 MT tokens): block s multiplies the
+// joined sums of latent columns 64 s .. + 63 by that slice of W_uv[h] and the
+// cluster adds the slices up.  The joined sums enter the product as two values
+// of the type (v and what its rounding left), which costs nothing here and
+// saves a rounding.  With JOIN (few tokens, MT = 1) the block joins them
+// itself, else they are in o_lat.
+template <int DT, int MT, bool JOIN>
+__global__ void __launch_bounds__(JOIN ? 512 : 256, JOIN ? 1 : 3) latent_out_kernel(const __grid_constant__ LatentParams p) {
+    static_assert(!JOIN || MT == 1, "a row per warp at least");
+    constexpr int kThreads = JOIN ? 512 : 256;
     extern __shared__ __align__(128) uint8_t lo_smem[];
     uint16_t *wv = reinterpret_cast<uint16_t *>(lo_smem);          // [dv][72]
     uint16_t *hi = wv + p.dv * 72, *lo = hi + 16 * MT * 72;        // [16 MT][72] each
     float *part = reinterpret_cast<float *>(lo + 16 * MT * 72);    // [16 MT][dv]
-    __shared__ float4 spread[16][16];
     const int s = blockIdx.x, h = blockIdx.y, n0 = blockIdx.z * 16 * MT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = min(16 * MT, p.N - n0);
     griddep_wait();
     griddep_launch_dependents();
     const uint16_t *wsrc = p.w_uv + (size_t)h * p.dv * p.R + 64 * s;
-    for (int i = threadIdx.x; i < p.dv * 8; i += 512)
+    for (int i = threadIdx.x; i < p.dv * 8; i += kThreads)
         cp_async16(wv + (i >> 3) * 72 + 8 * (i & 7), wsrc + (size_t)(i >> 3) * p.R + 8 * (i & 7));
-    if (rows < 16 * MT) {  // rows past the last token
-        for (int i = rows * 9 + threadIdx.x; i < 16 * MT * 9; i += 512)
-            reinterpret_cast<uint4 *>(hi)[i] = reinterpret_cast<uint4 *>(lo)[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-    }
-    // 16 warps: MT rows each, or with few rows several warps (and always both halves) for one
-    const int wp = MT > 1 || rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;
-    const int sub = warp % wp, half = lane >> 4, d4 = 4 * (lane & 15);
-    int n[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) n[i] = warp / wp + 16 * i < rows ? n0 + warp / wp + 16 * i : -1;
-    RowSums<MT> rs;
-    if (MT == 1) {
+    for (int i = rows * 9 + threadIdx.x; i < 16 * MT * 9; i += kThreads)  // rows past the last token
+        reinterpret_cast<uint4 *>(hi)[i] = reinterpret_cast<uint4 *>(lo)[i] = make_uint4(0, 0, 0, 0);
+    const int half = lane >> 4, d4 = 4 * (lane & 15);
+    auto put = [&](int r, const float4 &a) {
+        const uint2 v = make_uint2(Elem<DT>::down2(a.x, a.y), Elem<DT>::down2(a.z, a.w));
+        const float2 y = Elem<DT>::up2(v.x), z = Elem<DT>::up2(v.y);
+        *reinterpret_cast<uint2 *>(hi + r * 72 + d4) = v;
+        *reinterpret_cast<uint2 *>(lo + r * 72 + d4) =
+            make_uint2(Elem<DT>::down2(a.x - y.x, a.y - y.y), Elem<DT>::down2(a.z - z.x, a.w - z.y));
+    };
+    if constexpr (JOIN) {
+        __shared__ float4 spread[16][16];
         __shared__ RowCard cards[16];
+        // 16 warps: a row each, or with few rows several warps (and always both halves) for one
+        const int wp = rows > 8 ? 1 : rows > 4 ? 2 : rows > 2 ? 4 : rows > 1 ? 8 : 16;
+        const int sub = warp % wp, r = warp / wp;
+        RowSums<1> rs;
         if (warp < rows) {
-            const int one[1] = {n0 + warp};
-            RowSums<1> r;
-            find_rows<1>(p, one, h, lane, r);
-            cards[warp].put(r, lane);
-            if (r.owned[0] && !r.whole[0] && s == 0 && lane == 0 && p.lse)
-                p.lse[(size_t)one[0] * p.heads + h] = r.lse[0];
+            const int n[1] = {n0 + warp};
+            find_rows<1>(p, n, h, lane, rs);
+            cards[warp].put(rs, lane);
+            if (rs.owned[0] && !rs.whole[0] && s == 0 && lane == 0 && p.lse) p.lse[(size_t)n[0] * p.heads + h] = rs.lse[0];
         }
         __syncthreads();
-        cards[min(warp / wp, rows - 1)].get(reinterpret_cast<RowSums<1> &>(rs), lane);
-        if (n[0] < 0) rs.n[0] = rs.whole[0] = 0;
-    } else {
-        find_rows<MT>(p, n, h, lane, rs);
-    }
-    float4 sum[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const size_t row = (size_t)n[i] * p.heads + h;
-        if (rs.whole[i] && sub == 0 && half == 0)
-            sum[i] = __ldcg(reinterpret_cast<const float4 *>(p.o_lat + row * p.R + 64 * s + d4));
-        if (MT > 1 && rs.owned[i] && !rs.whole[i] && s == 0 && lane == 0 && p.lse) p.lse[row] = rs.lse[i];
-    }
-    join_sums<MT>(p, rs, 2 * sub + half, 2 * wp, 64 * s + d4, sum);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        float4 a = sum[i];
+        cards[min(r, rows - 1)].get(rs, lane);
+        if (r >= rows) rs.n[0] = rs.whole[0] = 0;
+        float4 sum[1] = {make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (rs.whole[0] && sub == 0 && half == 0)
+            sum[0] = __ldcg(reinterpret_cast<const float4 *>(p.o_lat + ((size_t)(n0 + r) * p.heads + h) * p.R + 64 * s + d4));
+        join_sums<1>(p, rs, 2 * sub + half, 2 * wp, 64 * s + d4, sum);
+        float4 a = sum[0];
         a.x += __shfl_xor_sync(0xffffffffu, a.x, 16);
         a.y += __shfl_xor_sync(0xffffffffu, a.y, 16);
         a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);
@@ -1012,48 +1004,52 @@ __global__ void __launch_bounds__(512, 1) latent_out_kernel(const __grid_constan
                     a.w += v.w;
                 }
         }
-        if (sub == 0 && half == 0 && n[i] >= 0) {
-            const int r = n[i] - n0;
-            const uint2 v = make_uint2(Elem<DT>::down2(a.x, a.y), Elem<DT>::down2(a.z, a.w));
-            const float2 y = Elem<DT>::up2(v.x), z = Elem<DT>::up2(v.y);
-            *reinterpret_cast<uint2 *>(hi + r * 72 + d4) = v;
-            *reinterpret_cast<uint2 *>(lo + r * 72 + d4) =
-                make_uint2(Elem<DT>::down2(a.x - y.x, a.y - y.y), Elem<DT>::down2(a.z - z.x, a.w - z.y));
+        if (sub == 0 && half == 0 && r < rows) put(r, a);
+    } else {
+        float4 a[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int r = 16 * i + 2 * warp + half;
+            a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows)
+                a[i] = __ldcg(reinterpret_cast<const float4 *>(p.o_lat + ((size_t)(n0 + r) * p.heads + h) * p.R + 64 * s + d4));
         }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            if (16 * i + 2 * warp + half < rows) put(16 * i + 2 * warp + half, a[i]);
     }
     cp_async_wait_all();
     __syncthreads();
-    const int v0 = 16 * (warp & 7), m0 = MT / 2 * (warp >> 3);  // with 4 m-tiles, half of them a warp
-    if (v0 < p.dv && (MT > 1 || warp < 8)) {
-        constexpr int MW = MT > 1 ? MT / 2 : 1;
-        float acc[MW][2][4] = {};
+    const int v0 = 16 * warp;
+    if (v0 < p.dv) {
+        float acc[MT][2][4] = {};
 #pragma unroll
         for (int k = 0; k < 64; k += 16) {
             uint32_t b[4];
             ldsm4(b, wv + (v0 + (lane & 7) + 8 * (lane >> 4)) * 72 + k + 8 * ((lane >> 3) & 1));
 #pragma unroll
-            for (int m = 0; m < MW; ++m) {
+            for (int m = 0; m < MT; ++m) {
                 uint32_t a[4];
-                ldsm4(a, hi + (16 * (m0 + m) + (lane & 15)) * 72 + k + 8 * (lane >> 4));
+                ldsm4(a, hi + (16 * m + (lane & 15)) * 72 + k + 8 * (lane >> 4));
                 mma16816<DT>(acc[m][0], a, b[0], b[1]);
                 mma16816<DT>(acc[m][1], a, b[2], b[3]);
-                ldsm4(a, lo + (16 * (m0 + m) + (lane & 15)) * 72 + k + 8 * (lane >> 4));
+                ldsm4(a, lo + (16 * m + (lane & 15)) * 72 + k + 8 * (lane >> 4));
                 mma16816<DT>(acc[m][0], a, b[0], b[1]);
                 mma16816<DT>(acc[m][1], a, b[2], b[3]);
             }
         }
 #pragma unroll
-        for (int m = 0; m < MW; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<float2 *>(part + (16 * (m0 + m) + (lane >> 2) + 8 * (j & 1)) * p.dv + v0 + 8 * (j >> 1) +
+                *reinterpret_cast<float2 *>(part + (16 * m + (lane >> 2) + 8 * (j & 1)) * p.dv + v0 + 8 * (j >> 1) +
                                             2 * (lane & 3)) =
                     make_float2(acc[m][j >> 1][2 * (j & 1)], acc[m][j >> 1][2 * (j & 1) + 1]);
     }
     cluster_arrive();
     cluster_wait();
     const int ns = p.R / 64, dv_log2 = p.dv == 128 ? 7 : 6, pairs = rows << (dv_log2 - 1);
-    for (int i = (int)cluster_rank() * 512 + threadIdx.x; i < pairs; i += ns * 512) {
+    for (int i = (int)cluster_rank() * kThreads + threadIdx.x; i < pairs; i += ns * kThreads) {
         float2 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = k < ns ? cluster_ld2(part + 2 * i, (uint32_t)k) : make_float2(0.f, 0.f);
@@ -1071,8 +1067,9 @@ __global__ void __launch_bounds__(512, 1) latent_out_kernel(const __grid_constan
     cluster_wait();
 }
 
-// Folded weights: one block per row joins its partial sums, 4 columns a thread
-// and SUB threads a column; rows of whole units are there already.  SUB = 4
+// Folded weights, and many tokens: one block per row joins its partial sums, 4
+// columns a thread and SUB threads a column, into out or (fp32, for the product
+// that follows) o_lat; rows of whole units are there already.  SUB = 4
 // shortens the sums of few rows, 1 leaves room for more blocks (4096 rows of 3
 // shares: 25 us with 4).
 template <int DT, int SUB>
@@ -1089,7 +1086,7 @@ __global__ void __launch_bounds__(128 * SUB) latent_join_kernel(const __grid_con
         card.put(rs, lane);
     }
     __syncthreads();
-    if (card.whole || !card.owned) return;
+    if (card.whole || (!card.owned && !p.w_uv)) return;
     card.get(rs, lane);
     float4 a[1] = {make_float4(0.f, 0.f, 0.f, 0.f)};
     if (d4 < p.R) join_sums<1>(p, rs, sub, SUB, d4, a);
@@ -1105,10 +1102,14 @@ __global__ void __launch_bounds__(128 * SUB) latent_join_kernel(const __grid_con
             a[0].w += v.w;
         }
     }
-    if (d4 < p.R)
-        *reinterpret_cast<uint2 *>(p.out + n[0] * p.out_stride + (size_t)h * p.R + d4) =
-            make_uint2(Elem<DT>::down2(a[0].x, a[0].y), Elem<DT>::down2(a[0].z, a[0].w));
-    if (threadIdx.x == 0 && p.lse) p.lse[row] = rs.lse[0];
+    if (d4 < p.R) {
+        if (p.w_uv)
+            *reinterpret_cast<float4 *>(p.o_lat + (size_t)row * p.R + d4) = a[0];
+        else
+            *reinterpret_cast<uint2 *>(p.out + n[0] * p.out_stride + (size_t)h * p.R + d4) =
+                make_uint2(Elem<DT>::down2(a[0].x, a[0].y), Elem<DT>::down2(a[0].z, a[0].w));
+    }
+    if (threadIdx.x == 0 && p.lse && rs.owned[0]) p.lse[row] = rs.lse[0];
 }
 
 // -------------------------------------------------------------------- host --
@@ -1133,9 +1134,9 @@ int launch_attn(const LatentParams &p, const AttnMaps &maps, int blocks, cudaStr
     return record_launch(cudaLaunchKernelEx(&c, latent_attn_kernel<DT, NR>, p, maps));
 }
 
-// Tokens per block of the products with the up-projections: 64 once there are
-// enough of them to fill the SMs (16 heads x 8 slices of blocks per group).
-int token_tiles(int N) { return N > 64 ? 4 : 1; }
+// Tokens per block of the products with the up-projections, in sixteens: 64 once
+// there are enough of them to fill the SMs (heads x R / 64 blocks per group).
+int token_tiles(int N) { return N > 32 ? 4 : 1; }
 
 template <int DT>
 int launch_q(const LatentParams &p, cudaStream_t s) {
@@ -1151,15 +1152,15 @@ int launch_q(const LatentParams &p, cudaStream_t s) {
                                  : cudaLaunchKernelEx(&c, latent_q_kernel<DT, 4>, p));
 }
 
-template <int DT, int MT>
-int launch_out_mt(const LatentParams &p, cudaStream_t s) {
+template <int DT, int MT, bool JOIN>
+int launch_out(const LatentParams &p, cudaStream_t s) {
     const size_t smem = (size_t)(p.dv * 72 + 2 * 16 * MT * 72) * 2 + (size_t)16 * MT * p.dv * 4;
-    const int st = set_smem<latent_out_kernel<DT, MT>>((size_t)(128 * 72 + 2 * 16 * MT * 72) * 2 + (size_t)16 * MT * 512);
+    const int st = set_smem<latent_out_kernel<DT, MT, JOIN>>((size_t)(128 * 72 + 2 * 16 * MT * 72) * 2 + (size_t)16 * MT * 512);
     if (st) return st;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t c =
-        latent_config(dim3(p.R / 64, p.heads, (p.N + 16 * MT - 1) / (16 * MT)), 512, smem, s, attr, p.R / 64);
-    return record_launch(cudaLaunchKernelEx(&c, latent_out_kernel<DT, MT>, p));
+    cudaLaunchConfig_t c = latent_config(dim3(p.R / 64, p.heads, (p.N + 16 * MT - 1) / (16 * MT)), JOIN ? 512 : 256, smem, s,
+                                         attr, p.R / 64);
+    return record_launch(cudaLaunchKernelEx(&c, latent_out_kernel<DT, MT, JOIN>, p));
 }
 
 template <int DT>
@@ -1178,12 +1179,14 @@ int launch_absorbed(LatentParams &p, int dtype, bool packed, cudaStream_t s) {
          : p.nr == 32 ? launch_attn<DT, 32>(p, maps, blocks, s)
                       : launch_attn<DT, 64>(p, maps, blocks, s);
     if (st) return st;
-    if (p.w_uv) return token_tiles(p.N) == 1 ? launch_out_mt<DT, 1>(p, s) : launch_out_mt<DT, 4>(p, s);
+    // Many tokens: their rows are joined once, not by each of the R / 64 blocks that multiply them.
+    if (p.w_uv && token_tiles(p.N) == 1) return launch_out<DT, 1, true>(p, s);
     cudaLaunchAttribute attr[2];
     const int sub = p.N * p.heads <= 4 * sms ? 4 : 1;
     cudaLaunchConfig_t c = latent_config(dim3(p.N * p.heads), 128 * sub, 0, s, attr, 1);
-    return record_launch(sub == 4 ? cudaLaunchKernelEx(&c, latent_join_kernel<DT, 4>, p)
-                                  : cudaLaunchKernelEx(&c, latent_join_kernel<DT, 1>, p));
+    st = record_launch(sub == 4 ? cudaLaunchKernelEx(&c, latent_join_kernel<DT, 4>, p)
+                                : cudaLaunchKernelEx(&c, latent_join_kernel<DT, 1>, p));
+    return st || !p.w_uv ? st : launch_out<DT, 4, false>(p, s);
 }
 
 // Rows per unit: the call's largest request in one unit where 16 or 32 rows
@@ -1193,7 +1196,6 @@ int rows_per_unit(int max_q, int heads) {
     return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-constexpr int kExpandFrom = 200;
 constexpr size_t kHdr = 256;
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // The workspace of the absorbed form.
@@ -1227,10 +1229,23 @@ ExpandedLayout expanded_layout(int B, int max_len, int heads) {
     l.bytes = l.rope + (size_t)B * l.rows * 128;
     return l;
 }
-// The form that a call takes.
-int latent_form(int form, int max_q, int dn, int dv) {
+// The form that a call takes: the one whose estimate is smaller, in us on 152
+// SMs.  Absorbed: 1.55 per tile of 64 tokens and 64 rows and SM, 4 ns per (token,
+// head) row of the joined results.  Expanded: 3.4 per key tile of 128 tokens,
+// head and SM to write keys and values, 2.2 per key tile in which a block attends
+// (blocks of 256 rows; few of them leave SMs idle).  Measured, absorbed /
+// expanded: 16 heads, 4 x 4096 cached, 64 rows 81 / 120, 256 rows 249 / 129; 1 x
+// 16384, 256 rows 199 / 300; 1 x 600, 32 rows 27 / 19; 32 heads, 4 x 4096, 96
+// rows 196 / 187.
+int latent_form(int form, int B, int max_q, int max_len, int heads, int dn, int dv) {
     if (form != SPX_LATENT_AUTO) return form;
-    return dn == 128 && dv == 128 && max_q >= kExpandFrom ? SPX_LATENT_EXPANDED : SPX_LATENT_ABSORBED;
+    if (dn != 128 || dv != 128) return SPX_LATENT_ABSORBED;
+    const double sms = 152, rows = (double)max_q * heads, tiles = ceil(max_len / 128.0);
+    const double seen = ceil((max_len - (max_q < max_len ? max_q : max_len) / 2.0) / 128.0);  // causal
+    const double blocks = (double)B * heads * ceil(max_q / 256.0);
+    const double absorbed = 14 + 1.55 * ceil(B * ceil(rows / 64) * ceil(max_len / 64.0) / sms) + 0.004 * B * rows;
+    const double expanded = 8 + 3.4 * ceil(B * tiles * heads / sms) + 2.2 * seen * (blocks > sms ? blocks / sms : 1);
+    return expanded < absorbed ? SPX_LATENT_EXPANDED : SPX_LATENT_ABSORBED;
 }
 
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -1261,7 +1276,7 @@ extern "C" size_t spx_latent_workspace_size(int B, int N, int max_q, int max_len
     // (token, head) rows and cached rows are counted in 31 bits
     if ((long long)N * heads > 1 << 30 || (long long)max_q * heads > 1 << 30 || (long long)B * max_len > 1 << 30) return 0;
     if ((dn != 0) != (dv != 0) || (dn && dn != 64 && dn != 128) || (dv && dv != 64 && dv != 128)) return 0;
-    const int used = latent_form(form, max_q, dn, dv);
+    const int used = latent_form(form, B, max_q, max_len, heads, dn, dv);
     if (used == SPX_LATENT_EXPANDED) return dn == 128 && dv == 128 ? expanded_layout(B, max_len, heads).bytes : 0;
     return absorbed_layout(B, N, max_q, heads, R, P, dn != 0).bytes;
 }
@@ -1322,7 +1337,7 @@ extern "C" int spx_latent_attention(const spx_latent_args *a, spx_stream_t strea
     p.budget = a->wait_budget_ns ? a->wait_budget_ns : 2000000000ull;
     p.box_tokens = c.page_size % 64 == 0 ? 64 : c.page_size % 32 == 0 ? 32 : 16;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (latent_form(a->form, a->max_q, a->dn, a->dv) == SPX_LATENT_EXPANDED) {
+    if (latent_form(a->form, c.B, a->max_q, a->max_len, a->heads, a->dn, a->dv) == SPX_LATENT_EXPANDED) {
         const ExpandedLayout l = expanded_layout(c.B, a->max_len, a->heads);
         p.k_x = reinterpret_cast<uint16_t *>(ws + l.k);
         p.v_x = reinterpret_cast<uint16_t *>(ws + l.v);
