@@ -85,6 +85,8 @@ constexpr int kUnitsPerThread = 4;
 template <int DT>
 __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constant__ AppendParams p) {
     const int lane = threadIdx.x & 31;
+    griddep_wait();
+    griddep_launch_dependents();
     if ((int)blockIdx.x < p.kv_blocks) {
         const int n = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
         if (n >= p.N) return;
@@ -235,9 +237,8 @@ extern "C" int spx_latent_append(const spx_latent_append_args *a, spx_stream_t s
     p.by_units.set(per_head ? per_head : 1);
     p.by_heads.set(a->q ? a->heads : 1);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (c.dtype == SPX_F16)
-        latent_append_kernel<SPX_F16><<<(unsigned)blocks, 256, 0, s>>>(p);
-    else
-        latent_append_kernel<SPX_BF16><<<(unsigned)blocks, 256, 0, s>>>(p);
-    return record_launch(cudaGetLastError());
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = latent_config(dim3((unsigned)blocks), 256, 0, s, attr, 1);
+    return record_launch(c.dtype == SPX_F16 ? cudaLaunchKernelEx(&cfg, latent_append_kernel<SPX_F16>, p)
+                                            : cudaLaunchKernelEx(&cfg, latent_append_kernel<SPX_BF16>, p));
 }

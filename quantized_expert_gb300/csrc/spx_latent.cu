@@ -140,19 +140,21 @@ constexpr int kMaxBlocks = 160;  // blocks of the attention launch: one per SM, 
 constexpr int kRopeBytes = kTile * 128;
 // Copies are issued by one warp per pair of a tile: a warp takes 250 to 300
 // cycles for each, and one warp's nine of a tile were slower than the products.
-constexpr int kCopyWarps = 4;
+// One more takes the queries, which wait for the launch that writes them.
+constexpr int kCopyWarps = 4, kQueryWarp = kCopyWarps, kIssueWarp = kCopyWarps + 1;
 
-// Ring depths by rows per unit, as shared memory allows: 2.75, 2.5 and 2 tiles.
+// Ring depths by rows per unit: 2.25, 2.5 and 2 tiles.  Shared memory would allow
+// 2.75 for 16 rows, but then no block starts beside one of the query launch.
 // A tile's rotated part is not needed once its S^T is there, so its slot then
 // takes the tile's softmax weights, P^T [64 tokens x 64 rows].
 template <int NR>
 struct AttnGeo {
-    static constexpr int kPairs = NR <= 16 ? 11 : NR <= 32 ? 10 : 8;
+    static constexpr int kPairs = NR <= 16 ? 9 : NR <= 32 ? 10 : 8;
     static constexpr int kRopes = 3;
     // Softmax warps: four (one per quarter of tensor memory) for each share of
     // the rows: one warp a scheduler cannot keep up with the products on 64 rows.
     static constexpr int kShares = NR <= 16 ? 1 : 2;
-    static constexpr int kThreads = 32 * (kCopyWarps + 1) + 128 * kShares;
+    static constexpr int kThreads = 32 * (kIssueWarp + 1) + 128 * kShares;
     static constexpr int kQBytes = 9 * NR * 128;
     static constexpr int kMisc = 3072;
     static constexpr int kSmem = kQBytes + kPairs * kPairBytes + kRopes * kRopeBytes + kMisc;
@@ -173,7 +175,8 @@ struct AttnMisc {
     uint32_t tmem;
     int abort;
     int b, g, off, flat, left, share;  // tiles of a share, and where this block's begins
-    int pad[2];
+    LatentReq rq;                      // the request b
+    int pad[3];
     int lim[64];                  // positions that each row sees
     float fac[64];
     float red[2][4][64];
@@ -229,7 +232,7 @@ struct Walk {
         left = m.left;
         first = true;
         if (left <= 0) return;
-        rq = latent_req(p, b);
+        rq = m.rq;
         nt = unit_tiles<NR>(p, rq, g);
         tile = m.off;
         end = min(nt, tile + left);
@@ -292,6 +295,7 @@ __device__ __forceinline__ void find_share(const LatentParams &p, AttnMisc &m, i
                     m.b = b0 + lane;
                     m.g = g;
                     m.off = off;
+                    m.rq = r;
                 }
                 found = __any_sync(0xffffffffu, mine);
             }
@@ -324,10 +328,10 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
     if (!p.chained) griddep_wait();
     if (warp == 0) {
         find_share<NR>(p, m, lane);
-    } else if (warp == kCopyWarps) {
+    } else if (warp == kIssueWarp) {
         tmem_alloc(&m.tmem, G::kTmem);
         tmem_relinquish();
-    } else if (warp == kCopyWarps + 1) {
+    } else if (warp == kQueryWarp) {
         // a barrier a lane; the words from full to fin are all barriers
         uint64_t *bars = m.full;
         constexpr int kBars = 4 + 12 + 4 + 2 + 2 + 2 + 3;
@@ -354,27 +358,15 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
     Walk<NR> w;
 
     if (warp < kCopyWarps) {
-        // ---- copies: warp c takes pair c of every tile, warp 0 the rotated part and the queries too
+        // ---- copies: warp c takes pair c of every tile, warp 0 the rotated part too
         const uint64_t pol = p.groups > 1 ? policy_evict_normal() : policy_evict_first();
         const int bt = p.box_tokens, nb = kTile / bt;  // boxes do not cross a page
-        uint32_t tc = 0, seg = 0;
+        uint32_t tc = 0;
         Slot<PR> ps;
         Slot<RR> rs;
         ps.i = warp;
-        bool ok = true, waited = !p.chained;
-        auto queries = [&]() {  // the unit's, once the last unit's have been read
-            if (!(ok = ctl_wait(&m.qempty, (seg & 1) ^ 1, ctl))) return;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&m.qfull, (uint32_t)(2 * np + 1) * NR * 128);
-                tma_load_3d(qs, &maps.q, 0, w.rq.row0 * p.heads + NR * w.g, 0, &m.qfull, pol);
-            }
-            __syncwarp();
-        };
-        for (w.begin(p, m); ok && warp < np && w.left > 0; w.next(p), ++seg) {
-            // Queries that no launch of this call writes come first in the block; the others, and those of
-            // later units, behind the unit's first two tiles, which find room without the queries' products.
-            const bool ahead = !p.chained && seg == 0;
-            if (warp == 0 && ahead) queries();
+        bool ok = true;
+        for (w.begin(p, m); ok && warp < np && w.left > 0; w.next(p)) {
             const int32_t *tab = p.table + (size_t)w.b * p.max_pages;
             int box = 32, my_page = 0, my_at = 0;  // this lane's box of the 32 looked up together
 #pragma unroll 1
@@ -409,19 +401,25 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                 __syncwarp();
                 ps.advance(np);
                 rs.next();
-                if (warp == 0 && !ahead && i == min(w.tile + 1, w.end - 1)) {
-                    if (!waited) {
-                        griddep_wait();
-                        waited = true;
-                    }
-                    queries();
-                    if (!ok) break;
-                }
             }
         }
-        if (!waited) griddep_wait();
         if (!ok) ctl_settle(100000000ull);  // copies in flight land before the block ends
-    } else if (warp == kCopyWarps) {
+    } else if (warp == kQueryWarp) {
+        // ---- the units' queries, each once the last unit's have been read
+        const uint64_t pol = policy_evict_normal();
+        uint32_t seg = 0;
+        bool ok = true;
+        if (p.chained) griddep_wait();
+        for (w.begin(p, m); ok && w.left > 0; w.next(p), ++seg) {
+            if (!(ok = ctl_wait(&m.qempty, (seg & 1) ^ 1, ctl))) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&m.qfull, (uint32_t)(2 * np + 1) * NR * 128);
+                tma_load_3d(qs, &maps.q, 0, w.rq.row0 * p.heads + NR * w.g, 0, &m.qfull, pol);
+            }
+            __syncwarp();
+        }
+        if (!ok) ctl_settle(100000000ull);
+    } else if (warp == kIssueWarp) {
         // ---- products: whichever is ready, the oldest tile's O first; S at most two tiles ahead of O
         const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
         const uint64_t qd = sw128_desc(smem_u32(qs)), kd = sw128_desc(smem_u32(pairs)), rd = sw128_desc(smem_u32(ropes));
@@ -510,7 +508,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
         // ---- softmax, rescaling, results
         constexpr int SH = G::kShares, NC = NR / SH, NB = NC / 8;  // rows of a share, in blocks of 8
         const int q = warp & 3;                                    // tensor-memory quarter
-        const int sh = (warp - kCopyWarps - 1) >> 2, c0 = NC * sh;              // this warp's share of the rows: c0 ..
+        const int sh = (warp - kIssueWarp - 1) >> 2, c0 = NC * sh;              // this warp's share of the rows: c0 ..
         const int tid = 32 * q + lane, all = 128 * sh + tid;       // index within the share's warps, among all
         const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16);
         const int cl = c0 + 2 * (lane & 3);    // this lane's rows: 8x + cl, 8x + cl + 1
@@ -772,7 +770,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kCopyWarps) {
+    if (warp == kIssueWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, G::kTmem);
     }

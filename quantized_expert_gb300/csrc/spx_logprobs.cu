@@ -206,6 +206,8 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
     const int chunks = (p.V + shift + N - 1) / N, share = (chunks + nb - 1) / nb;
     const int c0 = (int)rank * share, c1 = min(chunks, c0 + share);
 
+    griddep_wait();
+    griddep_launch_dependents();
     float given = NAN;  // the given token's logit
     if (rank == 0 && tid == 0 && p.logp) {
         const int id = p.ids[row];
@@ -412,16 +414,8 @@ int launch(const LogprobParams &p, cudaStream_t s) {
         q.entropy = p.entropy ? p.entropy + r0 : nullptr;
         q.top_ids = p.top_ids ? p.top_ids + (size_t)r0 * p.k : nullptr;
         q.top_logp = p.top_logp ? p.top_logp + (size_t)r0 * p.k : nullptr;
-        cudaLaunchConfig_t c = {};
-        c.gridDim = dim3(nb, q.N);
-        c.blockDim = dim3(kThreadsLp);
-        c.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = nb;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        c.attrs = attr;
-        c.numAttrs = nb > 1;
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t c = latent_config(dim3(nb, q.N), kThreadsLp, 0, s, attr, nb);
         const int st = record_launch(cudaLaunchKernelEx(&c, logprobs_kernel<DT>, q));
         if (st) return st;
     }
