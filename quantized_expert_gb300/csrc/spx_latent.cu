@@ -265,6 +265,25 @@ struct Walk {
 // One warp: all tiles of the call, this block's share, and where it begins.
 template <int NR>
 __device__ __forceinline__ void find_share(const LatentParams &p, AttnMisc &m, int lane) {
+    if (p.B == 1) {  // (the same without the scans, which a single short call would wait for)
+        const LatentReq r = latent_req(p, 0);
+        int total = 0;
+        for (int g = 0; g * NR < r.T * p.heads; ++g) total += unit_tiles<NR>(p, r, g);
+        const int share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1), from = share * (int)blockIdx.x;
+        int off = from, g = 0;
+        if (from < total)
+            for (int u; off >= (u = unit_tiles<NR>(p, r, g)); ++g) off -= u;
+        if (lane == 0) {
+            m.left = min(share, total - from);
+            m.flat = from;
+            m.share = share;
+            m.b = 0;
+            m.g = g;
+            m.off = off;
+            m.rq = r;
+        }
+        return;
+    }
     LatentReq r{0, 0, 0};
     int n = 0, total = 0, share = 0, from = 0;
     bool found = false;
