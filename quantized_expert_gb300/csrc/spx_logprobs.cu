@@ -70,6 +70,32 @@ __device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
     return r;
 }
 
+// Two packed 16-bit values at a time: the larger of each pair (a NaN loses), and
+// the pair with nothing below `low` (a NaN stays).
+template <int DT>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (DT == SPX_F16)
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t floor_pair(uint32_t a, uint32_t low) {
+    uint32_t r;
+    if (DT == SPX_F16)
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(low));
+    else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(low));
+    return r;
+}
+__device__ __forceinline__ float floor_nan(float a, float low) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(low));
+    return r;
+}
+
 // 16 bytes of a row: kN elements from index v0 on, those outside [0, V) as -inf.
 template <int DT>
 struct Chunk {
@@ -96,45 +122,66 @@ struct Chunk {
             }
         }
     }
+    // the largest (a NaN loses; NaN if all are)
+    static __device__ __forceinline__ float largest(const uint4 &r) {
+        if (kN == 4)
+            return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+        const float2 p = Elem<DT == SPX_F32 ? SPX_F16 : DT>::up2(max_pair<DT>(max_pair<DT>(r.x, r.y), max_pair<DT>(r.z, r.w)));
+        return fmaxf(p.x, p.y);
+    }
+    // What the lowest values count as.  A -inf has weight 0 and must not meet an
+    // infinite exponent in d; and a difference from it, taken by a product with log2(e)
+    // that is rounded, is still right to 1.
+    static constexpr float kFloor = DT == SPX_F16 ? -65504.f : -16777216.f;
+    static __device__ __forceinline__ uint4 floored(const uint4 &r) {
+        if (kN == 4)
+            return make_uint4(__float_as_uint(floor_nan(__uint_as_float(r.x), kFloor)),
+                              __float_as_uint(floor_nan(__uint_as_float(r.y), kFloor)),
+                              __float_as_uint(floor_nan(__uint_as_float(r.z), kFloor)),
+                              __float_as_uint(floor_nan(__uint_as_float(r.w), kFloor)));
+        constexpr uint32_t low = DT == SPX_F16 ? 0xFBFFFBFFu : 0xCB80CB80u;  // kFloor
+        return make_uint4(floor_pair<DT>(r.x, low), floor_pair<DT>(r.y, low), floor_pair<DT>(r.z, low),
+                          floor_pair<DT>(r.w, low));
+    }
 };
+// A maximum above kLarge sends its row through exact passes: the differences in
+// base 2 are right to 2^-24 of log2(e) times the maximum, 0.1 there, and a larger
+// one could overflow 2^t.  So does a row's maximum that is not above kLow, from
+// which the floor is not far enough.  (fp16's next value above its lowest is 32
+// higher: what is floored weighs e^-32 at most there.)
+constexpr float kLarge = 1e6f;
+template <int DT>
+constexpr float kLow = DT == SPX_F16 ? -65504.f : -kLarge;
 
 // One thread's running sums over the elements of its chunks (two of each kind).
 template <int DT>
 struct Running {
-    float m = -INFINITY;
-    uint64_t minus_m = 0, z = 0, d = 0;
+    float m = -INFINITY;  // the maximum; its max with kFloor is the reference
+    uint64_t minus_mc = 0, z = 0, d = 0;  // minus the reference, times log2(e)
     int at;  // chunk of the first maximum
-    bool bad = false;
     __device__ __forceinline__ void take(const uint4 &raw, int c) {
         using C = Chunk<DT>;
-        float f[C::kN];
-        C::unpack(raw, f);
-        float mx = f[0];
-#pragma unroll
-        for (int i = 1; i < C::kN; ++i) mx = fmaxf(mx, f[i]);
+        const float mx = C::largest(raw);
         if (mx > m) {
+            const float ref = fmaxf(mx, C::kFloor);
             if (m > -INFINITY) {
-                const float t = (m - mx) * kLog2e, g = ex2f(t);
+                const float t = (fmaxf(m, C::kFloor) - ref) * kLog2e, g = ex2f(t);
                 d = mul2(fma2(pack2(t, t), z, d), pack2(g, g));
                 z = mul2(z, pack2(g, g));
             }
             m = mx;
-            minus_m = pack2(-mx, -mx);
+            minus_mc = pack2(-ref * kLog2e, -ref * kLog2e);
             at = c;
         }
-        if (m > -INFINITY) {
-            // A difference first: logits near the type's largest would overflow in base 2.  The weight
-            // of -inf is 0, and so is its term of d (0 times a clamped exponent); a NaN stays in z.
+        float f[C::kN];
+        C::unpack(C::floored(raw), f);
 #pragma unroll
-            for (int i = 0; i < C::kN; i += 2) {
-                const float2 t = unpack2(mul2(add2(pack2(f[i], f[i + 1]), minus_m), pack2(kLog2e, kLog2e)));
-                const uint64_t e = pack2(ex2f(t.x), ex2f(t.y));
-                z = add2(z, e);
-                d = fma2(e, pack2(fmaxf(t.x, -200.f), fmaxf(t.y, -200.f)), d);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < C::kN; ++i) bad |= f[i] != f[i];
+        for (int i = 0; i < C::kN; i += 2) {
+            const uint64_t t2 = fma2(pack2(f[i], f[i + 1]), pack2(kLog2e, kLog2e), minus_mc);
+            const float2 t = unpack2(t2);
+            const uint64_t e = pack2(ex2f(t.x), ex2f(t.y));
+            z = add2(z, e);
+            d = fma2(e, t2, d);
         }
     }
 };
@@ -168,8 +215,8 @@ __device__ __forceinline__ float value_of(uint32_t o) {
     return o == 0xFFFFFFFFu ? NAN : __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
 
-// The k largest keys of a row, one pass over it for each: rows with an
-// infinity or a NaN, and more candidates than the buffer holds.
+// The k largest keys of a row, one pass over it for each: rows with a
+// NaN or a maximum above kLarge, and more candidates than the buffer holds.
 template <int DT>
 __device__ void top_by_passes(const typename Elem<DT>::T *x, int lo, int hi, int k, uint64_t *top, uint64_t *scratch) {
     uint64_t last = ~0ull;
@@ -242,11 +289,13 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
     Stat a;
     {
         const float2 z = unpack2(run.z), d = unpack2(run.d);
-        a = Stat{run.m, z.x + z.y, d.x + d.y};
+        // (nothing but -inf: a reference of 0 so far, and no weight)
+        a = Stat{run.m > -INFINITY ? fmaxf(run.m, C::kFloor) : -INFINITY, z.x + z.y, d.x + d.y};
+        if (run.m == -INFINITY) a.d = 0.f;
     }
     const int at = run.at;
-    const bool bad = run.bad || a.m == INFINITY || a.z != a.z;
-    const float own_m = a.m;
+    const bool bad = a.m > kLarge || a.z != a.z;
+    const float own_m = run.m;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         Stat b;
@@ -292,12 +341,16 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
         __syncthreads();
         // their chunks, dealt out over the block
         const int per = (c1 - c0 + kThreadsLp - 1) / kThreadsLp, items = s.n_slices * per;
+        const uint32_t tau32 = (uint32_t)(tau >> 32);
+        const float tau_value = tau32 > order32(-INFINITY) ? value_of(tau32) : -INFINITY;
 #pragma unroll 1
         for (int i = tid; i < items; i += kThreadsLp) {
             const int slice = i / per, c = c0 + s.slices[slice] + (i - slice * per) * kThreadsLp;
             if (c >= c1) continue;
+            const uint4 raw = C::load(x, N * c - shift, p.V);
+            if (!(C::largest(raw) >= tau_value)) continue;
             float f[N];
-            C::unpack(C::load(x, N * c - shift, p.V), f);
+            C::unpack(raw, f);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 const int v = N * c - shift + e;
@@ -354,19 +407,49 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
         slow |= s.part[b].z != s.part[b].z;
         a = join(a, s.part[b]);
     }
-    if (slow) {  // an infinity or a NaN somewhere
+    if (slow || (a.m > -INFINITY && a.m <= kLow<DT>)) {  // two passes, differences first
         bool n = false;
+        float m = -INFINITY;
         for (int v = tid; v < p.V; v += kThreadsLp) {
             const float f = E::up(x[v]);
             n |= f != f;
+            m = fmaxf(m, f);
         }
         nan = __syncthreads_or(n);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) s.warp[warp].m = m;
+        __syncthreads();
+        for (int w = 0; w < kWarpsLp; ++w) m = fmaxf(m, s.warp[w].m);
+        a = Stat{m, 0.f, 0.f};
+        if (!nan && m < INFINITY && m > -INFINITY) {
+            for (int v = tid; v < p.V; v += kThreadsLp) {
+                const float t = (E::up(x[v]) - m) * kLog2e, e = ex2f(t);
+                a.z += e;
+                a.d = fmaf(e, fmaxf(t, -200.f), a.d);
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
+                a.d += __shfl_xor_sync(0xffffffffu, a.d, o);
+            }
+            __syncthreads();
+            if (lane == 0) s.warp[warp] = a;
+            __syncthreads();
+            a.z = a.d = 0.f;
+            for (int w = 0; w < kWarpsLp; ++w) {
+                a.z += s.warp[w].z;
+                a.d += s.warp[w].d;
+            }
+        }
     }
-    const bool none = !slow && a.m == -INFINITY;
-    const float log_z = slow ? (nan ? NAN : INFINITY) : none ? 0.f : a.m + logf(a.z);
+    // without a distribution: a NaN, an infinity
+    const bool no = slow && (nan || a.m == INFINITY);
+    const bool none = !no && a.m == -INFINITY;
+    const float log_z = no ? (nan ? NAN : INFINITY) : none ? 0.f : a.m + logf(a.z);
     if (tid == 0) {
         if (p.logp) p.logp[row] = given - log_z;
-        if (p.entropy) p.entropy[row] = slow ? NAN : none ? 0.f : fmaxf(logf(a.z) - kLn2 * a.d / a.z, 0.f);
+        if (p.entropy) p.entropy[row] = no ? NAN : none ? 0.f : fmaxf(logf(a.z) - kLn2 * a.d / a.z, 0.f);
     }
     if (p.k > 0) {
         if (slow) top_by_passes<DT>(x, 0, p.V, p.k, s.cand, s.key);

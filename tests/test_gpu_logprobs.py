@@ -109,6 +109,49 @@ def test_ties_masks_and_extremes(dtype, V):
     check(x, ids, k, call(x, ids, k))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("V", [77, 5003, 66000])
+def test_lowest_and_infinite_masks_together(dtype, V):
+    """Whole stretches at the type's lowest value, next to -inf and to ordinary logits; rows of
+    nothing but those two; values between them; few that are left."""
+    g = torch.Generator(device="cuda").manual_seed(V + 1)
+    big = torch.finfo(dtype).max
+    x = (torch.randn(10, V, generator=g, device="cuda") * 3).to(dtype)
+    x[0, 5: V - 3] = -big
+    x[1, : V // 2] = -big
+    x[1, V // 2: V - 2] = -math.inf
+    x[2] = -math.inf
+    x[2, ::3] = -big                            # uniform over a third
+    x[3] = -math.inf
+    x[3, V - 1] = -big                          # one left, at the lowest value
+    x[4] = -big
+    x[4, V // 3] = -big / 2
+    x[5] = -big / 2                             # all equal and low
+    x[6] = -math.inf
+    x[6, V // 2: V // 2 + 3] = 1.0
+    x[7, 1::2] = -big / 3
+    x[8, 4:] = -math.inf
+    x[8, :4] = big / 2                          # large ones
+    x[9, : V - 1] = -big
+    x[9, V - 1] = -100.0
+    ids = torch.randint(0, V, (10,), generator=g, device="cuda").to(torch.int32)
+    ids[3], ids[6] = V - 1, V // 2
+    k = 8
+    check(x, ids, k, call(x, ids, k))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [1e5, 9e5, 3e6, 1e8, 1e20, 1e37])
+def test_large_logits(dtype, size):
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x = (torch.randn(4, 9000, generator=g, device="cuda") * 0.25 * size).to(dtype)
+    x[1] = x[1].abs()
+    x[2] = -x[2].abs() - size
+    x[3, ::7] = size
+    ids = torch.randint(0, 9000, (4,), generator=g, device="cuda").to(torch.int32)
+    check(x, ids, 5, call(x, ids, 5))
+
+
 def test_infinite_logit():
     x = torch.zeros(1, 100, device="cuda")
     x[0, 7] = math.inf
