@@ -9,9 +9,17 @@
 //
 // Alternatives: each thread also remembers where its maximum lies.  A bound
 // that between k and 2k of the threads' maxima reach (found by bisection) is
-// one that at least k elements reach, and only those threads can hold an
-// alternative; their elements alone are read again (from L2), and the few that
-// reach the bound are ranked by counting.
+// one that at least k elements reach.  Long rows get such a bound from the first
+// eighth of their elements, and the chunks that reach it are noted from there on;
+// at the end only these, and the first eighth of the few threads whose maximum
+// reaches the last bound, are read again (from L2), and the elements that reach
+// it are ranked by counting.  (All the chunks of such threads read again: 63 us
+// for 1088 rows of 102400 in bf16 and 20 alternatives, noted 56 us, without
+// alternatives 45 us.)
+//
+// What bounds it: 4.0 TB/s of logits, where a copy runs at 6.8: an
+// element takes 11 instructions, 60% of the issue slots are taken, and 1088 rows
+// are 1.8 waves of blocks (608 rows, one wave: 31 us; fp32, 544 rows: 5.0 TB/s).
 #include "spx_latent.cuh"
 
 #include <math.h>
@@ -41,6 +49,7 @@ __device__ __forceinline__ uint64_t order64(float x, int v) { return ((uint64_t)
 constexpr int kThreadsLp = 256, kWarpsLp = kThreadsLp / 32;
 constexpr int kMaxCluster = 8, kMaxTop = 32;
 constexpr int kCandidates = 2048;
+constexpr int kHigh = 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -154,35 +163,41 @@ template <int DT>
 constexpr float kLow = DT == SPX_F16 ? -65504.f : -kLarge;
 
 // One thread's running sums over the elements of its chunks (two of each kind).
+// Their reference follows the maximum only once that is kSlack above it: with a
+// reference that moves at every new maximum some thread of a warp moves at most
+// chunks.  e^kSlack stays small, since the entropy is a difference of ln z and d/z.
+constexpr float kSlack = 4.f;
 template <int DT>
 struct Running {
-    float m = -INFINITY;  // the maximum; its max with kFloor is the reference
-    uint64_t minus_mc = 0, z = 0, d = 0;  // minus the reference, times log2(e)
+    float m = -INFINITY, ref = -INFINITY;
+    uint64_t minus_rc = 0, z = 0, d = 0;  // minus the reference, times log2(e)
     int at;  // chunk of the first maximum
-    __device__ __forceinline__ void take(const uint4 &raw, int c) {
+    __device__ __forceinline__ float take(const uint4 &raw, int c) {
         using C = Chunk<DT>;
         const float mx = C::largest(raw);
-        if (mx > m) {
-            const float ref = fmaxf(mx, C::kFloor);
-            if (m > -INFINITY) {
-                const float t = (fmaxf(m, C::kFloor) - ref) * kLog2e, g = ex2f(t);
+        at = mx > m ? c : at;
+        m = fmaxf(m, mx);
+        if (mx > ref + kSlack) {
+            const float to = fmaxf(mx, C::kFloor);
+            if (ref > -INFINITY) {
+                const float t = (ref - to) * kLog2e, g = ex2f(t);
                 d = mul2(fma2(pack2(t, t), z, d), pack2(g, g));
                 z = mul2(z, pack2(g, g));
             }
-            m = mx;
-            minus_mc = pack2(-ref * kLog2e, -ref * kLog2e);
-            at = c;
+            ref = to;
+            minus_rc = pack2(-to * kLog2e, -to * kLog2e);
         }
         float f[C::kN];
         C::unpack(C::floored(raw), f);
 #pragma unroll
         for (int i = 0; i < C::kN; i += 2) {
-            const uint64_t t2 = fma2(pack2(f[i], f[i + 1]), pack2(kLog2e, kLog2e), minus_mc);
+            const uint64_t t2 = fma2(pack2(f[i], f[i + 1]), pack2(kLog2e, kLog2e), minus_rc);
             const float2 t = unpack2(t2);
             const uint64_t e = pack2(ex2f(t.x), ex2f(t.y));
             z = add2(z, e);
             d = fma2(e, t2, d);
         }
+        return mx;
     }
 };
 
@@ -194,6 +209,7 @@ struct LogprobSmem {
     Stat warp[kWarpsLp];
     uint32_t lo[kWarpsLp], hi[kWarpsLp];
     int n_cand, n_slices, slices[kThreadsLp];
+    int n_high, high[kHigh];
     int slow;
 };
 
@@ -237,9 +253,35 @@ __device__ void top_by_passes(const typename Elem<DT>::T *x, int lo, int hi, int
     __syncthreads();
 }
 
+// A value that at least k of the block's threads' values (as order32 has them)
+// reach, and no more than 2k if twelve halvings find such a one.
+__device__ __forceinline__ uint32_t reached_by(uint32_t val, int k, LogprobSmem &s) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t lo = __reduce_min_sync(0xffffffffu, val), hi = __reduce_max_sync(0xffffffffu, val);
+    if (lane == 0) {
+        s.lo[warp] = lo;
+        s.hi[warp] = hi;
+    }
+    __syncthreads();
+    lo = __reduce_min_sync(0xffffffffu, s.lo[lane & (kWarpsLp - 1)]);
+    hi = __reduce_max_sync(0xffffffffu, s.hi[lane & (kWarpsLp - 1)]);
+    int reach = kThreadsLp;
+    for (int i = 0; i < 12 && reach > 2 * k && hi - lo > 1; ++i) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int n = __syncthreads_count(val >= mid);
+        if (n >= k) {
+            lo = mid;
+            reach = n;
+        } else {
+            hi = mid;
+        }
+    }
+    return lo;
+}
+
 // One cluster per row, its blocks taking equal stretches of it.
 template <int DT>
-__global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_constant__ LogprobParams p) {
+__global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_constant__ LogprobParams p) {
     using E = Elem<DT>;
     using T = typename E::T;
     using C = Chunk<DT>;
@@ -264,6 +306,19 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
     run.at = c0 + tid;
     constexpr int kAhead = 4;  // loads in flight per thread
     const int whole = min(c1, (p.V + shift) / N);  // chunks that do not reach past the row
+    // After the first chunks of each thread (an eighth) comes a first bound for the
+    // alternatives, and the chunks that reach it are noted from there on.
+    const int per = (c1 - c0 + kThreadsLp - 1) / kThreadsLp;
+    const bool noting = p.k > 0 && per >= 4 * kAhead;
+    const int first = noting ? (per / 8 + kAhead - 1) / kAhead * kAhead : per;
+    float bound = INFINITY;
+    if (tid == 0) s.n_cand = s.n_slices = s.n_high = 0;
+    const auto take = [&](const uint4 &raw, int c) {
+        if (run.take(raw, c) >= bound) {
+            const int n = atomicAdd(&s.n_high, 1);
+            if (n < kHigh) s.high[n] = c;
+        }
+    };
     int c = c0 + tid;
 #pragma unroll 1
     for (; c + (kAhead - 1) * kThreadsLp < whole; c += kAhead * kThreadsLp) {
@@ -273,8 +328,12 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
             const int v0 = N * (c + u * kThreadsLp) - shift;
             raw[u] = u == 0 && v0 < 0 ? C::load(x, v0, p.V) : __ldg(reinterpret_cast<const uint4 *>(x + v0));
         }
+        if (noting && c - tid == c0 + first * kThreadsLp) {
+            const uint32_t o = reached_by(order32(run.m), p.k, s);
+            if (o > order32(-INFINITY)) bound = value_of(o);
+        }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) run.take(raw[u], c + u * kThreadsLp);
+        for (int u = 0; u < kAhead; ++u) take(raw[u], c + u * kThreadsLp);
     }
 #pragma unroll 1
     for (; c < c1; c += kAhead * kThreadsLp) {
@@ -284,17 +343,16 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
             if (c + u * kThreadsLp < c1) raw[u] = C::load(x, N * (c + u * kThreadsLp) - shift, p.V);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
-            if (c + u * kThreadsLp < c1) run.take(raw[u], c + u * kThreadsLp);
+            if (c + u * kThreadsLp < c1) take(raw[u], c + u * kThreadsLp);
     }
     Stat a;
     {
         const float2 z = unpack2(run.z), d = unpack2(run.d);
-        // (nothing but -inf: a reference of 0 so far, and no weight)
-        a = Stat{run.m > -INFINITY ? fmaxf(run.m, C::kFloor) : -INFINITY, z.x + z.y, d.x + d.y};
-        if (run.m == -INFINITY) a.d = 0.f;
+        a = Stat{run.ref, z.x + z.y, d.x + d.y};
+        if (run.ref == -INFINITY) a.d = 0.f;  // (nothing but -inf: no weight)
     }
     const int at = run.at;
-    const bool bad = a.m > kLarge || a.z != a.z;
+    const bool bad = run.m > kLarge || a.z != a.z;
     const float own_m = run.m;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -314,7 +372,6 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
             s.hi[warp] = hi;
         }
     }
-    if (tid == 0) s.n_cand = s.n_slices = 0;
     const bool block_bad = __syncthreads_or(bad);
 
     if (p.k > 0 && !block_bad) {
@@ -324,7 +381,8 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
         uint32_t lo32 = s.lo[lane & (kWarpsLp - 1)], hi32 = s.hi[lane & (kWarpsLp - 1)];
         lo32 = __reduce_min_sync(0xffffffffu, lo32);
         hi32 = __reduce_max_sync(0xffffffffu, hi32);
-        // at least k keys reach lo (all of them at first), fewer reach hi
+        // at least k keys reach tau (at first all of them, or those of the first bound), fewer reach hi
+        if (bound < INFINITY) lo32 = max(lo32, order32(bound));
         uint64_t tau = (uint64_t)lo32 << 32, hi = ((uint64_t)hi32 << 32) + 0xffffffffull;
         int reach = kThreadsLp;
         while (reach > 2 * p.k && hi - tau > 1) {
@@ -339,13 +397,16 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
         }
         if (any && hi_key >= tau) s.slices[atomicAdd(&s.n_slices, 1)] = tid;
         __syncthreads();
-        // their chunks, dealt out over the block
-        const int per = (c1 - c0 + kThreadsLp - 1) / kThreadsLp, items = s.n_slices * per;
+        // their chunks up to the first bound and those noted after it (if there are
+        // too many, all the chunks of theirs), dealt out over the block
+        const int high = s.n_high, each = bound < INFINITY && high <= kHigh ? first : per;
+        const int slices = s.n_slices * each, items = slices + (high > kHigh ? 0 : high);
         const uint32_t tau32 = (uint32_t)(tau >> 32);
         const float tau_value = tau32 > order32(-INFINITY) ? value_of(tau32) : -INFINITY;
 #pragma unroll 1
         for (int i = tid; i < items; i += kThreadsLp) {
-            const int slice = i / per, c = c0 + s.slices[slice] + (i - slice * per) * kThreadsLp;
+            const int slice = i / each;
+            const int c = i < slices ? c0 + s.slices[slice] + (i - slice * each) * kThreadsLp : s.high[i - slices];
             if (c >= c1) continue;
             const uint4 raw = C::load(x, N * c - shift, p.V);
             if (!(C::largest(raw) >= tau_value)) continue;
@@ -476,9 +537,9 @@ __global__ void __launch_bounds__(kThreadsLp, 5) logprobs_kernel(const __grid_co
 // Blocks per row: doubled while there are fewer than 256 of them (1.7 an SM),
 // to a portable cluster at most, and while each keeps 16 KB of the row; a block
 // costs some 5 us of its own.  Measured with 102400 logits a row, blocks 1, 2,
-// 4, 8 (us): 17 rows fp32 20.3, 13.1, 9.2, 8.3; 64 rows bf16 17.8, 12.0, 10.9,
-// 13.8; 152 rows 17.9, 14.4, 17.1, 23.8; 608 rows 38.3, 43.0, 52.6, 74.4; 17
-// rows of 32000 8.6, 8.2, 7.8, 9.0.
+// 4, 8 (us): 17 rows fp32 18.2, 12.4, 9.7, 8.3; 64 rows bf16 15.0, 11.6, 10.5,
+// 13.5; 152 rows 15.2, 13.5, 18.5, 25.7; 608 rows 30.9, 39.4, 57.4, 83.6; 17
+// rows of 32000 8.2, 8.0, 7.6, 8.8.
 int blocks_per_row(int N, int64_t bytes) {
     int nb = 1;
     while (nb < kMaxCluster && (int64_t)N * nb < 256 && bytes / (2 * nb) >= 16000) nb *= 2;
