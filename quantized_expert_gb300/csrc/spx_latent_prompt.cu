@@ -52,10 +52,10 @@ __device__ __forceinline__ size_t value_unit(int tile, int t, int unit) {
 // rows of B: D[128 tokens x 256] = keys and values of one head, in one of two
 // accumulators.  A product of 256 columns takes 512 cycles a stage, in which an
 // SM would have to fetch 32 KB from L2, 64 bytes a cycle and more than it gets:
-// two blocks of neighbouring token tiles form a cluster, each fetches one of
-// the two matrices and the copy goes to both.
-constexpr int kExStages = 3;
-constexpr int kExStage = 2 * kPiece;
+// two blocks of neighbouring token tiles form one product of 256 tokens, for
+// which each holds one of the two matrices, 32 bytes a cycle.
+constexpr int kExStages = 6;
+constexpr int kExStage = kPiece;  // this block's half of B
 constexpr int kExThreads = 384;  // copies of W, products, 2 warps' copies of A, 8 epilogue warps
 struct ExMisc {
     uint64_t afull, wfull[kExStages], wempty[kExStages], dfull[2], dempty[2], fin;
@@ -96,20 +96,17 @@ __global__ void __launch_bounds__(kExThreads, 1)
         mbar_init(&m.afull, 2);
         for (int s = 0; s < kExStages; ++s) {
             mbar_init(&m.wfull[s], 1);
-            mbar_init(&m.wempty[s], 2);  // both blocks have used it
+            mbar_init(&m.wempty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&m.dfull[s], 1);
-            mbar_init(&m.dempty[s], 8);
+            mbar_init(&m.dempty[s], 16);  // the epilogue warps of both blocks
         }
         mbar_init(&m.fin, 1);
         m.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
-        tmem_alloc(&m.tmem, 512);
-        tmem_relinquish();
-    }
+    if (warp == 1) pair_tmem_alloc(&m.tmem, 512);
     tc_fence_before();
     __syncthreads();
     cluster_arrive();  // the other block's barriers exist
@@ -125,13 +122,16 @@ __global__ void __launch_bounds__(kExThreads, 1)
         const int pos = t0 + 64 * half + bt * (lane & 3), pi = p.by_page(pos), my_at = pos - pi * p.page_size;
         int my_page = pos < rq.len ? __ldg(p.table + (size_t)b * p.max_pages + pi) : p.num_pages;
         if (my_page < 0 || my_page >= p.num_pages) my_page = p.num_pages;
-        if (elect_one()) mbar_arrive_expect_tx(&m.afull, (uint32_t)nc * (kPiece / 2));
+        // (both blocks' copies count on rank 0's barriers, where the products are issued)
+        const uint32_t afull = smem_of_rank(&m.afull, 0);
+        if (rank == 0 && elect_one()) mbar_arrive_expect_tx(&m.afull, (uint32_t)nc * kPiece);
+        __syncwarp();
         for (int j = 0; j < nb; ++j) {
             const int at = __shfl_sync(0xffffffffu, my_at, j), page = __shfl_sync(0xffffffffu, my_page, j);
             if (elect_one())
                 for (int c = 0; c < nc; ++c)
-                    tma_load_4d(as + c * kPiece + half * (kPiece / 2) + j * bt * 128, &maps.cache, 0, at, c, page,
-                                &m.afull, pol);
+                    pair_load_4d(as + c * kPiece + half * (kPiece / 2) + j * bt * 128, &maps.cache, 0, at, c, page,
+                                 afull, pol);
             __syncwarp();
         }
         // ---- their rotated parts (once for all heads), a token a lane
@@ -158,39 +158,42 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 const uint32_t s = it % kExStages;
                 if (!(ok = ctl_wait(&m.wempty[s], ((it / kExStages) & 1) ^ 1, ctl))) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&m.wfull[s], kExStage);
-                    tma_load_3d_multicast(ws + s * kExStage + rank * kPiece, rank ? &maps.w_uv : &maps.w_uk, 0, 128 * h, c,
-                                          &m.wfull[s], 3, pol);
+                    if (rank == 0) mbar_arrive_expect_tx(&m.wfull[s], 2 * kExStage);
+                    pair_load_3d(ws + s * kExStage, rank ? &maps.w_uv : &maps.w_uk, 0, 128 * h, c,
+                                 smem_of_rank(&m.wfull[s], 0), pol);
                 }
                 __syncwarp();
             }
         if (!ok) ctl_settle(100000000ull);
     } else if (warp == 1) {
-        // ---- products
-        const uint32_t id = idesc_f16_f32(128, 256) | (DT == SPX_BF16 ? kIdescBf16 : 0u);
-        const uint64_t ad = sw128_desc(smem_u32(as)), wd = sw128_desc(smem_u32(ws));
-        uint32_t it = 0;
-        bool ok = ctl_wait(&m.afull, 0, ctl);
-        for (int i = 0; ok && i < nh; ++i) {
-            const uint32_t d = tmem + (i & 1) * 256;
-            if (!(ok = ctl_wait(&m.dempty[i & 1], ((i >> 1) & 1) ^ 1, ctl))) break;
-            for (int c = 0; c < nc; ++c, ++it) {
-                const uint32_t s = it % kExStages;
-                if (!(ok = ctl_wait(&m.wfull[s], (it / kExStages) & 1, ctl))) break;
-                tc_fence_after();
-                if (elect_one()) {
+        if (rank == 0) {
+            // ---- products
+            const uint32_t id = idesc_f16_f32(256, 256) | (DT == SPX_BF16 ? kIdescBf16 : 0u);
+            const uint64_t ad = sw128_desc(smem_u32(as)), wd = sw128_desc(smem_u32(ws));
+            uint32_t it = 0;
+            bool ok = ctl_wait(&m.afull, 0, ctl);
+            for (int i = 0; ok && i < nh; ++i) {
+                const uint32_t d = tmem + (i & 1) * 256;
+                if (!(ok = ctl_wait(&m.dempty[i & 1], ((i >> 1) & 1) ^ 1, ctl))) break;
+                for (int c = 0; c < nc; ++c, ++it) {
+                    const uint32_t s = it % kExStages;
+                    if (!(ok = ctl_wait(&m.wfull[s], (it / kExStages) & 1, ctl))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        umma_f16(d, ad + c * (kPiece / 16) + 2 * j, wd + s * (kExStage / 16) + 2 * j, id, (c | j) != 0);
-                    umma_commit_multicast(&m.wempty[s], 3);
-                    if (c == nc - 1) umma_commit(&m.dfull[i & 1]);
+                        for (int j = 0; j < 4; ++j)
+                            pair_umma_f16(d, ad + c * (kPiece / 16) + 2 * j, wd + s * (kExStage / 16) + 2 * j, id,
+                                          (c | j) != 0);
+                        pair_commit(&m.wempty[s]);
+                        if (c == nc - 1) pair_commit(&m.dfull[i & 1]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-        }
-        if (m.abort) {
-            if (elect_one()) umma_commit(&m.fin);
-            ctl_drain(&m.fin, 0, 100000000ull);
+            if (m.abort) {
+                if (elect_one()) pair_commit(&m.fin);
+                ctl_drain(&m.fin, 0, 100000000ull);
+            }
         }
     } else {
         // ---- epilogue: a token a lane, its keys (warps 4-7) or its values
@@ -230,16 +233,18 @@ __global__ void __launch_bounds__(kExThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&m.dempty[i & 1]);
+            if (lane == 0) mbar_arrive_remote(smem_of_rank(&m.dempty[i & 1], 0));
         }
     }
     tc_fence_before();
     __syncthreads();
+    cluster_arrive();  // both are done with the other's memories and barriers
+    cluster_wait();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        pair_tmem_dealloc(tmem, 512);
     }
-    cluster_arrive();  // the other block copies into this one's shared memory until its end
+    cluster_arrive();
     cluster_wait();
 }
 
