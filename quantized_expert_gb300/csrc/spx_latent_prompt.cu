@@ -58,7 +58,7 @@ constexpr int kExStages = 6;
 constexpr int kExStage = kPiece;  // this block's half of B
 constexpr int kExThreads = 384;  // copies of W, products, 2 warps' copies of A, 8 epilogue warps
 struct ExMisc {
-    uint64_t afull, wfull[kExStages], wempty[kExStages], dfull[2], dempty[2], fin;
+    uint64_t afull[8], wfull[kExStages], wempty[kExStages], dfull[2], dempty[2], fin;
     uint32_t tmem;
     int abort;
 };
@@ -87,13 +87,9 @@ __global__ void __launch_bounds__(kExThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.z, t0 = kPTile * blockIdx.x, h0 = p.head_group * blockIdx.y;
     const int nh = min(p.head_group, p.heads - h0), nc = p.R / 64;
-    griddep_wait();
-    griddep_launch_dependents();
-    const LatentReq rq = latent_req(p, b);
     const uint32_t rank = cluster_rank();
-    if (t0 - kPTile * (int)rank >= rq.len || rq.T == 0) return;  // both blocks of the cluster alike
     if (threadIdx.x == 0) {
-        mbar_init(&m.afull, 2);
+        for (int c = 0; c < nc; ++c) mbar_init(&m.afull[c], 2);
         for (int s = 0; s < kExStages; ++s) {
             mbar_init(&m.wfull[s], 1);
             mbar_init(&m.wempty[s], 1);
@@ -106,6 +102,10 @@ __global__ void __launch_bounds__(kExThreads, 1)
         m.abort = 0;
         fence_mbar_init();
     }
+    griddep_wait();
+    griddep_launch_dependents();
+    const LatentReq rq = latent_req(p, b);
+    if (t0 - kPTile * (int)rank >= rq.len || rq.T == 0) return;  // both blocks of the cluster alike
     if (warp == 1) pair_tmem_alloc(&m.tmem, 512);
     tc_fence_before();
     __syncthreads();
@@ -123,16 +123,17 @@ __global__ void __launch_bounds__(kExThreads, 1)
         int my_page = pos < rq.len ? __ldg(p.table + (size_t)b * p.max_pages + pi) : p.num_pages;
         if (my_page < 0 || my_page >= p.num_pages) my_page = p.num_pages;
         // (both blocks' copies count on rank 0's barriers, where the products are issued)
-        const uint32_t afull = smem_of_rank(&m.afull, 0);
-        if (rank == 0 && elect_one()) mbar_arrive_expect_tx(&m.afull, (uint32_t)nc * kPiece);
-        __syncwarp();
-        for (int j = 0; j < nb; ++j) {
-            const int at = __shfl_sync(0xffffffffu, my_at, j), page = __shfl_sync(0xffffffffu, my_page, j);
-            if (elect_one())
-                for (int c = 0; c < nc; ++c)
+        for (int c = 0; c < nc; ++c) {
+            const uint32_t afull = smem_of_rank(&m.afull[c], 0);
+            if (rank == 0 && elect_one()) mbar_arrive_expect_tx(&m.afull[c], kPiece);
+            __syncwarp();
+            for (int j = 0; j < nb; ++j) {
+                const int at = __shfl_sync(0xffffffffu, my_at, j), page = __shfl_sync(0xffffffffu, my_page, j);
+                if (elect_one())
                     pair_load_4d(as + c * kPiece + half * (kPiece / 2) + j * bt * 128, &maps.cache, 0, at, c, page,
                                  afull, pol);
-            __syncwarp();
+                __syncwarp();
+            }
         }
         // ---- their rotated parts (once for all heads), a token a lane
         if (h0 == 0 && t0 < rq.len)
@@ -171,12 +172,13 @@ __global__ void __launch_bounds__(kExThreads, 1)
             const uint32_t id = idesc_f16_f32(256, 256) | (DT == SPX_BF16 ? kIdescBf16 : 0u);
             const uint64_t ad = sw128_desc(smem_u32(as)), wd = sw128_desc(smem_u32(ws));
             uint32_t it = 0;
-            bool ok = ctl_wait(&m.afull, 0, ctl);
+            bool ok = true;
             for (int i = 0; ok && i < nh; ++i) {
                 const uint32_t d = tmem + (i & 1) * 256;
                 if (!(ok = ctl_wait(&m.dempty[i & 1], ((i >> 1) & 1) ^ 1, ctl))) break;
                 for (int c = 0; c < nc; ++c, ++it) {
                     const uint32_t s = it % kExStages;
+                    if (i == 0 && !(ok = ctl_wait(&m.afull[c], 0, ctl))) break;
                     if (!(ok = ctl_wait(&m.wfull[s], (it / kExStages) & 1, ctl))) break;
                     tc_fence_after();
                     if (elect_one()) {
