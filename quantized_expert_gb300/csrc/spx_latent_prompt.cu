@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
 constexpr int kFaThreads = 384;  // copies of Q and K, two issuers of products, copies of V; 4 softmax warps per tile
 constexpr int kKRing = 5, kVRing = 3;
 struct FaMisc {
-    uint64_t qfull[2], kfull[2], rfull[2], vfull[2];  // by tiles, of which two are under way; rfull: the rotated part
+    uint64_t qfull[2], kfull[2], rfull[2], vfull[2][2];  // by tiles, of which two are under way; rfull: the rotated part, vfull: by halves
     uint64_t kempty[kKRing], vempty[kVRing];     // both issuers are done with a piece
     uint64_t sfull[2], pfull[2][2], odone[2], fin[2];  // pfull: by halves of the keys
     uint64_t turn[2];                            // the other issuer has handed in its products
@@ -334,7 +334,8 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             mbar_init(&m.qfull[i], 1);
             mbar_init(&m.kfull[i], 1);
             mbar_init(&m.rfull[i], 1);
-            mbar_init(&m.vfull[i], 1);
+            mbar_init(&m.vfull[i][0], 1);
+            mbar_init(&m.vfull[i][1], 1);
             mbar_init(&m.sfull[i], 1);
             mbar_init(&m.pfull[i][0], 4);
             mbar_init(&m.pfull[i][1], 4);
@@ -392,10 +393,10 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             for (int c = 0; c < 2; ++c, vr.next()) {
                 if (!(ok = ctl_wait(&m.vempty[vr.i], vr.phase ^ 1, ctl))) break;
                 if (elect_one()) {
-                    if (c == 0) mbar_arrive_expect_tx(&m.vfull[j & 1], 2 * kPiece);
+                    mbar_arrive_expect_tx(&m.vfull[j & 1][c], kPiece);
                     bulk_g2s(vs + vr.i * kPiece,
                              p.v_x + ((size_t)h * p.B + b) * p.kv_rows * 128 + value_unit(j, 64 * c, 0), kPiece,
-                             &m.vfull[j & 1], pol);
+                             &m.vfull[j & 1][c], pol);
                 }
                 __syncwarp();
             }
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kFaThreads, 1)
         for (int j = 0; ok && j <= most; ++j) {
             const bool has_o = j > 0 && j <= nx, has_s = j < nx;
             ok = (j == most || ctl_wait(&m.kfull[j & 1], (j >> 1) & 1, ctl)) &&
-                 (j == 0 || ctl_wait(&m.vfull[(j - 1) & 1], ((j - 1) >> 1) & 1, ctl)) &&
+                 (j == 0 || ctl_wait(&m.vfull[(j - 1) & 1][0], ((j - 1) >> 1) & 1, ctl)) &&
                  // tile 1 goes behind tile 0's products of the same j, tile 0 behind tile 1's of the last
                  (x ? ctl_wait(&m.turn[1], j & 1, ctl) : j == 0 || ctl_wait(&m.turn[0], (j - 1) & 1, ctl)) &&
                  (!has_o || ctl_wait(&m.pfull[x][0], (j - 1) & 1, ctl));
@@ -438,7 +439,9 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 }
                 __syncwarp();
                 vr.next();
-                if (has_o && !(ok = ctl_wait(&m.pfull[x][1], (j - 1) & 1, ctl))) break;
+                ok = ctl_wait(&m.vfull[(j - 1) & 1][1], ((j - 1) >> 1) & 1, ctl) &&
+                     (!has_o || ctl_wait(&m.pfull[x][1], (j - 1) & 1, ctl));
+                if (!ok) break;
                 tc_fence_after();
             }
             if (elect_one()) {
