@@ -12,7 +12,11 @@
 //   result launch     partial sums joined, times W_uv (or, with folded
 //                     weights, a launch that only joins).
 //
-// Every launch is a programmatic dependent of the one before it.
+// Every launch is a programmatic dependent of the one before it.  What bounds a
+// call: one request's draft step is a chain of three launches (517 cached tokens
+// 14 us, 65536 27 us); many requests' is the cache (64 of up to 8192 tokens, 370
+// MB: 80 us, of which the attention launch 68 at 5.4 TB/s); with 64 rows a unit
+// it is the ring of tiles (see the attention launch).
 #include <math.h>
 #include <string.h>
 
@@ -51,7 +55,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // Block (s, h, g): 16 * MT tokens' queries of head h times columns 64 s .. + 63
 // of W_uk[h]; block s = 0 also copies the rotated part.  A block reads its
 // slice of the weights once for all its tokens; the whole of W_uk is 2 MB for
-// 16 heads, so the launch is bound by latency up to some hundred tokens.
+// 16 heads, so the launch is bound by latency up to some hundred tokens (64
+// tokens: 8.6 us alone, from DRAM; in a call the attention launch's set-up runs
+// beside it).  q_lat is rounded to the type, as the tensor cores take it.
 template <int DT, int MT>
 __global__ void __launch_bounds__(128) latent_q_kernel(const __grid_constant__ LatentParams p) {
     extern __shared__ __align__(128) uint8_t lq_smem[];
@@ -128,6 +134,13 @@ __global__ void __launch_bounds__(128) latent_pack_kernel(const __grid_constant_
 //   O^T [R x rows]        += V^T [R x 64 tokens] . P^T     (A = the tile, m-major)
 // with Q and P as the B operands (N = rows) and O^T in tensor memory (R / 128
 // accumulators of 128 lanes).  S^T has M = 64 (16 lanes of each quarter).
+//
+// The products of a tile read shared memory at its rate: 36 of 64 x 64 x 16 (32
+// cycles each) and 16 of 128 x 64 x 16 (48), 1920 cycles on 64 rows, 1200 on
+// 16.  Units of 16 rows wait for DRAM all the same.  Units of 64 rows leave room
+// for two tiles, whose slots are taken from the copy's start to the last
+// product: 2840 cycles a tile (16 requests of 9 x 16 rows over up to 8191
+// tokens: 41 us for 13 of products at the dense rate).
 //
 // Softmax runs in base 2 with one reference per row; the sums are rescaled
 // only when a maximum rises by more than 2^kSlack over it, which fp32 sums and
@@ -957,7 +970,8 @@ __device__ __forceinline__ float2 cluster_ld2(const void *p, uint32_t rank) {
 // cluster adds the slices up.  The joined sums enter the product as two values
 // of the type (v and what its rounding left), which costs nothing here and
 // saves a rounding.  With JOIN (few tokens, MT = 1) the block joins them
-// itself, else they are in o_lat.
+// itself, else they are in o_lat.  Bound by the chain of reads before its short
+// product (144 tokens of 16 heads: 10.7 us alone).
 template <int DT, int MT, bool JOIN>
 __global__ void __launch_bounds__(JOIN ? 512 : 256, JOIN ? 1 : 3) latent_out_kernel(const __grid_constant__ LatentParams p) {
     static_assert(!JOIN || MT == 1, "a row per warp at least");
@@ -1088,7 +1102,8 @@ __global__ void __launch_bounds__(JOIN ? 512 : 256, JOIN ? 1 : 3) latent_out_ker
 // columns a thread and SUB threads a column, into out or (fp32, for the product
 // that follows) o_lat; rows of whole units are there already.  SUB = 4
 // shortens the sums of few rows, 1 leaves room for more blocks (4096 rows of 3
-// shares: 25 us with 4).
+// shares: 25 us with 4, 13 with 1, from DRAM).  Bound by latency: two look-ups,
+// then the sums.
 template <int DT, int SUB>
 __global__ void __launch_bounds__(128 * SUB) latent_join_kernel(const __grid_constant__ LatentParams p) {
     __shared__ float4 spread[SUB][128];

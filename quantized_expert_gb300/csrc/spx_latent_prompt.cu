@@ -53,7 +53,11 @@ __device__ __forceinline__ size_t value_unit(int tile, int t, int unit) {
 // accumulators.  A product of 256 columns takes 512 cycles a stage, in which an
 // SM would have to fetch 32 KB from L2, 64 bytes a cycle and more than it gets:
 // two blocks of neighbouring token tiles form one product of 256 tokens, for
-// which each holds one of the two matrices, 32 bytes a cycle.
+// which each holds one of the two matrices, 32 bytes a cycle (each fetching one
+// for both by multicast: 154 us for four prompt chunks, halved 147).  A head's
+// 8 stages take 4430 cycles while nothing else moves and 5000 beside the stores
+// of the head before: 4096 tokens and 16 heads 15 us, 1.15 PFLOP/s.  Keys and
+// values are rounded to the type once, as a cache of them would be.
 constexpr int kExStages = 6;
 constexpr int kExStage = kPiece;  // this block's half of B
 constexpr int kExThreads = 384;  // copies of W, products, 2 warps' copies of A, 8 epilogue warps
@@ -260,14 +264,18 @@ __global__ void __launch_bounds__(kExThreads, 1)
 // are long complete cost 150 cycles each, and with one issuing warp for both
 // they left the tensor cores idle half the time.  The two pass a turn to each
 // other, for otherwise they fall into step, both softmaxes at once and then
-// both products (3900 cycles per key tile instead of 2900).  Tensor memory:
+// both products (3900 cycles per key tile instead of 3100).  Tensor memory:
 // S_0, S_1, O_0, O_1, 128 columns each.  Shared memory: Q 96 KB, keys in a
 // ring of 5 pieces (128 tokens x 64), values in one of 3 halves (64 tokens x
 // 128).
 //
 // Per key tile 2 (768 + 512) cycles of products against 2 x 16384 exponentials;
-// the keys and values of a tile, 80 KB, come once per 256 rows (32 bytes a
-// cycle and SM).
+// the keys and values of a tile, 80 KB, come once per 256 rows (26 bytes a
+// cycle and SM).  3100 cycles: a softmax takes 1250 from S to the last of P, and
+// a slot of either ring is free too late for the copy into it to be there when
+// it is wanted (6 + 2 pieces 78 us for 4096 tokens, 4 + 4 85, 5 + 3 75; half
+// pieces 78, for twice the copies and commits).  4096 tokens, 16 heads: 58 us.
+// P is rounded to the type, scaled by 2^kFaShift off the subnormals of fp16.
 constexpr int kFaThreads = 384;  // copies of Q and K, two issuers of products, copies of V; 4 softmax warps per tile
 constexpr int kKRing = 5, kVRing = 3;
 struct FaMisc {
