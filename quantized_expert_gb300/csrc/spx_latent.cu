@@ -1266,9 +1266,9 @@ ExpandedLayout expanded_layout(int B, int max_len, int heads) {
 // head) row of the joined results.  Expanded: 3.4 per key tile of 128 tokens,
 // head and SM to write keys and values, 2.2 per key tile in which a block attends
 // (blocks of 256 rows; few of them leave SMs idle).  Measured, absorbed /
-// expanded: 16 heads, 4 x 4096 cached, 64 rows 81 / 120, 256 rows 249 / 129; 1 x
-// 16384, 256 rows 199 / 300; 1 x 600, 32 rows 27 / 19; 32 heads, 4 x 4096, 96
-// rows 196 / 187.
+// expanded: 16 heads, 4 x 4096 cached, 64 rows 81 / 114, 256 rows 249 / 118; 1 x
+// 16384, 256 rows 197 / 269; 1 x 600, 32 rows 25 / 20; 32 heads, 4 x 4096, 96
+// rows 197 / 176.
 int latent_form(int form, int B, int max_q, int max_len, int heads, int dn, int dv) {
     if (form != SPX_LATENT_AUTO) return form;
     if (dn != 128 || dv != 128) return SPX_LATENT_ABSORBED;

@@ -276,6 +276,7 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t val, int k, LogprobSmem 
             hi = mid;
         }
     }
+    __syncthreads();  // (s.lo and s.hi are written again)
     return lo;
 }
 
