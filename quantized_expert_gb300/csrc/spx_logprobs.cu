@@ -105,52 +105,68 @@ __device__ __forceinline__ float floor_nan(float a, float low) {
     return r;
 }
 
-// 16 bytes of a row: kN elements from index v0 on, those outside [0, V) as -inf.
+// 32 bytes of a row: kN elements from index v0 on, those outside [0, V) as -inf.
+struct Raw {
+    uint32_t w[8];
+};
 template <int DT>
 struct Chunk {
     using T = typename Elem<DT>::T;
-    static constexpr int kN = 16 / (int)sizeof(T);
-    static __device__ __forceinline__ uint4 load(const T *x, int v0, int V) {
-        if (v0 >= 0 && v0 + kN <= V) return __ldg(reinterpret_cast<const uint4 *>(x + v0));
-        uint4 r;
+    static constexpr int kN = 32 / (int)sizeof(T);
+    static constexpr int kDT = DT == SPX_F32 ? SPX_F16 : DT;
+    static __device__ __forceinline__ Raw load(const T *x) {
+        Raw r;
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                       "=r"(r.w[7])
+                     : "l"(x));
+        return r;
+    }
+    static __device__ __forceinline__ Raw load(const T *x, int v0, int V) {
+        if (v0 >= 0 && v0 + kN <= V) return load(x + v0);
+        Raw r;
         T *e = reinterpret_cast<T *>(&r);
 #pragma unroll
         for (int i = 0; i < kN; ++i) e[i] = v0 + i >= 0 && v0 + i < V ? x[v0 + i] : Elem<DT>::down(-INFINITY);
         return r;
     }
-    static __device__ __forceinline__ void unpack(const uint4 &r, float (&f)[kN]) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    static __device__ __forceinline__ void unpack(const Raw &r, float (&f)[kN]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (kN == 4) {
-                f[i] = __uint_as_float(w[i]);
+        for (int i = 0; i < 8; ++i) {
+            if (DT == SPX_F32) {
+                f[i] = __uint_as_float(r.w[i]);
             } else {
-                const float2 p = Elem<DT == SPX_F32 ? SPX_F16 : DT>::up2(w[i]);
-                f[kN == 4 ? i : 2 * i] = p.x;
-                f[kN == 4 ? i : 2 * i + 1] = p.y;
+                const float2 p = Elem<kDT>::up2(r.w[i]);
+                f[kN == 8 ? i : 2 * i] = p.x;
+                f[kN == 8 ? i : 2 * i + 1] = p.y;
             }
         }
     }
     // the largest (a NaN loses; NaN if all are)
-    static __device__ __forceinline__ float largest(const uint4 &r) {
-        if (kN == 4)
-            return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
-        const float2 p = Elem<DT == SPX_F32 ? SPX_F16 : DT>::up2(max_pair<DT>(max_pair<DT>(r.x, r.y), max_pair<DT>(r.z, r.w)));
+    static __device__ __forceinline__ float largest(const Raw &r) {
+        if (DT == SPX_F32) {
+            float m = __uint_as_float(r.w[0]);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m = fmaxf(m, __uint_as_float(r.w[i]));
+            return m;
+        }
+        uint32_t m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = max_pair<kDT>(r.w[i], r.w[i + 4]);
+        const float2 p = Elem<kDT>::up2(max_pair<kDT>(max_pair<kDT>(m[0], m[1]), max_pair<kDT>(m[2], m[3])));
         return fmaxf(p.x, p.y);
     }
     // What the lowest values count as.  A -inf has weight 0 and must not meet an
     // infinite exponent in d; and a difference from it, taken by a product with log2(e)
     // that is rounded, is still right to 1.
     static constexpr float kFloor = DT == SPX_F16 ? -65504.f : -16777216.f;
-    static __device__ __forceinline__ uint4 floored(const uint4 &r) {
-        if (kN == 4)
-            return make_uint4(__float_as_uint(floor_nan(__uint_as_float(r.x), kFloor)),
-                              __float_as_uint(floor_nan(__uint_as_float(r.y), kFloor)),
-                              __float_as_uint(floor_nan(__uint_as_float(r.z), kFloor)),
-                              __float_as_uint(floor_nan(__uint_as_float(r.w), kFloor)));
+    static __device__ __forceinline__ Raw floored(const Raw &r) {
         constexpr uint32_t low = DT == SPX_F16 ? 0xFBFFFBFFu : 0xCB80CB80u;  // kFloor
-        return make_uint4(floor_pair<DT>(r.x, low), floor_pair<DT>(r.y, low), floor_pair<DT>(r.z, low),
-                          floor_pair<DT>(r.w, low));
+        Raw o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o.w[i] = DT == SPX_F32 ? __float_as_uint(floor_nan(__uint_as_float(r.w[i]), kFloor)) : floor_pair<kDT>(r.w[i], low);
+        return o;
     }
 };
 // A maximum above kLarge sends its row through exact passes: the differences in
@@ -172,7 +188,7 @@ struct Running {
     float m = -INFINITY, ref = -INFINITY;
     uint64_t minus_rc = 0, z = 0, d = 0;  // minus the reference, times log2(e)
     int at;  // chunk of the first maximum
-    __device__ __forceinline__ float take(const uint4 &raw, int c) {
+    __device__ __forceinline__ float take(const Raw &raw, int c) {
         using C = Chunk<DT>;
         const float mx = C::largest(raw);
         at = mx > m ? c : at;
@@ -210,6 +226,7 @@ struct LogprobSmem {
     uint32_t lo[kWarpsLp], hi[kWarpsLp];
     int n_cand, n_slices, slices[kThreadsLp];
     int n_high, high[kHigh];
+    uint64_t few[2 * kMaxTop];
     int slow;
 };
 
@@ -291,8 +308,8 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
     const int nb = gridDim.x, row = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const T *x = static_cast<const T *>(p.logits) + (int64_t)row * p.stride;
-    // chunk c holds the elements N c - shift on, so that its 16 bytes are aligned
-    const int shift = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    // chunk c holds the elements N c - shift on, so that its 32 bytes are aligned
+    const int shift = (int)((reinterpret_cast<uintptr_t>(x) & 31) / sizeof(T));
     const int chunks = (p.V + shift + N - 1) / N, share = (chunks + nb - 1) / nb;
     const int c0 = (int)rank * share, c1 = min(chunks, c0 + share);
 
@@ -305,7 +322,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
     }
     Running<DT> run;
     run.at = c0 + tid;
-    constexpr int kAhead = 4;  // loads in flight per thread
+    constexpr int kAhead = 3;  // loads in flight per thread
     const int whole = min(c1, (p.V + shift) / N);  // chunks that do not reach past the row
     // After the first chunks of each thread (an eighth) comes a first bound for the
     // alternatives, and the chunks that reach it are noted from there on.
@@ -314,7 +331,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
     const int first = noting ? (per / 8 + kAhead - 1) / kAhead * kAhead : per;
     float bound = INFINITY;
     if (tid == 0) s.n_cand = s.n_slices = s.n_high = 0;
-    const auto take = [&](const uint4 &raw, int c) {
+    const auto take = [&](const Raw &raw, int c) {
         if (run.take(raw, c) >= bound) {
             const int n = atomicAdd(&s.n_high, 1);
             if (n < kHigh) s.high[n] = c;
@@ -323,11 +340,11 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
     int c = c0 + tid;
 #pragma unroll 1
     for (; c + (kAhead - 1) * kThreadsLp < whole; c += kAhead * kThreadsLp) {
-        uint4 raw[kAhead];
+        Raw raw[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int v0 = N * (c + u * kThreadsLp) - shift;
-            raw[u] = u == 0 && v0 < 0 ? C::load(x, v0, p.V) : __ldg(reinterpret_cast<const uint4 *>(x + v0));
+            raw[u] = u == 0 && v0 < 0 ? C::load(x, v0, p.V) : C::load(x + v0);
         }
         if (noting && c - tid == c0 + first * kThreadsLp) {
             const uint32_t o = reached_by(order32(run.m), p.k, s);
@@ -338,7 +355,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
     }
 #pragma unroll 1
     for (; c < c1; c += kAhead * kThreadsLp) {
-        uint4 raw[kAhead];
+        Raw raw[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
             if (c + u * kThreadsLp < c1) raw[u] = C::load(x, N * (c + u * kThreadsLp) - shift, p.V);
@@ -409,7 +426,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
             const int slice = i / each;
             const int c = i < slices ? c0 + s.slices[slice] + (i - slice * each) * kThreadsLp : s.high[i - slices];
             if (c >= c1) continue;
-            const uint4 raw = C::load(x, N * c - shift, p.V);
+            const Raw raw = C::load(x, N * c - shift, p.V);
             if (!(C::largest(raw) >= tau_value)) continue;
             float f[N];
             C::unpack(raw, f);
@@ -429,13 +446,38 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
             if (tid == 0) s.n_cand = p.k;
             __syncthreads();
         }
+        int n = s.n_cand;
+        const uint64_t *list = s.cand;
+        // Ties leave many (all of a chunk's elements next to the one that counted):
+        // a higher bound among them, found as the first, before they are ranked.
+        if (n > kThreadsLp) {
+            uint64_t lo = tau, end = ((uint64_t)hi32 << 32) + 0xffffffffull;
+            int over = n;
+            while (over > 2 * p.k && end - lo > 1) {
+                const uint64_t mid = lo + (end - lo) / 2;
+                int c = 0;
+                for (int i = 0; i < n; i += kThreadsLp) c += __syncthreads_count(i + tid < n && s.cand[i + tid] >= mid);
+                if (c >= p.k) {
+                    lo = mid;
+                    over = c;
+                } else {
+                    end = mid;
+                }
+            }
+            if (tid == 0) s.n_slices = 0;
+            __syncthreads();
+            for (int i = tid; i < n; i += kThreadsLp)
+                if (s.cand[i] >= lo) s.few[atomicAdd(&s.n_slices, 1)] = s.cand[i];
+            __syncthreads();
+            list = s.few;
+            n = s.n_slices;
+        }
         // the block's alternatives, to block 0
-        const int n = s.n_cand;
         for (int i = tid; i < n; i += kThreadsLp) {
-            const uint64_t kk = s.cand[i];
+            const uint64_t kk = list[i];
             int r = 0;
 #pragma unroll 8
-            for (int j = 0; j < n; ++j) r += s.cand[j] > kk;
+            for (int j = 0; j < n; ++j) r += list[j] > kk;
             // (a pass over too short a stretch leaves zeros)
             if (r < p.k && kk) cluster_st(cluster_addr(&s.top[rank][r], 0), kk);
         }
