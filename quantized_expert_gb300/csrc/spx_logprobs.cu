@@ -13,13 +13,13 @@
 // eighth of their elements, and the chunks that reach it are noted from there on;
 // at the end only these, and the first eighth of the few threads whose maximum
 // reaches the last bound, are read again (from L2), and the elements that reach
-// it are ranked by counting.  (All the chunks of such threads read again: 63 us
-// for 1088 rows of 102400 in bf16 and 20 alternatives, noted 56 us, without
-// alternatives 45 us.)
+// it are ranked by counting.  (1088 rows of 102400 in bf16 with 20 alternatives:
+// 52.5 us; all the chunks of such threads read again, 7 us more; without
+// alternatives 39.6.)
 //
-// What bounds it: 4.0 TB/s of logits, where a copy runs at 6.8: an
-// element takes 11 instructions, 60% of the issue slots are taken, and 1088 rows
-// are 1.8 waves of blocks (608 rows, one wave: 31 us; fp32, 544 rows: 5.0 TB/s).
+// What bounds it: 4.25 TB/s of logits, where a copy runs at 6.8: 60% of the issue
+// slots are taken, and 1088 rows are 1.8 waves of blocks (608 rows, one wave: 29
+// us; fp32, 544 rows: 5.5 TB/s).
 #include "spx_latent.cuh"
 
 #include <math.h>
@@ -297,7 +297,8 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t val, int k, LogprobSmem 
     return lo;
 }
 
-// One cluster per row, its blocks taking equal stretches of it.
+// One cluster per row, its blocks taking equal stretches of it.  Four blocks an
+// SM, for the registers of the loads in flight (five: 56 us for 52.5).
 template <int DT>
 __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_constant__ LogprobParams p) {
     using E = Elem<DT>;
@@ -580,9 +581,9 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
 // Blocks per row: doubled while there are fewer than 256 of them (1.7 an SM),
 // to a portable cluster at most, and while each keeps 16 KB of the row; a block
 // costs some 5 us of its own.  Measured with 102400 logits a row, blocks 1, 2,
-// 4, 8 (us): 17 rows fp32 18.2, 12.4, 9.7, 8.3; 64 rows bf16 15.0, 11.6, 10.5,
-// 13.5; 152 rows 15.2, 13.5, 18.5, 25.7; 608 rows 30.9, 39.4, 57.4, 83.6; 17
-// rows of 32000 8.2, 8.0, 7.6, 8.8.
+// 4, 8 (us): 17 rows fp32 14.0, 10.5, 8.5, 8.0; 64 rows bf16 13.6, 10.7, 10.9,
+// 13.6; 152 rows 14.2, 12.6, 17.9, 25.6; 608 rows 29.3, 36.6, 53.5, 83.7; 17
+// rows of 32000 8.0, 7.3, 7.6, 9.9.
 int blocks_per_row(int N, int64_t bytes) {
     int nb = 1;
     while (nb < kMaxCluster && (int64_t)N * nb < 256 && bytes / (2 * nb) >= 16000) nb *= 2;
