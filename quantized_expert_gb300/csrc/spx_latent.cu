@@ -1094,7 +1094,7 @@ __global__ void __launch_bounds__(JOIN ? 512 : 256, JOIN ? 1 : 3) latent_out_ker
         *reinterpret_cast<uint32_t *>(p.out + (n0 + r) * p.out_stride + (size_t)h * p.dv + d) =
             Elem<DT>::down2(a.x, a.y);
     }
-    cluster_arrive();
+    cluster_arrive_relaxed();  // the others have read this block's sums
     cluster_wait();
 }
 

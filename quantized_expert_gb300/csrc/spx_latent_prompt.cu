@@ -244,13 +244,13 @@ __global__ void __launch_bounds__(kExThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_arrive();  // both are done with the other's memories and barriers
+    cluster_arrive_relaxed();  // both are done with the other's memories and barriers
     cluster_wait();
     if (warp == 1) {
         tc_fence_after();
         pair_tmem_dealloc(tmem, 512);
     }
-    cluster_arrive();
+    cluster_arrive_relaxed();
     cluster_wait();
 }
 

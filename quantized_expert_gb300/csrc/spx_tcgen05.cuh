@@ -95,8 +95,10 @@ __device__ __forceinline__ uint32_t smem_of_rank(const void *p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
 }
+// (Relaxed: it tells that tensor memory has been read, into registers by then; a
+// release would wait for the global stores before it.)
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Copies into this block that count on a barrier of either block of the pair (an address by smem_of_rank).
 __device__ __forceinline__ void pair_load_3d(void *dst, const CUtensorMap *tm, int x, int y, int z, uint32_t bar,
