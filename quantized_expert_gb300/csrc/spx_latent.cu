@@ -173,11 +173,11 @@ struct AttnGeo {
     static constexpr int kSmem = kQBytes + kPairs * kPairBytes + kRopes * kRopeBytes + kMisc;
     static constexpr uint32_t kTmem = NR <= 16 ? 128 : NR <= 32 ? 256 : 512;  // >= 6 NR, a power of two
     static_assert(kSmem <= kSmemLimit, "shared memory of one block");
-    static_assert(kPairs < 12 && kRopes == 3, "at most 3 tiles begun: 4 landing barriers never lap");
+    static_assert(kPairs <= 12 && kRopes <= 4, "a landing barrier and a release for each slot");
 };
 
 struct AttnMisc {
-    uint64_t full[4];             // a tile's copies have landed (one arrival per copying warp)
+    uint64_t pfull[12], rfull[4];    // copies have landed, by slots: pairs, rotated parts
     uint64_t pempty[12], rempty[4];  // slots free: pairs, rotated parts
     uint64_t qfull, qempty;       // the unit's queries landed / read for the last time
     uint64_t sfull[2];            // S^T of a tile is in tensor memory
@@ -364,14 +364,11 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
         tmem_alloc(&m.tmem, G::kTmem);
         tmem_relinquish();
     } else if (warp == kQueryWarp) {
-        // a barrier a lane; the words from full to fin are all barriers
-        uint64_t *bars = m.full;
-        constexpr int kBars = 4 + 12 + 4 + 2 + 2 + 2 + 3;
-        if (lane < kBars)
-            mbar_init(&bars[lane], lane < 4 ? np
-                                    : &bars[lane] == m.wfull || &bars[lane] == m.wfull + 1 || &bars[lane] == &m.ofree
-                                        ? 4 * G::kShares
-                                        : 1);
+        // the words from pfull to fin are all barriers
+        uint64_t *bars = m.pfull;
+        constexpr int kBars = 12 + 4 + 12 + 4 + 2 + 2 + 2 + 3;
+        for (int i = lane; i < kBars; i += 32)
+            mbar_init(&bars[i], &bars[i] == m.wfull || &bars[i] == m.wfull + 1 || &bars[i] == &m.ofree ? 4 * G::kShares : 1);
         if (lane == 0) m.abort = 0;
         fence_mbar_init();
         if (lane == 0) {
@@ -393,7 +390,6 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
         // ---- copies: warp c takes pair c of every tile, warp 0 the rotated part too
         const uint64_t pol = p.groups > 1 ? policy_evict_normal() : policy_evict_first();
         const int bt = p.box_tokens, nb = kTile / bt;  // boxes do not cross a page
-        uint32_t tc = 0;
         Slot<PR> ps;
         Slot<RR> rs;
         ps.i = warp;
@@ -402,7 +398,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
             const int32_t *tab = p.table + (size_t)w.b * p.max_pages;
             int box = 32, my_page = 0, my_at = 0;  // this lane's box of the 32 looked up together
 #pragma unroll 1
-            for (int i = w.tile; i < w.end; ++i, ++tc, box += nb) {
+            for (int i = w.tile; i < w.end; ++i, box += nb) {
                 if (box >= 32) {
                     const int pos = kTile * i + bt * lane, pi = p.by_page(pos);
                     my_at = pos - pi * p.page_size;
@@ -411,13 +407,16 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     if (my_page < 0 || my_page >= p.num_pages) my_page = p.num_pages;
                     box = 0;
                 }
-                uint64_t *full = &m.full[tc & 3];
-                // a tile is begun once its rotated slot is free, so that a landing barrier never laps
-                if (!(ok = ctl_wait(&m.rempty[rs.i], rs.phase ^ 1, ctl) && ctl_wait(&m.pempty[ps.i], ps.phase ^ 1, ctl)))
+                uint64_t *full = &m.pfull[ps.i], *rfull = &m.rfull[rs.i];
+                if (!(ok = (warp || ctl_wait(&m.rempty[rs.i], rs.phase ^ 1, ctl)) &&
+                           ctl_wait(&m.pempty[ps.i], ps.phase ^ 1, ctl)))
                     break;
                 uint8_t *dst = pairs + ps.i * kPairBytes, *rope = ropes + rs.i * kRopeBytes;
                 const bool lead = elect_one();
-                if (lead) mbar_arrive_expect_tx(full, kPairBytes + (warp == 0 ? kRopeBytes : 0));
+                if (lead) {
+                    mbar_arrive_expect_tx(full, kPairBytes);
+                    if (warp == 0) mbar_arrive_expect_tx(rfull, kRopeBytes);
+                }
 #pragma unroll 1
                 for (int j = 0; j < nb; ++j) {
                     const int at = __shfl_sync(0xffffffffu, my_at, box + j);
@@ -427,7 +426,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                         if (nb > 1)
                             tma_load_4d(dst + kPairBytes / 2 + j * bt * 128, &maps.pair, 0, at, 2 * warp + 1, page, full,
                                         pol);
-                        if (warp == 0) tma_load_4d(rope + j * bt * 128, &maps.rope, 0, at, 2 * np, page, full, pol);
+                        if (warp == 0) tma_load_4d(rope + j * bt * 128, &maps.rope, 0, at, 2 * np, page, rfull, pol);
                     }
                 }
                 __syncwarp();
@@ -491,7 +490,9 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     orp.next();
                     ++to;
                     since = 0;
-                } else if (room && mbar_test(&m.full[ts & 3], (ts >> 2) & 1)) {
+                } else if (room && mbar_test(&m.pfull[sp.i], sp.phase)) {
+                    // begun with the first pair: the others follow within its products, mostly
+                    bool landed = true;
                     tc_fence_after();
                     const uint32_t sd = tmem + s_col + (ts & 1) * NR;
                     if (elect_one()) {
@@ -500,6 +501,8 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                         uint64_t q = qd;
 #pragma unroll 1
                         for (int c = 0; c < np; ++c) {
+                            if (c && !mbar_test(&m.pfull[k.i], k.phase) && !(landed = ctl_wait(&m.pfull[k.i], k.phase, ctl)))
+                                break;
                             const uint64_t a = kd + k.i * (kPairBytes / 16);
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
@@ -508,13 +511,16 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                             q += 2 * NR * 8;
                             k.next();
                         }
-                        const uint64_t a = rd + sr.i * (kRopeBytes / 16);
+                        if (landed) landed = mbar_test(&m.rfull[sr.i], sr.phase) || ctl_wait(&m.rfull[sr.i], sr.phase, ctl);
+                        if (landed) {
+                            const uint64_t a = rd + sr.i * (kRopeBytes / 16);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) umma_f16(sd, a + 2 * j, q + 2 * j, idS, 1);
-                        umma_commit(&m.sfull[ts & 1]);
-                        if (ts + 1 == t1) umma_commit(&m.qempty);
+                            for (int j = 0; j < 4; ++j) umma_f16(sd, a + 2 * j, q + 2 * j, idS, 1);
+                            umma_commit(&m.sfull[ts & 1]);
+                            if (ts + 1 == t1) umma_commit(&m.qempty);
+                        }
                     }
-                    __syncwarp();
+                    if (!(ok = __all_sync(0xffffffffu, landed))) break;
                     sp.advance(np);
                     sr.next();
                     ++ts;
