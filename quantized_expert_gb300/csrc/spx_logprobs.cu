@@ -3,7 +3,7 @@
 //
 // With a reference m and t_v = (x_v - m) log2(e) a row needs z = sum 2^t_v and
 // d = sum t_v 2^t_v:  log_z = m + ln z,  entropy = ln z - ln(2) d / z.  Every
-// thread keeps a reference of its own (its running maximum), its z and d, and
+// thread keeps a reference of its own (near its running maximum), its z and d, and
 // the threads' triples are joined at the end, as are those of the blocks that
 // share a row (a cluster).
 //
