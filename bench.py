@@ -47,13 +47,13 @@ GATE_CONFIGS = ("deepseek_v2_lite", "qwen15_moe", "phi35_moe")
 # hash the same; a changed kernel reports null until it is captured again.
 KERNEL_SOURCES = {
     "draft": ["spx_draft.cu", "spx_draft_gguf.cuh", "spx_routing.cuh", "spx_internal.cuh"],
-    "verify": ["spx_tc.cu", "spx_route.cu", "spx_routing.cuh", "spx_internal.cuh"],
+    "verify": ["spx_tc.cu", "spx_tcgen05.cuh", "spx_route.cu", "spx_routing.cuh", "spx_internal.cuh"],
 }
 PROFILED_TRAFFIC = {
-    "verify": {"kernel": "tc_mlp_kernel", "dram_bytes": 677_542_912 + 3_924_480,
-               "algorithmic_bytes": 674_897_920, "source_sha": "09a4a987efe1e0e7"},
-    "draft": {"kernel": "draft_kernel<2,0>", "dram_bytes": 61_500_160 + 238_848, "algorithmic_bytes": 61_374_720,
-              "source_sha": "b75136a8eb199793"},
+    "verify": {"kernel": "tc_mlp_kernel", "dram_bytes": 677_540_864 + 3_668_224,
+               "algorithmic_bytes": 674_897_920, "source_sha": "405684f7481d0356"},
+    "draft": {"kernel": "draft_kernel<2,0>", "dram_bytes": 61_501_952 + 173_824, "algorithmic_bytes": 61_374_720,
+              "source_sha": "09b2f75bd5704629"},
 }
 NSETS = 8  # default; --sets overrides (profiling captures use fewer)
 NINPUTS = 16
