@@ -1326,7 +1326,8 @@ extern "C" int spx_latent_attention(const spx_latent_args *a, spx_stream_t strea
     const spx_latent_cache &c = *a->cache;
     if (!a->q_start || a->N < 0 || a->heads < 1 || a->max_q < 0 || a->max_len < 0) return SPX_ERR_INVALID_ARG;
     if (a->N > 0 && (!a->q || !a->out)) return SPX_ERR_INVALID_ARG;
-    if (!a->w_uk != !a->w_uv || (!a->w_uk && (a->dn || a->dv))) return SPX_ERR_INVALID_ARG;
+    // weights and widths together or neither: the workspace's size goes by the widths, the launches by the weights
+    if (!a->w_uk != !a->w_uv || !a->w_uk != !a->dn || !a->w_uv != !a->dv) return SPX_ERR_INVALID_ARG;
     if (!(a->scale > 0.f) || !(a->scale < INFINITY)) return SPX_ERR_INVALID_ARG;
     if (a->form < 0 || a->form > 2 || !al16(a->q) || !al16(a->out) || !al16(a->w_uk) || !al16(a->w_uv))
         return SPX_ERR_INVALID_ARG;
