@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
 
     griddep_wait();
     griddep_launch_dependents();
+    cluster_arrive_relaxed();  // (awaited before the first store to block 0, which has begun by then)
     float given = NAN;  // the given token's logit
     if (rank == 0 && tid == 0 && p.logp) {
         const int id = p.ids[row];
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
         }
     }
     const bool block_bad = __syncthreads_or(bad);
+    cluster_wait();
 
     if (p.k > 0 && !block_bad) {
         // Upper and lower end of the keys that this thread's maximum may have.
