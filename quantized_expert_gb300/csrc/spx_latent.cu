@@ -183,13 +183,14 @@ struct AttnMisc {
     uint64_t sfull[2];            // S^T of a tile is in tensor memory
     uint64_t wfull[2];            // a tile's weights are in shared memory (all softmax warps)
     uint64_t odone;               // O^T has taken a tile
+    uint64_t udone;               // O^T has taken the last tile of a unit
     uint64_t ofree;               // O^T of the unit has been read out (all softmax warps)
     uint64_t fin;                 // products drained (abort path)
     uint32_t tmem;
     int abort;
     int b, g, off, flat, left, share;  // tiles of a share, and where this block's begins
     LatentReq rq;                      // the request b
-    int pad[3];
+    int pad[1];
     int lim[64];                  // positions that each row sees
     float fac[64];
     float red[2][4][64];
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
     } else if (warp == kQueryWarp) {
         // the words from pfull to fin are all barriers
         uint64_t *bars = m.pfull;
-        constexpr int kBars = 12 + 4 + 12 + 4 + 2 + 2 + 2 + 3;
+        constexpr int kBars = 12 + 4 + 12 + 4 + 2 + 2 + 2 + 4;
         for (int i = lane; i < kBars; i += 32)
             mbar_init(&bars[i], &bars[i] == m.wfull || &bars[i] == m.wfull + 1 || &bars[i] == &m.ofree ? 4 * G::kShares : 1);
         if (lane == 0) m.abort = 0;
@@ -484,6 +485,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                         }
                         umma_commit(&m.rempty[orp.i]);
                         umma_commit(&m.odone);
+                        if (to + 1 == t1) umma_commit(&m.udone);
                     }
                     __syncwarp();
                     op.advance(np);
@@ -551,11 +553,11 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
         const uint32_t quarter = tmem + ((uint32_t)(32 * q) << 16);
         const int cl = c0 + 2 * (lane & 3);    // this lane's rows: 8x + cl, 8x + cl + 1
         const int tok = 16 * q + (lane >> 2);  // its tokens: tok, tok + 8
-        uint32_t tc = 0;
+        uint32_t tc = 0, seg = 0;  // tiles so far, parity of the units
         Slot<RR> rs;
         Slot<PR> ps;
         // (after a wait that gave up the loop runs on, as every warp has to meet the barriers)
-        for (w.begin(p, m); w.left > 0; w.next(p)) {
+        for (w.begin(p, m); w.left > 0; w.next(p), seg ^= 1) {
             const int rows = min(NR, w.rq.T * p.heads - NR * w.g), n16 = (rows + 15) & ~15;
             const int row0 = NR * w.g;
             bar_sync(7, 128 * SH);  // the last unit's limits and sums are read
@@ -660,7 +662,8 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     }
                     if (i > w.tile) {
                         bar_sync(1 + sh, 128);
-                        // (O of the tile before that is done: S of this tile came behind it)
+                        // (O of tile tc - 2 is done, as S of this tile was issued behind it, and O of this one waits
+                        // for this warp's weights: the barrier is in the phase of tc - 1 or just past it)
                         ctl_wait(&m.odone, (tc - 1) & 1, ctl);
                         tc_fence_after();
 #pragma unroll 1
@@ -730,9 +733,8 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                 if (lane == 0) mbar_arrive(&m.wfull[tc & 1]);
             }
             // ---- results of the unit, or of its part in this share
-            // (phase by phase: S of the last tile does not wait for O of the one before)
-            if (w.end - w.tile > 1) ctl_wait(&m.odone, (tc - 2) & 1, ctl);
-            ctl_wait(&m.odone, (tc - 1) & 1, ctl);
+            // (odone may be one or two phases on by now; the next of udone waits for this unit's results)
+            ctl_wait(&m.udone, seg, ctl);
             tc_fence_after();
             const bool whole = w.tile == 0 && w.end == w.nt;
             const int slot = 2 * (int)blockIdx.x + (w.first ? 0 : 1);
