@@ -435,7 +435,6 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                 rs.next();
             }
         }
-        if (!ok) ctl_settle(100000000ull);  // copies in flight land before the block ends
     } else if (warp == kQueryWarp) {
         // ---- the units' queries, each once the last unit's have been read
         const uint64_t pol = policy_evict_normal();
@@ -450,7 +449,6 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
             }
             __syncwarp();
         }
-        if (!ok) ctl_settle(100000000ull);
     } else if (warp == kIssueWarp) {
         // ---- products: whichever is ready, the oldest tile's O first; S at most two tiles ahead of O
         const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
@@ -539,10 +537,6 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     break;
                 }
             }
-        }
-        if (m.abort) {
-            if (elect_one()) umma_commit(&m.fin);
-            ctl_drain(&m.fin, 0, 100000000ull);
         }
     } else {
         // ---- softmax, rescaling, results
@@ -810,6 +804,13 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (m.abort) {
+        if (warp == 0) ctl_settle(kSettleNs);
+        if (warp == kIssueWarp) {
+            if (elect_one()) umma_commit(&m.fin);
+            ctl_drain(&m.fin, 0, kSettleNs);
+        }
+    }
     if (warp == kIssueWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, G::kTmem);

@@ -134,6 +134,12 @@ __device__ __forceinline__ int latent_limit(const LatentParams &p, const LatentR
     return p.causal ? max(r.len - r.T + t + 1, 0) : r.len;
 }
 
+// Where a role of a block gave up, what is in flight is waited for, this long at
+// most, before shared and tensor memory are given back: once every role has left
+// its loops, as those that had nothing more to wait for may have issued copies
+// and products all the same.
+constexpr uint64_t kSettleNs = 100000000ull;
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

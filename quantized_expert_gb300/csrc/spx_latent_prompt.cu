@@ -169,7 +169,6 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 }
                 __syncwarp();
             }
-        if (!ok) ctl_settle(100000000ull);
     } else if (warp == 1) {
         if (rank == 0) {
             // ---- products
@@ -195,10 +194,6 @@ __global__ void __launch_bounds__(kExThreads, 1)
                     }
                     __syncwarp();
                 }
-            }
-            if (m.abort) {
-                if (elect_one()) pair_commit(&m.fin);
-                ctl_drain(&m.fin, 0, 100000000ull);
             }
         }
     } else {
@@ -244,6 +239,16 @@ __global__ void __launch_bounds__(kExThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (m.abort) {
+        // (A block that has not given up has seen its last product, and with it every copy of both blocks; one
+        // that has holds both back at the barrier below.)
+        if (warp == 0) ctl_settle(kSettleNs);
+        if (warp == 1 && rank == 0) {
+            if (elect_one()) pair_commit(&m.fin);
+            ctl_drain(&m.fin, 0, kSettleNs);
+        }
+        __syncwarp();
+    }
     cluster_arrive_relaxed();  // both are done with the other's memories and barriers
     cluster_wait();
     if (warp == 1) {
@@ -390,7 +395,6 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 }
                 __syncwarp();
             }
-        if (!ok) ctl_settle(100000000ull);
     } else if (warp == 3) {
         // ---- copies of V: apart from those of K, which would wait behind them for room
         const uint64_t pol = policy_evict_normal();
@@ -408,7 +412,6 @@ __global__ void __launch_bounds__(kFaThreads, 1)
                 }
                 __syncwarp();
             }
-        if (!ok) ctl_settle(100000000ull);
     } else if (warp < 3) {
         // ---- products of one query tile
         const int x = warp - 1;
@@ -496,10 +499,6 @@ __global__ void __launch_bounds__(kFaThreads, 1)
             }
             __syncwarp();
             kr.next();
-        }
-        if (m.abort) {
-            if (elect_one()) umma_commit(&m.fin[x]);
-            ctl_drain(&m.fin[x], 0, 100000000ull);
         }
     } else if (warp >= 4) {
         // ---- softmax and results: a row a thread
@@ -608,6 +607,14 @@ __global__ void __launch_bounds__(kFaThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (m.abort) {
+        if (warp == 0) ctl_settle(kSettleNs);
+        if (warp == 1 || warp == 2) {
+            if (elect_one()) umma_commit(&m.fin[warp - 1]);
+            ctl_drain(&m.fin[warp - 1], 0, kSettleNs);
+        }
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
