@@ -594,8 +594,11 @@ typedef struct {
 SPX_API int spx_latent_attention(const spx_latent_args *args, spx_stream_t stream);
 /* Workspace of a call with B requests, N query rows (sum over the requests), at
  * most max_q rows and max_len cached tokens each, in the form that such a call
- * takes; 0 if unsupported.  Any larger workspace serves too (a program takes the
- * largest over its calls).  Its status word (spx_workspace_status) is
+ * takes; 0 if unsupported (among others, in the absorbed form: more than 2e9
+ * tiles, B x ceil(max_q x heads / 64) x ceil(max_len / 64) of them, 16 or 32 rows
+ * in place of 64 where they hold max_q x heads; or more than 4194240 rows with
+ * weights: such a call is split).  Any larger workspace serves too (a program
+ * takes the largest over its calls).  Its status word (spx_workspace_status) is
  * SPX_ERR_TIMEOUT after a bounded wait that gave up. */
 SPX_API size_t spx_latent_workspace_size(int B, int N, int max_q, int max_len, int heads, int R, int P, int dn, int dv,
                                          int form);

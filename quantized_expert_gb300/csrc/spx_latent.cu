@@ -1319,6 +1319,10 @@ extern "C" size_t spx_latent_workspace_size(int B, int N, int max_q, int max_len
     if ((dn != 0) != (dv != 0) || (dn && dn != 64 && dn != 128) || (dv && dv != 64 && dv != 128)) return 0;
     const int used = latent_form(form, B, max_q, max_len, heads, dn, dv);
     if (used == SPX_LATENT_EXPANDED) return dn == 128 && dv == 128 ? expanded_layout(B, max_len, heads).bytes : 0;
+    // So are the tiles of all units, whatever q_start and lens hold; and the grid of the products with the
+    // up-projections ends at 65535 blocks of 64 tokens.
+    const long long nr = rows_per_unit(max_q, heads), rows = (long long)(max_q < N ? max_q : N) * heads;
+    if ((double)B * ((rows + nr - 1) / nr) * ((max_len + 63) / 64) > 2e9 || (dn && N > 64 * 65535)) return 0;
     return absorbed_layout(B, N, max_q, heads, R, P, dn != 0).bytes;
 }
 

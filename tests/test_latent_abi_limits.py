@@ -4,7 +4,7 @@ import ctypes as C
 
 import pytest
 
-from test_latent_abi import INV, attention, cache, lib  # noqa: F401
+from test_latent_abi import INV, UNS, attention, cache, lib  # noqa: F401
 
 
 @pytest.mark.parametrize("bad", [
@@ -16,3 +16,29 @@ def test_weights_and_widths_belong_together(lib, bad):  # noqa: F811
     for form in (0, 1, 2):
         a = attention(c, form=form, **bad)
         assert lib.spx_latent_attention(C.byref(a), None) == INV
+
+
+@pytest.mark.parametrize("kw,fits", [
+    # tiles of 64 tokens times units of rows: B x ceil(max_q x heads / 64) x ceil(max_len / 64), counted in 31 bits
+    (dict(B=1024, N=1 << 22, max_q=4096, max_len=1 << 17, heads=16), False),
+    (dict(B=64, N=64 * 4096, max_q=4096, max_len=1 << 16, heads=128), True),
+    (dict(B=1, N=1 << 20, max_q=1 << 20, max_len=1 << 20, heads=128), False),
+    (dict(B=1, N=1 << 14, max_q=1 << 14, max_len=1 << 20, heads=128), True),
+    # (only as many rows as there are)
+    (dict(B=1, N=17, max_q=1 << 20, max_len=1 << 20, heads=128), True),
+    # tokens of the products with the up-projections: 64 a block, 65535 blocks in the grid's third dimension
+    (dict(B=1, N=64 * 65535, max_q=1, max_len=100, heads=16, dn=128, dv=128), True),
+    (dict(B=1, N=64 * 65535 + 1, max_q=1, max_len=100, heads=16, dn=128, dv=128), False),
+    (dict(B=1, N=64 * 65535 + 1, max_q=1, max_len=100, heads=16), True)])
+def test_counts_that_do_not_fit_are_refused(lib, kw, fits):  # noqa: F811
+    from quantized_expert_gb300 import spx
+    assert (spx.spx_latent_workspace_size(form=spx.SPX_LATENT_ABSORBED, **kw) > 0) == fits
+    if fits:
+        return
+    c = cache(B=kw["B"])
+    a = attention(c, form=spx.SPX_LATENT_ABSORBED, N=kw["N"], heads=kw["heads"], max_q=kw["max_q"],
+                  max_len=kw["max_len"], q_stride=1 << 20, out_stride=1 << 20, ws_bytes=1 << 62)
+    if not kw.get("dn"):
+        a.w_uk = a.w_uv = None
+        a.dn = a.dv = 0
+    assert lib.spx_latent_attention(C.byref(a), None) == UNS
