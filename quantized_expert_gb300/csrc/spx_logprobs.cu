@@ -252,12 +252,12 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 // NaN or a maximum above kLarge, and more candidates than the buffer holds.
 template <int DT>
 __device__ void top_by_passes(const typename Elem<DT>::T *x, int lo, int hi, int k, uint64_t *top, uint64_t *scratch) {
-    uint64_t last = ~0ull;
+    uint64_t last = 0;
     for (int j = 0; j < k; ++j) {
         uint64_t best = 0;
         for (int v = lo + threadIdx.x; v < hi; v += kThreadsLp) {
             const uint64_t key = order64(Elem<DT>::up(x[v]), v);
-            if (key < last && key > best) best = key;
+            if ((j == 0 || key < last) && key > best) best = key;  // (a NaN at index 0 is the largest key there is)
         }
         for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
         __syncthreads();
