@@ -1,11 +1,13 @@
 // spx_logprobs.cu -- log probabilities of given tokens, entropy and the most
 // likely alternatives of rows of logits, in one pass over memory.
 //
-// With a reference m and t_v = (x_v - m) log2(e) a row needs z = sum 2^t_v and
-// d = sum t_v 2^t_v:  log_z = m + ln z,  entropy = ln z - ln(2) d / z.  Every
-// thread keeps a reference of its own (near its running maximum), its z and d, and
-// the threads' triples are joined at the end, as are those of the blocks that
-// share a row (a cluster).
+// With a reference r (in base 2) and t_v = x_v log2(e) - r a row needs z = sum
+// 2^t_v and d = sum t_v 2^t_v:  log p_v = ln(2) t_v - ln z,  entropy = ln z - ln(2)
+// d / z.  Every thread keeps a reference of its own (near its running maximum), its
+// z and d, and the threads' triples are joined at the end, as are those of the
+// blocks that share a row (a cluster).  References are kept as they were rounded:
+// then t_v is one rounding of its exact value, whatever the size of x_v, and what
+// log2(e) itself lacks is 1e-8 of x_v - x_w between any two.
 //
 // Alternatives: each thread also remembers where its maximum lies.  A bound
 // that between k and 2k of the threads' maxima reach (found by bisection) is
@@ -58,7 +60,7 @@ __device__ __forceinline__ float ex2f(float x) {
     return y;
 }
 
-// Reference, sum, and sum weighted by the exponent (in base 2).
+// Reference (in base 2), sum, and sum weighted by the exponent.
 struct Stat {
     float m, z, d;
 };
@@ -67,12 +69,12 @@ __device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
     r.m = fmaxf(a.m, b.m);
     r.z = r.d = 0.f;
     if (a.z != 0.f) {  // (a NaN is not 0)
-        const float t = (a.m - r.m) * kLog2e, f = ex2f(t);
+        const float t = a.m - r.m, f = ex2f(t);
         r.z += a.z * f;
         r.d += (a.d + t * a.z) * f;
     }
     if (b.z != 0.f) {
-        const float t = (b.m - r.m) * kLog2e, f = ex2f(t);
+        const float t = b.m - r.m, f = ex2f(t);
         r.z += b.z * f;
         r.d += (b.d + t * b.z) * f;
     }
@@ -156,9 +158,8 @@ struct Chunk {
         const float2 p = Elem<kDT>::up2(max_pair<kDT>(max_pair<kDT>(m[0], m[1]), max_pair<kDT>(m[2], m[3])));
         return fmaxf(p.x, p.y);
     }
-    // What the lowest values count as.  A -inf has weight 0 and must not meet an
-    // infinite exponent in d; and a difference from it, taken by a product with log2(e)
-    // that is rounded, is still right to 1.
+    // What the lowest values count as: a -inf has weight 0 and must not meet an
+    // infinite exponent in d.
     static constexpr float kFloor = DT == SPX_F16 ? -65504.f : -16777216.f;
     static __device__ __forceinline__ Raw floored(const Raw &r) {
         constexpr uint32_t low = DT == SPX_F16 ? 0xFBFFFBFFu : 0xCB80CB80u;  // kFloor
@@ -169,9 +170,9 @@ struct Chunk {
         return o;
     }
 };
-// A maximum above kLarge sends its row through exact passes: the differences in
-// base 2 are right to 2^-24 of log2(e) times the maximum, 0.1 there, and a larger
-// one could overflow 2^t.  So does a row's maximum that is not above kLow, from
+// A maximum above kLarge sends its row through passes with differences first: a
+// reference is its maximum's to 2^-24 of it, and 2^t could overflow for a much larger
+// one.  So does a row's maximum that is not above kLow, from
 // which the floor is not far enough.  (fp16's next value above its lowest is 32
 // higher: what is floored weighs e^-32 at most there.)
 constexpr float kLarge = 1e6f;
@@ -186,7 +187,8 @@ constexpr float kSlack = 4.f;
 template <int DT>
 struct Running {
     float m = -INFINITY, ref = -INFINITY;
-    uint64_t minus_rc = 0, z = 0, d = 0;  // minus the reference, times log2(e)
+    float rc = 0.f;                       // ref log2(e), rounded: what the exponents refer to
+    uint64_t minus_rc = 0, z = 0, d = 0;
     int at;  // chunk of the first maximum
     __device__ __forceinline__ float take(const Raw &raw, int c) {
         using C = Chunk<DT>;
@@ -194,14 +196,15 @@ struct Running {
         at = mx > m ? c : at;
         m = fmaxf(m, mx);
         if (mx > ref + kSlack) {
-            const float to = fmaxf(mx, C::kFloor);
+            const float to = fmaxf(mx, C::kFloor), to_rc = __fmul_rn(to, kLog2e);  // (not contracted with what follows)
             if (ref > -INFINITY) {
-                const float t = (ref - to) * kLog2e, g = ex2f(t);
+                const float t = rc - to_rc, g = ex2f(t);
                 d = mul2(fma2(pack2(t, t), z, d), pack2(g, g));
                 z = mul2(z, pack2(g, g));
             }
             ref = to;
-            minus_rc = pack2(-to * kLog2e, -to * kLog2e);
+            rc = to_rc;
+            minus_rc = pack2(-rc, -rc);
         }
         float f[C::kN];
         C::unpack(C::floored(raw), f);
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
     Stat a;
     {
         const float2 z = unpack2(run.z), d = unpack2(run.d);
-        a = Stat{run.ref, z.x + z.y, d.x + d.y};
+        a = Stat{run.ref > -INFINITY ? run.rc : -INFINITY, z.x + z.y, d.x + d.y};
         if (run.ref == -INFINITY) a.d = 0.f;  // (nothing but -inf: no weight)
     }
     const int at = run.at;
@@ -514,7 +517,8 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
         slow |= s.part[b].z != s.part[b].z;
         a = join(a, s.part[b]);
     }
-    if (slow || (a.m > -INFINITY && a.m <= kLow<DT>)) {  // two passes, differences first
+    const bool differences = slow || (a.m > -INFINITY && a.m <= kLow<DT> * kLog2e);
+    if (differences) {  // two passes; the reference is the maximum itself from here on
         bool n = false;
         float m = -INFINITY;
         for (int v = tid; v < p.V; v += kThreadsLp) {
@@ -553,10 +557,17 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
     // without a distribution: a NaN, an infinity
     const bool no = slow && (nan || a.m == INFINITY);
     const bool none = !no && a.m == -INFINITY;
-    const float log_z = no ? (nan ? NAN : INFINITY) : none ? 0.f : a.m + logf(a.z);
+    const float ln_z = no || none ? 0.f : logf(a.z);
+    const auto log_p = [&](float f) {
+        if (no) return nan ? NAN : f - INFINITY;
+        if (none) return f;
+        if (differences) return (f - a.m) - ln_z;
+        // (far below the others the product could overflow, and nothing is lost by the plain difference)
+        return f < -2.f * kLarge ? f - fmaf(a.m, kLn2, ln_z) : fmaf(fmaf(f, kLog2e, -a.m), kLn2, -ln_z);
+    };
     if (tid == 0) {
-        if (p.logp) p.logp[row] = given - log_z;
-        if (p.entropy) p.entropy[row] = no ? NAN : none ? 0.f : fmaxf(logf(a.z) - kLn2 * a.d / a.z, 0.f);
+        if (p.logp) p.logp[row] = log_p(given);
+        if (p.entropy) p.entropy[row] = no ? NAN : none ? 0.f : fmaxf(ln_z - kLn2 * a.d / a.z, 0.f);
     }
     if (p.k > 0) {
         if (slow) top_by_passes<DT>(x, 0, p.V, p.k, s.cand, s.key);
@@ -574,7 +585,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
             if (r < p.k) {
                 const int v = (int)~(uint32_t)kk;
                 p.top_ids[(size_t)row * p.k + r] = v;
-                p.top_logp[(size_t)row * p.k + r] = value_of((uint32_t)(kk >> 32)) - log_z;
+                p.top_logp[(size_t)row * p.k + r] = log_p(value_of((uint32_t)(kk >> 32)));
             }
         }
     }
