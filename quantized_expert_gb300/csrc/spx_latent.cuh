@@ -8,7 +8,8 @@
 
 namespace spx {
 
-// Element type by its spx_dtype: conversions to and from fp32, one rounding.
+// Element type by its spx_dtype: conversions to and from fp32, one rounding; of
+// two packed values, a product and sum, and what replaces one that is not finite.
 template <int DT>
 struct Elem;
 template <>
@@ -20,6 +21,16 @@ struct Elem<SPX_F16> {
     static __device__ __forceinline__ uint32_t down2(float a, float b) {
         __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t finite2(uint32_t v, uint32_t other) {
+        if ((v & 0x7C00u) == 0x7C00u) v = (v & 0xFFFF0000u) | (other & 0xFFFFu);
+        if ((v & 0x7C000000u) == 0x7C000000u) v = (v & 0xFFFFu) | (other & 0xFFFF0000u);
+        return v;
     }
 };
 template <>
@@ -33,6 +44,16 @@ struct Elem<SPX_BF16> {
     static __device__ __forceinline__ uint32_t down2(float a, float b) {
         __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t finite2(uint32_t v, uint32_t other) {
+        if ((v & 0x7F80u) == 0x7F80u) v = (v & 0xFFFF0000u) | (other & 0xFFFFu);
+        if ((v & 0x7F800000u) == 0x7F800000u) v = (v & 0xFFFFu) | (other & 0xFFFF0000u);
+        return v;
     }
 };
 template <>

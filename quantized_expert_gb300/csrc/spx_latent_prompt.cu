@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
     tc_fence_after();
     const uint32_t tmem = m.tmem;
     const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_LATENT};
+    uint32_t lost = 0;  // heads (of the block's) in which this lane's token has a value that is not finite
 
     if (warp == 2 || warp == 3) {
         // ---- the latent vectors of 64 tokens
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kExThreads, 1)
             }
         }
     } else {
-        // ---- epilogue: a token a lane, its keys (warps 4-7) or its values
+        // ---- epilogue: a token a lane, its keys (warps 4-7) or its values (warps 8-11)
         const int q = warp & 3, t = t0 + 32 * q + lane;
         const bool live = t < rq.len, values = warp >= 8;
         for (int i = 0; i < nh; ++i) {
@@ -211,22 +212,23 @@ __global__ void __launch_bounds__(kExThreads, 1)
                 uint32_t r[32];
                 tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (i & 1) * 256 + (values ? 128 : 0) + x, r);
                 tmem_wait_ld();
-                // A value that is not finite becomes 0, as its weight 0 elsewhere times it would not be 0; its
-                // key carries it to the rows that see it.  (0 times the 32, summed, is a NaN if one is not.)
-                uint64_t test = 0;
-                if (values)
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2)
-                        test = fma2(pack2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), 0ull, test);
-                const float2 bad = unpack2(test);
-                if (bad.x + bad.y != 0.f)
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!(fabsf(__uint_as_float(r[k])) < INFINITY)) r[k] = 0u;
                 uint32_t o[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k)  // past the length: zeros
                     o[k] = live ? Elem<DT>::down2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])) : 0u;
+                // A value that is not finite, or that the type cannot hold, becomes 0, as its weight 0 in the rows
+                // that do not see it times it would not be 0; a NaN in its key shows it to those that do.  Such a
+                // key becomes a NaN (an infinity's score could be -inf, which only leaves the token out).  (0 times
+                // all of them, summed, is a NaN if one is not finite.)
+                uint32_t test = 0;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) test = Elem<DT>::fma2(o[k], 0u, test);
+                if (test & 0x7FFF7FFFu) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        o[k] = values ? Elem<DT>::finite2(o[k], 0u) : Elem<DT>::finite2(o[k], 0x7FFF7FFFu);
+                    if (values) lost |= 1u << i;
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     *reinterpret_cast<uint4 *>(dst + (x / 8 + k) * step) =
@@ -239,6 +241,11 @@ __global__ void __launch_bounds__(kExThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    for (; lost; lost &= lost - 1) {  // behind the key's own stores
+        const size_t of_head = ((size_t)(h0 + __ffs(lost) - 1) * p.B + b) * p.kv_rows * 128;
+        p.k_x[of_head + key_unit(blockIdx.x, t0 + 32 * (warp & 3) + lane, 0)] = 0x7FFF;
+    }
+    __syncwarp();
     if (m.abort) {
         // (A block that has not given up has seen its last product, and with it every copy of both blocks; one
         // that has holds both back at the barrier below.)
