@@ -190,7 +190,7 @@ struct AttnMisc {
     int abort;
     int b, g, off, flat, left, share;  // tiles of a share, and where this block's begins
     LatentReq rq;                      // the request b
-    int pad[1];
+    int odd;                           // the unit: a latent value that only some rows see is not finite
     int lim[64];                  // positions that each row sees
     float fac[64];
     float red[2][4][64];
@@ -555,6 +555,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
             const int rows = min(NR, w.rq.T * p.heads - NR * w.g), n16 = (rows + 15) & ~15;
             const int row0 = NR * w.g;
             bar_sync(7, 128 * SH);  // the last unit's limits and sums are read
+            if (all == 0) m.odd = 0;
             if (all < NR) m.lim[all] = all < rows ? latent_limit(p, w.rq, p.by_heads(row0 + all)) : 0;
             bar_sync(7, 128 * SH);
             const int lim_lo = m.lim[0], lim_hi = m.lim[rows - 1];
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                 if (masked) {
                     // What some row may not see has weight 0 there, and 0 times an infinity or a NaN would
                     // still reach it: rows of the tile that nobody sees become 0, and in those that only
-                    // some see every value that is not finite (whoever sees it got a NaN from S already).
+                    // some see every value that is not finite (those who see it get theirs with the results).
                     const int t0 = max(lim_lo - p0, 0);
                     Slot<PR> k0 = ps;
 #pragma unroll 1
@@ -709,12 +710,13 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                             uint4 v = make_uint4(0, 0, 0, 0);
                             if (p0 + t < lim_hi) {
                                 v = *at;
-                                uint32_t *h = &v.x;
-                                constexpr uint32_t kExp = DT == SPX_F16 ? 0x7C00u : 0x7F80u;
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    if ((h[y] & kExp) == kExp) h[y] &= 0xFFFF0000u;
-                                    if (((h[y] >> 16) & kExp) == kExp) h[y] &= 0x0000FFFFu;
+                                // (0 times all eight, summed, is a NaN if one is not finite)
+                                uint32_t test = Elem<DT>::fma2(v.x, 0u, Elem<DT>::fma2(v.y, 0u, 0u));
+                                test = Elem<DT>::fma2(v.z, 0u, Elem<DT>::fma2(v.w, 0u, test));
+                                if (test & 0x7FFF7FFFu) {
+                                    v = make_uint4(Elem<DT>::finite2(v.x, 0u), Elem<DT>::finite2(v.y, 0u),
+                                                   Elem<DT>::finite2(v.z, 0u), Elem<DT>::finite2(v.w, 0u));
+                                    m.odd = 1;
                                 }
                             }
                             *at = v;
@@ -797,6 +799,27 @@ __global__ void __launch_bounds__(AttnGeo<NR>::kThreads, 1)
                     }
                 }
             }
+            // A latent value that is not finite makes a NaN of its column in the rows that see it, whatever their
+            // weight; where all rows of a tile see it the products have done so.  (Behind this thread's own stores.)
+            if (m.odd)
+#pragma unroll 1
+                for (int t = max(lim_lo, kTile * w.tile); t < min(lim_hi, kTile * w.end); ++t) {
+                    const int pi = p.by_page(t), pg = __ldg(p.table + (size_t)w.b * p.max_pages + pi);
+                    if (pg < 0 || pg >= p.num_pages) continue;
+                    const uint16_t *src = p.cache + (int64_t)pg * p.page_stride + (int64_t)(t - pi * p.page_size) * p.token_stride;
+#pragma unroll 1
+                    for (int d = tid; d < p.R; d += 128) {
+                        if (Elem<DT>::finite2(src[d], 0u) == src[d]) continue;
+#pragma unroll 1
+                        for (int x = c0; x < min(c0 + NC, rows); ++x) {
+                            if (m.lim[x] <= t) continue;
+                            if (direct)
+                                p.out[at[x] + d] = 0x7FFFu;
+                            else
+                                __stcg(dst + (size_t)x * p.R + d, NAN);
+                        }
+                    }
+                }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&m.ofree);
