@@ -570,8 +570,9 @@ SPX_API int spx_latent_append(const spx_latent_append_args *args, spx_stream_t s
  * 128); SPX_LATENT_AUTO chooses by B, max_q, max_len and heads.  max_q and max_len bound every
  * request's rows and length (larger ones are cut to them).
  * Roundings to the type: q W_uk, the softmax weights, and in the expanded form
- * keys and values.  There a key or value that is not finite or beyond the type's
- * range gives the rows that see its token a NaN in that head. */
+ * keys and values.  A row whose q W_uk is not finite or beyond the type's range
+ * becomes a NaN, and so do, in a head, the rows that see a token whose key or value
+ * is (in the expanded form). */
 enum { SPX_LATENT_AUTO = 0, SPX_LATENT_ABSORBED = 1, SPX_LATENT_EXPANDED = 2 };
 typedef struct {
     const spx_latent_cache *cache;

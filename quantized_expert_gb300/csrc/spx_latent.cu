@@ -100,10 +100,12 @@ __global__ void __launch_bounds__(128) latent_q_kernel(const __grid_constant__ L
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = 16 * m + (lane >> 2) + 8 * (j & 1);
+            // o + 0 o: one that the type cannot hold becomes a NaN, as an infinity's scores could be -inf, which only
+            // leave their tokens out
+            const uint32_t o = Elem<DT>::down2(acc[m][j >> 1][2 * (j & 1)], acc[m][j >> 1][2 * (j & 1) + 1]);
             if (r < rows)
                 *reinterpret_cast<uint32_t *>(p.q_lat + ((size_t)(n0 + r) * p.heads + h) * D + 64 * s + 16 * warp +
-                                              8 * (j >> 1) + 2 * (lane & 3)) =
-                    Elem<DT>::down2(acc[m][j >> 1][2 * (j & 1)], acc[m][j >> 1][2 * (j & 1) + 1]);
+                                              8 * (j >> 1) + 2 * (lane & 3)) = Elem<DT>::fma2(o, 0u, o);
         }
     if (s == 0)
         for (int i = threadIdx.x; i < rows * (p.P / 8); i += 128) {

@@ -34,3 +34,23 @@ def test_one_rotated_value(bad):
     s["kv"][0][195, 512] = bad
     out, _ = call(s, form=1)
     check(s, (out, None), reference(s))
+
+
+@pytest.mark.parametrize("lens,news,heads", [([1], [1], 2), ([40], [3], 16), ([200], [40], 4)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_latent_query_beyond_fp16(lens, news, heads, sign):
+    """q W_uk = 120000 in one latent column: finite in 32 bits, not in fp16.  The row
+    shows it, also where the infinity's scores are all -inf; no other row does."""
+    s = make(lens, news, heads, F16, 64)
+    s["cache"].buf[:, :, 5] = -1.0                         # every cached token has the same sign there
+    s["w_uk"][1, 3, 5] = 2.0 * sign
+    s["w_uk"][1, 3, :5] = 0
+    s["w_uk"][1, 3, 6:] = 0
+    s["q"][:, 1, 3] = 0
+    clean, clean_lse = call(s, form=1)
+    s["q"][0, 1, 3] = 60000.0
+    out, lse = call(s, form=1)
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+    keep = torch.ones_like(lse, dtype=torch.bool)
+    keep[0, 1] = False
+    assert torch.equal(out[keep], clean[keep]) and torch.equal(lse[keep], clean_lse[keep])
