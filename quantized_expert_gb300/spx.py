@@ -632,6 +632,10 @@ def latent_append_args(cache: LatentCache, kv, req, pos, w_norm=None, eps=1e-6, 
     a.cache, a.N = C.pointer(cs), N
     a.kv, a.kv_stride = _rows(kv, "kv")
     a.req, a.pos, a.w_norm, a.eps = _i32(req, "req", (N,)), _i32(pos, "pos", (N,)), _p(w_norm), float(eps)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin: both or neither")
+    if q is None and q_out is not None:
+        raise ValueError("q_out goes with q")
     if cos is not None:
         if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.shape != sin.shape or \
                 cos.dim() != 2 or cos.shape[1] != cache.P // 2:
