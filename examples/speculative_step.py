@@ -64,7 +64,10 @@ class Decoder:
         self.cache = spx.LatentCache(torch.zeros(pages, PAGE, R + P, dtype=torch.float16, device="cuda"), table,
                                      torch.zeros(1, dtype=torch.int32, device="cuda"), R, P)
         self.experts = {}  # workspace and routing buffers by the number of tokens
-        self.workspaces = {}
+        # one attention workspace for every call: the larger of the two forms' for the largest call
+        size = max(spx.spx_latent_workspace_size(1, max_len, max_len, max_len, HEADS, R, P, NOPE, VALUE, form)
+                   for form in (spx.SPX_LATENT_ABSORBED, spx.SPX_LATENT_EXPANDED))
+        self.attn_ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
 
     def attend(self, x, start):
         """Tokens x [T][H] at the positions start ..: to the cache, then attention over it."""
@@ -75,13 +78,10 @@ class Decoder:
                                             cos=self.cos, sin=self.sin, q=q)  # the queries turn in place
         spx.spx_latent_append(args)
         self.cache.lens.fill_(start + T)
-        key = (T, start + T)
-        if key not in self.workspaces:
-            self.workspaces[key] = spx.new_latent_workspace(q, self.cache, T, start + T, self.w_uk, self.w_uv)
         out = torch.empty(T, HEADS, VALUE, dtype=torch.float16, device="cuda")
         rows = torch.tensor([0, T], dtype=torch.int32, device="cuda")
-        args, keep = spx.latent_args(q, self.cache, rows, T, start + T, 1 / math.sqrt(NOPE + P), out,
-                                     self.workspaces[key], w_uk=self.w_uk, w_uv=self.w_uv)
+        args, keep = spx.latent_args(q, self.cache, rows, T, start + T, 1 / math.sqrt(NOPE + P), out, self.attn_ws,
+                                     w_uk=self.w_uk, w_uv=self.w_uv)
         spx.spx_latent_attention(args)
         return x + out.view(T, -1) @ self.w_o.T
 

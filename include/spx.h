@@ -599,8 +599,9 @@ SPX_API int spx_latent_attention(const spx_latent_args *args, spx_stream_t strea
  * takes; 0 if unsupported (among others, in the absorbed form: more than 2e9
  * tiles, B x ceil(max_q x heads / 64) x ceil(max_len / 64) of them, 16 or 32 rows
  * in place of 64 where they hold max_q x heads; or more than 4194240 rows with
- * weights: such a call is split).  Any larger workspace serves too (a program
- * takes the largest over its calls).  Its status word (spx_workspace_status) is
+ * weights: such a call is split).  Any larger workspace serves too: the larger of
+ * the two forms' sizes for a program's largest B, N, max_q and max_len serves all
+ * its calls.  Its status word (spx_workspace_status) is
  * SPX_ERR_TIMEOUT after a bounded wait that gave up. */
 SPX_API size_t spx_latent_workspace_size(int B, int N, int max_q, int max_len, int heads, int R, int P, int dn, int dv,
                                          int form);

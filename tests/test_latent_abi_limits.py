@@ -42,3 +42,15 @@ def test_counts_that_do_not_fit_are_refused(lib, kw, fits):  # noqa: F811
         a.w_uk = a.w_uv = None
         a.dn = a.dv = 0
     assert lib.spx_latent_attention(C.byref(a), None) == UNS
+
+
+def test_one_workspace_serves_every_smaller_call(lib):  # noqa: F811
+    from quantized_expert_gb300 import spx
+    import random
+    rng = random.Random(5)
+    for dn in (0, 128):
+        most = dict(B=32, N=5000, max_q=3000, max_len=20000, heads=16, dn=dn, dv=dn)
+        have = max(spx.spx_latent_workspace_size(form=f, **most) for f in (1, 2))
+        for _ in range(3000):
+            kw = dict(most, **{k: int(round(most[k] ** rng.random())) for k in ("B", "N", "max_q", "max_len")})
+            assert 0 < spx.spx_latent_workspace_size(form=0, **kw) <= have, kw
