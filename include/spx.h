@@ -567,8 +567,11 @@ SPX_API int spx_latent_append(const spx_latent_append_args *args, spx_stream_t s
  * verify calls); SPX_LATENT_EXPANDED writes every head's keys and values to the
  * workspace and attends per head with (R + P + R) / (dn + P + dv) times fewer
  * operations per query-key pair (prompts; needs the weights with dn = dv =
- * 128); SPX_LATENT_AUTO chooses by B, max_q, max_len and heads.  max_q and max_len bound every
- * request's rows and length (larger ones are cut to them).
+ * 128); SPX_LATENT_AUTO chooses by B, max_q, max_len and heads, one form for all
+ * requests: a batch of a prompt's chunk and many single tokens is better split
+ * into two calls, as the expanded form writes out every request's whole cache.
+ * max_q and max_len bound every request's rows and length (larger ones are cut to
+ * them).  What out and lse hold in rows that no request owns is not specified.
  * Roundings to the type: q W_uk, the softmax weights, and in the expanded form
  * keys and values.  A row whose q W_uk is not finite or beyond the type's range
  * becomes a NaN, and so do, in a head, the rows that see a token whose key or value

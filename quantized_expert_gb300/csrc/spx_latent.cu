@@ -14,9 +14,9 @@
 //
 // Every launch is a programmatic dependent of the one before it.  What bounds a
 // call: one request's draft step is a chain of three launches (517 cached tokens
-// 14 us, 65536 27 us); many requests' is the cache (64 of up to 8192 tokens, 370
-// MB: 80 us, of which the attention launch 68 at 5.4 TB/s); with 64 rows a unit
-// it is the ring of tiles (see the attention launch).
+// 15 us, 65536 28 us); many requests' is the cache (64 of up to 8192 tokens, 370
+// MB: 83 us, of which the attention launch 68 at 5.4 TB/s); with 64 rows a unit
+// half of the attention launch is the ring of tiles (see there).
 #include <math.h>
 #include <string.h>
 
@@ -141,8 +141,12 @@ __global__ void __launch_bounds__(128) latent_pack_kernel(const __grid_constant_
 // cycles each) and 16 of 128 x 64 x 16 (48), 1920 cycles on 64 rows, 1200 on
 // 16.  Units of 16 rows wait for DRAM all the same.  Units of 64 rows leave room
 // for two tiles, whose slots are taken from the copy's start to the last
-// product: 2840 cycles a tile (16 requests of 9 x 16 rows over up to 8191
-// tokens: 41 us for 13 of products at the dense rate).
+// product: 2840 cycles a tile.  That is half of the launch (16 requests of 9 x 16
+// rows over up to 8191 tokens: 16 tiles a share, 22 of 41 us; 32 of 2 x 64 rows
+// over up to 4096: 23 of 47).  The other half is the wait for the query launch
+// (7 us in the first, none in the second) and, not told apart by measurement,
+// the units that begin inside a share, whose queries and first O wait for the
+// unit before, and the partial sums.
 //
 // Softmax runs in base 2 with one reference per row; the sums are rescaled
 // only when a maximum rises by more than 2^kSlack over it, which fp32 sums and

@@ -54,7 +54,8 @@ __device__ __forceinline__ size_t value_unit(int tile, int t, int unit) {
 // SM would have to fetch 32 KB from L2, 64 bytes a cycle and more than it gets:
 // two blocks of neighbouring token tiles form one product of 256 tokens, for
 // which each holds one of the two matrices, 32 bytes a cycle (each fetching one
-// for both by multicast: 154 us for four prompt chunks, halved 147).  A head's
+// for both by multicast: 154 us for four prompt chunks replayed from a graph,
+// halved 147; now 140, and 143 in a stream of calls).  A head's
 // 8 stages take 4430 cycles while nothing else moves and 5000 beside the stores
 // of the head before: 4096 tokens and 16 heads 15 us, 1.15 PFLOP/s.  Keys and
 // values are rounded to the type once, as a cache of them would be.
@@ -285,8 +286,9 @@ __global__ void __launch_bounds__(kExThreads, 1)
 // the keys and values of a tile, 80 KB, come once per 256 rows (26 bytes a
 // cycle and SM).  3100 cycles: a softmax takes 1250 from S to the last of P, and
 // a slot of either ring is free too late for the copy into it to be there when
-// it is wanted (6 + 2 pieces 78 us for 4096 tokens, 4 + 4 85, 5 + 3 75; half
-// pieces 78, for twice the copies and commits).  4096 tokens, 16 heads: 58 us.
+// it is wanted (both launches for 4096 tokens, replayed from a graph: 6 + 2 pieces
+// 78 us, 4 + 4 85, 5 + 3 75; half pieces 78, for twice the copies and commits).
+// 4096 tokens, 16 heads: 58 us; the call 79 in a stream of calls, 74 replayed.
 // P is rounded to the type, scaled by 2^kFaShift off the subnormals of fp16.
 constexpr int kFaThreads = 384;  // copies of Q and K, two issuers of products, copies of V; 4 softmax warps per tile
 constexpr int kKRing = 5, kVRing = 3;
