@@ -634,6 +634,148 @@ typedef struct {
 } spx_logprobs_args;
 SPX_API int spx_token_logprobs(const spx_logprobs_args *args, spx_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Trees of drafted tokens over a paged cache of keys and values              */
+/* ------------------------------------------------------------------------ */
+/* Speculation with several candidates per step: the rows of one request are
+ * its last token (row 0, not in the cache yet) and drafted tokens, each behind
+ * an earlier row, its parent.  A step is: spx_tree_layout (what each row sees
+ * and where it goes), spx_kv_append and spx_kv_attention per layer,
+ * spx_tree_accept (the path that the target agrees with).  A chain, a single
+ * token and a prompt's chunk are the same calls without parents.
+ *
+ * Rows.  N rows of a batch; request b owns rows q_start[b] .. q_start[b+1] - 1,
+ * its newest ones, at most max_q of them (larger counts are cut to max_q),
+ * none allowed.  lens[b] counts the request's tokens, those rows included: row
+ * i of T stands in the cache at token lens[b] - T + i.  Rows that no request
+ * owns (a padded batch) are left as they were in every output. */
+
+/* Keys and values of a layer, in pages of page_size tokens: token p of request
+ * b is row p % page_size of page block_table[b][p / page_size].  k and v have
+ * the same strides; any order of pages, tokens and heads that does not
+ * overlap.  Positions at or after lens[b] are never used, whatever they hold;
+ * a block-table entry that names no page reads as zeros. */
+typedef struct {
+    int dtype;                   /* SPX_F16 or SPX_BF16 */
+    void *k, *v;                 /* [num_pages][page_size][kv_heads][D], 16-byte aligned */
+    int num_pages, page_size;    /* page_size a multiple of 16 */
+    int kv_heads, D;             /* D 64 or 128 */
+    int64_t page_stride, token_stride, head_stride; /* elements, multiples of 8 */
+    const int32_t *block_table;  /* [B][max_pages] */
+    int max_pages;
+    int B;                       /* requests */
+    const int32_t *lens;         /* [B] tokens in the cache (new ones included) */
+} spx_kv_cache;
+
+/* From the parents of the rows, one launch.  parent[q_start[b] + i] is row i's
+ * parent, an index among the request's rows; one that is not an earlier row
+ * (row 0's own among them) makes the row a root.  parent == NULL: a chain.
+ *   mask = the row itself, its parent and so on: bit j for row j of the request
+ *          (max_q <= 64 with mask or parent, else SPX_ERR_UNSUPPORTED);
+ *   pos  = lens[b] - T + the number of rows above it (its rotary position);
+ *   slot = lens[b] - T + i (its place in the cache); req = b.
+ * Each output may be NULL. */
+typedef struct {
+    int B, N, max_q;
+    const int32_t *q_start;      /* [B + 1], ascending from 0 on */
+    const int32_t *lens;         /* [B] */
+    const int32_t *parent;       /* [N], or NULL */
+    int32_t *req, *slot, *pos;   /* [N] */
+    uint64_t *mask;              /* [N] */
+} spx_tree_layout_args;
+SPX_API int spx_tree_layout(const spx_tree_layout_args *args, spx_stream_t stream);
+
+/* New tokens to the cache, one launch.  Per head x of row n's queries and keys
+ * (rows of [heads][D] and [kv_heads][D], heads contiguous within a row, rows
+ * k_stride, v_stride, q_stride elements apart, so that the parts of one
+ * projection's output serve as they lie):
+ *   x = x * rsqrt(mean(x^2) + eps) * w        (w = q_norm, k_norm; NULL: not)
+ *   x[0..P) = rotation of x[0..P) by row pos[n] of cos/sin      (cos != NULL)
+ * rounded once; keys and values go to token slot[n] of request req[n], queries
+ * to q_out (which may be q).  The rotation turns the pair (a, b) into (a cos -
+ * b sin, b cos + a sin), pairs being elements (2i, 2i + 1) when interleaved,
+ * else (i, i + P/2); cos and sin are fp32 [max_pos][P/2].  pos == NULL: slot.
+ * A row is skipped when slot[n] is negative, or pos[n] negative or beyond the
+ * cos/sin rows; its keys and values also when req[n] is outside [0, B) or its
+ * table entry is missing or names no page.  Two rows must not name the same
+ * token. */
+typedef struct {
+    const spx_kv_cache *cache;
+    int N;
+    const void *k, *v;           /* 16-byte aligned */
+    int64_t k_stride, v_stride;  /* multiples of 8 */
+    const int32_t *req, *slot;   /* [N] */
+    const int32_t *pos;          /* [N], or NULL */
+    const void *q;               /* 16-byte aligned; both NULL: no queries */
+    void *q_out;
+    int64_t q_stride, q_out_stride;
+    int heads;
+    const void *q_norm, *k_norm; /* [D], 16-byte aligned, or NULL */
+    float eps;
+    const float *cos, *sin;      /* [max_pos][P/2], 16-byte aligned, or both NULL: no rotation */
+    int max_pos, P, interleaved; /* P a multiple of 16, at most D */
+} spx_kv_append_args;
+SPX_API int spx_kv_append(const spx_kv_append_args *args, spx_stream_t stream);
+
+/* Attention of the requests' rows over their cache; query head h reads key
+ * head h / (heads / kv_heads).  Row i of T sees the positions
+ *   p < lens[b] - T + i + 1                                       (causal)
+ *   p < lens[b]                                                   (causal == 0)
+ *   p < lens[b] - T, and lens[b] - T + j for every bit j < T of its mask (tree
+ *     != NULL; causal is ignored; max_q <= 64);
+ *   out = sum_p softmax(scale * q . k_p) v_p,  lse = log sum_p exp(scale * q . k_p).
+ * A row that sees nothing gives out = 0 and lse = -inf.  A position that holds
+ * an infinity or a NaN reaches only the rows that see it (an infinite or NaN
+ * value in at least its own column of out).  max_len bounds every request's
+ * length (longer ones are cut to it).  Softmax weights are rounded to the type
+ * before they meet the values; every sum is fp32. */
+typedef struct {
+    const spx_kv_cache *cache;
+    int N, heads;                /* heads a multiple of kv_heads, at most 64 to one key head */
+    const void *q;               /* [N][heads][D], 16-byte aligned; heads contiguous within a row */
+    int64_t q_stride, out_stride;/* elements from row to row, multiples of 8 */
+    const int32_t *q_start;      /* [B + 1], ascending from 0 on */
+    int max_q, max_len;
+    float scale;                 /* finite and above 0 */
+    int causal;
+    const uint64_t *tree;        /* [N] masks as of spx_tree_layout, or NULL */
+    void *out;                   /* [N][heads][D], 16-byte aligned */
+    float *lse;                  /* [N][heads], or NULL */
+    void *ws;                    /* spx_kv_workspace_size() bytes, 16-byte aligned; the first
+                                    SPX_KV_WORKSPACE_ZERO zeroed once by spx_workspace_init() */
+    size_t ws_bytes;
+    uint64_t wait_budget_ns;     /* bound of every device-side wait; 0 = 2 s */
+} spx_kv_attention_args;
+#define SPX_KV_WORKSPACE_ZERO 8192
+SPX_API int spx_kv_attention(const spx_kv_attention_args *args, spx_stream_t stream);
+/* Workspace of a call; 0 if unsupported.  Any larger workspace serves too.  Its
+ * status word (spx_workspace_status) is SPX_ERR_TIMEOUT after a bounded wait
+ * that gave up; it is zeroed again then. */
+SPX_API size_t spx_kv_workspace_size(int B, int N, int max_q, int max_len, int heads, int kv_heads, int D);
+
+/* The end of a step, one launch: from row 0 on, the walk goes from row i to
+ * the lowest row that has i as its parent (an earlier row) and whose token[]
+ * is target[i], the target's choice behind row i, as long as there is one.
+ *   n_kept[b] rows are on the path (row 0 included; 0 without rows), path[
+ *   q_start[b] + d] is the d-th of them, -1 from n_kept[b] on; next[b] = target
+ *   of the last one (-1 without rows); lens_out[b] = lens[b] - T + n_kept[b].
+ * In each of the n_layers caches, which share cache's layout, block table and
+ * lens, the keys and values of the path's d-th row are moved to token lens[b] -
+ * T + d.  layer_k and layer_v are host arrays of device pointers. */
+typedef struct {
+    const spx_kv_cache *cache;   /* its k and v are not used */
+    int n_layers;                /* 0 to 128; 0: nothing is moved */
+    void *const *layer_k, *const *layer_v;
+    int N, max_q;                /* max_q <= 64 */
+    const int32_t *q_start;      /* [B + 1] */
+    const int32_t *parent, *token, *target; /* [N] */
+    int32_t *n_kept;             /* [B] */
+    int32_t *path;               /* [N] */
+    int32_t *next;               /* [B] */
+    int32_t *lens_out;           /* [B], apart from cache->lens */
+} spx_tree_accept_args;
+SPX_API int spx_tree_accept(const spx_tree_accept_args *args, spx_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,241 @@
+// spx_kv_append.cu -- new tokens to the paged cache of keys and values: norm per
+// head, rotation and scatter in one launch, the queries' norm and rotation with it.
+#include "spx_kv.cuh"
+
+namespace spx {
+
+namespace {
+
+struct KvAppendParams {
+    uint16_t *ck, *cv;
+    int64_t page_stride, token_stride, head_stride;
+    int num_pages, page_size, kv_heads, D, max_pages, B;
+    const int32_t *table;
+    int N, heads;  // heads: 0 without queries
+    const uint16_t *k, *v, *q, *q_norm, *k_norm;
+    uint16_t *q_out;
+    int64_t k_stride, v_stride, q_stride, q_out_stride;
+    const int32_t *req, *slot, *pos;
+    float eps;
+    const float *cos, *sin;
+    int max_pos, P, interleaved;
+    FastDiv by_page, by_sets;  // sets of heads of a row
+    int64_t threads;
+};
+
+template <int DT>
+__device__ __forceinline__ void unpack8(float (&x)[8], uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = Elem<DT>::up2(w[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+    }
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    return make_uint4(Elem<DT>::down2(x[0], x[1]), Elem<DT>::down2(x[2], x[3]), Elem<DT>::down2(x[4], x[5]),
+                      Elem<DT>::down2(x[6], x[7]));
+}
+
+// D / 16 lanes hold a head, each two units of 8 values: of the rotated part
+// units u and u + P / 16 (which hold whole pairs in either order of the pairs),
+// of the rest two neighbouring ones.  They take kSet heads of a row in turn
+// (queries, then keys, then values), so that the row's sines are read once for
+// all of them and the loads of all are under way together.
+template <int DT, int D, int kSet>
+__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ KvAppendParams p) {
+    constexpr int kLanes = D / 16;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int u = threadIdx.x % kLanes, all = (int)(i / kLanes);
+    const int n = p.by_sets(all), h0 = (all - n * p.by_sets.d) * kSet;
+    const bool in = n < p.N;
+    const int slot = in ? __ldg(p.slot + n) : -1, pos = in ? (p.pos ? __ldg(p.pos + n) : slot) : -1;
+    const bool live = slot >= 0 && pos >= 0 && !(p.cos && pos >= p.max_pos);
+    // (no lane leaves: those of a head sum up its squares together)
+    const int half = p.P / 16;
+    const bool turns = p.cos && u < half;
+    const int c0 = 8 * (u < half ? u : 2 * u), c1 = u < half ? c0 + 8 * half : c0 + 8;
+    uint4 raw[kSet][2];
+    uint16_t *dst[kSet];
+    int64_t place = -1;  // of the token in the cache
+    if (live) {
+        const int b = __ldg(p.req + n), pi = p.by_page(slot);
+        if (b >= 0 && b < p.B && pi < p.max_pages) {
+            const int pg = __ldg(p.table + (size_t)b * p.max_pages + pi);
+            if (pg >= 0 && pg < p.num_pages)
+                place = (int64_t)pg * p.page_stride + (int64_t)(slot - pi * p.page_size) * p.token_stride;
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < kSet; ++s) {
+        const int h = h0 + s, hk = h - p.heads, hv = hk - p.kv_heads;
+        const uint16_t *src = nullptr;
+        dst[s] = nullptr;
+        raw[s][0] = raw[s][1] = make_uint4(0, 0, 0, 0);
+        if (!live || hv >= p.kv_heads) continue;
+        if (hk < 0) {
+            src = p.q + (int64_t)n * p.q_stride + (int64_t)h * D;
+            dst[s] = p.q_out + (int64_t)n * p.q_out_stride + (int64_t)h * D;
+        } else {
+            if (place < 0) continue;
+            const int x = hv < 0 ? hk : hv;
+            src = hv < 0 ? p.k + (int64_t)n * p.k_stride + (int64_t)x * D : p.v + (int64_t)n * p.v_stride + (int64_t)x * D;
+            dst[s] = (hv < 0 ? p.ck : p.cv) + place + (int64_t)x * p.head_stride;
+        }
+        raw[s][0] = *reinterpret_cast<const uint4 *>(src + c0);
+        raw[s][1] = *reinterpret_cast<const uint4 *>(src + c1);
+    }
+    float cs[8], sn[8];
+    if (turns && live) {
+        // interleaved: the pairs of unit c are 4c .. 4c + 3; else those of units u and u + half are 8u .. 8u + 7
+        const int a = p.interleaved ? c0 / 2 : c0, b = p.interleaved ? c1 / 2 : c0 + 4;
+        const float *cr = p.cos + (int64_t)pos * (p.P / 2), *sr = p.sin + (int64_t)pos * (p.P / 2);
+        const float4 x0 = __ldg(reinterpret_cast<const float4 *>(cr + a)), x1 = __ldg(reinterpret_cast<const float4 *>(cr + b));
+        const float4 y0 = __ldg(reinterpret_cast<const float4 *>(sr + a)), y1 = __ldg(reinterpret_cast<const float4 *>(sr + b));
+        cs[0] = x0.x; cs[1] = x0.y; cs[2] = x0.z; cs[3] = x0.w; cs[4] = x1.x; cs[5] = x1.y; cs[6] = x1.z; cs[7] = x1.w;
+        sn[0] = y0.x; sn[1] = y0.y; sn[2] = y0.z; sn[3] = y0.w; sn[4] = y1.x; sn[5] = y1.y; sn[6] = y1.z; sn[7] = y1.w;
+    }
+#pragma unroll
+    for (int s = 0; s < kSet; ++s) {
+        const int h = h0 + s, hk = h - p.heads;
+        const bool value = hk >= p.kv_heads;
+        const uint16_t *w = value ? nullptr : hk < 0 ? p.q_norm : p.k_norm;
+        float x[8], y[8];
+        unpack8<DT>(x, raw[s][0]);
+        unpack8<DT>(y, raw[s][1]);
+        // (heads differ from lane group to lane group of a warp: the sum is made whether or not it is wanted)
+        if (p.q_norm || p.k_norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
+#pragma unroll
+            for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (w) {
+                const float inv = rsqrtf(ss / (float)D + p.eps);
+                float a[8], b[8];
+                unpack8<DT>(a, __ldg(reinterpret_cast<const uint4 *>(w + c0)));
+                unpack8<DT>(b, __ldg(reinterpret_cast<const uint4 *>(w + c1)));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[j] = x[j] * inv * a[j];
+                    y[j] = y[j] * inv * b[j];
+                }
+            }
+        }
+        if (!dst[s]) continue;
+        if (turns && !value) {
+            if (p.interleaved) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float a = x[2 * j], b = x[2 * j + 1], d = y[2 * j], e = y[2 * j + 1];
+                    x[2 * j] = a * cs[j] - b * sn[j];
+                    x[2 * j + 1] = b * cs[j] + a * sn[j];
+                    y[2 * j] = d * cs[4 + j] - e * sn[4 + j];
+                    y[2 * j + 1] = e * cs[4 + j] + d * sn[4 + j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float a = x[j], b = y[j];
+                    x[j] = a * cs[j] - b * sn[j];
+                    y[j] = b * cs[j] + a * sn[j];
+                }
+            }
+        }
+        // (what is neither normalised nor turned goes as it came: a NaN keeps its bits)
+        const bool same = value || (!w && !turns);
+        *reinterpret_cast<uint4 *>(dst[s] + c0) = same ? raw[s][0] : pack8<DT>(x);
+        *reinterpret_cast<uint4 *>(dst[s] + c1) = same ? raw[s][1] : pack8<DT>(y);
+    }
+}
+
+bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+constexpr int kSetLarge = 4;
+
+template <int DT, int D>
+int launch(KvAppendParams &p, cudaStream_t s) {
+    const int all = p.heads + 2 * p.kv_heads;
+    // Four heads to a thread where that leaves every SM its threads, else one.
+    const bool large = (int64_t)p.N * all * (D / 16) >= (int64_t)kKvMaxBlocks * 2048 * kSetLarge;
+    const int sets = large ? (all + kSetLarge - 1) / kSetLarge : all;
+    p.by_sets.set(sets);
+    const int64_t threads = (int64_t)p.N * sets * (D / 16), blocks = (threads + 255) / 256;
+    if (blocks * 256 / (D / 16) > 0x7fffffffll) return SPX_ERR_UNSUPPORTED;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = latent_config(dim3((unsigned)blocks), 256, 0, s, attr, 1);
+    return record_launch(large ? cudaLaunchKernelEx(&cfg, kv_append_kernel<DT, D, kSetLarge>, p)
+                               : cudaLaunchKernelEx(&cfg, kv_append_kernel<DT, D, 1>, p));
+}
+
+}  // namespace
+
+}  // namespace spx
+
+using namespace spx;
+
+extern "C" int spx_kv_append(const spx_kv_append_args *a, spx_stream_t stream) {
+    if (!a) return SPX_ERR_INVALID_ARG;
+    const int st = kv_cache_check(a->cache);
+    if (st) return st;
+    const spx_kv_cache &c = *a->cache;
+    if (a->N < 0 || !a->cos != !a->sin || !a->q != !a->q_out || (a->q_norm && !a->q)) return SPX_ERR_INVALID_ARG;
+    if (a->cos && (a->max_pos < 1 || !al16(a->cos) || !al16(a->sin))) return SPX_ERR_INVALID_ARG;
+    if (a->cos && (a->P < 16 || a->P > c.D || a->P % 16)) return SPX_ERR_UNSUPPORTED;
+    if ((a->q_norm || a->k_norm) && !(a->eps >= 0.f)) return SPX_ERR_INVALID_ARG;
+    const int64_t kw = (int64_t)c.kv_heads * c.D;
+    if (!al16(a->k) || !al16(a->v) || !al16(a->q_norm) || !al16(a->k_norm) || a->k_stride < kw || a->v_stride < kw ||
+        a->k_stride % 8 || a->v_stride % 8)
+        return SPX_ERR_INVALID_ARG;
+    if (a->q) {
+        const int64_t w = (int64_t)a->heads * c.D;
+        if (a->heads < 1 || a->q_stride < w || a->q_out_stride < w || a->q_stride % 8 || a->q_out_stride % 8 ||
+            !al16(a->q) || !al16(a->q_out) || (a->q == a->q_out && a->q_stride != a->q_out_stride))
+            return SPX_ERR_INVALID_ARG;
+        if (a->heads > 1024) return SPX_ERR_UNSUPPORTED;
+    }
+    if (a->N == 0) return SPX_OK;
+    if (!a->k || !a->v || !a->req || !a->slot) return SPX_ERR_INVALID_ARG;
+    KvAppendParams p{};
+    p.ck = static_cast<uint16_t *>(c.k);
+    p.cv = static_cast<uint16_t *>(c.v);
+    p.page_stride = c.page_stride;
+    p.token_stride = c.token_stride;
+    p.head_stride = c.head_stride;
+    p.num_pages = c.num_pages;
+    p.page_size = c.page_size;
+    p.kv_heads = c.kv_heads;
+    p.D = c.D;
+    p.max_pages = c.max_pages;
+    p.B = c.B;
+    p.table = c.block_table;
+    p.N = a->N;
+    p.heads = a->q ? a->heads : 0;
+    p.k = static_cast<const uint16_t *>(a->k);
+    p.v = static_cast<const uint16_t *>(a->v);
+    p.q = static_cast<const uint16_t *>(a->q);
+    p.q_norm = static_cast<const uint16_t *>(a->q_norm);
+    p.k_norm = static_cast<const uint16_t *>(a->k_norm);
+    p.q_out = static_cast<uint16_t *>(a->q_out);
+    p.k_stride = a->k_stride;
+    p.v_stride = a->v_stride;
+    p.q_stride = a->q_stride;
+    p.q_out_stride = a->q_out_stride;
+    p.req = a->req;
+    p.slot = a->slot;
+    p.pos = a->pos;
+    p.eps = a->eps;
+    p.cos = a->cos;
+    p.sin = a->sin;
+    p.max_pos = a->max_pos;
+    p.P = a->cos ? a->P : 0;
+    p.interleaved = a->interleaved;
+    p.by_page.set(c.page_size);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (c.D == 128) return c.dtype == SPX_F16 ? launch<SPX_F16, 128>(p, s) : launch<SPX_BF16, 128>(p, s);
+    return c.dtype == SPX_F16 ? launch<SPX_F16, 64>(p, s) : launch<SPX_BF16, 64>(p, s);
+}

@@ -94,6 +94,43 @@ class LogprobsArgs(C.Structure):
                 ("top_ids", C.c_void_p), ("top_logp", C.c_void_p)]
 
 
+class KvCacheC(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("k", C.c_void_p), ("v", C.c_void_p), ("num_pages", C.c_int),
+                ("page_size", C.c_int), ("kv_heads", C.c_int), ("D", C.c_int), ("page_stride", C.c_int64),
+                ("token_stride", C.c_int64), ("head_stride", C.c_int64), ("block_table", C.c_void_p),
+                ("max_pages", C.c_int), ("B", C.c_int), ("lens", C.c_void_p)]
+
+
+class TreeLayoutArgs(C.Structure):
+    _fields_ = [("B", C.c_int), ("N", C.c_int), ("max_q", C.c_int), ("q_start", C.c_void_p), ("lens", C.c_void_p),
+                ("parent", C.c_void_p), ("req", C.c_void_p), ("slot", C.c_void_p), ("pos", C.c_void_p),
+                ("mask", C.c_void_p)]
+
+
+class KvAppendArgs(C.Structure):
+    _fields_ = [("cache", C.POINTER(KvCacheC)), ("N", C.c_int), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("k_stride", C.c_int64), ("v_stride", C.c_int64), ("req", C.c_void_p), ("slot", C.c_void_p),
+                ("pos", C.c_void_p), ("q", C.c_void_p), ("q_out", C.c_void_p), ("q_stride", C.c_int64),
+                ("q_out_stride", C.c_int64), ("heads", C.c_int), ("q_norm", C.c_void_p), ("k_norm", C.c_void_p),
+                ("eps", C.c_float), ("cos", C.c_void_p), ("sin", C.c_void_p), ("max_pos", C.c_int), ("P", C.c_int),
+                ("interleaved", C.c_int)]
+
+
+class KvAttentionArgs(C.Structure):
+    _fields_ = [("cache", C.POINTER(KvCacheC)), ("N", C.c_int), ("heads", C.c_int), ("q", C.c_void_p),
+                ("q_stride", C.c_int64), ("out_stride", C.c_int64), ("q_start", C.c_void_p), ("max_q", C.c_int),
+                ("max_len", C.c_int), ("scale", C.c_float), ("causal", C.c_int), ("tree", C.c_void_p),
+                ("out", C.c_void_p), ("lse", C.c_void_p), ("ws", C.c_void_p), ("ws_bytes", C.c_size_t),
+                ("wait_budget_ns", C.c_uint64)]
+
+
+class TreeAcceptArgs(C.Structure):
+    _fields_ = [("cache", C.POINTER(KvCacheC)), ("n_layers", C.c_int), ("layer_k", C.POINTER(C.c_void_p)),
+                ("layer_v", C.POINTER(C.c_void_p)), ("N", C.c_int), ("max_q", C.c_int), ("q_start", C.c_void_p),
+                ("parent", C.c_void_p), ("token", C.c_void_p), ("target", C.c_void_p), ("n_kept", C.c_void_p),
+                ("path", C.c_void_p), ("next", C.c_void_p), ("lens_out", C.c_void_p)]
+
+
 _SIGS = {
     "spx_status_string": (C.c_char_p, [C.c_int]),
     "spx_version": (C.c_int, []),
@@ -142,6 +179,11 @@ _SIGS = {
     "spx_latent_attention": (C.c_int, [C.POINTER(LatentArgs), C.c_void_p]),
     "spx_latent_workspace_size": (C.c_size_t, [C.c_int] * 10),
     "spx_token_logprobs": (C.c_int, [C.POINTER(LogprobsArgs), C.c_void_p]),
+    "spx_tree_layout": (C.c_int, [C.POINTER(TreeLayoutArgs), C.c_void_p]),
+    "spx_kv_append": (C.c_int, [C.POINTER(KvAppendArgs), C.c_void_p]),
+    "spx_kv_attention": (C.c_int, [C.POINTER(KvAttentionArgs), C.c_void_p]),
+    "spx_kv_workspace_size": (C.c_size_t, [C.c_int] * 7),
+    "spx_tree_accept": (C.c_int, [C.POINTER(TreeAcceptArgs), C.c_void_p]),
 }
 
 
@@ -737,3 +779,216 @@ def spx_token_logprobs(args: LogprobsArgs, stream=None):
     """Log probabilities of given tokens, entropy and most likely alternatives
     of rows of logits.  See include/spx.h."""
     _chk(load().spx_token_logprobs(C.byref(args), _stream(stream)), "spx_token_logprobs")
+
+
+# ------------------------- trees of drafted tokens, keys and values in pages --
+SPX_KV_WORKSPACE_ZERO = 8192
+
+
+def _on_one_device(a, *tensors):
+    """Note on the argument block the one device that its tensors lie on."""
+    devices = {t.device for t in tensors if t is not None}
+    if any(d.type != "cuda" for d in devices):
+        raise ValueError("libspx takes device tensors")
+    if len(devices) != 1:
+        raise ValueError(f"tensors of one device expected, got {sorted(map(str, devices))}")
+    a.device = devices.pop().index
+
+
+def _launch(name: str, args, stream):
+    """The call of that name on its tensors' device, whichever is current."""
+    call = getattr(load(), name)
+    if getattr(args, "device", torch.cuda.current_device()) == torch.cuda.current_device():
+        _chk(call(C.byref(args), _stream(stream)), name)
+    else:
+        with torch.cuda.device(args.device):
+            _chk(call(C.byref(args), _stream(stream)), name)
+
+
+def _rows3(t, what: str, heads=None):
+    """Pointer and row stride of [N][heads][D], heads contiguous within a row."""
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{what}: [N][{'heads' if heads is None else heads}][D] expected")
+    return _rows(t, what)
+
+
+@dataclass
+class KvCache:
+    """Paged cache of a layer's keys and values: k and v [pages][page_size]
+    [kv_heads][D] (views with the same strides, any order of the first three
+    dimensions, values of a head contiguous), block_table int32 [B][max_pages],
+    lens int32 [B].  See include/spx.h."""
+    k: torch.Tensor
+    v: torch.Tensor
+    block_table: torch.Tensor
+    lens: torch.Tensor
+
+    def cstruct(self) -> KvCacheC:
+        k, v = self.k, self.v
+        if not k.is_cuda or k.dim() != 4 or k.stride(3) != 1 or k.shape != v.shape or k.stride() != v.stride() or \
+                k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k, v: device tensors [pages][page_size][kv_heads][D] of one layout expected")
+        B = self.lens.numel()
+        if self.block_table.dim() != 2 or self.block_table.shape[0] != B:
+            raise ValueError("block_table: [B][max_pages] expected")
+        return KvCacheC(_dt(k), k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], k.shape[2], k.shape[3],
+                        k.stride(0), k.stride(1), k.stride(2), _i32(self.block_table, "block_table"),
+                        self.block_table.shape[1], B, _i32(self.lens, "lens", (B,)))
+
+
+def tree_layout_args(q_start, lens, max_q: int, parent=None, req=None, slot=None, pos=None, mask=None):
+    """Build (and keep alive) the argument block of spx_tree_layout: q_start int32
+    [B + 1], lens int32 [B], parent int32 [N] (None: chains); outputs req, slot,
+    pos int32 [N] and mask int64 [N] (the 64 bits of what a row sees)."""
+    a = TreeLayoutArgs()
+    some = next((t for t in (parent, req, slot, pos, mask) if t is not None), None)
+    if some is None:
+        raise ValueError("no output to write")
+    B, N = lens.numel(), some.numel()
+    if mask is not None and (mask.dtype != torch.int64 or tuple(mask.shape) != (N,)):
+        raise ValueError(f"mask: int64 ({N},) expected")
+    a.B, a.N, a.max_q = B, N, int(max_q)
+    a.q_start, a.lens = _i32(q_start, "q_start", (B + 1,)), _i32(lens, "lens", (B,))
+    a.parent, a.req, a.slot, a.pos = (None if t is None else _i32(t, what, (N,)) for t, what in
+                                      ((parent, "parent"), (req, "req"), (slot, "slot"), (pos, "pos")))
+    a.mask = _p(mask)
+    _on_one_device(a, q_start, lens, parent, req, slot, pos, mask)
+    return a, [q_start, lens, parent, req, slot, pos, mask]
+
+
+def spx_tree_layout(args: TreeLayoutArgs, stream=None):
+    """Masks, cache slots and rotary positions of trees of drafted rows (or of
+    chains).  See include/spx.h."""
+    _launch("spx_tree_layout", args, stream)
+
+
+def kv_append_args(cache: KvCache, k, v, req, slot, pos=None, q=None, q_out=None, q_norm=None, k_norm=None, eps=1e-6,
+                   cos=None, sin=None, interleaved=False):
+    """Build (and keep alive) the argument block of spx_kv_append: k and v
+    [N][kv_heads][D] and q [N][heads][D] (parts of one projection's output may
+    lie side by side), req, slot and pos int32 [N], q_norm and k_norm [D], cos and
+    sin float32 [max_pos][P/2]; q_out is q itself if not given."""
+    cs = cache.cstruct()
+    a = KvAppendArgs()
+    N, D = k.shape[0], cs.D
+    for t, what in ((k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"), (q_norm, "q_norm"), (k_norm, "k_norm")):
+        _same(t, cache.k, what)
+    if tuple(k.shape) != (N, cs.kv_heads, D) or v.shape != k.shape:
+        raise ValueError("k, v: [N][kv_heads][D] expected")
+    for t, what in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None and tuple(t.shape) != (D,):
+            raise ValueError(f"{what}: [D] expected")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin: both or neither")
+    if q is None and (q_out is not None or q_norm is not None):
+        raise ValueError("q_out and q_norm go with q")
+    a.cache, a.N = C.pointer(cs), N
+    a.k, a.k_stride = _rows3(k, "k")
+    a.v, a.v_stride = _rows3(v, "v")
+    a.req, a.slot = _i32(req, "req", (N,)), _i32(slot, "slot", (N,))
+    a.pos = None if pos is None else _i32(pos, "pos", (N,))
+    if q is not None:
+        if q_out is None:
+            q_out = q
+        if q.dim() != 3 or q.shape[0] != N or q.shape[2] != D or q_out.shape != q.shape:
+            raise ValueError("q, q_out: [N][heads][D] expected")
+        a.q, a.q_stride = _rows3(q, "q")
+        a.q_out, a.q_out_stride = _rows3(q_out, "q_out")
+        a.heads = q.shape[1]
+    a.q_norm, a.k_norm, a.eps, a.interleaved = _p(q_norm), _p(k_norm), float(eps), int(bool(interleaved))
+    if cos is not None:
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.shape != sin.shape or cos.dim() != 2:
+            raise ValueError("cos, sin: float32 [max_pos][P/2] expected")
+        a.cos, a.sin, a.max_pos, a.P = _p(cos), _p(sin), cos.shape[0], 2 * cos.shape[1]
+    keep = [k, v, req, slot, pos, q, q_out, q_norm, k_norm, cos, sin]
+    _on_one_device(a, cache.k, cache.block_table, cache.lens, *keep)
+    return a, [cs, cache, *keep]
+
+
+def spx_kv_append(args: KvAppendArgs, stream=None):
+    """New tokens' keys and values to the paged cache, with norms per head and
+    rotation, and the queries'.  See include/spx.h."""
+    _launch("spx_kv_append", args, stream)
+
+
+def spx_kv_workspace_size(B, N, max_q, max_len, heads, kv_heads, D=128) -> int:
+    return load().spx_kv_workspace_size(B, N, max_q, max_len, heads, kv_heads, D)
+
+
+def new_kv_workspace(q, cache: KvCache, max_q: int, max_len: int, stream=None) -> torch.Tensor:
+    """Allocate (through torch) and initialise a workspace for kv_attention_args()."""
+    n = spx_kv_workspace_size(cache.lens.numel(), q.shape[0], max_q, max_len, q.shape[1], cache.k.shape[2],
+                              cache.k.shape[3])
+    if n == 0:
+        raise SpxError(SPX_ERR_UNSUPPORTED, "spx_kv_workspace_size")
+    with torch.cuda.device(q.device):
+        ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+        _chk(load().spx_workspace_init(_p(ws), SPX_KV_WORKSPACE_ZERO, _stream(stream)), "spx_workspace_init")
+    return ws
+
+
+def kv_attention_args(q, cache: KvCache, q_start, max_q: int, max_len: int, scale: float, out, ws, causal=True,
+                      tree=None, lse=None, wait_budget_ns=0):
+    """Build (and keep alive) the argument block of spx_kv_attention: q and out
+    [N][heads][D], q_start int32 [B + 1], tree int64 [N] (masks of spx_tree_layout;
+    None: causal or full), lse float32 [N][heads]."""
+    cs = cache.cstruct()
+    a = KvAttentionArgs()
+    for t, what in ((q, "q"), (out, "out")):
+        _same(t, cache.k, what)
+    if q.dim() != 3 or q.shape[2] != cs.D or out.shape != q.shape:
+        raise ValueError("q, out: [N][heads][D] expected")
+    N, heads = q.shape[:2]
+    if tree is not None and (tree.dtype != torch.int64 or tuple(tree.shape) != (N,)):
+        raise ValueError(f"tree: int64 ({N},) expected")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (N, heads)):
+        raise ValueError("lse: float32 [N][heads] expected")
+    a.cache, a.N, a.heads = C.pointer(cs), N, heads
+    a.q, a.q_stride = _rows3(q, "q")
+    a.out, a.out_stride = _rows3(out, "out")
+    a.q_start, a.max_q, a.max_len = _i32(q_start, "q_start", (cs.B + 1,)), int(max_q), int(max_len)
+    a.scale, a.causal, a.tree, a.lse = float(scale), int(bool(causal)), _p(tree), _p(lse)
+    a.ws, a.ws_bytes, a.wait_budget_ns = _p(ws), ws.numel() if ws is not None else 0, int(wait_budget_ns)
+    keep = [q, q_start, out, ws, tree, lse]
+    _on_one_device(a, cache.k, cache.block_table, cache.lens, *keep)
+    return a, [cs, cache, *keep]
+
+
+def spx_kv_attention(args: KvAttentionArgs, stream=None):
+    """Attention of the requests' newest rows (one, a tree, a prompt's chunk)
+    over the paged cache of keys and values.  See include/spx.h."""
+    _launch("spx_kv_attention", args, stream)
+
+
+def tree_accept_args(caches, q_start, max_q: int, parent, token, target, n_kept, path, next_token, lens_out):
+    """Build (and keep alive) the argument block of spx_tree_accept: caches (one
+    KvCache per layer, of one layout, block table and lens), q_start int32
+    [B + 1]; parent, token, target and path int32 [N]; n_kept, next_token and
+    lens_out int32 [B]."""
+    caches = list(caches)
+    if not caches:
+        raise ValueError("one cache per layer expected")
+    cs = caches[0].cstruct()
+    for c in caches[1:]:
+        o = c.cstruct()
+        if any(getattr(o, f) != getattr(cs, f) for f, _ in KvCacheC._fields_ if f not in ("k", "v")):
+            raise ValueError("caches of one layout, block table and lens expected")
+    a = TreeAcceptArgs()
+    B, N, n = cs.B, parent.numel(), len(caches)
+    a.cache, a.n_layers, a.N, a.max_q = C.pointer(cs), n, N, int(max_q)
+    a.layer_k = (C.c_void_p * n)(*[c.k.data_ptr() for c in caches])
+    a.layer_v = (C.c_void_p * n)(*[c.v.data_ptr() for c in caches])
+    a.q_start = _i32(q_start, "q_start", (B + 1,))
+    a.parent, a.token, a.target, a.path = (_i32(t, what, (N,)) for t, what in (
+        (parent, "parent"), (token, "token"), (target, "target"), (path, "path")))
+    a.n_kept, a.next, a.lens_out = (_i32(t, what, (B,)) for t, what in (
+        (n_kept, "n_kept"), (next_token, "next_token"), (lens_out, "lens_out")))
+    keep = [q_start, parent, token, target, n_kept, path, next_token, lens_out]
+    _on_one_device(a, *[t for c in caches for t in (c.k, c.v)], caches[0].block_table, caches[0].lens, *keep)
+    return a, [cs, caches, *keep]
+
+
+def spx_tree_accept(args: TreeAcceptArgs, stream=None):
+    """The path of drafted rows that the target agrees with, its keys and values
+    moved together in every layer's cache.  See include/spx.h."""
+    _launch("spx_tree_accept", args, stream)
