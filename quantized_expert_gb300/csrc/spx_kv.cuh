@@ -33,6 +33,10 @@ struct KvParams {
     // workspace
     WsHeader *hdr;
     uint64_t budget;
+    uint32_t *done;    // [blocks] parts of the unit that begins in a block and ends in a later one; zero between calls
+    float2 *ml;        // [2 blocks][rows] reference and weight of a partial sum's row
+    float *part;       // [2 blocks][rows][D] partial sums
+    int span;          // rows (tokens) of a unit
 };
 
 // A request's rows and cached length, cut to the call's bounds, so that no
@@ -94,8 +98,132 @@ __device__ __forceinline__ int kv_none_see(const KvParams &p, const KvReq &r, in
     return p.tree || !p.causal ? r.len : max(r.len - r.T + t + 1, 0);
 }
 
+// ------------------------------------------------------------------ shares --
+// A unit of work is a key head's query heads on up to `span` consecutive rows of
+// a request; its tiles are the key tiles that any of these rows sees, one at
+// least, so that a row which sees nothing is written too.  The tiles of all
+// units, in the order request, key head, rows, are dealt out in equal
+// contiguous shares, one a block: a long request and a ragged batch both fill
+// the machine, and a block meets at most two units that are not its own alone.
+// A share that begins or ends inside a unit leaves a partial sum in the
+// workspace: block c has place 2c for the unit in which its share begins,
+// 2c + 1 for one that begins in its share and ends in a later block's.
+__device__ __forceinline__ int kv_groups(int T, int span) { return (T + span - 1) / span; }
+__device__ __forceinline__ int kv_tiles(const KvParams &p, const KvReq &r, int g, int span) {
+    return max((kv_none_see(p, r, min((g + 1) * span, r.T) - 1) + kKvTile - 1) / kKvTile, 1);
+}
+__device__ __forceinline__ int kv_head_tiles(const KvParams &p, const KvReq &r, int span) {
+    int n = 0;
+    for (int g = 0; g < kv_groups(r.T, span); ++g) n += kv_tiles(p, r, g, span);
+    return n;
+}
+
+// Where a block's share begins, the same for all its threads.
+struct KvShare {
+    int b, h, g, off;  // unit, and the first tile of it
+    int flat, left;    // index of that tile among the call's; tiles of the share
+    int share;         // tiles of a whole share
+    KvReq rq;
+};
+
+// One warp: every lane gets the block's share.
+__device__ __forceinline__ KvShare kv_find_share(const KvParams &p, int span, int lane) {
+    KvShare w{};
+    // tiles of the requests, 32 at a time; the last 32 stay in registers, which is all of them for a small batch
+    int total = 0, n = 0;
+    KvReq r{};
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        n = 0;
+        if (b0 + lane < p.B) {
+            r = kv_req(p, b0 + lane);
+            n = kv_head_tiles(p, r, span) * p.kv_heads;
+        }
+        total += __reduce_add_sync(0xffffffffu, n);
+    }
+    w.share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
+    w.flat = (int)min((int64_t)w.share * blockIdx.x, (int64_t)total);
+    w.left = min(w.share, total - w.flat);
+    if (w.left <= 0) return w;
+    int before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        if (p.B > 32) {
+            n = 0;
+            if (b0 + lane < p.B) {
+                r = kv_req(p, b0 + lane);
+                n = kv_head_tiles(p, r, span) * p.kv_heads;
+            }
+        }
+        int upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const int off = w.flat - (before + upto - n);
+        const uint32_t mine = __ballot_sync(0xffffffffu, off >= 0 && off < n);
+        if (mine) {
+            const int l = __ffs(mine) - 1;
+            w.b = b0 + l;
+            w.off = __shfl_sync(0xffffffffu, off, l);
+            w.rq.row0 = __shfl_sync(0xffffffffu, r.row0, l);
+            w.rq.T = __shfl_sync(0xffffffffu, r.T, l);
+            w.rq.len = __shfl_sync(0xffffffffu, r.len, l);
+            const int per = __shfl_sync(0xffffffffu, n, l) / p.kv_heads;
+            w.h = w.off / per;
+            w.off -= w.h * per;
+            for (int t; w.off >= (t = kv_tiles(p, w.rq, w.g, span)); ++w.g) w.off -= t;
+            return w;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    w.left = 0;  // (not reached)
+    return w;
+}
+
+// A walk over a share, unit by unit; the same in every role of a block.
+struct KvWalk {
+    int b, h, g, nt;    // unit, its tiles
+    int tile, end;      // tiles of the unit in this share
+    int flat, left;     // index of `tile` among the call's tiles; tiles of the share from `tile` on
+    KvReq rq;
+    __device__ __forceinline__ void begin(const KvParams &p, const KvShare &w, int span) {
+        b = w.b;
+        h = w.h;
+        g = w.g;
+        flat = w.flat;
+        left = w.left;
+        rq = w.rq;
+        if (left <= 0) return;
+        nt = kv_tiles(p, rq, g, span);
+        tile = w.off;
+        end = min(nt, tile + left);
+    }
+    __device__ __forceinline__ bool whole() const { return tile == 0 && end == nt; }
+    __device__ __forceinline__ void next(const KvParams &p, int span) {
+        left -= end - tile;
+        flat += end - tile;
+        if (left <= 0) return;
+        if (++g == kv_groups(rq.T, span)) {
+            g = 0;
+            if (++h == p.kv_heads) {
+                h = 0;
+                do {
+                    if (++b >= p.B) {  // (does not happen while tiles are left)
+                        left = 0;
+                        return;
+                    }
+                    rq = kv_req(p, b);
+                } while (rq.T == 0);
+            }
+        }
+        nt = kv_tiles(p, rq, g, span);
+        tile = 0;
+        end = min(nt, left);
+    }
+};
+
 // -------------------------------------------------------------------- host --
-// spx_kv.cu
+// spx_kv_attention.cu
 int kv_cache_check(const spx_kv_cache *c);
 
 }  // namespace spx
