@@ -26,7 +26,7 @@ VARIANTS = {None: (BUILD, LIB, []),
                          ["-DSPX_TIMELINE"])}
 SOURCES = ["spx_route.cu", "spx_engine.cu", "spx_draft.cu", "spx_pack.cu", "spx_api.cu", "spx_noalloc.cu",
            "spx_plan.cu", "spx_tc.cu", "spx_latent.cu", "spx_latent_prompt.cu", "spx_append.cu", "spx_logprobs.cu",
-           "spx_kv_append.cu", "spx_kv_attention.cu", "spx_tree.cu"]
+           "spx_kv_append.cu", "spx_kv_attention.cu", "spx_kv_tiles.cu", "spx_tree.cu"]
 # every header of csrc/ and the public one: a change to any rebuilds every source
 HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith(".cuh")) + [os.path.join("..", "..", "include", "spx.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

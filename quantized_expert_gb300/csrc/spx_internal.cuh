@@ -39,7 +39,7 @@ static_assert(offsetof(WsHeader, timeout_site) - offsetof(WsHeader, status) == 3
               "a wait that holds &status records its site three words on");
 // Bounded waits that give up record their site next to the status word.
 enum : int32_t { SITE_ALL_SYNC = 1, SITE_FILL = 2, SITE_HSLICE = 3, SITE_GATE = 4, SITE_ROUTING = 5, SITE_SLOT = 6,
-                 SITE_STAGE = 7, SITE_POLLER = 8, SITE_ENGINE = 9, SITE_TC = 10, SITE_LATENT = 11 };
+                 SITE_STAGE = 7, SITE_POLLER = 8, SITE_ENGINE = 9, SITE_TC = 10, SITE_LATENT = 11, SITE_KV = 12 };
 #if defined(__CUDACC__)
 __device__ __forceinline__ void record_timeout(int32_t *status, int32_t site) {
     atomicCAS(status, 0, (int32_t)SPX_ERR_TIMEOUT);

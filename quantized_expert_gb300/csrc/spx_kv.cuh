@@ -36,7 +36,11 @@ struct KvParams {
     uint32_t *done;    // [blocks] parts of the unit that begins in a block and ends in a later one; zero between calls
     float2 *ml;        // [2 blocks][rows] reference and weight of a partial sum's row
     float *part;       // [2 blocks][rows][D] partial sums
+    int4 *seams;       // [blocks] request, key head, rows and last block of the unit that begins in a block and ends in
+                       // a later one (request -1: none)
     int span;          // rows (tokens) of a unit
+    int tile_tokens;   // rows (tokens) of a product of 128 (token, head) rows
+    int box_tokens;    // cached tokens of one copy: the largest power of two that divides a page, 128 at most
 };
 
 // A request's rows and cached length, cut to the call's bounds, so that no
@@ -222,8 +226,58 @@ struct KvWalk {
     }
 };
 
+// ------------------------------------------------------------------- results --
+constexpr float kKvLn2 = 0.6931471805599453f;
+// The reference of a row moves only when a score is 2^kKvSlack above it, and
+// weights are scaled by 2^kKvShift: they stay below fp16's largest value (2^16)
+// and most of what is worth adding above its subnormals (2^-14).
+constexpr float kKvSlack = 8.f, kKvShift = 5.f;
+
+__device__ __forceinline__ float kv_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Log of a row's sum of exponentials from its reference and weight.
+__device__ __forceinline__ float kv_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + log2f(l) - kKvShift) * kKvLn2;
+}
+// The factor of a part with reference m under a common reference (0 without
+// any, unless no part has one).
+__device__ __forceinline__ float kv_factor(float m, float common) {
+    return m == -INFINITY ? (common == -INFINITY ? 1.f : 0.f) : kv_ex2(m - common);
+}
+// Four values of a row from the partial sums of the blocks c0 .. c1, in their
+// order, to the output.  r: row of a place, of which there are `rows`.
+template <int DT, int D>
+__device__ __forceinline__ void kv_join4(const KvParams &p, int c0, int c1, int rows, int r, int c, int row, int head) {
+    float mm = -INFINITY, ll = 0.f;
+    for (int k = c0; k <= c1; ++k) mm = fmaxf(mm, __ldcg(&p.ml[(size_t)(2 * k + (k == c0)) * rows + r]).x);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = c0; k <= c1; ++k) {
+        const size_t at = (size_t)(2 * k + (k == c0)) * rows + r;
+        const float2 a = __ldcg(&p.ml[at]);
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D + 4 * c));
+        const float f = kv_factor(a.x, mm);
+        ll += a.y * f;
+        v.x += x.x * f;
+        v.y += x.y * f;
+        v.z += x.z * f;
+        v.w += x.w * f;
+    }
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    *reinterpret_cast<uint2 *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + 4 * c) =
+        make_uint2(Elem<DT>::down2(v.x * inv, v.y * inv), Elem<DT>::down2(v.z * inv, v.w * inv));
+    if (p.lse && c == 0) p.lse[(int64_t)row * p.heads + head] = kv_lse(mm, ll);
+}
+
 // -------------------------------------------------------------------- host --
 // spx_kv_attention.cu
 int kv_cache_check(const spx_kv_cache *c);
+// spx_kv_tiles.cu: calls of more rows, on `blocks` blocks.
+constexpr int kKvTileRows = 128;  // rows of one product
+inline int kv_tile_tokens(int group) { return kKvTileRows / group; }
+int launch_kv_tiles(KvParams &p, int dt, int blocks, cudaStream_t s);
 
 }  // namespace spx

@@ -16,17 +16,6 @@ namespace spx {
 
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
-// The reference of a row moves only when a score is 2^kSlack above it, and
-// weights are scaled by 2^kShift: they stay below fp16's largest value (2^16)
-// and most of what is worth adding above its subnormals (2^-14).
-constexpr float kSlack = 8.f, kShift = 5.f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -250,13 +239,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
                     top[y] = t * p.scale_log2;  // (scale > 0)
-                    rise |= top[y] > m[x][y] + kSlack;
+                    rise |= top[y] > m[x][y] + kKvSlack;
                 }
                 if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float mn = top[y] > m[x][y] + kSlack ? top[y] : m[x][y];
-                        fac[y] = mn == m[x][y] ? 1.f : ex2(m[x][y] - mn);
+                        const float mn = top[y] > m[x][y] + kKvSlack ? top[y] : m[x][y];
+                        fac[y] = mn == m[x][y] ? 1.f : kv_ex2(m[x][y] - mn);
                         m[x][y] = mn;
                         l[x][y] *= fac[y];
                     }
@@ -268,11 +257,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                 uint32_t pa[4];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const float ref = m[x][y] == -INFINITY ? 0.f : kShift - m[x][y];
+                    const float ref = m[x][y] == -INFINITY ? 0.f : kKvShift - m[x][y];
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
-                        const float a = ex2(fmaf(s[x][n][2 * y], p.scale_log2, ref));
-                        const float b = ex2(fmaf(s[x][n][2 * y + 1], p.scale_log2, ref));
+                        const float a = kv_ex2(fmaf(s[x][n][2 * y], p.scale_log2, ref));
+                        const float b = kv_ex2(fmaf(s[x][n][2 * y + 1], p.scale_log2, ref));
                         l[x][y] += a + b;
                         pa[2 * n + y] = Elem<DT>::down2(a, b);  // rounded for the tensor cores; the weight's own sum is not
                     }
@@ -315,7 +304,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) t = fmaxf(t, mls[i * C::kRows + 16 * x + 8 * y + quad].x);
                 top[x][y] = t;
-                const float f = m[x][y] == -INFINITY ? (m[x][y] == t ? 1.f : 0.f) : ex2(m[x][y] - t);
+                const float f = kv_factor(m[x][y], t);
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n) {
                     o[x][n][2 * y] *= f;
@@ -357,7 +346,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
                 const float2 v = mls[k * C::kRows + r];
-                if (v.x != -INFINITY) ll += v.y * ex2(v.x - mm);
+                if (v.x != -INFINITY) ll += v.y * kv_ex2(v.x - mm);
             }
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -374,7 +363,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                 *reinterpret_cast<uint2 *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + 4 * c) =
                     make_uint2(Elem<DT>::down2(v.x * inv, v.y * inv), Elem<DT>::down2(v.z * inv, v.w * inv));
                 if (p.lse && c == 0)
-                    p.lse[(int64_t)row * p.heads + head] = ll == 0.f ? -INFINITY : (mm + log2f(ll) - kShift) * kLn2;
+                    p.lse[(int64_t)row * p.heads + head] = kv_lse(mm, ll);
             } else {
                 *reinterpret_cast<float4 *>(p.part + ((size_t)place * C::kRows + r) * D + 4 * c) = v;
                 if (c == 0) p.ml[(size_t)place * C::kRows + r] = make_float2(mm, ll);
@@ -394,28 +383,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                 __threadfence();
                 for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kWarps) {
                     const int r = i / (D / 4), c = i % (D / 4), t = p.by_group(r), j = r - t * p.group;
-                    float mm = -INFINITY, ll = 0.f;
-                    for (int k = c0; k <= c1; ++k)
-                        mm = fmaxf(mm, __ldcg(&p.ml[(size_t)(2 * k + (k == c0)) * C::kRows + r]).x);
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int k = c0; k <= c1; ++k) {
-                        const size_t at = (size_t)(2 * k + (k == c0)) * C::kRows + r;
-                        const float2 a = __ldcg(&p.ml[at]);
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D + 4 * c));
-                        const float f = a.x == -INFINITY ? (mm == -INFINITY ? 1.f : 0.f) : ex2(a.x - mm);
-                        ll += a.y * f;
-                        v.x += x.x * f;
-                        v.y += x.y * f;
-                        v.z += x.z * f;
-                        v.w += x.w * f;
-                    }
-                    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                    const int row = w.rq.row0 + t, head = w.h * p.group + j;
-                    *reinterpret_cast<uint2 *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + 4 * c) =
-                        make_uint2(Elem<DT>::down2(v.x * inv, v.y * inv), Elem<DT>::down2(v.z * inv, v.w * inv));
-                    if (p.lse && c == 0)
-                        p.lse[(int64_t)row * p.heads + head] = ll == 0.f ? -INFINITY : (mm + log2f(ll) - kShift) * kLn2;
+                    kv_join4<DT, D>(p, c0, c1, C::kRows, r, c, w.rq.row0 + t, w.h * p.group + j);
                 }
             }
         }
@@ -424,63 +392,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
     cp_async_wait_all();
 }
 
-// A warp per (row, head), a token at a time.
-template <int DT, int D>
-__global__ void __launch_bounds__(256) kv_plain_kernel(const __grid_constant__ KvParams p) {
-    constexpr int kPer = D / 32;
-    griddep_wait();
-    griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, at = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int n = at / p.heads, h = at - n * p.heads;
-    if (n >= p.N) return;
-    for (int b = 0; b < p.B; ++b) {
-        const KvReq r = kv_req(p, b);
-        if (n < r.row0 || n >= r.row0 + r.T) continue;
-        const KvSeen seen = kv_seen(p, r, n - r.row0);
-        const int64_t head = (int64_t)(h / p.group) * p.head_stride;
-        using T = typename Elem<DT>::T;
-        float q[kPer], o[kPer] = {}, m = -INFINITY, l = 0.f;
-        for (int j = 0; j < kPer; ++j)
-            q[j] = Elem<DT>::up(reinterpret_cast<const T *>(p.q)[(int64_t)n * p.q_stride + (int64_t)h * D + kPer * lane + j]);
-        for (int x = 0; x < r.len; ++x) {
-            if (!(seen.word(x) & 1)) continue;
-            const int pi = p.by_page(x), pg = __ldg(p.table + (size_t)b * p.max_pages + pi);
-            const bool ok = pg >= 0 && pg < p.num_pages;
-            const int64_t row = (int64_t)pg * p.page_stride + (int64_t)(x - pi * p.page_size) * p.token_stride + head;
-            float s = 0.f, v[kPer];
-            for (int j = 0; j < kPer; ++j) {
-                s += ok ? q[j] * Elem<DT>::up(reinterpret_cast<const T *>(p.k)[row + kPer * lane + j]) : 0.f;
-                v[j] = ok ? Elem<DT>::up(reinterpret_cast<const T *>(p.v)[row + kPer * lane + j]) : 0.f;
-            }
-            for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-            s *= p.scale_log2;
-            const float mn = fmaxf(m, s), f = mn == m ? 1.f : exp2f(m - mn), w = mn == -INFINITY ? 0.f : exp2f(s - mn);
-            m = mn;
-            l = l * f + w;
-            for (int j = 0; j < kPer; ++j) o[j] = o[j] * f + w * v[j];
-        }
-        for (int j = 0; j < kPer; ++j)
-            reinterpret_cast<T *>(p.out)[(int64_t)n * p.out_stride + (int64_t)h * D + kPer * lane + j] =
-                Elem<DT>::down(l == 0.f ? 0.f : o[j] / l);
-        if (p.lse && lane == 0) p.lse[(int64_t)n * p.heads + h] = (m + log2f(l)) * 0.6931471805599453f;
-    }
-}
-
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Rows of a partial sum's place in the workspace: (token, head) rows of a unit.
+// Rows of a partial sum's place in the workspace: (token, head) rows of a unit
+// of the launch that takes a call of `tokens` rows at most.
 constexpr int kFewRows = 32;
-int place_rows(long long rows) { return rows <= kFewRows ? kFewRows : rows <= 128 ? 128 : 256; }
+int place_rows(long long tokens, int group) {
+    return tokens * group <= kFewRows ? kFewRows : tokens <= kv_tile_tokens(group) ? kKvTileRows : 2 * kKvTileRows;
+}
 
 constexpr size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 constexpr size_t kDoneOffset = sizeof(WsHeader);
 static_assert(kDoneOffset + kKvMaxBlocks * 4 <= SPX_KV_WORKSPACE_ZERO, "what must start at zero");
 struct KvLayout {
-    size_t ml, part, bytes;
+    size_t seams, ml, part, bytes;
 };
 KvLayout kv_layout(int rows, int D) {
     KvLayout l;
-    l.ml = SPX_KV_WORKSPACE_ZERO;
+    l.seams = SPX_KV_WORKSPACE_ZERO;
+    l.ml = l.seams + up256((size_t)kKvMaxBlocks * 16);
     l.part = l.ml + up256((size_t)2 * kKvMaxBlocks * rows * 8);
     l.bytes = l.part + (size_t)2 * kKvMaxBlocks * rows * D * 4;
     return l;
@@ -538,7 +468,7 @@ extern "C" size_t spx_kv_workspace_size(int B, int N, int max_q, int max_len, in
     if ((long long)N * heads > 1 << 30 || (long long)max_q * heads > 1 << 30) return 0;
     const long long rows = max_q < N ? max_q : N;
     if ((double)B * kv_heads * (rows * (heads / kv_heads) / 64 + 1) * (max_len / kKvTile + 1) > 2e9) return 0;
-    return kv_layout(place_rows(rows * (heads / kv_heads)), D).bytes;
+    return kv_layout(place_rows(rows, heads / kv_heads), D).bytes;
 }
 
 extern "C" int spx_kv_attention(const spx_kv_attention_args *a, spx_stream_t stream) {
@@ -591,9 +521,10 @@ extern "C" int spx_kv_attention(const spx_kv_attention_args *a, spx_stream_t str
     p.scale_log2 = a->scale * 1.4426950408889634f;
     p.hdr = static_cast<WsHeader *>(a->ws);
     p.budget = a->wait_budget_ns ? a->wait_budget_ns : 2000000000ull;
-    const long long rows = (long long)(a->max_q < a->N ? a->max_q : a->N) * p.group;
+    const int tokens = a->max_q < a->N ? a->max_q : a->N;
+    const long long rows = (long long)tokens * p.group;
     uint8_t *ws = static_cast<uint8_t *>(a->ws);
-    const KvLayout l = kv_layout(place_rows(rows), c.D);
+    const KvLayout l = kv_layout(place_rows(tokens, p.group), c.D);
     p.done = reinterpret_cast<uint32_t *>(ws + kDoneOffset);
     p.ml = reinterpret_cast<float2 *>(ws + l.ml);
     p.part = reinterpret_cast<float *>(ws + l.part);
@@ -609,11 +540,6 @@ extern "C" int spx_kv_attention(const spx_kv_attention_args *a, spx_stream_t str
         return c.D == 128 ? (f16 ? launch_few_rt<SPX_F16, 128>(p, blocks, rows, s) : launch_few_rt<SPX_BF16, 128>(p, blocks, rows, s))
                           : (f16 ? launch_few_rt<SPX_F16, 64>(p, blocks, rows, s) : launch_few_rt<SPX_BF16, 64>(p, blocks, rows, s));
     }
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = latent_config(dim3((unsigned)(((long long)a->N * a->heads + 7) / 8)), 256, 0,
-                                           s, attr, 1);
-    return record_launch(c.D == 128 ? (f16 ? cudaLaunchKernelEx(&cfg, kv_plain_kernel<SPX_F16, 128>, p)
-                                           : cudaLaunchKernelEx(&cfg, kv_plain_kernel<SPX_BF16, 128>, p))
-                                    : (f16 ? cudaLaunchKernelEx(&cfg, kv_plain_kernel<SPX_F16, 64>, p)
-                                           : cudaLaunchKernelEx(&cfg, kv_plain_kernel<SPX_BF16, 64>, p)));
+    p.seams = reinterpret_cast<int4 *>(ws + l.seams);
+    return launch_kv_tiles(p, c.dtype, sms < kKvMaxBlocks ? sms : kKvMaxBlocks, s);
 }

@@ -1,0 +1,550 @@
+// spx_kv_tiles.cu -- attention over the paged cache of keys and values, calls
+// of more than 32 (token, head) rows a key head: trees, verify passes, prompts.
+//
+// Rows that share a key head (the tokens of a request times the query heads of
+// the group) are the 128 rows of a product:  S = Q K^T (128 rows x 128 cached
+// tokens), softmax in registers, a row a thread, P back into S's tensor memory
+// as the A operand of O += P V.  Keys and values come from the cache's pages as
+// they lie, by tensor copies of whole runs of a page's tokens.
+//
+//   attention launch  shares of key tiles, one block an SM; partial sums of the
+//                     units that cross from block to block
+//   join launch       their sums, weighed and added in the order of the blocks
+#include <math.h>
+#include <string.h>
+
+#include "spx_kv.cuh"
+#include "spx_tcgen05.cuh"
+
+namespace spx {
+
+namespace {
+
+constexpr int kThreads = 384;  // copies, two issuers of products, the list of seams; 2 x 4 softmax warps
+constexpr int kPiece = kKvTile * 128;  // 128 rows of 64 values, 16 KB
+
+struct KvMaps {
+    CUtensorMap k, v;  // [page][head][token][D], boxes of 64 values x box_tokens
+    CUtensorMap q;     // [row][head][D], boxes of 64 values x a group's heads x tile_tokens
+};
+
+// Two products are under way at a time, X = 0 and 1, and take turns: while one's
+// softmax runs, the other's products do.  TALL: two tiles of 128 rows of a unit,
+// on the same key tiles.  Otherwise a unit is one tile of rows, and X takes
+// every second key tile; the two sums are joined at the unit's end.
+template <int D, bool TALL>
+struct Tiles {
+    static constexpr int kPieces = D / 64;
+    static constexpr int kSlot = kPieces * kPiece;  // keys or values of a tile
+    static constexpr int kQTiles = TALL ? 2 : 1;
+    static constexpr int kRing = (14 - kQTiles * kPieces) / kPieces;  // slots, keys and values of a tile in turn
+    static constexpr int kSmem = (kQTiles * kPieces + kRing * kPieces) * kPiece + 3072;
+    static constexpr int kRows = kQTiles * kKvTileRows;  // rows of a unit
+    static_assert(kSmem <= kSmemLimit && kRing >= 5, "shared memory of one block");
+};
+struct Misc {
+    uint64_t qfull, qempty;              // by units
+    uint64_t full[16], empty[16];        // by slots
+    uint64_t sfull[2], pfull[2][2];      // by tiles of X; pfull: by halves of the keys
+    uint64_t odone[2], oempty[2];        // by units in which X has tiles
+    uint64_t turn[2], fin[2];
+    uint32_t tmem;
+    int abort;
+    uint32_t bad[2][4][4];               // tokens with values that are not finite, in the last four tiles of a unit
+    float2 ml[2][kKvTileRows];           // X's references and weights
+};
+static_assert(sizeof(Misc) <= 3072, "the misc area holds it");
+
+// A place in the ring and the parity of its use.
+template <int N>
+struct Place {
+    uint32_t i = 0, phase = 0;
+    __device__ __forceinline__ void advance(uint32_t n) {  // n <= N
+        i += n;
+        if (i >= N) {
+            i -= N;
+            phase ^= 1;
+        }
+    }
+    __device__ __forceinline__ void jump(uint32_t n) {
+        i += n;
+        phase ^= (i / N) & 1;
+        i %= N;
+    }
+};
+
+// A softmax row takes 128 scores in registers: 168 a thread, what 384 threads
+// share out evenly, are too few (65 spilled), so the first four warps give up
+// some (4 x 32 x 80 + 8 x 32 x 208 <= 384 x 168).
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+
+template <int DT, int D, bool TALL>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_tiles_kernel(const __grid_constant__ KvParams p, const __grid_constant__ KvMaps maps) {
+    using C = Tiles<D, TALL>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *qs = smem, *ring = smem + C::kQTiles * C::kSlot;
+    Misc &m = *reinterpret_cast<Misc *>(ring + C::kRing * C::kSlot);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(&m.qfull, 1);
+        mbar_init(&m.qempty, 2);
+        for (int i = 0; i < C::kRing; ++i) {
+            mbar_init(&m.full[i], 1);
+            mbar_init(&m.empty[i], TALL ? 2 : 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&m.sfull[x], 1);
+            mbar_init(&m.pfull[x][0], 4);
+            mbar_init(&m.pfull[x][1], 4);
+            mbar_init(&m.odone[x], 1);
+            mbar_init(&m.oempty[x], TALL ? 4 : 8);
+            mbar_init(&m.turn[x], 1);
+            mbar_init(&m.fin[x], 1);
+        }
+        m.abort = 0;
+        fence_mbar_init();
+    }
+    if (threadIdx.x < 32) (&m.bad[0][0][0])[threadIdx.x] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    const KvShare share = kv_find_share(p, p.span, lane);
+    if (share.left <= 0) {  // (all threads alike)
+        if (threadIdx.x == 0) p.seams[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    if (warp == 1) {
+        tmem_alloc(&m.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m.tmem;
+    const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_KV};
+    KvWalk w;
+    w.begin(p, share, p.span);
+    // Key tiles of X in the unit's part: TALL, those of its rows; else every second one.
+    const auto tiles_of = [&](int x) {
+        if (!TALL) return (w.end - w.tile - x + 1) / 2;
+        const int t0 = w.g * p.span + x * p.tile_tokens, last = min(t0 + p.tile_tokens, w.rq.T) - 1;
+        const int n = last < t0 ? 0 : (kv_none_see(p, w.rq, last) + kKvTile - 1) / kKvTile;
+        return min(max(n - w.tile, 0), w.end - w.tile);
+    };
+
+    if (warp < 4) {
+        fewer_registers();
+        if (warp == 0) {
+            // ---- copies: a unit's queries, then keys and values of its tiles in turn
+            const uint64_t pol = policy_evict_normal();
+            const int bt = p.box_tokens, boxes = kKvTile / bt, box = lane % boxes, piece = lane / boxes;
+            const bool mine = lane < boxes * C::kPieces;  // the lane's box of a tile
+            Place<C::kRing> r;
+            bool ok = true;
+            for (uint32_t u = 0; ok && w.left > 0; w.next(p, p.span), ++u) {
+                int next = -1;  // the page of the lane's box, looked up a tile ahead
+                const auto look_up = [&](int tile) {
+                    const int p0 = kKvTile * tile + bt * box;
+                    next = p0 < w.rq.len ? __ldg(p.table + (size_t)w.b * p.max_pages + p.by_page(p0)) : -1;
+                };
+                look_up(w.tile);
+                if (!(ok = ctl_wait(&m.qempty, (u & 1) ^ 1, ctl))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&m.qfull, C::kQTiles * C::kPieces * 128 * p.group * p.tile_tokens);
+                    for (int x = 0; x < C::kQTiles; ++x)
+                        for (int c = 0; c < C::kPieces; ++c)
+                            tma_load_3d(qs + (x * C::kPieces + c) * kPiece, &maps.q, 64 * c, w.h * p.group,
+                                        w.rq.row0 + w.g * p.span + x * p.tile_tokens, &m.qfull, pol);
+                }
+                __syncwarp();
+                for (int j = w.tile; ok && j < w.end; ++j) {
+                    const int p0 = kKvTile * j + bt * box, at = p0 - p.by_page(p0) * p.page_size;
+                    const int page = next < 0 || next >= p.num_pages ? p.num_pages : next;  // (past the last one: zeros)
+                    if (j + 1 < w.end) look_up(j + 1);
+    #pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, r.advance(1)) {
+                        if (!(ok = ctl_wait(&m.empty[r.i], r.phase ^ 1, ctl))) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&m.full[r.i], C::kSlot);
+                        __syncwarp();
+                        if (mine)
+                            tma_load_4d(ring + r.i * C::kSlot + piece * kPiece + box * bt * 128, kv ? &maps.v : &maps.k, 64 * piece,
+                                        at, w.h, page, &m.full[r.i], pol);
+                        __syncwarp();
+                    }
+                }
+            }
+        } else if (warp < 3) {
+            // ---- products of X: O_X of the last tile, then S_X of the next one, in one stretch behind everything that
+            // they wait for
+            const int x = warp - 1;
+            const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
+            const uint32_t id_s = idesc_f16_f32(128, 128) | fmt, id_o = idesc_f16_f32(128, D) | fmt | kIdescBMn;
+            const uint64_t qd = sw128_desc(smem_u32(qs) + (TALL ? x * C::kSlot : 0)), kd = sw128_desc(smem_u32(ring));
+            const uint64_t vd = sw128_desc_mn(smem_u32(ring), kPiece);
+            const uint32_t st = tmem + 128 * x, ot = tmem + 256 + 128 * x;
+            const auto scores = [&](uint32_t slot) {
+    #pragma unroll
+                for (int c = 0; c < C::kPieces; ++c)
+    #pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        umma_f16(st, qd + c * (kPiece / 16) + 2 * i, kd + slot * (C::kSlot / 16) + c * (kPiece / 16) + 2 * i, id_s,
+                                 c | i);
+            };
+            const auto sums = [&](uint32_t slot, int half, bool first) {
+    #pragma unroll
+                for (int i = 4 * half; i < 4 * half + 4; ++i)
+                    umma_f16_ta(ot, st + 8 * i, vd + slot * (C::kSlot / 16) + 128 * i, id_o, !first || i);
+            };
+            Place<C::kRing> at;             // of the keys of the unit's first tile
+            uint32_t tile = 0, step = 0, unit = 0;  // tiles and units of X before this one, turns
+            bool ok = true;
+            for (uint32_t u = 0; ok && w.left > 0; w.next(p, p.span), ++u) {
+                const int all = w.end - w.tile, n = tiles_of(x), most = TALL ? all : n;
+                Place<C::kRing> kr = at, vr = at;
+                vr.advance(1);
+                if (!TALL && x) {
+                    kr.advance(2);
+                    vr.advance(2);
+                }
+                ok = ctl_wait(&m.qfull, u & 1, ctl);
+    #pragma unroll 1
+                for (int j = 0; ok && j <= most; ++j, ++step) {
+                    const bool has_o = j > 0 && j <= n, has_s = j < n;
+                    ok = (j == most || ctl_wait(&m.full[kr.i], kr.phase, ctl)) && (j == 0 || ctl_wait(&m.full[vr.i], vr.phase, ctl)) &&
+                         // tile 1 goes behind tile 0's products of the same step, tile 0 behind tile 1's of the last one,
+                         // or they fall into step, both softmaxes at once and then both products
+                         (!TALL || (x ? ctl_wait(&m.turn[1], step & 1, ctl) : step == 0 || ctl_wait(&m.turn[0], (step - 1) & 1, ctl))) &&
+                         (!has_o || j > 1 || ctl_wait(&m.oempty[x], (unit & 1) ^ 1, ctl)) &&
+                         (!has_o || ctl_wait(&m.pfull[x][0], (tile + j - 1) & 1, ctl));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (has_o) {  // the first half while the softmax is at the second
+                        if (elect_one()) sums(vr.i, 0, j == 1);
+                        __syncwarp();
+                        if (!(ok = ctl_wait(&m.pfull[x][1], (tile + j - 1) & 1, ctl))) break;
+                        tc_fence_after();
+                    }
+                    if (elect_one()) {
+                        if (has_o) {
+                            sums(vr.i, 1, false);
+                            umma_commit(&m.empty[vr.i]);
+                            if (j == n) umma_commit(&m.odone[x]);
+                        } else if (j > 0) {
+                            mbar_arrive(&m.empty[vr.i]);
+                        }
+                        if (has_s) {
+                            scores(kr.i);
+                            umma_commit(&m.empty[kr.i]);
+                            umma_commit(&m.sfull[x]);
+                            if (j == n - 1) umma_commit(&m.qempty);
+                        } else if (j < most) {
+                            mbar_arrive(&m.empty[kr.i]);
+                        }
+                        if (n == 0 && j == 0) mbar_arrive(&m.qempty);
+                        if (TALL) mbar_arrive(&m.turn[x ^ 1]);
+                    }
+                    __syncwarp();
+                    if (j > 0) vr.advance(TALL ? 2 : 4);
+                    kr.advance(TALL ? 2 : 4);
+                }
+                tile += n;
+                unit += n > 0;
+                at.jump(2 * all);
+            }
+        } else if (warp == 3) {
+            // ---- the unit that begins in this share and ends in a later one, for the join launch
+            int4 seam = make_int4(-1, 0, 0, 0);
+            for (; w.left > 0; w.next(p, p.span))
+                if (w.tile == 0 && w.end < w.nt) seam = make_int4(w.b, w.h, w.g, (w.flat + w.nt - 1) / share.share);
+            if (lane == 0) p.seams[blockIdx.x] = seam;
+        }
+    } else {
+        more_registers();
+        // ---- softmax and results: a row a thread
+        const int x = (warp - 4) >> 2, q = warp & 3, r = 32 * q + lane;
+        const uint32_t quarter = (uint32_t)(32 * q) << 16;
+        const uint32_t st = tmem + quarter + 128 * x, ot = tmem + quarter + 256;
+        const int t_of = p.by_group(r), j_of = r - t_of * p.group;
+        uint32_t tile = 0, before = 0, units[2] = {0, 0};  // tiles of X, tiles of the block, units with tiles of each X, so far
+#pragma unroll 1
+        for (uint32_t u = 0; w.left > 0; w.next(p, p.span), ++u) {
+            const int n = tiles_of(x), t0 = w.g * p.span, t = t0 + (TALL ? x * p.tile_tokens : 0) + t_of;
+            const bool live = t_of < p.tile_tokens && t < w.rq.T;
+            const KvSeen seen = kv_seen(p, w.rq, live ? t : w.rq.T);
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int all = kv_all_see(p, w.rq, t0);
+            float mr = -INFINITY, l = 0.f;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                ctl_wait(&m.sfull[x], (tile + i) & 1, ctl);
+                tc_fence_after();
+                const int li = TALL ? i : 2 * i + x, j = w.tile + li, p0 = kKvTile * j;
+                const bool masked = p0 + kKvTile > all;
+                if (warp_live) {
+                    uint32_t s[128];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(st + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+                    tmem_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t word = seen.word(p0 + 32 * c);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!(word >> k & 1)) s[32 * c + k] = 0xFF800000u;
+                        }
+                    }
+                    float mx[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(s[k]);
+#pragma unroll
+                    for (int k = 8; k < 128; ++k) mx[k & 7] = fmaxf(mx[k & 7], __uint_as_float(s[k]));
+#pragma unroll
+                    for (int o = 4; o; o >>= 1)
+#pragma unroll
+                        for (int k = 0; k < o; ++k) mx[k] = fmaxf(mx[k], mx[k + o]);
+                    const float top = mx[0] * p.scale_log2;  // (scale > 0)
+                    const bool rise = top > mr + kKvSlack;
+                    if (__any_sync(0xffffffffu, rise)) {
+                        const float mn = rise ? top : mr, f = mn == mr ? 1.f : ex2(mr - mn);
+                        mr = mn;
+                        l *= f;
+                        if (i > 0) {
+                            // (O_X of the last tile is done: this tile's S_X came behind it)
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(ot + 128 * x + c, o);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_st16(ot + 128 * x + c, o);
+                            }
+                        }
+                    }
+                    const float ref = mr == -INFINITY ? 0.f : kKvShift - mr;
+                    const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), ref2 = pack2(ref, ref);
+                    uint64_t l2[2] = {0, 0};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 v = unpack2(fma2(pack2(__uint_as_float(s[32 * c + 2 * k]), __uint_as_float(s[32 * c + 2 * k + 1])),
+                                                          sc2, ref2));
+                            const float a = ex2(v.x), b = ex2(v.y);
+                            l2[k & 1] = add2(l2[k & 1], pack2(a, b));
+                            o[k] = Elem<DT>::down2(a, b);  // rounded for the tensor cores; the weights' own sum is not
+                        }
+                        tmem_st16(st + 16 * c, o);  // over S, which is in registers
+                        if ((c & 1) && !masked) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&m.pfull[x][c >> 1]);
+                        }
+                    }
+                    const float2 la = unpack2(add2(l2[0], l2[1]));
+                    l += la.x + la.y;
+                } else if (!masked && lane == 0) {
+                    mbar_arrive(&m.pfull[x][0]);
+                    mbar_arrive(&m.pfull[x][1]);
+                }
+                if (masked) {
+                    // Of a tile that not every row sees whole, the values of tokens past the length, and of those that
+                    // hold one which is not finite, become zeros, as a weight of 0 does not make them so; the rows
+                    // that see such a token become NaNs at the end.  A token a thread.
+                    const uint32_t item = 2 * (before + li) + 1, slot = item % C::kRing;
+                    ctl_wait(&m.full[slot], (item / C::kRing) & 1, ctl);
+                    uint8_t *row = ring + slot * C::kSlot + r * 128;
+                    bool zero = p0 + r >= w.rq.len;
+                    if (!zero) {
+                        uint32_t z = 0;
+#pragma unroll
+                        for (int k = 0; k < 8 * C::kPieces; ++k) {
+                            const uint4 v = lds128(row + (k >> 3) * kPiece + (((k ^ r) & 7) << 4));
+                            z = Elem<DT>::fma2(v.x, 0u, z);
+                            z = Elem<DT>::fma2(v.y, 0u, z);
+                            z = Elem<DT>::fma2(v.z, 0u, z);
+                            z = Elem<DT>::fma2(v.w, 0u, z);
+                        }
+                        if (z & 0x7FFF7FFFu) {
+                            zero = true;
+                            atomicOr(&m.bad[u & 1][j & 3][r >> 5], 1u << (r & 31));
+                        }
+                    }
+                    if (zero)
+#pragma unroll
+                        for (int k = 0; k < 8 * C::kPieces; ++k)
+                            *reinterpret_cast<uint4 *>(row + (k >> 3) * kPiece + (((k ^ r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&m.pfull[x][0]);
+                        mbar_arrive(&m.pfull[x][1]);
+                    }
+                }
+            }
+            // ---- the unit's end
+            const int other = TALL ? 0 : tiles_of(x ^ 1);
+            if (n) ctl_wait(&m.odone[x], units[x] & 1, ctl);
+            if (other) ctl_wait(&m.odone[x ^ 1], units[x ^ 1] & 1, ctl);
+            tc_fence_after();
+            if (!TALL) m.ml[x][r] = make_float2(mr, l);
+            bar_sync(1, 256);  // references, weights and lists of bad tokens are there
+            float f[2] = {1.f, 1.f};
+            if (!TALL) {
+                const float2 a = m.ml[0][r], b = m.ml[1][r];
+                mr = fmaxf(a.x, b.x);
+                f[0] = kv_factor(a.x, mr);
+                f[1] = kv_factor(b.x, mr);
+                l = a.y * f[0] + b.y * f[1];
+            }
+            float poison = 0.f;
+            for (int j = max(w.tile, all / kKvTile); j < w.end; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (m.bad[u & 1][j & 3][c] & seen.word(kKvTile * j + 32 * c)) poison = NAN;
+            const bool whole = w.whole();
+            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            f[0] *= inv;
+            f[1] *= inv;
+            const int head = w.h * p.group + j_of, out_row = w.rq.row0 + t;
+            const int own = TALL ? 128 * x + r : r;  // row of the unit
+            const size_t place = ((size_t)(2 * blockIdx.x + (w.tile == 0)) * C::kRows + own);
+            if (live && (TALL || x == 0)) {
+                if (!whole)
+                    p.ml[place] = make_float2(mr, l);
+                else if (p.lse)
+                    p.lse[(int64_t)out_row * p.heads + head] = kv_lse(mr, l);
+            }
+            // (else a half of the columns each)
+            const int c0 = TALL ? 0 : x * (D / 2), c1 = TALL ? D : c0 + D / 2;
+            const bool has[2] = {TALL ? n > 0 : (x ? other : n) > 0, !TALL && (x ? n : other) > 0};
+            if (warp_live) {
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 16) {
+                    float v[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = poison;
+#pragma unroll
+                    for (int y = 0; y < (TALL ? 1 : 2); ++y)
+                        if (has[y]) {
+                            uint32_t o[16];
+                            tmem_ld16(ot + 128 * (TALL ? x : y) + c, o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(o[k]), f[y], v[k]);
+                        }
+                    if (live && whole) {
+                        uint32_t o[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = Elem<DT>::down2(v[2 * k], v[2 * k + 1]);
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)out_row * p.out_stride + (int64_t)head * D + c);
+                        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                    } else if (live) {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part + place * D + c);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (n) mbar_arrive(&m.oempty[x]);
+                if (other) mbar_arrive(&m.oempty[x ^ 1]);
+            }
+            if (warp == 4 && lane < 16) (&m.bad[(u & 1) ^ 1][0][0])[lane] = 0;
+            bar_sync(1, 256);  // everyone has read what the next unit writes
+            tile += n;
+            before += w.end - w.tile;
+            units[x] += n > 0;
+            units[x ^ 1] += other > 0;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (m.abort) {
+        if (warp == 0) ctl_settle(kSettleNs);
+        if (warp == 1 || warp == 2) {
+            if (elect_one()) umma_commit(&m.fin[warp - 1]);
+            ctl_drain(&m.fin[warp - 1], 0, kSettleNs);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------- join --
+// Block (block of the attention launch in which a unit begins that ends in a
+// later one, 16 rows of it): 4 values a thread.
+constexpr int kJoinRows = 16, kJoinThreads = 256;
+template <int DT, int D>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ KvParams p, int unit_rows) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int c0 = blockIdx.x;
+    const int4 seam = __ldcg(p.seams + c0);
+    if (seam.x < 0) return;
+    const KvReq rq = kv_req(p, seam.x);
+    for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
+        const int r = (int)blockIdx.y * kJoinRows + i / (D / 4), c = i % (D / 4), in = r % kKvTileRows;
+        const int t_of = p.by_group(in), t = seam.z * p.span + r / kKvTileRows * p.tile_tokens + t_of;
+        if (t_of >= p.tile_tokens || t >= rq.T) continue;
+        kv_join4<DT, D>(p, c0, seam.w, unit_rows, r, c, rq.row0 + t, seam.y * p.group + in - t_of * p.group);
+    }
+}
+
+// -------------------------------------------------------------------- host --
+bool kv_maps(const KvParams &p, int dt, KvMaps *m) {
+    memset(m, 0, sizeof(*m));
+    // (a stride of a dimension of one is not used, but has to pass for one)
+    const uint64_t row = (uint64_t)p.D * 2;
+    const uint64_t cd[4] = {(uint64_t)p.D, (uint64_t)p.page_size, (uint64_t)p.kv_heads, (uint64_t)p.num_pages};
+    const uint64_t cs[3] = {(uint64_t)p.token_stride * 2, p.kv_heads > 1 ? (uint64_t)p.head_stride * 2 : row,
+                            p.num_pages > 1 ? (uint64_t)p.page_stride * 2 : row};
+    const uint32_t cb[4] = {64, (uint32_t)p.box_tokens, 1, 1};
+    const uint64_t qd[3] = {(uint64_t)p.D, (uint64_t)p.heads, (uint64_t)p.N};
+    const uint64_t qst[2] = {row, p.N > 1 ? (uint64_t)p.q_stride * 2 : row};
+    const uint32_t qb[3] = {64, (uint32_t)p.group, (uint32_t)p.tile_tokens};
+    return map_rows64(&m->k, dt, p.k, 4, cd, cs, cb) && map_rows64(&m->v, dt, p.v, 4, cd, cs, cb) &&
+           map_rows64(&m->q, dt, p.q, 3, qd, qst, qb);
+}
+
+template <int DT, int D, bool TALL>
+int launch_dt(const KvParams &p, const KvMaps &maps, int blocks, cudaStream_t s) {
+    using C = Tiles<D, TALL>;
+    int st = set_smem<kv_tiles_kernel<DT, D, TALL>>(C::kSmem);
+    if (st) return st;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t c = latent_config(dim3((unsigned)blocks), kThreads, C::kSmem, s, attr, 1);
+    if ((st = record_launch(cudaLaunchKernelEx(&c, kv_tiles_kernel<DT, D, TALL>, p, maps)))) return st;
+    c = latent_config(dim3((unsigned)blocks, C::kRows / kJoinRows), kJoinThreads, 0, s, attr, 1);
+    return record_launch(cudaLaunchKernelEx(&c, kv_join_kernel<DT, D>, p, C::kRows));
+}
+template <int DT>
+int launch_d(const KvParams &p, const KvMaps &maps, int blocks, bool tall, cudaStream_t s) {
+    if (p.D == 128) return tall ? launch_dt<DT, 128, true>(p, maps, blocks, s) : launch_dt<DT, 128, false>(p, maps, blocks, s);
+    return tall ? launch_dt<DT, 64, true>(p, maps, blocks, s) : launch_dt<DT, 64, false>(p, maps, blocks, s);
+}
+
+}  // namespace
+
+int launch_kv_tiles(KvParams &p, int dt, int blocks, cudaStream_t s) {
+    p.tile_tokens = kv_tile_tokens(p.group);
+    const bool tall = (p.max_q < p.N ? p.max_q : p.N) > p.tile_tokens;
+    p.span = tall ? 2 * p.tile_tokens : p.tile_tokens;
+    p.box_tokens = 16;
+    while (p.box_tokens < kKvTile && p.page_size % (2 * p.box_tokens) == 0) p.box_tokens *= 2;
+    KvMaps maps;
+    if (!kv_maps(p, dt, &maps)) return SPX_ERR_UNSUPPORTED;
+    return dt == SPX_F16 ? launch_d<SPX_F16>(p, maps, blocks, tall, s) : launch_d<SPX_BF16>(p, maps, blocks, tall, s);
+}
+
+}  // namespace spx
