@@ -39,6 +39,7 @@ struct KvParams {
     int4 *seams;       // [blocks] request, key head, rows and last block of the unit that begins in a block and ends in
                        // a later one (request -1: none)
     int span;          // rows (tokens) of a unit
+    int unit_cost;     // of a unit beside its tiles, in tiles
     int tile_tokens;   // rows (tokens) of a product of 128 (token, head) rows
     int box_tokens;    // cached tokens of one copy: the largest power of two that divides a page, 128 at most
 };
@@ -109,6 +110,8 @@ __device__ __forceinline__ int kv_none_see(const KvParams &p, const KvReq &r, in
 // units, in the order request, key head, rows, are dealt out in equal
 // contiguous shares, one a block: a long request and a ragged batch both fill
 // the machine, and a block meets at most two units that are not its own alone.
+// What a unit costs beside its tiles counts as `unit_cost` tiles in front of
+// them that nobody works on, or a block with many short units would be late.
 // A share that begins or ends inside a unit leaves a partial sum in the
 // workspace: block c has place 2c for the unit in which its share begins,
 // 2c + 1 for one that begins in its share and ends in a later block's.
@@ -116,16 +119,20 @@ __device__ __forceinline__ int kv_groups(int T, int span) { return (T + span - 1
 __device__ __forceinline__ int kv_tiles(const KvParams &p, const KvReq &r, int g, int span) {
     return max((kv_none_see(p, r, min((g + 1) * span, r.T) - 1) + kKvTile - 1) / kKvTile, 1);
 }
+// Tiles of all of a key head's units, with what a unit costs beside them.
 __device__ __forceinline__ int kv_head_tiles(const KvParams &p, const KvReq &r, int span) {
-    int n = 0;
-    for (int g = 0; g < kv_groups(r.T, span); ++g) n += kv_tiles(p, r, g, span);
+    const int groups = kv_groups(r.T, span);
+    if (groups <= 1 || p.tree || !p.causal) return groups ? groups * (kv_tiles(p, r, 0, span) + p.unit_cost) : 0;
+    // (kv_tiles of all but the last unit in three instructions each, as a long prompt has many)
+    int n = kv_tiles(p, r, groups - 1, span) + groups * p.unit_cost, a = r.len - r.T + span + kKvTile - 1;
+    for (int g = 1; g < groups; ++g, a += span) n += max(a / kKvTile, 1);
     return n;
 }
 
 // Where a block's share begins, the same for all its threads.
 struct KvShare {
     int b, h, g, off;  // unit, and the first tile of it
-    int flat, left;    // index of that tile among the call's; tiles of the share
+    int flat, left;    // index of that tile among the call's; tiles of the share from it on
     int share;         // tiles of a whole share
     KvReq rq;
 };
@@ -175,7 +182,13 @@ __device__ __forceinline__ KvShare kv_find_share(const KvParams &p, int span, in
             const int per = __shfl_sync(0xffffffffu, n, l) / p.kv_heads;
             w.h = w.off / per;
             w.off -= w.h * per;
-            for (int t; w.off >= (t = kv_tiles(p, w.rq, w.g, span)); ++w.g) w.off -= t;
+            for (int t; w.off >= (t = kv_tiles(p, w.rq, w.g, span) + p.unit_cost); ++w.g) w.off -= t;
+            w.off -= p.unit_cost;
+            if (w.off < 0) {  // the share begins with what a unit costs
+                w.flat -= w.off;
+                w.left += w.off;
+                w.off = 0;
+            }
             return w;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
@@ -187,7 +200,7 @@ __device__ __forceinline__ KvShare kv_find_share(const KvParams &p, int span, in
 // A walk over a share, unit by unit; the same in every role of a block.
 struct KvWalk {
     int b, h, g, nt;    // unit, its tiles
-    int tile, end;      // tiles of the unit in this share
+    int tile, end;      // tiles of the unit in this share, one at least
     int flat, left;     // index of `tile` among the call's tiles; tiles of the share from `tile` on
     KvReq rq;
     __device__ __forceinline__ void begin(const KvParams &p, const KvShare &w, int span) {
@@ -204,8 +217,8 @@ struct KvWalk {
     }
     __device__ __forceinline__ bool whole() const { return tile == 0 && end == nt; }
     __device__ __forceinline__ void next(const KvParams &p, int span) {
-        left -= end - tile;
-        flat += end - tile;
+        left -= end - tile + p.unit_cost;
+        flat += end - tile + p.unit_cost;
         if (left <= 0) return;
         if (++g == kv_groups(rq.T, span)) {
             g = 0;
@@ -247,29 +260,48 @@ __device__ __forceinline__ float kv_lse(float m, float l) {
 __device__ __forceinline__ float kv_factor(float m, float common) {
     return m == -INFINITY ? (common == -INFINITY ? 1.f : 0.f) : kv_ex2(m - common);
 }
-// Four values of a row from the partial sums of the blocks c0 .. c1, in their
-// order, to the output.  r: row of a place, of which there are `rows`.
+// One warp: a row's result from the partial sums of the blocks c0 .. c1, added
+// in their order.  r: row of a place, of which there are `rows`.  The parts'
+// weights are read 32 at a time, a part a lane, so that the sums' loads wait
+// for one read and not for each other.
 template <int DT, int D>
-__device__ __forceinline__ void kv_join4(const KvParams &p, int c0, int c1, int rows, int r, int c, int row, int head) {
-    float mm = -INFINITY, ll = 0.f;
-    for (int k = c0; k <= c1; ++k) mm = fmaxf(mm, __ldcg(&p.ml[(size_t)(2 * k + (k == c0)) * rows + r]).x);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = c0; k <= c1; ++k) {
-        const size_t at = (size_t)(2 * k + (k == c0)) * rows + r;
-        const float2 a = __ldcg(&p.ml[at]);
-        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.part + at * D + 4 * c));
-        const float f = kv_factor(a.x, mm);
-        ll += a.y * f;
-        v.x += x.x * f;
-        v.y += x.y * f;
-        v.z += x.z * f;
-        v.w += x.w * f;
+__device__ __forceinline__ void kv_join_row(const KvParams &p, int c0, int c1, int rows, int r, int row, int head, int lane) {
+    constexpr int kPer = D / 32;
+    const auto place = [&](int k) { return (size_t)(2 * k + (k == c0)) * rows + r; };
+    float mm = -INFINITY, ll = 0.f, v[kPer] = {};
+    for (int k = c0 + lane; k <= c1; k += 32) mm = fmaxf(mm, __ldcg(&p.ml[place(k)]).x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    for (int k0 = c0; k0 <= c1; k0 += 32) {
+        const int n = min(c1 + 1 - k0, 32);
+        const float2 a = lane < n ? __ldcg(&p.ml[place(k0 + lane)]) : make_float2(-INFINITY, 0.f);
+        const float f = kv_factor(a.x, mm), w = a.y * f;
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float *src = p.part + place(k0 + i) * D + kPer * lane;
+            const float g = __shfl_sync(0xffffffffu, f, i);
+            ll += __shfl_sync(0xffffffffu, w, i);
+            if (kPer == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                v[0] = fmaf(x.x, g, v[0]);
+                v[1] = fmaf(x.y, g, v[1]);
+                v[kPer - 2] = fmaf(x.z, g, v[kPer - 2]);
+                v[kPer - 1] = fmaf(x.w, g, v[kPer - 1]);
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                v[0] = fmaf(x.x, g, v[0]);
+                v[1] = fmaf(x.y, g, v[1]);
+            }
+        }
     }
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    *reinterpret_cast<uint2 *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + 4 * c) =
-        make_uint2(Elem<DT>::down2(v.x * inv, v.y * inv), Elem<DT>::down2(v.z * inv, v.w * inv));
-    if (p.lse && c == 0) p.lse[(int64_t)row * p.heads + head] = kv_lse(mm, ll);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + kPer * lane);
+    const uint32_t lo = Elem<DT>::down2(v[0] * inv, v[1] * inv);
+    if (kPer == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, Elem<DT>::down2(v[kPer - 2] * inv, v[kPer - 1] * inv));
+    else
+        *dst = lo;
+    if (p.lse && lane == 0) p.lse[(int64_t)row * p.heads + head] = kv_lse(mm, ll);
 }
 
 // -------------------------------------------------------------------- host --

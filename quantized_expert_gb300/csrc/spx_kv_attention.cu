@@ -381,9 +381,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
             __syncthreads();
             if (*last_part) {
                 __threadfence();
-                for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kWarps) {
-                    const int r = i / (D / 4), c = i % (D / 4), t = p.by_group(r), j = r - t * p.group;
-                    kv_join4<DT, D>(p, c0, c1, C::kRows, r, c, w.rq.row0 + t, w.h * p.group + j);
+                for (int r = warp; r < rows; r += kWarps) {
+                    const int t = p.by_group(r), j = r - t * p.group;
+                    kv_join_row<DT, D>(p, c0, c1, C::kRows, r, w.rq.row0 + t, w.h * p.group + j, lane);
                 }
             }
         }
@@ -537,6 +537,7 @@ extern "C" int spx_kv_attention(const spx_kv_attention_args *a, spx_stream_t str
         const long long most = (long long)c.B * c.kv_heads * ((p.max_len + kKvTile - 1) / kKvTile + (p.max_len == 0));
         const int blocks = (int)(most < sms && most < kKvMaxBlocks ? most : sms < kKvMaxBlocks ? sms : kKvMaxBlocks);
         p.span = a->max_q;
+        p.unit_cost = 0;
         return c.D == 128 ? (f16 ? launch_few_rt<SPX_F16, 128>(p, blocks, rows, s) : launch_few_rt<SPX_BF16, 128>(p, blocks, rows, s))
                           : (f16 ? launch_few_rt<SPX_F16, 64>(p, blocks, rows, s) : launch_few_rt<SPX_BF16, 64>(p, blocks, rows, s));
     }

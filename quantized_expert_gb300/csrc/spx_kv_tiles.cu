@@ -20,8 +20,10 @@ namespace spx {
 
 namespace {
 
-constexpr int kThreads = 384;  // copies, two issuers of products, the list of seams; 2 x 4 softmax warps
+constexpr int kThreads = 384;  // copies of K and V, two issuers of products, copies of Q; 2 x 4 softmax warps
 constexpr int kPiece = kKvTile * 128;  // 128 rows of 64 values, 16 KB
+
+constexpr int kUnitCost = 2;  // tiles
 
 struct KvMaps {
     CUtensorMap k, v;  // [page][head][token][D], boxes of 64 values x box_tokens
@@ -136,28 +138,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 4) {
         fewer_registers();
         if (warp == 0) {
-            // ---- copies: a unit's queries, then keys and values of its tiles in turn
+            // ---- copies: keys and values of the tiles in turn
             const uint64_t pol = policy_evict_normal();
             const int bt = p.box_tokens, boxes = kKvTile / bt, box = lane % boxes, piece = lane / boxes;
             const bool mine = lane < boxes * C::kPieces;  // the lane's box of a tile
             Place<C::kRing> r;
             bool ok = true;
-            for (uint32_t u = 0; ok && w.left > 0; w.next(p, p.span), ++u) {
+            for (; ok && w.left > 0; w.next(p, p.span)) {
                 int next = -1;  // the page of the lane's box, looked up a tile ahead
                 const auto look_up = [&](int tile) {
                     const int p0 = kKvTile * tile + bt * box;
                     next = p0 < w.rq.len ? __ldg(p.table + (size_t)w.b * p.max_pages + p.by_page(p0)) : -1;
                 };
                 look_up(w.tile);
-                if (!(ok = ctl_wait(&m.qempty, (u & 1) ^ 1, ctl))) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&m.qfull, C::kQTiles * C::kPieces * 128 * p.group * p.tile_tokens);
-                    for (int x = 0; x < C::kQTiles; ++x)
-                        for (int c = 0; c < C::kPieces; ++c)
-                            tma_load_3d(qs + (x * C::kPieces + c) * kPiece, &maps.q, 64 * c, w.h * p.group,
-                                        w.rq.row0 + w.g * p.span + x * p.tile_tokens, &m.qfull, pol);
-                }
-                __syncwarp();
                 for (int j = w.tile; ok && j < w.end; ++j) {
                     const int p0 = kKvTile * j + bt * box, at = p0 - p.by_page(p0) * p.page_size;
                     const int page = next < 0 || next >= p.num_pages ? p.num_pages : next;  // (past the last one: zeros)
@@ -211,6 +204,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     #pragma unroll 1
                 for (int j = 0; ok && j <= most; ++j, ++step) {
                     const bool has_o = j > 0 && j <= n, has_s = j < n;
+                    // the slots of the unit's last tile are room for its results, and given back by the softmax warps
+                    const bool last_k = TALL && j == all - 1, last_v = (TALL ? j - 1 : 2 * (j - 1) + x) == all - 1;
                     ok = (j == most || ctl_wait(&m.full[kr.i], kr.phase, ctl)) && (j == 0 || ctl_wait(&m.full[vr.i], vr.phase, ctl)) &&
                          // tile 1 goes behind tile 0's products of the same step, tile 0 behind tile 1's of the last one,
                          // or they fall into step, both softmaxes at once and then both products
@@ -228,17 +223,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elect_one()) {
                         if (has_o) {
                             sums(vr.i, 1, false);
-                            umma_commit(&m.empty[vr.i]);
+                            if (!last_v) umma_commit(&m.empty[vr.i]);
                             if (j == n) umma_commit(&m.odone[x]);
-                        } else if (j > 0) {
+                        } else if (j > 0 && !last_v) {
                             mbar_arrive(&m.empty[vr.i]);
                         }
                         if (has_s) {
                             scores(kr.i);
-                            umma_commit(&m.empty[kr.i]);
+                            if (!last_k) umma_commit(&m.empty[kr.i]);
                             umma_commit(&m.sfull[x]);
                             if (j == n - 1) umma_commit(&m.qempty);
-                        } else if (j < most) {
+                        } else if (j < most && !last_k) {
                             mbar_arrive(&m.empty[kr.i]);
                         }
                         if (n == 0 && j == 0) mbar_arrive(&m.qempty);
@@ -253,10 +248,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 at.jump(2 * all);
             }
         } else if (warp == 3) {
-            // ---- the unit that begins in this share and ends in a later one, for the join launch
+            // ---- copies of the queries; the unit that begins in this share and ends in a later one, for the join launch
+            const uint64_t pol = policy_evict_normal();
             int4 seam = make_int4(-1, 0, 0, 0);
-            for (; w.left > 0; w.next(p, p.span))
+            bool ok = true;
+            for (uint32_t u = 0; w.left > 0; w.next(p, p.span), ++u) {
                 if (w.tile == 0 && w.end < w.nt) seam = make_int4(w.b, w.h, w.g, (w.flat + w.nt - 1) / share.share);
+                if (!ok || !(ok = ctl_wait(&m.qempty, (u & 1) ^ 1, ctl))) continue;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&m.qfull, C::kQTiles * C::kPieces * 128 * p.group * p.tile_tokens);
+                    for (int x = 0; x < C::kQTiles; ++x)
+                        for (int c = 0; c < C::kPieces; ++c)
+                            tma_load_3d(qs + (x * C::kPieces + c) * kPiece, &maps.q, 64 * c, w.h * p.group,
+                                        w.rq.row0 + w.g * p.span + x * p.tile_tokens, &m.qfull, pol);
+                }
+                __syncwarp();
+            }
             if (lane == 0) p.seams[blockIdx.x] = seam;
         }
     } else {
@@ -388,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- the unit's end
-            const int other = TALL ? 0 : tiles_of(x ^ 1);
+            const int other = tiles_of(x ^ 1), parts = w.end - w.tile;
             if (n) ctl_wait(&m.odone[x], units[x] & 1, ctl);
             if (other) ctl_wait(&m.odone[x ^ 1], units[x ^ 1] & 1, ctl);
             tc_fence_after();
@@ -420,47 +427,87 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else if (p.lse)
                     p.lse[(int64_t)out_row * p.heads + head] = kv_lse(mr, l);
             }
-            // (else a half of the columns each)
-            const int c0 = TALL ? 0 : x * (D / 2), c1 = TALL ? D : c0 + D / 2;
+            // Results pass through the slots of the unit's last tile (TALL: of its keys for X = 0, of its values for
+            // X = 1; else of its values), a warp's rows in a place of their own, so that stores are of whole rows and
+            // not of 16 bytes of 32 rows.  Units of 16 bytes are permuted by the row.
+            constexpr int kCols = TALL ? D : D / 2, kRow = kCols * 2, kU = kRow / 16;  // a warp's columns (else halves of D), bytes of a row
+            const uint32_t item = 2 * (before + parts - 1), k_slot = item % C::kRing, v_slot = (item + 1) % C::kRing;
+            if (TALL) ctl_wait(&m.full[k_slot], (item / C::kRing) & 1, ctl);  // (else it may hold another unit's by now)
+            ctl_wait(&m.full[v_slot], ((item + 1) / C::kRing) & 1, ctl);
+            uint8_t *stage = ring + (TALL && x == 0 ? k_slot : v_slot) * C::kSlot + ((TALL ? 0 : 4 * x) + q) * 32 * kRow;
+            const int c0 = TALL ? 0 : x * kCols;
             const bool has[2] = {TALL ? n > 0 : (x ? other : n) > 0, !TALL && (x ? n : other) > 0};
-            if (warp_live) {
-#pragma unroll 1
-                for (int c = c0; c < c1; c += 16) {
-                    float v[16];
+            const auto columns = [&](int c, float (&v)[16]) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = poison;
+                for (int k = 0; k < 16; ++k) v[k] = poison;
 #pragma unroll
-                    for (int y = 0; y < (TALL ? 1 : 2); ++y)
-                        if (has[y]) {
-                            uint32_t o[16];
-                            tmem_ld16(ot + 128 * (TALL ? x : y) + c, o);
+                for (int y = 0; y < (TALL ? 1 : 2); ++y)
+                    if (has[y]) {
+                        uint32_t o[16];
+                        tmem_ld16(ot + 128 * (TALL ? x : y) + c, o);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(o[k]), f[y], v[k]);
-                        }
-                    if (live && whole) {
-                        uint32_t o[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] = Elem<DT>::down2(v[2 * k], v[2 * k + 1]);
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)out_row * p.out_stride + (int64_t)head * D + c);
-                        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-                    } else if (live) {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part + place * D + c);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(o[k]), f[y], v[k]);
                     }
+            };
+            // unit k of row i of the warp's 32
+            const auto staged = [&](int i, int k) { return reinterpret_cast<uint4 *>(stage + i * kRow + ((k ^ (i & (kU - 1))) << 4)); };
+            const int first_row = 32 * q;
+            if (warp_live && whole) {
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 16) {
+                    float v[16];
+                    columns(c0 + c, v);
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = Elem<DT>::down2(v[2 * k], v[2 * k + 1]);
+                    *staged(lane, c / 8) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *staged(lane, c / 8 + 1) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                __syncwarp();
+#pragma unroll 4
+                for (int i = lane; i < 32 * kU; i += 32) {
+                    const int k = i % kU, tt = p.by_group(first_row + i / kU), jj = first_row + i / kU - tt * p.group;
+                    const int row = t0 + (TALL ? x * p.tile_tokens : 0) + tt;
+                    if (tt < p.tile_tokens && row < w.rq.T)
+                        *reinterpret_cast<uint4 *>(p.out + (int64_t)(w.rq.row0 + row) * p.out_stride +
+                                                   (int64_t)(w.h * p.group + jj) * D + c0 + 8 * k) = *staged(i / kU, k);
+                }
+            } else if (warp_live) {
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {  // 32 bits a value
+#pragma unroll 1
+                    for (int c = 0; c < kCols / 2; c += 16) {
+                        float v[16];
+                        columns(c0 + half * (kCols / 2) + c, v);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<float4 *>(staged(lane, c / 4 + k)) =
+                                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    }
+                    __syncwarp();
+                    float *dst = p.part + ((size_t)(2 * blockIdx.x + (w.tile == 0)) * C::kRows + (TALL ? 128 * x : 0) + first_row) * D +
+                                 c0 + half * (kCols / 2);
+#pragma unroll 4
+                    for (int i = lane; i < 32 * kU; i += 32)
+                        *reinterpret_cast<uint4 *>(dst + (size_t)(i / kU) * D + 4 * (i % kU)) = *staged(i / kU, i % kU);
+                    __syncwarp();
                 }
             }
+            fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 if (n) mbar_arrive(&m.oempty[x]);
-                if (other) mbar_arrive(&m.oempty[x ^ 1]);
+                if (!TALL && other) mbar_arrive(&m.oempty[x ^ 1]);
             }
             if (warp == 4 && lane < 16) (&m.bad[(u & 1) ^ 1][0][0])[lane] = 0;
             bar_sync(1, 256);  // everyone has read what the next unit writes
+            if (q == 0 && lane == 0 && (TALL || x == 0)) {
+                if (TALL) mbar_arrive(&m.empty[k_slot]);
+                mbar_arrive(&m.empty[v_slot]);
+            }
             tile += n;
-            before += w.end - w.tile;
+            before += parts;
             units[x] += n > 0;
             units[x ^ 1] += other > 0;
         }
@@ -483,21 +530,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- join --
 // Block (block of the attention launch in which a unit begins that ends in a
-// later one, 16 rows of it): 4 values a thread.
-constexpr int kJoinRows = 16, kJoinThreads = 256;
+// later one, 32 rows of it): 8 warps, a row a warp at a time.
+constexpr int kJoinRows = 32, kJoinThreads = 256;
 template <int DT, int D>
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ KvParams p, int unit_rows) {
     griddep_wait();
     griddep_launch_dependents();
-    const int c0 = blockIdx.x;
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31;
     const int4 seam = __ldcg(p.seams + c0);
     if (seam.x < 0) return;
     const KvReq rq = kv_req(p, seam.x);
-    for (int i = threadIdx.x; i < kJoinRows * (D / 4); i += kJoinThreads) {
-        const int r = (int)blockIdx.y * kJoinRows + i / (D / 4), c = i % (D / 4), in = r % kKvTileRows;
+#pragma unroll 1
+    for (int i = threadIdx.x >> 5; i < kJoinRows; i += kJoinThreads / 32) {
+        const int r = (int)blockIdx.y * kJoinRows + i, in = r % kKvTileRows;
         const int t_of = p.by_group(in), t = seam.z * p.span + r / kKvTileRows * p.tile_tokens + t_of;
         if (t_of >= p.tile_tokens || t >= rq.T) continue;
-        kv_join4<DT, D>(p, c0, seam.w, unit_rows, r, c, rq.row0 + t, seam.y * p.group + in - t_of * p.group);
+        kv_join_row<DT, D>(p, c0, seam.w, unit_rows, r, rq.row0 + t, seam.y * p.group + in - t_of * p.group, lane);
     }
 }
 
@@ -540,6 +588,7 @@ int launch_kv_tiles(KvParams &p, int dt, int blocks, cudaStream_t s) {
     p.tile_tokens = kv_tile_tokens(p.group);
     const bool tall = (p.max_q < p.N ? p.max_q : p.N) > p.tile_tokens;
     p.span = tall ? 2 * p.tile_tokens : p.tile_tokens;
+    p.unit_cost = kUnitCost;
     p.box_tokens = 16;
     while (p.box_tokens < kKvTile && p.page_size % (2 * p.box_tokens) == 0) p.box_tokens *= 2;
     KvMaps maps;
