@@ -36,8 +36,8 @@ struct KvParams {
     uint32_t *done;    // [blocks] parts of the unit that begins in a block and ends in a later one; zero between calls
     float2 *ml;        // [2 blocks][rows] reference and weight of a partial sum's row
     float *part;       // [2 blocks][rows][D] partial sums
-    int4 *seams;       // [blocks] request, key head, rows and last block of the unit that begins in a block and ends in
-                       // a later one (request -1: none)
+    int4 *seams;       // [blocks] of the unit that begins in a block and ends in a later one: its first row, its rows, key
+                       // head and last block (rows 0: none)
     int span;          // rows (tokens) of a unit
     int unit_cost;     // of a unit beside its tiles, in tiles
     int tile_tokens;   // rows (tokens) of a product of 128 (token, head) rows
@@ -261,37 +261,53 @@ __device__ __forceinline__ float kv_factor(float m, float common) {
     return m == -INFINITY ? (common == -INFINITY ? 1.f : 0.f) : kv_ex2(m - common);
 }
 // One warp: a row's result from the partial sums of the blocks c0 .. c1, added
-// in their order.  r: row of a place, of which there are `rows`.  The parts'
-// weights are read 32 at a time, a part a lane, so that the sums' loads wait
-// for one read and not for each other.
+// in their order.  r: row of a place, of which there are `rows`.  Sums are read
+// eight parts at a time, the first ones with the references and weights (a part
+// a lane, 32 at a time) and not behind them: what a row costs is the time of
+// one read after the other.
 template <int DT, int D>
 __device__ __forceinline__ void kv_join_row(const KvParams &p, int c0, int c1, int rows, int r, int row, int head, int lane) {
-    constexpr int kPer = D / 32;
+    constexpr int kPer = D / 32, kAhead = 8;
     const auto place = [&](int k) { return (size_t)(2 * k + (k == c0)) * rows + r; };
-    float mm = -INFINITY, ll = 0.f, v[kPer] = {};
-    for (int k = c0 + lane; k <= c1; k += 32) mm = fmaxf(mm, __ldcg(&p.ml[place(k)]).x);
+    uint32_t x[kAhead][kPer];
+    const auto fetch = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (k0 + i > c1) continue;
+            const float *src = p.part + place(k0 + i) * D + kPer * lane;
+            if (kPer == 4) {
+                const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(src));
+                x[i][0] = v.x;
+                x[i][1] = v.y;
+                x[i][kPer - 2] = v.z;
+                x[i][kPer - 1] = v.w;
+            } else {
+                const uint2 v = __ldcg(reinterpret_cast<const uint2 *>(src));
+                x[i][0] = v.x;
+                x[i][1] = v.y;
+            }
+        }
+    };
+    fetch(c0);
+    float2 a = c0 + lane <= c1 ? __ldcg(&p.ml[place(c0 + lane)]) : make_float2(-INFINITY, 0.f);
+    float mm = a.x, ll = 0.f, v[kPer] = {};
+    for (int k = c0 + 32 + lane; k <= c1; k += 32) mm = fmaxf(mm, __ldcg(&p.ml[place(k)]).x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    for (int k0 = c0; k0 <= c1; k0 += 32) {
-        const int n = min(c1 + 1 - k0, 32);
-        const float2 a = lane < n ? __ldcg(&p.ml[place(k0 + lane)]) : make_float2(-INFINITY, 0.f);
+    for (int k0 = c0; k0 <= c1; k0 += kAhead) {
+        const int at = (k0 - c0) & 31;
+        if (k0 > c0) {
+            fetch(k0);
+            if (at == 0) a = k0 + lane <= c1 ? __ldcg(&p.ml[place(k0 + lane)]) : make_float2(-INFINITY, 0.f);
+        }
         const float f = kv_factor(a.x, mm), w = a.y * f;
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float *src = p.part + place(k0 + i) * D + kPer * lane;
-            const float g = __shfl_sync(0xffffffffu, f, i);
-            ll += __shfl_sync(0xffffffffu, w, i);
-            if (kPer == 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
-                v[0] = fmaf(x.x, g, v[0]);
-                v[1] = fmaf(x.y, g, v[1]);
-                v[kPer - 2] = fmaf(x.z, g, v[kPer - 2]);
-                v[kPer - 1] = fmaf(x.w, g, v[kPer - 1]);
-            } else {
-                const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
-                v[0] = fmaf(x.x, g, v[0]);
-                v[1] = fmaf(x.y, g, v[1]);
-            }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const float g = __shfl_sync(0xffffffffu, f, at + i), h = __shfl_sync(0xffffffffu, w, at + i);
+            if (k0 + i > c1) continue;
+            ll += h;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) v[j] = fmaf(__uint_as_float(x[i][j]), g, v[j]);
         }
     }
     const float inv = ll == 0.f ? 0.f : 1.f / ll;

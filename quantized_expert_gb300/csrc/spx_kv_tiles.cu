@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     const KvShare share = kv_find_share(p, p.span, lane);
     if (share.left <= 0) {  // (all threads alike)
-        if (threadIdx.x == 0) p.seams[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        if (threadIdx.x == 0) p.seams[blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
     if (warp == 1) {
@@ -250,10 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 3) {
             // ---- copies of the queries; the unit that begins in this share and ends in a later one, for the join launch
             const uint64_t pol = policy_evict_normal();
-            int4 seam = make_int4(-1, 0, 0, 0);
+            int4 seam = make_int4(0, 0, 0, 0);
             bool ok = true;
             for (uint32_t u = 0; w.left > 0; w.next(p, p.span), ++u) {
-                if (w.tile == 0 && w.end < w.nt) seam = make_int4(w.b, w.h, w.g, (w.flat + w.nt - 1) / share.share);
+                if (w.tile == 0 && w.end < w.nt)
+                    seam = make_int4(w.rq.row0 + w.g * p.span, min(w.rq.T - w.g * p.span, p.span), w.h,
+                                     (w.flat + w.nt - 1) / share.share);
                 if (!ok || !(ok = ctl_wait(&m.qempty, (u & 1) ^ 1, ctl))) continue;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&m.qfull, C::kQTiles * C::kPieces * 128 * p.group * p.tile_tokens);
@@ -529,24 +531,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------- join --
-// Block (block of the attention launch in which a unit begins that ends in a
-// later one, 32 rows of it): 8 warps, a row a warp at a time.
-constexpr int kJoinRows = 32, kJoinThreads = 256;
+// Block (8 rows of a unit, block of the attention launch in which it begins to
+// end in a later one), a row a warp.
+constexpr int kJoinRows = 8;
 template <int DT, int D>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ KvParams p, int unit_rows) {
+__global__ void __launch_bounds__(32 * kJoinRows) kv_join_kernel(const __grid_constant__ KvParams p, int unit_rows) {
+    const int c0 = blockIdx.y, lane = threadIdx.x & 31;
+    const int r = (int)blockIdx.x * kJoinRows + (threadIdx.x >> 5), in = r % kKvTileRows;
+    const int t_of = p.by_group(in), t = r / kKvTileRows * p.tile_tokens + t_of;
     griddep_wait();
     griddep_launch_dependents();
-    const int c0 = blockIdx.x, lane = threadIdx.x & 31;
     const int4 seam = __ldcg(p.seams + c0);
-    if (seam.x < 0) return;
-    const KvReq rq = kv_req(p, seam.x);
-#pragma unroll 1
-    for (int i = threadIdx.x >> 5; i < kJoinRows; i += kJoinThreads / 32) {
-        const int r = (int)blockIdx.y * kJoinRows + i, in = r % kKvTileRows;
-        const int t_of = p.by_group(in), t = seam.z * p.span + r / kKvTileRows * p.tile_tokens + t_of;
-        if (t_of >= p.tile_tokens || t >= rq.T) continue;
-        kv_join_row<DT, D>(p, c0, seam.w, unit_rows, r, rq.row0 + t, seam.y * p.group + in - t_of * p.group, lane);
-    }
+    if (t_of >= p.tile_tokens || t >= seam.y) return;
+    kv_join_row<DT, D>(p, c0, seam.w, unit_rows, r, seam.x + t, seam.z * p.group + in - t_of * p.group, lane);
 }
 
 // -------------------------------------------------------------------- host --
@@ -573,7 +570,9 @@ int launch_dt(const KvParams &p, const KvMaps &maps, int blocks, cudaStream_t s)
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t c = latent_config(dim3((unsigned)blocks), kThreads, C::kSmem, s, attr, 1);
     if ((st = record_launch(cudaLaunchKernelEx(&c, kv_tiles_kernel<DT, D, TALL>, p, maps)))) return st;
-    c = latent_config(dim3((unsigned)blocks, C::kRows / kJoinRows), kJoinThreads, 0, s, attr, 1);
+    const int tokens = p.max_q < p.N ? p.max_q : p.N;  // rows of the largest unit
+    const int rows = TALL ? C::kRows : tokens * p.group;
+    c = latent_config(dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows), (unsigned)blocks), 32 * kJoinRows, 0, s, attr, 1);
     return record_launch(cudaLaunchKernelEx(&c, kv_join_kernel<DT, D>, p, C::kRows));
 }
 template <int DT>
