@@ -137,63 +137,99 @@ struct KvShare {
     KvReq rq;
 };
 
-// One warp: every lane gets the block's share.
+// Tiles of a unit with what it costs beside them, 0 past the request's last one.
+__device__ __forceinline__ int kv_unit_tiles(const KvParams &p, const KvReq &r, int g, int span, int groups) {
+    return g < groups ? kv_tiles(p, r, g, span) + p.unit_cost : 0;
+}
+__device__ __forceinline__ int warp_upto(int n, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) n += v;
+    }
+    return n;
+}
+
+// One warp: every lane gets the block's share.  Requests a lane each (the last
+// 32 stay in registers, which is all of a small batch); a single request's
+// units a lane each, as a long prompt has many.
 __device__ __forceinline__ KvShare kv_find_share(const KvParams &p, int span, int lane) {
     KvShare w{};
-    // tiles of the requests, 32 at a time; the last 32 stay in registers, which is all of them for a small batch
     int total = 0, n = 0;
     KvReq r{};
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        n = 0;
-        if (b0 + lane < p.B) {
-            r = kv_req(p, b0 + lane);
-            n = kv_head_tiles(p, r, span) * p.kv_heads;
-        }
-        total += __reduce_add_sync(0xffffffffu, n);
-    }
-    w.share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
-    w.flat = (int)min((int64_t)w.share * blockIdx.x, (int64_t)total);
-    w.left = min(w.share, total - w.flat);
-    if (w.left <= 0) return w;
-    int before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        if (p.B > 32) {
+    if (p.B == 1) {
+        r = kv_req(p, 0);
+        const int groups = kv_groups(r.T, span);
+        for (int g = lane; g < groups; g += 32) n += kv_unit_tiles(p, r, g, span, groups);
+        n = __reduce_add_sync(0xffffffffu, n) * p.kv_heads;
+        total = n;
+    } else {
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
             n = 0;
             if (b0 + lane < p.B) {
                 r = kv_req(p, b0 + lane);
                 n = kv_head_tiles(p, r, span) * p.kv_heads;
             }
+            total += __reduce_add_sync(0xffffffffu, n);
         }
-        int upto = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
+    }
+    w.share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
+    w.flat = (int)min((int64_t)w.share * blockIdx.x, (int64_t)total);
+    w.left = min(w.share, total - w.flat);
+    if (w.left <= 0) return w;
+    int per = n;  // of the request in which the share begins
+    w.off = w.flat;
+    if (p.B > 1) {
+        int before = 0;
+        for (int b0 = 0;; b0 += 32) {
+            if (b0 >= p.B) {  // (not reached)
+                w.left = 0;
+                return w;
+            }
+            if (p.B > 32) {
+                n = 0;
+                if (b0 + lane < p.B) {
+                    r = kv_req(p, b0 + lane);
+                    n = kv_head_tiles(p, r, span) * p.kv_heads;
+                }
+            }
+            const int upto = warp_upto(n, lane), off = w.flat - (before + upto - n);
+            const uint32_t mine = __ballot_sync(0xffffffffu, off >= 0 && off < n);
+            if (mine) {
+                const int l = __ffs(mine) - 1;
+                w.b = b0 + l;
+                w.off = __shfl_sync(0xffffffffu, off, l);
+                r.row0 = __shfl_sync(0xffffffffu, r.row0, l);
+                r.T = __shfl_sync(0xffffffffu, r.T, l);
+                r.len = __shfl_sync(0xffffffffu, r.len, l);
+                per = __shfl_sync(0xffffffffu, n, l);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
         }
-        const int off = w.flat - (before + upto - n);
-        const uint32_t mine = __ballot_sync(0xffffffffu, off >= 0 && off < n);
+    }
+    w.rq = r;
+    per /= p.kv_heads;
+    w.h = w.off / per;
+    w.off -= w.h * per;
+    const int groups = kv_groups(r.T, span);
+    for (int g0 = 0; g0 < groups; g0 += 32) {
+        const int t = kv_unit_tiles(p, r, g0 + lane, span, groups), upto = warp_upto(t, lane);
+        const uint32_t mine = __ballot_sync(0xffffffffu, w.off >= upto - t && w.off < upto);
         if (mine) {
             const int l = __ffs(mine) - 1;
-            w.b = b0 + l;
-            w.off = __shfl_sync(0xffffffffu, off, l);
-            w.rq.row0 = __shfl_sync(0xffffffffu, r.row0, l);
-            w.rq.T = __shfl_sync(0xffffffffu, r.T, l);
-            w.rq.len = __shfl_sync(0xffffffffu, r.len, l);
-            const int per = __shfl_sync(0xffffffffu, n, l) / p.kv_heads;
-            w.h = w.off / per;
-            w.off -= w.h * per;
-            for (int t; w.off >= (t = kv_tiles(p, w.rq, w.g, span) + p.unit_cost); ++w.g) w.off -= t;
-            w.off -= p.unit_cost;
-            if (w.off < 0) {  // the share begins with what a unit costs
-                w.flat -= w.off;
-                w.left += w.off;
-                w.off = 0;
-            }
-            return w;
+            w.g = g0 + l;
+            w.off -= __shfl_sync(0xffffffffu, upto - t, l);
+            break;
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        w.off -= __shfl_sync(0xffffffffu, upto, 31);
     }
-    w.left = 0;  // (not reached)
+    w.off -= p.unit_cost;
+    if (w.off < 0) {  // the share begins with what a unit costs
+        w.flat -= w.off;
+        w.left += w.off;
+        w.off = 0;
+    }
     return w;
 }
 

@@ -44,14 +44,26 @@ struct Tiles {
     static constexpr int kRows = kQTiles * kKvTileRows;  // rows of a unit
     static_assert(kSmem <= kSmemLimit && kRing >= 5, "shared memory of one block");
 };
+// A unit's part in a block's share, as the fourth warp hands it to the others.
+struct Unit {
+    int end;             // tiles tile .. end - 1 of the unit; 0: no more units
+    int tile, whole;     // whole: these are all of them
+    int row0, T, len;    // the request
+    int t0, h;           // first row (of the request), key head
+    int n[2];            // tiles of X
+    int b, pad;
+};
+constexpr int kUnitRing = 4;
 struct Misc {
+    uint64_t ufull[kUnitRing], uempty[kUnitRing];
     uint64_t qfull, qempty;              // by units
-    uint64_t full[16], empty[16];        // by slots
+    uint64_t full[14], empty[14];        // by slots
     uint64_t sfull[2], pfull[2][2];      // by tiles of X; pfull: by halves of the keys
     uint64_t odone[2], oempty[2];        // by units in which X has tiles
     uint64_t turn[2], fin[2];
     uint32_t tmem;
     int abort;
+    Unit unit[kUnitRing];
     uint32_t bad[2][4][4];               // tokens with values that are not finite, in the last four tiles of a unit
     float2 ml[2][kKvTileRows];           // X's references and weights
 };
@@ -76,7 +88,7 @@ struct Place {
 };
 
 // A softmax row takes 128 scores in registers: 168 a thread, what 384 threads
-// share out evenly, are too few (65 spilled), so the first four warps give up
+// share out evenly, are too few, so the first four warps give up
 // some (4 x 32 x 80 + 8 x 32 x 208 <= 384 x 168).
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
@@ -90,6 +102,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Misc &m = *reinterpret_cast<Misc *>(ring + C::kRing * C::kSlot);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        for (int i = 0; i < kUnitRing; ++i) {
+            mbar_init(&m.ufull[i], 1);
+            mbar_init(&m.uempty[i], 11);  // copies, issuers, softmax warps
+        }
         mbar_init(&m.qfull, 1);
         mbar_init(&m.qempty, 2);
         for (int i = 0; i < C::kRing; ++i) {
@@ -108,14 +124,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         m.abort = 0;
         fence_mbar_init();
     }
-    if (threadIdx.x < 32) (&m.bad[0][0][0])[threadIdx.x] = 0;
-    griddep_wait();
-    griddep_launch_dependents();
-    const KvShare share = kv_find_share(p, p.span, lane);
-    if (share.left <= 0) {  // (all threads alike)
-        if (threadIdx.x == 0) p.seams[blockIdx.x] = make_int4(0, 0, 0, 0);
-        return;
-    }
+    if (warp == 2) (&m.bad[0][0][0])[lane] = 0;
+    if (warp == 0 && lane < 3) prefetch_tmap(lane == 0 ? &maps.k : lane == 1 ? &maps.v : &maps.q);
     if (warp == 1) {
         tmem_alloc(&m.tmem, 512);
         tmem_relinquish();
@@ -125,49 +135,99 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = m.tmem;
     const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_KV};
-    KvWalk w;
-    w.begin(p, share, p.span);
-    // Key tiles of X in the unit's part: TALL, those of its rows; else every second one.
-    const auto tiles_of = [&](int x) {
-        if (!TALL) return (w.end - w.tile - x + 1) / 2;
-        const int t0 = w.g * p.span + x * p.tile_tokens, last = min(t0 + p.tile_tokens, w.rq.T) - 1;
-        const int n = last < t0 ? 0 : (kv_none_see(p, w.rq, last) + kKvTile - 1) / kKvTile;
-        return min(max(n - w.tile, 0), w.end - w.tile);
-    };
+    griddep_wait();
+    griddep_launch_dependents();
 
     if (warp < 4) {
         fewer_registers();
-        if (warp == 0) {
+        if (warp == 3) {
+            // ---- the share's units, one ahead of the copies of their queries; the unit that begins in this share and
+            // ends in a later one, for the join launch
+            const uint64_t pol = policy_evict_normal();
+            const KvShare share = kv_find_share(p, p.span, lane);
+            KvWalk w;
+            w.begin(p, share, p.span);
+            int4 seam = make_int4(0, 0, 0, 0);
+            int q_row = 0, q_head = 0;  // of the unit whose queries are to be copied next
+            bool ok = true;
+            for (uint32_t u = 0; ok; ++u) {
+                const bool more = w.left > 0;
+                if (!(ok = ctl_wait(&m.uempty[u % kUnitRing], ((u / kUnitRing) & 1) ^ 1, ctl))) break;
+                const int row = w.rq.row0 + w.g * p.span, head = w.h * p.group;
+                if (more) {
+                    // Key tiles of X in the unit's part: TALL, those of its rows; else every second one.
+                    const int parts = w.end - w.tile, t0 = w.g * p.span;
+                    int n[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int first = t0 + x * p.tile_tokens, last = min(first + p.tile_tokens, w.rq.T) - 1;
+                        const int all = last < first ? 0 : (kv_none_see(p, w.rq, last) + kKvTile - 1) / kKvTile;
+                        n[x] = TALL ? min(max(all - w.tile, 0), parts) : (parts - x + 1) / 2;
+                    }
+                    if (lane == 0)
+                        m.unit[u % kUnitRing] = Unit{w.end, w.tile, w.whole(), w.rq.row0, w.rq.T, w.rq.len, t0, w.h, {n[0], n[1]}, w.b, 0};
+                    if (w.tile == 0 && w.end < w.nt)
+                        seam = make_int4(row, min(w.rq.T - t0, p.span), w.h, (w.flat + w.nt - 1) / share.share);
+                    w.next(p, p.span);
+                } else if (lane == 0) {
+                    m.unit[u % kUnitRing].end = 0;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.ufull[u % kUnitRing]);
+                if (u > 0) {
+                    if (!(ok = ctl_wait(&m.qempty, (u & 1), ctl))) break;  // of the unit before the last
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&m.qfull, C::kQTiles * C::kPieces * 128 * p.group * p.tile_tokens);
+                        for (int x = 0; x < C::kQTiles; ++x)
+                            for (int c = 0; c < C::kPieces; ++c)
+                                tma_load_3d(qs + (x * C::kPieces + c) * kPiece, &maps.q, 64 * c, q_head,
+                                            q_row + x * p.tile_tokens, &m.qfull, pol);
+                    }
+                    __syncwarp();
+                }
+                q_row = row;
+                q_head = head;
+                if (!more) break;
+            }
+            if (lane == 0) p.seams[blockIdx.x] = seam;
+        } else if (warp == 0) {
             // ---- copies: keys and values of the tiles in turn
             const uint64_t pol = policy_evict_normal();
             const int bt = p.box_tokens, boxes = kKvTile / bt, box = lane % boxes, piece = lane / boxes;
             const bool mine = lane < boxes * C::kPieces;  // the lane's box of a tile
             Place<C::kRing> r;
             bool ok = true;
-            for (; ok && w.left > 0; w.next(p, p.span)) {
+            for (uint32_t u = 0; ok; ++u) {
+                if (!(ok = ctl_wait(&m.ufull[u % kUnitRing], (u / kUnitRing) & 1, ctl))) break;
+                const Unit &d = m.unit[u % kUnitRing];
+                const int end = d.end, first = d.tile, len = d.len, h = d.h;
+                const int32_t *table = p.table + (size_t)d.b * p.max_pages;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.uempty[u % kUnitRing]);
+                if (end == 0) break;
                 int next = -1;  // the page of the lane's box, looked up a tile ahead
                 const auto look_up = [&](int tile) {
                     const int p0 = kKvTile * tile + bt * box;
-                    next = p0 < w.rq.len ? __ldg(p.table + (size_t)w.b * p.max_pages + p.by_page(p0)) : -1;
+                    next = p0 < len ? __ldg(table + p.by_page(p0)) : -1;
                 };
-                look_up(w.tile);
-                for (int j = w.tile; ok && j < w.end; ++j) {
+                look_up(first);
+                for (int j = first; ok && j < end; ++j) {
                     const int p0 = kKvTile * j + bt * box, at = p0 - p.by_page(p0) * p.page_size;
                     const int page = next < 0 || next >= p.num_pages ? p.num_pages : next;  // (past the last one: zeros)
-                    if (j + 1 < w.end) look_up(j + 1);
-    #pragma unroll
+                    if (j + 1 < end) look_up(j + 1);
+#pragma unroll
                     for (int kv = 0; kv < 2; ++kv, r.advance(1)) {
                         if (!(ok = ctl_wait(&m.empty[r.i], r.phase ^ 1, ctl))) break;
                         if (lane == 0) mbar_arrive_expect_tx(&m.full[r.i], C::kSlot);
                         __syncwarp();
                         if (mine)
                             tma_load_4d(ring + r.i * C::kSlot + piece * kPiece + box * bt * 128, kv ? &maps.v : &maps.k, 64 * piece,
-                                        at, w.h, page, &m.full[r.i], pol);
+                                        at, h, page, &m.full[r.i], pol);
                         __syncwarp();
                     }
                 }
             }
-        } else if (warp < 3) {
+        } else {
             // ---- products of X: O_X of the last tile, then S_X of the next one, in one stretch behind everything that
             // they wait for
             const int x = warp - 1;
@@ -177,23 +237,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t vd = sw128_desc_mn(smem_u32(ring), kPiece);
             const uint32_t st = tmem + 128 * x, ot = tmem + 256 + 128 * x;
             const auto scores = [&](uint32_t slot) {
-    #pragma unroll
+#pragma unroll
                 for (int c = 0; c < C::kPieces; ++c)
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 4; ++i)
                         umma_f16(st, qd + c * (kPiece / 16) + 2 * i, kd + slot * (C::kSlot / 16) + c * (kPiece / 16) + 2 * i, id_s,
                                  c | i);
             };
             const auto sums = [&](uint32_t slot, int half, bool first) {
-    #pragma unroll
+#pragma unroll
                 for (int i = 4 * half; i < 4 * half + 4; ++i)
                     umma_f16_ta(ot, st + 8 * i, vd + slot * (C::kSlot / 16) + 128 * i, id_o, !first || i);
             };
             Place<C::kRing> at;             // of the keys of the unit's first tile
             uint32_t tile = 0, step = 0, unit = 0;  // tiles and units of X before this one, turns
             bool ok = true;
-            for (uint32_t u = 0; ok && w.left > 0; w.next(p, p.span), ++u) {
-                const int all = w.end - w.tile, n = tiles_of(x), most = TALL ? all : n;
+            for (uint32_t u = 0; ok; ++u) {
+                if (!(ok = ctl_wait(&m.ufull[u % kUnitRing], (u / kUnitRing) & 1, ctl))) break;
+                const Unit &d = m.unit[u % kUnitRing];
+                const int end = d.end, all = end - d.tile, n = d.n[x], most = TALL ? all : n;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.uempty[u % kUnitRing]);
+                if (end == 0) break;
                 Place<C::kRing> kr = at, vr = at;
                 vr.advance(1);
                 if (!TALL && x) {
@@ -201,14 +266,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     vr.advance(2);
                 }
                 ok = ctl_wait(&m.qfull, u & 1, ctl);
-    #pragma unroll 1
+#pragma unroll 1
                 for (int j = 0; ok && j <= most; ++j, ++step) {
                     const bool has_o = j > 0 && j <= n, has_s = j < n;
                     // the slots of the unit's last tile are room for its results, and given back by the softmax warps
                     const bool last_k = TALL && j == all - 1, last_v = (TALL ? j - 1 : 2 * (j - 1) + x) == all - 1;
                     ok = (j == most || ctl_wait(&m.full[kr.i], kr.phase, ctl)) && (j == 0 || ctl_wait(&m.full[vr.i], vr.phase, ctl)) &&
-                         // tile 1 goes behind tile 0's products of the same step, tile 0 behind tile 1's of the last one,
-                         // or they fall into step, both softmaxes at once and then both products
+                         // tile 1 goes behind tile 0's products of the same step, tile 0 behind tile 1's of the last
+                         // one, or they fall into step, both softmaxes at once and then both products
                          (!TALL || (x ? ctl_wait(&m.turn[1], step & 1, ctl) : step == 0 || ctl_wait(&m.turn[0], (step - 1) & 1, ctl))) &&
                          (!has_o || j > 1 || ctl_wait(&m.oempty[x], (unit & 1) ^ 1, ctl)) &&
                          (!has_o || ctl_wait(&m.pfull[x][0], (tile + j - 1) & 1, ctl));
@@ -247,26 +312,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 unit += n > 0;
                 at.jump(2 * all);
             }
-        } else if (warp == 3) {
-            // ---- copies of the queries; the unit that begins in this share and ends in a later one, for the join launch
-            const uint64_t pol = policy_evict_normal();
-            int4 seam = make_int4(0, 0, 0, 0);
-            bool ok = true;
-            for (uint32_t u = 0; w.left > 0; w.next(p, p.span), ++u) {
-                if (w.tile == 0 && w.end < w.nt)
-                    seam = make_int4(w.rq.row0 + w.g * p.span, min(w.rq.T - w.g * p.span, p.span), w.h,
-                                     (w.flat + w.nt - 1) / share.share);
-                if (!ok || !(ok = ctl_wait(&m.qempty, (u & 1) ^ 1, ctl))) continue;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&m.qfull, C::kQTiles * C::kPieces * 128 * p.group * p.tile_tokens);
-                    for (int x = 0; x < C::kQTiles; ++x)
-                        for (int c = 0; c < C::kPieces; ++c)
-                            tma_load_3d(qs + (x * C::kPieces + c) * kPiece, &maps.q, 64 * c, w.h * p.group,
-                                        w.rq.row0 + w.g * p.span + x * p.tile_tokens, &m.qfull, pol);
-                }
-                __syncwarp();
-            }
-            if (lane == 0) p.seams[blockIdx.x] = seam;
         }
     } else {
         more_registers();
@@ -274,21 +319,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = (warp - 4) >> 2, q = warp & 3, r = 32 * q + lane;
         const uint32_t quarter = (uint32_t)(32 * q) << 16;
         const uint32_t st = tmem + quarter + 128 * x, ot = tmem + quarter + 256;
-        const int t_of = p.by_group(r), j_of = r - t_of * p.group;
+        const int t_of = p.by_group(r);
         uint32_t tile = 0, before = 0, units[2] = {0, 0};  // tiles of X, tiles of the block, units with tiles of each X, so far
+        // (Warps that meet at barriers leave together: where one gave up, all hear of it.)
+        bool ok = ctl_wait(&m.ufull[0], 0, ctl);
+        if (bar_any(1, 256, !ok)) ok = false;
 #pragma unroll 1
-        for (uint32_t u = 0; w.left > 0; w.next(p, p.span), ++u) {
-            const int n = tiles_of(x), t0 = w.g * p.span, t = t0 + (TALL ? x * p.tile_tokens : 0) + t_of;
-            const bool live = t_of < p.tile_tokens && t < w.rq.T;
-            const KvSeen seen = kv_seen(p, w.rq, live ? t : w.rq.T);
-            const bool warp_live = __any_sync(0xffffffffu, live);
-            const int all = kv_all_see(p, w.rq, t0);
+        for (uint32_t u = 0; ok; ++u) {
+            const Unit &d = m.unit[u % kUnitRing];
+            if (d.end == 0) break;
+            const int n = d.n[x], other = d.n[x ^ 1], first = d.tile;
+            const KvReq rq{d.row0, d.T, d.len};
+            const int t = d.t0 + (TALL ? x * p.tile_tokens : 0) + t_of;
+            const bool live = t_of < p.tile_tokens && t < rq.T, warp_live = __any_sync(0xffffffffu, live);
+            const KvSeen seen = kv_seen(p, rq, live ? t : rq.T);
+            const int all = kv_all_see(p, rq, d.t0);
             float mr = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 ctl_wait(&m.sfull[x], (tile + i) & 1, ctl);
                 tc_fence_after();
-                const int li = TALL ? i : 2 * i + x, j = w.tile + li, p0 = kKvTile * j;
+                const int li = TALL ? i : 2 * i + x, j = first + li, p0 = kKvTile * j;
                 const bool masked = p0 + kKvTile > all;
                 if (warp_live) {
                     uint32_t s[128];
@@ -366,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t item = 2 * (before + li) + 1, slot = item % C::kRing;
                     ctl_wait(&m.full[slot], (item / C::kRing) & 1, ctl);
                     uint8_t *row = ring + slot * C::kSlot + r * 128;
-                    bool zero = p0 + r >= w.rq.len;
+                    bool zero = p0 + r >= rq.len;
                     if (!zero) {
                         uint32_t z = 0;
 #pragma unroll
@@ -397,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- the unit's end
-            const int other = tiles_of(x ^ 1), parts = w.end - w.tile;
+            const int parts = d.end - first;
             if (n) ctl_wait(&m.odone[x], units[x] & 1, ctl);
             if (other) ctl_wait(&m.odone[x ^ 1], units[x ^ 1] & 1, ctl);
             tc_fence_after();
@@ -412,98 +463,95 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = a.y * f[0] + b.y * f[1];
             }
             float poison = 0.f;
-            for (int j = max(w.tile, all / kKvTile); j < w.end; ++j)
+            for (int j = max(first, all / kKvTile); j < first + parts; ++j)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     if (m.bad[u & 1][j & 3][c] & seen.word(kKvTile * j + 32 * c)) poison = NAN;
-            const bool whole = w.whole();
+            const bool whole = d.whole;
             const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
             f[0] *= inv;
             f[1] *= inv;
-            const int head = w.h * p.group + j_of, out_row = w.rq.row0 + t;
-            const int own = TALL ? 128 * x + r : r;  // row of the unit
-            const size_t place = ((size_t)(2 * blockIdx.x + (w.tile == 0)) * C::kRows + own);
-            if (live && (TALL || x == 0)) {
-                if (!whole)
-                    p.ml[place] = make_float2(mr, l);
-                else if (p.lse)
-                    p.lse[(int64_t)out_row * p.heads + head] = kv_lse(mr, l);
-            }
             // Results pass through the slots of the unit's last tile (TALL: of its keys for X = 0, of its values for
             // X = 1; else of its values), a warp's rows in a place of their own, so that stores are of whole rows and
             // not of 16 bytes of 32 rows.  Units of 16 bytes are permuted by the row.
             constexpr int kCols = TALL ? D : D / 2, kRow = kCols * 2, kU = kRow / 16;  // a warp's columns (else halves of D), bytes of a row
             const uint32_t item = 2 * (before + parts - 1), k_slot = item % C::kRing, v_slot = (item + 1) % C::kRing;
-            if (TALL) ctl_wait(&m.full[k_slot], (item / C::kRing) & 1, ctl);  // (else it may hold another unit's by now)
-            ctl_wait(&m.full[v_slot], ((item + 1) / C::kRing) & 1, ctl);
-            uint8_t *stage = ring + (TALL && x == 0 ? k_slot : v_slot) * C::kSlot + ((TALL ? 0 : 4 * x) + q) * 32 * kRow;
             const int c0 = TALL ? 0 : x * kCols;
-            const bool has[2] = {TALL ? n > 0 : (x ? other : n) > 0, !TALL && (x ? n : other) > 0};
-            const auto columns = [&](int c, float (&v)[16]) {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = poison;
+            const size_t place = (size_t)(2 * blockIdx.x + (first == 0)) * C::kRows + (TALL ? 128 * x : 0) + 32 * q;
+            if (warp_live) {
+                if (TALL) ctl_wait(&m.full[k_slot], (item / C::kRing) & 1, ctl);  // (else it may hold another unit's by now)
+                ctl_wait(&m.full[v_slot], ((item + 1) / C::kRing) & 1, ctl);
+                uint8_t *stage = ring + (TALL && x == 0 ? k_slot : v_slot) * C::kSlot + ((TALL ? 0 : 4 * x) + q) * 32 * kRow;
+                // unit k of row i of the warp's 32
+                const auto staged = [&](int i, int k) {
+                    return reinterpret_cast<uint4 *>(stage + i * kRow + ((k ^ (i & (kU - 1))) << 4));
+                };
+                const bool has[2] = {TALL ? n > 0 : (x ? other : n) > 0, !TALL && (x ? n : other) > 0};
+                uint32_t o[TALL ? 1 : 2][kCols];
 #pragma unroll
                 for (int y = 0; y < (TALL ? 1 : 2); ++y)
-                    if (has[y]) {
-                        uint32_t o[16];
-                        tmem_ld16(ot + 128 * (TALL ? x : y) + c, o);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(o[k]), f[y], v[k]);
-                    }
-            };
-            // unit k of row i of the warp's 32
-            const auto staged = [&](int i, int k) { return reinterpret_cast<uint4 *>(stage + i * kRow + ((k ^ (i & (kU - 1))) << 4)); };
-            const int first_row = 32 * q;
-            if (warp_live && whole) {
-#pragma unroll 1
-                for (int c = 0; c < kCols; c += 16) {
-                    float v[16];
-                    columns(c0 + c, v);
-                    uint32_t o[8];
+                    for (int c = 0; c < kCols; c += 32)
+                        tmem_ld32(ot + 128 * (TALL ? x : y) + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(&o[y][c]));
+                tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = Elem<DT>::down2(v[2 * k], v[2 * k + 1]);
-                    *staged(lane, c / 8) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *staged(lane, c / 8 + 1) = make_uint4(o[4], o[5], o[6], o[7]);
+                for (int k = 0; k < kCols; ++k) {
+                    float v = poison;
+#pragma unroll
+                    for (int y = 0; y < (TALL ? 1 : 2); ++y)
+                        if (has[y]) v = fmaf(__uint_as_float(o[y][k]), f[y], v);
+                    o[0][k] = __float_as_uint(v);
                 }
-                __syncwarp();
-#pragma unroll 4
-                for (int i = lane; i < 32 * kU; i += 32) {
-                    const int k = i % kU, tt = p.by_group(first_row + i / kU), jj = first_row + i / kU - tt * p.group;
-                    const int row = t0 + (TALL ? x * p.tile_tokens : 0) + tt;
-                    if (tt < p.tile_tokens && row < w.rq.T)
-                        *reinterpret_cast<uint4 *>(p.out + (int64_t)(w.rq.row0 + row) * p.out_stride +
-                                                   (int64_t)(w.h * p.group + jj) * D + c0 + 8 * k) = *staged(i / kU, k);
-                }
-            } else if (warp_live) {
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {  // 32 bits a value
-#pragma unroll 1
-                    for (int c = 0; c < kCols / 2; c += 16) {
-                        float v[16];
-                        columns(c0 + half * (kCols / 2) + c, v);
+                if (whole) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<float4 *>(staged(lane, c / 4 + k)) =
-                                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    for (int k = 0; k < kU; ++k) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = Elem<DT>::down2(__uint_as_float(o[0][8 * k + 2 * i]), __uint_as_float(o[0][8 * k + 2 * i + 1]));
+                        *staged(lane, k) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
+                    fence_proxy_async_smem();
                     __syncwarp();
-                    float *dst = p.part + ((size_t)(2 * blockIdx.x + (w.tile == 0)) * C::kRows + (TALL ? 128 * x : 0) + first_row) * D +
-                                 c0 + half * (kCols / 2);
+                    const int row0 = d.t0 + (TALL ? x * p.tile_tokens : 0), head0 = d.h * p.group;
+                    uint16_t *out = p.out + (int64_t)(rq.row0 + row0) * p.out_stride + (int64_t)head0 * D + c0;
 #pragma unroll 4
-                    for (int i = lane; i < 32 * kU; i += 32)
-                        *reinterpret_cast<uint4 *>(dst + (size_t)(i / kU) * D + 4 * (i % kU)) = *staged(i / kU, i % kU);
-                    __syncwarp();
+                    for (int i = lane; i < 32 * kU; i += 32) {
+                        const int k = i % kU, in = 32 * q + i / kU, tt = p.by_group(in), jj = in - tt * p.group;
+                        if (tt < p.tile_tokens && row0 + tt < rq.T)
+                            *reinterpret_cast<uint4 *>(out + (int64_t)tt * p.out_stride + jj * D + 8 * k) = *staged(i / kU, k);
+                    }
+                    if (live && p.lse && (TALL || x == 0))
+                        p.lse[(int64_t)(rq.row0 + t) * p.heads + head0 + r - t_of * p.group] = kv_lse(mr, l);
+                } else {
+                    float *dst = p.part + place * D + c0;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {  // 32 bits a value
+#pragma unroll
+                        for (int k = 0; k < kU; ++k)
+                            *staged(lane, k) = make_uint4(o[0][half * (kCols / 2) + 4 * k], o[0][half * (kCols / 2) + 4 * k + 1],
+                                                          o[0][half * (kCols / 2) + 4 * k + 2], o[0][half * (kCols / 2) + 4 * k + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+#pragma unroll 4
+                        for (int i = lane; i < 32 * kU; i += 32)
+                            *reinterpret_cast<uint4 *>(dst + (size_t)(i / kU) * D + half * (kCols / 2) + 4 * (i % kU)) =
+                                *staged(i / kU, i % kU);
+                        __syncwarp();
+                    }
+                    if (live && (TALL || x == 0)) p.ml[place + lane] = make_float2(mr, l);
                 }
             }
-            fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 if (n) mbar_arrive(&m.oempty[x]);
                 if (!TALL && other) mbar_arrive(&m.oempty[x ^ 1]);
+                mbar_arrive(&m.uempty[u % kUnitRing]);
             }
             if (warp == 4 && lane < 16) (&m.bad[(u & 1) ^ 1][0][0])[lane] = 0;
-            bar_sync(1, 256);  // everyone has read what the next unit writes
+            ok = ctl_wait(&m.ufull[(u + 1) % kUnitRing], ((u + 1) / kUnitRing) & 1, ctl);
+            if (bar_any(1, 256, !ok)) ok = false;  // and everyone has read what the next unit writes
             if (q == 0 && lane == 0 && (TALL || x == 0)) {
                 if (TALL) mbar_arrive(&m.empty[k_slot]);
                 mbar_arrive(&m.empty[v_slot]);
