@@ -23,7 +23,7 @@ namespace {
 constexpr int kThreads = 384;  // copies of K and V, two issuers of products, copies of Q; 2 x 4 softmax warps
 constexpr int kPiece = kKvTile * 128;  // 128 rows of 64 values, 16 KB
 
-constexpr int kUnitCost = 2;  // tiles
+constexpr int kUnitCost = 3;  // tiles
 
 struct KvMaps {
     CUtensorMap k, v;  // [page][head][token][D], boxes of 64 values x box_tokens
@@ -64,7 +64,7 @@ struct Misc {
     uint32_t tmem;
     int abort;
     Unit unit[kUnitRing];
-    uint32_t bad[2][4][4];               // tokens with values that are not finite, in the last four tiles of a unit
+    alignas(16) uint32_t bad[2][4][4];   // tokens with values that are not finite, in the last four tiles of a unit
     float2 ml[2][kKvTileRows];           // X's references and weights
 };
 static_assert(sizeof(Misc) <= 3072, "the misc area holds it");
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t quarter = (uint32_t)(32 * q) << 16;
         const uint32_t st = tmem + quarter + 128 * x, ot = tmem + quarter + 256;
         const int t_of = p.by_group(r);
-        uint32_t tile = 0, before = 0, units[2] = {0, 0};  // tiles of X, tiles of the block, units with tiles of each X, so far
+        uint32_t tile = 0, before = 0, units = 0, units_o = 0;  // tiles of X, tiles of the block, units with tiles of X and of the other, so far
         // (Warps that meet at barriers leave together: where one gave up, all hear of it.)
         bool ok = ctl_wait(&m.ufull[0], 0, ctl);
         if (bar_any(1, 256, !ok)) ok = false;
@@ -449,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- the unit's end
             const int parts = d.end - first;
-            if (n) ctl_wait(&m.odone[x], units[x] & 1, ctl);
-            if (other) ctl_wait(&m.odone[x ^ 1], units[x ^ 1] & 1, ctl);
+            if (n) ctl_wait(&m.odone[x], units & 1, ctl);
+            if (other) ctl_wait(&m.odone[x ^ 1], units_o & 1, ctl);
             tc_fence_after();
             if (!TALL) m.ml[x][r] = make_float2(mr, l);
             bar_sync(1, 256);  // references, weights and lists of bad tokens are there
@@ -462,15 +462,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f[1] = kv_factor(b.x, mr);
                 l = a.y * f[0] + b.y * f[1];
             }
-            float poison = 0.f;
-            for (int j = max(first, all / kKvTile); j < first + parts; ++j)
+            // Whether the row sees a token with a value that is not finite: hardly ever is there one at all.
+            bool poison = false;
+            {
+                const uint4 *lists = reinterpret_cast<const uint4 *>(&m.bad[u & 1][0][0]);
+                uint4 any = lists[0];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (m.bad[u & 1][j & 3][c] & seen.word(kKvTile * j + 32 * c)) poison = NAN;
+                for (int i = 1; i < 4; ++i) any = make_uint4(any.x | lists[i].x, any.y | lists[i].y, any.z | lists[i].z, any.w | lists[i].w);
+                if (any.x | any.y | any.z | any.w)
+                    for (int j = max(first, all / kKvTile); j < first + parts; ++j)
+                        for (int c = 0; c < 4; ++c)
+                            if (m.bad[u & 1][j & 3][c] & seen.word(kKvTile * j + 32 * c)) poison = true;
+            }
             const bool whole = d.whole;
             const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            f[0] *= inv;
-            f[1] *= inv;
+            f[0] = poison ? NAN : f[0] * inv;
+            f[1] = poison ? NAN : f[1] * inv;
             // Results pass through the slots of the unit's last tile (TALL: of its keys for X = 0, of its values for
             // X = 1; else of its values), a warp's rows in a place of their own, so that stores are of whole rows and
             // not of 16 bytes of 32 rows.  Units of 16 bytes are permuted by the row.
@@ -487,56 +494,94 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return reinterpret_cast<uint4 *>(stage + i * kRow + ((k ^ (i & (kU - 1))) << 4));
                 };
                 const bool has[2] = {TALL ? n > 0 : (x ? other : n) > 0, !TALL && (x ? n : other) > 0};
-                uint32_t o[TALL ? 1 : 2][kCols];
+                // A half of the warp's columns at a time, scaled.
+                constexpr int kHalf = kCols / 2, kLd = kHalf < 32 ? 16 : 32;
+                const auto half_of = [&](int half, uint32_t (&o)[kHalf]) {
+                    const uint32_t at = ot + c0 + half * kHalf;
 #pragma unroll
-                for (int y = 0; y < (TALL ? 1 : 2); ++y)
+                    for (int y = 0; y < (TALL ? 1 : 2); ++y) {
+                        if (!has[y]) {
+                            if (y == 0)
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 32)
-                        tmem_ld32(ot + 128 * (TALL ? x : y) + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(&o[y][c]));
-                tmem_wait_ld();
+                                for (int k = 0; k < kHalf; ++k) o[k] = 0;
+                            continue;
+                        }
+                        uint32_t v[kHalf];
 #pragma unroll
-                for (int k = 0; k < kCols; ++k) {
-                    float v = poison;
+                        for (int c = 0; c < kHalf; c += kLd) {
+                            if (kLd == 32)
+                                tmem_ld32(at + 128 * (TALL ? x : y) + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+                            else
+                                tmem_ld16(at + 128 * (TALL ? x : y) + c, *reinterpret_cast<uint32_t(*)[16]>(&v[c]));
+                        }
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int y = 0; y < (TALL ? 1 : 2); ++y)
-                        if (has[y]) v = fmaf(__uint_as_float(o[y][k]), f[y], v);
-                    o[0][k] = __float_as_uint(v);
-                }
+                        for (int k = 0; k < kHalf; ++k)
+                            o[k] = __float_as_uint(y == 0 ? __uint_as_float(v[k]) * f[0]
+                                                          : fmaf(__uint_as_float(v[k]), f[1], __uint_as_float(o[k])));
+                    }
+                };
                 if (whole) {
 #pragma unroll
-                    for (int k = 0; k < kU; ++k) {
-                        uint32_t v[4];
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t o[kHalf];
+                        half_of(half, o);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = Elem<DT>::down2(__uint_as_float(o[0][8 * k + 2 * i]), __uint_as_float(o[0][8 * k + 2 * i + 1]));
-                        *staged(lane, k) = make_uint4(v[0], v[1], v[2], v[3]);
+                        for (int k = 0; k < kU / 2; ++k) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                v[i] = Elem<DT>::down2(__uint_as_float(o[8 * k + 2 * i]), __uint_as_float(o[8 * k + 2 * i + 1]));
+                            *staged(lane, half * (kU / 2) + k) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                     const int row0 = d.t0 + (TALL ? x * p.tile_tokens : 0), head0 = d.h * p.group;
-                    uint16_t *out = p.out + (int64_t)(rq.row0 + row0) * p.out_stride + (int64_t)head0 * D + c0;
-#pragma unroll 4
-                    for (int i = lane; i < 32 * kU; i += 32) {
-                        const int k = i % kU, in = 32 * q + i / kU, tt = p.by_group(in), jj = in - tt * p.group;
-                        if (tt < p.tile_tokens && row0 + tt < rq.T)
-                            *reinterpret_cast<uint4 *>(out + (int64_t)tt * p.out_stride + jj * D + 8 * k) = *staged(i / kU, k);
+                    // 16-byte unit k of the rows lane / kU + kStep i of the warp's 32, (row, head) by (row, head)
+                    constexpr int kStep = 32 / kU;
+                    const int k = lane % kU, step_t = kStep / p.group, step_j = kStep - step_t * p.group;
+                    int i = lane / kU, tt = p.by_group(32 * q + i), jj = 32 * q + i - tt * p.group;
+                    const int most = min(p.tile_tokens, rq.T - row0);
+                    uint16_t *out = p.out + (int64_t)(rq.row0 + row0 + tt) * p.out_stride + (int64_t)(head0 + jj) * D + c0 + 8 * k;
+                    const int64_t step = (int64_t)step_t * p.out_stride + step_j * D, wrap = p.out_stride - (int64_t)p.group * D;
+#pragma unroll
+                    for (int n8 = 0; n8 < kU; n8 += 8) {
+                        uint4 v[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            if (n8 + y < kU) v[y] = *staged(i + kStep * (n8 + y), k);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            if (n8 + y >= kU) continue;
+                            if (tt < most) *reinterpret_cast<uint4 *>(out) = v[y];
+                            tt += step_t;
+                            jj += step_j;
+                            out += step;
+                            if (jj >= p.group) {
+                                jj -= p.group;
+                                ++tt;
+                                out += wrap;
+                            }
+                        }
                     }
                     if (live && p.lse && (TALL || x == 0))
                         p.lse[(int64_t)(rq.row0 + t) * p.heads + head0 + r - t_of * p.group] = kv_lse(mr, l);
                 } else {
                     float *dst = p.part + place * D + c0;
-#pragma unroll
+#pragma unroll 1
                     for (int half = 0; half < 2; ++half) {  // 32 bits a value
+                        uint32_t o[kHalf];
+                        half_of(half, o);
 #pragma unroll
-                        for (int k = 0; k < kU; ++k)
-                            *staged(lane, k) = make_uint4(o[0][half * (kCols / 2) + 4 * k], o[0][half * (kCols / 2) + 4 * k + 1],
-                                                          o[0][half * (kCols / 2) + 4 * k + 2], o[0][half * (kCols / 2) + 4 * k + 3]);
+                        for (int k = 0; k < kU; ++k) *staged(lane, k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                         fence_proxy_async_smem();
                         __syncwarp();
-#pragma unroll 4
-                        for (int i = lane; i < 32 * kU; i += 32)
-                            *reinterpret_cast<uint4 *>(dst + (size_t)(i / kU) * D + half * (kCols / 2) + 4 * (i % kU)) =
-                                *staged(i / kU, i % kU);
+#pragma unroll 8
+                        for (int i = 0; i < kU; ++i) {
+                            const int row = i * (32 / kU) + lane / kU, k = lane % kU;
+                            *reinterpret_cast<uint4 *>(dst + row * D + half * kHalf + 4 * k) = *staged(row, k);
+                        }
                         __syncwarp();
                     }
                     if (live && (TALL || x == 0)) p.ml[place + lane] = make_float2(mr, l);
@@ -558,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tile += n;
             before += parts;
-            units[x] += n > 0;
-            units[x ^ 1] += other > 0;
+            units += n > 0;
+            units_o += other > 0;
         }
     }
     tc_fence_before();
