@@ -22,7 +22,7 @@ struct KvParams {
     const int32_t *lens;
     // call
     int N, heads, group, max_q, max_len, causal;  // group: query heads to a key head; max_len: within the block table too
-    FastDiv by_group, by_page;
+    FastDiv by_group, by_page, by_blocks;  // blocks of the attention launch
     int64_t q_stride, out_stride;
     const int32_t *q_start;
     const uint64_t *tree;
@@ -152,32 +152,37 @@ __device__ __forceinline__ int warp_upto(int n, int lane) {
 
 // One warp: every lane gets the block's share.  Requests a lane each (the last
 // 32 stay in registers, which is all of a small batch); a single request's
-// units a lane each, as a long prompt has many.
+// units a lane each, as a long prompt has many.  This is what a short call
+// waits for, so divisors that the host knows are multiplied by.
 __device__ __forceinline__ KvShare kv_find_share(const KvParams &p, int span, int lane) {
     KvShare w{};
-    int total = 0, n = 0;
+    int total = 0, n = 0;  // tiles of a key head
     KvReq r{};
     if (p.B == 1) {
         r = kv_req(p, 0);
-        const int groups = kv_groups(r.T, span);
-        for (int g = lane; g < groups; g += 32) n += kv_unit_tiles(p, r, g, span, groups);
-        n = __reduce_add_sync(0xffffffffu, n) * p.kv_heads;
+        if (r.T <= span) {
+            n = r.T > 0 ? kv_tiles(p, r, 0, span) + p.unit_cost : 0;
+        } else {
+            const int groups = kv_groups(r.T, span);
+            for (int g = lane; g < groups; g += 32) n += kv_unit_tiles(p, r, g, span, groups);
+            n = __reduce_add_sync(0xffffffffu, n);
+        }
         total = n;
     } else {
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             n = 0;
             if (b0 + lane < p.B) {
                 r = kv_req(p, b0 + lane);
-                n = kv_head_tiles(p, r, span) * p.kv_heads;
+                n = kv_head_tiles(p, r, span);
             }
             total += __reduce_add_sync(0xffffffffu, n);
         }
     }
-    w.share = max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1);
+    total *= p.kv_heads;
+    w.share = max(p.by_blocks(total + p.by_blocks.d - 1), 1);
     w.flat = (int)min((int64_t)w.share * blockIdx.x, (int64_t)total);
     w.left = min(w.share, total - w.flat);
     if (w.left <= 0) return w;
-    int per = n;  // of the request in which the share begins
     w.off = w.flat;
     if (p.B > 1) {
         int before = 0;
@@ -190,11 +195,11 @@ __device__ __forceinline__ KvShare kv_find_share(const KvParams &p, int span, in
                 n = 0;
                 if (b0 + lane < p.B) {
                     r = kv_req(p, b0 + lane);
-                    n = kv_head_tiles(p, r, span) * p.kv_heads;
+                    n = kv_head_tiles(p, r, span);
                 }
             }
-            const int upto = warp_upto(n, lane), off = w.flat - (before + upto - n);
-            const uint32_t mine = __ballot_sync(0xffffffffu, off >= 0 && off < n);
+            const int own = n * p.kv_heads, upto = warp_upto(own, lane), off = w.flat - (before + upto - own);
+            const uint32_t mine = __ballot_sync(0xffffffffu, off >= 0 && off < own);
             if (mine) {
                 const int l = __ffs(mine) - 1;
                 w.b = b0 + l;
@@ -202,27 +207,28 @@ __device__ __forceinline__ KvShare kv_find_share(const KvParams &p, int span, in
                 r.row0 = __shfl_sync(0xffffffffu, r.row0, l);
                 r.T = __shfl_sync(0xffffffffu, r.T, l);
                 r.len = __shfl_sync(0xffffffffu, r.len, l);
-                per = __shfl_sync(0xffffffffu, n, l);
+                n = __shfl_sync(0xffffffffu, n, l);
                 break;
             }
             before += __shfl_sync(0xffffffffu, upto, 31);
         }
     }
     w.rq = r;
-    per /= p.kv_heads;
-    w.h = w.off / per;
-    w.off -= w.h * per;
-    const int groups = kv_groups(r.T, span);
-    for (int g0 = 0; g0 < groups; g0 += 32) {
-        const int t = kv_unit_tiles(p, r, g0 + lane, span, groups), upto = warp_upto(t, lane);
-        const uint32_t mine = __ballot_sync(0xffffffffu, w.off >= upto - t && w.off < upto);
-        if (mine) {
-            const int l = __ffs(mine) - 1;
-            w.g = g0 + l;
-            w.off -= __shfl_sync(0xffffffffu, upto - t, l);
-            break;
+    w.h = (int)((uint32_t)w.off / (uint32_t)n);
+    w.off -= w.h * n;
+    if (r.T > span) {
+        const int groups = kv_groups(r.T, span);
+        for (int g0 = 0; g0 < groups; g0 += 32) {
+            const int t = kv_unit_tiles(p, r, g0 + lane, span, groups), upto = warp_upto(t, lane);
+            const uint32_t mine = __ballot_sync(0xffffffffu, w.off >= upto - t && w.off < upto);
+            if (mine) {
+                const int l = __ffs(mine) - 1;
+                w.g = g0 + l;
+                w.off -= __shfl_sync(0xffffffffu, upto - t, l);
+                break;
+            }
+            w.off -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        w.off -= __shfl_sync(0xffffffffu, upto, 31);
     }
     w.off -= p.unit_cost;
     if (w.off < 0) {  // the share begins with what a unit costs
@@ -296,21 +302,28 @@ __device__ __forceinline__ float kv_lse(float m, float l) {
 __device__ __forceinline__ float kv_factor(float m, float common) {
     return m == -INFINITY ? (common == -INFINITY ? 1.f : 0.f) : kv_ex2(m - common);
 }
-// One warp: a row's result from the partial sums of the blocks c0 .. c1, added
-// in their order.  r: row of a place, of which there are `rows`.  Sums are read
-// eight parts at a time, the first ones with the references and weights (a part
-// a lane, 32 at a time) and not behind them: what a row costs is the time of
-// one read after the other.
-template <int DT, int D>
-__device__ __forceinline__ void kv_join_row(const KvParams &p, int c0, int c1, int rows, int r, int row, int head, int lane) {
+// One warp: a row's sum over the parts `first`, first + step and so on of the
+// blocks c0 .. c1, in their order, under the reference of them all.  r: row of a
+// place, of which there are `rows`.  Sums are read eight parts at a time, the
+// first ones with the references and weights (a part a lane, 32 at a time) and
+// not behind them: what a row costs is the time of one read after the other.
+template <int D>
+struct KvSum {
+    static constexpr int kPer = D / 32;
+    float m, l, v[kPer];  // v: the lane's values
+};
+template <int D>
+__device__ __forceinline__ KvSum<D> kv_sum_parts(const KvParams &p, int c0, int c1, int first, int step, int rows, int r, int lane) {
     constexpr int kPer = D / 32, kAhead = 8;
+    KvSum<D> s;
     const auto place = [&](int k) { return (size_t)(2 * k + (k == c0)) * rows + r; };
+    const int n = (c1 - c0 - first) / step + 1;  // (first <= c1 - c0)
     uint32_t x[kAhead][kPer];
-    const auto fetch = [&](int k0) {
+    const auto fetch = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (k0 + i > c1) continue;
-            const float *src = p.part + place(k0 + i) * D + kPer * lane;
+            if (i0 + i >= n) continue;
+            const float *src = p.part + place(c0 + first + step * (i0 + i)) * D + kPer * lane;
             if (kPer == 4) {
                 const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(src));
                 x[i][0] = v.x;
@@ -324,36 +337,48 @@ __device__ __forceinline__ void kv_join_row(const KvParams &p, int c0, int c1, i
             }
         }
     };
-    fetch(c0);
-    float2 a = c0 + lane <= c1 ? __ldcg(&p.ml[place(c0 + lane)]) : make_float2(-INFINITY, 0.f);
-    float mm = a.x, ll = 0.f, v[kPer] = {};
-    for (int k = c0 + 32 + lane; k <= c1; k += 32) mm = fmaxf(mm, __ldcg(&p.ml[place(k)]).x);
+    fetch(0);
+    s.m = -INFINITY;
+    s.l = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    for (int k0 = c0; k0 <= c1; k0 += kAhead) {
-        const int at = (k0 - c0) & 31;
-        if (k0 > c0) {
-            fetch(k0);
-            if (at == 0) a = k0 + lane <= c1 ? __ldcg(&p.ml[place(k0 + lane)]) : make_float2(-INFINITY, 0.f);
+    for (int j = 0; j < kPer; ++j) s.v[j] = 0.f;
+    for (int k = c0 + lane; k <= c1; k += 32) s.m = fmaxf(s.m, __ldcg(&p.ml[place(k)]).x);
+    const auto weights = [&](int i) {
+        return i < n ? __ldcg(&p.ml[place(c0 + first + step * i)]) : make_float2(-INFINITY, 0.f);
+    };
+    float2 a = weights(lane);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s.m = fmaxf(s.m, __shfl_xor_sync(0xffffffffu, s.m, o));
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+        const int at = i0 & 31;
+        if (i0 > 0) {
+            fetch(i0);
+            if (at == 0) a = weights(i0 + lane);
         }
-        const float f = kv_factor(a.x, mm), w = a.y * f;
+        const float f = kv_factor(a.x, s.m), w = a.y * f;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const float g = __shfl_sync(0xffffffffu, f, at + i), h = __shfl_sync(0xffffffffu, w, at + i);
-            if (k0 + i > c1) continue;
-            ll += h;
+            if (i0 + i >= n) continue;
+            s.l += h;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) v[j] = fmaf(__uint_as_float(x[i][j]), g, v[j]);
+            for (int j = 0; j < kPer; ++j) s.v[j] = fmaf(__uint_as_float(x[i][j]), g, s.v[j]);
         }
     }
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    return s;
+}
+// One warp: a row's sum to the output.
+template <int DT, int D>
+__device__ __forceinline__ void kv_write_row(const KvParams &p, const KvSum<D> &s, int row, int head, int lane) {
+    constexpr int kPer = D / 32;
+    const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
     uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + kPer * lane);
-    const uint32_t lo = Elem<DT>::down2(v[0] * inv, v[1] * inv);
+    const uint32_t lo = Elem<DT>::down2(s.v[0] * inv, s.v[1] * inv);
     if (kPer == 4)
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, Elem<DT>::down2(v[kPer - 2] * inv, v[kPer - 1] * inv));
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, Elem<DT>::down2(s.v[kPer - 2] * inv, s.v[kPer - 1] * inv));
     else
         *dst = lo;
-    if (p.lse && lane == 0) p.lse[(int64_t)row * p.heads + head] = kv_lse(mm, ll);
+    if (p.lse && lane == 0) p.lse[(int64_t)row * p.heads + head] = kv_lse(s.m, s.l);
 }
 
 // -------------------------------------------------------------------- host --

@@ -3,11 +3,13 @@
 //
 //   out = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale q . k_p - m),
 //
-// m a running reference of the row.  A unit of at most 32 (token, head) rows
-// that share a key head (one token of a grouped model, a short chain or tree) is
-// bound by reading its keys and values once: 4 D bytes a token and key head
-// against 4 D products a row, 16 of which the mma.sync tensor-core path does in
-// a quarter of the time that the bytes take.
+// m a running reference of the row.  A unit of at most 16 (token, head) rows
+// that share a key head (one token of a grouped model, a short chain) is bound
+// by reading its keys and values once: 4 D bytes a token and key head against
+// 4 D products a row, 16 of which the mma.sync tensor-core path does in a
+// quarter of the time that the bytes take.  With two such tiles, 17 to 32 rows,
+// it is no longer so (8 tokens of 4 heads, 16 requests of 4096 tokens: 75.9 us,
+// and 55.9 in the launch for more rows; one request of 1000 tokens 11.9, 11.8).
 #include <math.h>
 
 #include "spx_kv.cuh"
@@ -49,39 +51,115 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Block: a share of tiles, 8 warps.  Each warp takes 16 tokens of every tile of
+// Block: a share of tiles, 8 warps.  Or (CLUSTER) the blocks of a cluster have
+// the tiles of one unit, in equal parts: nothing is searched for, and the parts
+// are joined from the blocks' shared memories instead of by way of the
+// workspace and a counter, which is 3 us for a short call (517 tokens of 16
+// heads XXX).  Each warp takes 16 tokens of every tile of
 // 128 on its own, from copies of its own that run kStages - 1 tiles ahead, into
 // the units behind as well, so that a block's warps meet only at the end of a
 // unit, where their sums are joined; 16 tokens lie in one page.  A block of 16
 // tokens of keys (rows of D values, the 16-byte units of a row permuted by the
 // row's last three bits) is the B operand of S = Q K^T, of values transposed
 // that of O = P V; P passes from one product to the other in registers.
+constexpr int kFewRows = 16;  // (token, head) rows of a unit at most
 constexpr int kWarps = 8;
-template <int D, int RT>
+constexpr int kMostRanks = 8;  // blocks of a cluster
+template <int D>
 struct FewRows {
-    static constexpr int kRows = 16 * RT;
+    static constexpr int kRows = kFewRows;
     static constexpr int kBlk = 16 * D * 2;  // keys or values of 16 tokens
-    static constexpr int kStages = (RT == 1 ? 3 : 2) * (128 / D);
+    static constexpr int kStages = 3 * (128 / D);
     static constexpr int kRing = kWarps * kStages * 2 * kBlk;
     static constexpr int kSums = 4 * kRows * D * 4;  // sums of four warps
-    static constexpr int kBytes = kRing + kSums + kWarps * kRows * 8 + 64;
+    static constexpr int kBytes = kRing + kSums + (kWarps + 1) * kRows * 8 + 64;
     static_assert(kBytes <= kSmemLimit, "shared memory of one block");
 };
 
-template <int DT, int D, int RT>
+// The block that brings the last part of a unit joins them all.  A row's parts
+// are dealt out to as many warps as there are for it; their sums are added in
+// the order of the warps.  (A call of its own, for the registers of the loop.)
+template <int DT, int D, int kRows>
+__device__ __noinline__ void kv_join_unit(const KvParams &p, float *room, int c0, int c1, int rows, int row0, int head0) {
+    constexpr int kPer = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // warps a row: one for every eight parts, which it reads together
+    const int per = rows >= kWarps ? 1 : min(kWarps / rows, (c1 - c0) / 8 + 1);
+    for (int i = warp; i < rows * per; i += kWarps) {  // (more than one round: per is 1)
+        const int r = i / per, w = i - r * per, t = p.by_group(r), head = head0 + r - t * p.group;
+        const KvSum<D> s = kv_sum_parts<D>(p, c0, c1, w, per, kRows, r, lane);
+        if (per == 1) {
+            kv_write_row<DT, D>(p, s, row0 + t, head, lane);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) room[(i * kPer + j) * 32 + lane] = s.v[j];
+            if (lane == 0) room[kWarps * D + 2 * i] = s.m, room[kWarps * D + 2 * i + 1] = s.l;
+        }
+    }
+    if (per == 1) return;
+    __syncthreads();
+    if (warp < rows) {
+        const int r = warp, t = p.by_group(r);
+        KvSum<D> s;
+        s.m = room[kWarps * D + 2 * r * per];
+        s.l = 0.f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) s.v[j] = 0.f;
+        for (int w = 0; w < per; ++w) {
+            s.l += room[kWarps * D + 2 * (r * per + w) + 1];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) s.v[j] += room[((r * per + w) * kPer + j) * 32 + lane];
+        }
+        kv_write_row<DT, D>(p, s, row0 + t, head0 + r - t * p.group, lane);
+    }
+}
+
+__device__ __forceinline__ float2 ld_cluster2(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t at, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(at), "r"(rank));
+    return a;
+}
+
+template <int DT, int D, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __grid_constant__ KvParams p) {
-    using C = FewRows<D, RT>;
+    using C = FewRows<D>;
     constexpr int kUnits = D / 8;  // 16-byte units of a row
     extern __shared__ __align__(1024) uint8_t smem[];
     float *sums = reinterpret_cast<float *>(smem + C::kRing);
     float2 *mls = reinterpret_cast<float2 *>(smem + C::kRing + C::kSums);  // [warp][row]
-    int *last_part = reinterpret_cast<int *>(mls + kWarps * C::kRows);
+    float2 *own_ml = mls + kWarps * C::kRows;  // CLUSTER: [row] of the block
+    int *last_part = reinterpret_cast<int *>(own_ml + C::kRows);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, pair = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * (C::kStages * 2 * C::kBlk);
     griddep_wait();
     griddep_launch_dependents();
-    const KvShare share = kv_find_share(p, p.span, lane);
-    if (share.left <= 0) return;
+    KvShare share{};
+    if (CLUSTER) {
+        const int unit = (int)blockIdx.x / p.by_blocks.d, rank = (int)blockIdx.x - unit * p.by_blocks.d;
+        share.b = unit / p.kv_heads;
+        share.h = unit - share.b * p.kv_heads;
+        share.rq = kv_req(p, share.b);
+        // (a part without tiles, or of a request without rows, takes part in the join all the same)
+        const int nt = share.rq.T > 0 ? kv_tiles(p, share.rq, 0, p.span) : 0, per = p.by_blocks(nt + p.by_blocks.d - 1);
+        share.off = min(rank * per, nt);
+        share.left = min(per, nt - share.off);
+    } else {
+        share = kv_find_share(p, p.span, lane);
+        if (share.left <= 0) return;
+    }
 
     // ---- copies
     KvWalk ahead;
@@ -126,37 +204,38 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
     // ---- products
     KvWalk w;
     w.begin(p, share, p.span);
+    if (CLUSTER) {
+        if (share.rq.T == 0) return;  // (the cluster's blocks alike)
+        w.tile = share.off;
+        w.end = share.off + share.left;
+    }
     int stage = 0;
 #pragma unroll 1
-    for (; w.left > 0; w.next(p, p.span)) {
+    for (; CLUSTER || w.left > 0; w.next(p, p.span)) {
         const int rows = w.rq.T * p.group;
         // the queries, A operand: row quad (+ 8), values 16 ks + 2 pair (+ 8)
-        uint32_t qa[RT][D / 16][4];
-        KvSeen seen[RT][2];
-        float m[RT][2], l[RT][2], o[RT][D / 8][4];
+        uint32_t qa[D / 16][4];
+        KvSeen seen[2];
+        float m[2], l[2], o[D / 8][4];
 #pragma unroll
-        for (int x = 0; x < RT; ++x)
+        for (int y = 0; y < 2; ++y) {
+            const int r = 8 * y + quad, t = p.by_group(r), j = r - t * p.group;
+            const bool live = r < rows;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                p.q + (int64_t)(w.rq.row0 + (live ? t : 0)) * p.q_stride + (int64_t)(w.h * p.group + (live ? j : 0)) * D);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int r = 16 * x + 8 * y + quad, t = p.by_group(r), j = r - t * p.group;
-                const bool live = r < rows;
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(
-                    p.q + (int64_t)(w.rq.row0 + (live ? t : 0)) * p.q_stride + (int64_t)(w.h * p.group + (live ? j : 0)) * D);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    qa[x][k][y] = live ? __ldg(src + 8 * k + pair) : 0u;
-                    qa[x][k][y + 2] = live ? __ldg(src + 8 * k + 4 + pair) : 0u;
-                }
-                seen[x][y] = kv_seen(p, w.rq, t);
-                m[x][y] = -INFINITY;
-                l[x][y] = 0.f;
+            for (int k = 0; k < D / 16; ++k) {
+                qa[k][y] = live ? __ldg(src + 8 * k + pair) : 0u;
+                qa[k][y + 2] = live ? __ldg(src + 8 * k + 4 + pair) : 0u;
             }
+            seen[y] = kv_seen(p, w.rq, t);
+            m[y] = -INFINITY;
+            l[y] = 0.f;
+        }
 #pragma unroll
-        for (int x = 0; x < RT; ++x)
+        for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[x][n][i] = 0.f;
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
         const int all = kv_all_see(p, w.rq, 0);
 #pragma unroll 1
         for (int tile = w.tile; tile < w.end; ++tile) {
@@ -167,24 +246,19 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
             if (++stage == C::kStages) stage = 0;
             const int p0 = kKvTile * tile + 16 * warp;
             if (p0 >= w.rq.len) continue;
-            float s[RT][2][4];
+            float s[2][4];
 #pragma unroll
-            for (int x = 0; x < RT; ++x)
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[x][n][i] = 0.f;
+                for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 // tokens 0-7 and 8-15, units 2k and 2k + 1
                 const int t = (lane & 7) + ((lane & 16) >> 1), u = 2 * k + ((lane >> 3) & 1);
                 uint32_t b[4];
                 ldsm4(b, ks + t * (2 * D) + ((u ^ (t & 7)) << 4));
-#pragma unroll
-                for (int x = 0; x < RT; ++x) {
-                    mma<DT>(s[x][0], qa[x][k], b[0], b[1]);
-                    mma<DT>(s[x][1], qa[x][k], b[2], b[3]);
-                }
+                mma<DT>(s[0], qa[k], b[0], b[1]);
+                mma<DT>(s[1], qa[k], b[2], b[3]);
             }
             if (p0 + 16 > all) {
                 // what is not seen by every row: masks, and values that are not finite, whose weight 0 does not make
@@ -215,59 +289,52 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                     __syncwarp();
                 }
 #pragma unroll
-                for (int x = 0; x < RT; ++x)
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t word = seen[y].word(p0) & (p0 + 16 > w.rq.len ? (1u << (w.rq.len - p0)) - 1 : 0xFFFFu);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint32_t word = seen[x][y].word(p0) & (p0 + 16 > w.rq.len ? (1u << (w.rq.len - p0)) - 1 : 0xFFFFu);
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                        for (int i = 0; i < 2; ++i)
+                            if (!(word >> (8 * n + 2 * pair + i) & 1)) s[n][2 * y + i] = -INFINITY;
+                    if (word & bad)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                if (!(word >> (8 * n + 2 * pair + i) & 1)) s[x][n][2 * y + i] = -INFINITY;
-                        if (word & bad)
-#pragma unroll
-                            for (int n = 0; n < D / 8; ++n) o[x][n][2 * y] = o[x][n][2 * y + 1] = NAN;
-                    }
+                        for (int n = 0; n < D / 8; ++n) o[n][2 * y] = o[n][2 * y + 1] = NAN;
+                }
             }
+            float top[2], fac[2];
+            bool rise = false;
 #pragma unroll
-            for (int x = 0; x < RT; ++x) {
-                float top[2], fac[2];
-                bool rise = false;
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    float t = fmaxf(fmaxf(s[x][0][2 * y], s[x][0][2 * y + 1]), fmaxf(s[x][1][2 * y], s[x][1][2 * y + 1]));
-                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                    top[y] = t * p.scale_log2;  // (scale > 0)
-                    rise |= top[y] > m[x][y] + kKvSlack;
-                }
-                if (__any_sync(0xffffffffu, rise)) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float mn = top[y] > m[x][y] + kKvSlack ? top[y] : m[x][y];
-                        fac[y] = mn == m[x][y] ? 1.f : kv_ex2(m[x][y] - mn);
-                        m[x][y] = mn;
-                        l[x][y] *= fac[y];
-                    }
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[x][n][i] *= fac[i >> 1];
-                }
-                uint32_t pa[4];
+            for (int y = 0; y < 2; ++y) {
+                float t = fmaxf(fmaxf(s[0][2 * y], s[0][2 * y + 1]), fmaxf(s[1][2 * y], s[1][2 * y + 1]));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                top[y] = t * p.scale_log2;  // (scale > 0)
+                rise |= top[y] > m[y] + kKvSlack;
+            }
+            if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const float ref = m[x][y] == -INFINITY ? 0.f : kKvShift - m[x][y];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const float a = kv_ex2(fmaf(s[x][n][2 * y], p.scale_log2, ref));
-                        const float b = kv_ex2(fmaf(s[x][n][2 * y + 1], p.scale_log2, ref));
-                        l[x][y] += a + b;
-                        pa[2 * n + y] = Elem<DT>::down2(a, b);  // rounded for the tensor cores; the weight's own sum is not
-                    }
+                    const float mn = top[y] > m[y] + kKvSlack ? top[y] : m[y];
+                    fac[y] = mn == m[y] ? 1.f : kv_ex2(m[y] - mn);
+                    m[y] = mn;
+                    l[y] *= fac[y];
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t *>(&s[x][0][i]) = pa[i];
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[n][i] *= fac[i >> 1];
+            }
+            uint32_t pa[4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const float ref = m[y] == -INFINITY ? 0.f : kKvShift - m[y];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float a = kv_ex2(fmaf(s[n][2 * y], p.scale_log2, ref));
+                    const float b = kv_ex2(fmaf(s[n][2 * y + 1], p.scale_log2, ref));
+                    l[y] += a + b;
+                    pa[2 * n + y] = Elem<DT>::down2(a, b);  // rounded for the tensor cores; the weight's own sum is not
+                }
             }
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) {
@@ -275,68 +342,57 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                 const int t = lane & 15, u = 2 * n + (lane >> 4);
                 uint32_t b[4];
                 ldsm4_t(b, vs + t * (2 * D) + ((u ^ (t & 7)) << 4));
-#pragma unroll
-                for (int x = 0; x < RT; ++x) {
-                    const uint32_t pa[4] = {__float_as_uint(s[x][0][0]), __float_as_uint(s[x][0][1]),
-                                            __float_as_uint(s[x][0][2]), __float_as_uint(s[x][0][3])};
-                    mma<DT>(o[x][2 * n], pa, b[0], b[1]);
-                    mma<DT>(o[x][2 * n + 1], pa, b[2], b[3]);
-                }
+                mma<DT>(o[2 * n], pa, b[0], b[1]);
+                mma<DT>(o[2 * n + 1], pa, b[2], b[3]);
             }
             __syncwarp();  // the stage may be copied into again
         }
         // ---- the warps' sums joined, in a fixed order
 #pragma unroll
-        for (int x = 0; x < RT; ++x)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                l[x][y] += __shfl_xor_sync(0xffffffffu, l[x][y], 1);
-                l[x][y] += __shfl_xor_sync(0xffffffffu, l[x][y], 2);
-                if (pair == 0) mls[warp * C::kRows + 16 * x + 8 * y + quad] = make_float2(m[x][y], l[x][y]);
-            }
+        for (int y = 0; y < 2; ++y) {
+            l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+            l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+            if (pair == 0) mls[warp * C::kRows + 8 * y + quad] = make_float2(m[y], l[y]);
+        }
         __syncthreads();
-        float top[RT][2];
+        float top[2];
 #pragma unroll
-        for (int x = 0; x < RT; ++x)
+        for (int y = 0; y < 2; ++y) {
+            float t = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                float t = -INFINITY;
+            for (int i = 0; i < kWarps; ++i) t = fmaxf(t, mls[i * C::kRows + 8 * y + quad].x);
+            top[y] = t;
+            const float f = kv_factor(m[y], t);
 #pragma unroll
-                for (int i = 0; i < kWarps; ++i) t = fmaxf(t, mls[i * C::kRows + 16 * x + 8 * y + quad].x);
-                top[x][y] = t;
-                const float f = kv_factor(m[x][y], t);
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    o[x][n][2 * y] *= f;
-                    o[x][n][2 * y + 1] *= f;
-                }
+            for (int n = 0; n < D / 8; ++n) {
+                o[n][2 * y] *= f;
+                o[n][2 * y + 1] *= f;
             }
+        }
         // warps 4-7 first, then warps 0-3 on top of them
 #pragma unroll
         for (int half = 1; half >= 0; --half) {
             if (warp >> 2 == half)
 #pragma unroll
-                for (int x = 0; x < RT; ++x)
+                for (int y = 0; y < 2; ++y) {
+                    const int r = 8 * y + quad;
+                    if (r >= rows) continue;
+                    float2 *dst = reinterpret_cast<float2 *>(sums + ((warp & 3) * C::kRows + r) * D);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int r = 16 * x + 8 * y + quad;
-                        if (r >= rows) continue;
-                        float2 *dst = reinterpret_cast<float2 *>(sums + ((warp & 3) * C::kRows + r) * D);
-#pragma unroll
-                        for (int n = 0; n < D / 8; ++n) {
-                            const int u = (4 * n + pair) ^ (4 * (r & 3));  // spread over the banks
-                            float2 v = make_float2(o[x][n][2 * y], o[x][n][2 * y + 1]);
-                            if (half == 0) {
-                                const float2 was = dst[u];
-                                v.x += was.x;
-                                v.y += was.y;
-                            }
-                            dst[u] = v;
+                    for (int n = 0; n < D / 8; ++n) {
+                        const int u = (4 * n + pair) ^ (4 * (r & 3));  // spread over the banks
+                        float2 v = make_float2(o[n][2 * y], o[n][2 * y + 1]);
+                        if (half == 0) {
+                            const float2 was = dst[u];
+                            v.x += was.x;
+                            v.y += was.y;
                         }
+                        dst[u] = v;
                     }
+                }
             __syncthreads();
         }
-        const bool whole = w.whole();
+        const bool whole = CLUSTER || w.whole();
         const int place = 2 * blockIdx.x + (w.tile == 0);  // of a partial sum
         for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kWarps) {
             const int r = i / (D / 4), c = i % (D / 4), t = p.by_group(r), j = r - t * p.group;
@@ -357,7 +413,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                 v.z += a.z;
                 v.w += a.w;
             }
-            if (whole) {
+            if (CLUSTER) {
+                *reinterpret_cast<float4 *>(sums + r * D + ((4 * c) ^ (8 * (r & 3)))) = v;
+                if (c == 0) own_ml[r] = make_float2(mm, ll);
+            } else if (whole) {
                 const float inv = ll == 0.f ? 0.f : 1.f / ll;
                 const int row = w.rq.row0 + t, head = w.h * p.group + j;
                 *reinterpret_cast<uint2 *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + 4 * c) =
@@ -369,9 +428,49 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                 if (c == 0) p.ml[(size_t)place * C::kRows + r] = make_float2(mm, ll);
             }
         }
+        if (CLUSTER) {
+            // ---- the blocks' sums joined, in their order; a block writes a part of the results
+            cluster_arrive();
+            cluster_wait();
+            const int ranks = p.by_blocks.d, rank = (int)cluster_rank();
+            for (int i = rank * 32 * kWarps + threadIdx.x; i < rows * (D / 4); i += ranks * 32 * kWarps) {
+                const int r = i / (D / 4), c = i % (D / 4), t = p.by_group(r), j = r - t * p.group;
+                float2 a[kMostRanks];
+                float4 x[kMostRanks];
+                float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+                for (int k = 0; k < kMostRanks; ++k) {
+                    if (k >= ranks) continue;
+                    a[k] = ld_cluster2(map_rank(smem_u32(own_ml + r), k));
+                    x[k] = ld_cluster4(map_rank(smem_u32(sums + r * D + ((4 * c) ^ (8 * (r & 3)))), k));
+                }
+#pragma unroll
+                for (int k = 0; k < kMostRanks; ++k)
+                    if (k < ranks) mm = fmaxf(mm, a[k].x);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kMostRanks; ++k) {
+                    if (k >= ranks) continue;
+                    const float f = kv_factor(a[k].x, mm);
+                    ll += a[k].y * f;
+                    v.x = fmaf(x[k].x, f, v.x);
+                    v.y = fmaf(x[k].y, f, v.y);
+                    v.z = fmaf(x[k].z, f, v.z);
+                    v.w = fmaf(x[k].w, f, v.w);
+                }
+                const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                const int row = w.rq.row0 + t, head = w.h * p.group + j;
+                *reinterpret_cast<uint2 *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + 4 * c) =
+                    make_uint2(Elem<DT>::down2(v.x * inv, v.y * inv), Elem<DT>::down2(v.z * inv, v.w * inv));
+                if (p.lse && c == 0) p.lse[(int64_t)row * p.heads + head] = kv_lse(mm, ll);
+            }
+            cluster_arrive();  // no block leaves while its memory is read
+            cluster_wait();
+            break;
+        }
         if (!whole) {
-            // ---- the block that brings the last part of a unit joins them all, in their order
-            const int c0 = (w.flat - w.tile) / share.share, c1 = (w.flat - w.tile + w.nt - 1) / share.share;
+            const int c0 = w.tile == 0 ? (int)blockIdx.x : (w.flat - w.tile) / share.share;
+            const int c1 = w.end == w.nt ? (int)blockIdx.x : (w.flat - w.tile + w.nt - 1) / share.share;
             __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
@@ -381,10 +480,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
             __syncthreads();
             if (*last_part) {
                 __threadfence();
-                for (int r = warp; r < rows; r += kWarps) {
-                    const int t = p.by_group(r), j = r - t * p.group;
-                    kv_join_row<DT, D>(p, c0, c1, C::kRows, r, w.rq.row0 + t, w.h * p.group + j, lane);
-                }
+                kv_join_unit<DT, D, C::kRows>(p, sums, c0, c1, rows, w.rq.row0, w.h * p.group);
             }
         }
         __syncthreads();
@@ -396,7 +492,6 @@ bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Rows of a partial sum's place in the workspace: (token, head) rows of a unit
 // of the launch that takes a call of `tokens` rows at most.
-constexpr int kFewRows = 32;
 int place_rows(long long tokens, int group) {
     return tokens * group <= kFewRows ? kFewRows : tokens <= kv_tile_tokens(group) ? kKvTileRows : 2 * kKvTileRows;
 }
@@ -416,17 +511,72 @@ KvLayout kv_layout(int rows, int D) {
     return l;
 }
 
-template <int DT, int D, int RT>
+template <int DT, int D, bool CLUSTER>
 int launch_few(const KvParams &p, int blocks, cudaStream_t s) {
-    const int st = set_smem<kv_few_rows_kernel<DT, D, RT>>(FewRows<D, RT>::kBytes);
+    const int st = set_smem<kv_few_rows_kernel<DT, D, CLUSTER>>(FewRows<D>::kBytes);
     if (st) return st;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = latent_config(dim3((unsigned)blocks), 32 * kWarps, FewRows<D, RT>::kBytes, s, attr, 1);
-    return record_launch(cudaLaunchKernelEx(&cfg, kv_few_rows_kernel<DT, D, RT>, p));
+    cudaLaunchConfig_t cfg = latent_config(dim3((unsigned)blocks), 32 * kWarps, FewRows<D>::kBytes, s, attr,
+                                           CLUSTER ? p.by_blocks.d : 1);
+    return record_launch(cudaLaunchKernelEx(&cfg, kv_few_rows_kernel<DT, D, CLUSTER>, p));
 }
+
+// Clusters of 2, 4 and 8 blocks that the device runs at a time (0: not known).
 template <int DT, int D>
-int launch_few_rt(const KvParams &p, int blocks, long long rows, cudaStream_t s) {
-    return rows <= 16 ? launch_few<DT, D, 1>(p, blocks, s) : launch_few<DT, D, 2>(p, blocks, s);
+const int *active_clusters() {
+    static thread_local int done_dev = -1, active[3];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+    if (dev < 0 || done_dev != dev) {
+        for (int i = 0; i < 3; ++i) {
+            cudaLaunchAttribute attr[2];
+            cudaLaunchConfig_t cfg = latent_config(dim3(1024), 32 * kWarps, FewRows<D>::kBytes, nullptr, attr, 2 << i);
+            active[i] = 0;
+            if (dev < 0 || set_smem<kv_few_rows_kernel<DT, D, true>>(FewRows<D>::kBytes)) continue;
+            if (cudaOccupancyMaxActiveClusters(&active[i], kv_few_rows_kernel<DT, D, true>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                active[i] = 0;
+            }
+        }
+        done_dev = dev;
+    }
+    return active;
+}
+
+// Blocks of a cluster for a call of few rows, or 0 for equal shares.  Clusters
+// of S blocks take ceil(tiles / S) tiles' time, if the device runs all at once
+// (8 of 8 blocks, 32 of 4); shares go by the number of all tiles, and their
+// search and join cost two tiles more and a sixteenth for every part of a unit.
+// Both, us, one token: 16 units of 512 tokens 6.6 and 8.5, of 2048 9.9 and 9.9;
+// 8 units of 4096 tokens 9.4 and 10.3, of 8192 12.7 and 12.0; 1 unit of 4096
+// tokens 9.6 and 11.7, of 8192 15.0 and 15.0; 128 units of 512 tokens (clusters
+// in rounds) 13.6 and 8.6.
+template <int DT, int D>
+int cluster_ranks(long long units, int max_len, int blocks) {
+    const long long tiles = (max_len + kKvTile - 1) / kKvTile;
+    if (tiles <= 1 || units * tiles >= (1 << 20)) return 0;  // nothing to join; far from worth it
+    const long long parts = blocks / units < tiles ? blocks / units : tiles;
+    long long best = (units * tiles + blocks - 1) / blocks + 2 + parts / 16;
+    const int *active = active_clusters<DT, D>();
+    int ranks = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int s = 2 << i;
+        const long long cost = (tiles + s - 1) / s;
+        if (units <= active[i] && cost < best) {
+            best = cost;
+            ranks = s;
+        }
+    }
+    return ranks;
+}
+
+template <int DT, int D>
+int launch_few_rows(KvParams &p, int sms, cudaStream_t s) {
+    const long long units = (long long)p.B * p.kv_heads, tiles = units * ((p.max_len + kKvTile - 1) / kKvTile + (p.max_len == 0));
+    const int ranks = cluster_ranks<DT, D>(units, p.max_len, sms);
+    const int blocks = ranks ? (int)units * ranks : (int)(tiles < sms ? tiles : sms);  // no more blocks than tiles
+    p.by_blocks.set(ranks ? ranks : blocks);
+    return ranks ? launch_few<DT, D, true>(p, blocks, s) : launch_few<DT, D, false>(p, blocks, s);
 }
 
 }  // namespace
@@ -533,13 +683,11 @@ extern "C" int spx_kv_attention(const spx_kv_attention_args *a, spx_stream_t str
     const bool f16 = c.dtype == SPX_F16;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (rows <= kFewRows) {
-        // no more blocks than tiles
-        const long long most = (long long)c.B * c.kv_heads * ((p.max_len + kKvTile - 1) / kKvTile + (p.max_len == 0));
-        const int blocks = (int)(most < sms && most < kKvMaxBlocks ? most : sms < kKvMaxBlocks ? sms : kKvMaxBlocks);
+        const int most = sms < kKvMaxBlocks ? sms : kKvMaxBlocks;
         p.span = a->max_q;
         p.unit_cost = 0;
-        return c.D == 128 ? (f16 ? launch_few_rt<SPX_F16, 128>(p, blocks, rows, s) : launch_few_rt<SPX_BF16, 128>(p, blocks, rows, s))
-                          : (f16 ? launch_few_rt<SPX_F16, 64>(p, blocks, rows, s) : launch_few_rt<SPX_BF16, 64>(p, blocks, rows, s));
+        return c.D == 128 ? (f16 ? launch_few_rows<SPX_F16, 128>(p, most, s) : launch_few_rows<SPX_BF16, 128>(p, most, s))
+                          : (f16 ? launch_few_rows<SPX_F16, 64>(p, most, s) : launch_few_rows<SPX_BF16, 64>(p, most, s));
     }
     p.seams = reinterpret_cast<int4 *>(ws + l.seams);
     return launch_kv_tiles(p, c.dtype, sms < kKvMaxBlocks ? sms : kKvMaxBlocks, s);

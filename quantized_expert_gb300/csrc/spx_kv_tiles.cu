@@ -1,5 +1,5 @@
 // spx_kv_tiles.cu -- attention over the paged cache of keys and values, calls
-// of more than 32 (token, head) rows a key head: trees, verify passes, prompts.
+// of more than 16 (token, head) rows a key head: trees, verify passes, prompts.
 //
 // Rows that share a key head (the tokens of a request times the query heads of
 // the group) are the 128 rows of a product:  S = Q K^T (128 rows x 128 cached
@@ -636,7 +636,8 @@ __global__ void __launch_bounds__(32 * kJoinRows) kv_join_kernel(const __grid_co
     griddep_launch_dependents();
     const int4 seam = __ldcg(p.seams + c0);
     if (t_of >= p.tile_tokens || t >= seam.y) return;
-    kv_join_row<DT, D>(p, c0, seam.w, unit_rows, r, seam.x + t, seam.z * p.group + in - t_of * p.group, lane);
+    kv_write_row<DT, D>(p, kv_sum_parts<D>(p, c0, seam.w, 0, 1, unit_rows, r, lane), seam.x + t,
+                        seam.z * p.group + in - t_of * p.group, lane);
 }
 
 // -------------------------------------------------------------------- host --
@@ -681,6 +682,7 @@ int launch_kv_tiles(KvParams &p, int dt, int blocks, cudaStream_t s) {
     const bool tall = (p.max_q < p.N ? p.max_q : p.N) > p.tile_tokens;
     p.span = tall ? 2 * p.tile_tokens : p.tile_tokens;
     p.unit_cost = kUnitCost;
+    p.by_blocks.set(blocks);
     p.box_tokens = 16;
     while (p.box_tokens < kKvTile && p.page_size % (2 * p.box_tokens) == 0) p.box_tokens *= 2;
     KvMaps maps;
