@@ -64,6 +64,7 @@ __device__ __forceinline__ void cp_async_wait() {
 // that of O = P V; P passes from one product to the other in registers.
 constexpr int kFewRows = 16;  // (token, head) rows of a unit at most
 constexpr int kWarps = 8;
+constexpr int kFewUnitCost = 1;  // of a unit beside its tiles, in tiles (65536 tokens of 8 units, us: 0 51.4, 1 47.6, 2 51.6; 32 requests of 16 units 92.7, 91.2, 92.0)
 constexpr int kMostRanks = 8;  // blocks of a cluster
 template <int D>
 struct FewRows {
@@ -685,7 +686,7 @@ extern "C" int spx_kv_attention(const spx_kv_attention_args *a, spx_stream_t str
     if (rows <= kFewRows) {
         const int most = sms < kKvMaxBlocks ? sms : kKvMaxBlocks;
         p.span = a->max_q;
-        p.unit_cost = 0;
+        p.unit_cost = kFewUnitCost;
         return c.D == 128 ? (f16 ? launch_few_rows<SPX_F16, 128>(p, most, s) : launch_few_rows<SPX_BF16, 128>(p, most, s))
                           : (f16 ? launch_few_rows<SPX_F16, 64>(p, most, s) : launch_few_rows<SPX_BF16, 64>(p, most, s));
     }

@@ -20,10 +20,11 @@ namespace spx {
 
 namespace {
 
-constexpr int kThreads = 384;  // copies of K and V, two issuers of products, copies of Q; 2 x 4 softmax warps
+constexpr int kThreads = 384;  // copies of K and V, two warps for products, copies of Q; 2 x 4 softmax warps
 constexpr int kPiece = kKvTile * 128;  // 128 rows of 64 values, 16 KB
 
 constexpr int kUnitCost = 3;  // tiles
+constexpr int kMostBoxes = kKvTile / 16;  // copies of 64 values of a tile's tokens, by the size of a page
 
 struct KvMaps {
     CUtensorMap k, v;  // [page][head][token][D], boxes of 64 values x box_tokens
@@ -87,11 +88,13 @@ struct Place {
     }
 };
 
-// A softmax row takes 128 scores in registers: 168 a thread, what 384 threads
-// share out evenly, are too few, so the first four warps give up
-// some (4 x 32 x 80 + 8 x 32 x 208 <= 384 x 168).
-__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
-__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+// ctl_wait by a whole warp, converged behind it: loads of tensor memory and
+// barriers take a warp as one, and lanes may leave the wait apart.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtl &c) {
+    const bool ok = ctl_wait(bar, parity, c);
+    __syncwarp();
+    return ok;
+}
 
 template <int DT, int D, bool TALL>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&m.uempty[i], 11);  // copies, issuers, softmax warps
         }
         mbar_init(&m.qfull, 1);
-        mbar_init(&m.qempty, 2);
+        mbar_init(&m.qempty, TALL ? 2 : 1);
         for (int i = 0; i < C::kRing; ++i) {
             mbar_init(&m.full[i], 1);
             mbar_init(&m.empty[i], TALL ? 2 : 1);
@@ -125,7 +128,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 2) (&m.bad[0][0][0])[lane] = 0;
-    if (warp == 0 && lane < 3) prefetch_tmap(lane == 0 ? &maps.k : lane == 1 ? &maps.v : &maps.q);
+    griddep_wait();
+    griddep_launch_dependents();
     if (warp == 1) {
         tmem_alloc(&m.tmem, 512);
         tmem_relinquish();
@@ -135,11 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = m.tmem;
     const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_KV};
-    griddep_wait();
-    griddep_launch_dependents();
 
     if (warp < 4) {
-        fewer_registers();
         if (warp == 3) {
             // ---- the share's units, one ahead of the copies of their queries; the unit that begins in this share and
             // ends in a later one, for the join launch
@@ -193,8 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 0) {
             // ---- copies: keys and values of the tiles in turn
             const uint64_t pol = policy_evict_normal();
-            const int bt = p.box_tokens, boxes = kKvTile / bt, box = lane % boxes, piece = lane / boxes;
-            const bool mine = lane < boxes * C::kPieces;  // the lane's box of a tile
+            const int bt = p.box_tokens, boxes = kKvTile / bt, box = lane % boxes;
             Place<C::kRing> r;
             bool ok = true;
             for (uint32_t u = 0; ok; ++u) {
@@ -218,103 +218,121 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, r.advance(1)) {
                         if (!(ok = ctl_wait(&m.empty[r.i], r.phase ^ 1, ctl))) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&m.full[r.i], C::kSlot);
+                        if (elect_one()) mbar_arrive_expect_tx(&m.full[r.i], C::kSlot);
                         __syncwarp();
-                        if (mine)
-                            tma_load_4d(ring + r.i * C::kSlot + piece * kPiece + box * bt * 128, kv ? &maps.v : &maps.k, 64 * piece,
-                                        at, h, page, &m.full[r.i], pol);
-                        __syncwarp();
+                        uint8_t *dst = ring + r.i * C::kSlot;
+#pragma unroll
+                        for (int i = 0; i < kMostBoxes; i += 2) {
+                            if (i >= boxes) break;
+                            const int a = __shfl_sync(0xffffffffu, at, i), g = __shfl_sync(0xffffffffu, page, i);
+                            const int a1 = __shfl_sync(0xffffffffu, at, i + 1), g1 = __shfl_sync(0xffffffffu, page, i + 1);
+                            if (elect_one())
+#pragma unroll
+                                for (int c = 0; c < C::kPieces; ++c) {
+                                    tma_load_4d(dst + c * kPiece + i * bt * 128, kv ? &maps.v : &maps.k, 64 * c, a, h, g,
+                                                &m.full[r.i], pol);
+                                    if (i + 1 < boxes)
+                                        tma_load_4d(dst + c * kPiece + (i + 1) * bt * 128, kv ? &maps.v : &maps.k, 64 * c, a1, h, g1,
+                                                    &m.full[r.i], pol);
+                                }
+                            __syncwarp();
+                        }
                     }
                 }
             }
         } else {
-            // ---- products of X: O_X of the last tile, then S_X of the next one, in one stretch behind everything that
-            // they wait for
-            const int x = warp - 1;
+            // ---- products: O_X of X's last tile, then S_X of its next one, in one stretch behind everything that they
+            // wait for.  TALL: a warp for each X, which pass a turn to each other; else the first for both, as two that
+            // hand in products at will are more than the order of the tiles needs.
             const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
             const uint32_t id_s = idesc_f16_f32(128, 128) | fmt, id_o = idesc_f16_f32(128, D) | fmt | kIdescBMn;
-            const uint64_t qd = sw128_desc(smem_u32(qs) + (TALL ? x * C::kSlot : 0)), kd = sw128_desc(smem_u32(ring));
+            const uint64_t qd = sw128_desc(smem_u32(qs)), kd = sw128_desc(smem_u32(ring));
             const uint64_t vd = sw128_desc_mn(smem_u32(ring), kPiece);
-            const uint32_t st = tmem + 128 * x, ot = tmem + 256 + 128 * x;
-            const auto scores = [&](uint32_t slot) {
+            const auto scores = [&](int x, uint32_t slot) {
+                const uint64_t q = qd + (TALL ? x * (C::kSlot / 16) : 0), k = kd + slot * (C::kSlot / 16);
 #pragma unroll
                 for (int c = 0; c < C::kPieces; ++c)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        umma_f16(st, qd + c * (kPiece / 16) + 2 * i, kd + slot * (C::kSlot / 16) + c * (kPiece / 16) + 2 * i, id_s,
-                                 c | i);
+                        umma_f16(tmem + 128 * x, q + c * (kPiece / 16) + 2 * i, k + c * (kPiece / 16) + 2 * i, id_s, c | i);
             };
-            const auto sums = [&](uint32_t slot, int half, bool first) {
+            const auto sums = [&](int x, uint32_t slot, int half, bool first) {
 #pragma unroll
                 for (int i = 4 * half; i < 4 * half + 4; ++i)
-                    umma_f16_ta(ot, st + 8 * i, vd + slot * (C::kSlot / 16) + 128 * i, id_o, !first || i);
+                    umma_f16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 8 * i, vd + slot * (C::kSlot / 16) + 128 * i, id_o,
+                                !first || i);
             };
-            Place<C::kRing> at;             // of the keys of the unit's first tile
-            uint32_t tile = 0, step = 0, unit = 0;  // tiles and units of X before this one, turns
+            Place<C::kRing> at;  // of the keys of the unit's first tile
+            uint32_t tile0 = 0, tile1 = 0, unit0 = 0, unit1 = 0, step = 0;  // tiles and units of X before this one, turns
             bool ok = true;
             for (uint32_t u = 0; ok; ++u) {
                 if (!(ok = ctl_wait(&m.ufull[u % kUnitRing], (u / kUnitRing) & 1, ctl))) break;
                 const Unit &d = m.unit[u % kUnitRing];
-                const int end = d.end, all = end - d.tile, n = d.n[x], most = TALL ? all : n;
+                const int end = d.end, all = end - d.tile, n0 = d.n[0], n1 = d.n[1];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m.uempty[u % kUnitRing]);
                 if (end == 0) break;
+                if (!TALL && warp == 2) continue;
                 Place<C::kRing> kr = at, vr = at;
                 vr.advance(1);
-                if (!TALL && x) {
-                    kr.advance(2);
-                    vr.advance(2);
-                }
                 ok = ctl_wait(&m.qfull, u & 1, ctl);
+                // Step j: S of tile j, and O of the tile before (TALL; X's own, on the same tiles), or of the one before
+                // that (tiles belong to X = 0 and 1 in turn).
+                constexpr int kLag = TALL ? 1 : 2;
 #pragma unroll 1
-                for (int j = 0; ok && j <= most; ++j, ++step) {
-                    const bool has_o = j > 0 && j <= n, has_s = j < n;
+                for (int j = 0; ok && j < all + kLag; ++j) {
+                    const int x = TALL ? warp - 1 : j & 1, t = j - kLag, n = TALL ? (x ? n1 : n0) : all;
+                    const bool has_o = t >= 0 && t < n, has_s = j < n;
+                    const uint32_t parity = ((x ? tile1 : tile0) + (TALL ? t : t >> 1)) & 1;  // of O's weights
+                    const bool first = TALL ? t == 0 : t < 2, last = TALL ? t == n - 1 : t >= all - 2;  // O of X in the unit
                     // the slots of the unit's last tile are room for its results, and given back by the softmax warps
-                    const bool last_k = TALL && j == all - 1, last_v = (TALL ? j - 1 : 2 * (j - 1) + x) == all - 1;
-                    ok = (j == most || ctl_wait(&m.full[kr.i], kr.phase, ctl)) && (j == 0 || ctl_wait(&m.full[vr.i], vr.phase, ctl)) &&
+                    const bool last_k = TALL && j == all - 1, last_v = t == all - 1;
+                    ok = (j >= all || ctl_wait(&m.full[kr.i], kr.phase, ctl)) && (t < 0 || ctl_wait(&m.full[vr.i], vr.phase, ctl)) &&
                          // tile 1 goes behind tile 0's products of the same step, tile 0 behind tile 1's of the last
                          // one, or they fall into step, both softmaxes at once and then both products
                          (!TALL || (x ? ctl_wait(&m.turn[1], step & 1, ctl) : step == 0 || ctl_wait(&m.turn[0], (step - 1) & 1, ctl))) &&
-                         (!has_o || j > 1 || ctl_wait(&m.oempty[x], (unit & 1) ^ 1, ctl)) &&
-                         (!has_o || ctl_wait(&m.pfull[x][0], (tile + j - 1) & 1, ctl));
+                         (!has_o || !first || ctl_wait(&m.oempty[x], ((x ? unit1 : unit0) & 1) ^ 1, ctl)) &&
+                         (!has_o || ctl_wait(&m.pfull[x][0], parity, ctl));
                     if (!ok) break;
                     tc_fence_after();
                     if (has_o) {  // the first half while the softmax is at the second
-                        if (elect_one()) sums(vr.i, 0, j == 1);
+                        if (elect_one()) sums(x, vr.i, 0, first);
                         __syncwarp();
-                        if (!(ok = ctl_wait(&m.pfull[x][1], (tile + j - 1) & 1, ctl))) break;
+                        if (!(ok = ctl_wait(&m.pfull[x][1], parity, ctl))) break;
                         tc_fence_after();
                     }
                     if (elect_one()) {
                         if (has_o) {
-                            sums(vr.i, 1, false);
+                            sums(x, vr.i, 1, false);
                             if (!last_v) umma_commit(&m.empty[vr.i]);
-                            if (j == n) umma_commit(&m.odone[x]);
-                        } else if (j > 0 && !last_v) {
+                            if (last) umma_commit(&m.odone[x]);
+                        } else if (t >= 0 && !last_v) {
                             mbar_arrive(&m.empty[vr.i]);
                         }
                         if (has_s) {
-                            scores(kr.i);
+                            scores(x, kr.i);
                             if (!last_k) umma_commit(&m.empty[kr.i]);
                             umma_commit(&m.sfull[x]);
                             if (j == n - 1) umma_commit(&m.qempty);
-                        } else if (j < most && !last_k) {
+                        } else if (j < all && !last_k) {
                             mbar_arrive(&m.empty[kr.i]);
                         }
                         if (n == 0 && j == 0) mbar_arrive(&m.qempty);
                         if (TALL) mbar_arrive(&m.turn[x ^ 1]);
                     }
                     __syncwarp();
-                    if (j > 0) vr.advance(TALL ? 2 : 4);
-                    kr.advance(TALL ? 2 : 4);
+                    if (t >= 0) vr.advance(2);
+                    kr.advance(2);
+                    ++step;
                 }
-                tile += n;
-                unit += n > 0;
+                tile0 += n0;
+                tile1 += n1;
+                unit0 += n0 > 0;
+                unit1 += n1 > 0;
                 at.jump(2 * all);
             }
         }
     } else {
-        more_registers();
         // ---- softmax and results: a row a thread
         const int x = (warp - 4) >> 2, q = warp & 3, r = 32 * q + lane;
         const uint32_t quarter = (uint32_t)(32 * q) << 16;
@@ -322,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t_of = p.by_group(r);
         uint32_t tile = 0, before = 0, units = 0, units_o = 0;  // tiles of X, tiles of the block, units with tiles of X and of the other, so far
         // (Warps that meet at barriers leave together: where one gave up, all hear of it.)
-        bool ok = ctl_wait(&m.ufull[0], 0, ctl);
-        if (bar_any(1, 256, !ok)) ok = false;
+        bool ok = warp_wait(&m.ufull[0], 0, ctl);
+        if (bar_any(2, 256, !ok)) ok = false;
 #pragma unroll 1
         for (uint32_t u = 0; ok; ++u) {
             const Unit &d = m.unit[u % kUnitRing];
@@ -337,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float mr = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
-                ctl_wait(&m.sfull[x], (tile + i) & 1, ctl);
+                warp_wait(&m.sfull[x], (tile + i) & 1, ctl);
                 tc_fence_after();
                 const int li = TALL ? i : 2 * i + x, j = first + li, p0 = kKvTile * j;
                 const bool masked = p0 + kKvTile > all;
@@ -415,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // hold one which is not finite, become zeros, as a weight of 0 does not make them so; the rows
                     // that see such a token become NaNs at the end.  A token a thread.
                     const uint32_t item = 2 * (before + li) + 1, slot = item % C::kRing;
-                    ctl_wait(&m.full[slot], (item / C::kRing) & 1, ctl);
+                    warp_wait(&m.full[slot], (item / C::kRing) & 1, ctl);
                     uint8_t *row = ring + slot * C::kSlot + r * 128;
                     bool zero = p0 + r >= rq.len;
                     if (!zero) {
@@ -438,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 8 * C::kPieces; ++k)
                             *reinterpret_cast<uint4 *>(row + (k >> 3) * kPiece + (((k ^ r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
+                    __syncwarp();
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -449,10 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- the unit's end
             const int parts = d.end - first;
-            if (n) ctl_wait(&m.odone[x], units & 1, ctl);
-            if (other) ctl_wait(&m.odone[x ^ 1], units_o & 1, ctl);
+            if (n) warp_wait(&m.odone[x], units & 1, ctl);
+            if (other) warp_wait(&m.odone[x ^ 1], units_o & 1, ctl);
             tc_fence_after();
             if (!TALL) m.ml[x][r] = make_float2(mr, l);
+            __syncwarp();
             bar_sync(1, 256);  // references, weights and lists of bad tokens are there
             float f[2] = {1.f, 1.f};
             if (!TALL) {
@@ -486,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c0 = TALL ? 0 : x * kCols;
             const size_t place = (size_t)(2 * blockIdx.x + (first == 0)) * C::kRows + (TALL ? 128 * x : 0) + 32 * q;
             if (warp_live) {
-                if (TALL) ctl_wait(&m.full[k_slot], (item / C::kRing) & 1, ctl);  // (else it may hold another unit's by now)
-                ctl_wait(&m.full[v_slot], ((item + 1) / C::kRing) & 1, ctl);
+                if (TALL) warp_wait(&m.full[k_slot], (item / C::kRing) & 1, ctl);  // (else it may hold another unit's by now)
+                warp_wait(&m.full[v_slot], ((item + 1) / C::kRing) & 1, ctl);
                 uint8_t *stage = ring + (TALL && x == 0 ? k_slot : v_slot) * C::kSlot + ((TALL ? 0 : 4 * x) + q) * 32 * kRow;
                 // unit k of row i of the warp's 32
                 const auto staged = [&](int i, int k) {
@@ -595,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&m.uempty[u % kUnitRing]);
             }
             if (warp == 4 && lane < 16) (&m.bad[(u & 1) ^ 1][0][0])[lane] = 0;
-            ok = ctl_wait(&m.ufull[(u + 1) % kUnitRing], ((u + 1) / kUnitRing) & 1, ctl);
-            if (bar_any(1, 256, !ok)) ok = false;  // and everyone has read what the next unit writes
+            ok = warp_wait(&m.ufull[(u + 1) % kUnitRing], ((u + 1) / kUnitRing) & 1, ctl);
+            if (bar_any(2, 256, !ok)) ok = false;  // and everyone has read what the next unit writes
             if (q == 0 && lane == 0 && (TALL || x == 0)) {
                 if (TALL) mbar_arrive(&m.empty[k_slot]);
                 mbar_arrive(&m.empty[v_slot]);
@@ -607,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             units_o += other > 0;
         }
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (m.abort) {
