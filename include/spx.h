@@ -692,9 +692,10 @@ SPX_API int spx_tree_layout(const spx_tree_layout_args *args, spx_stream_t strea
  *   x = x * rsqrt(mean(x^2) + eps) * w        (w = q_norm, k_norm; NULL: not)
  *   x[0..P) = rotation of x[0..P) by row pos[n] of cos/sin      (cos != NULL)
  * rounded once; keys and values go to token slot[n] of request req[n], queries
- * to q_out (which may be q).  The rotation turns the pair (a, b) into (a cos -
- * b sin, b cos + a sin), pairs being elements (2i, 2i + 1) when interleaved,
- * else (i, i + P/2); cos and sin are fp32 [max_pos][P/2].  pos == NULL: slot.
+ * to q_out (q itself, or apart from it).  The rotation turns the pair (a, b)
+ * into (a cos - b sin, b cos + a sin), pairs being elements (2i, 2i + 1) when
+ * interleaved, else (i, i + P/2); cos and sin are fp32 [max_pos][P/2].  pos ==
+ * NULL: slot.  The cache's k and v are two buffers.
  * A row is skipped when slot[n] is negative, or pos[n] negative or beyond the
  * cos/sin rows; its keys and values also when req[n] is outside [0, B) or its
  * table entry is missing or names no page.  Two rows must not name the same
@@ -728,7 +729,8 @@ SPX_API int spx_kv_append(const spx_kv_append_args *args, spx_stream_t stream);
  * an infinity or a NaN reaches only the rows that see it (an infinite or NaN
  * value in at least its own column of out).  max_len bounds every request's
  * length (longer ones are cut to it).  Softmax weights are rounded to the type
- * before they meet the values; every sum is fp32. */
+ * before they meet the values; every sum is fp32.  out lies apart from what is
+ * read.  Calls with one workspace must not run at the same time. */
 typedef struct {
     const spx_kv_cache *cache;
     int N, heads;                /* heads a multiple of kv_heads, at most 64 to one key head */
@@ -750,7 +752,8 @@ typedef struct {
 SPX_API int spx_kv_attention(const spx_kv_attention_args *args, spx_stream_t stream);
 /* Workspace of a call; 0 if unsupported.  Any larger workspace serves too.  Its
  * status word (spx_workspace_status) is SPX_ERR_TIMEOUT after a bounded wait
- * that gave up; it is zeroed again then. */
+ * that gave up; out is not valid then, and the workspace's first
+ * SPX_KV_WORKSPACE_ZERO bytes are to be zeroed before the next call. */
 SPX_API size_t spx_kv_workspace_size(int B, int N, int max_q, int max_len, int heads, int kv_heads, int D);
 
 /* The end of a step, one launch: from row 0 on, the walk goes from row i to
@@ -760,7 +763,7 @@ SPX_API size_t spx_kv_workspace_size(int B, int N, int max_q, int max_len, int h
  *   q_start[b] + d] is the d-th of them, -1 from n_kept[b] on; next[b] = target
  *   of the last one (-1 without rows); lens_out[b] = lens[b] - T + n_kept[b].
  * In each of the n_layers caches, which share cache's layout, block table and
- * lens, the keys and values of the path's d-th row are moved to token lens[b] -
+ * lens and have buffers of their own, the keys and values of the path's d-th row are moved to token lens[b] -
  * T + d.  layer_k and layer_v are host arrays of device pointers. */
 typedef struct {
     const spx_kv_cache *cache;   /* its k and v are not used */

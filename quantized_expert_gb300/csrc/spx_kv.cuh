@@ -10,6 +10,7 @@ namespace spx {
 constexpr int kKvMaxTree = 64;    // rows of a tree: the bits of a mask
 constexpr int kKvMaxGroup = 64;   // query heads to a key head
 constexpr int kKvTile = 128;      // cached tokens of a tile
+constexpr int kKvMostCost = 4;    // of a unit beside its tiles, in tiles, in any launch
 constexpr int kKvMaxBlocks = 152; // blocks of an attention launch: one per SM at most
 
 struct KvParams {

@@ -198,7 +198,7 @@ extern "C" int spx_kv_append(const spx_kv_append_args *a, spx_stream_t stream) {
     const int st = kv_cache_check(a->cache);
     if (st) return st;
     const spx_kv_cache &c = *a->cache;
-    if (a->N < 0 || !a->cos != !a->sin || !a->q != !a->q_out || (a->q_norm && !a->q)) return SPX_ERR_INVALID_ARG;
+    if (c.k == c.v || a->N < 0 || !a->cos != !a->sin || !a->q != !a->q_out || (a->q_norm && !a->q)) return SPX_ERR_INVALID_ARG;
     if (a->cos && (a->max_pos < 1 || !al16(a->cos) || !al16(a->sin))) return SPX_ERR_INVALID_ARG;
     if (a->cos && (a->P < 16 || a->P > c.D || a->P % 16)) return SPX_ERR_UNSUPPORTED;
     if ((a->q_norm || a->k_norm) && !(a->eps >= 0.f)) return SPX_ERR_INVALID_ARG;

@@ -615,10 +615,10 @@ using namespace spx;
 extern "C" size_t spx_kv_workspace_size(int B, int N, int max_q, int max_len, int heads, int kv_heads, int D) {
     if (B < 1 || N < 0 || max_q < 0 || max_len < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads) return 0;
     if ((D != 64 && D != 128) || heads / kv_heads > kKvMaxGroup || kv_heads > 1024 || B > 65535) return 0;
-    // rows of (token, head) and cached tokens are counted in 31 bits, and so are the tiles of the call
+    // rows of (token, head) and cached tokens are counted in 31 bits, and so are the call's tiles with what units cost
     if ((long long)N * heads > 1 << 30 || (long long)max_q * heads > 1 << 30) return 0;
     const long long rows = max_q < N ? max_q : N;
-    if ((double)B * kv_heads * (rows * (heads / kv_heads) / 64 + 1) * (max_len / kKvTile + 1) > 2e9) return 0;
+    if ((double)B * kv_heads * (rows * (heads / kv_heads) / 64 + 1) * (max_len / kKvTile + 1 + kKvMostCost) > 2e9) return 0;
     return kv_layout(place_rows(rows, heads / kv_heads), D).bytes;
 }
 

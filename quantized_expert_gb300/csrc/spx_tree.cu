@@ -215,6 +215,10 @@ extern "C" int spx_tree_accept(const spx_tree_accept_args *a, spx_stream_t strea
         const int st = kv_cache_check(&c);
         if (st) return st;
     }
+    // a buffer that is moved twice would be read after it was written
+    for (int i = 1; i < 2 * a->n_layers; ++i)
+        for (int j = 0; j < i; ++j)
+            if (p.kv[i] == p.kv[j]) return SPX_ERR_INVALID_ARG;
     if (!a->q_start || !a->n_kept || !a->next || !a->lens_out || a->N < 0 || a->max_q < 0) return SPX_ERR_INVALID_ARG;
     if (a->N > 0 && (!a->parent || !a->token || !a->target || !a->path)) return SPX_ERR_INVALID_ARG;
     const size_t nb = (size_t)c.B * 4, nn = (size_t)a->N * 4;

@@ -797,12 +797,14 @@ def _on_one_device(a, *tensors):
 
 def _launch(name: str, args, stream):
     """The call of that name on its tensors' device, whichever is current."""
-    call = getattr(load(), name)
-    if getattr(args, "device", torch.cuda.current_device()) == torch.cuda.current_device():
-        _chk(call(C.byref(args), _stream(stream)), name)
-    else:
+    here = torch._C._cuda_getDevice()  # (torch.cuda.current_device() costs half a us a call)
+    if getattr(args, "device", here) != here:
         with torch.cuda.device(args.device):
-            _chk(call(C.byref(args), _stream(stream)), name)
+            return _launch(name, args, stream)
+    status = getattr(_lib or load(), name)(
+        C.byref(args), torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream)
+    if status:
+        _chk(status, name)
 
 
 def _rows3(t, what: str, heads=None):
@@ -973,6 +975,8 @@ def tree_accept_args(caches, q_start, max_q: int, parent, token, target, n_kept,
         o = c.cstruct()
         if any(getattr(o, f) != getattr(cs, f) for f, _ in KvCacheC._fields_ if f not in ("k", "v")):
             raise ValueError("caches of one layout, block table and lens expected")
+    if len({t.data_ptr() for c in caches for t in (c.k, c.v)}) != 2 * len(caches):
+        raise ValueError("a buffer of its own expected for each layer's keys and values")
     a = TreeAcceptArgs()
     B, N, n = cs.B, parent.numel(), len(caches)
     a.cache, a.n_layers, a.N, a.max_q = C.pointer(cs), n, N, int(max_q)

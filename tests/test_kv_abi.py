@@ -40,7 +40,7 @@ def test_struct_layouts_match_the_header(tmp_path, cname, pyname):
 def cache(**kw):
     """8 key heads of 128, pages of 64 tokens, tokens outside heads."""
     from quantized_expert_gb300 import spx
-    c = spx.KvCacheC(spx.SPX_F16, FAKE, FAKE, 10, 64, 8, 128, 64 * 1024, 1024, 128, FAKE, 5, 2, FAKE)
+    c = spx.KvCacheC(spx.SPX_F16, FAKE, FAKE + (1 << 24), 10, 64, 8, 128, 64 * 1024, 1024, 128, FAKE, 5, 2, FAKE)
     for k, v in kw.items():
         setattr(c, k, v)
     return c
@@ -81,8 +81,8 @@ def accept(c, layers=2, k=None, v=None, **kw):
     a = spx.TreeAcceptArgs()
     a.cache, a.n_layers, a.N, a.max_q = C.pointer(c), layers, 3, 2
     n = max(layers, 0)
-    a.layer_k = (C.c_void_p * (n + 1))(*(k or [FAKE + 16 * i for i in range(n)]))
-    a.layer_v = (C.c_void_p * (n + 1))(*(v or [FAKE + 16 * i for i in range(n)]))
+    a.layer_k = (C.c_void_p * (n + 1))(*(k or [FAKE + 32 * i for i in range(n)]))
+    a.layer_v = (C.c_void_p * (n + 1))(*(v or [FAKE + 32 * i + 16 for i in range(n)]))
     for i, f in enumerate(("q_start", "parent", "token", "target", "n_kept", "path", "next", "lens_out")):
         setattr(a, f, FAKE + 4096 * (i + 1))
     for f, x in kw.items():
@@ -156,6 +156,10 @@ def test_append_refusals(lib, bad, status):
     assert lib.spx_kv_append(None, None) == INV
 
 
+def test_append_wants_two_buffers(lib):
+    assert lib.spx_kv_append(C.byref(append(cache(v=FAKE))), None) == INV
+
+
 def test_append_of_nothing(lib):
     assert lib.spx_kv_append(C.byref(append(cache(), N=0)), None) == 0
 
@@ -186,7 +190,8 @@ def test_accept_refusals(lib, bad, status):
     assert lib.spx_tree_accept(None, None) == INV
 
 
-@pytest.mark.parametrize("kw", [dict(k=[FAKE, None]), dict(v=[None, FAKE]), dict(k=[FAKE, FAKE + 8])])
+@pytest.mark.parametrize("kw", [dict(k=[FAKE, None]), dict(v=[None, FAKE]), dict(k=[FAKE, FAKE + 8]),
+                                dict(k=[FAKE, FAKE]), dict(k=[FAKE, FAKE + 32], v=[FAKE + 64, FAKE])])
 def test_accept_layers(lib, kw):
     assert lib.spx_tree_accept(C.byref(accept(cache(), **kw)), None) == INV
 
