@@ -28,7 +28,8 @@ static_assert(kUnitCost <= kKvMostCost, "what the workspace's size is checked fo
 constexpr int kMostBoxes = kKvTile / 16;  // copies of 64 values of a tile's tokens, by the size of a page
 
 struct KvMaps {
-    CUtensorMap k, v;  // [page][head][token][D], boxes of 64 values x box_tokens
+    CUtensorMap k;     // [page][head][token][D], boxes of 64 values x box_tokens
+    CUtensorMap v;     // [page][head][D / 64][token][64], boxes of all a token's values x box_tokens
     CUtensorMap q;     // [row][head][D], boxes of 64 values x a group's heads x tile_tokens
 };
 
@@ -88,6 +89,16 @@ struct Place {
         i %= N;
     }
 };
+
+// Where the 64 values c of a tile's token t lie in a slot of values: a copy's
+// tokens, 64 values each, then the next 64 of the same tokens.  (Keys lie 64
+// values of all the tile's tokens after the other, as a K-major operand wants
+// its groups of 8 rows at one distance; an MN-major one has no such wish, so
+// that one copy brings whole rows, and pages of 16 tokens half the copies.)
+template <int kPieces>
+__device__ __forceinline__ int v_row(int box_tokens, int t, int c) {
+    return (t & -box_tokens) * (128 * kPieces) + c * box_tokens * 128 + (t & (box_tokens - 1)) * 128;
+}
 
 // ctl_wait by a whole warp, converged behind it: loads of tensor memory and
 // barriers take a warp as one, and lanes may leave the wait apart.
@@ -227,15 +238,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (i >= boxes) break;
                             const int a = __shfl_sync(0xffffffffu, at, i), g = __shfl_sync(0xffffffffu, page, i);
                             const int a1 = __shfl_sync(0xffffffffu, at, i + 1), g1 = __shfl_sync(0xffffffffu, page, i + 1);
-                            if (elect_one())
-#pragma unroll
-                                for (int c = 0; c < C::kPieces; ++c) {
-                                    tma_load_4d(dst + c * kPiece + i * bt * 128, kv ? &maps.v : &maps.k, 64 * c, a, h, g,
-                                                &m.full[r.i], pol);
+                            if (elect_one()) {
+                                uint8_t *to = dst + i * bt * 128;
+                                if (kv) {
+                                    to = dst + i * bt * 128 * C::kPieces;
+                                    tma_load_5d(to, &maps.v, 0, a, 0, h, g, &m.full[r.i], pol);
                                     if (i + 1 < boxes)
-                                        tma_load_4d(dst + c * kPiece + (i + 1) * bt * 128, kv ? &maps.v : &maps.k, 64 * c, a1, h, g1,
-                                                    &m.full[r.i], pol);
+                                        tma_load_5d(to + bt * 128 * C::kPieces, &maps.v, 0, a1, 0, h, g1, &m.full[r.i], pol);
+                                } else {
+#pragma unroll
+                                    for (int c = 0; c < C::kPieces; ++c) {
+                                        tma_load_4d(to + c * kPiece, &maps.k, 64 * c, a, h, g, &m.full[r.i], pol);
+                                        if (i + 1 < boxes)
+                                            tma_load_4d(to + c * kPiece + bt * 128, &maps.k, 64 * c, a1, h, g1, &m.full[r.i], pol);
+                                    }
                                 }
+                            }
                             __syncwarp();
                         }
                     }
@@ -248,7 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
             const uint32_t id_s = idesc_f16_f32(128, 128) | fmt, id_o = idesc_f16_f32(128, D) | fmt | kIdescBMn;
             const uint64_t qd = sw128_desc(smem_u32(qs)), kd = sw128_desc(smem_u32(ring));
-            const uint64_t vd = sw128_desc_mn(smem_u32(ring), kPiece);
+            const uint64_t vd = sw128_desc_mn(smem_u32(ring), p.box_tokens * 128);
+            uint32_t vk[kKvTile / 16];  // of 16 tokens' values in a slot, in the descriptor's units
+#pragma unroll
+            for (int i = 0; i < kKvTile / 16; ++i) vk[i] = v_row<C::kPieces>(p.box_tokens, 16 * i, 0) / 16;
             const auto scores = [&](int x, uint32_t slot) {
                 const uint64_t q = qd + (TALL ? x * (C::kSlot / 16) : 0), k = kd + slot * (C::kSlot / 16);
 #pragma unroll
@@ -260,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const auto sums = [&](int x, uint32_t slot, int half, bool first) {
 #pragma unroll
                 for (int i = 4 * half; i < 4 * half + 4; ++i)
-                    umma_f16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 8 * i, vd + slot * (C::kSlot / 16) + 128 * i, id_o,
+                    umma_f16_ta(tmem + 256 + 128 * x, tmem + 128 * x + 8 * i, vd + slot * (C::kSlot / 16) + vk[i], id_o,
                                 !first || i);
             };
             Place<C::kRing> at;  // of the keys of the unit's first tile
@@ -435,13 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // that see such a token become NaNs at the end.  A token a thread.
                     const uint32_t item = 2 * (before + li) + 1, slot = item % C::kRing;
                     warp_wait(&m.full[slot], (item / C::kRing) & 1, ctl);
-                    uint8_t *row = ring + slot * C::kSlot + r * 128;
+                    uint8_t *row = ring + slot * C::kSlot + v_row<C::kPieces>(p.box_tokens, r, 0);
+                    const int piece = p.box_tokens * 128;  // to the row's next 64 values
                     bool zero = p0 + r >= rq.len;
                     if (!zero) {
                         uint32_t z = 0;
 #pragma unroll
                         for (int k = 0; k < 8 * C::kPieces; ++k) {
-                            const uint4 v = lds128(row + (k >> 3) * kPiece + (((k ^ r) & 7) << 4));
+                            const uint4 v = lds128(row + (k >> 3) * piece + (((k ^ r) & 7) << 4));
                             z = Elem<DT>::fma2(v.x, 0u, z);
                             z = Elem<DT>::fma2(v.y, 0u, z);
                             z = Elem<DT>::fma2(v.z, 0u, z);
@@ -455,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (zero)
 #pragma unroll
                         for (int k = 0; k < 8 * C::kPieces; ++k)
-                            *reinterpret_cast<uint4 *>(row + (k >> 3) * kPiece + (((k ^ r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(row + (k >> 3) * piece + (((k ^ r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                     __syncwarp();
                     tmem_wait_st();
@@ -671,10 +693,12 @@ bool kv_maps(const KvParams &p, int dt, KvMaps *m) {
     const uint64_t cs[3] = {(uint64_t)p.token_stride * 2, p.kv_heads > 1 ? (uint64_t)p.head_stride * 2 : row,
                             p.num_pages > 1 ? (uint64_t)p.page_stride * 2 : row};
     const uint32_t cb[4] = {64, (uint32_t)p.box_tokens, 1, 1};
+    const uint64_t vd[5] = {64, cd[1], (uint64_t)p.D / 64, cd[2], cd[3]}, vs[4] = {cs[0], 128, cs[1], cs[2]};
+    const uint32_t vb[5] = {64, (uint32_t)p.box_tokens, (uint32_t)p.D / 64, 1, 1};
     const uint64_t qd[3] = {(uint64_t)p.D, (uint64_t)p.heads, (uint64_t)p.N};
     const uint64_t qst[2] = {row, p.N > 1 ? (uint64_t)p.q_stride * 2 : row};
     const uint32_t qb[3] = {64, (uint32_t)p.group, (uint32_t)p.tile_tokens};
-    return map_rows64(&m->k, dt, p.k, 4, cd, cs, cb) && map_rows64(&m->v, dt, p.v, 4, cd, cs, cb) &&
+    return map_rows64(&m->k, dt, p.k, 4, cd, cs, cb) && map_rows64(&m->v, dt, p.v, 5, vd, vs, vb) &&
            map_rows64(&m->q, dt, p.q, 3, qd, qst, qb);
 }
 

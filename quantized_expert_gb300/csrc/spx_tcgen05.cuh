@@ -33,6 +33,14 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *tm, in
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *tm, int x, int y, int z, int w, int v, uint64_t *bar,
+                                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)),
                  "r"(ncols)
@@ -330,8 +338,8 @@ inline bool map_rows64(CUtensorMap *m, int dt, const void *base, int rank, const
                 const uint32_t *box) {
     const EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t d[4], st[3];
-    cuuint32_t b[4], es[4];
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], es[5];
     for (int i = 0; i < rank; ++i) {
         d[i] = dims[i];
         b[i] = box[i];

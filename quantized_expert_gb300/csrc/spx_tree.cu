@@ -204,21 +204,16 @@ extern "C" int spx_tree_accept(const spx_tree_accept_args *a, spx_stream_t strea
     if (a->n_layers < 0 || (a->n_layers > 0 && (!a->layer_k || !a->layer_v))) return SPX_ERR_INVALID_ARG;
     if (a->n_layers > kMaxLayers) return SPX_ERR_UNSUPPORTED;
     AcceptParams p{};
-    for (int l = 0; l < a->n_layers; ++l) {
-        c.k = p.kv[2 * l] = a->layer_k[l];
-        c.v = p.kv[2 * l + 1] = a->layer_v[l];
-        const int st = kv_cache_check(&c);
-        if (st) return st;
-    }
-    if (a->n_layers == 0) {
-        c.k = c.v = reinterpret_cast<void *>(uintptr_t(16));  // stands for a buffer that is not used
-        const int st = kv_cache_check(&c);
-        if (st) return st;
-    }
-    // a buffer that is moved twice would be read after it was written
-    for (int i = 1; i < 2 * a->n_layers; ++i)
+    c.k = c.v = reinterpret_cast<void *>(uintptr_t(16));  // stands for a buffer: the layers' own are checked below
+    const int st = kv_cache_check(&c);
+    if (st) return st;
+    for (int i = 0; i < 2 * a->n_layers; ++i) {
+        void *const buf = i & 1 ? a->layer_v[i >> 1] : a->layer_k[i >> 1];
+        if (!buf || (reinterpret_cast<uintptr_t>(buf) & 15)) return SPX_ERR_INVALID_ARG;
         for (int j = 0; j < i; ++j)
-            if (p.kv[i] == p.kv[j]) return SPX_ERR_INVALID_ARG;
+            if (p.kv[j] == buf) return SPX_ERR_INVALID_ARG;  // moved twice, it would be read after it was written
+        p.kv[i] = buf;
+    }
     if (!a->q_start || !a->n_kept || !a->next || !a->lens_out || a->N < 0 || a->max_q < 0) return SPX_ERR_INVALID_ARG;
     if (a->N > 0 && (!a->parent || !a->token || !a->target || !a->path)) return SPX_ERR_INVALID_ARG;
     const size_t nb = (size_t)c.B * 4, nn = (size_t)a->N * 4;
