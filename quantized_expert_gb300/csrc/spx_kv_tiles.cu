@@ -54,7 +54,9 @@ struct Unit {
     int row0, T, len;    // the request
     int t0, h;           // first row (of the request), key head
     int n[2];            // tiles of X
-    int b, pad;
+    int b;
+    int before;          // tiles of the block before it
+    int tiles[2], units[2]; // of X before it: its tiles, units in which it has any
 };
 constexpr int kUnitRing = 4;
 struct Misc {
@@ -162,6 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.begin(p, share, p.span);
             int4 seam = make_int4(0, 0, 0, 0);
             int q_row = 0, q_head = 0;  // of the unit whose queries are to be copied next
+            int before = 0, tiles[2] = {0, 0}, units[2] = {0, 0};
             bool ok = true;
             for (uint32_t u = 0; ok; ++u) {
                 const bool more = w.left > 0;
@@ -178,7 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         n[x] = TALL ? min(max(all - w.tile, 0), parts) : (parts - x + 1) / 2;
                     }
                     if (lane == 0)
-                        m.unit[u % kUnitRing] = Unit{w.end, w.tile, w.whole(), w.rq.row0, w.rq.T, w.rq.len, t0, w.h, {n[0], n[1]}, w.b, 0};
+                        m.unit[u % kUnitRing] = Unit{w.end, w.tile, w.whole(), w.rq.row0, w.rq.T, w.rq.len, t0, w.h, {n[0], n[1]},
+                                                     w.b, before, {tiles[0], tiles[1]}, {units[0], units[1]}};
+                    before += parts;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        tiles[x] += n[x];
+                        units[x] += n[x] > 0;
+                    }
                     if (w.tile == 0 && w.end < w.nt)
                         seam = make_int4(row, min(w.rq.T - t0, p.span), w.h, (w.flat + w.nt - 1) / share.share);
                     w.next(p, p.span);
@@ -359,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = (warp - 4) >> 2, q = warp & 3, r = 32 * q + lane;
         const uint32_t quarter = (uint32_t)(32 * q) << 16;
         const uint32_t st = tmem + quarter + 128 * x, ot = tmem + quarter + 256;
-        const int t_of = p.by_group(r);
-        uint32_t tile = 0, before = 0, units = 0, units_o = 0;  // tiles of X, tiles of the block, units with tiles of X and of the other, so far
+        // (What a unit's end needs is read from its description there, and not held in registers beside a row's scores.)
         // (Warps that meet at barriers leave together: where one gave up, all hear of it.)
         bool ok = warp_wait(&m.ufull[0], 0, ctl);
         if (bar_any(2, 256, !ok)) ok = false;
@@ -368,13 +377,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t u = 0; ok; ++u) {
             const Unit &d = m.unit[u % kUnitRing];
             if (d.end == 0) break;
-            const int n = d.n[x], other = d.n[x ^ 1], first = d.tile;
-            const KvReq rq{d.row0, d.T, d.len};
-            const int t = d.t0 + (TALL ? x * p.tile_tokens : 0) + t_of;
-            const bool live = t_of < p.tile_tokens && t < rq.T, warp_live = __any_sync(0xffffffffu, live);
-            const KvSeen seen = kv_seen(p, rq, live ? t : rq.T);
-            const int all = kv_all_see(p, rq, d.t0);
+            const auto row_of = [&](int &t) {  // the thread's row of the request, and whether there is one
+                const int t_of = p.by_group(r);
+                t = d.t0 + (TALL ? x * p.tile_tokens : 0) + t_of;
+                return t_of < p.tile_tokens && t < d.T;
+            };
+            const int n = d.n[x], first = d.tile;
+            KvSeen seen;
+            int all;
+            bool warp_live;
+            {
+                int t;
+                const bool live = row_of(t);
+                const KvReq rq{d.row0, d.T, d.len};
+                warp_live = __any_sync(0xffffffffu, live);
+                seen = kv_seen(p, rq, live ? t : rq.T);
+                all = kv_all_see(p, rq, d.t0);
+            }
             float mr = -INFINITY, l = 0.f;
+            const uint32_t tile = d.tiles[x];
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 warp_wait(&m.sfull[x], (tile + i) & 1, ctl);
@@ -454,11 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // Of a tile that not every row sees whole, the values of tokens past the length, and of those that
                     // hold one which is not finite, become zeros, as a weight of 0 does not make them so; the rows
                     // that see such a token become NaNs at the end.  A token a thread.
-                    const uint32_t item = 2 * (before + li) + 1, slot = item % C::kRing;
+                    const uint32_t item = 2 * (d.before + li) + 1, slot = item % C::kRing;
                     warp_wait(&m.full[slot], (item / C::kRing) & 1, ctl);
                     uint8_t *row = ring + slot * C::kSlot + v_row<C::kPieces>(p.box_tokens, r, 0);
                     const int piece = p.box_tokens * 128;  // to the row's next 64 values
-                    bool zero = p0 + r >= rq.len;
+                    bool zero = p0 + r >= d.len;
                     if (!zero) {
                         uint32_t z = 0;
 #pragma unroll
@@ -490,9 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- the unit's end
-            const int parts = d.end - first;
-            if (n) warp_wait(&m.odone[x], units & 1, ctl);
-            if (other) warp_wait(&m.odone[x ^ 1], units_o & 1, ctl);
+            const int parts = d.end - first, other = d.n[x ^ 1];
+            if (n) warp_wait(&m.odone[x], d.units[x] & 1, ctl);
+            if (other) warp_wait(&m.odone[x ^ 1], d.units[x ^ 1] & 1, ctl);
             tc_fence_after();
             if (!TALL) m.ml[x][r] = make_float2(mr, l);
             __syncwarp();
@@ -525,10 +546,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // X = 1; else of its values), a warp's rows in a place of their own, so that stores are of whole rows and
             // not of 16 bytes of 32 rows.  Units of 16 bytes are permuted by the row.
             constexpr int kCols = TALL ? D : D / 2, kRow = kCols * 2, kU = kRow / 16;  // a warp's columns (else halves of D), bytes of a row
-            const uint32_t item = 2 * (before + parts - 1), k_slot = item % C::kRing, v_slot = (item + 1) % C::kRing;
+            const uint32_t item = 2 * (d.before + parts - 1), k_slot = item % C::kRing, v_slot = (item + 1) % C::kRing;
             const int c0 = TALL ? 0 : x * kCols;
             const size_t place = (size_t)(2 * blockIdx.x + (first == 0)) * C::kRows + (TALL ? 128 * x : 0) + 32 * q;
             if (warp_live) {
+                int t;
+                const bool live = row_of(t);
+                const KvReq rq{d.row0, d.T, d.len};
                 if (TALL) warp_wait(&m.full[k_slot], (item / C::kRing) & 1, ctl);  // (else it may hold another unit's by now)
                 warp_wait(&m.full[v_slot], ((item + 1) / C::kRing) & 1, ctl);
                 uint8_t *stage = ring + (TALL && x == 0 ? k_slot : v_slot) * C::kSlot + ((TALL ? 0 : 4 * x) + q) * 32 * kRow;
@@ -609,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (live && p.lse && (TALL || x == 0))
-                        p.lse[(int64_t)(rq.row0 + t) * p.heads + head0 + r - t_of * p.group] = kv_lse(mr, l);
+                        p.lse[(int64_t)(rq.row0 + t) * p.heads + head0 + r - p.by_group(r) * p.group] = kv_lse(mr, l);
                 } else {
                     float *dst = p.part + place * D + c0;
 #pragma unroll 1
@@ -644,10 +668,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (TALL) mbar_arrive(&m.empty[k_slot]);
                 mbar_arrive(&m.empty[v_slot]);
             }
-            tile += n;
-            before += parts;
-            units += n > 0;
-            units_o += other > 0;
         }
     }
     __syncwarp();
