@@ -23,7 +23,7 @@ namespace {
 constexpr int kThreads = 384;  // copies of K and V, two warps for products, copies of Q; 2 x 4 softmax warps
 constexpr int kPiece = kKvTile * 128;  // 128 rows of 64 values, 16 KB
 
-constexpr int kUnitCost = 3;  // tiles
+constexpr int kUnitCost = 4;  // tiles
 static_assert(kUnitCost <= kKvMostCost, "what the workspace's size is checked for");
 constexpr int kMostBoxes = kKvTile / 16;  // copies of 64 values of a tile's tokens, by the size of a page
 
