@@ -19,7 +19,9 @@ constexpr int kLayoutThreads = kKvMaxTree;
 // Block (request, 64 rows of it), a row a thread.  A row's mask is its own bit
 // and its parent's mask: after round r a row holds its nearest 2^r ancestors
 // and knows the next one, so six rounds do for 64 rows (a walk up the tree
-// takes as many dependent reads as the tree is deep).
+// takes as many dependent reads as the tree is deep).  One launch of a few dozen
+// bytes a row: bound by its own latency (1.4 us for 17 rows, 1.7 for 64 trees of
+// 64, replayed from a graph).
 __global__ void __launch_bounds__(kLayoutThreads) tree_layout_kernel(const __grid_constant__ LayoutParams p) {
     __shared__ uint64_t seen[2][kKvMaxTree];
     __shared__ int up[2][kKvMaxTree];
@@ -75,6 +77,8 @@ struct AcceptParams {
 // lane in registers, a vote a step; then a thread moves one unit of 16 bytes of
 // the path's rows, which ascend, so that a row is read before it is written
 // over.  Every block of a request takes the same walk rather than wait for one.
+// 24 layers of one request's 8 rows 3.1 us, its latency (walk, table, rows); 32
+// layers of 16 requests, 50 MB moved, 10.6 us, 4.7 TB/s.
 __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __grid_constant__ AcceptParams p) {
     __shared__ int way[kKvMaxTree], count, last_target;
     __shared__ int64_t from[kKvMaxTree], to[kKvMaxTree];
