@@ -378,6 +378,41 @@ def test_offsets_beyond_32_bits(t):
     check(s, *call(s))
 
 
+@pytest.mark.parametrize("page", [16, 80, 112, 256, 1024])
+@pytest.mark.parametrize("t,tree", [(1, False), (20, True), (300, False)])
+def test_page_sizes(page, t, tree):
+    s = make([t + 1100, t + 3], [t, t], heads=8, kv=2, page=page, tree=tree)
+    check(s, *call(s))
+    s = make([t + 5], [t], heads=5, kv=1, D=64, dtype=BF16, page=max(page, -(-(t + 5) // 16) * 16), tree=tree)  # one page holds all
+    check(s, *call(s))
+
+
+@pytest.mark.parametrize("t", [1, 6, 40])
+def test_long_caches(t):
+    s = make([150001, 70000], [t, t], heads=4, kv=1, D=64, dtype=BF16, page=128, tree=t > 1)
+    check(s, *call(s))
+
+
+def test_two_streams_with_a_workspace_each():
+    spx = _spx()
+    states = [make([3000] * 4, [t] * 4, heads=8, kv=2, dtype=BF16, tree=tree, seed=t) for t, tree in
+              ((1, False), (1, False), (64, True), (200, False))]
+    want = [call(s)[0] for s in states]
+    streams, calls = [torch.cuda.Stream() for _ in states], []
+    for s in states:
+        out = torch.zeros_like(s["q"])
+        ws = spx.new_kv_workspace(s["q"], s["cache"], s["max_q"], s["max_len"])
+        calls.append((spx.kv_attention_args(s["q"], s["cache"], s["q_start"], s["max_q"], s["max_len"], s["scale"], out, ws,
+                                            tree=mask_tensor(s)), out, ws))
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for stream, ((args, keep), out, ws) in zip(streams, calls):
+            spx.spx_kv_attention(args, stream)
+    torch.cuda.synchronize()
+    for ((args, keep), out, ws), w in zip(calls, want):
+        assert torch.equal(out, w) and spx.spx_workspace_status(ws) == 0
+
+
 def test_many_requests():
     g = torch.Generator().manual_seed(1)
     lens = torch.randint(0, 400, (1000,), generator=g).tolist()
