@@ -39,7 +39,6 @@ constexpr int kPiece = kKvTile * 128;  // 128 rows of 64 values, 16 KB
 // 56.2, 56.2.
 constexpr int kUnitCost = 4;
 static_assert(kUnitCost <= kKvMostCost, "what the workspace's size is checked for");
-constexpr int kMostBoxes = kKvTile / 16;  // copies of 64 values of a tile's tokens, by the size of a page
 
 struct KvMaps {
     CUtensorMap k;     // [page][head][token][D], boxes of 64 values x box_tokens
@@ -56,7 +55,8 @@ struct Tiles {
     static constexpr int kPieces = D / 64;
     static constexpr int kSlot = kPieces * kPiece;  // keys or values of a tile
     static constexpr int kQTiles = TALL ? 2 : 1;
-    static constexpr int kRing = (14 - kQTiles * kPieces) / kPieces;  // slots, keys and values of a tile in turn
+    // Slots, keys and values of a tile in turn; an even number where two warps fill them, so that each has its own.
+    static constexpr int kRing = (14 - kQTiles * kPieces) / kPieces & (TALL ? ~0 : ~1);
     static constexpr int kSmem = (kQTiles * kPieces + kRing * kPieces) * kPiece + 3072;
     static constexpr int kRows = kQTiles * kKvTileRows;  // rows of a unit
     static_assert(kSmem <= kSmemLimit && kRing >= 5, "shared memory of one block");
@@ -116,6 +116,12 @@ __device__ __forceinline__ int v_row(int box_tokens, int t, int c) {
     return (t & -box_tokens) * (128 * kPieces) + c * box_tokens * 128 + (t & (box_tokens - 1)) * 128;
 }
 
+// A softmax row takes 128 scores in registers: 168 a thread, what 384 threads
+// share out evenly, are too few (spills; prompt of 4096 tokens 127 us for XXX), so
+// the first four warps give up some (4 x 32 x 72 + 8 x 32 x 208 <= 384 x 168).
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+
 // ctl_wait by a whole warp, converged behind it: loads of tensor memory and
 // barriers take a warp as one, and lanes may leave the wait apart.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtl &c) {
@@ -156,19 +162,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 2) (&m.bad[0][0][0])[lane] = 0;
-    griddep_wait();
-    griddep_launch_dependents();
+    if (warp == 0 && elect_one()) {
+        prefetch_tmap(&maps.k);
+        prefetch_tmap(&maps.v);
+        prefetch_tmap(&maps.q);
+    }
     if (warp == 1) {
         tmem_alloc(&m.tmem, 512);
         tmem_relinquish();
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m.tmem;
     const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_KV};
+    griddep_wait();
+    griddep_launch_dependents();
 
     if (warp < 4) {
+        fewer_registers();
         if (warp == 3) {
             // ---- the share's units, one ahead of the copies of their queries; the unit that begins in this share and
             // ends in a later one, for the join launch
@@ -227,11 +240,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!more) break;
             }
             if (lane == 0) p.seams[blockIdx.x] = seam;
-        } else if (warp == 0) {
-            // ---- copies: keys and values of the tiles in turn
+        } else if (warp == 0 || (!TALL && warp == 2)) {
+            // ---- copies: keys and values of the tiles in turn; where a warp is to spare, the values by that one, as a
+            // short call waits for both
             const uint64_t pol = policy_evict_normal();
-            const int bt = p.box_tokens, boxes = kKvTile / bt, box = lane % boxes;
+            // (a lane a copy: keys lane % boxes, 64 values lane / boxes; values lane)
+            const int bt = p.box_tokens, boxes = kKvTile / bt, box = lane % boxes, piece = lane / boxes;
+            // (a single request's table comes nearer while its share is looked for)
+            if (p.B == 1 && 32 * lane < p.max_pages)
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(p.table + 32 * lane) : "memory");
             Place<C::kRing> r;
+            const int kv0 = TALL ? 0 : warp >> 1, kv1 = TALL ? 2 : kv0 + 1;
+            r.advance(kv0);
             bool ok = true;
             for (uint32_t u = 0; ok; ++u) {
                 if (!(ok = ctl_wait(&m.ufull[u % kUnitRing], (u / kUnitRing) & 1, ctl))) break;
@@ -251,35 +271,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int p0 = kKvTile * j + bt * box, at = p0 - p.by_page(p0) * p.page_size;
                     const int page = next < 0 || next >= p.num_pages ? p.num_pages : next;  // (past the last one: zeros)
                     if (j + 1 < end) look_up(j + 1);
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, r.advance(1)) {
+#pragma unroll 1
+                    for (int kv = kv0; kv < kv1; ++kv, r.advance(TALL ? 1 : 2)) {
                         if (!(ok = ctl_wait(&m.empty[r.i], r.phase ^ 1, ctl))) break;
                         if (elect_one()) mbar_arrive_expect_tx(&m.full[r.i], C::kSlot);
                         __syncwarp();
                         uint8_t *dst = ring + r.i * C::kSlot;
-#pragma unroll
-                        for (int i = 0; i < kMostBoxes; i += 2) {
-                            if (i >= boxes) break;
-                            const int a = __shfl_sync(0xffffffffu, at, i), g = __shfl_sync(0xffffffffu, page, i);
-                            const int a1 = __shfl_sync(0xffffffffu, at, i + 1), g1 = __shfl_sync(0xffffffffu, page, i + 1);
-                            if (elect_one()) {
-                                uint8_t *to = dst + i * bt * 128;
-                                if (kv) {
-                                    to = dst + i * bt * 128 * C::kPieces;
-                                    tma_load_5d(to, &maps.v, 0, a, 0, h, g, &m.full[r.i], pol);
-                                    if (i + 1 < boxes)
-                                        tma_load_5d(to + bt * 128 * C::kPieces, &maps.v, 0, a1, 0, h, g1, &m.full[r.i], pol);
-                                } else {
-#pragma unroll
-                                    for (int c = 0; c < C::kPieces; ++c) {
-                                        tma_load_4d(to + c * kPiece, &maps.k, 64 * c, a, h, g, &m.full[r.i], pol);
-                                        if (i + 1 < boxes)
-                                            tma_load_4d(to + c * kPiece + bt * 128, &maps.k, 64 * c, a1, h, g1, &m.full[r.i], pol);
-                                    }
-                                }
-                            }
-                            __syncwarp();
+                        if (kv) {
+                            if (lane < boxes)
+                                tma_load_5d(dst + box * bt * 128 * C::kPieces, &maps.v, 0, at, 0, h, page, &m.full[r.i], pol);
+                        } else if (lane < boxes * C::kPieces) {
+                            tma_load_4d(dst + piece * kPiece + box * bt * 128, &maps.k, 64 * piece, at, h, page, &m.full[r.i], pol);
                         }
+                        __syncwarp();
                     }
                 }
             }
@@ -318,7 +322,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&m.uempty[u % kUnitRing]);
                 if (end == 0) break;
-                if (!TALL && warp == 2) continue;
                 Place<C::kRing> kr = at, vr = at;
                 vr.advance(1);
                 ok = ctl_wait(&m.qfull, u & 1, ctl);
@@ -379,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
+        more_registers();
         // ---- softmax and results: a row a thread
         const int x = (warp - 4) >> 2, q = warp & 3, r = 32 * q + lane;
         const uint32_t quarter = (uint32_t)(32 * q) << 16;
@@ -412,10 +416,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t tile = d.tiles[x];
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
-                warp_wait(&m.sfull[x], (tile + i) & 1, ctl);
-                tc_fence_after();
                 const int li = TALL ? i : 2 * i + x, j = first + li, p0 = kKvTile * j;
                 const bool masked = p0 + kKvTile > all;
+                warp_wait(&m.sfull[x], (tile + i) & 1, ctl);
+                tc_fence_after();
+                if (masked) {
+                    // Of a tile that not every row sees whole, the values of tokens past the length, and of those that
+                    // hold one which is not finite, become zeros, as a weight of 0 does not make them so; the rows
+                    // that see such a token become NaNs at the end.  A token a thread.  (Not before the scores are there: only
+                    // then is the slot's last use known to be over, and the wait's parity that of this use.)
+                    const uint32_t item = 2 * (d.before + li) + 1, slot = item % C::kRing;
+                    warp_wait(&m.full[slot], (item / C::kRing) & 1, ctl);
+                    uint8_t *row = ring + slot * C::kSlot + v_row<C::kPieces>(p.box_tokens, r, 0);
+                    const int piece = p.box_tokens * 128;  // to the row's next 64 values
+                    bool zero = p0 + r >= d.len;
+                    if (!zero) {
+                        uint32_t z = 0;
+#pragma unroll
+                        for (int k = 0; k < 8 * C::kPieces; ++k) {
+                            const uint4 v = lds128(row + (k >> 3) * piece + (((k ^ r) & 7) << 4));
+                            z = Elem<DT>::fma2(v.x, 0u, z);
+                            z = Elem<DT>::fma2(v.y, 0u, z);
+                            z = Elem<DT>::fma2(v.z, 0u, z);
+                            z = Elem<DT>::fma2(v.w, 0u, z);
+                        }
+                        if (z & 0x7FFF7FFFu) {
+                            zero = true;
+                            atomicOr(&m.bad[u & 1][j & 3][r >> 5], 1u << (r & 31));
+                        }
+                    }
+                    if (zero)
+#pragma unroll
+                        for (int k = 0; k < 8 * C::kPieces; ++k)
+                            *reinterpret_cast<uint4 *>(row + (k >> 3) * piece + (((k ^ r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
                 if (warp_live) {
                     uint32_t s[128];
 #pragma unroll
@@ -472,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             o[k] = Elem<DT>::down2(a, b);  // rounded for the tensor cores; the weights' own sum is not
                         }
                         tmem_st16(st + 16 * c, o);  // over S, which is in registers
-                        if ((c & 1) && !masked) {
+                        if (c & 1) {
                             tmem_wait_st();
                             tc_fence_before();
                             __syncwarp();
@@ -481,47 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float2 la = unpack2(add2(l2[0], l2[1]));
                     l += la.x + la.y;
-                } else if (!masked && lane == 0) {
+                } else if (lane == 0) {
                     mbar_arrive(&m.pfull[x][0]);
                     mbar_arrive(&m.pfull[x][1]);
-                }
-                if (masked) {
-                    // Of a tile that not every row sees whole, the values of tokens past the length, and of those that
-                    // hold one which is not finite, become zeros, as a weight of 0 does not make them so; the rows
-                    // that see such a token become NaNs at the end.  A token a thread.
-                    const uint32_t item = 2 * (d.before + li) + 1, slot = item % C::kRing;
-                    warp_wait(&m.full[slot], (item / C::kRing) & 1, ctl);
-                    uint8_t *row = ring + slot * C::kSlot + v_row<C::kPieces>(p.box_tokens, r, 0);
-                    const int piece = p.box_tokens * 128;  // to the row's next 64 values
-                    bool zero = p0 + r >= d.len;
-                    if (!zero) {
-                        uint32_t z = 0;
-#pragma unroll
-                        for (int k = 0; k < 8 * C::kPieces; ++k) {
-                            const uint4 v = lds128(row + (k >> 3) * piece + (((k ^ r) & 7) << 4));
-                            z = Elem<DT>::fma2(v.x, 0u, z);
-                            z = Elem<DT>::fma2(v.y, 0u, z);
-                            z = Elem<DT>::fma2(v.z, 0u, z);
-                            z = Elem<DT>::fma2(v.w, 0u, z);
-                        }
-                        if (z & 0x7FFF7FFFu) {
-                            zero = true;
-                            atomicOr(&m.bad[u & 1][j & 3][r >> 5], 1u << (r & 31));
-                        }
-                    }
-                    if (zero)
-#pragma unroll
-                        for (int k = 0; k < 8 * C::kPieces; ++k)
-                            *reinterpret_cast<uint4 *>(row + (k >> 3) * piece + (((k ^ r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&m.pfull[x][0]);
-                        mbar_arrive(&m.pfull[x][1]);
-                    }
                 }
             }
             // ---- the unit's end
