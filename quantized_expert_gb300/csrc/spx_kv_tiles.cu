@@ -16,10 +16,10 @@
 // 256 rows and 128 keys 2 x (512 + 256) cycles of products (S takes both operands
 // from shared memory, 128 bytes a cycle; P V one) against 2600 measured.  16384
 // tokens, 32 heads: 1.6 PFLOP/s; a unit's beginning and end cost what four tiles
-// take, so that shorter prompts run at less (4096 tokens 122 us, 1.13 PFLOP/s;
-// four chunks of up to 1021 tokens behind up to 6007, pages of 16, 149 us).
-// Trees of 64 rows, 16 requests of up to 3001 tokens and 16 heads: 56.2 us, 4.5
-// TB/s, of which 48 in the attention launch beyond its first copies.
+// take, so that shorter prompts run at less (4096 tokens 124 us, 1.11 PFLOP/s;
+// four chunks of up to 1021 tokens behind up to 6007, pages of 16, 147 us).
+// Trees of 64 rows, 16 requests of up to 3001 tokens and 16 heads: 52.5 us, 4.8
+// TB/s.
 #include <math.h>
 #include <string.h>
 
@@ -117,8 +117,9 @@ __device__ __forceinline__ int v_row(int box_tokens, int t, int c) {
 }
 
 // A softmax row takes 128 scores in registers: 168 a thread, what 384 threads
-// share out evenly, are too few (spills; prompt of 4096 tokens 127 us for XXX), so
-// the first four warps give up some (4 x 32 x 72 + 8 x 32 x 208 <= 384 x 168).
+// share out evenly, are too few, so the first four warps give up some (4 x 32 x
+// 72 + 8 x 32 x 208 <= 384 x 168; trees of 16 requests 55.2 us, with it 53.5, of
+// one 15.7, 15.05; prompts within 1%).
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
 
@@ -289,8 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else {
             // ---- products: O_X of X's last tile, then S_X of its next one, in one stretch behind everything that they
-            // wait for.  TALL: a warp for each X, which pass a turn to each other; else the first for both, as two that
-            // hand in products at will are more than the order of the tiles needs.
+            // wait for.  TALL: a warp for each X, which pass a turn to each other and both see every slot.  Else the first
+            // for both: a warp that saw only every second tile could wait for a slot before its last use, by the other,
+            // had landed, and take the use before that, of the same parity, for the one that it waits for.
             const uint32_t fmt = DT == SPX_BF16 ? kIdescBf16 : 0u;
             const uint32_t id_s = idesc_f16_f32(128, 128) | fmt, id_o = idesc_f16_f32(128, D) | fmt | kIdescBMn;
             const uint64_t qd = sw128_desc(smem_u32(qs)), kd = sw128_desc(smem_u32(ring));
