@@ -39,6 +39,7 @@ constexpr int kPiece = kKvTile * 128;  // 128 rows of 64 values, 16 KB
 // 56.2, 56.2.
 constexpr int kUnitCost = 4;
 static_assert(kUnitCost <= kKvMostCost, "what the workspace's size is checked for");
+constexpr int kMiscBytes = 3 << 10;  // of a block's shared memory, behind the tiles
 
 struct KvMaps {
     CUtensorMap k;     // [page][head][token][D], boxes of 64 values x box_tokens
@@ -57,7 +58,7 @@ struct Tiles {
     static constexpr int kQTiles = TALL ? 2 : 1;
     // Slots, keys and values of a tile in turn; an even number where two warps fill them, so that each has its own.
     static constexpr int kRing = (14 - kQTiles * kPieces) / kPieces & (TALL ? ~0 : ~1);
-    static constexpr int kSmem = (kQTiles * kPieces + kRing * kPieces) * kPiece + 3072;
+    static constexpr int kSmem = (kQTiles * kPieces + kRing * kPieces) * kPiece + kMiscBytes;
     static constexpr int kRows = kQTiles * kKvTileRows;  // rows of a unit
     static_assert(kSmem <= kSmemLimit && kRing >= 5, "shared memory of one block");
 };
@@ -86,7 +87,7 @@ struct Misc {
     alignas(16) uint32_t bad[2][4][4];   // tokens with values that are not finite, in the last four tiles of a unit
     float2 ml[2][kKvTileRows];           // X's references and weights
 };
-static_assert(sizeof(Misc) <= 3072, "the misc area holds it");
+static_assert(sizeof(Misc) <= kMiscBytes, "the misc area holds it");
 
 // A place in the ring and the parity of its use.
 template <int N>
@@ -208,9 +209,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int all = last < first ? 0 : (kv_none_see(p, w.rq, last) + kKvTile - 1) / kKvTile;
                         n[x] = TALL ? min(max(all - w.tile, 0), parts) : (parts - x + 1) / 2;
                     }
-                    if (lane == 0)
+                    if (lane == 0) {
                         m.unit[u % kUnitRing] = Unit{w.end, w.tile, w.whole(), w.rq.row0, w.rq.T, w.rq.len, t0, w.h, {n[0], n[1]},
                                                      w.b, before, {tiles[0], tiles[1]}, {units[0], units[1]}};
+                        mbar_arrive(&m.ufull[u % kUnitRing]);
+                    }
                     before += parts;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -222,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w.next(p, p.span);
                 } else if (lane == 0) {
                     m.unit[u % kUnitRing].end = 0;
+                    mbar_arrive(&m.ufull[u % kUnitRing]);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&m.ufull[u % kUnitRing]);
                 if (u > 0) {
                     if (!(ok = ctl_wait(&m.qempty, (u & 1), ctl))) break;  // of the unit before the last
                     if (elect_one()) {

@@ -61,7 +61,8 @@ __global__ void __launch_bounds__(kLayoutThreads) tree_layout_kernel(const __gri
 
 // -------------------------------------------------------------------- accept --
 constexpr int kMaxLayers = 128;
-constexpr int kAcceptThreads = 256;
+constexpr int kAcceptThreads = 128;
+template <int M>  // room for the buffers of M / 2 layers
 struct AcceptParams {
     int64_t page_stride, token_stride, head_stride;
     int num_pages, page_size, kv_heads, units, max_pages;  // units of 8 values of a head
@@ -70,16 +71,18 @@ struct AcceptParams {
     FastDiv by_page, by_units, by_heads;
     const int32_t *q_start, *parent, *token, *target;
     int32_t *n_kept, *path, *next, *lens_out;
-    void *kv[2 * kMaxLayers];  // of layer l: keys 2l, values 2l + 1
+    void *kv[M];  // of layer l: keys 2l, values 2l + 1
 };
 
-// Block (request, 256 columns): its first warp walks down the tree, two rows a
+// Block (request, 128 columns): its first warp walks down the tree, two rows a
 // lane in registers, a vote a step; then a thread moves one unit of 16 bytes of
 // the path's rows, which ascend, so that a row is read before it is written
 // over.  Every block of a request takes the same walk rather than wait for one.
 // 24 layers of one request's 8 rows 3.1 us, its latency (walk, table, rows); 32
-// layers of 16 requests, 50 MB moved, 10.6 us, 4.7 TB/s.
-__global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __grid_constant__ AcceptParams p) {
+// layers of 16 requests, 50 MB moved, 9.0 us, 5.6 TB/s (rows 8 at a time 10.6, 16
+// at a time 9.5, and in blocks of 128 threads for 256 9.0).
+template <int M>
+__global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __grid_constant__ AcceptParams<M> p) {
     __shared__ int way[kKvMaxTree], count, last_target;
     __shared__ int64_t from[kKvMaxTree], to[kKvMaxTree];
     griddep_wait();
@@ -147,7 +150,7 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
     if (c >= p.columns) return;
     const int head = p.by_units(c), unit = c - head * p.units, x = p.by_heads(head), h = head - x * p.kv_heads;
     uint16_t *buf = static_cast<uint16_t *>(p.kv[x]) + (int64_t)h * p.head_stride + 8 * unit;
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     for (int d0 = 1; d0 < n; d0 += kAhead) {
         uint4 v[kAhead];
 #pragma unroll
@@ -179,6 +182,47 @@ bool any_overlap(const Span (&in)[I], const Span (&out)[O]) {
     return false;
 }
 
+template <int M>
+int launch_accept(const spx_tree_accept_args &a, const spx_kv_cache &c, cudaStream_t s) {
+    AcceptParams<M> p{};
+    for (int i = 0; i < 2 * a.n_layers; ++i) {
+        p.kv[i] = i & 1 ? a.layer_v[i >> 1] : a.layer_k[i >> 1];
+        for (int j = 0; j < i; ++j)
+            if (p.kv[j] == p.kv[i]) return SPX_ERR_INVALID_ARG;  // moved twice, it would be read after it was written
+    }
+    p.page_stride = c.page_stride;
+    p.token_stride = c.token_stride;
+    p.head_stride = c.head_stride;
+    p.num_pages = c.num_pages;
+    p.page_size = c.page_size;
+    p.kv_heads = c.kv_heads;
+    p.units = c.D / 8;
+    p.max_pages = c.max_pages;
+    p.table = c.block_table;
+    p.lens = c.lens;
+    p.N = a.N;
+    p.max_q = a.max_q;
+    p.by_page.set(c.page_size);
+    p.by_units.set(p.units);
+    p.by_heads.set(c.kv_heads);
+    p.q_start = a.q_start;
+    p.parent = a.parent;
+    p.token = a.token;
+    p.target = a.target;
+    p.n_kept = a.n_kept;
+    p.path = a.path;
+    p.next = a.next;
+    p.lens_out = a.lens_out;
+    const long long columns = 2ll * a.n_layers * c.kv_heads * p.units;
+    const long long groups = columns ? (columns + kAcceptThreads - 1) / kAcceptThreads : 1;
+    if (groups > 65535) return SPX_ERR_UNSUPPORTED;
+    p.columns = (int)columns;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = latent_config(dim3((unsigned)c.B, (unsigned)groups), kAcceptThreads, 0,
+                                           s, attr, 1);
+    return record_launch(cudaLaunchKernelEx(&cfg, tree_accept_kernel<M>, p));
+}
+
 }  // namespace
 
 }  // namespace spx
@@ -207,16 +251,12 @@ extern "C" int spx_tree_accept(const spx_tree_accept_args *a, spx_stream_t strea
     spx_kv_cache c = *a->cache;
     if (a->n_layers < 0 || (a->n_layers > 0 && (!a->layer_k || !a->layer_v))) return SPX_ERR_INVALID_ARG;
     if (a->n_layers > kMaxLayers) return SPX_ERR_UNSUPPORTED;
-    AcceptParams p{};
     c.k = c.v = reinterpret_cast<void *>(uintptr_t(16));  // stands for a buffer: the layers' own are checked below
     const int st = kv_cache_check(&c);
     if (st) return st;
     for (int i = 0; i < 2 * a->n_layers; ++i) {
-        void *const buf = i & 1 ? a->layer_v[i >> 1] : a->layer_k[i >> 1];
+        const void *const buf = i & 1 ? a->layer_v[i >> 1] : a->layer_k[i >> 1];
         if (!buf || (reinterpret_cast<uintptr_t>(buf) & 15)) return SPX_ERR_INVALID_ARG;
-        for (int j = 0; j < i; ++j)
-            if (p.kv[j] == buf) return SPX_ERR_INVALID_ARG;  // moved twice, it would be read after it was written
-        p.kv[i] = buf;
     }
     if (!a->q_start || !a->n_kept || !a->next || !a->lens_out || a->N < 0 || a->max_q < 0) return SPX_ERR_INVALID_ARG;
     if (a->N > 0 && (!a->parent || !a->token || !a->target || !a->path)) return SPX_ERR_INVALID_ARG;
@@ -226,35 +266,7 @@ extern "C" int spx_tree_accept(const spx_tree_accept_args *a, spx_stream_t strea
     const Span out[] = {{a->n_kept, nb}, {a->path, nn}, {a->next, nb}, {a->lens_out, nb}};
     if (any_overlap(in, out)) return SPX_ERR_INVALID_ARG;
     if (a->max_q > kKvMaxTree) return SPX_ERR_UNSUPPORTED;
-    p.page_stride = c.page_stride;
-    p.token_stride = c.token_stride;
-    p.head_stride = c.head_stride;
-    p.num_pages = c.num_pages;
-    p.page_size = c.page_size;
-    p.kv_heads = c.kv_heads;
-    p.units = c.D / 8;
-    p.max_pages = c.max_pages;
-    p.table = c.block_table;
-    p.lens = c.lens;
-    p.N = a->N;
-    p.max_q = a->max_q;
-    p.by_page.set(c.page_size);
-    p.by_units.set(p.units);
-    p.by_heads.set(c.kv_heads);
-    p.q_start = a->q_start;
-    p.parent = a->parent;
-    p.token = a->token;
-    p.target = a->target;
-    p.n_kept = a->n_kept;
-    p.path = a->path;
-    p.next = a->next;
-    p.lens_out = a->lens_out;
-    const long long columns = 2ll * a->n_layers * c.kv_heads * p.units;
-    const long long groups = columns ? (columns + kAcceptThreads - 1) / kAcceptThreads : 1;
-    if (groups > 65535) return SPX_ERR_UNSUPPORTED;
-    p.columns = (int)columns;
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = latent_config(dim3((unsigned)c.B, (unsigned)groups), kAcceptThreads, 0,
-                                           reinterpret_cast<cudaStream_t>(stream), attr, 1);
-    return record_launch(cudaLaunchKernelEx(&cfg, tree_accept_kernel, p));
+    // (kernel parameters are copied with every launch: room for as many layers as usual, or for the most)
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return a->n_layers <= 32 ? launch_accept<64>(*a, c, s) : launch_accept<2 * kMaxLayers>(*a, c, s);
 }
