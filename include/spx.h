@@ -725,12 +725,13 @@ SPX_API int spx_kv_append(const spx_kv_append_args *args, spx_stream_t stream);
  *   p < lens[b] - T, and lens[b] - T + j for every bit j < T of its mask (tree
  *     != NULL; causal is ignored; max_q <= 64);
  *   out = sum_p softmax(scale * q . k_p) v_p,  lse = log sum_p exp(scale * q . k_p).
- * A row that sees nothing gives out = 0 and lse = -inf.  A position that holds
- * an infinity or a NaN reaches only the rows that see it (an infinite or NaN
- * value in at least its own column of out).  max_len bounds every request's
+ * A row that sees nothing, or whose every score is -inf, gives out = 0 and lse =
+ * -inf.  A position that holds an infinity or a NaN reaches only the rows that
+ * see it (one among its values, at least that column of out).  max_len bounds every request's
  * length (longer ones are cut to it).  Softmax weights are rounded to the type
  * before they meet the values; every sum is fp32.  out lies apart from what is
- * read.  Calls with one workspace must not run at the same time. */
+ * read.  Calls with one workspace must not run at the same time.  Block tables
+ * and max_len that both go beyond 2^31 - 2^16 tokens are SPX_ERR_UNSUPPORTED. */
 typedef struct {
     const spx_kv_cache *cache;
     int N, heads;                /* heads a multiple of kv_heads, at most 64 to one key head */
@@ -738,7 +739,7 @@ typedef struct {
     int64_t q_stride, out_stride;/* elements from row to row, multiples of 8 */
     const int32_t *q_start;      /* [B + 1], ascending from 0 on */
     int max_q, max_len;
-    float scale;                 /* finite and above 0 */
+    float scale;                 /* above 0, below 2.3e38 */
     int causal;
     const uint64_t *tree;        /* [N] masks as of spx_tree_layout, or NULL */
     void *out;                   /* [N][heads][D], 16-byte aligned */
@@ -763,8 +764,9 @@ SPX_API size_t spx_kv_workspace_size(int B, int N, int max_q, int max_len, int h
  *   q_start[b] + d] is the d-th of them, -1 from n_kept[b] on; next[b] = target
  *   of the last one (-1 without rows); lens_out[b] = lens[b] - T + n_kept[b].
  * In each of the n_layers caches, which share cache's layout, block table and
- * lens and have buffers of their own, the keys and values of the path's d-th row are moved to token lens[b] -
- * T + d.  layer_k and layer_v are host arrays of device pointers. */
+ * lens and have buffers of their own, the keys and values of the path's d-th row
+ * are moved to token lens[b] - T + d.  layer_k and layer_v are host arrays of
+ * device pointers. */
 typedef struct {
     const spx_kv_cache *cache;   /* its k and v are not used */
     int n_layers;                /* 0 to 128; 0: nothing is moved */

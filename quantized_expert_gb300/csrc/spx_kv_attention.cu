@@ -503,6 +503,9 @@ int place_rows(long long tokens, int group) {
     return tokens * group <= kFewRows ? kFewRows : tokens <= kv_tile_tokens(group) ? kKvTileRows : 2 * kKvTileRows;
 }
 
+// Tokens of a request at most: positions rounded up to a tile behind the rows of a unit are counted in 31 bits too.
+constexpr int kMostLen = 0x7fff0000;
+
 constexpr size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 constexpr size_t kDoneOffset = sizeof(WsHeader);
 static_assert(kDoneOffset + kKvMaxBlocks * 4 <= SPX_KV_WORKSPACE_ZERO, "what must start at zero");
@@ -607,7 +610,8 @@ int kv_cache_check(const spx_kv_cache *c) {
             if (!done[i] && (next < 0 || st[i] < st[next])) next = i;
         if (next < 0) break;
         if (st[next] < span) return SPX_ERR_INVALID_ARG;
-        if (st[next] >= (int64_t)1 << 38) return SPX_ERR_UNSUPPORTED;
+        // (2^47 bytes, more than any device holds: sums of these stay within 64 bits, and strides within a tensor map's)
+        if (st[next] >= (int64_t)1 << 38 || n[next] > ((int64_t)1 << 46) / st[next]) return SPX_ERR_UNSUPPORTED;
         span += (n[next] - 1) * st[next];
         done[next] = true;
     }
@@ -635,7 +639,8 @@ extern "C" int spx_kv_attention(const spx_kv_attention_args *a, spx_stream_t str
     const spx_kv_cache &c = *a->cache;
     if (!a->q_start || a->N < 0 || a->heads < 1 || a->max_q < 0 || a->max_len < 0 || a->heads % c.kv_heads)
         return SPX_ERR_INVALID_ARG;
-    if (!(a->scale > 0.f) || !(a->scale < INFINITY)) return SPX_ERR_INVALID_ARG;
+    const float scale_log2 = a->scale * 1.4426950408889634f;
+    if (!(a->scale > 0.f) || !(scale_log2 < INFINITY)) return SPX_ERR_INVALID_ARG;
     if (a->N > 0 && (!a->q || !a->out)) return SPX_ERR_INVALID_ARG;
     const int64_t w = (int64_t)a->heads * c.D;
     if (!al16(a->q) || !al16(a->out) || a->q_stride < w || a->out_stride < w || a->q_stride % 8 || a->out_stride % 8)
@@ -665,6 +670,7 @@ extern "C" int spx_kv_attention(const spx_kv_attention_args *a, spx_stream_t str
     p.max_q = a->max_q;
     const long long held = (long long)c.max_pages * c.page_size;
     p.max_len = a->max_len < held ? a->max_len : (int)held;
+    if (p.max_len > kMostLen) return SPX_ERR_UNSUPPORTED;
     p.causal = a->causal != 0;
     p.by_group.set(p.group);
     p.by_page.set(c.page_size);
@@ -675,7 +681,7 @@ extern "C" int spx_kv_attention(const spx_kv_attention_args *a, spx_stream_t str
     p.q = static_cast<const uint16_t *>(a->q);
     p.out = static_cast<uint16_t *>(a->out);
     p.lse = a->lse;
-    p.scale_log2 = a->scale * 1.4426950408889634f;
+    p.scale_log2 = scale_log2;
     p.hdr = static_cast<WsHeader *>(a->ws);
     p.budget = a->wait_budget_ns ? a->wait_budget_ns : 2000000000ull;
     const int tokens = a->max_q < a->N ? a->max_q : a->N;

@@ -211,3 +211,20 @@ def test_workspace_sizes(lib):
         now = size(2, n, n, 8000, 32, 8)
         assert now >= last
         last = now
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(scale=3e38), INV),  # its product with log2(e) is infinite
+    (dict(max_len=0x7fffffff), UNS), (dict(max_len=0x7fff0001), UNS)])
+def test_attention_beyond_what_is_counted(lib, bad, status):
+    c = cache(max_pages=1 << 25)  # 2^31 tokens
+    assert lib.spx_kv_attention(C.byref(attention(c, N=1, max_q=1, tree=None, **bad)), None) == status
+
+
+@pytest.mark.parametrize("bad", [dict(num_pages=0x7fffffff, page_stride=1 << 37), dict(token_stride=1 << 30, num_pages=1 << 20,
+                                                                                       page_stride=1 << 36)])
+def test_caches_larger_than_any_memory(lib, bad):
+    c = cache(**bad)
+    assert lib.spx_kv_attention(C.byref(attention(c)), None) == UNS
+    assert lib.spx_kv_append(C.byref(append(c)), None) == UNS
+    assert lib.spx_tree_accept(C.byref(accept(c)), None) == UNS
