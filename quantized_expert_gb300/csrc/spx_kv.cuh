@@ -37,8 +37,9 @@ struct KvParams {
     uint32_t *done;    // [blocks] parts of the unit that begins in a block and ends in a later one; zero between calls
     float2 *ml;        // [2 blocks][rows] reference and weight of a partial sum's row
     float *part;       // [2 blocks][rows][D] partial sums
-    int4 *seams;       // [blocks] of the unit that begins in a block and ends in a later one: its first row, its rows, key
-                       // head and last block (rows 0: none)
+    int4 *seams;       // of a unit that crosses from block to block: its first row, its rows, key head, and its first block
+                       // << 16 | its last (the same block: it does not)
+    int seam_groups;   // above 0: one for each unit, this many to a request and key head; 0: one for each block
     int span;          // rows (tokens) of a unit
     int unit_cost;     // of a unit beside its tiles, in tiles
     int tile_tokens;   // rows (tokens) of a product of 128 (token, head) rows
@@ -305,17 +306,18 @@ __device__ __forceinline__ float kv_factor(float m, float common) {
 }
 // One warp: a row's sum over the parts `first`, first + step and so on of the
 // blocks c0 .. c1, in their order, under the reference of them all.  r: row of a
-// place, of which there are `rows`.  Sums are read eight parts at a time, the
-// first ones with the references and weights (a part a lane, 32 at a time) and
-// not behind them: what a row costs is the time of one read after the other.
+// place, of which there are `rows`.  Sums are read kAhead parts at a time (a
+// divisor of 32), the first ones with the references and weights (a part a lane,
+// 32 at a time) and not behind them: what a row costs is the time of one read
+// after the other.
 template <int D>
 struct KvSum {
     static constexpr int kPer = D / 32;
     float m, l, v[kPer];  // v: the lane's values
 };
-template <int D>
+template <int D, int kAhead = 8>
 __device__ __forceinline__ KvSum<D> kv_sum_parts(const KvParams &p, int c0, int c1, int first, int step, int rows, int r, int lane) {
-    constexpr int kPer = D / 32, kAhead = 8;
+    constexpr int kPer = D / 32;
     KvSum<D> s;
     const auto place = [&](int k) { return (size_t)(2 * k + (k == c0)) * rows + r; };
     const int n = (c1 - c0 - first) / step + 1;  // (first <= c1 - c0)

@@ -17,9 +17,9 @@
 // from shared memory, 128 bytes a cycle; P V one) against 2600 measured.  16384
 // tokens, 32 heads: 1.6 PFLOP/s; a unit's beginning and end cost what four tiles
 // take, so that shorter prompts run at less (4096 tokens 124 us, 1.11 PFLOP/s;
-// four chunks of up to 1021 tokens behind up to 6007, pages of 16, 147 us).
-// Trees of 64 rows, 16 requests of up to 3001 tokens and 16 heads: 52.5 us, 4.8
-// TB/s.
+// four chunks of up to 1021 tokens behind up to 6007, pages of 16, 146 us).
+// Trees of 64 rows, 16 requests of up to 3001 tokens and 16 heads: 53 us, 4.8
+// TB/s; 17 rows, one request of 4113 tokens and 8 key heads: 12.6 us.
 #include <math.h>
 #include <string.h>
 
@@ -132,6 +132,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
     return ok;
 }
 
+// (four chunks as above 147.2 us, with it 146.6)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Values loaded from tensor memory are used behind this only: nothing else keeps
+// arithmetic on them behind the wait.
+template <int N>
+__device__ __forceinline__ void hold(uint32_t (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                          "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
 template <int DT, int D, bool TALL>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_tiles_kernel(const __grid_constant__ KvParams p, const __grid_constant__ KvMaps maps) {
@@ -191,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const KvShare share = kv_find_share(p, p.span, lane);
             KvWalk w;
             w.begin(p, share, p.span);
-            int4 seam = make_int4(0, 0, 0, 0);
+            int4 seam = make_int4(0, 0, 0, 0);  // where there is one for each block
             int q_row = 0, q_head = 0;  // of the unit whose queries are to be copied next
             int before = 0, tiles[2] = {0, 0}, units[2] = {0, 0};
             bool ok = true;
@@ -220,8 +237,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tiles[x] += n[x];
                         units[x] += n[x] > 0;
                     }
-                    if (w.tile == 0 && w.end < w.nt)
-                        seam = make_int4(row, min(w.rq.T - t0, p.span), w.h, (w.flat + w.nt - 1) / share.share);
+                    if (w.tile == 0) {
+                        const bool cut = w.end < w.nt;
+                        const int4 s = make_int4(row, min(w.rq.T - t0, p.span), w.h,
+                                                 cut ? (int)blockIdx.x << 16 | (w.flat + w.nt - 1) / share.share : 0);
+                        if (cut) seam = s;
+                        if (p.seam_groups && lane == 0) p.seams[(w.b * p.kv_heads + w.h) * p.seam_groups + w.g] = s;
+                    }
                     w.next(p, p.span);
                 } else if (lane == 0) {
                     m.unit[u % kUnitRing].end = 0;
@@ -243,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 q_head = head;
                 if (!more) break;
             }
-            if (lane == 0) p.seams[blockIdx.x] = seam;
+            if (!p.seam_groups && lane == 0) p.seams[blockIdx.x] = seam;
         } else if (warp == 0 || (!TALL && warp == 2)) {
             // ---- copies: keys and values of the tiles in turn; where a warp is to spare, the values by that one, as a
             // short call waits for both
@@ -461,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(st + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
                     tmem_wait_ld();
+                    hold(s);
                     if (masked) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -472,14 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float mx[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(s[k]);
+                    for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 8]));
 #pragma unroll
-                    for (int k = 8; k < 128; ++k) mx[k & 7] = fmaxf(mx[k & 7], __uint_as_float(s[k]));
+                    for (int k = 16; k < 128; k += 16)
 #pragma unroll
-                    for (int o = 4; o; o >>= 1)
-#pragma unroll
-                        for (int k = 0; k < o; ++k) mx[k] = fmaxf(mx[k], mx[k + o]);
-                    const float top = mx[0] * p.scale_log2;  // (scale > 0)
+                        for (int y = 0; y < 8; ++y) mx[y] = max3(mx[y], __uint_as_float(s[k + y]), __uint_as_float(s[k + y + 8]));
+                    const float all_mx = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                    const float top = all_mx * p.scale_log2;  // (scale > 0)
                     const bool rise = top > mr + kKvSlack;
                     if (__any_sync(0xffffffffu, rise)) {
                         const float mn = rise ? top : mr, f = mn == mr ? 1.f : ex2(mr - mn);
@@ -598,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_ld16(at + 128 * (TALL ? x : y) + c, *reinterpret_cast<uint32_t(*)[16]>(&v[c]));
                         }
                         tmem_wait_ld();
+                        hold(v);
 #pragma unroll
                         for (int k = 0; k < kHalf; ++k)
                             o[k] = __float_as_uint(y == 0 ? __uint_as_float(v[k]) * f[0]
@@ -704,19 +727,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------- join --
-// Block (8 rows of a unit, block of the attention launch in which it begins to
-// end in a later one), a row a warp.
+// Block (8 rows, unit), a row a warp: dependent reads (seam, parts), and at a
+// prompt's end the bytes.  The unit is the one that begins in block y of the
+// attention launch and ends in a later one, or (kByUnits) where units are half as
+// many as blocks or fewer, unit y: few blocks without work, and if it has many
+// parts they are read 16 or 32 at a time (not if it has few: 256 rows behind 5120
+// tokens, 32 units, 32.6 us, 16 at a time, with half the warps, 39.1).  By units
+// and by blocks, us: one tree of 17 rows over 4113 tokens, 8 units, 12.6 and 15.1;
+// four trees of 64, 32 units, 32.4 and 35.2; 16 trees of 32 over 700, 128 units,
+// 26.1 and 25.0.  At 8 a time four blocks fit an SM (four chunks as above 145.2 us,
+// three 152.9).
 constexpr int kJoinRows = 8;
-template <int DT, int D>
-__global__ void __launch_bounds__(32 * kJoinRows) kv_join_kernel(const __grid_constant__ KvParams p, int unit_rows) {
-    const int c0 = blockIdx.y, lane = threadIdx.x & 31;
+template <int DT, int D, int kAhead, bool kByUnits>
+__global__ void __launch_bounds__(32 * kJoinRows, kAhead == 8 ? 4 : 1) kv_join_kernel(const __grid_constant__ KvParams p, int unit_rows) {
+    const int lane = threadIdx.x & 31;
     const int r = (int)blockIdx.x * kJoinRows + (threadIdx.x >> 5), in = r % kKvTileRows;
     const int t_of = p.by_group(in), t = r / kKvTileRows * p.tile_tokens + t_of;
+    const int groups = kByUnits ? p.seam_groups : 1, y = blockIdx.y, g = y % groups, b = y / (groups * p.kv_heads);
     griddep_wait();
     griddep_launch_dependents();
-    const int4 seam = __ldcg(p.seams + c0);
-    if (t_of >= p.tile_tokens || t >= seam.y) return;
-    kv_write_row<DT, D>(p, kv_sum_parts<D>(p, c0, seam.w, 0, 1, unit_rows, r, lane), seam.x + t,
+    int4 seam = __ldcg(p.seams + y);
+    if (kByUnits) {
+        // (a unit of a request that has fewer has no entry, and none is sure to be there where a wait gave up)
+        const KvReq rq = kv_req(p, b);
+        seam.x = rq.row0 + g * p.span;
+        seam.y = min(max(rq.T - g * p.span, 0), p.span);
+        seam.z = (y - g) / groups - b * p.kv_heads;
+    }
+    const int c1 = min(seam.w & 0xFFFF, p.by_blocks.d - 1), c0 = seam.w >> 16 & 0xFFFF;
+    if (c0 >= c1 || t_of >= p.tile_tokens || t >= seam.y) return;
+    kv_write_row<DT, D>(p, kv_sum_parts<D, kAhead>(p, c0, c1, 0, 1, unit_rows, r, lane), seam.x + t,
                         seam.z * p.group + in - t_of * p.group, lane);
 }
 
@@ -748,8 +788,12 @@ int launch_dt(const KvParams &p, const KvMaps &maps, int blocks, cudaStream_t s)
     if ((st = record_launch(cudaLaunchKernelEx(&c, kv_tiles_kernel<DT, D, TALL>, p, maps)))) return st;
     const int tokens = p.max_q < p.N ? p.max_q : p.N;  // rows of the largest unit
     const int rows = TALL ? C::kRows : tokens * p.group;
-    c = latent_config(dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows), (unsigned)blocks), 32 * kJoinRows, 0, s, attr, 1);
-    return record_launch(cudaLaunchKernelEx(&c, kv_join_kernel<DT, D>, p, C::kRows));
+    const int units = p.seam_groups ? p.B * p.kv_heads * p.seam_groups : blocks, parts = blocks / units;
+    c = latent_config(dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows), (unsigned)units), 32 * kJoinRows, 0, s, attr, 1);
+    return record_launch(!p.seam_groups ? cudaLaunchKernelEx(&c, kv_join_kernel<DT, D, 8, false>, p, C::kRows)
+                         : parts <= 8   ? cudaLaunchKernelEx(&c, kv_join_kernel<DT, D, 8, true>, p, C::kRows)
+                         : parts <= 16  ? cudaLaunchKernelEx(&c, kv_join_kernel<DT, D, 16, true>, p, C::kRows)
+                                        : cudaLaunchKernelEx(&c, kv_join_kernel<DT, D, 32, true>, p, C::kRows));
 }
 template <int DT>
 int launch_d(const KvParams &p, const KvMaps &maps, int blocks, bool tall, cudaStream_t s) {
@@ -761,10 +805,13 @@ int launch_d(const KvParams &p, const KvMaps &maps, int blocks, bool tall, cudaS
 
 int launch_kv_tiles(KvParams &p, int dt, int blocks, cudaStream_t s) {
     p.tile_tokens = kv_tile_tokens(p.group);
-    const bool tall = (p.max_q < p.N ? p.max_q : p.N) > p.tile_tokens;
+    const int tokens = p.max_q < p.N ? p.max_q : p.N;  // of a request at most
+    const bool tall = tokens > p.tile_tokens;
     p.span = tall ? 2 * p.tile_tokens : p.tile_tokens;
     p.unit_cost = kUnitCost;
     p.by_blocks.set(blocks);
+    const long long groups = (tokens + p.span - 1) / p.span, units = groups * p.B * p.kv_heads;
+    p.seam_groups = 2 * units <= blocks ? (int)groups : 0;
     p.box_tokens = 16;
     while (p.box_tokens < kKvTile && p.page_size % (2 * p.box_tokens) == 0) p.box_tokens *= 2;
     KvMaps maps;

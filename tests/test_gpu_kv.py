@@ -538,3 +538,24 @@ def test_binding_refusals():
     with pytest.raises(spx.SpxError):
         args, keep = spx.kv_attention_args(**{**good, "ws": ws[:100]})
         spx.spx_kv_attention(args)
+
+
+@pytest.mark.parametrize("fill", [0x7f, 0xff, 0x00, 0x01])
+def test_one_workspace_for_calls_of_all_sizes(fill):
+    """Whatever an earlier call, or nobody, left behind the workspace's first bytes: requests without rows, with few and
+    with many among those of one call, units that cross from block to block and units that do not."""
+    spx = _spx()
+    states = [make([3000, 40, 0, 2600], [200, 40, 0, 3], heads=8, kv=2, seed=31),
+              make([5000, 300, 900], [64, 0, 17], heads=8, kv=2, tree=True, seed=32),
+              make([2500, 2500, 130], [1, 65, 129], heads=8, kv=2, dtype=BF16, D=64, seed=33),
+              make([260] * 8, [33] * 8, heads=8, kv=8, tree=True, seed=34),
+              make([6000, 10], [1, 1], heads=8, kv=2, seed=35),
+              make([1500, 1400], [0, 300], heads=4, kv=1, seed=36)]
+    size = max(spx.spx_kv_workspace_size(len(s["lens"]), len(s["q"]), s["max_q"], s["max_len"], s["heads"], s["kv"], s["D"])
+               for s in states)
+    ws = torch.full((size,), fill, dtype=torch.uint8, device="cuda")
+    ws[:spx.SPX_KV_WORKSPACE_ZERO] = 0
+    for turn in range(2):
+        for s in states if turn == 0 else states[::-1]:
+            out, lse = call(s, ws=ws)
+            check(s, out, lse)
