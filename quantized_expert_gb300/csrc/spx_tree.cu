@@ -62,12 +62,13 @@ __global__ void __launch_bounds__(kLayoutThreads) tree_layout_kernel(const __gri
 // -------------------------------------------------------------------- accept --
 constexpr int kMaxLayers = 128;
 constexpr int kAcceptThreads = 128;
+static_assert(kAcceptThreads >= 32 + kKvMaxTree, "a warp for the path, a thread for each row's place");
 template <int M>  // room for the buffers of M / 2 layers
 struct AcceptParams {
     int64_t page_stride, token_stride, head_stride;
     int num_pages, page_size, kv_heads, units, max_pages;  // units of 8 values of a head
     const int32_t *table, *lens;
-    int N, max_q, max_len, columns;  // units of all layers
+    int N, max_q, columns;  // columns: units of all layers
     FastDiv by_page, by_units, by_heads;
     const int32_t *q_start, *parent, *token, *target;
     int32_t *n_kept, *path, *next, *lens_out;
@@ -75,15 +76,17 @@ struct AcceptParams {
 };
 
 // Block (request, 128 columns): its first warp walks down the tree, two rows a
-// lane in registers, a vote a step; then a thread moves one unit of 16 bytes of
-// the path's rows, which ascend, so that a row is read before it is written
-// over.  Every block of a request takes the same walk rather than wait for one.
-// 24 layers of one request's 8 rows 3.1 us, its latency (walk, table, rows); 32
-// layers of 16 requests, 50 MB moved, 9.0 us, 5.6 TB/s (rows 8 at a time 10.6, 16
-// at a time 9.5, and in blocks of 128 threads for 256 9.0).
+// lane in registers, a vote a step, while others look up where the rows are; then
+// a thread moves one unit of 16 bytes of the path's rows, which ascend, so that a
+// row is read before it is written over.  Every block of a request takes the same
+// walk rather than wait for one.  24 layers of one request's 8 rows 2.8 us, its
+// latency (walk, rows; 3.1 with the table read behind the walk); 32 layers of 16
+// requests, 50 MB moved, 8.6 us from L2, 12.2 from DRAM (8 rows at a time for 16,
+// 1.1 more; blocks of 256 threads 0.5; the table behind the walk 0.4).
 template <int M>
 __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __grid_constant__ AcceptParams<M> p) {
     __shared__ int way[kKvMaxTree], count, last_target;
+    __shared__ int64_t place[kKvMaxTree];  // of the request's rows in the cache, -1: nowhere
     __shared__ int64_t from[kKvMaxTree], to[kKvMaxTree];
     griddep_wait();
     griddep_launch_dependents();
@@ -117,6 +120,15 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
             count = n;
             last_target = want;
         }
+    } else if (threadIdx.x >= kAcceptThreads - kKvMaxTree) {  // meanwhile
+        const int d = threadIdx.x - (kAcceptThreads - kKvMaxTree), at = base + d, pi = p.by_page(max(at, 0));
+        int64_t to = -1;
+        if (d < r.T && at >= 0 && pi < p.max_pages) {
+            const int pg = __ldg(p.table + (size_t)b * p.max_pages + pi);
+            if (pg >= 0 && pg < p.num_pages)
+                to = (int64_t)pg * p.page_stride + (int64_t)(at - pi * p.page_size) * p.token_stride;
+        }
+        place[d] = to;
     }
     __syncthreads();
     const int n = count;
@@ -130,20 +142,8 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
     }
     if (threadIdx.x < kKvMaxTree) {
         const int d = threadIdx.x, i = d < n ? way[d] : d;
-        int64_t at[2] = {-1, -1};
-        if (i != d) {
-            const int place[2] = {base + i, base + d};
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int pi = p.by_page(max(place[x], 0));
-                if (place[x] < 0 || pi >= p.max_pages) continue;
-                const int pg = __ldg(p.table + (size_t)b * p.max_pages + pi);
-                if (pg >= 0 && pg < p.num_pages)
-                    at[x] = (int64_t)pg * p.page_stride + (int64_t)(place[x] - pi * p.page_size) * p.token_stride;
-            }
-        }
-        from[d] = at[1] < 0 ? -1 : at[0];
-        to[d] = at[1];
+        from[d] = i == d || place[d] < 0 ? -1 : place[i];
+        to[d] = place[d];
     }
     __syncthreads();
     const int c = (int)blockIdx.y * kAcceptThreads + threadIdx.x;
