@@ -63,10 +63,10 @@ __device__ __forceinline__ void cp_async_wait() {
 // parts: nothing is searched for, and the parts are joined from the blocks'
 // shared memories instead of by way of the workspace and a counter.
 //
-// Measured, replayed from a graph: 65536 tokens of 8 key heads 47.4 us, 5.7 TB/s,
+// Measured, replayed from a graph: 65536 tokens of 8 key heads 46.5 us, 5.8 TB/s,
 // 5 of them the launch's beginning (search, table, first copies) and 4 its end
 // (sums of warps, of blocks); 32 requests of up to 4096 tokens and 16 key heads
-// 90.6 us, 6.2 TB/s; 517 tokens of 16 heads 6.6 us, a chain of dependent reads
+// 89.6 us, 6.2 TB/s; 517 tokens of 16 heads 6.6 us, a chain of dependent reads
 // (lengths, table, keys) and of barriers.  DRAM reads are the cache's bytes, once.
 constexpr int kFewRows = 16;  // (token, head) rows of a unit at most
 constexpr int kWarps = 8;
@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
     int *last_part = reinterpret_cast<int *>(own_ml + C::kRows);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = lane >> 2, pair = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * (C::kStages * 2 * C::kBlk);
+    if (warp == 0) kv_prefetch(p, lane);
     griddep_wait();
     griddep_launch_dependents();
     KvShare share{};

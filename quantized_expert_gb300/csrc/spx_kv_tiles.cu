@@ -196,14 +196,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = m.tmem;
     const WaitCtl ctl{&m.abort, &p.hdr->status, p.budget, SITE_KV};
+    if (warp == 3) kv_prefetch(p, lane);
     griddep_wait();
     griddep_launch_dependents();
 
     if (warp < 4) {
         fewer_registers();
         if (warp == 3) {
-            // ---- the share's units, one ahead of the copies of their queries; the unit that begins in this share and
-            // ends in a later one, for the join launch
+            // ---- the share's units, one ahead of the copies of their queries but the first's; the unit that begins in this
+            // share and ends in a later one, for the join launch
             const uint64_t pol = policy_evict_normal();
             const KvShare share = kv_find_share(p, p.span, lane);
             KvWalk w;
@@ -212,11 +213,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             int q_row = 0, q_head = 0;  // of the unit whose queries are to be copied next
             int before = 0, tiles[2] = {0, 0}, units[2] = {0, 0};
             bool ok = true;
+            const auto copy_queries = [&]() {
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&m.qfull, C::kQTiles * C::kPieces * 128 * p.group * p.tile_tokens);
+                    for (int x = 0; x < C::kQTiles; ++x)
+                        for (int c = 0; c < C::kPieces; ++c)
+                            tma_load_3d(qs + (x * C::kPieces + c) * kPiece, &maps.q, 64 * c, q_head, q_row + x * p.tile_tokens,
+                                        &m.qfull, pol);
+                }
+                __syncwarp();
+            };
             for (uint32_t u = 0; ok; ++u) {
                 const bool more = w.left > 0;
                 if (!(ok = ctl_wait(&m.uempty[u % kUnitRing], ((u / kUnitRing) & 1) ^ 1, ctl))) break;
                 const int row = w.rq.row0 + w.g * p.span, head = w.h * p.group;
                 if (more) {
+                    if (u == 0) {  // nothing to wait for
+                        q_row = row;
+                        q_head = head;
+                        copy_queries();
+                    }
                     // Key tiles of X in the unit's part: TALL, those of its rows; else every second one.
                     const int parts = w.end - w.tile, t0 = w.g * p.span;
                     int n[2];
@@ -250,16 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&m.ufull[u % kUnitRing]);
                 }
                 __syncwarp();
-                if (u > 0) {
+                if (u > 1) {
                     if (!(ok = ctl_wait(&m.qempty, (u & 1), ctl))) break;  // of the unit before the last
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&m.qfull, C::kQTiles * C::kPieces * 128 * p.group * p.tile_tokens);
-                        for (int x = 0; x < C::kQTiles; ++x)
-                            for (int c = 0; c < C::kPieces; ++c)
-                                tma_load_3d(qs + (x * C::kPieces + c) * kPiece, &maps.q, 64 * c, q_head,
-                                            q_row + x * p.tile_tokens, &m.qfull, pol);
-                    }
                     __syncwarp();
+                    copy_queries();
                 }
                 q_row = row;
                 q_head = head;
