@@ -16,10 +16,10 @@
 // 256 rows and 128 keys 2 x (512 + 256) cycles of products (S takes both operands
 // from shared memory, 128 bytes a cycle; P V one) against 2600 measured.  16384
 // tokens, 32 heads: 1.6 PFLOP/s; a unit's beginning and end cost what four tiles
-// take, so that shorter prompts run at less (4096 tokens 124 us, 1.11 PFLOP/s;
-// four chunks of up to 1021 tokens behind up to 6007, pages of 16, 146 us).
-// Trees of 64 rows, 16 requests of up to 3001 tokens and 16 heads: 53 us, 4.8
-// TB/s; 17 rows, one request of 4113 tokens and 8 key heads: 12.6 us.
+// take, so that shorter prompts run at less (4096 tokens 121 us, 1.13 PFLOP/s;
+// four chunks of up to 1021 tokens behind up to 6007, pages of 16, 145 us).
+// Trees of 64 rows, 16 requests of up to 3001 tokens and 16 heads: 52.5 us, 4.8
+// TB/s; 17 rows, one request of 4113 tokens and 8 key heads: 12.2 us.
 #include <math.h>
 #include <string.h>
 
