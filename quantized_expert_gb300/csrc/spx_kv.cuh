@@ -43,6 +43,7 @@ struct KvParams {
     int span;          // rows (tokens) of a unit
     int unit_cost;     // of a unit beside its tiles, in tiles
     int tile_tokens;   // rows (tokens) of a product of 128 (token, head) rows
+    int q_tokens;      // of them, those that the copy of a unit's queries brings
     int box_tokens;    // cached tokens of one copy: the largest power of two that divides a page, 128 at most
 };
 

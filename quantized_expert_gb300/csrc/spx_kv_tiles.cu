@@ -44,7 +44,7 @@ constexpr int kMiscBytes = 3 << 10;  // of a block's shared memory, behind the t
 struct KvMaps {
     CUtensorMap k;     // [page][head][token][D], boxes of 64 values x box_tokens
     CUtensorMap v;     // [page][head][D / 64][token][64], boxes of all a token's values x box_tokens
-    CUtensorMap q;     // [row][head][D], boxes of 64 values x a group's heads x tile_tokens
+    CUtensorMap q;     // [row][head][D], boxes of 64 values x a group's heads x q_tokens
 };
 
 // Two products are under way at a time, X = 0 and 1, and take turns: while one's
@@ -181,6 +181,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 2) (&m.bad[0][0][0])[lane] = 0;
+    if (p.q_tokens * p.group < kKvTileRows) {  // rows that no copy brings
+        for (int i = threadIdx.x; i < C::kQTiles * C::kSlot / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(qs)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
     if (warp == 0 && elect_one()) {
         prefetch_tmap(&maps.k);
         prefetch_tmap(&maps.v);
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             const auto copy_queries = [&]() {
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&m.qfull, C::kQTiles * C::kPieces * 128 * p.group * p.tile_tokens);
+                    mbar_arrive_expect_tx(&m.qfull, C::kQTiles * C::kPieces * 128 * p.group * p.q_tokens);
                     for (int x = 0; x < C::kQTiles; ++x)
                         for (int c = 0; c < C::kPieces; ++c)
                             tma_load_3d(qs + (x * C::kPieces + c) * kPiece, &maps.q, 64 * c, q_head, q_row + x * p.tile_tokens,
@@ -783,7 +788,7 @@ bool kv_maps(const KvParams &p, int dt, KvMaps *m) {
     const uint32_t vb[5] = {64, (uint32_t)p.box_tokens, (uint32_t)p.D / 64, 1, 1};
     const uint64_t qd[3] = {(uint64_t)p.D, (uint64_t)p.heads, (uint64_t)p.N};
     const uint64_t qst[2] = {row, p.N > 1 ? (uint64_t)p.q_stride * 2 : row};
-    const uint32_t qb[3] = {64, (uint32_t)p.group, (uint32_t)p.tile_tokens};
+    const uint32_t qb[3] = {64, (uint32_t)p.group, (uint32_t)p.q_tokens};
     return map_rows64(&m->k, dt, p.k, 4, cd, cs, cb) && map_rows64(&m->v, dt, p.v, 5, vd, vs, vb) &&
            map_rows64(&m->q, dt, p.q, 3, qd, qst, qb);
 }
@@ -818,6 +823,9 @@ int launch_kv_tiles(KvParams &p, int dt, int blocks, cudaStream_t s) {
     const int tokens = p.max_q < p.N ? p.max_q : p.N;  // of a request at most
     const bool tall = tokens > p.tile_tokens;
     p.span = tall ? 2 * p.tile_tokens : p.tile_tokens;
+    // (no more rows than a request may have: a copy takes long over rows past the last of all.  One tree of 17 rows over
+    // 4113 tokens, 16 heads of their own: boxes of 128 rows 16.1 us, of 17 13.5)
+    p.q_tokens = tokens < p.tile_tokens ? tokens : p.tile_tokens;
     p.unit_cost = kUnitCost;
     p.by_blocks.set(blocks);
     const long long groups = (tokens + p.span - 1) / p.span, units = groups * p.B * p.kv_heads;
