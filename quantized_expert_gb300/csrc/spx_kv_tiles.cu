@@ -492,6 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 8 * C::kPieces; ++k)
                             *reinterpret_cast<uint4 *>(row + (k >> 3) * piece + (((k ^ r) & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
+                    __syncwarp();  // the lane that tells of the warp's weights tells of these zeros too, and a warp without rows
+                                   // has nothing else to meet at
                 }
                 if (warp_live) {
                     uint32_t s[128];
