@@ -409,8 +409,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
             for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, mls[k * C::kRows + r].x);
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
+                // (a warp without tokens brings 0, one whose scores are all NaN no reference and a NaN, which stays)
                 const float2 v = mls[k * C::kRows + r];
-                if (v.x != -INFINITY) ll += v.y * kv_ex2(v.x - mm);
+                ll += v.y * kv_factor(v.x, mm);
             }
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
