@@ -765,7 +765,8 @@ SPX_API size_t spx_kv_workspace_size(int B, int N, int max_q, int max_len, int h
  *   of the last one (-1 without rows); lens_out[b] = lens[b] - T + n_kept[b].
  * In each of the n_layers caches, which share cache's layout, block table and
  * lens and have buffers of their own, the keys and values of the path's d-th row
- * are moved to token lens[b] - T + d.  layer_k and layer_v are host arrays of
+ * are moved to token lens[b] - T + d (zeros, where the row's table entry names no
+ * page; nowhere, where the token's does).  layer_k and layer_v are host arrays of
  * device pointers. */
 typedef struct {
     const spx_kv_cache *cache;   /* its k and v are not used */

@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kLayoutThreads) tree_layout_kernel(const __gri
 // -------------------------------------------------------------------- accept --
 constexpr int kMaxLayers = 128;
 constexpr int kAcceptThreads = 128;
+constexpr int64_t kNoPage = -2;  // as where a row is moved from
 static_assert(kAcceptThreads >= 32 + kKvMaxTree, "a warp for the path, a thread for each row's place");
 template <int M>  // room for the buffers of M / 2 layers
 struct AcceptParams {
@@ -142,7 +143,9 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
     }
     if (threadIdx.x < kKvMaxTree) {
         const int d = threadIdx.x, i = d < n ? way[d] : d;
-        from[d] = i == d || place[d] < 0 ? -1 : place[i];
+        // (-1: nothing to write.  A row without a page reads as zeros, and as zeros it is moved: what stood at its destination
+        // is another row's.)
+        from[d] = i == d || place[d] < 0 ? -1 : place[i] < 0 ? kNoPage : place[i];
         to[d] = place[d];
     }
     __syncthreads();
@@ -155,10 +158,11 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
         uint4 v[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (d0 + k < n && from[d0 + k] >= 0) v[k] = *reinterpret_cast<const uint4 *>(buf + from[d0 + k]);
+            if (d0 + k < n && from[d0 + k] != -1)
+                v[k] = from[d0 + k] == kNoPage ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(buf + from[d0 + k]);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (d0 + k < n && from[d0 + k] >= 0) *reinterpret_cast<uint4 *>(buf + to[d0 + k]) = v[k];
+            if (d0 + k < n && from[d0 + k] != -1) *reinterpret_cast<uint4 *>(buf + to[d0 + k]) = v[k];
     }
 }
 
