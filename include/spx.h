@@ -648,7 +648,10 @@ SPX_API int spx_token_logprobs(const spx_logprobs_args *args, spx_stream_t strea
  * its newest ones, at most max_q of them (larger counts are cut to max_q),
  * none allowed.  lens[b] counts the request's tokens, those rows included: row
  * i of T stands in the cache at token lens[b] - T + i.  Rows that no request
- * owns (a padded batch) are left as they were in every output. */
+ * owns (a padded batch) are left as they were in every output; as spx_kv_append
+ * goes by req and slot alone, a program whose rows vary in number over one N (a
+ * graph replayed with fewer than it was captured for) has spx_tree_layout clear
+ * them, or they name the places of an earlier step. */
 
 /* Keys and values of a layer, in pages of page_size tokens: token p of request
  * b is row p % page_size of page block_table[b][p / page_size].  k and v have
@@ -674,7 +677,8 @@ typedef struct {
  *          (max_q <= 64 with mask or parent, else SPX_ERR_UNSUPPORTED);
  *   pos  = lens[b] - T + the number of rows above it (its rotary position);
  *   slot = lens[b] - T + i (its place in the cache); req = b.
- * Each output may be NULL. */
+ * Each output may be NULL.  With clear_rest the rows that no request owns get req,
+ * slot and pos -1, which spx_kv_append skips, and mask 0. */
 typedef struct {
     int B, N, max_q;
     const int32_t *q_start;      /* [B + 1], ascending from 0 on */
@@ -682,6 +686,7 @@ typedef struct {
     const int32_t *parent;       /* [N], or NULL */
     int32_t *req, *slot, *pos;   /* [N] */
     uint64_t *mask;              /* [N] */
+    int clear_rest;              /* 0: rows that no request owns are left as they were */
 } spx_tree_layout_args;
 SPX_API int spx_tree_layout(const spx_tree_layout_args *args, spx_stream_t stream);
 

@@ -8,7 +8,7 @@ namespace {
 
 // -------------------------------------------------------------------- layout --
 struct LayoutParams {
-    int N, max_q;
+    int N, max_q, clear_rest;
     const int32_t *q_start, *lens, *parent;
     int32_t *req, *slot, *pos;
     uint64_t *mask;
@@ -29,6 +29,15 @@ __global__ void __launch_bounds__(kLayoutThreads) tree_layout_kernel(const __gri
     griddep_launch_dependents();
     const int b = blockIdx.x, j = threadIdx.x, i = (int)blockIdx.y * kLayoutThreads + j;
     const KvReq r = kv_req(p.q_start, p.lens, b, p.N, p.max_q, 0x7fffffff);
+    if (p.clear_rest) {  // the rows between this request's and the next one's, or behind the last one's
+        const int end = b + 1 < (int)gridDim.x ? min(__ldg(p.q_start + b + 1), p.N) : p.N;
+        for (int row = r.row0 + r.T + i; row < end; row += (int)gridDim.y * kLayoutThreads) {
+            if (p.req) p.req[row] = -1;
+            if (p.slot) p.slot[row] = -1;
+            if (p.pos) p.pos[row] = -1;
+            if (p.mask) p.mask[row] = 0;
+        }
+    }
     if ((int)blockIdx.y * kLayoutThreads >= r.T) return;
     int above = i;
     uint64_t m = i < 64 ? (2ull << i) - 1 : 0;
@@ -240,10 +249,10 @@ extern "C" int spx_tree_layout(const spx_tree_layout_args *a, spx_stream_t strea
     const Span out[] = {{a->req, nn}, {a->slot, nn}, {a->pos, nn}, {a->mask, 2 * nn}};
     if (any_overlap(in, out)) return SPX_ERR_INVALID_ARG;
     if (a->max_q > kKvMaxTree && (a->parent || a->mask)) return SPX_ERR_UNSUPPORTED;
-    if (a->N == 0 || a->max_q == 0) return SPX_OK;
-    const int rows = a->max_q < a->N ? a->max_q : a->N, groups = (rows + kLayoutThreads - 1) / kLayoutThreads;
+    if (a->N == 0 || (a->max_q == 0 && !a->clear_rest)) return SPX_OK;
+    const int rows = a->max_q < a->N ? a->max_q : a->N, groups = rows ? (rows + kLayoutThreads - 1) / kLayoutThreads : 1;
     if (groups > 65535) return SPX_ERR_UNSUPPORTED;
-    LayoutParams p{a->N, a->max_q, a->q_start, a->lens, a->parent, a->req, a->slot, a->pos, a->mask};
+    LayoutParams p{a->N, a->max_q, a->clear_rest, a->q_start, a->lens, a->parent, a->req, a->slot, a->pos, a->mask};
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = latent_config(dim3((unsigned)a->B, (unsigned)groups), kLayoutThreads, 0,
                                            reinterpret_cast<cudaStream_t>(stream), attr, 1);

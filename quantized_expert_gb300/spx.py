@@ -104,7 +104,7 @@ class KvCacheC(C.Structure):
 class TreeLayoutArgs(C.Structure):
     _fields_ = [("B", C.c_int), ("N", C.c_int), ("max_q", C.c_int), ("q_start", C.c_void_p), ("lens", C.c_void_p),
                 ("parent", C.c_void_p), ("req", C.c_void_p), ("slot", C.c_void_p), ("pos", C.c_void_p),
-                ("mask", C.c_void_p)]
+                ("mask", C.c_void_p), ("clear_rest", C.c_int)]
 
 
 class KvAppendArgs(C.Structure):
@@ -838,10 +838,11 @@ class KvCache:
                         self.block_table.shape[1], B, _i32(self.lens, "lens", (B,)))
 
 
-def tree_layout_args(q_start, lens, max_q: int, parent=None, req=None, slot=None, pos=None, mask=None):
+def tree_layout_args(q_start, lens, max_q: int, parent=None, req=None, slot=None, pos=None, mask=None, clear_rest=False):
     """Build (and keep alive) the argument block of spx_tree_layout: q_start int32
     [B + 1], lens int32 [B], parent int32 [N] (None: chains); outputs req, slot,
-    pos int32 [N] and mask int64 [N] (the 64 bits of what a row sees)."""
+    pos int32 [N] and mask int64 [N] (the 64 bits of what a row sees).  clear_rest:
+    rows that no request owns get -1 (mask 0) and are not left as they were."""
     a = TreeLayoutArgs()
     some = next((t for t in (parent, req, slot, pos, mask) if t is not None), None)
     if some is None:
@@ -849,7 +850,7 @@ def tree_layout_args(q_start, lens, max_q: int, parent=None, req=None, slot=None
     B, N = lens.numel(), some.numel()
     if mask is not None and (mask.dtype != torch.int64 or tuple(mask.shape) != (N,)):
         raise ValueError(f"mask: int64 ({N},) expected")
-    a.B, a.N, a.max_q = B, N, int(max_q)
+    a.B, a.N, a.max_q, a.clear_rest = B, N, int(max_q), int(bool(clear_rest))
     a.q_start, a.lens = _i32(q_start, "q_start", (B + 1,)), _i32(lens, "lens", (B,))
     a.parent, a.req, a.slot, a.pos = (None if t is None else _i32(t, what, (N,)) for t, what in
                                       ((parent, "parent"), (req, "req"), (slot, "slot"), (pos, "pos")))
