@@ -124,12 +124,12 @@ __device__ __forceinline__ int v_row(int box_tokens, int t, int c) {
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
 
-// ctl_wait by a whole warp, converged behind it: loads of tensor memory and
-// barriers take a warp as one, and lanes may leave the wait apart.
+// ctl_wait by a whole warp, which goes on or gives up as one: elections, loads of
+// tensor memory and barriers take a warp together, and nothing else says that
+// lanes do not leave the wait apart.  (One tree of 17 rows 13.1 us, with the votes
+// 13.24; four chunks as above 149.7 and 150.2.)
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtl &c) {
-    const bool ok = ctl_wait(bar, parity, c);
-    __syncwarp();
-    return ok;
+    return __all_sync(0xffffffffu, ctl_wait(bar, parity, c));
 }
 
 // (four chunks as above 147.2 us, with it 146.6)
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (uint32_t u = 0; ok; ++u) {
                 const bool more = w.left > 0;
-                if (!(ok = ctl_wait(&m.uempty[u % kUnitRing], ((u / kUnitRing) & 1) ^ 1, ctl))) break;
+                if (!(ok = warp_wait(&m.uempty[u % kUnitRing], ((u / kUnitRing) & 1) ^ 1, ctl))) break;
                 const int row = w.rq.row0 + w.g * p.span, head = w.h * p.group;
                 if (more) {
                     if (u == 0) {  // nothing to wait for
@@ -272,8 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 if (u > 1) {
-                    if (!(ok = ctl_wait(&m.qempty, (u & 1), ctl))) break;  // of the unit before the last
-                    __syncwarp();
+                    if (!(ok = warp_wait(&m.qempty, (u & 1), ctl))) break;  // of the unit before the last
                     copy_queries();
                 }
                 q_row = row;
@@ -295,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             r.advance(kv0);
             bool ok = true;
             for (uint32_t u = 0; ok; ++u) {
-                if (!(ok = ctl_wait(&m.ufull[u % kUnitRing], (u / kUnitRing) & 1, ctl))) break;
+                if (!(ok = warp_wait(&m.ufull[u % kUnitRing], (u / kUnitRing) & 1, ctl))) break;
                 const Unit &d = m.unit[u % kUnitRing];
                 const int end = d.end, first = d.tile, len = d.len, h = d.h;
                 const int32_t *table = p.table + (size_t)d.b * p.max_pages;
@@ -314,6 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j + 1 < end) look_up(j + 1);
 #pragma unroll 1
                     for (int kv = kv0; kv < kv1; ++kv, r.advance(TALL ? 1 : 2)) {
+                        // (a converged warp asks one barrier, one word and one clock here; with a vote four chunks take
+                        // 154 us for 149)
                         if (!(ok = ctl_wait(&m.empty[r.i], r.phase ^ 1, ctl))) break;
                         if (elect_one()) mbar_arrive_expect_tx(&m.full[r.i], C::kSlot);
                         __syncwarp();
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t tile0 = 0, tile1 = 0, unit0 = 0, unit1 = 0, step = 0;  // tiles and units of X before this one, turns
             bool ok = true;
             for (uint32_t u = 0; ok; ++u) {
-                if (!(ok = ctl_wait(&m.ufull[u % kUnitRing], (u / kUnitRing) & 1, ctl))) break;
+                if (!(ok = warp_wait(&m.ufull[u % kUnitRing], (u / kUnitRing) & 1, ctl))) break;
                 const Unit &d = m.unit[u % kUnitRing];
                 const int end = d.end, all = end - d.tile, n0 = d.n[0], n1 = d.n[1];
                 __syncwarp();
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (end == 0) break;
                 Place<C::kRing> kr = at, vr = at;
                 vr.advance(1);
-                ok = ctl_wait(&m.qfull, u & 1, ctl);
+                ok = warp_wait(&m.qfull, u & 1, ctl);
                 // Step j: S of tile j, and O of the tile before (TALL; X's own, on the same tiles), or of the one before
                 // that (tiles belong to X = 0 and 1 in turn).
                 constexpr int kLag = TALL ? 1 : 2;
@@ -384,12 +385,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                          (!TALL || (x ? ctl_wait(&m.turn[1], step & 1, ctl) : step == 0 || ctl_wait(&m.turn[0], (step - 1) & 1, ctl))) &&
                          (!has_o || !first || ctl_wait(&m.oempty[x], ((x ? unit1 : unit0) & 1) ^ 1, ctl)) &&
                          (!has_o || ctl_wait(&m.pfull[x][0], parity, ctl));
-                    if (!ok) break;
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_fence_after();
                     if (has_o) {  // the first half while the softmax is at the second
                         if (elect_one()) sums(x, vr.i, 0, first);
                         __syncwarp();
-                        if (!(ok = ctl_wait(&m.pfull[x][1], parity, ctl))) break;
+                        if (!(ok = warp_wait(&m.pfull[x][1], parity, ctl))) break;
                         tc_fence_after();
                     }
                     if (elect_one()) {
@@ -455,12 +456,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 all = kv_all_see(p, rq, d.t0);
             }
             float mr = -INFINITY, l = 0.f;
+            bool fine = true;  // no wait of the unit has given up
             const uint32_t tile = d.tiles[x];
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 const int li = TALL ? i : 2 * i + x, j = first + li, p0 = kKvTile * j;
                 const bool masked = p0 + kKvTile > all;
-                warp_wait(&m.sfull[x], (tile + i) & 1, ctl);
+                if (!(fine = warp_wait(&m.sfull[x], (tile + i) & 1, ctl))) break;
                 tc_fence_after();
                 if (masked) {
                     // Of a tile that not every row sees whole, the values of tokens past the length, and of those that
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // that see such a token become NaNs at the end.  A token a thread.  (Not before the scores are there: only
                     // then is the slot's last use known to be over, and the wait's parity that of this use.)
                     const uint32_t item = 2 * (d.before + li) + 1, slot = item % C::kRing;
-                    warp_wait(&m.full[slot], (item / C::kRing) & 1, ctl);
+                    if (!(fine = warp_wait(&m.full[slot], (item / C::kRing) & 1, ctl))) break;
                     uint8_t *row = ring + slot * C::kSlot + v_row<C::kPieces>(p.box_tokens, r, 0);
                     const int piece = p.box_tokens * 128;  // to the row's next 64 values
                     bool zero = p0 + r >= d.len;
@@ -567,12 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- the unit's end
             const int parts = d.end - first, other = d.n[x ^ 1];
-            if (n) warp_wait(&m.odone[x], d.units[x] & 1, ctl);
-            if (other) warp_wait(&m.odone[x ^ 1], d.units[x ^ 1] & 1, ctl);
+            fine = fine && (n == 0 || warp_wait(&m.odone[x], d.units[x] & 1, ctl)) &&
+                   (other == 0 || warp_wait(&m.odone[x ^ 1], d.units[x ^ 1] & 1, ctl));
             tc_fence_after();
             if (!TALL) m.ml[x][r] = make_float2(mr, l);
             __syncwarp();
-            bar_sync(1, 256);  // references, weights and lists of bad tokens are there
+            // References, weights and lists of bad tokens are there.  Where a wait gave up all leave, and give no slot back: a
+            // copy into it may be in flight, and the next one's bytes would count on the same phase of its barrier.
+            if (bar_any(1, 256, !fine)) break;
             float f[2] = {1.f, 1.f};
             if (!TALL) {
                 const float2 a = m.ml[0][r], b = m.ml[1][r];
@@ -608,8 +612,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int t;
                 const bool live = row_of(t);
                 const KvReq rq{d.row0, d.T, d.len};
-                if (TALL) warp_wait(&m.full[k_slot], (item / C::kRing) & 1, ctl);  // (else it may hold another unit's by now)
-                warp_wait(&m.full[v_slot], ((item + 1) / C::kRing) & 1, ctl);
+                // (TALL; else it may hold another unit's by now)
+                fine = (!TALL || warp_wait(&m.full[k_slot], (item / C::kRing) & 1, ctl)) &&
+                       warp_wait(&m.full[v_slot], ((item + 1) / C::kRing) & 1, ctl);
                 uint8_t *stage = ring + (TALL && x == 0 ? k_slot : v_slot) * C::kSlot + ((TALL ? 0 : 4 * x) + q) * 32 * kRow;
                 // unit k of row i of the warp's 32
                 const auto staged = [&](int i, int k) {
@@ -718,9 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&m.uempty[u % kUnitRing]);
             }
             if (warp == 4 && lane < 16) (&m.bad[(u & 1) ^ 1][0][0])[lane] = 0;
-            ok = warp_wait(&m.ufull[(u + 1) % kUnitRing], ((u + 1) / kUnitRing) & 1, ctl);
+            ok = fine && warp_wait(&m.ufull[(u + 1) % kUnitRing], ((u + 1) / kUnitRing) & 1, ctl);
             if (bar_any(2, 256, !ok)) ok = false;  // and everyone has read what the next unit writes
-            if (q == 0 && lane == 0 && (TALL || x == 0)) {
+            if (ok && q == 0 && lane == 0 && (TALL || x == 0)) {
                 if (TALL) mbar_arrive(&m.empty[k_slot]);
                 mbar_arrive(&m.empty[v_slot]);
             }
