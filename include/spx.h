@@ -752,7 +752,8 @@ typedef struct {
     void *ws;                    /* spx_kv_workspace_size() bytes, 16-byte aligned; the first
                                     SPX_KV_WORKSPACE_ZERO zeroed once by spx_workspace_init() */
     size_t ws_bytes;
-    uint64_t wait_budget_ns;     /* bound of every device-side wait; 0 = 2 s */
+    uint64_t wait_budget_ns;     /* bound of every device-side wait, to the microseconds for which a waiting thread is
+                                    suspended; 0 = 2 s */
 } spx_kv_attention_args;
 #define SPX_KV_WORKSPACE_ZERO 8192
 SPX_API int spx_kv_attention(const spx_kv_attention_args *args, spx_stream_t stream);

@@ -132,6 +132,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
     return __all_sync(0xffffffffu, ctl_wait(bar, parity, c));
 }
 
+// The same for the next unit.  A thread that waits is suspended for as long as the
+// hardware likes, some microseconds, in which a shorter limit is lost; here one is
+// kept to by asking without (in every wait it costs 1 to 2%), so that a call with a
+// limit below a microsecond is sure to give up.
+constexpr uint64_t kBriefNs = 1000;
+__device__ __forceinline__ bool unit_wait(uint64_t *bar, uint32_t parity, const WaitCtl &c) {
+    if (c.budget >= kBriefNs) return warp_wait(bar, parity, c);
+    const uint64_t t0 = global_timer_ns();
+    while (!__all_sync(0xffffffffu, mbar_test(bar, parity))) {
+        if (__any_sync(0xffffffffu, *c.abort)) return false;
+        if (__any_sync(0xffffffffu, global_timer_ns() - t0 > c.budget)) {
+            record_timeout(c.status, c.site);
+            *c.abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // (four chunks as above 147.2 us, with it 146.6)
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
@@ -432,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t st = tmem + quarter + 128 * x, ot = tmem + quarter + 256;
         // (What a unit's end needs is read from its description there, and not held in registers beside a row's scores.)
         // (Warps that meet at barriers leave together: where one gave up, all hear of it.)
-        bool ok = warp_wait(&m.ufull[0], 0, ctl);
+        bool ok = unit_wait(&m.ufull[0], 0, ctl);
         if (bar_any(2, 256, !ok)) ok = false;
 #pragma unroll 1
         for (uint32_t u = 0; ok; ++u) {
@@ -723,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&m.uempty[u % kUnitRing]);
             }
             if (warp == 4 && lane < 16) (&m.bad[(u & 1) ^ 1][0][0])[lane] = 0;
-            ok = fine && warp_wait(&m.ufull[(u + 1) % kUnitRing], ((u + 1) / kUnitRing) & 1, ctl);
+            ok = fine && unit_wait(&m.ufull[(u + 1) % kUnitRing], ((u + 1) / kUnitRing) & 1, ctl);
             if (bar_any(2, 256, !ok)) ok = false;  // and everyone has read what the next unit writes
             if (ok && q == 0 && lane == 0 && (TALL || x == 0)) {
                 if (TALL) mbar_arrive(&m.empty[k_slot]);

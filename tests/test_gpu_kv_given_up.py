@@ -43,3 +43,15 @@ def test_blocks_with_many_units(lens, news, heads, kv, D, tree, dtype, limit):
     want, _ = call(s)
     ws = _spx().new_kv_workspace(s["q"], s["cache"], s["max_q"], s["max_len"])
     print("ran out", give_up(s, ws, want, limit, 4))
+
+
+@pytest.mark.parametrize("lens,news,heads,kv,D,tree,dtype", SHAPES + [
+    ([200], [20], 8, 4, 128, True, F16), ([9000, 40, 700], [64, 40, 9], 8, 2, 128, True, F16),
+    ([3000] * 8, [33] * 8, 16, 16, 64, False, BF16), ([900], [700], 4, 4, 128, False, F16),
+    ([4000, 300], [1500, 200], 8, 2, 64, False, BF16), ([1], [1], 24, 1, 128, True, F16)])
+def test_a_limit_below_a_microsecond_runs_out(lens, news, heads, kv, D, tree, dtype):
+    """No unit is described within a nanosecond: every call has a wait that runs out, and says so."""
+    s = make(lens, news, heads=heads, kv=kv, D=D, dtype=dtype, tree=tree)
+    want, _ = call(s)
+    ws = _spx().new_kv_workspace(s["q"], s["cache"], s["max_q"], s["max_len"])
+    assert give_up(s, ws, want, 1, 5) == 5
