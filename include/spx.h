@@ -731,7 +731,8 @@ SPX_API int spx_kv_append(const spx_kv_append_args *args, spx_stream_t stream);
  *     != NULL; causal is ignored; max_q <= 64);
  *   out = sum_p softmax(scale * q . k_p) v_p,  lse = log sum_p exp(scale * q . k_p).
  * A row that sees nothing, or whose every score is -inf, gives out = 0 and lse =
- * -inf.  A position that holds an infinity or a NaN reaches only the rows that
+ * -inf; one that sees a score of +inf or a NaN (scores are fp32) gives NaNs for
+ * both.  A position that holds an infinity or a NaN reaches only the rows that
  * see it (one among its values, at least that column of out).  max_len bounds every request's
  * length (longer ones are cut to it).  Softmax weights are rounded to the type
  * before they meet the values; every sum is fp32.  out lies apart from what is

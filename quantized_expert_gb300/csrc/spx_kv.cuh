@@ -300,6 +300,16 @@ constexpr float kKvLn2 = 0.6931471805599453f;
 // weights are scaled by 2^kKvShift: they stay below fp16's largest value (2^16)
 // and most of what is worth adding above its subnormals (2^-14).
 constexpr float kKvSlack = 8.f, kKvShift = 5.f;
+// References are held as scores are, without the scale.  The exponent of a weight
+// is score * scale_log2 + kv_ref, rounded once, which is exact enough while a step
+// of the reference's product with the scale is below 1; from there on (kv_far) the
+// difference of score and reference is taken first, or a row's best weight might
+// be 2^(half a step), infinite or nothing.
+constexpr float kKvFar = 8388608.f;  // 2^23
+__device__ __forceinline__ float kv_ref(float m, float scale_log2) { return m == -INFINITY ? 0.f : kKvShift - m * scale_log2; }
+__device__ __forceinline__ bool kv_far(float m, float scale_log2) {
+    return m != -INFINITY && fabsf(m * scale_log2) >= kKvFar;
+}
 
 __device__ __forceinline__ float kv_ex2(float x) {
     float y;

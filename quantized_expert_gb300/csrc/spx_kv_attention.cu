@@ -316,14 +316,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                 float t = fmaxf(fmaxf(s[0][2 * y], s[0][2 * y + 1]), fmaxf(s[1][2 * y], s[1][2 * y + 1]));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                top[y] = t * p.scale_log2;  // (scale > 0)
-                rise |= top[y] > m[y] + kKvSlack;
+                top[y] = t;
+                rise |= (t - m[y]) * p.scale_log2 > kKvSlack;  // (scale > 0; not if both are -inf)
             }
             if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const float mn = top[y] > m[y] + kKvSlack ? top[y] : m[y];
-                    fac[y] = mn == m[y] ? 1.f : kv_ex2(m[y] - mn);
+                    const float mn = (top[y] - m[y]) * p.scale_log2 > kKvSlack ? top[y] : m[y];
+                    fac[y] = mn == m[y] ? 1.f : kv_ex2((m[y] - mn) * p.scale_log2);
                     m[y] = mn;
                     l[y] *= fac[y];
                 }
@@ -332,14 +332,23 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[n][i] *= fac[i >> 1];
             }
+            float ref[2] = {kv_ref(m[0], p.scale_log2), kv_ref(m[1], p.scale_log2)};
+            if (__any_sync(0xffffffffu, kv_far(m[0], p.scale_log2) || kv_far(m[1], p.scale_log2))) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    if (kv_far(m[y], p.scale_log2)) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[i >> 1][2 * y + (i & 1)] -= m[y];
+                        ref[y] = kKvShift;
+                    }
+            }
             uint32_t pa[4];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const float ref = m[y] == -INFINITY ? 0.f : kKvShift - m[y];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const float a = kv_ex2(fmaf(s[n][2 * y], p.scale_log2, ref));
-                    const float b = kv_ex2(fmaf(s[n][2 * y + 1], p.scale_log2, ref));
+                    const float a = kv_ex2(fmaf(s[n][2 * y], p.scale_log2, ref[y]));
+                    const float b = kv_ex2(fmaf(s[n][2 * y + 1], p.scale_log2, ref[y]));
                     l[y] += a + b;
                     pa[2 * n + y] = Elem<DT>::down2(a, b);  // rounded for the tensor cores; the weight's own sum is not
                 }
@@ -358,6 +367,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
         // ---- the warps' sums joined, in a fixed order
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
+            m[y] *= p.scale_log2;  // from here on with the scale
             l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
             l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
             if (pair == 0) mls[warp * C::kRows + 8 * y + quad] = make_float2(m[y], l[y]);

@@ -538,11 +538,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 16; k < 128; k += 16)
 #pragma unroll
                         for (int y = 0; y < 8; ++y) mx[y] = max3(mx[y], __uint_as_float(s[k + y]), __uint_as_float(s[k + y + 8]));
-                    const float all_mx = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-                    const float top = all_mx * p.scale_log2;  // (scale > 0)
-                    const bool rise = top > mr + kKvSlack;
+                    const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                    const bool rise = (top - mr) * p.scale_log2 > kKvSlack;  // (scale > 0; not if both are -inf)
                     if (__any_sync(0xffffffffu, rise)) {
-                        const float mn = rise ? top : mr, f = mn == mr ? 1.f : ex2(mr - mn);
+                        const float mn = rise ? top : mr, f = mn == mr ? 1.f : ex2((mr - mn) * p.scale_log2);
                         mr = mn;
                         l *= f;
                         if (i > 0) {
@@ -557,7 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    const float ref = mr == -INFINITY ? 0.f : kKvShift - mr;
+                    float ref = kv_ref(mr, p.scale_log2);
+                    const bool far = kv_far(mr, p.scale_log2);
+                    if (__any_sync(0xffffffffu, far)) {
+                        const float from = far ? mr : 0.f;
+#pragma unroll
+                        for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(__uint_as_float(s[k]) - from);
+                        if (far) ref = kKvShift;
+                    }
                     const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), ref2 = pack2(ref, ref);
                     uint64_t l2[2] = {0, 0};
 #pragma unroll
@@ -587,6 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- the unit's end
+            mr *= p.scale_log2;  // from here on with the scale
             const int parts = d.end - first, other = d.n[x ^ 1];
             fine = fine && (n == 0 || warp_wait(&m.odone[x], d.units[x] & 1, ctl)) &&
                    (other == 0 || warp_wait(&m.odone[x ^ 1], d.units[x ^ 1] & 1, ctl));
