@@ -68,3 +68,23 @@ def test_all_keys_not_numbers(rows):
     s["cache"].k[s["cache"].block_table[0, :5].long()] = math.nan
     out, lse = call(s)
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("rows", [1, 16, 17, 64, 200])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+def test_scores_that_are_infinite(rows, value):
+    """One value of a key: a score of +inf makes out and lse NaN, one of -inf leaves the token out."""
+    s = make([300 + rows], [rows], heads=4, kv=2, D=64)
+    clean, clean_lse = call(s)
+    at = 150
+    s["cache"].k[int(s["cache"].block_table[0, at // 64]), at % 64, 1, 9] = value
+    out, lse = call(s)
+    assert torch.equal(out[:, :2], clean[:, :2]) and torch.equal(lse[:, :2], clean_lse[:, :2])
+    up = s["q"][:, 2:, 9] * value > 0
+    assert torch.isnan(out[:, 2:][up]).all() and torch.isnan(lse[:, 2:][up]).all()
+    down = ~up
+    s["cache"].k[int(s["cache"].block_table[0, at // 64]), at % 64, 1] = 0
+    # (without the token: its weight taken out of the sum that holds it with a score of 0; two lse, each within 1.3e-4)
+    zero, zero_lse = call(s)
+    want = torch.log(torch.exp(zero_lse.double()) - 1)[:, 2:][down]
+    assert ((lse[:, 2:].double()[down] - want).abs() <= 3e-4).all() and torch.isfinite(out[:, 2:][down]).all()
