@@ -69,8 +69,6 @@ using namespace spx;
 
 static const uint64_t kWaitBudgetNs = 2000000000ull;  // 2 s per bounded wait
 
-static bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 extern "C" const char *spx_status_string(int st) {
     switch (st) {
         case SPX_OK: return "ok";

@@ -172,8 +172,6 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const __grid_constan
     store8<DT>(dst + 32, y);
 }
 
-bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 }  // namespace
 
 }  // namespace spx

@@ -233,6 +233,11 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint64_t global_timer_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -472,6 +477,9 @@ struct TcArgs {
     WsHeader *hdr;
     uint64_t wait_budget_ns;
 };
+// Of a pointer: what 16-byte accesses and copies need.
+inline bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
 // Verify calls of at least kTcMinT tokens take the tensor-memory launches
 // when the experts' tile packs are given.  Measured on GB300 (DeepSeek-, Qwen-
 // and Phi-shaped layers, µs per layer, expert launch -> tensor-memory

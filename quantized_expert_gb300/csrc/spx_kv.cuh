@@ -311,11 +311,6 @@ __device__ __forceinline__ bool kv_far(float m, float scale_log2) {
     return m != -INFINITY && fabsf(m * scale_log2) >= kKvFar;
 }
 
-__device__ __forceinline__ float kv_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Log of a row's sum of exponentials from its reference and weight.
 __device__ __forceinline__ float kv_lse(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l) - kKvShift) * kKvLn2;
@@ -323,7 +318,7 @@ __device__ __forceinline__ float kv_lse(float m, float l) {
 // The factor of a part with reference m under a common reference (0 without
 // any, unless no part has one).
 __device__ __forceinline__ float kv_factor(float m, float common) {
-    return m == -INFINITY ? (common == -INFINITY ? 1.f : 0.f) : kv_ex2(m - common);
+    return m == -INFINITY ? (common == -INFINITY ? 1.f : 0.f) : ex2(m - common);
 }
 // One warp: a row's sum over the parts `first`, first + step and so on of the
 // blocks c0 .. c1, in their order, under the reference of them all.  r: row of a

@@ -166,8 +166,6 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const __grid_con
     }
 }
 
-bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 // Two heads a thread from what L2 keeps on (half of its 126 MB, read and
 // written); below, one, for more threads and results that stay.
 constexpr long long kLargeBytes = 64ll << 20;

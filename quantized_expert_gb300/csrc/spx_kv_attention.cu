@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const float mn = (top[y] - m[y]) * p.scale_log2 > kKvSlack ? top[y] : m[y];
-                    fac[y] = mn == m[y] ? 1.f : kv_ex2((m[y] - mn) * p.scale_log2);
+                    fac[y] = mn == m[y] ? 1.f : ex2((m[y] - mn) * p.scale_log2);
                     m[y] = mn;
                     l[y] *= fac[y];
                 }
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
             for (int y = 0; y < 2; ++y) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const float a = kv_ex2(fmaf(s[n][2 * y], p.scale_log2, ref[y]));
-                    const float b = kv_ex2(fmaf(s[n][2 * y + 1], p.scale_log2, ref[y]));
+                    const float a = ex2(fmaf(s[n][2 * y], p.scale_log2, ref[y]));
+                    const float b = ex2(fmaf(s[n][2 * y + 1], p.scale_log2, ref[y]));
                     l[y] += a + b;
                     pa[2 * n + y] = Elem<DT>::down2(a, b);  // rounded for the tensor cores; the weight's own sum is not
                 }
@@ -506,8 +506,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
     }
     cp_async_wait_all();
 }
-
-bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Rows of a partial sum's place in the workspace: (token, head) rows of a unit
 // of the launch that takes a call of `tokens` rows at most.

@@ -1318,8 +1318,6 @@ int latent_form(int form, int B, int max_q, int max_len, int heads, int dn, int 
     return expanded < absorbed ? SPX_LATENT_EXPANDED : SPX_LATENT_ABSORBED;
 }
 
-bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 }  // namespace
 
 // Checks of a cache's description that need no device.

@@ -54,12 +54,6 @@ constexpr int kCandidates = 2048;
 constexpr int kHigh = 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float ex2f(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Reference (in base 2), sum, and sum weighted by the exponent.
 struct Stat {
     float m, z, d;
@@ -69,12 +63,12 @@ __device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
     r.m = fmaxf(a.m, b.m);
     r.z = r.d = 0.f;
     if (a.z != 0.f) {  // (a NaN is not 0)
-        const float t = a.m - r.m, f = ex2f(t);
+        const float t = a.m - r.m, f = ex2(t);
         r.z += a.z * f;
         r.d += (a.d + t * a.z) * f;
     }
     if (b.z != 0.f) {
-        const float t = b.m - r.m, f = ex2f(t);
+        const float t = b.m - r.m, f = ex2(t);
         r.z += b.z * f;
         r.d += (b.d + t * b.z) * f;
     }
@@ -198,7 +192,7 @@ struct Running {
         if (mx > ref + kSlack) {
             const float to = fmaxf(mx, C::kFloor), to_rc = __fmul_rn(to, kLog2e);  // (not contracted with what follows)
             if (ref > -INFINITY) {
-                const float t = rc - to_rc, g = ex2f(t);
+                const float t = rc - to_rc, g = ex2(t);
                 d = mul2(fma2(pack2(t, t), z, d), pack2(g, g));
                 z = mul2(z, pack2(g, g));
             }
@@ -212,7 +206,7 @@ struct Running {
         for (int i = 0; i < C::kN; i += 2) {
             const uint64_t t2 = fma2(pack2(f[i], f[i + 1]), pack2(kLog2e, kLog2e), minus_rc);
             const float2 t = unpack2(t2);
-            const uint64_t e = pack2(ex2f(t.x), ex2f(t.y));
+            const uint64_t e = pack2(ex2(t.x), ex2(t.y));
             z = add2(z, e);
             d = fma2(e, t2, d);
         }
@@ -535,7 +529,7 @@ __global__ void __launch_bounds__(kThreadsLp, 4) logprobs_kernel(const __grid_co
         a = Stat{m, 0.f, 0.f};
         if (!nan && m < INFINITY && m > -INFINITY) {
             for (int v = tid; v < p.V; v += kThreadsLp) {
-                const float t = (E::up(x[v]) - m) * kLog2e, e = ex2f(t);
+                const float t = (E::up(x[v]) - m) * kLog2e, e = ex2(t);
                 a.z += e;
                 a.d = fmaf(e, fmaxf(t, -200.f), a.d);
             }
