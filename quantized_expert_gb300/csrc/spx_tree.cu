@@ -195,14 +195,27 @@ bool any_overlap(const Span (&in)[I], const Span (&out)[O]) {
     return false;
 }
 
+// Whether no pointer is there twice (none is null): a table of twice as many
+// places, probed from where a pointer's bits lead.  (Every pair of 256, compared,
+// would take as long as the launch.)
+bool distinct(void *const *at, int n) {
+    constexpr int kBits = 9;
+    static_assert(1 << kBits >= 4 * kMaxLayers, "half of the places stay empty");
+    void *seen[1 << kBits] = {};
+    for (int i = 0; i < n; ++i) {
+        uint32_t h = (uint32_t)(reinterpret_cast<uintptr_t>(at[i]) * 0x9E3779B97F4A7C15ull >> (64 - kBits));
+        for (; seen[h]; h = (h + 1) & ((1 << kBits) - 1))
+            if (seen[h] == at[i]) return false;
+        seen[h] = at[i];
+    }
+    return true;
+}
+
 template <int M>
 int launch_accept(const spx_tree_accept_args &a, const spx_kv_cache &c, cudaStream_t s) {
     AcceptParams<M> p{};
-    for (int i = 0; i < 2 * a.n_layers; ++i) {
-        p.kv[i] = i & 1 ? a.layer_v[i >> 1] : a.layer_k[i >> 1];
-        for (int j = 0; j < i; ++j)
-            if (p.kv[j] == p.kv[i]) return SPX_ERR_INVALID_ARG;  // moved twice, it would be read after it was written
-    }
+    for (int i = 0; i < 2 * a.n_layers; ++i) p.kv[i] = i & 1 ? a.layer_v[i >> 1] : a.layer_k[i >> 1];
+    if (!distinct(p.kv, 2 * a.n_layers)) return SPX_ERR_INVALID_ARG;  // moved twice, it would be read after it was written
     p.page_stride = c.page_stride;
     p.token_stride = c.token_stride;
     p.head_stride = c.head_stride;
