@@ -71,7 +71,6 @@ __global__ void __launch_bounds__(kLayoutThreads) tree_layout_kernel(const __gri
 // -------------------------------------------------------------------- accept --
 constexpr int kMaxLayers = 128;
 constexpr int kAcceptThreads = 128;
-constexpr int64_t kNoPage = -2;  // as where a row is moved from
 static_assert(kAcceptThreads >= 32 + kKvMaxTree, "a warp for the path, a thread for each row's place");
 template <int M>  // room for the buffers of M / 2 layers
 struct AcceptParams {
@@ -150,14 +149,15 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
             p.lens_out[b] = base + n;
         }
     }
+    // A row without a page reads as zeros, and as zeros it is moved: what stood at its destination is another row's.
+    bool blank = false;
     if (threadIdx.x < kKvMaxTree) {
         const int d = threadIdx.x, i = d < n ? way[d] : d;
-        // (-1: nothing to write.  A row without a page reads as zeros, and as zeros it is moved: what stood at its destination
-        // is another row's.)
-        from[d] = i == d || place[d] < 0 ? -1 : place[i] < 0 ? kNoPage : place[i];
+        from[d] = i == d || place[d] < 0 ? -1 : place[i];
         to[d] = place[d];
+        blank = i != d && place[d] >= 0 && place[i] < 0;
     }
-    __syncthreads();
+    const bool blanks = __syncthreads_or(blank);
     const int c = (int)blockIdx.y * kAcceptThreads + threadIdx.x;
     if (c >= p.columns) return;
     const int head = p.by_units(c), unit = c - head * p.units, x = p.by_heads(head), h = head - x * p.kv_heads;
@@ -167,12 +167,14 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
         uint4 v[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (d0 + k < n && from[d0 + k] != -1)
-                v[k] = from[d0 + k] == kNoPage ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(buf + from[d0 + k]);
+            if (d0 + k < n && from[d0 + k] >= 0) v[k] = *reinterpret_cast<const uint4 *>(buf + from[d0 + k]);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (d0 + k < n && from[d0 + k] != -1) *reinterpret_cast<uint4 *>(buf + to[d0 + k]) = v[k];
+            if (d0 + k < n && from[d0 + k] >= 0) *reinterpret_cast<uint4 *>(buf + to[d0 + k]) = v[k];
     }
+    if (blanks)  // (behind the moves: nothing is read any more)
+        for (int d = 1; d < n; ++d)
+            if (way[d] != d && from[d] < 0 && to[d] >= 0) *reinterpret_cast<uint4 *>(buf + to[d]) = make_uint4(0, 0, 0, 0);
 }
 
 // Buffers that one block reads while another writes must lie apart.
