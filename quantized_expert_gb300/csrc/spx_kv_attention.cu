@@ -63,10 +63,10 @@ __device__ __forceinline__ void cp_async_wait() {
 // parts: nothing is searched for, and the parts are joined from the blocks'
 // shared memories instead of by way of the workspace and a counter.
 //
-// Measured, replayed from a graph: 65536 tokens of 8 key heads 46.5 us, 5.8 TB/s,
+// Measured, replayed from a graph: 65536 tokens of 8 key heads 47.6 us, 5.6 TB/s,
 // 5 of them the launch's beginning (search, table, first copies) and 4 its end
 // (sums of warps, of blocks); 32 requests of up to 4096 tokens and 16 key heads
-// 89.6 us, 6.2 TB/s; 517 tokens of 16 heads 6.6 us, a chain of dependent reads
+// 91.7 us, 6.1 TB/s; 517 tokens of 16 heads 6.7 us, a chain of dependent reads
 // (lengths, table, keys) and of barriers.  DRAM reads are the cache's bytes, once.
 constexpr int kFewRows = 16;  // (token, head) rows of a unit at most
 constexpr int kWarps = 8;

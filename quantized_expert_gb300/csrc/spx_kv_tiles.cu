@@ -13,13 +13,13 @@
 //
 // The unit of a tree or a verify pass is bound by reading its keys and values,
 // that of a prompt by the chain of one product, softmax and product: per tile of
-// 256 rows and 128 keys 2 x (512 + 256) cycles of products (S takes both operands
-// from shared memory, 128 bytes a cycle; P V one) against 2600 measured.  16384
-// tokens, 32 heads: 1.6 PFLOP/s; a unit's beginning and end cost what four tiles
-// take, so that shorter prompts run at less (4096 tokens 121 us, 1.13 PFLOP/s;
-// four chunks of up to 1021 tokens behind up to 6007, pages of 16, 145 us).
-// Trees of 64 rows, 16 requests of up to 3001 tokens and 16 heads: 52.5 us, 4.8
-// TB/s; 17 rows, one request of 4113 tokens and 8 key heads: 12.2 us.
+// 256 rows and 128 keys 2 x (512 + 512) cycles of products, at the chip's rate,
+// of 2600 to 2700 measured.  16384 tokens, 32 heads: 1.5 to 1.57 PFLOP/s.  A unit's
+// beginning and end, 8000 cycles, leave the tensor cores idle, so that shorter
+// prompts run at less (4096 tokens 120 us, 1.14 PFLOP/s; four chunks of up to 1021
+// tokens behind up to 6007, pages of 16, 146 us, of which 73 tiles a block are
+// 100).  Trees of 64 rows, 16 requests of up to 3001 tokens and 16 heads: 53.9 us,
+// 4.7 TB/s; 17 rows, one request of 4113 tokens and 8 key heads: 12.6 us.
 #include <math.h>
 #include <string.h>
 
@@ -36,7 +36,7 @@ constexpr int kPiece = kKvTile * 128;  // 128 rows of 64 values, 16 KB
 // What a unit costs beside its tiles (its first copies, the last product, the
 // results), in tiles; us for 2, 3, 4: prompt of 4096 tokens 138, 126.5, 122, three
 // of 2048 126, 120, 111, chunks as above 152.6, 150.1, 148.9, trees as above 56.4,
-// 56.2, 56.2.
+// 56.2, 56.2.  (5 and more are not measured: no minimum is known.)
 constexpr int kUnitCost = 4;
 static_assert(kUnitCost <= kKvMostCost, "what the workspace's size is checked for");
 constexpr int kMiscBytes = 3 << 10;  // of a block's shared memory, behind the tiles

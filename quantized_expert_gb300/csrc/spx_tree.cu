@@ -20,7 +20,7 @@ constexpr int kLayoutThreads = kKvMaxTree;
 // and its parent's mask: after round r a row holds its nearest 2^r ancestors
 // and knows the next one, so six rounds do for 64 rows (a walk up the tree
 // takes as many dependent reads as the tree is deep).  One launch of a few dozen
-// bytes a row: bound by its own latency (1.4 us for 17 rows, 1.7 for 64 trees of
+// bytes a row: bound by its own latency (1.5 us for 17 rows, 1.65 for 64 trees of
 // 64, replayed from a graph).
 __global__ void __launch_bounds__(kLayoutThreads) tree_layout_kernel(const __grid_constant__ LayoutParams p) {
     __shared__ uint64_t seen[2][kKvMaxTree];
@@ -88,9 +88,9 @@ struct AcceptParams {
 // lane in registers, a vote a step, while others look up where the rows are; then
 // a thread moves one unit of 16 bytes of the path's rows, which ascend, so that a
 // row is read before it is written over.  Every block of a request takes the same
-// walk rather than wait for one.  24 layers of one request's 8 rows 2.8 us, its
+// walk rather than wait for one.  24 layers of one request's 8 rows 2.9 us, its
 // latency (walk, rows; 3.1 with the table read behind the walk); 32 layers of 16
-// requests, 50 MB moved, 8.6 us from L2, 12.2 from DRAM (8 rows at a time for 16,
+// requests, 50 MB moved, 8.7 us from L2, 12.5 from DRAM (8 rows at a time for 16,
 // 1.1 more; blocks of 256 threads 0.5; the table behind the walk 0.4).
 template <int M>
 __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __grid_constant__ AcceptParams<M> p) {
