@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kLayoutThreads) tree_layout_kernel(const __gri
     const KvReq r = kv_req(p.q_start, p.lens, b, p.N, p.max_q, 0x7fffffff);
     if (p.clear_rest) {  // the rows between this request's and the next one's, or behind the last one's
         const int end = b + 1 < (int)gridDim.x ? min(__ldg(p.q_start + b + 1), p.N) : p.N;
-        for (int row = r.row0 + r.T + i; row < end; row += (int)gridDim.y * kLayoutThreads) {
+        for (int64_t row = (int64_t)r.row0 + r.T + i; row < end; row += (int)gridDim.y * kLayoutThreads) {
             if (p.req) p.req[row] = -1;
             if (p.slot) p.slot[row] = -1;
             if (p.pos) p.pos[row] = -1;
