@@ -50,10 +50,10 @@ KERNEL_SOURCES = {
     "verify": ["spx_tc.cu", "spx_tcgen05.cuh", "spx_route.cu", "spx_routing.cuh", "spx_internal.cuh"],
 }
 PROFILED_TRAFFIC = {
-    "verify": {"kernel": "tc_mlp_kernel", "dram_bytes": 677_540_864 + 3_668_224,
-               "algorithmic_bytes": 674_897_920, "source_sha": "405684f7481d0356"},
-    "draft": {"kernel": "draft_kernel<2,0>", "dram_bytes": 61_501_952 + 173_824, "algorithmic_bytes": 61_374_720,
-              "source_sha": "09b2f75bd5704629"},
+    "verify": {"kernel": "tc_mlp_kernel", "dram_bytes": 677_541_632 + 3_813_632,
+               "algorithmic_bytes": 674_897_920, "source_sha": "4831f27bca14633f"},
+    "draft": {"kernel": "draft_kernel<2,0>", "dram_bytes": 61_501_440 + 197_632, "algorithmic_bytes": 61_374_720,
+              "source_sha": "1d337ce7bced4c9b"},
 }
 NSETS = 8  # default; --sets overrides (profiling captures use fewer)
 NINPUTS = 16
