@@ -320,6 +320,18 @@ __device__ __forceinline__ float kv_lse(float m, float l) {
 __device__ __forceinline__ float kv_factor(float m, float common) {
     return m == -INFINITY ? (common == -INFINITY ? 1.f : 0.f) : ex2(m - common);
 }
+// A result before its rounding.  The rounded weights may sum to more than their
+// sum, by 2^-11 of it, and carry a mean of values at fp16's largest, 65504, past
+// what fp16 holds; an infinity or a NaN stays.  (bf16 ends where fp32 does: sums of
+// such values overflow before.)
+template <int DT>
+__device__ __forceinline__ float kv_held(float v) {
+    return DT == SPX_F16 && fabsf(v) < 65536.f ? fminf(fmaxf(v, -65504.f), 65504.f) : v;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t kv_down2(float a, float b) {
+    return Elem<DT>::down2(kv_held<DT>(a), kv_held<DT>(b));
+}
 // One warp: a row's sum over the parts `first`, first + step and so on of the
 // blocks c0 .. c1, in their order, under the reference of them all.  r: row of a
 // place, of which there are `rows`.  Sums are read kAhead parts at a time (a
@@ -392,9 +404,9 @@ __device__ __forceinline__ void kv_write_row(const KvParams &p, const KvSum<D> &
     constexpr int kPer = D / 32;
     const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
     uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + kPer * lane);
-    const uint32_t lo = Elem<DT>::down2(s.v[0] * inv, s.v[1] * inv);
+    const uint32_t lo = kv_down2<DT>(s.v[0] * inv, s.v[1] * inv);
     if (kPer == 4)
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, Elem<DT>::down2(s.v[kPer - 2] * inv, s.v[kPer - 1] * inv));
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, kv_down2<DT>(s.v[kPer - 2] * inv, s.v[kPer - 1] * inv));
     else
         *dst = lo;
     if (p.lse && lane == 0) p.lse[(int64_t)row * p.heads + head] = kv_lse(s.m, s.l);

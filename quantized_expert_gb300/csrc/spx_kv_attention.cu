@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                 const float inv = ll == 0.f ? 0.f : 1.f / ll;
                 const int row = w.rq.row0 + t, head = w.h * p.group + j;
                 *reinterpret_cast<uint2 *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + 4 * c) =
-                    make_uint2(Elem<DT>::down2(v.x * inv, v.y * inv), Elem<DT>::down2(v.z * inv, v.w * inv));
+                    make_uint2(kv_down2<DT>(v.x * inv, v.y * inv), kv_down2<DT>(v.z * inv, v.w * inv));
                 if (p.lse && c == 0)
                     p.lse[(int64_t)row * p.heads + head] = kv_lse(mm, ll);
             } else {
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) kv_few_rows_kernel(const __gri
                 const float inv = ll == 0.f ? 0.f : 1.f / ll;
                 const int row = w.rq.row0 + t, head = w.h * p.group + j;
                 *reinterpret_cast<uint2 *>(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + 4 * c) =
-                    make_uint2(Elem<DT>::down2(v.x * inv, v.y * inv), Elem<DT>::down2(v.z * inv, v.w * inv));
+                    make_uint2(kv_down2<DT>(v.x * inv, v.y * inv), kv_down2<DT>(v.z * inv, v.w * inv));
                 if (p.lse && c == 0) p.lse[(int64_t)row * p.heads + head] = kv_lse(mm, ll);
             }
             cluster_arrive();  // no block leaves while its memory is read

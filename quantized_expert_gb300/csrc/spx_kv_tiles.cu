@@ -680,14 +680,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int half = 0; half < 2; ++half) {
                         uint32_t o[kHalf];
                         half_of(half, o);
+                        uint32_t over = 0;  // not zero: one is not finite
 #pragma unroll
                         for (int k = 0; k < kU / 2; ++k) {
                             uint32_t v[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
+                            for (int i = 0; i < 4; ++i) {
                                 v[i] = Elem<DT>::down2(__uint_as_float(o[8 * k + 2 * i]), __uint_as_float(o[8 * k + 2 * i + 1]));
+                                if (DT == SPX_F16) over = Elem<DT>::fma2(v[i], 0u, over);
+                            }
                             *staged(lane, half * (kU / 2) + k) = make_uint4(v[0], v[1], v[2], v[3]);
                         }
+                        if (DT == SPX_F16 && (over & 0x7FFF7FFFu))  // (hardly ever: kv_held for all would cost what they do)
+#pragma unroll
+                            for (int k = 0; k < kU / 2; ++k) {
+                                uint32_t v[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    v[i] = kv_down2<DT>(__uint_as_float(o[8 * k + 2 * i]), __uint_as_float(o[8 * k + 2 * i + 1]));
+                                *staged(lane, half * (kU / 2) + k) = make_uint4(v[0], v[1], v[2], v[3]);
+                            }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
