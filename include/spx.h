@@ -733,10 +733,11 @@ SPX_API int spx_kv_append(const spx_kv_append_args *args, spx_stream_t stream);
  * A row that sees nothing, or whose every score is -inf, gives out = 0 and lse =
  * -inf; one that sees a score of +inf or a NaN (scores are fp32) gives NaNs for
  * both.  A position that holds an infinity or a NaN reaches only the rows that
- * see it (one among its values, at least that column of out).  max_len bounds every request's
- * length (longer ones are cut to it).  Softmax weights are rounded to the type
- * before they meet the values; every sum is fp32, of weights up to 2^13 (bf16 values
- * beyond 2^80 may overflow it).  out lies apart from what is read.  Calls with one workspace must not run at the same time.  Block tables
+ * see it (one among its values, at least that column of out).  max_len bounds
+ * every request's length (longer ones are cut to it).  Softmax weights are rounded
+ * to the type before they meet the values; every sum is fp32, of weights up to
+ * 2^13 (bf16 values beyond 2^80 may overflow it).  out lies apart from what is
+ * read.  Calls with one workspace must not run at the same time.  Block tables
  * and max_len that both go beyond 2^31 - 2^16 tokens are SPX_ERR_UNSUPPORTED. */
 typedef struct {
     const spx_kv_cache *cache;
